@@ -86,6 +86,10 @@ enum sv_status {
 #define SV_DEVERR_SEQ_LEN    0x8u   /* seq_lens[b] < 1 or needs more than max_pages pages */
 #define SV_DEVERR_TIMEOUT    0x10u  /* a kernel gave up a wait on its own bulk copies after
                                        2^28 SM clock cycles */
+#define SV_DEVERR_Q_START    0x20u  /* q_start not ascending inside [0, total_q], or a chunk longer than its
+                                       request */
+#define SV_DEVERR_GROUP      0x40u  /* group_start not ascending inside [0, batch], or shared_pages negative or
+                                       more than a request of the group holds */
 
 /* K/V pool formats (sv_cache.kv_format). */
 #define SV_KV_BF16     0   /* k_pool, v_pool bf16 [pages][Hkv][16][128] */
@@ -308,6 +312,79 @@ int sv_quest_decode_step(const sv_cache* cache, const void* q, int32_t num_q_hea
 /* Workspace bytes of sv_quest_decode_step. */
 size_t sv_quest_decode_step_workspace_size(int32_t batch, int32_t num_q_heads, int32_t num_kv_heads,
                                            int32_t max_pages, int32_t budget_pages);
+
+/*
+ * sv_window_attention -- exact softmax attention of query tokens over their
+ * own request's cached tokens, with a causal mask and, optionally, a sliding
+ * window and a few first tokens that stay visible (sinks): chunks of a
+ * prefill, single decode tokens, and both in one batch.  The tokens' K/V are
+ * in the cache already (sv_quest_update_meta).  The query token at position p
+ * of its request sees the tokens
+ *   j <= p  and  (window == 0  or  j > p - window  or  j < sink_tokens)
+ * and, over those, z_j = (q_h . k_j) * softmax_scale,
+ *   out = sum_j softmax(z)_j v_j     bf16 [total_q][num_q_heads][128]
+ *   lse = ln(sum_j exp(z_j))         fp32 [total_q][num_q_heads]
+ *   q        bf16 [total_q][num_q_heads][128]
+ *   q_start  int32 [batch + 1], ascending: rows q_start[b] .. q_start[b + 1] - 1
+ *            of q are the last tokens of request b's seq_lens[b] tokens.  An
+ *            empty range is a request without query tokens.  NULL: one token a
+ *            request, row b is request b's last (total_q == batch).
+ *  - Rows that no request's range holds (behind q_start[batch]) are not
+ *    written.  total_q == 0 launches nothing.
+ *  - A request with seq_lens 0 (a padded batch) gets out = 0, lse = -inf.  So
+ *    does, with an error bit, one whose length or chunk is invalid
+ *    (SV_DEVERR_SEQ_LEN, SV_DEVERR_Q_START); a range outside [0, total_q] is
+ *    skipped.  Pages that the table does not give (SV_DEVERR_PAGE_TABLE) count
+ *    as masked.
+ *  - Only page table entries of visible tokens are read, so the pages behind a
+ *    window may have been freed (sv_pages_free) and their entries be -1.
+ *  - A K/V row that no query token of the call sees may hold anything.  One
+ *    that some see has to be finite: an infinite or NaN value may also reach
+ *    query tokens of the same request that do not see it.
+ *  - Rows of one request and kv head are processed 256 at a time
+ *    (token, query head), on the tensor cores; work is divided evenly over
+ *    the GPU whatever the lengths.  The result does not depend on timing.
+ *  - workspace: sv_window_attention_workspace_size(...) bytes, not shared with
+ *    a call that may run at the same time; nothing in it needs to start at
+ *    zero.  total_q <= 2^24, max_pages < 2^26.
+ */
+int sv_window_attention(const sv_cache* cache, const void* q, int32_t num_q_heads, const int32_t* q_start,
+                        int32_t total_q, const int32_t* page_table, const int32_t* seq_lens, int32_t batch,
+                        int32_t max_pages, int32_t window, int32_t sink_tokens, float softmax_scale, void* out,
+                        float* lse, void* workspace, size_t workspace_bytes, void* stream);
+
+/* Workspace bytes of sv_window_attention (0 for sizes it does not take). */
+size_t sv_window_attention_workspace_size(int32_t batch, int32_t num_q_heads, int32_t num_kv_heads, int32_t total_q);
+
+/*
+ * sv_prefix_decode -- dense decode attention of a batch in which groups of
+ * requests hold the same first pages (what sv_pages_fork makes): the result of
+ * sv_sparse_decode with sel_idx = NULL, with every shared page read once for
+ * its whole group instead of once a request.
+ *   group_start   int32 [num_groups + 1], ascending: requests group_start[g] ..
+ *                 group_start[g + 1] - 1 are group g; a request behind
+ *                 group_start[num_groups] is not touched
+ *   shared_pages  int32 [num_groups]: the first shared_pages[g] entries of the
+ *                 group's page table rows are the same pages, all full of
+ *                 tokens (0: nothing is shared).  They are read from the row
+ *                 of the group's first request.
+ *   q, out, lse   as in sv_sparse_decode, one token a request
+ *  - A request with seq_lens 0 gets out = 0, lse = -inf (the group's first
+ *    request still has to hold the group's pages).  So does, with
+ *    SV_DEVERR_GROUP, one shorter than its group's shared pages or one whose
+ *    group is invalid.
+ *  - The prefix's query rows of a group (requests x query heads of a kv head)
+ *    are one tensor-core product per 256 rows; prefix and rest are joined by
+ *    log-sum-exp.
+ *  - workspace: sv_prefix_decode_workspace_size(...) bytes, as above.
+ */
+int sv_prefix_decode(const sv_cache* cache, const void* q, int32_t num_q_heads, const int32_t* page_table,
+                     const int32_t* seq_lens, int32_t batch, int32_t max_pages, const int32_t* group_start,
+                     const int32_t* shared_pages, int32_t num_groups, float softmax_scale, void* out, float* lse,
+                     void* workspace, size_t workspace_bytes, void* stream);
+
+/* Workspace bytes of sv_prefix_decode (0 for sizes it does not take). */
+size_t sv_prefix_decode_workspace_size(int32_t batch, int32_t num_q_heads, int32_t num_kv_heads, int32_t num_groups);
 
 /* Reads (and with reset != 0 clears) the current device's error word; the
  * read synchronises the device.  Returns SV_OK or SV_ERR_CUDA. */

@@ -66,6 +66,8 @@ def _load():
         "sv_quest_decode_step": [cp, vp, i32, vp, vp, i32, i32, i32, f32, vp, vp, vp, vp, vp, sz, vp],
         "sv_quest_select_ex": [cp, vp, i32, vp, vp, i32, i32, i32, op, vp, vp, vp, vp, sz, vp],
         "sv_sparse_decode_ex": [cp, vp, i32, vp, vp, i32, i32, vp, vp, i32, op, f32, vp, vp, vp, sz, vp],
+        "sv_window_attention": [cp, vp, i32, vp, i32, vp, vp, i32, i32, i32, i32, f32, vp, vp, vp, sz, vp],
+        "sv_prefix_decode": [cp, vp, i32, vp, vp, i32, i32, vp, vp, i32, f32, vp, vp, vp, sz, vp],
         "sv_get_device_error": [ctypes.POINTER(ctypes.c_uint32), ctypes.c_int],
     }
     for name, args in sig.items():
@@ -80,6 +82,10 @@ def _load():
     lib.sv_quest_decode_step_workspace_size.restype = sz
     lib.sv_quest_select_ex_workspace_size.argtypes = [i32, i32, i32, i32, op]
     lib.sv_quest_select_ex_workspace_size.restype = sz
+    lib.sv_window_attention_workspace_size.argtypes = [i32, i32, i32, i32]
+    lib.sv_window_attention_workspace_size.restype = sz
+    lib.sv_prefix_decode_workspace_size.argtypes = [i32, i32, i32, i32]
+    lib.sv_prefix_decode_workspace_size.restype = sz
     lib.sv_status_string.argtypes = [ctypes.c_int]
     lib.sv_status_string.restype = ctypes.c_char_p
     lib.sv_version.argtypes = []
@@ -296,6 +302,68 @@ def sv_sparse_decode_ex(cache: Cache, q: torch.Tensor, page_table: torch.Tensor,
         int(page_table.shape[1]), _p(sel_idx, _I32, "sel_idx"),
         _p(sel_cnt, _I32, "sel_cnt"), K, None if opts is None else ctypes.byref(opts), scale,
         _p(out, _BF16, "out"), _p(lse, _F32, "lse"), _p(workspace, None, "workspace"),
+        workspace.numel() * workspace.element_size(), _stream(stream)))
+
+
+def _shape(t: torch.Tensor, shape, name: str) -> None:
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+
+
+def _here(cache: Cache, *tensors: Optional[torch.Tensor]) -> None:
+    """The kernels run on the current device: every tensor has to be there."""
+    dev = torch.cuda.current_device()
+    for t in (cache.k_pool, *tensors):
+        if t is not None and t.is_cuda and t.device.index != dev:
+            raise ValueError(f"tensors on cuda:{t.device.index} while cuda:{dev} is current")
+
+
+def sv_window_attention_workspace_size(batch: int, num_q_heads: int, num_kv_heads: int, total_q: int) -> int:
+    return int(_load().sv_window_attention_workspace_size(batch, num_q_heads, num_kv_heads, total_q))
+
+
+def sv_window_attention(cache: Cache, q: torch.Tensor, page_table: torch.Tensor, seq_lens: torch.Tensor, window: int,
+                        sink_tokens: int, out: torch.Tensor, lse: torch.Tensor, workspace: torch.Tensor,
+                        q_start: Optional[torch.Tensor] = None, softmax_scale: Optional[float] = None,
+                        stream=None) -> None:
+    """q, out [total_q][Hq][128], lse [total_q][Hq]; window 0: none; q_start None: one token a request."""
+    T, Hq, D = q.shape
+    B, max_pages = page_table.shape
+    _shape(seq_lens, (B,), "seq_lens")
+    _shape(out, q.shape, "out")
+    _shape(lse, (T, Hq), "lse")
+    if q_start is not None:
+        _shape(q_start, (B + 1,), "q_start")
+    _here(cache, q, page_table, seq_lens, q_start, out, lse, workspace)
+    scale = float(D) ** -0.5 if softmax_scale is None else float(softmax_scale)
+    _check("sv_window_attention", _load().sv_window_attention(
+        cache.ref(), _p(q, _BF16, "q"), Hq, _p(q_start, _I32, "q_start"), T, _p(page_table, _I32, "page_table"),
+        _p(seq_lens, _I32, "seq_lens"), B, max_pages, int(window), int(sink_tokens), scale, _p(out, _BF16, "out"),
+        _p(lse, _F32, "lse"), _p(workspace, None, "workspace"), workspace.numel() * workspace.element_size(),
+        _stream(stream)))
+
+
+def sv_prefix_decode_workspace_size(batch: int, num_q_heads: int, num_kv_heads: int, num_groups: int) -> int:
+    return int(_load().sv_prefix_decode_workspace_size(batch, num_q_heads, num_kv_heads, num_groups))
+
+
+def sv_prefix_decode(cache: Cache, q: torch.Tensor, page_table: torch.Tensor, seq_lens: torch.Tensor,
+                     group_start: torch.Tensor, shared_pages: torch.Tensor, out: torch.Tensor, lse: torch.Tensor,
+                     workspace: torch.Tensor, softmax_scale: Optional[float] = None, stream=None) -> None:
+    """Dense decode with the first shared_pages[g] pages of requests group_start[g] .. read once a group."""
+    B, Hq, D = q.shape
+    groups = int(shared_pages.numel())
+    _shape(page_table, (B, page_table.shape[-1]), "page_table")
+    _shape(seq_lens, (B,), "seq_lens")
+    _shape(group_start, (groups + 1,), "group_start")
+    _shape(out, q.shape, "out")
+    _shape(lse, (B, Hq), "lse")
+    _here(cache, q, page_table, seq_lens, group_start, shared_pages, out, lse, workspace)
+    scale = float(D) ** -0.5 if softmax_scale is None else float(softmax_scale)
+    _check("sv_prefix_decode", _load().sv_prefix_decode(
+        cache.ref(), _p(q, _BF16, "q"), Hq, _p(page_table, _I32, "page_table"), _p(seq_lens, _I32, "seq_lens"), B,
+        int(page_table.shape[1]), _p(group_start, _I32, "group_start"), _p(shared_pages, _I32, "shared_pages"), groups,
+        scale, _p(out, _BF16, "out"), _p(lse, _F32, "lse"), _p(workspace, None, "workspace"),
         workspace.numel() * workspace.element_size(), _stream(stream)))
 
 

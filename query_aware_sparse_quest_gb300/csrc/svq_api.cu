@@ -25,6 +25,16 @@ int launch_decode(const sv_cache* c, const void* q, int num_q_heads, const int32
 int decode_max_splits(int pages);
 size_t decode_workspace_bytes(int batch, int num_q_heads, int splits);
 int read_error_decode_fp8(uint32_t* flags, int reset);
+int read_error_attend(uint32_t* flags, int reset);
+size_t window_workspace_bytes(int batch, int num_q_heads, int num_kv_heads, int total_q);
+size_t prefix_workspace_bytes(int batch, int num_q_heads, int num_kv_heads, int num_groups);
+int launch_window(const sv_cache* c, const void* q, int num_q_heads, const int32_t* q_start, int total_q,
+                  const int32_t* page_table, const int32_t* seq_lens, int batch, int max_pages, int window, int sink,
+                  float softmax_scale, void* out, float* lse, void* workspace, int sm_count, cudaStream_t stream);
+int launch_prefix(const sv_cache* c, const void* q, int num_q_heads, const int32_t* page_table,
+                  const int32_t* seq_lens, int batch, int max_pages, const int32_t* group_start,
+                  const int32_t* shared_pages, int num_groups, float softmax_scale, void* out, float* lse,
+                  void* workspace, int sm_count, cudaStream_t stream);
 
 constexpr int kMaxTopkPages = 32768;
 
@@ -298,6 +308,33 @@ int step_checks(const sv_cache* cache, const void* q, int32_t num_q_heads, const
 }
 }  // namespace
 
+namespace {
+// Query tokens of one call: the row count times 8 query heads, and the row
+// tiles of all of them, stay within 31 bits.
+constexpr int kMaxQueryTokens = 1 << 24;
+// Tokens of a page table's row: positions are 32-bit, below 2^30.
+constexpr int kMaxRowPages = 1 << 26;
+
+bool attend_sizes_ok(int batch, int num_q_heads, int num_kv_heads) {
+    return batch >= 1 && batch <= 65535 && num_kv_heads >= 1 && num_q_heads >= 1 && num_q_heads % num_kv_heads == 0 &&
+           num_q_heads / num_kv_heads <= kMaxGroup;
+}
+
+int attend_checks(const sv_cache* cache, const void* q, int num_q_heads, const int32_t* page_table,
+                  const int32_t* seq_lens, int batch, int max_pages, float softmax_scale, const void* out,
+                  const float* lse) {
+    int st = check_cache(cache);
+    if (st) return st;
+    if ((st = check_heads(cache, num_q_heads))) return st;
+    if ((st = check_batch(q, page_table, seq_lens, batch, max_pages))) return st;
+    if (max_pages >= kMaxRowPages) return SV_ERR_UNSUPPORTED;
+    if (!out || !lse || !aligned16(out)) return SV_ERR_INVALID_ARG;
+    if (!(softmax_scale > 0.f) || softmax_scale == INFINITY) return SV_ERR_INVALID_ARG;
+    if (static_cast<int64_t>(batch) * num_q_heads > INT_MAX) return SV_ERR_UNSUPPORTED;
+    return SV_OK;
+}
+}  // namespace
+
 extern "C" {
 
 int sv_quest_decode_step(const sv_cache* cache, const void* q, int32_t num_q_heads, const int32_t* page_table,
@@ -335,6 +372,52 @@ int sv_quest_decode_step(const sv_cache* cache, const void* q, int32_t num_q_hea
                          budget_pages, false, softmax_scale, out, lse, ws + sb + qb, workspace_bytes - sb - qb, sms, s);
 }
 
+size_t sv_window_attention_workspace_size(int32_t batch, int32_t num_q_heads, int32_t num_kv_heads, int32_t total_q) {
+    if (!attend_sizes_ok(batch, num_q_heads, num_kv_heads) || total_q < 0) return 0;
+    return window_workspace_bytes(batch, num_q_heads, num_kv_heads, total_q);
+}
+
+int sv_window_attention(const sv_cache* cache, const void* q, int32_t num_q_heads, const int32_t* q_start,
+                        int32_t total_q, const int32_t* page_table, const int32_t* seq_lens, int32_t batch,
+                        int32_t max_pages, int32_t window, int32_t sink_tokens, float softmax_scale, void* out,
+                        float* lse, void* workspace, size_t workspace_bytes, void* stream) {
+    int st = attend_checks(cache, q, num_q_heads, page_table, seq_lens, batch, max_pages, softmax_scale, out, lse);
+    if (st) return st;
+    if (window < 0 || sink_tokens < 0 || total_q < 0) return SV_ERR_INVALID_ARG;
+    if (!q_start && total_q != batch) return SV_ERR_INVALID_ARG;
+    if (total_q > kMaxQueryTokens) return SV_ERR_UNSUPPORTED;
+    if (!workspace || workspace_bytes < sv_window_attention_workspace_size(batch, num_q_heads, cache->num_kv_heads, total_q))
+        return SV_ERR_WORKSPACE;
+    if (!aligned16(workspace)) return SV_ERR_INVALID_ARG;
+    if (total_q == 0) return SV_OK;
+    int sms = 0;
+    if ((st = sm_count_of_current_device(&sms))) return st;
+    return launch_window(cache, q, num_q_heads, q_start, total_q, page_table, seq_lens, batch, max_pages, window,
+                         sink_tokens, softmax_scale, out, lse, workspace, sms, static_cast<cudaStream_t>(stream));
+}
+
+size_t sv_prefix_decode_workspace_size(int32_t batch, int32_t num_q_heads, int32_t num_kv_heads, int32_t num_groups) {
+    if (!attend_sizes_ok(batch, num_q_heads, num_kv_heads) || num_groups < 1) return 0;
+    return prefix_workspace_bytes(batch, num_q_heads, num_kv_heads, num_groups);
+}
+
+int sv_prefix_decode(const sv_cache* cache, const void* q, int32_t num_q_heads, const int32_t* page_table,
+                     const int32_t* seq_lens, int32_t batch, int32_t max_pages, const int32_t* group_start,
+                     const int32_t* shared_pages, int32_t num_groups, float softmax_scale, void* out, float* lse,
+                     void* workspace, size_t workspace_bytes, void* stream) {
+    int st = attend_checks(cache, q, num_q_heads, page_table, seq_lens, batch, max_pages, softmax_scale, out, lse);
+    if (st) return st;
+    if (!group_start || !shared_pages || num_groups < 1) return SV_ERR_INVALID_ARG;
+    if (num_groups > 65535) return SV_ERR_UNSUPPORTED;
+    if (!workspace || workspace_bytes < sv_prefix_decode_workspace_size(batch, num_q_heads, cache->num_kv_heads, num_groups))
+        return SV_ERR_WORKSPACE;
+    if (!aligned16(workspace)) return SV_ERR_INVALID_ARG;
+    int sms = 0;
+    if ((st = sm_count_of_current_device(&sms))) return st;
+    return launch_prefix(cache, q, num_q_heads, page_table, seq_lens, batch, max_pages, group_start, shared_pages,
+                         num_groups, softmax_scale, out, lse, workspace, sms, static_cast<cudaStream_t>(stream));
+}
+
 int sv_get_device_error(uint32_t* flags, int reset) {
     if (!flags) return SV_ERR_INVALID_ARG;
     *flags = 0;
@@ -342,6 +425,7 @@ int sv_get_device_error(uint32_t* flags, int reset) {
     if ((st = read_error_meta(flags, reset))) return st;
     if ((st = read_error_select(flags, reset))) return st;
     if ((st = read_error_decode_fp8(flags, reset))) return st;
+    if ((st = read_error_attend(flags, reset))) return st;
     return read_error_decode(flags, reset);
 }
 

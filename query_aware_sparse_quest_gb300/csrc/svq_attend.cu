@@ -1,0 +1,1446 @@
+// Attention of query rows over ranges of cached pages on the tcgen05 tensor
+// cores: sliding-window attention with sinks (chunks and single tokens) and
+// decode of requests that share a prefix.
+//
+// Mathematics.  A row tile is up to 256 (query token, query head) pairs that
+// read the same pages of one kv head; 128 of them are one MMA's M side, so the
+// group's query heads share every key and value.  With Q (128 x 128), a key
+// tile K (128 tokens x 128) and a value tile V,
+//   S = Q K^T                  (fp32 in TMEM, 8 MMAs of k = 16 channels)
+//   P = exp2(S * scale - base) (bf16 in TMEM over S; base = a running maximum)
+//   O = O * 2^(old - new base) + P V   (fp32 in TMEM, one MMA of k = 16 per page)
+// and at the end out = O / sum P, lse = ln 2 * (base + log2 sum P).  The sums and
+// bases are fp32.  P is rounded to bf16 because one MMA takes both operands in
+// one type and V is bf16; the sum is taken of the unrounded weights.
+//
+// Work.  The plan lists entries (row tiles with their page ranges) and the
+// running count of 128-token tiles.  Every CTA takes an equal run of the
+// (entry, kv head, tile) sequence, so ragged batches, short windows and long
+// contexts all fill the GPU without a choice of splits; a run that starts or
+// ends inside an item leaves a partial (O, base, sum) in the workspace, joined
+// by a second kernel.  A CTA has at most two such partials, so their traffic
+// does not grow with the problem.
+//
+// Roles of a CTA (one per SM; TMEM holds S0, S1, O0, O1 of 128 columns each):
+//   warp 0       loads pages through a ring of 32 KB stages (TMA, one box a page)
+//   warp 1       issues the MMAs (one thread)
+//   warps 4-7    softmax of stream 0, one row a thread
+//   warps 8-11   softmax of stream 1
+//   warps 12-15  (e4m3 pools) widen the codes to bf16 tiles
+// Two streams keep the tensor cores busy while the other's softmax runs: the
+// two 128-row halves of a tile of more than 128 rows, each over every key
+// tile; or, for up to 128 rows, the even and the odd key tiles of the same
+// rows, joined at the end.
+#include <cuda.h>
+#include <cudaTypedefs.h>
+
+#include <climits>
+
+#include "svq_common.cuh"
+
+namespace svq {
+
+SVQ_DEFINE_ERROR_WORD(read_error_attend)
+
+namespace {
+
+constexpr int kTilePages = 8;                       // pages of a key tile
+constexpr int kTileTok = kTilePages * kPage;        // 128 tokens
+constexpr int kPageBytes = kPage * kHeadDim * 2;    // a page's bf16 tile of one kv head: 4 KB
+constexpr int kStageBytes = kTilePages * kPageBytes;
+constexpr int kRowTile = 256;                       // rows of an entry at most
+constexpr int kInfoSlots = 8;                       // tiles whose page faults / scales are kept (the loads run at most 3 ahead)
+constexpr int kMaxCtas = 160;                       // partial slots in the workspace
+constexpr float kSlack = 8.f;                       // log2 units the base may lag behind the maximum
+constexpr int kColS = 0, kColO = 256;               // TMEM columns of S0 and O0; S1 and O1 lie 128 further
+
+// One row tile and the pages that some row of it sees: the first `sink_pages`
+// logical pages, then pages from w0 on.
+struct __align__(16) Entry {
+    int row0;         // first query token (row of q)
+    int ntok;         // query tokens
+    int pos0;         // position of the first one; kAllVisible: no mask
+    int req;          // page table row
+    int sink_pages;
+    int w0;
+    int npages;       // pages in the list
+    int kind;         // kDirect, kPrefix or kSuffix
+};
+constexpr int kAllVisible = 1 << 30;
+constexpr int kDirect = 0, kPrefix = 1, kSuffix = 2;
+
+__device__ __forceinline__ int tiles_of(int npages) { return (npages + kTilePages - 1) / kTilePages; }
+
+struct Plan {
+    Entry* entries;
+    int64_t* cum;      // [E + 1] tiles per kv head before each entry
+    int* num_entries;
+    int* req_entry;    // kPrefix mode: entry that holds each request's prefix rows, -1: none
+    int* req_offset;   // ragged chunks: first entry of each request
+};
+
+struct AttendArgs {
+    const __nv_bfloat16* q;
+    int num_q_heads, num_kv_heads, group;
+    const int32_t* page_table;
+    int max_pages;
+    int64_t num_phys_pages;
+    const unsigned char* k_pool;
+    const unsigned char* v_pool;
+    const float* k_scale;
+    const float* v_scale;
+    Plan plan;
+    int window;        // INT_MAX: none
+    int sink;
+    float scale_log2;  // softmax_scale * log2(e)
+    __nv_bfloat16* out;
+    float* lse;
+    float* cut_o;      // [2 CTAs][slot_rows][128] partials of items that are cut
+    float2* cut_ml;    // [2 CTAs][slot_rows] (base in log2 units, sum)
+    int slot_rows;
+    float* whole_o[2];    // prefix / suffix parts of whole items, [B Hq][128]
+    float2* whole_ml[2];
+};
+
+// The run of tiles of CTA c: total / ctas each, the first total % ctas one more.
+struct Share {
+    int64_t q, r;
+    __device__ __forceinline__ Share(int64_t total, int ctas) : q(total / ctas), r(total % ctas) {}
+    __device__ __forceinline__ int64_t start(int c) const { return c * q + (c < r ? c : r); }
+    __device__ __forceinline__ int cta_of(int64_t x) const {
+        const int64_t head = r * (q + 1);
+        return static_cast<int>(x < head ? x / (q + 1) : r + (x - head) / q);
+    }
+};
+
+// Largest e in [0, n) with cum[e] <= u, by the whole warp (32 probes a round trip).
+__device__ __forceinline__ int warp_find(const int64_t* cum, int n, int64_t u) {
+    const int lane = threadIdx.x & 31;
+    int lo = 0, len = n;
+    while (len > 1) {
+        const int step = (len + 31) / 32;
+        const int at = lo + lane * step;
+        const bool le = lane * step < len && cum[at] <= u;
+        const int k = __popc(__ballot_sync(0xffffffffu, le)) - 1;   // cum is non-decreasing: a prefix of the lanes
+        const int nlo = lo + max(k, 0) * step;
+        len = min(step, lo + len - nlo);
+        lo = nlo;
+    }
+    return lo;
+}
+
+// ---------------------------------------------------------------- tcgen05
+__device__ __forceinline__ uint64_t smem_desc(uint32_t addr, uint32_t lbo, uint32_t sbo) {
+    return static_cast<uint64_t>((addr & 0x3ffffu) >> 4) | (static_cast<uint64_t>(lbo >> 4) << 16) |
+           (static_cast<uint64_t>(sbo >> 4) << 32) | (1ull << 46) | (2ull << 61);   // version 1, 128-byte swizzle
+}
+// bf16 x bf16 -> fp32, M = 128, N = 128, A K-major; B K-major (keys) or N-major (values).
+constexpr uint32_t kIdescQK = (1u << 4) | (1u << 7) | (1u << 10) | ((128u / 8) << 17) | ((128u / 16) << 24);
+constexpr uint32_t kIdescPV = kIdescQK | (1u << 16);
+
+__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(acc)
+        : "memory");
+}
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d), "r"(a), "l"(b), "r"(idesc), "r"(acc)
+        : "memory");
+}
+__device__ __forceinline__ void mma_commit(uint32_t bar) {
+    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tc_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ void tc_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+__device__ __forceinline__ void tc_ld32(uint32_t addr, uint32_t (&r)[32]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+        "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+        "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
+          "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+          "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+        : "r"(addr));
+}
+__device__ __forceinline__ void tc_st32(uint32_t addr, const uint32_t (&r)[32]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
+        "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,"
+        "%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(addr),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+        "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]),
+        "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]),
+        "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+        : "memory");
+}
+__device__ __forceinline__ void tc_st16(uint32_t addr, const uint32_t (&r)[16]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
+        "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(addr),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+        "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+        : "memory");
+}
+__device__ __forceinline__ void tma_load_4d(uint32_t dst, const void* tmap, int y, uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %2, %2, %3}], [%4];"
+        ::"r"(dst), "l"(tmap), "r"(0), "r"(y), "r"(bar)
+        : "memory");
+}
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// ---------------------------------------------------------------- shared memory
+template <bool FP8>
+struct Cfg {
+    static constexpr int kStages = FP8 ? 3 : 5;
+    static constexpr int kCodeStages = FP8 ? 3 : 0;             // 16 KB of e4m3 codes each
+    static constexpr int kThreads = FP8 ? 512 : 384;
+    static constexpr int kRing = kStages * kStageBytes;
+    static constexpr int kQ = 2 * 128 * kHeadDim * 2;           // one 128-row tile a stream
+    static constexpr int kCodes = kCodeStages * kTileTok * kHeadDim;
+    static constexpr int kScales = FP8 ? kInfoSlots * 2 * kTileTok * 4 : 0;
+    static constexpr int kControl = 3072;
+    static constexpr int kSmem = kRing + kQ + kCodes + kScales + kControl;
+};
+static_assert(Cfg<false>::kSmem <= 227 * 1024 && Cfg<true>::kSmem <= 227 * 1024, "shared memory of one CTA");
+
+struct Control {
+    uint64_t full[5], empty[5];       // ring stages
+    uint64_t code_full[3], code_empty[3];
+    uint64_t s_full[2], p_full[2], o_full[2], q_full[2];
+    uint64_t join[2];                 // both streams have published their statistics / have read O0 and O1
+    uint64_t drain;
+    uint32_t tmem;
+    int start_e, start_h;
+    int64_t start_t;
+    int fault[kInfoSlots];            // pages of a tile that the table does not give
+    float2 ml[2][128];                // stream statistics of a joined tile
+};
+static_assert(sizeof(Control) <= 3072, "control block");
+
+// A run of tiles of one item (entry, kv head).
+struct Seg {
+    Entry en;
+    int h;        // kv head
+    int t0, t1;   // tiles of the item
+    int tiles;    // of the whole item
+};
+
+// The CTA's segments in order; every role walks its own copy.
+struct Walk {
+    const AttendArgs& a;
+    int e, h, t;
+    int64_t left;   // tiles still to walk
+    __device__ __forceinline__ Walk(const AttendArgs& args, const Control* c, int64_t n)
+        : a(args), e(c->start_e), h(c->start_h), t(static_cast<int>(c->start_t)), left(n) {}
+    __device__ __forceinline__ bool next(Seg& s) {
+        if (left <= 0) return false;
+        const int4* p = reinterpret_cast<const int4*>(a.plan.entries + e);
+        int4 x = p[0], y = p[1];
+        while (y.z == 0) {   // entries without pages
+            ++e;
+            p += 2;
+            x = p[0];
+            y = p[1];
+        }
+        s.en = Entry{x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
+        s.h = h;
+        s.tiles = tiles_of(y.z);
+        s.t0 = t;
+        const int64_t n = min(left, static_cast<int64_t>(s.tiles - t));
+        s.t1 = t + static_cast<int>(n);
+        left -= n;
+        t = 0;
+        if (s.t1 == s.tiles && ++h == a.num_kv_heads) {
+            h = 0;
+            ++e;
+        }
+        return true;
+    }
+};
+
+__device__ __forceinline__ int logical_page(const Entry& en, int i) {
+    return i < en.sink_pages ? i : en.w0 + i - en.sink_pages;
+}
+// Bit t: some row of the entry (positions qlo .. qhi) sees token t of the page.
+__device__ __forceinline__ uint32_t union_mask(int base, int qlo, int qhi, int window, int sink) {
+    const int hi = min(16, qhi - base + 1);
+    if (hi <= 0) return 0u;
+    const int lo = max(0, min(16, max(0, qlo - window + 1) - base));
+    const int sk = max(0, min(16, sink - base));
+    return ((1u << hi) - 1u) & (~((1u << lo) - 1u) | ((1u << sk) - 1u));
+}
+// Bit t: the row at position qpos does.
+__device__ __forceinline__ uint32_t page_mask(int base, int qpos, int window, int sink) {
+    return union_mask(base, qpos, qpos, window, sink);
+}
+__device__ __forceinline__ int last_pos(const Entry& en) {
+    return en.pos0 == kAllVisible ? kAllVisible : en.pos0 + en.ntok - 1;
+}
+
+// Four e4m3 codes -> two bf16 pairs, exactly: the code's exponent and mantissa
+// fields are moved under bf16's, which scales the value by 2^-120; the product
+// with 2^120 is exact, subnormal codes included.  The two NaN codes, which that
+// would read as +-480, stay NaN.
+__device__ __forceinline__ void widen4(uint32_t c, uint32_t& lo, uint32_t& hi) {
+    const uint32_t a = __byte_perm(c, 0u, 0x1404);   // bytes 1, 0 of c in the high bytes of the halves
+    const uint32_t b = __byte_perm(c, 0u, 0x3424);
+    const uint32_t x = ((a & 0x7f007f00u) >> 4) | (a & 0x80008000u);
+    const uint32_t y = ((b & 0x7f007f00u) >> 4) | (b & 0x80008000u);
+    const __nv_bfloat162 two120 = __halves2bfloat162(__ushort_as_bfloat16(0x7b80), __ushort_as_bfloat16(0x7b80));
+    const __nv_bfloat162 xr = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&x), two120);
+    const __nv_bfloat162 yr = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&y), two120);
+    lo = *reinterpret_cast<const uint32_t*>(&xr);
+    hi = *reinterpret_cast<const uint32_t*>(&yr);
+    const uint32_t nan = __vcmpeq4(c & 0x7f7f7f7fu, 0x7f7f7f7fu);
+    if (nan) {
+        if (nan & 0x000000ffu) lo |= 0x00007fffu;
+        if (nan & 0x0000ff00u) lo |= 0x7fff0000u;
+        if (nan & 0x00ff0000u) hi |= 0x00007fffu;
+        if (nan & 0xff000000u) hi |= 0x7fff0000u;
+    }
+}
+
+// A bounded wait by a whole warp; all of it leaves for `out` when it gave up.
+#define SVQ_WAIT(bar, parity, out)                                                        \
+    do {                                                                                  \
+        if (__any_sync(0xffffffffu, !mbar_wait_bounded(smem_addr(&(bar)), (parity)))) {   \
+            if (lane == 0) svq_flag(SV_DEVERR_TIMEOUT);                                   \
+            goto out;                                                                     \
+        }                                                                                 \
+    } while (0)
+
+template <bool FP8>
+__global__ void __launch_bounds__(Cfg<FP8>::kThreads, 1)
+    attend_kernel(const __grid_constant__ AttendArgs a, const __grid_constant__ CUtensorMap tmap_k,
+                  const __grid_constant__ CUtensorMap tmap_v) {
+    using C = Cfg<FP8>;
+    extern __shared__ __align__(1024) unsigned char smem[];
+    unsigned char* const ring = smem;
+    unsigned char* const qs = smem + C::kRing;
+    unsigned char* const codes = qs + C::kQ;
+    float* const scales = reinterpret_cast<float*>(codes + C::kCodes);   // [slot][K | V][128]
+    Control* const ct = reinterpret_cast<Control*>(codes + C::kCodes + C::kScales);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int group = a.group;
+
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < C::kStages; ++i) {
+            mbar_init(smem_addr(&ct->full[i]), FP8 ? 4 : 1);
+            mbar_init(smem_addr(&ct->empty[i]), 1);
+        }
+        for (int i = 0; i < C::kCodeStages; ++i) {
+            mbar_init(smem_addr(&ct->code_full[i]), 1);
+            mbar_init(smem_addr(&ct->code_empty[i]), 4);
+        }
+        for (int w = 0; w < 2; ++w) {
+            mbar_init(smem_addr(&ct->s_full[w]), 1);
+            mbar_init(smem_addr(&ct->p_full[w]), 4);
+            mbar_init(smem_addr(&ct->o_full[w]), 1);
+            mbar_init(smem_addr(&ct->q_full[w]), 128);
+        }
+        mbar_init(smem_addr(&ct->join[0]), 256);
+        mbar_init(smem_addr(&ct->join[1]), 256);
+        mbar_init(smem_addr(&ct->drain), 1);
+        mbar_init_fence();
+        if (!FP8) {
+            prefetch_tmap(&tmap_k);
+            prefetch_tmap(&tmap_v);
+        }
+    }
+    if (warp == 1) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_addr(&ct->tmem))
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    }
+    pdl_wait();   // the plan comes from the kernel launched just before
+    pdl_launch_dependents();
+    const int num_entries = *a.plan.num_entries;
+    const int64_t total = a.plan.cum[num_entries] * a.num_kv_heads;
+    const Share share(total, gridDim.x);
+    const int64_t first = share.start(blockIdx.x);
+    const int64_t count = share.start(blockIdx.x + 1) - first;
+    if (warp == 2 && count > 0) {
+        const int e = warp_find(a.plan.cum, num_entries, first / a.num_kv_heads);
+        if (lane == 0) {
+            const int tiles = tiles_of(a.plan.entries[e].npages);
+            const int64_t in = first - a.plan.cum[e] * a.num_kv_heads;
+            ct->start_e = e;
+            ct->start_h = static_cast<int>(in / tiles);
+            ct->start_t = in % tiles;
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = ct->tmem;
+
+    if (count > 0) {
+        if (warp == 0) {
+            // ---------------- loads
+            Walk walk(a, ct, count);
+            Seg s;
+            uint32_t ld = 0, tile = 0;   // loads and key tiles issued
+            constexpr int kDepth = FP8 ? C::kCodeStages : C::kStages;
+            while (walk.next(s)) {
+                const int n = s.t1 - s.t0;
+                const int qlo = s.en.pos0, qhi = last_pos(s.en);
+                const int32_t* row = a.page_table + static_cast<int64_t>(s.en.req) * a.max_pages;
+                // Lane l resolves page l of a tile one tile ahead of its loads.
+                auto fetch = [&](int t, int& lp, int& ph) {
+                    const int i = t * kTilePages + lane;
+                    lp = ph = -1;
+                    if (lane < kTilePages && i < s.en.npages && t < s.t1) {
+                        lp = logical_page(s.en, i);
+                        ph = row[lp];
+                    }
+                };
+                int lp, ph, lp_next, ph_next, lp_prev = -1, ph_prev = -1;
+                fetch(s.t0, lp_next, ph_next);
+                for (int i = 0; i <= n; ++i) {
+                    lp = lp_next;
+                    ph = ph_next;
+                    fetch(s.t0 + i + 1, lp_next, ph_next);
+                    // K of tile i, then V of tile i - 1.
+#pragma unroll
+                    for (int kv = 0; kv < 2; ++kv) {
+                        if (kv == 0 ? i == n : i == 0) continue;
+                        const int my_lp = kv == 0 ? lp : lp_prev;
+                        int my_ph = kv == 0 ? ph : ph_prev;
+                        const bool bad = my_lp >= 0 && (my_ph < 0 || my_ph >= a.num_phys_pages);
+                        const uint32_t faults = __ballot_sync(0xffffffffu, bad);
+                        const int st = ld % kDepth;
+                        uint64_t* const full = FP8 ? &ct->code_full[st] : &ct->full[st];
+                        uint64_t* const empty = FP8 ? &ct->code_empty[st] : &ct->empty[st];
+                        SVQ_WAIT(*empty, ((ld / kDepth) & 1) ^ 1, loads_end);
+                        const uint32_t bar = smem_addr(full);
+                        const bool load = my_lp >= 0 && !bad;
+                        if (kv == 0 && lane == 0) ct->fault[tile % kInfoSlots] = static_cast<int>(faults);
+                        if (faults && lane == 0) svq_flag(SV_DEVERR_PAGE_TABLE);
+                        const int64_t at = (static_cast<int64_t>(load ? my_ph : 0) * a.num_kv_heads + s.h);
+                        if (FP8) {
+                            const uint32_t loads = __ballot_sync(0xffffffffu, load);
+                            const uint32_t bytes = __popc(loads) * (kPage * kHeadDim + (kv == 0 ? 2 * kPage * 4 : 0));
+                            if (lane == 0) {
+                                if (bytes) mbar_arrive_expect_tx(bar, bytes);
+                                else mbar_arrive(bar);
+                            }
+                            __syncwarp();
+                            if (load) {
+                                const uint32_t dst = smem_addr(codes) + st * (kTileTok * kHeadDim) + lane * (kPage * kHeadDim);
+                                bulk_copy_g2s(dst, (kv == 0 ? a.k_pool : a.v_pool) + at * (kPage * kHeadDim),
+                                              kPage * kHeadDim, bar);
+                                if (kv == 0) {
+                                    const uint32_t sc = smem_addr(scales + (tile % kInfoSlots) * 2 * kTileTok + lane * kPage);
+                                    bulk_copy_g2s(sc, a.k_scale + at * kPage, kPage * 4, bar);
+                                    bulk_copy_g2s(sc + kTileTok * 4, a.v_scale + at * kPage, kPage * 4, bar);
+                                }
+                            }
+                        } else {
+                            // A value page with tokens that no row sees (they may hold anything) is
+                            // copied by the warp with zeros in their place, so that P = 0 never
+                            // meets a NaN; a page the table does not give is all zeros.
+                            const uint32_t seen = my_lp < 0 ? 0u : union_mask(my_lp * kPage, qlo, qhi, a.window, a.sink);
+                            const bool part = kv == 1 && my_lp >= 0 && (bad || seen != 0xffffu);
+                            const uint32_t parts = __ballot_sync(0xffffffffu, part);
+                            const uint32_t loads = __ballot_sync(0xffffffffu, load && !part);
+                            unsigned char* const stage = ring + st * kStageBytes;
+                            for (uint32_t rest = parts; rest; rest &= rest - 1) {
+                                const int p = __ffs(rest) - 1;
+                                const uint32_t m = __shfl_sync(0xffffffffu, bad ? 0u : seen, p);
+                                const int64_t from = __shfl_sync(0xffffffffu, at, p);
+                                const uint4* src = reinterpret_cast<const uint4*>(a.v_pool + from * kPageBytes);
+#pragma unroll
+                                for (int k = 0; k < 8; ++k) {
+                                    const int r = 2 * k + (lane >> 4), c = lane & 15;
+                                    const uint4 v = (m >> r) & 1u ? src[r * 16 + c] : make_uint4(0u, 0u, 0u, 0u);
+                                    *reinterpret_cast<uint4*>(stage + p * kPageBytes + (r >> 3) * 2048 + (c >> 3) * 1024 +
+                                                              (r & 7) * 128 + (((c & 7) ^ (r & 7)) << 4)) = v;
+                                }
+                            }
+                            if (parts) fence_proxy_async_smem();
+                            __syncwarp();
+                            if (lane == 0) {
+                                if (loads) mbar_arrive_expect_tx(bar, __popc(loads) * kPageBytes);
+                                else mbar_arrive(bar);
+                            }
+                            __syncwarp();
+                            if (load && !part)
+                                tma_load_4d(smem_addr(stage) + lane * kPageBytes,
+                                            kv == 0 ? static_cast<const void*>(&tmap_k) : static_cast<const void*>(&tmap_v),
+                                            static_cast<int>(at * 2), bar);
+                        }
+                        ++ld;
+                        if (kv == 0) ++tile;
+                    }
+                    lp_prev = lp;
+                    ph_prev = ph;
+                }
+            }
+        loads_end:
+            // The copies in flight land before the CTA (and its shared memory) retires.
+            for (uint32_t i = ld > kDepth ? ld - kDepth : 0; i < ld; ++i) {
+                uint64_t* const full = FP8 ? &ct->code_full[i % kDepth] : &ct->full[i % kDepth];
+                (void)mbar_wait_bounded(smem_addr(full), (i / kDepth) & 1);
+            }
+        } else if (warp == 1) {
+            // ---------------- MMAs (one thread)
+            if (lane == 0) {
+                Walk walk(a, ct, count);
+                Seg s;
+                uint32_t ld = 0;
+                uint32_t q_ph[2] = {0, 0}, p_ph[2] = {0, 0};
+                const uint32_t ring_s = smem_addr(ring), qs_s = smem_addr(qs);
+                while (walk.next(s)) {
+                    const int n = s.t1 - s.t0;
+                    const bool two = s.en.ntok * group > 128;   // two row halves; else even and odd tiles
+                    // Loads of the segment in order: K0 K1 V0 K2 V1 .. K(n-1) V(n-2) V(n-1).
+                    auto k_at = [&](int t) { return ld + (t == 0 ? 0u : 2u * t - 1u); };
+                    auto v_at = [&](int t) { return ld + (t == n - 1 ? 2u * n - 1u : 2u * t + 2u); };
+                    auto wait_load = [&](uint32_t i) {
+                        return mbar_wait_bounded(smem_addr(&ct->full[i % C::kStages]), (i / C::kStages) & 1);
+                    };
+                    auto qk = [&](int w, int t) {
+                        if (!wait_load(k_at(t))) return false;
+                        tc_fence_after();
+                        const uint32_t ks = ring_s + (k_at(t) % C::kStages) * kStageBytes;
+                        const uint32_t qw = qs_s + w * (128 * kHeadDim * 2);
+#pragma unroll
+                        for (int k = 0; k < 8; ++k)
+                            mma_ss(tmem + kColS + w * 128, smem_desc(qw + (k >> 2) * 16384 + (k & 3) * 32, 16, 1024),
+                                   smem_desc(ks + (k >> 2) * 1024 + (k & 3) * 32, 16, 2048), kIdescQK, k != 0);
+                        mma_commit(smem_addr(&ct->s_full[w]));
+                        return true;
+                    };
+                    auto pv = [&](int w, int t, bool acc) {
+                        if (!wait_load(v_at(t))) return false;
+                        tc_fence_after();
+                        const uint32_t vs = ring_s + (v_at(t) % C::kStages) * kStageBytes;
+                        const int pages = min(kTilePages, s.en.npages - (s.t0 + t) * kTilePages);
+                        for (int k = 0; k < pages; ++k)
+                            mma_ts(tmem + kColO + w * 128, tmem + kColS + w * 128 + k * 8, smem_desc(vs + k * kPageBytes, 1024, 2048),
+                                   kIdescPV, acc || k != 0);
+                        return true;
+                    };
+                    auto release = [&](uint32_t i) { mma_commit(smem_addr(&ct->empty[i % C::kStages])); };
+                    bool ok = true;
+                    for (int w = 0; w < 2 && ok; ++w) {
+                        const int t = two ? 0 : w;
+                        if (t >= n) break;
+                        ok = mbar_wait_bounded(smem_addr(&ct->q_full[w]), q_ph[w]) && qk(w, t);
+                        q_ph[w] ^= 1;
+                        if (ok && (!two || w == 1)) release(k_at(t));
+                    }
+                    for (int t = 0; t < n && ok; ++t) {
+                        for (int v = 0; v < 2 && ok; ++v) {
+                            if (!two && v != (t & 1)) continue;
+                            const int w = v;
+                            const int step = two ? 1 : 2;
+                            ok = mbar_wait_bounded(smem_addr(&ct->p_full[w]), p_ph[w]);
+                            p_ph[w] ^= 1;
+                            ok = ok && pv(w, t, t >= step);
+                            if (!ok) break;
+                            if (!two || w == 1) release(v_at(t));
+                            if (t + step < n) {
+                                ok = qk(w, t + step);
+                                if (ok && (!two || w == 1)) release(k_at(t + step));
+                            } else {
+                                mma_commit(smem_addr(&ct->o_full[w]));
+                            }
+                        }
+                    }
+                    if (!ok) {
+                        svq_flag(SV_DEVERR_TIMEOUT);
+                        break;
+                    }
+                    ld += 2 * n;
+                }
+                mma_commit(smem_addr(&ct->drain));   // nothing of this CTA's is in flight when TMEM is freed
+                (void)mbar_wait_bounded(smem_addr(&ct->drain), 0);
+            }
+            __syncwarp();
+        } else if (warp >= 4 && warp < 12) {
+            // ---------------- softmax: warps 4-7 stream 0, warps 8-11 stream 1
+            const int w = (warp - 4) >> 2;
+            const int row = (warp & 3) * 32 + lane;
+            const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
+            const uint32_t s_col = tmem + lanes + kColS + w * 128;
+            const uint32_t o_col = tmem + lanes + kColO + w * 128;
+            Walk walk(a, ct, count);
+            Seg s, nx;
+            uint32_t s_ph = 0, o_ph0 = 0, o_ph1 = 0, join_ph = 0;
+            uint32_t tile0 = 0;          // key tiles of the CTA before the segment
+            bool more = walk.next(s);
+            bool first_seg = true;
+            auto stream_tiles = [&](const Seg& g) {
+                const int n = g.t1 - g.t0;
+                return g.en.ntok * group > 128 ? n : (n - w + 1) / 2;
+            };
+            // The stream's 128 rows of Q, 128-byte swizzled, two halves of 64 channels.
+            auto load_q = [&](const Seg& g) {
+                const int rows = g.en.ntok * group;
+                const int off = rows > 128 ? w * 128 : 0;
+                const int tid = row, c = tid & 15;
+                const uint32_t dst = smem_addr(qs) + w * (128 * kHeadDim * 2) + (c >> 3) * 16384;
+                for (int r = tid >> 4; r < 128 && off + r < rows; r += 8) {
+                    const int tok = (off + r) / group, head = (off + r) - tok * group;
+                    const __nv_bfloat16* src =
+                        a.q + (static_cast<int64_t>(g.en.row0 + tok) * a.num_q_heads + g.h * group + head) * kHeadDim + c * 8;
+                    cp_async16(dst + r * 128 + (((c & 7) ^ (r & 7)) << 4), src, 16);
+                }
+                cp_async_commit();
+            };
+            auto q_ready = [&] {
+                cp_async_wait<0>();
+                fence_proxy_async_smem();
+                mbar_arrive(smem_addr(&ct->q_full[w]));
+            };
+            if (more && stream_tiles(s) > 0) {
+                load_q(s);
+                q_ready();
+            }
+            while (more) {
+                const bool have_next = walk.next(nx);
+                const bool next_q = have_next && stream_tiles(nx) > 0;
+                const int n = s.t1 - s.t0;
+                const int rows = s.en.ntok * group;
+                const bool two = rows > 128;
+                const int nt = stream_tiles(s);
+                const int off = two ? w * 128 : 0;
+                const int r = off + row;
+                const bool valid = r < rows;
+                const bool warp_on = off + (warp & 3) * 32 < rows;
+                const int tok = r / group;
+                const bool all = s.en.pos0 == kAllVisible;
+                const int qpos = all ? kAllVisible : s.en.pos0 + min(tok, s.en.ntok - 1);
+                const int qlo = all ? kAllVisible : s.en.pos0 + off / group;
+                const int qhi = all ? kAllVisible : s.en.pos0 + (min(rows, off + 128) - 1) / group;
+                float m = -INFINITY, l = 0.f;
+                for (int j = 0; j < nt; ++j) {
+                    const int ti = two ? j : 2 * j + w;          // tile of the segment
+                    const int i0 = (s.t0 + ti) * kTilePages;     // first page of the tile in the list
+                    const int slot = (tile0 + ti) % kInfoSlots;
+                    SVQ_WAIT(ct->s_full[w], s_ph, softmax_end);
+                    s_ph ^= 1;
+                    tc_fence_after();
+                    if (j == nt - 1 && next_q) load_q(nx);       // the stream's last use of Q is over
+                    if (warp_on) {
+                        const int fault = ct->fault[slot];
+                        const int base0 = logical_page(s.en, i0) * kPage;
+                        const int base7 = logical_page(s.en, i0 + 7) * kPage;
+                        const bool plain = !fault && i0 + kTilePages <= s.en.npages && base7 - base0 == 7 * kPage &&
+                                           base7 + 15 <= qlo && (base0 > qhi - a.window || base7 + 15 < a.sink);
+                        auto mask_of = [&](int c) {   // the 32 columns from 32 c on: two pages
+                            uint32_t bits = 0;
+#pragma unroll
+                            for (int u = 0; u < 2; ++u) {
+                                const int i = i0 + 2 * c + u;
+                                if (i < s.en.npages && !((fault >> (2 * c + u)) & 1))
+                                    bits |= page_mask(logical_page(s.en, i) * kPage, qpos, a.window, a.sink) << (16 * u);
+                            }
+                            return bits;
+                        };
+                        const float4* ks = reinterpret_cast<const float4*>(scales + slot * 2 * kTileTok);
+                        const float4* vs = ks + kTileTok / 4;
+                        // Pass 1: the tile's maximum.
+                        float mx = -INFINITY;
+#pragma unroll
+                        for (int c = 0; c < 4; ++c) {
+                            uint32_t x[32];
+                            tc_ld32(s_col + c * 32, x);
+                            tc_wait_ld();
+                            if (FP8) {
+#pragma unroll
+                                for (int u = 0; u < 8; ++u) {
+                                    const float4 k4 = ks[c * 8 + u];
+                                    x[4 * u] = __float_as_uint(__uint_as_float(x[4 * u]) * k4.x);
+                                    x[4 * u + 1] = __float_as_uint(__uint_as_float(x[4 * u + 1]) * k4.y);
+                                    x[4 * u + 2] = __float_as_uint(__uint_as_float(x[4 * u + 2]) * k4.z);
+                                    x[4 * u + 3] = __float_as_uint(__uint_as_float(x[4 * u + 3]) * k4.w);
+                                }
+                            }
+                            if (plain) {
+#pragma unroll
+                                for (int u = 0; u < 32; u += 2)
+                                    mx = fmaxf(fmaxf(mx, __uint_as_float(x[u])), __uint_as_float(x[u + 1]));
+                            } else {
+                                const uint32_t bits = mask_of(c);
+#pragma unroll
+                                for (int u = 0; u < 32; ++u)
+                                    mx = fmaxf(mx, (bits >> u) & 1u ? __uint_as_float(x[u]) : -INFINITY);
+                            }
+                        }
+                        mx *= a.scale_log2;
+                        // The base moves only when the maximum is more than kSlack above it; weights
+                        // stay at most 2^kSlack, and sums and outputs share the base.
+                        if (__any_sync(0xffffffffu, mx > m + kSlack)) {
+                            const float mn = fmaxf(m, mx);
+                            const float alpha = mn == -INFINITY ? 1.f : ex2(m - mn);
+                            m = mn;
+                            l *= alpha;
+                            if (j > 0) {   // S of this tile is complete, so the MMAs into O before it are
+#pragma unroll
+                                for (int c = 0; c < 4; ++c) {
+                                    uint32_t x[32];
+                                    tc_ld32(o_col + c * 32, x);
+                                    tc_wait_ld();
+#pragma unroll
+                                    for (int u = 0; u < 32; ++u) x[u] = __float_as_uint(__uint_as_float(x[u]) * alpha);
+                                    tc_st32(o_col + c * 32, x);
+                                }
+                            }
+                        }
+                        const float base = m == -INFINITY ? 0.f : m;
+                        // Pass 2: weights, their sum, and P in bf16 over the columns already read.
+#pragma unroll
+                        for (int c = 0; c < 4; ++c) {
+                            uint32_t x[32], p[16];
+                            tc_ld32(s_col + c * 32, x);
+                            tc_wait_ld();
+                            if (FP8) {
+#pragma unroll
+                                for (int u = 0; u < 8; ++u) {
+                                    const float4 k4 = ks[c * 8 + u];
+                                    x[4 * u] = __float_as_uint(__uint_as_float(x[4 * u]) * k4.x);
+                                    x[4 * u + 1] = __float_as_uint(__uint_as_float(x[4 * u + 1]) * k4.y);
+                                    x[4 * u + 2] = __float_as_uint(__uint_as_float(x[4 * u + 2]) * k4.z);
+                                    x[4 * u + 3] = __float_as_uint(__uint_as_float(x[4 * u + 3]) * k4.w);
+                                }
+                            }
+                            float e[32];
+#pragma unroll
+                            for (int u = 0; u < 32; ++u) e[u] = ex2(fmaf(__uint_as_float(x[u]), a.scale_log2, -base));
+                            if (!plain) {
+                                const uint32_t bits = mask_of(c);
+#pragma unroll
+                                for (int u = 0; u < 32; ++u) e[u] = (bits >> u) & 1u ? e[u] : 0.f;
+                            }
+                            float s0 = 0.f, s1 = 0.f;
+#pragma unroll
+                            for (int u = 0; u < 32; u += 2) {
+                                s0 += e[u];
+                                s1 += e[u + 1];
+                            }
+                            l += s0 + s1;
+                            if (FP8) {
+#pragma unroll
+                                for (int u = 0; u < 8; ++u) {
+                                    const float4 v4 = vs[c * 8 + u];
+                                    e[4 * u] *= v4.x;
+                                    e[4 * u + 1] *= v4.y;
+                                    e[4 * u + 2] *= v4.z;
+                                    e[4 * u + 3] *= v4.w;
+                                }
+                            }
+#pragma unroll
+                            for (int u = 0; u < 16; ++u) p[u] = pack_bf16x2(e[2 * u], e[2 * u + 1]);
+                            tc_st16(s_col + c * 16, p);
+                        }
+                        tc_wait_st();
+                    }
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(smem_addr(&ct->p_full[w]));
+                }
+                if (nt == 0 && next_q) load_q(nx);
+                if (next_q) q_ready();
+
+                // ---------------- the segment's end
+                const bool whole = s.t0 == 0 && s.t1 == s.tiles;
+                float* po = nullptr;        // this row's fp32 partial
+                float2* pml = nullptr;
+                const int hr = r - tok * group;
+                const int64_t qrow = static_cast<int64_t>(s.en.row0 + tok) * a.num_q_heads + s.h * group + hr;
+                if (!whole) {
+                    const int64_t at = static_cast<int64_t>(blockIdx.x * 2 + (first_seg ? 0 : 1)) * a.slot_rows + r;
+                    po = a.cut_o + at * kHeadDim;
+                    pml = a.cut_ml + at;
+                } else if (s.en.kind != kDirect) {
+                    po = a.whole_o[s.en.kind - 1] + qrow * kHeadDim;
+                    pml = a.whole_ml[s.en.kind - 1] + qrow;
+                }
+                float f0 = 1.f, f1 = 0.f;   // factors of O0 and O1 (f0: of the own O when there are two row halves)
+                float M = m, L = l;
+                if (two) {
+                    SVQ_WAIT(ct->o_full[w], w ? o_ph1 : o_ph0, softmax_end);
+                    o_ph0 ^= 1;
+                    o_ph1 ^= 1;
+                } else {
+                    SVQ_WAIT(ct->o_full[0], o_ph0, softmax_end);
+                    o_ph0 ^= 1;
+                    if (n > 1) {
+                        SVQ_WAIT(ct->o_full[1], o_ph1, softmax_end);
+                        o_ph1 ^= 1;
+                    }
+                    ct->ml[w][row] = make_float2(m, l);
+                    mbar_arrive(smem_addr(&ct->join[0]));
+                    SVQ_WAIT(ct->join[0], join_ph, softmax_end);
+                    const float2 other = ct->ml[1 - w][row];
+                    M = fmaxf(m, other.x);
+                    const float mine = M == -INFINITY ? 0.f : ex2(m - M), theirs = M == -INFINITY ? 0.f : ex2(other.x - M);
+                    L = l * mine + other.y * theirs;
+                    f0 = w == 0 ? mine : theirs;
+                    f1 = w == 0 ? theirs : mine;
+                }
+                tc_fence_after();
+                if (warp_on) {
+                    const float inv = po ? 1.f : (L > 0.f ? 1.f / L : (L == 0.f ? 0.f : L));
+                    f0 *= inv;
+                    f1 *= inv;
+                    // Two halves: the whole row of the own stream.  Joined: 64 channels of both.
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) {
+                        if (!two && (c >> 1) != w) continue;
+                        uint32_t x[32];
+                        tc_ld32(tmem + lanes + (two ? kColO + w * 128 : kColO) + c * 32, x);
+                        tc_wait_ld();
+#pragma unroll
+                        for (int u = 0; u < 32; ++u) x[u] = __float_as_uint(__uint_as_float(x[u]) * f0);
+                        if (!two && n > 1) {
+                            uint32_t y[32];
+                            tc_ld32(tmem + lanes + kColO + 128 + c * 32, y);
+                            tc_wait_ld();
+#pragma unroll
+                            for (int u = 0; u < 32; ++u)
+                                x[u] = __float_as_uint(fmaf(__uint_as_float(y[u]), f1, __uint_as_float(x[u])));
+                        }
+                        if (valid) {
+                            if (po) {
+#pragma unroll
+                                for (int u = 0; u < 8; ++u)
+                                    *reinterpret_cast<uint4*>(po + c * 32 + 4 * u) =
+                                        make_uint4(x[4 * u], x[4 * u + 1], x[4 * u + 2], x[4 * u + 3]);
+                            } else {
+#pragma unroll
+                                for (int u = 0; u < 4; ++u) {
+                                    uint4 v;
+                                    v.x = pack_bf16x2(__uint_as_float(x[8 * u]), __uint_as_float(x[8 * u + 1]));
+                                    v.y = pack_bf16x2(__uint_as_float(x[8 * u + 2]), __uint_as_float(x[8 * u + 3]));
+                                    v.z = pack_bf16x2(__uint_as_float(x[8 * u + 4]), __uint_as_float(x[8 * u + 5]));
+                                    v.w = pack_bf16x2(__uint_as_float(x[8 * u + 6]), __uint_as_float(x[8 * u + 7]));
+                                    *reinterpret_cast<uint4*>(a.out + qrow * kHeadDim + c * 32 + 8 * u) = v;
+                                }
+                            }
+                        }
+                    }
+                    if (valid && (two || w == 0)) {
+                        if (po) *pml = make_float2(M, L);
+                        else a.lse[qrow] = L > 0.f ? (M + log2f(L)) * 0.69314718055994531f : (L == 0.f ? -INFINITY : L);
+                    }
+                }
+                // Joined tiles: both halves of the CTA have read O0 and O1 before either is written again.
+                tc_fence_before();
+                if (!two) {
+                    mbar_arrive(smem_addr(&ct->join[1]));
+                    SVQ_WAIT(ct->join[1], join_ph, softmax_end);
+                    join_ph ^= 1;
+                }
+                tile0 += n;
+                first_seg = false;
+                s = nx;
+                more = have_next;
+            }
+        softmax_end:;
+        } else if (FP8 && warp >= 12) {
+            // ---------------- e4m3 codes -> bf16 tiles in the MMAs' layout
+            Walk walk(a, ct, count);
+            Seg s;
+            const int tid = threadIdx.x - 384;
+            uint32_t ld = 0, tile = 0;
+            constexpr int kCodeDepth = FP8 ? C::kCodeStages : 1;
+            while (walk.next(s)) {
+                const int n = s.t1 - s.t0;
+                const int qlo = s.en.pos0, qhi = last_pos(s.en);
+                for (int i = 0; i < 2 * n; ++i) {
+                    // The loads' order: K0 K1 V0 K2 V1 .. V(n-1).
+                    const bool is_k = i == 0 || (i != 2 * n - 1 && (i & 1));
+                    const int t = is_k ? (i + 1) / 2 : (i == 2 * n - 1 ? n - 1 : i / 2 - 1);
+                    const int slot = (tile + t) % kInfoSlots;
+                    const int cs = ld % kCodeDepth, st = ld % C::kStages;
+                    SVQ_WAIT(ct->code_full[cs], (ld / kCodeDepth) & 1, widen_end);
+                    SVQ_WAIT(ct->empty[st], ((ld / C::kStages) & 1) ^ 1, widen_end);
+                    const unsigned char* src = codes + cs * (kTileTok * kHeadDim);
+                    unsigned char* dst = ring + st * kStageBytes;
+                    const int i0 = (s.t0 + t) * kTilePages;
+                    const int fault = ct->fault[slot];
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) {
+                        // Pass k is page k of the tile: thread -> row tid / 8, 16 codes at chunk tid % 8.
+                        const int r = tid >> 3, c = tid & 7;
+                        const int pi = i0 + k;
+                        uint32_t seen = 0;
+                        if (pi < s.en.npages && !((fault >> k) & 1))
+                            seen = union_mask(logical_page(s.en, pi) * kPage, qlo, qhi, a.window, a.sink);
+                        const bool on = (seen >> r) & 1u;
+                        uint4 v = *reinterpret_cast<const uint4*>(src + k * (kPage * kHeadDim) + r * kHeadDim + c * 16);
+                        if (!on) v = make_uint4(0u, 0u, 0u, 0u);   // tokens no row sees may hold anything
+                        uint4 lo, hi;
+                        widen4(v.x, lo.x, lo.y);
+                        widen4(v.y, lo.z, lo.w);
+                        widen4(v.z, hi.x, hi.y);
+                        widen4(v.w, hi.z, hi.w);
+                        unsigned char* o = dst + k * kPageBytes + (r >> 3) * 2048 + (c >> 2) * 1024 + (r & 7) * 128;
+                        *reinterpret_cast<uint4*>(o + ((((2 * c) & 7) ^ (r & 7)) << 4)) = lo;
+                        *reinterpret_cast<uint4*>(o + ((((2 * c + 1) & 7) ^ (r & 7)) << 4)) = hi;
+                        if (is_k && c == 0 && !on) {
+                            scales[slot * 2 * kTileTok + k * kPage + r] = 0.f;
+                            scales[slot * 2 * kTileTok + kTileTok + k * kPage + r] = 0.f;
+                        }
+                    }
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) {
+                        mbar_arrive(smem_addr(&ct->full[st]));
+                        mbar_arrive(smem_addr(&ct->code_empty[cs]));
+                    }
+                    ++ld;
+                }
+                tile += n;
+            }
+        widen_end:;
+        }
+    }
+    __syncthreads();
+    if (warp == 1)
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem));
+}
+
+// ---------------------------------------------------------------- plan
+struct PlanArgs {
+    Plan plan;
+    int max_entries;
+    int tok_per_entry;          // query tokens of a row tile: kRowTile / group
+    const int32_t* q_start;     // nullptr: one token a request
+    int total_q;
+    const int32_t* seq_lens;
+    int batch;
+    int max_pages;
+    int window;                 // INT_MAX: none
+    int sink;
+    const int32_t* group_start; // prefix mode
+    const int32_t* shared_pages;
+    int num_groups;
+    int num_q_heads;
+    __nv_bfloat16* out;         // window mode: rows that see nothing get 0 / -inf here
+    float* lse;
+};
+
+constexpr int kPlanThreads = 1024;
+
+// Exclusive prefix sum over the block; `total` gets the block's sum.
+__device__ __forceinline__ int64_t block_scan(int64_t v, int64_t* warp_sums, int64_t& total) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
+    int64_t x = v;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+        const int64_t y = __shfl_up_sync(0xffffffffu, x, d);
+        if (lane >= d) x += y;
+    }
+    if (lane == 31) warp_sums[warp] = x;
+    __syncthreads();
+    if (warp == 0) {
+        int64_t s = lane < warps ? warp_sums[lane] : 0;
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+            const int64_t y = __shfl_up_sync(0xffffffffu, s, d);
+            if (lane >= d) s += y;
+        }
+        if (lane < warps) warp_sums[lane] = s;
+    }
+    __syncthreads();
+    total = warp_sums[warps - 1];
+    const int64_t before = warp ? warp_sums[warp - 1] : 0;
+    __syncthreads();   // warp_sums may be written again
+    return before + x - v;
+}
+
+// Largest i in [0, n) with a[i] <= v (a non-decreasing, a[0] <= v).
+__device__ __forceinline__ int find_le(const int32_t* a, int n, int v) {
+    int lo = 0, hi = n;
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (a[mid] <= v) lo = mid;
+        else hi = mid;
+    }
+    return lo;
+}
+
+// Pages of request b, checked: 0 for a length the page table cannot hold.
+__device__ __forceinline__ int checked_len(const PlanArgs& p, int b) {
+    const int len = p.seq_lens[b];
+    if (len < 0 || (static_cast<int64_t>(len) + kPage - 1) / kPage > p.max_pages) {
+        svq_flag(SV_DEVERR_SEQ_LEN);
+        return 0;
+    }
+    return len;
+}
+
+// One CTA: the list of entries, and the running count of their key tiles.
+template <bool PREFIX>
+__global__ void __launch_bounds__(kPlanThreads) plan_kernel(const __grid_constant__ PlanArgs p) {
+    __shared__ int64_t warp_sums[32];
+    const int tid = threadIdx.x, lane = tid & 31;
+    int64_t total;
+    pdl_wait();   // the workspace may still be read by the call before
+    pdl_launch_dependents();
+    // Row tiles before each request (or group): the entries of one are consecutive.
+    int rows_entries = 0;   // entries of the row tiles
+    const int owners = PREFIX ? p.num_groups : (p.q_start ? p.batch : 0);
+    for (int i0 = 0; i0 < owners; i0 += kPlanThreads) {
+        const int i = i0 + tid;
+        int count = 0;
+        if (i < owners) {
+            const int32_t* start = PREFIX ? p.group_start : p.q_start;
+            const int a = start[i], b = start[i + 1], most = PREFIX ? p.batch : p.total_q;
+            if (a < 0 || b < a || b > most) {
+                svq_flag(PREFIX ? SV_DEVERR_GROUP : SV_DEVERR_Q_START);
+            } else if (PREFIX) {
+                const int sp = p.shared_pages[i];
+                if (sp < 0 || sp > p.max_pages) svq_flag(SV_DEVERR_GROUP);
+                else if (sp > 0) count = (b - a + p.tok_per_entry - 1) / p.tok_per_entry;
+            } else {
+                count = (b - a + p.tok_per_entry - 1) / p.tok_per_entry;
+            }
+        }
+        const int64_t before = rows_entries + block_scan(count, warp_sums, total);
+        if (i < owners) p.plan.req_offset[i] = static_cast<int>(min(before, static_cast<int64_t>(INT_MAX / 2)));
+        const int64_t sum = rows_entries + total;
+        rows_entries = static_cast<int>(min(sum, static_cast<int64_t>(INT_MAX / 2)));
+    }
+    // Overlapping (broken) starts could list more tiles than the workspace holds.
+    const int room = p.max_entries - (PREFIX ? p.batch : 0);
+    if (rows_entries > room) {
+        if (tid == 0) svq_flag(PREFIX ? SV_DEVERR_GROUP : SV_DEVERR_Q_START);
+        rows_entries = room;
+    }
+    __syncthreads();
+    const int n = PREFIX ? rows_entries + p.batch : (p.q_start ? rows_entries : p.batch);
+    int64_t base = 0;
+    for (int e0 = 0; e0 < n; e0 += kPlanThreads) {
+        const int e = e0 + tid;
+        Entry en = {0, 0, 0, 0, 0, 0, 0, kDirect};
+        bool empty = false;   // window mode: rows that see nothing
+        if (e < n) {
+            if (PREFIX && e < rows_entries) {
+                const int g = find_le(p.plan.req_offset, p.num_groups, e);
+                const int a = p.group_start[g], b = p.group_start[g + 1];
+                const int at = (e - p.plan.req_offset[g]) * p.tok_per_entry;
+                en.row0 = a + at;
+                en.ntok = min(p.tok_per_entry, b - en.row0);
+                en.pos0 = kAllVisible;
+                en.req = a;
+                en.npages = p.shared_pages[g];
+                en.kind = kPrefix;
+            } else if (PREFIX) {
+                const int b = e - rows_entries;
+                en.row0 = en.req = b;
+                en.ntok = 1;
+                en.kind = kSuffix;
+                int pre = -2;     // -2: no group holds the request, -1: no prefix
+                if (p.group_start[0] <= b && b < p.group_start[p.num_groups]) {
+                    const int g = find_le(p.group_start, p.num_groups, b);
+                    const int a = p.group_start[g], end = p.group_start[g + 1];
+                    const int sp = p.shared_pages[g];
+                    pre = -1;
+                    if (a < 0 || a > b || b >= end || end > p.batch || sp < 0 || sp > p.max_pages) {
+                        svq_flag(SV_DEVERR_GROUP);
+                    } else {
+                        const int len = checked_len(p, b);
+                        if (len < sp * kPage) {
+                            if (len > 0) svq_flag(SV_DEVERR_GROUP);
+                        } else if (len > 0) {
+                            const int pe = p.plan.req_offset[g] + (b - a) / p.tok_per_entry;
+                            if (sp > 0 && pe < rows_entries) pre = pe;
+                            en.pos0 = len - 1;
+                            en.w0 = sp;
+                            en.npages = (len + kPage - 1) / kPage - sp;
+                        }
+                    }
+                }
+                p.plan.req_entry[b] = pre;
+            } else {
+                int b = e, at = 0, size = 1, start = e;
+                if (p.q_start) {
+                    b = find_le(p.plan.req_offset, p.batch, e);
+                    start = p.q_start[b];
+                    size = p.q_start[b + 1] - start;
+                    at = (e - p.plan.req_offset[b]) * p.tok_per_entry;
+                }
+                int len = checked_len(p, b);
+                if (size > len) {
+                    if (len > 0 || size > 1) svq_flag(p.q_start ? SV_DEVERR_Q_START : SV_DEVERR_SEQ_LEN);
+                    len = 0;
+                }
+                en.row0 = start + at;
+                en.ntok = min(p.tok_per_entry, size - at);
+                en.req = b;
+                if (len > 0) {
+                    en.pos0 = len - size + at;
+                    const int last = (en.pos0 + en.ntok - 1) / kPage + 1;
+                    const int w0 = max(0, en.pos0 - p.window + 1) / kPage;
+                    en.sink_pages = min(w0, p.sink / kPage + (p.sink % kPage != 0));
+                    en.w0 = w0;
+                    en.npages = en.sink_pages + last - w0;
+                } else {
+                    empty = true;
+                }
+            }
+        }
+        const int64_t before = base + block_scan(tiles_of(en.npages), warp_sums, total);
+        base += total;
+        if (e < n) {
+            p.plan.entries[e] = en;
+            p.plan.cum[e] = before;
+        }
+        for (uint32_t rest = __ballot_sync(0xffffffffu, empty); rest; rest &= rest - 1) {
+            const int src = __ffs(rest) - 1;
+            const int64_t r0 = static_cast<int64_t>(__shfl_sync(0xffffffffu, en.row0, src)) * p.num_q_heads;
+            const int64_t r1 = r0 + static_cast<int64_t>(__shfl_sync(0xffffffffu, en.ntok, src)) * p.num_q_heads;
+            uint4* o = reinterpret_cast<uint4*>(p.out + r0 * kHeadDim);
+            for (int64_t i = lane; i < (r1 - r0) * (kHeadDim / 8); i += 32) o[i] = make_uint4(0u, 0u, 0u, 0u);
+            for (int64_t i = r0 + lane; i < r1; i += 32) p.lse[i] = -INFINITY;
+        }
+    }
+    if (tid == 0) {
+        p.plan.cum[n] = base;
+        *p.plan.num_entries = n;
+    }
+}
+
+// ---------------------------------------------------------------- joining partials
+// The partials of one item, in tile order: those of CTAs c0 .. c0 + n - 1, or
+// (whole) the one of the CTA that had all of it.
+struct Pieces {
+    const float* o;
+    const float2* ml;
+    int64_t first;     // row of the first piece
+    int64_t second;    // row of the second; the others follow `stride` apart
+    int64_t stride;
+    int n;
+    __device__ __forceinline__ int64_t row(int k) const { return k == 0 ? first : second + (k - 1) * stride; }
+};
+
+__device__ __forceinline__ Pieces cut_pieces(const AttendArgs& a, const Share& share, int64_t begin, int64_t end, int r) {
+    Pieces p;
+    const int c0 = share.cta_of(begin);
+    p.o = a.cut_o;
+    p.ml = a.cut_ml;
+    p.n = share.cta_of(end - 1) - c0 + 1;
+    p.stride = 2ll * a.slot_rows;
+    p.first = (2ll * c0 + (begin == share.start(c0) ? 0 : 1)) * a.slot_rows + r;
+    p.second = 2ll * (c0 + 1) * a.slot_rows + r;
+    return p;
+}
+
+constexpr int kJoinThreads = 128;
+
+// One row by the whole CTA: warps take pieces in turn, lane l channels 4 l .. 4 l + 3.
+__device__ __forceinline__ void join_row(const Pieces (&lists)[2], int nlists, __nv_bfloat16* out, float* lse) {
+    __shared__ float4 sm_o[kJoinThreads / 32][32];
+    __shared__ float2 sm_ml[kJoinThreads / 32];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    constexpr int kWarps = kJoinThreads / 32;
+    float m = -INFINITY, l = 0.f;
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    int k0 = warp;
+    for (int li = 0; li < nlists; ++li) {
+        const Pieces& p = lists[li];
+        int k = k0;
+        for (; k < p.n; k += 4 * kWarps) {
+            float2 ml[4];
+            float4 o[4];
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+                const int j = k + u * kWarps;
+                ml[u] = j < p.n ? p.ml[p.row(j)] : make_float2(-INFINITY, 0.f);
+                o[u] = j < p.n ? *reinterpret_cast<const float4*>(p.o + p.row(j) * kHeadDim + 4 * lane)
+                               : make_float4(0.f, 0.f, 0.f, 0.f);
+            }
+            float mn = m;
+#pragma unroll
+            for (int u = 0; u < 4; ++u) mn = fmaxf(mn, ml[u].x);
+            const float base = mn == -INFINITY ? 0.f : mn;   // pieces without a visible token: weights 0
+            const float e = ex2(m - base);
+            l *= e;
+            acc.x *= e;
+            acc.y *= e;
+            acc.z *= e;
+            acc.w *= e;
+            m = mn;
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+                const float f = ex2(ml[u].x - base);
+                l += ml[u].y * f;
+                acc.x += o[u].x * f;
+                acc.y += o[u].y * f;
+                acc.z += o[u].z * f;
+                acc.w += o[u].w * f;
+            }
+        }
+        k0 = (k0 + kWarps - p.n % kWarps) % kWarps;   // the next list goes on where this one ended
+    }
+    sm_o[warp][lane] = acc;
+    if (lane == 0) sm_ml[warp] = make_float2(m, l);
+    __syncthreads();
+    if (warp == 0) {
+        float M = -INFINITY;
+#pragma unroll
+        for (int u = 0; u < kWarps; ++u) M = fmaxf(M, sm_ml[u].x);
+        float L = 0.f;
+        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int u = 0; u < kWarps; ++u) {
+            const float f = ex2(sm_ml[u].x - (M == -INFINITY ? 0.f : M));
+            L += sm_ml[u].y * f;
+            o.x += sm_o[u][lane].x * f;
+            o.y += sm_o[u][lane].y * f;
+            o.z += sm_o[u][lane].z * f;
+            o.w += sm_o[u][lane].w * f;
+        }
+        const float inv = L > 0.f ? 1.f / L : (L == 0.f ? 0.f : L);
+        uint2 v;
+        v.x = pack_bf16x2(o.x * inv, o.y * inv);
+        v.y = pack_bf16x2(o.z * inv, o.w * inv);
+        *reinterpret_cast<uint2*>(out + 4 * lane) = v;
+        if (lane == 0) *lse = L > 0.f ? (M + log2f(L)) * 0.69314718055994531f : (L == 0.f ? -INFINITY : L);
+    }
+    __syncthreads();   // the shared arrays are written again for the next row
+}
+
+// Window mode: CTA (c, y) joins the item that attend CTA c goes on with, if c
+// is the first to do so; rows y, y + gridDim.y, ...
+__global__ void __launch_bounds__(kJoinThreads) join_cut_kernel(const __grid_constant__ AttendArgs a, int ctas) {
+    pdl_wait();
+    const int c = blockIdx.x + 1;
+    const int n = *a.plan.num_entries;
+    const int64_t total = a.plan.cum[n] * a.num_kv_heads;
+    const Share share(total, ctas);
+    const int64_t x = share.start(c);
+    if (x >= total) return;
+    const int e = warp_find(a.plan.cum, n, x / a.num_kv_heads);
+    const Entry en = a.plan.entries[e];
+    const int tiles = tiles_of(en.npages);
+    const int64_t at = a.plan.cum[e] * a.num_kv_heads;
+    const int h = static_cast<int>((x - at) / tiles);
+    const int64_t begin = at + static_cast<int64_t>(h) * tiles;
+    if (begin == x || share.start(c - 1) > begin) return;
+    const int rows = en.ntok * a.group;
+    for (int r = blockIdx.y; r < rows; r += gridDim.y) {
+        const Pieces lists[2] = {cut_pieces(a, share, begin, begin + tiles, r), {}};
+        const int tok = r / a.group;
+        const int64_t q = static_cast<int64_t>(en.row0 + tok) * a.num_q_heads + h * a.group + (r - tok * a.group);
+        join_row(lists, 1, a.out + q * kHeadDim, a.lse + q);
+    }
+}
+
+// Prefix mode: CTA per (request, query head) joins its prefix and its suffix.
+__global__ void __launch_bounds__(kJoinThreads) join_prefix_kernel(const __grid_constant__ AttendArgs a, int ctas) {
+    pdl_wait();
+    const int b = blockIdx.x / a.num_q_heads, hq = blockIdx.x % a.num_q_heads;
+    const int n = *a.plan.num_entries;
+    const int pre = a.plan.req_entry[b];
+    if (pre == -2) return;
+    const int64_t total = a.plan.cum[n] * a.num_kv_heads;
+    const Share share(total, ctas);
+    const int h = hq / a.group, hr = hq - h * a.group;
+    const int64_t q = blockIdx.x;
+    Pieces lists[2];
+    int nl = 0;
+    const int suf = n - static_cast<int>(gridDim.x / a.num_q_heads) + b;
+    for (int k = 0; k < 2; ++k) {
+        const int e = k == 0 ? pre : suf;
+        if (e < 0) continue;
+        const Entry en = a.plan.entries[e];
+        const int tiles = tiles_of(en.npages);
+        if (tiles == 0) continue;
+        const int64_t begin = a.plan.cum[e] * a.num_kv_heads + static_cast<int64_t>(h) * tiles;
+        if (share.cta_of(begin) == share.cta_of(begin + tiles - 1))
+            lists[nl++] = Pieces{a.whole_o[k], a.whole_ml[k], q, q, 0, 1};
+        else
+            lists[nl++] = cut_pieces(a, share, begin, begin + tiles, (b - en.row0) * a.group + hr);
+    }
+    join_row(lists, nl, a.out + q * kHeadDim, a.lse + q);
+}
+
+// ---------------------------------------------------------------- host side
+size_t up(size_t n) { return (n + 255) / 256 * 256; }
+
+struct Layout {
+    size_t entries, cum, num, req_entry, req_offset, cut_o, cut_ml, whole_o, whole_ml, total;
+    int max_entries, slot_rows;
+    // owners: requests (ragged chunks) or groups; rows: query tokens; prefix: room for whole parts
+    Layout(int64_t batch, int64_t owners, int64_t rows, int num_q_heads, int num_kv_heads, bool prefix) {
+        const int group = num_q_heads / num_kv_heads;
+        const int64_t per = kRowTile / group;
+        const int64_t e = rows / per + owners + (prefix ? batch : 0);
+        max_entries = static_cast<int>(e);
+        slot_rows = static_cast<int>(rows * group < kRowTile ? rows * group : kRowTile);
+        size_t at = 0;
+        auto take = [&](size_t bytes) { const size_t r = at; at += up(bytes); return r; };
+        entries = take(e * sizeof(Entry));
+        cum = take((e + 1) * sizeof(int64_t));
+        num = take(sizeof(int));
+        req_entry = take(prefix ? batch * sizeof(int) : 0);
+        req_offset = take(owners * sizeof(int));
+        cut_o = take(2ull * kMaxCtas * slot_rows * kHeadDim * sizeof(float));
+        cut_ml = take(2ull * kMaxCtas * slot_rows * sizeof(float2));
+        const size_t heads = prefix ? static_cast<size_t>(batch) * num_q_heads : 0;
+        whole_o = take(2 * heads * kHeadDim * sizeof(float));
+        whole_ml = take(2 * heads * sizeof(float2));
+        total = at;
+    }
+};
+
+// The K or V pool bf16 [pages][kv heads][16][128] as a 4-D tensor: 64 channels,
+// 8 rows (256 bytes apart), 2 channel halves (128 bytes apart), groups of 8
+// rows (2 KB apart).  A box of 64 x 8 x 2 x 2 is one page's tile of one kv head
+// and lands as [8-row group][half][8 rows of 128 bytes], each 1 KB block
+// 128-byte swizzled: 8-row groups 2 KB apart through the whole stage, the
+// uniform stride an MMA operand needs, with one copy a page.
+bool encode_map(CUtensorMap* map, const void* pool, int64_t row_groups) {
+    auto enc = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(tensor_map_encode_entry());
+    if (!enc) return false;
+    const cuuint64_t dims[4] = {64, 8, 2, static_cast<cuuint64_t>(row_groups)};
+    const cuuint64_t strides[3] = {256, 128, 2048};
+    const cuuint32_t box[4] = {64, 8, 2, 2};
+    const cuuint32_t ones[4] = {1, 1, 1, 1};
+    return enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(pool), dims, strides, box, ones,
+               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <bool FP8>
+int launch_attend(const AttendArgs& a, const CUtensorMap& tk, const CUtensorMap& tv, int ctas, cudaStream_t stream) {
+    static std::atomic<bool> attr_set[64];
+    const int st = once_per_device(attr_set, [] {
+        return cudaFuncSetAttribute(attend_kernel<FP8>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                    Cfg<FP8>::kSmem) == cudaSuccess
+                   ? SV_OK
+                   : SV_ERR_CUDA;
+    });
+    if (st) return st;
+    return launch_pdl(attend_kernel<FP8>, dim3(ctas), dim3(Cfg<FP8>::kThreads), Cfg<FP8>::kSmem, stream, a, tk, tv) ==
+                   cudaSuccess
+               ? SV_OK
+               : SV_ERR_CUDA;
+}
+
+// What both calls do: arguments, plan, attention.
+int launch_common(const sv_cache* c, const void* q, int num_q_heads, const int32_t* page_table, int max_pages,
+                  const Layout& lay, int window, int sink, float softmax_scale, void* out, float* lse, void* workspace,
+                  PlanArgs& p, bool prefix, int batch, int ctas, AttendArgs& a, cudaStream_t stream) {
+    unsigned char* ws = static_cast<unsigned char*>(workspace);
+    a.q = static_cast<const __nv_bfloat16*>(q);
+    a.num_q_heads = num_q_heads;
+    a.num_kv_heads = c->num_kv_heads;
+    a.group = num_q_heads / c->num_kv_heads;
+    a.page_table = page_table;
+    a.max_pages = max_pages;
+    a.num_phys_pages = c->num_phys_pages;
+    a.k_pool = static_cast<const unsigned char*>(c->k_pool);
+    a.v_pool = static_cast<const unsigned char*>(c->v_pool);
+    a.k_scale = static_cast<const float*>(c->k_scale);
+    a.v_scale = static_cast<const float*>(c->v_scale);
+    a.plan.entries = reinterpret_cast<Entry*>(ws + lay.entries);
+    a.plan.cum = reinterpret_cast<int64_t*>(ws + lay.cum);
+    a.plan.num_entries = reinterpret_cast<int*>(ws + lay.num);
+    a.plan.req_entry = reinterpret_cast<int*>(ws + lay.req_entry);
+    a.plan.req_offset = reinterpret_cast<int*>(ws + lay.req_offset);
+    a.window = window > 0 ? window : INT_MAX;
+    a.sink = sink;
+    a.scale_log2 = softmax_scale * 1.4426950408889634f;
+    a.out = static_cast<__nv_bfloat16*>(out);
+    a.lse = lse;
+    a.cut_o = reinterpret_cast<float*>(ws + lay.cut_o);
+    a.cut_ml = reinterpret_cast<float2*>(ws + lay.cut_ml);
+    a.slot_rows = lay.slot_rows;
+    const size_t heads = static_cast<size_t>(batch) * num_q_heads;
+    for (int k = 0; k < 2; ++k) {
+        a.whole_o[k] = reinterpret_cast<float*>(ws + lay.whole_o) + k * heads * kHeadDim;
+        a.whole_ml[k] = reinterpret_cast<float2*>(ws + lay.whole_ml) + k * heads;
+    }
+    p.plan = a.plan;
+    p.max_entries = lay.max_entries;
+    p.tok_per_entry = kRowTile / a.group;
+    p.batch = batch;
+    p.max_pages = max_pages;
+    p.window = a.window;
+    p.sink = sink;
+    p.num_q_heads = num_q_heads;
+    p.out = a.out;
+    p.lse = lse;
+    const bool fp8 = c->kv_format == SV_KV_FP8_E4M3;
+    CUtensorMap tk = {}, tv = {};
+    if (!fp8) {
+        // TMA coordinates are 32-bit.
+        const int64_t groups = c->num_phys_pages * c->num_kv_heads * 2;
+        if (groups > INT_MAX) return SV_ERR_UNSUPPORTED;
+        if (!encode_map(&tk, c->k_pool, groups) || !encode_map(&tv, c->v_pool, groups)) return SV_ERR_CUDA;
+    }
+    const cudaError_t err = prefix ? launch_pdl(plan_kernel<true>, dim3(1), dim3(kPlanThreads), 0, stream, p)
+                                   : launch_pdl(plan_kernel<false>, dim3(1), dim3(kPlanThreads), 0, stream, p);
+    if (err != cudaSuccess) return SV_ERR_CUDA;
+    return fp8 ? launch_attend<true>(a, tk, tv, ctas, stream) : launch_attend<false>(a, tk, tv, ctas, stream);
+}
+
+}  // namespace
+
+size_t window_workspace_bytes(int batch, int num_q_heads, int num_kv_heads, int total_q) {
+    return Layout(batch, batch, total_q, num_q_heads, num_kv_heads, false).total;
+}
+size_t prefix_workspace_bytes(int batch, int num_q_heads, int num_kv_heads, int num_groups) {
+    return Layout(batch, num_groups, batch, num_q_heads, num_kv_heads, true).total;
+}
+
+int launch_window(const sv_cache* c, const void* q, int num_q_heads, const int32_t* q_start, int total_q,
+                  const int32_t* page_table, const int32_t* seq_lens, int batch, int max_pages, int window, int sink,
+                  float softmax_scale, void* out, float* lse, void* workspace, int sm_count, cudaStream_t stream) {
+    const Layout lay(batch, batch, total_q, num_q_heads, c->num_kv_heads, false);
+    const int ctas = sm_count < kMaxCtas ? sm_count : kMaxCtas;
+    PlanArgs p = {};
+    p.q_start = q_start;
+    p.total_q = total_q;
+    p.seq_lens = seq_lens;
+    AttendArgs a = {};
+    const int st = launch_common(c, q, num_q_heads, page_table, max_pages, lay, window, sink, softmax_scale, out, lse,
+                                 workspace, p, false, batch, ctas, a, stream);
+    if (st || ctas < 2) return st;
+    const int y = lay.slot_rows < 32 ? lay.slot_rows : 32;
+    return launch_pdl(join_cut_kernel, dim3(ctas - 1, y), dim3(kJoinThreads), 0, stream, a, ctas) == cudaSuccess
+               ? SV_OK
+               : SV_ERR_CUDA;
+}
+
+int launch_prefix(const sv_cache* c, const void* q, int num_q_heads, const int32_t* page_table,
+                  const int32_t* seq_lens, int batch, int max_pages, const int32_t* group_start,
+                  const int32_t* shared_pages, int num_groups, float softmax_scale, void* out, float* lse,
+                  void* workspace, int sm_count, cudaStream_t stream) {
+    const Layout lay(batch, num_groups, batch, num_q_heads, c->num_kv_heads, true);
+    const int ctas = sm_count < kMaxCtas ? sm_count : kMaxCtas;
+    PlanArgs p = {};
+    p.seq_lens = seq_lens;
+    p.group_start = group_start;
+    p.shared_pages = shared_pages;
+    p.num_groups = num_groups;
+    AttendArgs a = {};
+    const int st = launch_common(c, q, num_q_heads, page_table, max_pages, lay, 0, 0, softmax_scale, out, lse, workspace,
+                                 p, true, batch, ctas, a, stream);
+    if (st) return st;
+    return launch_pdl(join_prefix_kernel, dim3(static_cast<unsigned>(batch) * num_q_heads), dim3(kJoinThreads), 0, stream,
+                      a, ctas) == cudaSuccess
+               ? SV_OK
+               : SV_ERR_CUDA;
+}
+
+}  // namespace svq

@@ -1,0 +1,200 @@
+"""sv_window_attention against the definition in 64 bits."""
+from __future__ import annotations
+
+import pytest
+import torch
+
+from attend_ref import DIM, PAGE, PagedCase, attend, check, window_seen
+from query_aware_sparse_quest_gb300 import binding
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda"
+
+
+def run(case, q, window, sink, starts=None, scale=None, rows=None, stream=None):
+    cache = case.cache()
+    T, Hq, _ = q.shape
+    out = torch.full_like(q, 7.0)
+    lse = torch.full((T, Hq), 7.0, device=DEV)
+    B = len(case.lens)
+    ws = torch.full((binding.sv_window_attention_workspace_size(B, Hq, case.hkv, T),), 0xFF, dtype=torch.uint8, device=DEV)
+    binding.sv_window_attention(cache, q, case.table.to(DEV), torch.tensor(case.lens, dtype=torch.int32, device=DEV), window,
+                                sink, out, lse, ws,
+                                q_start=None if starts is None else torch.tensor(starts, dtype=torch.int32, device=DEV),
+                                softmax_scale=scale, stream=stream)
+    torch.cuda.synchronize()
+    return out, lse
+
+
+def hide_unseen(case, sizes, window, sink):
+    """NaN in what no query token sees, -1 for the pages that none reads."""
+    if not window:
+        return
+    for b, (n, size) in enumerate(zip(case.lens, sizes)):
+        if size == 0 or n == 0:
+            continue
+        lo = max(0, n - size - window + 1)
+        case.hide_tokens(b, range(min(sink, lo), lo))
+        first, sinks = lo // PAGE, -(-sink // PAGE)
+        if sinks < first:
+            case.table[b, sinks:first] = -1
+
+
+def compare(case, sizes, group, window, sink, seed=1, tail=0, decode=False, scale=DIM ** -0.5):
+    g = torch.Generator().manual_seed(seed)
+    T = sum(sizes)
+    q = torch.randn((T + tail, case.hkv * group, DIM), generator=g).bfloat16().to(DEV)
+    ref = [attend(q[sum(sizes[:b]):sum(sizes[:b + 1])], *case.tokens(b), window_seen(n, sizes[b], window, sink, DEV), scale)
+           for b, n in enumerate(case.lens)]
+    hide_unseen(case, sizes, window, sink)
+    starts = None if decode else [sum(sizes[:b]) for b in range(len(sizes) + 1)]
+    out, lse = run(case, q, window, sink, starts, scale)
+    assert binding.sv_get_device_error() == 0
+    check(out[:T], lse[:T], [torch.cat(x) for x in zip(*ref)])
+    # rows behind the last range are left as they were
+    assert (out[T:] == 7.0).all() and (lse[T:] == 7.0).all()
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("lens,window,sink", [
+    ([1], 0, 0), ([17], 0, 0), ([128], 0, 0), ([129], 0, 0), ([1000], 0, 0),
+    ([1000], 1, 0), ([1000], 16, 1), ([1000], 100, 4), ([1000], 100, 16), ([1000], 333, 40), ([1000], 5000, 4),
+    ([5000, 1, 300, 2049], 700, 5),
+])
+def test_decode_one_token(lens, window, sink, fp8):
+    compare(PagedCase(lens, 2, fp8=fp8), [1] * len(lens), 4, window, sink, decode=True)
+
+
+@pytest.mark.parametrize("group", [1, 2, 3, 5, 6, 7, 8])
+def test_decode_groups(group):
+    compare(PagedCase([700, 33], 3), [1, 1], group, 200, 3, decode=True)
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("lens,sizes,group,window,sink", [
+    ([1], [1], 1, 0, 0),
+    ([16], [16], 8, 0, 0),
+    ([40], [40], 8, 0, 0),                       # 320 rows: two tiles
+    ([300], [300], 1, 0, 0),                     # no sharing of heads
+    ([300], [300], 7, 0, 0),                     # 36 tokens a tile, 252 rows
+    ([513], [100], 4, 0, 0),
+    ([900], [700], 4, 64, 4),                    # windows shorter than the chunk
+    ([900], [700], 8, 1, 0),                     # every token sees itself alone
+    ([2000], [500], 4, 300, 37),
+    ([2000], [500], 5, 1000, 500),
+    ([700, 5, 1, 333], [650, 5, 1, 64], 8, 128, 3),
+    ([700, 50, 400], [0, 50, 1], 4, 100, 16),    # a request without query tokens
+])
+def test_chunks(lens, sizes, group, window, sink, fp8):
+    compare(PagedCase(lens, 2, fp8=fp8), sizes, group, window, sink, tail=3)
+
+
+def test_many_short_requests():
+    """More items than CTAs: whole items and cut ones in one call."""
+    lens = [1 + (37 * i) % 400 for i in range(90)]
+    compare(PagedCase(lens, 4, spare=0), [1] * 90, 2, 90, 7, decode=True)
+
+
+def test_long_context_few_rows():
+    compare(PagedCase([40000], 1), [1], 8, 0, 0, decode=True)
+    compare(PagedCase([20000], 1, fp8=True), [3], 8, 0, 0)
+
+
+def test_large_logits_move_the_base():
+    """Logits that grow along the context by hundreds: every tile moves the base."""
+    case = PagedCase([1500], 1)
+    ramp = torch.linspace(0.1, 30, 1500)
+    for t in range(1500):
+        case.k[case.table[0, t // PAGE], 0, t % PAGE] *= ramp[t]
+    case.k = case.k.bfloat16()
+    compare(case, [200], 4, 0, 0)
+    case = PagedCase([1500], 1)
+    for t in range(1500):
+        case.k[case.table[0, t // PAGE], 0, t % PAGE] *= ramp[1499 - t]
+    compare(case, [200], 4, 0, 0, scale=0.5)
+
+
+def test_padded_and_invalid_requests():
+    case = PagedCase([50, 20, 300], 2)
+    q = torch.randn((3, 8, DIM), generator=torch.Generator().manual_seed(3)).bfloat16().to(DEV)
+    for bad, flag in ((0, 0), (-4, 0x8), (19 * PAGE + 1, 0x8)):
+        refs = [attend(q[b:b + 1], *case.tokens(b), window_seen(n, 1, 0, 0, DEV), DIM ** -0.5) for b, n in ((0, 50), (2, 300))]
+        held, case.lens[1] = case.lens[1], bad
+        out, lse = run(case, q, 0, 0)
+        case.lens[1] = held
+        assert binding.sv_get_device_error() == flag
+        check(out[[0, 2]], lse[[0, 2]], [torch.cat(x) for x in zip(*refs)])
+        assert (out[1] == 0).all() and torch.isneginf(lse[1]).all()
+
+
+def test_bad_pages_are_masked():
+    case = PagedCase([100, 260], 2)
+    for entry in (-1, case.k.shape[0], 2 ** 31 - 1):
+        keep = case.table.clone()
+        ref = []
+        q = torch.randn((11, 8, DIM), generator=torch.Generator().manual_seed(3)).bfloat16().to(DEV)
+        for b, (n, size) in enumerate(((100, 1), (260, 10))):
+            seen = window_seen(n, size, 0, 0, DEV)
+            seen[:, 32:48] = False
+            ref.append(attend(q[b:b + size] if b else q[:1], *case.tokens(b), seen, DIM ** -0.5))
+        case.table[:, 2] = entry
+        out, lse = run(case, q, 0, 0, starts=[0, 1, 11])
+        case.table = keep
+        assert binding.sv_get_device_error() == 0x1
+        check(out, lse, [torch.cat(x) for x in zip(*ref)])
+
+
+def test_bad_starts_are_skipped():
+    case = PagedCase([100, 200, 64], 1)
+    q = torch.randn((20, 4, DIM), generator=torch.Generator().manual_seed(3)).bfloat16().to(DEV)
+    ref = attend(q[:5], *case.tokens(0), window_seen(100, 5, 0, 0, DEV), DIM ** -0.5)
+    for starts in ([0, 5, 3, 900], [0, 5, 25, 21], [0, 5, -1, -7]):
+        out, lse = run(case, q, 0, 0, starts=starts)
+        assert binding.sv_get_device_error() & 0x20
+        check(out[:5], lse[:5], ref)
+    # a chunk longer than its request
+    out, lse = run(case, q, 0, 0, starts=[0, 5, 10, 20])
+    assert binding.sv_get_device_error() == 0
+    case.lens[2] = 9
+    out, lse = run(case, q, 0, 0, starts=[0, 5, 10, 20])
+    assert binding.sv_get_device_error() == 0x20
+    check(out[:5], lse[:5], ref)
+    assert (out[10:] == 0).all() and torch.isneginf(lse[10:]).all()
+    # starts that would list the same rows many times over
+    case = PagedCase([256] * 40, 1)
+    q = torch.randn((256, 8, DIM)).bfloat16().to(DEV)
+    run(case, q, 0, 0, starts=[0, 256] * 20 + [0])
+    assert binding.sv_get_device_error() == 0x20
+
+
+def test_repeats_are_identical_and_replays_in_a_graph():
+    case = PagedCase([3000, 500], 2)
+    cache, table = case.cache(), case.table.to(DEV)
+    lens = torch.tensor(case.lens, dtype=torch.int32, device=DEV)
+    starts = torch.tensor([0, 100, 133], dtype=torch.int32, device=DEV)
+    q = torch.randn((133, 16, DIM), device=DEV).bfloat16()
+    ws = torch.empty(binding.sv_window_attention_workspace_size(2, 16, 2, 133), dtype=torch.uint8, device=DEV)
+
+    def call(out, lse):
+        binding.sv_window_attention(cache, q, table, lens, 700, 4, out, lse, ws, q_start=starts)
+    first = torch.empty_like(q), torch.empty((133, 16), device=DEV)
+    call(*first)
+    out, lse = torch.empty_like(q), torch.empty((133, 16), device=DEV)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=side):
+        call(out, lse)
+    for _ in range(3):
+        out.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, first[0]) and torch.equal(lse, first[1])
+    # other lengths and queries in the same graph
+    lens.copy_(torch.tensor([2100, 33], dtype=torch.int32))
+    q.normal_()
+    graph.replay()
+    call(*first)
+    torch.cuda.synchronize()
+    assert torch.equal(out, first[0]) and torch.equal(lse, first[1])
+    assert binding.sv_get_device_error() == 0
