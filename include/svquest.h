@@ -90,6 +90,11 @@ enum sv_status {
                                        request */
 #define SV_DEVERR_GROUP      0x40u  /* group_start not ascending inside [0, batch], or shared_pages negative or
                                        more than a request of the group holds */
+#define SV_DEVERR_ROW        0x80u  /* a page-table row (or a token count) of an sv_pages_* list out of range, or a
+                                       row listed twice where it may not be */
+#define SV_DEVERR_REF_COUNT  0x100u /* a page's reference count does not allow the call: freed more often than held,
+                                       written on while shared, or free while a table lists it */
+#define SV_DEVERR_NO_PAGE    0x200u /* not enough free pages: the request was not served */
 
 /* K/V pool formats (sv_cache.kv_format). */
 #define SV_KV_BF16     0   /* k_pool, v_pool bf16 [pages][Hkv][16][128] */
@@ -385,6 +390,88 @@ int sv_prefix_decode(const sv_cache* cache, const void* q, int32_t num_q_heads, 
 
 /* Workspace bytes of sv_prefix_decode (0 for sizes it does not take). */
 size_t sv_prefix_decode_workspace_size(int32_t batch, int32_t num_q_heads, int32_t num_kv_heads, int32_t num_groups);
+
+/*
+ * sv_pages_* -- who holds which page.  For caches whose pages the library
+ * manages on the device:
+ *   page_table   int32 [num_rows][max_pages], seq_lens int32 [num_rows]: the
+ *                rows of all requests that hold pages; the first
+ *                ceil(seq_lens / 16) entries of a row are its pages, -1 for
+ *                pages that were freed behind a window.  Other entries are
+ *                neither read nor written.
+ *   ref_counts   int32 [num_phys_pages]: how many rows hold a page.  A page is
+ *                free when its count is 0.  Whoever else keeps pages (a prefix
+ *                cache) adds to their counts.  All start at 0.
+ * New pages are always the lowest free ones, in the order of the list that
+ * asks for them, so every result is determined by the arguments.  `caches` is
+ * an array of num_caches (1 .. SV_MAX_CACHES) caches, one a layer, that share
+ * the page table: same num_phys_pages (below 2^27: slots are 32-bit), their
+ * own heads and formats.  Page data means K, V, metadata and, for e4m3 pools,
+ * scales.  Lists hold n >= 0 entries (0 launches nothing).  What a list asks
+ * for that cannot be done is left out and sets an error bit; the rest is done.
+ * A workspace holds sv_pages_workspace_size(num_phys_pages, num_rows, n)
+ * bytes, is not shared with a call that may run at the same time, and needs no
+ * initial value.
+ */
+#define SV_MAX_CACHES 128
+
+size_t sv_pages_workspace_size(int64_t num_phys_pages, int32_t num_rows, int32_t n);
+
+/* Copies the data of page src[i] to page dst[i], in every cache.  No page is
+ * in dst twice or in both lists (the copies run at once). */
+int sv_pages_copy(const sv_cache* caches, int32_t num_caches, const int32_t* src, const int32_t* dst, int32_t n,
+                  void* stream);
+
+/*
+ * Row children[i] becomes a fork of row parents[i]: it shares the parent's full
+ * pages (their counts go up) and, if the last page is only partly filled, gets
+ * a copy of that page's data in a new page, so that both can go on by
+ * themselves.  The shared pages are what sv_prefix_decode reads once.  Child
+ * rows hold nothing before (their entries are overwritten).  A child listed
+ * twice (its first mention counts), or one that is also a parent, is
+ * SV_DEVERR_ROW; a fork for which no page is left is SV_DEVERR_NO_PAGE.
+ */
+int sv_pages_fork(const sv_cache* caches, int32_t num_caches, int32_t* page_table, int32_t* seq_lens, int32_t num_rows,
+                  int32_t max_pages, int32_t* ref_counts, const int32_t* parents, const int32_t* children, int32_t n,
+                  void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * Makes room for add_tokens[i] >= 0 more tokens in row rows[i]: takes new pages
+ * where the last one has no room, raises seq_lens, and writes the tokens'
+ * slots, request after request, to slot_mapping [num_slots]: the slots that
+ * sv_quest_update_meta takes.  A request is served if the free pages suffice for it and all before it in the
+ * list; one that is not (SV_DEVERR_NO_PAGE; SV_DEVERR_SEQ_LEN when the row's
+ * table is full; SV_DEVERR_SLOT when slot_mapping is; SV_DEVERR_REF_COUNT when
+ * its partly filled last page is shared; SV_DEVERR_ROW for a row listed again)
+ * is left as it was and its slots are -1.  Slots behind the last token asked
+ * for are not written.
+ */
+int sv_pages_reserve(int32_t* page_table, int32_t* seq_lens, int32_t num_rows, int32_t max_pages, int32_t* ref_counts,
+                     int64_t num_phys_pages, const int32_t* rows, const int32_t* add_tokens, int32_t n,
+                     int32_t* slot_mapping, int32_t num_slots, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * Lets go of pages: with first_page and end_page (both or neither) those at the
+ * logical indices first_page[i] <= p < end_page[i] of row rows[i] (the pages a
+ * window has passed), else the whole row, whose seq_lens becomes 0.  Their
+ * entries become -1 and their counts go down.  Entries that are -1 already are
+ * passed over, so freeing twice does nothing.
+ */
+int sv_pages_free(int32_t* page_table, int32_t* seq_lens, int32_t num_rows, int32_t max_pages, int32_t* ref_counts,
+                  int64_t num_phys_pages, const int32_t* rows, const int32_t* first_page, const int32_t* end_page,
+                  int32_t n, void* stream);
+
+/*
+ * Moves the pages with the highest numbers into the free ones with the lowest,
+ * until the pages held are exactly 0 .. *num_live - 1 (num_live: int32 [1] on
+ * the device), and rewrites the tables of all rows and the counts.
+ * page_table_out and ref_counts_out may be the inputs themselves; if they are
+ * not, a step still running on the old table reads the old pages, whose data
+ * stay until something new is written there.
+ */
+int sv_pages_compact(const sv_cache* caches, int32_t num_caches, const int32_t* page_table, const int32_t* seq_lens,
+                     int32_t num_rows, int32_t max_pages, const int32_t* ref_counts, int32_t* page_table_out,
+                     int32_t* ref_counts_out, int32_t* num_live, void* workspace, size_t workspace_bytes, void* stream);
 
 /* Reads (and with reset != 0 clears) the current device's error word; the
  * read synchronises the device.  Returns SV_OK or SV_ERR_CUDA. */

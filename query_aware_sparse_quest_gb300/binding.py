@@ -68,6 +68,11 @@ def _load():
         "sv_sparse_decode_ex": [cp, vp, i32, vp, vp, i32, i32, vp, vp, i32, op, f32, vp, vp, vp, sz, vp],
         "sv_window_attention": [cp, vp, i32, vp, i32, vp, vp, i32, i32, i32, i32, f32, vp, vp, vp, sz, vp],
         "sv_prefix_decode": [cp, vp, i32, vp, vp, i32, i32, vp, vp, i32, f32, vp, vp, vp, sz, vp],
+        "sv_pages_copy": [cp, i32, vp, vp, i32, vp],
+        "sv_pages_fork": [cp, i32, vp, vp, i32, i32, vp, vp, vp, i32, vp, sz, vp],
+        "sv_pages_reserve": [vp, vp, i32, i32, vp, i64, vp, vp, i32, vp, i32, vp, sz, vp],
+        "sv_pages_free": [vp, vp, i32, i32, vp, i64, vp, vp, vp, i32, vp],
+        "sv_pages_compact": [cp, i32, vp, vp, i32, i32, vp, vp, vp, vp, vp, sz, vp],
         "sv_get_device_error": [ctypes.POINTER(ctypes.c_uint32), ctypes.c_int],
     }
     for name, args in sig.items():
@@ -86,6 +91,8 @@ def _load():
     lib.sv_window_attention_workspace_size.restype = sz
     lib.sv_prefix_decode_workspace_size.argtypes = [i32, i32, i32, i32]
     lib.sv_prefix_decode_workspace_size.restype = sz
+    lib.sv_pages_workspace_size.argtypes = [i64, i32, i32]
+    lib.sv_pages_workspace_size.restype = sz
     lib.sv_status_string.argtypes = [ctypes.c_int]
     lib.sv_status_string.restype = ctypes.c_char_p
     lib.sv_version.argtypes = []
@@ -310,10 +317,15 @@ def _shape(t: torch.Tensor, shape, name: str) -> None:
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
 
 
-def _here(cache: Cache, *tensors: Optional[torch.Tensor]) -> None:
+def _channels(d: int) -> None:
+    if d != 128:
+        raise ValueError(f"q must have 128 channels, got {d}")
+
+
+def _here(*tensors: Optional[torch.Tensor]) -> None:
     """The kernels run on the current device: every tensor has to be there."""
     dev = torch.cuda.current_device()
-    for t in (cache.k_pool, *tensors):
+    for t in tensors:
         if t is not None and t.is_cuda and t.device.index != dev:
             raise ValueError(f"tensors on cuda:{t.device.index} while cuda:{dev} is current")
 
@@ -329,12 +341,13 @@ def sv_window_attention(cache: Cache, q: torch.Tensor, page_table: torch.Tensor,
     """q, out [total_q][Hq][128], lse [total_q][Hq]; window 0: none; q_start None: one token a request."""
     T, Hq, D = q.shape
     B, max_pages = page_table.shape
+    _channels(D)
     _shape(seq_lens, (B,), "seq_lens")
     _shape(out, q.shape, "out")
     _shape(lse, (T, Hq), "lse")
     if q_start is not None:
         _shape(q_start, (B + 1,), "q_start")
-    _here(cache, q, page_table, seq_lens, q_start, out, lse, workspace)
+    _here(cache.k_pool, q, page_table, seq_lens, q_start, out, lse, workspace)
     scale = float(D) ** -0.5 if softmax_scale is None else float(softmax_scale)
     _check("sv_window_attention", _load().sv_window_attention(
         cache.ref(), _p(q, _BF16, "q"), Hq, _p(q_start, _I32, "q_start"), T, _p(page_table, _I32, "page_table"),
@@ -353,17 +366,112 @@ def sv_prefix_decode(cache: Cache, q: torch.Tensor, page_table: torch.Tensor, se
     """Dense decode with the first shared_pages[g] pages of requests group_start[g] .. read once a group."""
     B, Hq, D = q.shape
     groups = int(shared_pages.numel())
+    _channels(D)
     _shape(page_table, (B, page_table.shape[-1]), "page_table")
     _shape(seq_lens, (B,), "seq_lens")
     _shape(group_start, (groups + 1,), "group_start")
     _shape(out, q.shape, "out")
     _shape(lse, (B, Hq), "lse")
-    _here(cache, q, page_table, seq_lens, group_start, shared_pages, out, lse, workspace)
+    _here(cache.k_pool, q, page_table, seq_lens, group_start, shared_pages, out, lse, workspace)
     scale = float(D) ** -0.5 if softmax_scale is None else float(softmax_scale)
     _check("sv_prefix_decode", _load().sv_prefix_decode(
         cache.ref(), _p(q, _BF16, "q"), Hq, _p(page_table, _I32, "page_table"), _p(seq_lens, _I32, "seq_lens"), B,
         int(page_table.shape[1]), _p(group_start, _I32, "group_start"), _p(shared_pages, _I32, "shared_pages"), groups,
         scale, _p(out, _BF16, "out"), _p(lse, _F32, "lse"), _p(workspace, None, "workspace"),
+        workspace.numel() * workspace.element_size(), _stream(stream)))
+
+
+class CacheList:
+    """The caches of the layers that share one page table, laid out once for the sv_pages_* calls."""
+
+    def __init__(self, caches):
+        self.caches = tuple(caches)
+        if not self.caches:
+            raise ValueError("at least one cache")
+        self.c = (sv_cache * len(self.caches))(*(c.c for c in self.caches))
+
+    @property
+    def num_phys_pages(self) -> int:
+        return int(self.c[0].num_phys_pages)
+
+
+def _cache_list(caches) -> CacheList:
+    if isinstance(caches, CacheList):
+        return caches
+    return CacheList([caches] if isinstance(caches, Cache) else caches)
+
+
+def _rows(page_table: torch.Tensor, seq_lens: torch.Tensor, ref_counts: torch.Tensor, pool: Optional[int] = None):
+    """The leading arguments of the sv_pages_* calls that go by rows."""
+    rows, max_pages = page_table.shape
+    _shape(seq_lens, (rows,), "seq_lens")
+    if pool is not None:
+        _shape(ref_counts, (pool,), "ref_counts")
+    return (_p(page_table, _I32, "page_table"), _p(seq_lens, _I32, "seq_lens"), rows, max_pages,
+            _p(ref_counts, _I32, "ref_counts"))
+
+
+def sv_pages_workspace_size(num_phys_pages: int, num_rows: int, n: int) -> int:
+    return int(_load().sv_pages_workspace_size(num_phys_pages, num_rows, n))
+
+
+def sv_pages_copy(caches, src: torch.Tensor, dst: torch.Tensor, stream=None) -> None:
+    """Copies page src[i] to page dst[i] in every cache (a Cache, several, or a CacheList)."""
+    cl = _cache_list(caches)
+    _shape(dst, src.shape, "dst")
+    _here(cl.caches[0].k_pool, src, dst)
+    _check("sv_pages_copy", _load().sv_pages_copy(cl.c, len(cl.c), _p(src, _I32, "src"), _p(dst, _I32, "dst"),
+                                                  src.numel(), _stream(stream)))
+
+
+def sv_pages_fork(caches, page_table: torch.Tensor, seq_lens: torch.Tensor, ref_counts: torch.Tensor,
+                  parents: torch.Tensor, children: torch.Tensor, workspace: torch.Tensor, stream=None) -> None:
+    cl = _cache_list(caches)
+    _shape(children, parents.shape, "children")
+    _here(cl.caches[0].k_pool, page_table, seq_lens, ref_counts, parents, children, workspace)
+    _check("sv_pages_fork", _load().sv_pages_fork(
+        cl.c, len(cl.c), *_rows(page_table, seq_lens, ref_counts, cl.num_phys_pages), _p(parents, _I32, "parents"),
+        _p(children, _I32, "children"), parents.numel(), _p(workspace, None, "workspace"),
+        workspace.numel() * workspace.element_size(), _stream(stream)))
+
+
+def sv_pages_reserve(page_table: torch.Tensor, seq_lens: torch.Tensor, ref_counts: torch.Tensor, rows: torch.Tensor,
+                     add_tokens: torch.Tensor, slot_mapping: torch.Tensor, workspace: torch.Tensor, stream=None) -> None:
+    """Room for add_tokens[i] more tokens in row rows[i]; their slots go to slot_mapping."""
+    _shape(add_tokens, rows.shape, "add_tokens")
+    _here(page_table, seq_lens, ref_counts, rows, add_tokens, slot_mapping, workspace)
+    _check("sv_pages_reserve", _load().sv_pages_reserve(
+        *_rows(page_table, seq_lens, ref_counts), ref_counts.numel(), _p(rows, _I32, "rows"),
+        _p(add_tokens, _I32, "add_tokens"), rows.numel(), _p(slot_mapping, _I32, "slot_mapping"), slot_mapping.numel(),
+        _p(workspace, None, "workspace"), workspace.numel() * workspace.element_size(), _stream(stream)))
+
+
+def sv_pages_free(page_table: torch.Tensor, seq_lens: torch.Tensor, ref_counts: torch.Tensor, rows: torch.Tensor,
+                  first_page: Optional[torch.Tensor] = None, end_page: Optional[torch.Tensor] = None,
+                  stream=None) -> None:
+    """Whole rows, or pages first_page[i] .. end_page[i] - 1 of each."""
+    for t, name in ((first_page, "first_page"), (end_page, "end_page")):
+        if t is not None:
+            _shape(t, rows.shape, name)
+    _here(page_table, seq_lens, ref_counts, rows, first_page, end_page)
+    _check("sv_pages_free", _load().sv_pages_free(
+        *_rows(page_table, seq_lens, ref_counts), ref_counts.numel(), _p(rows, _I32, "rows"),
+        _p(first_page, _I32, "first_page"), _p(end_page, _I32, "end_page"), rows.numel(), _stream(stream)))
+
+
+def sv_pages_compact(caches, page_table: torch.Tensor, seq_lens: torch.Tensor, ref_counts: torch.Tensor,
+                     page_table_out: torch.Tensor, ref_counts_out: torch.Tensor, num_live: torch.Tensor,
+                     workspace: torch.Tensor, stream=None) -> None:
+    """Live pages to the front of the pool; the outputs may be the inputs themselves."""
+    cl = _cache_list(caches)
+    _shape(page_table_out, page_table.shape, "page_table_out")
+    _shape(ref_counts_out, ref_counts.shape, "ref_counts_out")
+    _shape(num_live, (1,), "num_live")
+    _here(cl.caches[0].k_pool, page_table, seq_lens, ref_counts, page_table_out, ref_counts_out, num_live, workspace)
+    _check("sv_pages_compact", _load().sv_pages_compact(
+        cl.c, len(cl.c), *_rows(page_table, seq_lens, ref_counts, cl.num_phys_pages),
+        _p(page_table_out, _I32, "page_table_out"), _p(ref_counts_out, _I32, "ref_counts_out"),
+        _p(num_live, _I32, "num_live"), _p(workspace, None, "workspace"),
         workspace.numel() * workspace.element_size(), _stream(stream)))
 
 

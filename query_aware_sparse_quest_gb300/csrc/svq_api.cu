@@ -26,6 +26,21 @@ int decode_max_splits(int pages);
 size_t decode_workspace_bytes(int batch, int num_q_heads, int splits);
 int read_error_decode_fp8(uint32_t* flags, int reset);
 int read_error_attend(uint32_t* flags, int reset);
+int read_error_pages(uint32_t* flags, int reset);
+size_t pages_workspace_bytes(int64_t num_pages, int num_rows, int n);
+int launch_pages_copy(const sv_cache* caches, int num_caches, const int32_t* src, const int32_t* dst, int n,
+                      cudaStream_t stream);
+int launch_pages_fork(const sv_cache* caches, int num_caches, int32_t* table, int32_t* lens, int num_rows, int max_pages,
+                      int32_t* counts, const int32_t* parents, const int32_t* children, int n, void* ws,
+                      cudaStream_t stream);
+int launch_pages_reserve(int32_t* table, int32_t* lens, int num_rows, int max_pages, int32_t* counts, int num_pages,
+                         const int32_t* rows, const int32_t* add, int n, int32_t* slots, int num_slots, void* ws,
+                         cudaStream_t stream);
+int launch_pages_free(int32_t* table, int32_t* lens, int num_rows, int max_pages, int32_t* counts, int num_pages,
+                      const int32_t* rows, const int32_t* first, const int32_t* end, int n, cudaStream_t stream);
+int launch_pages_compact(const sv_cache* caches, int num_caches, const int32_t* table, const int32_t* lens, int num_rows,
+                         int max_pages, const int32_t* counts, int32_t* table_out, int32_t* counts_out, int32_t* live,
+                         void* ws, int sm_count, cudaStream_t stream);
 size_t window_workspace_bytes(int batch, int num_q_heads, int num_kv_heads, int total_q);
 size_t prefix_workspace_bytes(int batch, int num_q_heads, int num_kv_heads, int num_groups);
 int launch_window(const sv_cache* c, const void* q, int num_q_heads, const int32_t* q_start, int total_q,
@@ -333,6 +348,35 @@ int attend_checks(const sv_cache* cache, const void* q, int num_q_heads, const i
     if (static_cast<int64_t>(batch) * num_q_heads > INT_MAX) return SV_ERR_UNSUPPORTED;
     return SV_OK;
 }
+
+// Slots (page * 16 + offset) are 32-bit.
+constexpr int64_t kMaxPoolPages = 1ll << 27;
+
+int check_caches(const sv_cache* caches, int n) {
+    if (!caches || n < 1) return SV_ERR_INVALID_ARG;
+    if (n > SV_MAX_CACHES) return SV_ERR_UNSUPPORTED;
+    for (int i = 0; i < n; ++i) {
+        const int st = check_cache(caches + i);
+        if (st) return st;
+        if (caches[i].num_phys_pages != caches[0].num_phys_pages) return SV_ERR_INVALID_ARG;
+    }
+    return caches[0].num_phys_pages < kMaxPoolPages ? SV_OK : SV_ERR_UNSUPPORTED;
+}
+
+int check_rows(const int32_t* page_table, const int32_t* seq_lens, int num_rows, int max_pages, const int32_t* ref_counts,
+               int64_t num_phys_pages) {
+    if (!page_table || !seq_lens || !ref_counts || num_rows < 1 || max_pages < 1 || num_phys_pages < 1)
+        return SV_ERR_INVALID_ARG;
+    if (max_pages >= kMaxRowPages || num_phys_pages >= kMaxPoolPages) return SV_ERR_UNSUPPORTED;
+    return SV_OK;
+}
+
+int check_list(int n) { return n < 0 ? SV_ERR_INVALID_ARG : (n > 65535 ? SV_ERR_UNSUPPORTED : SV_OK); }
+
+int check_pages_ws(const void* ws, size_t bytes, int64_t num_phys_pages, int num_rows, int n) {
+    if (!ws || bytes < pages_workspace_bytes(num_phys_pages, num_rows, n)) return SV_ERR_WORKSPACE;
+    return aligned16(ws) ? SV_OK : SV_ERR_INVALID_ARG;
+}
 }  // namespace
 
 extern "C" {
@@ -418,6 +462,79 @@ int sv_prefix_decode(const sv_cache* cache, const void* q, int32_t num_q_heads, 
                          num_groups, softmax_scale, out, lse, workspace, sms, static_cast<cudaStream_t>(stream));
 }
 
+size_t sv_pages_workspace_size(int64_t num_phys_pages, int32_t num_rows, int32_t n) {
+    if (num_phys_pages < 1 || num_phys_pages >= kMaxPoolPages || num_rows < 1 || n < 0 || n > 65535) return 0;
+    return pages_workspace_bytes(num_phys_pages, num_rows, n);
+}
+
+int sv_pages_copy(const sv_cache* caches, int32_t num_caches, const int32_t* src, const int32_t* dst, int32_t n,
+                  void* stream) {
+    int st = check_caches(caches, num_caches);
+    if (st) return st;
+    if (n < 0) return SV_ERR_INVALID_ARG;
+    if (n == 0) return SV_OK;
+    if (!src || !dst) return SV_ERR_INVALID_ARG;
+    return launch_pages_copy(caches, num_caches, src, dst, n, static_cast<cudaStream_t>(stream));
+}
+
+int sv_pages_fork(const sv_cache* caches, int32_t num_caches, int32_t* page_table, int32_t* seq_lens, int32_t num_rows,
+                  int32_t max_pages, int32_t* ref_counts, const int32_t* parents, const int32_t* children, int32_t n,
+                  void* workspace, size_t workspace_bytes, void* stream) {
+    int st = check_caches(caches, num_caches);
+    if (st) return st;
+    const int64_t pool = caches[0].num_phys_pages;
+    if ((st = check_rows(page_table, seq_lens, num_rows, max_pages, ref_counts, pool))) return st;
+    if ((st = check_list(n))) return st;
+    if (n == 0) return SV_OK;
+    if (!parents || !children) return SV_ERR_INVALID_ARG;
+    if ((st = check_pages_ws(workspace, workspace_bytes, pool, num_rows, n))) return st;
+    return launch_pages_fork(caches, num_caches, page_table, seq_lens, num_rows, max_pages, ref_counts, parents, children,
+                             n, workspace, static_cast<cudaStream_t>(stream));
+}
+
+int sv_pages_reserve(int32_t* page_table, int32_t* seq_lens, int32_t num_rows, int32_t max_pages, int32_t* ref_counts,
+                     int64_t num_phys_pages, const int32_t* rows, const int32_t* add_tokens, int32_t n,
+                     int32_t* slot_mapping, int32_t num_slots, void* workspace, size_t workspace_bytes, void* stream) {
+    int st = check_rows(page_table, seq_lens, num_rows, max_pages, ref_counts, num_phys_pages);
+    if (st) return st;
+    if ((st = check_list(n))) return st;
+    if (num_slots < 0) return SV_ERR_INVALID_ARG;
+    if (n == 0) return SV_OK;
+    if (!rows || !add_tokens || (!slot_mapping && num_slots > 0)) return SV_ERR_INVALID_ARG;
+    if ((st = check_pages_ws(workspace, workspace_bytes, num_phys_pages, num_rows, n))) return st;
+    return launch_pages_reserve(page_table, seq_lens, num_rows, max_pages, ref_counts, static_cast<int>(num_phys_pages),
+                                rows, add_tokens, n, slot_mapping, num_slots, workspace,
+                                static_cast<cudaStream_t>(stream));
+}
+
+int sv_pages_free(int32_t* page_table, int32_t* seq_lens, int32_t num_rows, int32_t max_pages, int32_t* ref_counts,
+                  int64_t num_phys_pages, const int32_t* rows, const int32_t* first_page, const int32_t* end_page,
+                  int32_t n, void* stream) {
+    int st = check_rows(page_table, seq_lens, num_rows, max_pages, ref_counts, num_phys_pages);
+    if (st) return st;
+    if ((st = check_list(n))) return st;
+    if ((first_page == nullptr) != (end_page == nullptr)) return SV_ERR_INVALID_ARG;
+    if (n == 0) return SV_OK;
+    if (!rows) return SV_ERR_INVALID_ARG;
+    return launch_pages_free(page_table, seq_lens, num_rows, max_pages, ref_counts, static_cast<int>(num_phys_pages), rows,
+                             first_page, end_page, n, static_cast<cudaStream_t>(stream));
+}
+
+int sv_pages_compact(const sv_cache* caches, int32_t num_caches, const int32_t* page_table, const int32_t* seq_lens,
+                     int32_t num_rows, int32_t max_pages, const int32_t* ref_counts, int32_t* page_table_out,
+                     int32_t* ref_counts_out, int32_t* num_live, void* workspace, size_t workspace_bytes, void* stream) {
+    int st = check_caches(caches, num_caches);
+    if (st) return st;
+    const int64_t pool = caches[0].num_phys_pages;
+    if ((st = check_rows(page_table, seq_lens, num_rows, max_pages, ref_counts, pool))) return st;
+    if (!page_table_out || !ref_counts_out || !num_live) return SV_ERR_INVALID_ARG;
+    if ((st = check_pages_ws(workspace, workspace_bytes, pool, num_rows, 0))) return st;
+    int sms = 0;
+    if ((st = sm_count_of_current_device(&sms))) return st;
+    return launch_pages_compact(caches, num_caches, page_table, seq_lens, num_rows, max_pages, ref_counts, page_table_out,
+                                ref_counts_out, num_live, workspace, sms, static_cast<cudaStream_t>(stream));
+}
+
 int sv_get_device_error(uint32_t* flags, int reset) {
     if (!flags) return SV_ERR_INVALID_ARG;
     *flags = 0;
@@ -426,6 +543,7 @@ int sv_get_device_error(uint32_t* flags, int reset) {
     if ((st = read_error_select(flags, reset))) return st;
     if ((st = read_error_decode_fp8(flags, reset))) return st;
     if ((st = read_error_attend(flags, reset))) return st;
+    if ((st = read_error_pages(flags, reset))) return st;
     return read_error_decode(flags, reset);
 }
 

@@ -1,0 +1,693 @@
+// sv_pages_*: who holds which page of the pool.  Copying, forking, reserving,
+// freeing and compacting pages, for all layers that share one page table.
+//
+// The only state beside the page table and the lengths is one int32 reference
+// count a page; a page is free when its count is zero, and the lowest free
+// page is always taken first, so that results depend on nothing but the
+// arguments.  Finding free pages is a scan of the counts (4 bytes a page: 64 KB
+// for a pool of 16384 pages) instead of a free list that every call would have
+// to keep in order.
+//
+// A call that takes pages is planned by one cluster of 8 CTAs: each scans an
+// eighth of the counts, the CTAs' sums are exchanged through distributed
+// shared memory, and the cluster barrier orders its phases, so that a scan
+// over the whole pool and what depends on it are one launch.  Moving page
+// data is a second launch over the whole GPU, one CTA at a time per page and
+// layer (34 KB for 4 kv heads), bound by HBM.
+#include <climits>
+
+#include "svq_common.cuh"
+
+namespace svq {
+
+SVQ_DEFINE_ERROR_WORD(read_error_pages)
+
+namespace {
+
+constexpr int kCluster = 8;
+constexpr int kPlanThreads = 1024;
+constexpr int kMoveThreads = 256;
+
+struct CacheDesc {
+    unsigned char* k;
+    unsigned char* v;
+    unsigned char* meta;
+    unsigned char* k_scale;   // null for bf16 pools
+    unsigned char* v_scale;
+    int heads;
+    int row_chunks;           // 16-byte chunks of a page of one kv head: 256 (bf16) or 128 (e4m3)
+};
+struct CacheSet {
+    CacheDesc c[SV_MAX_CACHES];
+    int n;
+};
+
+// The rows of a page table.
+struct Rows {
+    int32_t* table;
+    int32_t* lens;
+    int num_rows;
+    int max_pages;
+    int32_t* counts;
+    int num_pages;            // of the pool
+};
+
+__device__ __forceinline__ int cluster_rank() {
+    int r;
+    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+// All threads of the cluster; orders their global and shared accesses.
+__device__ __forceinline__ void cluster_sync() {
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// Writes v to the same shared variable of every CTA of the cluster (one thread).
+__device__ __forceinline__ void cluster_store(const int* where, int v) {
+    const uint32_t mine = smem_addr(where);
+    for (int r = 0; r < kCluster; ++r) {
+        uint32_t there;
+        asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(there) : "r"(mine), "r"(r));
+        asm volatile("st.shared::cluster.s32 [%0], %1;" ::"r"(there), "r"(v) : "memory");
+    }
+}
+
+// Exclusive prefix sum over the block; `total` gets the sum.
+template <typename T>
+__device__ __forceinline__ T block_scan(T v, T* warp_sums, T& total) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    T x = v;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+        const T y = __shfl_up_sync(0xffffffffu, x, d);
+        if (lane >= d) x += y;
+    }
+    if (lane == 31) warp_sums[warp] = x;
+    __syncthreads();
+    if (warp == 0) {
+        T s = warp_sums[lane];
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+            const T y = __shfl_up_sync(0xffffffffu, s, d);
+            if (lane >= d) s += y;
+        }
+        warp_sums[lane] = s;
+    }
+    __syncthreads();
+    total = warp_sums[31];
+    const T before = warp ? warp_sums[warp - 1] : T(0);
+    __syncthreads();   // warp_sums may be written again
+    return before + x - v;
+}
+
+// This CTA's part of the pool: [lo, hi).
+__device__ __forceinline__ void slice(int num_pages, int rank, int& lo, int& hi) {
+    const int per = (num_pages + kCluster - 1) / kCluster;
+    lo = min(num_pages, rank * per);
+    hi = min(num_pages, lo + per);
+}
+
+// Sum of `v` over the CTA, published to every CTA of the cluster as out[rank]
+// (visible after the next cluster_sync).
+__device__ __forceinline__ void publish(int v, int rank, int* warp_sums, int* out) {
+    int total;
+    (void)block_scan(v, warp_sums, total);
+    if (threadIdx.x == 0) cluster_store(out + rank, total);
+}
+
+// Free pages of this CTA's part, in order: emit(rank over the pool, page) for ranks below `most`.
+template <typename F>
+__device__ __forceinline__ void each_free(const int32_t* counts, int lo, int hi, int before, int most, int* warp_sums, F&& emit) {
+    for (int base = lo; base < hi && before < most; base += kPlanThreads) {
+        const int p = base + threadIdx.x;
+        const int free = p < hi && counts[p] <= 0;
+        int total;
+        const int rank = before + block_scan(free, warp_sums, total);
+        if (free && rank < most) emit(rank, p);
+        before += total;
+    }
+}
+
+__device__ __forceinline__ int count_free(const int32_t* counts, int lo, int hi) {
+    int n = 0;
+    for (int p = lo + threadIdx.x; p < hi; p += kPlanThreads) n += counts[p] <= 0;
+    return n;
+}
+
+// Largest i in [0, n) with a[i] <= v (a non-decreasing, a[0] <= v).
+__device__ __forceinline__ int find_le(const int32_t* a, int n, int v) {
+    int lo = 0, hi = n;
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (a[mid] <= v) lo = mid;
+        else hi = mid;
+    }
+    return lo;
+}
+
+__device__ __forceinline__ bool len_ok(const Rows& t, int len) {
+    return len >= 0 && (static_cast<int64_t>(len) + kPage - 1) / kPage <= t.max_pages;
+}
+
+// One page of one layer, by the whole CTA: 16-byte chunks, eight loads a
+// thread in flight before their stores.
+__device__ __forceinline__ void copy_span(unsigned char* base, int64_t src, int64_t dst, int chunks) {
+    const uint4* s = reinterpret_cast<const uint4*>(base) + src * chunks;
+    uint4* d = reinterpret_cast<uint4*>(base) + dst * chunks;
+    for (int i = threadIdx.x; i < chunks; i += kMoveThreads) d[i] = ld_stream_v4(s + i);
+}
+__device__ __forceinline__ void copy_page(const CacheDesc& c, int64_t src, int64_t dst) {
+    const int chunks = c.heads * c.row_chunks;
+    const uint4* ks = reinterpret_cast<const uint4*>(c.k) + src * chunks;
+    const uint4* vs = reinterpret_cast<const uint4*>(c.v) + src * chunks;
+    uint4* kd = reinterpret_cast<uint4*>(c.k) + dst * chunks;
+    uint4* vd = reinterpret_cast<uint4*>(c.v) + dst * chunks;
+    for (int i0 = threadIdx.x; i0 < chunks; i0 += 4 * kMoveThreads) {
+        uint4 k[4], v[4];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+            const int i = i0 + u * kMoveThreads;
+            if (i < chunks) {
+                k[u] = ld_stream_v4(ks + i);
+                v[u] = ld_stream_v4(vs + i);
+            }
+        }
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+            const int i = i0 + u * kMoveThreads;
+            if (i < chunks) {
+                kd[i] = k[u];
+                vd[i] = v[u];
+            }
+        }
+    }
+    copy_span(c.meta, src, dst, c.heads * 32);
+    if (c.k_scale) {
+        copy_span(c.k_scale, src, dst, c.heads * 4);
+        copy_span(c.v_scale, src, dst, c.heads * 4);
+    }
+}
+
+// ---------------------------------------------------------------- copy
+// CTA (i, layer): page src[i] -> dst[i].
+__global__ void __launch_bounds__(kMoveThreads) copy_pages_kernel(const __grid_constant__ CacheSet set,
+                                                                  const int32_t* __restrict__ src,
+                                                                  const int32_t* __restrict__ dst, int num_pages) {
+    const int s = src[blockIdx.x], d = dst[blockIdx.x];
+    if (s < 0 || s >= num_pages || d < 0 || d >= num_pages) {
+        if (threadIdx.x == 0) svq_flag(SV_DEVERR_PAGE_TABLE);
+        return;
+    }
+    if (s != d) copy_page(set.c[blockIdx.y], s, d);
+}
+
+// ---------------------------------------------------------------- fork
+struct ForkArgs {
+    Rows t;
+    const int32_t* parents;
+    const int32_t* children;
+    int n;
+    int32_t* owner;      // [num_rows] first fork of a child row
+    int32_t* is_parent;  // [num_rows]
+    int32_t* rank;       // [n] free page a fork takes: its place among the forks that take one
+    int32_t* free;       // [n]
+    int32_t* take;       // [n] page the fork got, kNone: needs none, kSkip: not made
+};
+constexpr int kNone = -1, kSkip = -2;
+
+__device__ __forceinline__ bool row_ok(const Rows& t, int r) { return r >= 0 && r < t.num_rows; }
+
+__global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kPlanThreads)
+    fork_plan_kernel(const __grid_constant__ ForkArgs a) {
+    __shared__ int warp_sums[32];
+    __shared__ int frees[kCluster];
+    __shared__ int needed;
+    const int rank = cluster_rank();
+    const int me = rank * kPlanThreads + threadIdx.x;
+    constexpr int kAll = kCluster * kPlanThreads;
+    for (int i = me; i < a.n; i += kAll) {
+        const int c = a.children[i], p = a.parents[i];
+        if (row_ok(a.t, c)) a.owner[c] = INT_MAX, a.is_parent[c] = 0;
+        if (row_ok(a.t, p)) a.is_parent[p] = 0;
+    }
+    cluster_sync();
+    for (int i = me; i < a.n; i += kAll) {
+        const int c = a.children[i], p = a.parents[i];
+        if (row_ok(a.t, c)) atomicMin(&a.owner[c], i);
+        if (row_ok(a.t, p)) a.is_parent[p] = 1;
+    }
+    int lo, hi;
+    slice(a.t.num_pages, rank, lo, hi);
+    publish(count_free(a.t.counts, lo, hi), rank, warp_sums, frees);
+    cluster_sync();
+    if (rank == 0) {
+        int base = 0;
+        for (int i0 = 0; i0 < a.n; i0 += kPlanThreads) {
+            const int i = i0 + threadIdx.x;
+            int need = 0, take = kSkip;
+            if (i < a.n) {
+                const int c = a.children[i], p = a.parents[i];
+                if (!row_ok(a.t, c) || !row_ok(a.t, p) || a.owner[c] != i || a.is_parent[c]) {
+                    svq_flag(SV_DEVERR_ROW);
+                } else {
+                    const int len = a.t.lens[p];
+                    if (!len_ok(a.t, len)) {
+                        svq_flag(SV_DEVERR_SEQ_LEN);
+                    } else {
+                        take = kNone;
+                        if (len % kPage) {
+                            const int e = a.t.table[static_cast<int64_t>(p) * a.t.max_pages + len / kPage];
+                            if (e >= 0 && e < a.t.num_pages) need = 1;
+                            else svq_flag(SV_DEVERR_PAGE_TABLE);
+                        }
+                    }
+                }
+            }
+            int total;
+            const int r = base + block_scan(need, warp_sums, total);
+            if (i < a.n) {
+                a.take[i] = take;
+                a.rank[i] = need ? r : -1;
+            }
+            base += total;
+        }
+        if (threadIdx.x == 0) cluster_store(&needed, base);
+    }
+    cluster_sync();
+    int before = 0, all = 0;
+    for (int r = 0; r < kCluster; ++r) {
+        if (r < rank) before += frees[r];
+        all += frees[r];
+    }
+    each_free(a.t.counts, lo, hi, before, needed, warp_sums, [&](int r, int p) { a.free[r] = p; });
+    cluster_sync();
+    for (int i = me; i < a.n; i += kAll) {
+        const int r = a.rank[i];
+        if (r < 0) continue;
+        if (r < all) {
+            const int p = a.free[r];
+            a.take[i] = p;
+            a.t.counts[p] = 1;
+        } else {
+            a.take[i] = kSkip;
+            svq_flag(SV_DEVERR_NO_PAGE);
+        }
+    }
+    cluster_sync();   // no CTA leaves while another may still write its shared memory
+}
+
+// CTAs below n: the child's row and the counts of the pages it shares.  The
+// others: the partial page of fork i in one layer.
+__global__ void __launch_bounds__(kMoveThreads) fork_move_kernel(const __grid_constant__ CacheSet set,
+                                                                 const __grid_constant__ ForkArgs a) {
+    pdl_wait();
+    const int i = blockIdx.x;
+    const int take = a.take[i];
+    if (take == kSkip) return;
+    const int parent = a.parents[i];
+    const int len = a.t.lens[parent];
+    const int full = len / kPage;
+    const int32_t* from = a.t.table + static_cast<int64_t>(parent) * a.t.max_pages;
+    if (blockIdx.y > 0) {
+        if (take >= 0) copy_page(set.c[blockIdx.y - 1], from[full], take);
+        return;
+    }
+    int32_t* to = a.t.table + static_cast<int64_t>(a.children[i]) * a.t.max_pages;
+    for (int p = threadIdx.x; p < full; p += kMoveThreads) {
+        const int e = from[p];
+        to[p] = e;
+        if (e >= 0 && e < a.t.num_pages) atomicAdd(&a.t.counts[e], 1);
+        else if (e != -1) svq_flag(SV_DEVERR_PAGE_TABLE);
+    }
+    if (threadIdx.x == 0) {
+        if (len % kPage) to[full] = take;
+        a.t.lens[a.children[i]] = len;
+    }
+}
+
+// ---------------------------------------------------------------- reserve
+struct ReserveArgs {
+    Rows t;
+    const int32_t* rows;
+    const int32_t* add;
+    int n;
+    int32_t* slots;
+    int num_slots;
+    int32_t* owner;     // [num_rows]
+    int32_t* need;      // [n + 1] pages taken before each request
+    int32_t* tok;       // [n + 1] tokens before each request
+    int32_t* ok;        // [n]
+    int32_t* free;      // [num_pages]
+};
+
+__global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kPlanThreads)
+    reserve_kernel(const __grid_constant__ ReserveArgs a) {
+    __shared__ int warp_sums[32];
+    __shared__ int frees[kCluster];
+    __shared__ int needed, tokens;
+    __shared__ int64_t wide_sums[32];
+    constexpr int64_t kMost = INT_MAX;
+    const int rank = cluster_rank();
+    const int me = rank * kPlanThreads + threadIdx.x;
+    constexpr int kAll = kCluster * kPlanThreads;
+    for (int i = me; i < a.n; i += kAll)
+        if (row_ok(a.t, a.rows[i])) a.owner[a.rows[i]] = INT_MAX;
+    cluster_sync();
+    for (int i = me; i < a.n; i += kAll)
+        if (row_ok(a.t, a.rows[i])) atomicMin(&a.owner[a.rows[i]], i);
+    int lo, hi;
+    slice(a.t.num_pages, rank, lo, hi);
+    publish(count_free(a.t.counts, lo, hi), rank, warp_sums, frees);
+    cluster_sync();
+    if (rank == 0) {
+        // 64-bit sums; what is stored saturates past everything that can be served.
+        int64_t pages = 0, toks = 0, total;
+        for (int i0 = 0; i0 < a.n; i0 += kPlanThreads) {
+            const int i = i0 + threadIdx.x;
+            int need = 0, add = 0, ok = 0;
+            if (i < a.n) {
+                const int r = a.rows[i];
+                add = max(0, a.add[i]);
+                if (!row_ok(a.t, r) || a.owner[r] != i || a.add[i] < 0) {
+                    svq_flag(SV_DEVERR_ROW);
+                } else {
+                    const int len = a.t.lens[r];
+                    const int64_t end = static_cast<int64_t>(len) + add;
+                    if (!len_ok(a.t, len) || (end + kPage - 1) / kPage > a.t.max_pages) {
+                        svq_flag(SV_DEVERR_SEQ_LEN);
+                    } else {
+                        ok = 1;
+                        need = static_cast<int>((end + kPage - 1) / kPage) - (len + kPage - 1) / kPage;
+                        if (len % kPage && add > 0) {   // the page that is written on has to be the row's own
+                            const int e = a.t.table[static_cast<int64_t>(r) * a.t.max_pages + len / kPage];
+                            const bool in = e >= 0 && e < a.t.num_pages;
+                            if (!in || a.t.counts[e] != 1) {
+                                svq_flag(in ? SV_DEVERR_REF_COUNT : SV_DEVERR_PAGE_TABLE);
+                                ok = need = 0;
+                            }
+                        }
+                    }
+                }
+            }
+            const int64_t t0 = toks + block_scan(static_cast<int64_t>(add), wide_sums, total);
+            toks += total;
+            if (ok && t0 + add > a.num_slots) {
+                svq_flag(SV_DEVERR_SLOT);
+                ok = need = 0;
+            }
+            const int64_t p0 = pages + block_scan(static_cast<int64_t>(need), wide_sums, total);
+            pages += total;
+            if (i < a.n) {
+                a.ok[i] = ok;
+                a.tok[i] = static_cast<int>(min(t0, kMost));
+                a.need[i] = static_cast<int>(min(p0, kMost));
+            }
+        }
+        if (threadIdx.x == 0) {
+            a.need[a.n] = static_cast<int>(min(pages, kMost));
+            a.tok[a.n] = static_cast<int>(min(toks, kMost));
+            cluster_store(&needed, a.need[a.n]);
+            cluster_store(&tokens, a.tok[a.n]);
+        }
+    }
+    cluster_sync();
+    int before = 0, all = 0;
+    for (int r = 0; r < kCluster; ++r) {
+        if (r < rank) before += frees[r];
+        all += frees[r];
+    }
+    each_free(a.t.counts, lo, hi, before, min(needed, all), warp_sums, [&](int r, int p) { a.free[r] = p; });
+    cluster_sync();
+    // A request gets its pages if all that it and those before it need are there.
+    auto granted = [&](int i) { return a.ok[i] && (a.need[i + 1] == a.need[i] || a.need[i + 1] <= all); };
+    const int most = min(needed, all);
+    for (int k = me; k < most; k += kAll) {
+        const int i = find_le(a.need, a.n, k);
+        if (!granted(i)) continue;
+        const int r = a.rows[i];
+        const int at = (a.t.lens[r] + kPage - 1) / kPage + k - a.need[i];
+        const int p = a.free[k];
+        a.t.table[static_cast<int64_t>(r) * a.t.max_pages + at] = p;
+        a.t.counts[p] = 1;
+    }
+    cluster_sync();
+    const int ntok = min(tokens, a.num_slots);
+    for (int k = me; k < ntok; k += kAll) {
+        const int i = find_le(a.tok, a.n, k);
+        int slot = -1;
+        if (granted(i)) {
+            const int r = a.rows[i];
+            const int pos = a.t.lens[r] + k - a.tok[i];
+            slot = a.t.table[static_cast<int64_t>(r) * a.t.max_pages + pos / kPage] * kPage + pos % kPage;
+        }
+        a.slots[k] = slot;
+    }
+    cluster_sync();
+    for (int i = me; i < a.n; i += kAll) {
+        if (granted(i)) a.t.lens[a.rows[i]] += a.add[i];
+        else if (a.ok[i]) svq_flag(SV_DEVERR_NO_PAGE);
+    }
+}
+
+// ---------------------------------------------------------------- free
+// CTA i: pages [first, end) of row rows[i], or the whole row.  An entry is
+// exchanged for -1 before its page's count goes down, so a row that is listed
+// twice, or a page range freed twice, lets go of every page once.
+__global__ void __launch_bounds__(kMoveThreads) free_kernel(const __grid_constant__ Rows t, const int32_t* __restrict__ rows,
+                                                            const int32_t* __restrict__ first,
+                                                            const int32_t* __restrict__ end) {
+    const int i = blockIdx.x;
+    const int r = rows[i];
+    if (!row_ok(t, r)) {
+        if (threadIdx.x == 0) svq_flag(SV_DEVERR_ROW);
+        return;
+    }
+    int len = t.lens[r];
+    if (!len_ok(t, len)) {
+        if (threadIdx.x == 0) svq_flag(SV_DEVERR_SEQ_LEN);
+        return;
+    }
+    const int pages = (len + kPage - 1) / kPage;
+    const int lo = first ? max(0, first[i]) : 0;
+    const int hi = end ? min(pages, end[i]) : pages;
+    int32_t* row = t.table + static_cast<int64_t>(r) * t.max_pages;
+    for (int p = lo + threadIdx.x; p < hi; p += kMoveThreads) {
+        const int e = atomicExch(&row[p], -1);
+        if (e >= 0 && e < t.num_pages) {
+            if (atomicSub(&t.counts[e], 1) <= 0) {
+                atomicAdd(&t.counts[e], 1);
+                svq_flag(SV_DEVERR_REF_COUNT);
+            }
+        } else if (e != -1) {
+            svq_flag(SV_DEVERR_PAGE_TABLE);
+        }
+    }
+    __syncthreads();   // every thread has read the length
+    if (!first && threadIdx.x == 0) t.lens[r] = 0;
+}
+
+// ---------------------------------------------------------------- compact
+struct CompactArgs {
+    Rows t;                 // table, lens and counts are only read
+    int32_t* table_out;
+    int32_t* counts_out;
+    int32_t* live;          // [1]
+    int32_t* src;           // [num_pages] pages that move, ascending
+    int32_t* dst;           // [num_pages] where they go
+    int32_t* to;            // [num_pages] new place of a page, -1: free
+    int32_t* moves;         // [1]
+};
+
+__global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kPlanThreads)
+    compact_plan_kernel(const __grid_constant__ CompactArgs a) {
+    __shared__ int warp_sums[32];
+    __shared__ int frees[kCluster], holes[kCluster];
+    const int rank = cluster_rank();
+    const int n = a.t.num_pages;
+    int lo, hi;
+    slice(n, rank, lo, hi);
+    publish(count_free(a.t.counts, lo, hi), rank, warp_sums, frees);
+    cluster_sync();
+    int live = n;
+    for (int r = 0; r < kCluster; ++r) live -= frees[r];
+    // Free pages below `live` are filled from the live pages above it; there are as many.
+    publish(lo < live ? count_free(a.t.counts, lo, min(hi, live)) : 0, rank, warp_sums, holes);
+    cluster_sync();
+    int hole = 0, moves = 0, mover = 0;
+    for (int r = 0; r < kCluster; ++r) {
+        int l, h;
+        slice(n, r, l, h);
+        if (r < rank) {
+            hole += holes[r];
+            // live pages at or above `live` in that part
+            mover += max(0, h - max(l, live)) - (frees[r] - holes[r]);
+        }
+        moves += holes[r];
+    }
+    for (int base = lo; base < hi; base += kPlanThreads) {
+        const int p = base + threadIdx.x;
+        const int c = p < hi ? a.t.counts[p] : 0;
+        const bool in = p < hi, is_live = in && c > 0;
+        const bool is_hole = in && !is_live && p < live, moves_up = is_live && p >= live;
+        int nh, nm;
+        const int rh = hole + block_scan(static_cast<int>(is_hole), warp_sums, nh);
+        const int rm = mover + block_scan(static_cast<int>(moves_up), warp_sums, nm);
+        if (is_hole) a.dst[rh] = p;
+        if (moves_up) a.src[rm] = p;
+        if (in && !moves_up) {
+            a.to[p] = is_live ? p : -1;
+            if (!is_hole) a.counts_out[p] = is_live ? c : 0;
+        }
+        hole += nh;
+        mover += nm;
+    }
+    cluster_sync();
+    for (int k = rank * kPlanThreads + threadIdx.x; k < moves; k += kCluster * kPlanThreads) a.to[a.src[k]] = a.dst[k];
+    if (rank == 0 && threadIdx.x == 0) {
+        *a.live = live;
+        *a.moves = moves;
+    }
+}
+
+// Page copies (unit u: page u / layers in layer u % layers), counts of the
+// moved pages, and the rewritten tables, each spread over the grid.
+__global__ void __launch_bounds__(kMoveThreads) compact_move_kernel(const __grid_constant__ CacheSet set,
+                                                                    const __grid_constant__ CompactArgs a) {
+    pdl_wait();
+    const int moves = *a.moves;
+    const int64_t units = static_cast<int64_t>(moves) * set.n;
+    for (int64_t u = blockIdx.x; u < units; u += gridDim.x) {
+        const int k = static_cast<int>(u / set.n);
+        copy_page(set.c[u - static_cast<int64_t>(k) * set.n], a.src[k], a.dst[k]);
+    }
+    const int64_t me = static_cast<int64_t>(blockIdx.x) * kMoveThreads + threadIdx.x;
+    const int64_t all = static_cast<int64_t>(gridDim.x) * kMoveThreads;
+    for (int64_t k = me; k < moves; k += all) {
+        const int s = a.src[k];
+        const int c = a.t.counts[s];
+        a.counts_out[a.dst[k]] = c;
+        a.counts_out[s] = 0;
+    }
+    const int64_t entries = static_cast<int64_t>(a.t.num_rows) * a.t.max_pages;
+    for (int64_t i = me; i < entries; i += all) {
+        const int r = static_cast<int>(i / a.t.max_pages);
+        const int p = static_cast<int>(i - static_cast<int64_t>(r) * a.t.max_pages);
+        const int len = a.t.lens[r];
+        int e = a.t.table[i];
+        if (p == 0 && !len_ok(a.t, len)) svq_flag(SV_DEVERR_SEQ_LEN);
+        if (len > 0 && p < (len - 1) / kPage + 1) {
+            if (e >= 0 && e < a.t.num_pages) {
+                e = a.to[e];
+                if (e < 0) svq_flag(SV_DEVERR_REF_COUNT);   // a free page in a table
+            } else if (e != -1) {
+                svq_flag(SV_DEVERR_PAGE_TABLE);
+            }
+        }
+        a.table_out[i] = e;
+    }
+}
+
+bool fill_set(CacheSet* set, const sv_cache* caches, int n) {
+    set->n = n;
+    for (int i = 0; i < n; ++i) {
+        const sv_cache& c = caches[i];
+        const bool fp8 = c.kv_format == SV_KV_FP8_E4M3;
+        set->c[i] = CacheDesc{static_cast<unsigned char*>(c.k_pool), static_cast<unsigned char*>(c.v_pool),
+                              static_cast<unsigned char*>(c.meta),
+                              fp8 ? static_cast<unsigned char*>(c.k_scale) : nullptr,
+                              fp8 ? static_cast<unsigned char*>(c.v_scale) : nullptr, c.num_kv_heads, fp8 ? 128 : 256};
+    }
+    return true;
+}
+
+int status() { return cudaGetLastError() == cudaSuccess ? SV_OK : SV_ERR_CUDA; }
+
+size_t up(size_t n) { return (n + 255) / 256 * 256; }
+
+}  // namespace
+
+// owner, is_parent, then five lists of n + 1 (fork: rank, free, take; reserve:
+// need, tok, ok), then three of num_pages (reserve: free; compact: src, dst,
+// to) and a word.
+size_t pages_workspace_bytes(int64_t num_pages, int num_rows, int n) {
+    return 2 * up(4ull * num_rows) + 3 * up(4ull * (static_cast<size_t>(n) + 1)) + 3 * up(4ull * num_pages) + 256;
+}
+
+namespace {
+struct Carve {
+    int32_t *owner, *is_parent, *a, *b, *c, *p, *q, *r, *word;
+    Carve(void* ws, int64_t num_pages, int num_rows, int n) {
+        unsigned char* at = static_cast<unsigned char*>(ws);
+        auto take = [&](size_t ints) { int32_t* x = reinterpret_cast<int32_t*>(at); at += up(4 * ints); return x; };
+        owner = take(num_rows);
+        is_parent = take(num_rows);
+        a = take(static_cast<size_t>(n) + 1);
+        b = take(static_cast<size_t>(n) + 1);
+        c = take(static_cast<size_t>(n) + 1);
+        p = take(num_pages);
+        q = take(num_pages);
+        r = take(num_pages);
+        word = take(1);
+    }
+};
+}  // namespace
+
+int launch_pages_copy(const sv_cache* caches, int num_caches, const int32_t* src, const int32_t* dst, int n,
+                      cudaStream_t stream) {
+    CacheSet set;
+    fill_set(&set, caches, num_caches);
+    copy_pages_kernel<<<dim3(n, num_caches), kMoveThreads, 0, stream>>>(set, src, dst,
+                                                                        static_cast<int>(caches[0].num_phys_pages));
+    return status();
+}
+
+int launch_pages_fork(const sv_cache* caches, int num_caches, int32_t* table, int32_t* lens, int num_rows, int max_pages,
+                      int32_t* counts, const int32_t* parents, const int32_t* children, int n, void* ws,
+                      cudaStream_t stream) {
+    CacheSet set;
+    fill_set(&set, caches, num_caches);
+    const int num_pages = static_cast<int>(caches[0].num_phys_pages);
+    const Carve w(ws, num_pages, num_rows, n);
+    ForkArgs a = {{table, lens, num_rows, max_pages, counts, num_pages}, parents, children, n, w.owner, w.is_parent,
+                  w.a, w.b, w.c};
+    fork_plan_kernel<<<kCluster, kPlanThreads, 0, stream>>>(a);
+    if (status()) return SV_ERR_CUDA;
+    return launch_pdl(fork_move_kernel, dim3(n, num_caches + 1), dim3(kMoveThreads), 0, stream, set, a) == cudaSuccess
+               ? SV_OK
+               : SV_ERR_CUDA;
+}
+
+int launch_pages_reserve(int32_t* table, int32_t* lens, int num_rows, int max_pages, int32_t* counts, int num_pages,
+                         const int32_t* rows, const int32_t* add, int n, int32_t* slots, int num_slots, void* ws,
+                         cudaStream_t stream) {
+    const Carve w(ws, num_pages, num_rows, n);
+    ReserveArgs a = {{table, lens, num_rows, max_pages, counts, num_pages}, rows, add, n, slots, num_slots, w.owner,
+                     w.a, w.b, w.c, w.p};
+    reserve_kernel<<<kCluster, kPlanThreads, 0, stream>>>(a);
+    return status();
+}
+
+int launch_pages_free(int32_t* table, int32_t* lens, int num_rows, int max_pages, int32_t* counts, int num_pages,
+                      const int32_t* rows, const int32_t* first, const int32_t* end, int n, cudaStream_t stream) {
+    const Rows t = {table, lens, num_rows, max_pages, counts, num_pages};
+    free_kernel<<<n, kMoveThreads, 0, stream>>>(t, rows, first, end);
+    return status();
+}
+
+int launch_pages_compact(const sv_cache* caches, int num_caches, const int32_t* table, const int32_t* lens, int num_rows,
+                         int max_pages, const int32_t* counts, int32_t* table_out, int32_t* counts_out, int32_t* live,
+                         void* ws, int sm_count, cudaStream_t stream) {
+    CacheSet set;
+    fill_set(&set, caches, num_caches);
+    const int num_pages = static_cast<int>(caches[0].num_phys_pages);
+    const Carve w(ws, num_pages, num_rows, 0);
+    CompactArgs a = {{const_cast<int32_t*>(table), const_cast<int32_t*>(lens), num_rows, max_pages,
+                      const_cast<int32_t*>(counts), num_pages},
+                     table_out, counts_out, live, w.p, w.q, w.r, w.word};
+    compact_plan_kernel<<<kCluster, kPlanThreads, 0, stream>>>(a);
+    if (status()) return SV_ERR_CUDA;
+    return launch_pdl(compact_move_kernel, dim3(sm_count * 6), dim3(kMoveThreads), 0, stream, set, a) == cudaSuccess
+               ? SV_OK
+               : SV_ERR_CUDA;
+}
+
+}  // namespace svq
