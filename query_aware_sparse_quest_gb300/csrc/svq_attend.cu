@@ -22,7 +22,8 @@
 // does not grow with the problem.
 //
 // Roles of a CTA (one per SM; TMEM holds S0, S1, O0, O1 of 128 columns each):
-//   warp 0       loads pages through a ring of 32 KB stages (TMA, one box a page)
+//   warps 0, 3   load key and value pages through a ring of 32 KB stages (TMA, one
+//                box a page)
 //   warp 1       issues the MMAs (one thread)
 //   warps 4-7    softmax of stream 0, one row a thread
 //   warps 8-11   softmax of stream 1
@@ -130,24 +131,51 @@ __device__ __forceinline__ int warp_find(const int64_t* cum, int n, int64_t u) {
 }
 
 // ---------------------------------------------------------------- tcgen05
-__device__ __forceinline__ uint64_t smem_desc(uint32_t addr, uint32_t lbo, uint32_t sbo) {
-    return static_cast<uint64_t>((addr & 0x3ffffu) >> 4) | (static_cast<uint64_t>(lbo >> 4) << 16) |
-           (static_cast<uint64_t>(sbo >> 4) << 32) | (1ull << 46) | (2ull << 61);   // version 1, 128-byte swizzle
-}
 // bf16 x bf16 -> fp32, M = 128, N = 128, A K-major; B K-major (keys) or N-major (values).
 constexpr uint32_t kIdescQK = (1u << 4) | (1u << 7) | (1u << 10) | ((128u / 8) << 17) | ((128u / 16) << 24);
 constexpr uint32_t kIdescPV = kIdescQK | (1u << 16);
 
-__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+// Descriptors differ in their low words only; the high words (stride, version,
+// swizzle) are constants.  Eight k steps are issued from one statement, so that
+// the issuing thread keeps ahead of the tensor pipe (64 cycles a step): with a
+// descriptor built for each step it fell behind (2 x the pipe's time).
+constexpr uint32_t desc_hi(uint32_t sbo) { return (sbo >> 4) | (1u << 14) | (2u << 29); }
+__device__ __forceinline__ uint32_t desc_lo(uint32_t addr, uint32_t lbo) { return (addr >> 4) | (lbo >> 4 << 16); }
+
+#define SVQ_MMA_SS(ao, bo, acc)                                                  \
+    "add.u32 al, %1, " #ao ";\n\tadd.u32 bl, %2, " #bo ";\n\t"                   \
+    "mov.b64 ad, {al, %3};\n\tmov.b64 bd, {bl, %4};\n\t"                         \
+    "tcgen05.mma.cta_group::1.kind::f16 [%0], ad, bd, %5, " #acc ";\n\t"
+// S = Q K^T: channels 16 k .. of both operands are 32 bytes further in a half's
+// rows (2 in the descriptor); the second half is 16 KB (Q) and 1 KB (K) on.
+__device__ __forceinline__ void mma_qk(uint32_t d, uint32_t q_lo, uint32_t k_lo, uint32_t idesc) {
     asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(acc)
+        "{\n\t.reg .pred no, yes;\n\t.reg .b32 al, bl;\n\t.reg .b64 ad, bd;\n\t"
+        "setp.ne.u32 no, 0, 0;\n\tsetp.eq.u32 yes, 0, 0;\n\t"
+        SVQ_MMA_SS(0, 0, no) SVQ_MMA_SS(2, 2, yes) SVQ_MMA_SS(4, 4, yes) SVQ_MMA_SS(6, 6, yes)
+        SVQ_MMA_SS(1024, 64, yes) SVQ_MMA_SS(1026, 66, yes) SVQ_MMA_SS(1028, 68, yes) SVQ_MMA_SS(1030, 70, yes)
+        "}" ::"r"(d), "r"(q_lo), "r"(k_lo), "r"(desc_hi(1024)), "r"(desc_hi(2048)), "r"(idesc)
         : "memory");
 }
-__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+#define SVQ_MMA_TS(ao, bo, acc)                                                  \
+    "add.u32 al, %1, " #ao ";\n\tadd.u32 bl, %2, " #bo ";\n\t"                   \
+    "mov.b64 bd, {bl, %3};\n\t"                                                  \
+    "tcgen05.mma.cta_group::1.kind::f16 [%0], [al], bd, %4, " #acc ";\n\t"
+// O (+)= P V over a whole tile: one step a page (8 TMEM columns, 4 KB).
+__device__ __forceinline__ void mma_pv8(uint32_t d, uint32_t p, uint32_t v_lo, uint32_t idesc, uint32_t acc) {
     asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d), "r"(a), "l"(b), "r"(idesc), "r"(acc)
+        "{\n\t.reg .pred acc, yes;\n\t.reg .b32 al, bl;\n\t.reg .b64 bd;\n\t"
+        "setp.ne.u32 acc, %5, 0;\n\tsetp.eq.u32 yes, 0, 0;\n\t"
+        SVQ_MMA_TS(0, 0, acc) SVQ_MMA_TS(8, 256, yes) SVQ_MMA_TS(16, 512, yes) SVQ_MMA_TS(24, 768, yes)
+        SVQ_MMA_TS(32, 1024, yes) SVQ_MMA_TS(40, 1280, yes) SVQ_MMA_TS(48, 1536, yes) SVQ_MMA_TS(56, 1792, yes)
+        "}" ::"r"(d), "r"(p), "r"(v_lo), "r"(desc_hi(2048)), "r"(idesc), "r"(acc)
+        : "memory");
+}
+__device__ __forceinline__ void mma_pv1(uint32_t d, uint32_t p, uint32_t v_lo, uint32_t idesc, uint32_t acc) {
+    asm volatile(
+        "{\n\t.reg .pred acc;\n\t.reg .b32 al, bl;\n\t.reg .b64 bd;\n\tsetp.ne.u32 acc, %5, 0;\n\t"
+        SVQ_MMA_TS(0, 0, acc)
+        "}" ::"r"(d), "r"(p), "r"(v_lo), "r"(desc_hi(2048)), "r"(idesc), "r"(acc)
         : "memory");
 }
 __device__ __forceinline__ void mma_commit(uint32_t bar) {
@@ -169,16 +197,32 @@ __device__ __forceinline__ void tc_ld32(uint32_t addr, uint32_t (&r)[32]) {
           "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
         : "r"(addr));
 }
-__device__ __forceinline__ void tc_st32(uint32_t addr, const uint32_t (&r)[32]) {
+__device__ __forceinline__ void tc_ld16(uint32_t addr, uint32_t (&r)[16]) {
     asm volatile(
-        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
-        "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,"
-        "%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(addr),
-        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
-        "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]),
-        "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]),
-        "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
-        : "memory");
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+        "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(addr));
+}
+// Two fp32 values in one 64-bit register, for the paired fp32 instructions.
+__device__ __forceinline__ uint64_t pack2(float lo, float hi) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+    return r;
+}
+__device__ __forceinline__ void unpack2(uint64_t v, float& lo, float& hi) {
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
 }
 __device__ __forceinline__ void tc_st16(uint32_t addr, const uint32_t (&r)[16]) {
     asm volatile(
@@ -194,6 +238,10 @@ __device__ __forceinline__ void tma_load_4d(uint32_t dst, const void* tmap, int 
         ::"r"(dst), "l"(tmap), "r"(0), "r"(y), "r"(bar)
         : "memory");
 }
+template <int N>
+__device__ __forceinline__ void reg_dec() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
+template <int N>
+__device__ __forceinline__ void reg_inc() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
 __device__ __forceinline__ float ex2(float x) {
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -211,6 +259,10 @@ struct Cfg {
     static constexpr int kCodes = kCodeStages * kTileTok * kHeadDim;
     static constexpr int kScales = FP8 ? kInfoSlots * 2 * kTileTok * 4 : 0;
     static constexpr int kControl = 3072;
+    // Registers a thread after the start (the block is launched with 168 or 128 for each):
+    // 128 x 88 + 256 x 208 = 384 x 168; 256 x 80 + 256 x 176 = 512 x 128.
+    static constexpr int kOtherRegs = FP8 ? 80 : 88;
+    static constexpr int kSoftmaxRegs = FP8 ? 176 : 208;
     static constexpr int kSmem = kRing + kQ + kCodes + kScales + kControl;
 };
 static_assert(Cfg<false>::kSmem <= 227 * 1024 && Cfg<true>::kSmem <= 227 * 1024, "shared memory of one CTA");
@@ -289,10 +341,19 @@ __device__ __forceinline__ int last_pos(const Entry& en) {
     return en.pos0 == kAllVisible ? kAllVisible : en.pos0 + en.ntok - 1;
 }
 
+// The loads of a segment of n tiles, in order: K0 K1 V0 K2 V1 .. K(n-1) V(n-2) V(n-1):
+// the place of a tile's keys and values, and which load a place is.
+__device__ __forceinline__ uint32_t k_load(int t) { return t == 0 ? 0u : 2u * t - 1u; }
+__device__ __forceinline__ uint32_t v_load(int t, int n) { return t == n - 1 ? 2u * n - 1u : 2u * t + 2u; }
+__device__ __forceinline__ bool load_is_k(int i, int n) { return i == 0 || (i != 2 * n - 1 && (i & 1)); }
+__device__ __forceinline__ int load_tile(int i, int n) {
+    return load_is_k(i, n) ? (i + 1) / 2 : (i == 2 * n - 1 ? n - 1 : i / 2 - 1);
+}
+
 // Four e4m3 codes -> two bf16 pairs, exactly: the code's exponent and mantissa
 // fields are moved under bf16's, which scales the value by 2^-120; the product
-// with 2^120 is exact, subnormal codes included.  The two NaN codes, which that
-// would read as +-480, stay NaN.
+// with 2^120 is exact, subnormal codes included.  The two NaN codes would read
+// as +-480: see has_nan.
 __device__ __forceinline__ void widen4(uint32_t c, uint32_t& lo, uint32_t& hi) {
     const uint32_t a = __byte_perm(c, 0u, 0x1404);   // bytes 1, 0 of c in the high bytes of the halves
     const uint32_t b = __byte_perm(c, 0u, 0x3424);
@@ -303,19 +364,41 @@ __device__ __forceinline__ void widen4(uint32_t c, uint32_t& lo, uint32_t& hi) {
     const __nv_bfloat162 yr = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&y), two120);
     lo = *reinterpret_cast<const uint32_t*>(&xr);
     hi = *reinterpret_cast<const uint32_t*>(&yr);
-    const uint32_t nan = __vcmpeq4(c & 0x7f7f7f7fu, 0x7f7f7f7fu);
-    if (nan) {
-        if (nan & 0x000000ffu) lo |= 0x00007fffu;
-        if (nan & 0x0000ff00u) lo |= 0x7fff0000u;
-        if (nan & 0x00ff0000u) hi |= 0x00007fffu;
-        if (nan & 0xff000000u) hi |= 0x7fff0000u;
-    }
+}
+// Bit 7 of every byte of c that is a NaN code (0x7f or 0xff).
+__device__ __forceinline__ uint32_t has_nan(uint32_t c) { return ((c & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u; }
+__device__ __forceinline__ void keep_nan(uint32_t c, uint32_t& lo, uint32_t& hi) {
+    const uint32_t n = has_nan(c);
+    if (n & 0x00000080u) lo |= 0x00007fffu;
+    if (n & 0x00008000u) lo |= 0x7fff0000u;
+    if (n & 0x00800000u) hi |= 0x00007fffu;
+    if (n & 0x80000000u) hi |= 0x7fff0000u;
 }
 
-// A bounded wait by a whole warp; all of it leaves for `out` when it gave up.
+// Waits for a phase of an mbarrier, at most kPolls polls of at most kPollNs each
+// (0.5 s; no wait here comes near it: copies land in microseconds); false when
+// it gave up.  Few instructions, as every role's loop has several: the roles of
+// a CTA share the instruction caches.
+constexpr uint32_t kPolls = 1u << 19;
+constexpr uint32_t kPollNs = 1000;
+__device__ __forceinline__ bool bar_wait(uint32_t bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p, more;\n\t.reg .u32 i;\n\tmov.u32 i, 0;\n"
+        "again:\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %4;\n\t"
+        "@p bra done;\n\t"
+        "add.u32 i, i, 1;\n\tsetp.lt.u32 more, i, %3;\n\t@more bra again;\n"
+        "done:\n\tselp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity), "n"(kPolls), "r"(kPollNs)
+        : "memory");
+    return ok != 0;
+}
+// The same by a whole warp; all of it leaves for `out` when it gave up.
 #define SVQ_WAIT(bar, parity, out)                                                        \
     do {                                                                                  \
-        if (__any_sync(0xffffffffu, !mbar_wait_bounded(smem_addr(&(bar)), (parity)))) {   \
+        if (__any_sync(0xffffffffu, !bar_wait(smem_addr(&(bar)), (parity)))) {   \
             if (lane == 0) svq_flag(SV_DEVERR_TIMEOUT);                                   \
             goto out;                                                                     \
         }                                                                                 \
@@ -387,115 +470,132 @@ __global__ void __launch_bounds__(Cfg<FP8>::kThreads, 1)
     const uint32_t tmem = ct->tmem;
 
     if (count > 0) {
-        if (warp == 0) {
-            // ---------------- loads
+        if (warp == 0 || warp == 3) {
+            // ---------------- loads: warp 0 keys, warp 3 values
+            reg_dec<C::kOtherRegs>();
+            const bool is_v = warp == 3;
+            const void* const map = is_v ? static_cast<const void*>(&tmap_v) : static_cast<const void*>(&tmap_k);
+            const unsigned char* const pool = is_v ? a.v_pool : a.k_pool;
+            constexpr uint32_t kDepth = FP8 ? C::kCodeStages : C::kStages;
+            uint64_t* const full = FP8 ? ct->code_full : ct->full;
+            uint64_t* const empty = FP8 ? ct->code_empty : ct->empty;
+            const uint32_t to = FP8 ? smem_addr(codes) : smem_addr(ring);
+            constexpr uint32_t kTo = FP8 ? kTileTok * kHeadDim : kStageBytes;   // bytes of a stage, of a page
+            constexpr uint32_t kToPage = kTo / kTilePages;
             Walk walk(a, ct, count);
-            Seg s;
-            uint32_t ld = 0, tile = 0;   // loads and key tiles issued
-            constexpr int kDepth = FP8 ? C::kCodeStages : C::kStages;
-            while (walk.next(s)) {
+            Seg s, nx;
+            uint32_t base = 0, tile = 0;   // loads and key tiles before the segment
+            uint32_t last[3] = {0, 0, 0};  // the last loads issued here, each plus 1
+            // Lane l resolves page i + l of the segment's list (four tiles at a time), well
+            // before the loads that need it: the row (page, kv head) of the pool, or -1.
+            auto fetch = [&](const Seg& g, int i0) {
+                const int i = i0 + lane;
+                int ph = -2;               // behind the segment's pages
+                if (i < min(g.en.npages, g.t1 * kTilePages))
+                    ph = a.page_table[static_cast<int64_t>(g.en.req) * a.max_pages + logical_page(g.en, i)];
+                return ph;
+            };
+            bool more = walk.next(s);
+            int cur = -2, nxt = more ? fetch(s, s.t0 * kTilePages) : -2, seg = -2;
+            while (more) {
+                const bool have_next = walk.next(nx);
+                if (have_next) seg = fetch(nx, nx.t0 * kTilePages);
                 const int n = s.t1 - s.t0;
                 const int qlo = s.en.pos0, qhi = last_pos(s.en);
-                const int32_t* row = a.page_table + static_cast<int64_t>(s.en.req) * a.max_pages;
-                // Lane l resolves page l of a tile one tile ahead of its loads.
-                auto fetch = [&](int t, int& lp, int& ph) {
-                    const int i = t * kTilePages + lane;
-                    lp = ph = -1;
-                    if (lane < kTilePages && i < s.en.npages && t < s.t1) {
-                        lp = logical_page(s.en, i);
-                        ph = row[lp];
+                for (int i = 0; i < n; ++i) {
+                    if (i % 4 == 0) {
+                        cur = nxt;
+                        nxt = fetch(s, (s.t0 + i + 4) * kTilePages);
                     }
-                };
-                int lp, ph, lp_next, ph_next, lp_prev = -1, ph_prev = -1;
-                fetch(s.t0, lp_next, ph_next);
-                for (int i = 0; i <= n; ++i) {
-                    lp = lp_next;
-                    ph = ph_next;
-                    fetch(s.t0 + i + 1, lp_next, ph_next);
-                    // K of tile i, then V of tile i - 1.
+                    const uint32_t at = base + (is_v ? v_load(i, n) : k_load(i));
+                    const uint32_t st = at % kDepth;
+                    int ph = __shfl_sync(0xffffffffu, cur, (i % 4) * kTilePages + (lane & 7));
+                    if (lane >= kTilePages) ph = -2;
+                    const bool bad = ph != -2 && (ph < 0 || ph >= a.num_phys_pages);
+                    uint32_t seen = 0xffffu;
+                    if (!FP8 && is_v && ph != -2) {
+                        seen = union_mask(logical_page(s.en, (s.t0 + i) * kTilePages + lane) * kPage, qlo, qhi, a.window, a.sink);
+                        if (bad) seen = 0u;
+                    }
+                    const uint32_t faults = __ballot_sync(0xffffffffu, bad);
+                    const uint32_t parts = __ballot_sync(0xffffffffu, seen != 0xffffu);
+                    const bool load = ph != -2 && !bad && seen == 0xffffu;
+                    const uint32_t loads = __ballot_sync(0xffffffffu, load);
+                    const int64_t from = (static_cast<int64_t>(bad ? 0 : ph) * a.num_kv_heads + s.h);
+                    // Value pages with tokens that no row sees: those tokens may hold anything, so
+                    // the warp copies such a page with zeros in their place (P = 0 must not meet a
+                    // NaN).  At most three pages of an item: the sinks' last, the window's first,
+                    // the last; and pages that the table does not give.  The first one's data are
+                    // requested before the stage is free.
+                    uint4 v[8];
+                    auto request = [&](int p) {
+                        const uint32_t m = __shfl_sync(0xffffffffu, seen, p);
+                        const uint4* src = reinterpret_cast<const uint4*>(a.v_pool + __shfl_sync(0xffffffffu, from, p) * kPageBytes);
 #pragma unroll
-                    for (int kv = 0; kv < 2; ++kv) {
-                        if (kv == 0 ? i == n : i == 0) continue;
-                        const int my_lp = kv == 0 ? lp : lp_prev;
-                        int my_ph = kv == 0 ? ph : ph_prev;
-                        const bool bad = my_lp >= 0 && (my_ph < 0 || my_ph >= a.num_phys_pages);
-                        const uint32_t faults = __ballot_sync(0xffffffffu, bad);
-                        const int st = ld % kDepth;
-                        uint64_t* const full = FP8 ? &ct->code_full[st] : &ct->full[st];
-                        uint64_t* const empty = FP8 ? &ct->code_empty[st] : &ct->empty[st];
-                        SVQ_WAIT(*empty, ((ld / kDepth) & 1) ^ 1, loads_end);
-                        const uint32_t bar = smem_addr(full);
-                        const bool load = my_lp >= 0 && !bad;
-                        if (kv == 0 && lane == 0) ct->fault[tile % kInfoSlots] = static_cast<int>(faults);
-                        if (faults && lane == 0) svq_flag(SV_DEVERR_PAGE_TABLE);
-                        const int64_t at = (static_cast<int64_t>(load ? my_ph : 0) * a.num_kv_heads + s.h);
-                        if (FP8) {
-                            const uint32_t loads = __ballot_sync(0xffffffffu, load);
-                            const uint32_t bytes = __popc(loads) * (kPage * kHeadDim + (kv == 0 ? 2 * kPage * 4 : 0));
-                            if (lane == 0) {
-                                if (bytes) mbar_arrive_expect_tx(bar, bytes);
-                                else mbar_arrive(bar);
+                        for (int k = 0; k < 8; ++k) {
+                            const int r = 2 * k + (lane >> 4);
+                            v[k] = (m >> r) & 1u ? src[r * 16 + (lane & 15)] : make_uint4(0u, 0u, 0u, 0u);
+                        }
+                    };
+                    if (!FP8 && parts) request(__ffs(parts) - 1);
+                    SVQ_WAIT(empty[st], ((at / kDepth) & 1) ^ 1, loads_end);
+                    if (faults && !is_v && lane == 0) svq_flag(SV_DEVERR_PAGE_TABLE);
+                    if (!is_v && lane == 0) ct->fault[(tile + i) % kInfoSlots] = static_cast<int>(faults);
+                    if (!FP8 && parts) {
+                        for (uint32_t rest = parts; rest;) {
+                            unsigned char* const o = ring + st * kStageBytes + (__ffs(rest) - 1) * kPageBytes;
+#pragma unroll
+                            for (int k = 0; k < 8; ++k) {
+                                const int r = 2 * k + (lane >> 4), c = lane & 15;
+                                *reinterpret_cast<uint4*>(o + (r >> 3) * 2048 + (c >> 3) * 1024 + (r & 7) * 128 +
+                                                          (((c & 7) ^ (r & 7)) << 4)) = v[k];
                             }
-                            __syncwarp();
-                            if (load) {
-                                const uint32_t dst = smem_addr(codes) + st * (kTileTok * kHeadDim) + lane * (kPage * kHeadDim);
-                                bulk_copy_g2s(dst, (kv == 0 ? a.k_pool : a.v_pool) + at * (kPage * kHeadDim),
-                                              kPage * kHeadDim, bar);
-                                if (kv == 0) {
-                                    const uint32_t sc = smem_addr(scales + (tile % kInfoSlots) * 2 * kTileTok + lane * kPage);
-                                    bulk_copy_g2s(sc, a.k_scale + at * kPage, kPage * 4, bar);
-                                    bulk_copy_g2s(sc + kTileTok * 4, a.v_scale + at * kPage, kPage * 4, bar);
-                                }
+                            rest &= rest - 1;
+                            if (rest) request(__ffs(rest) - 1);
+                        }
+                        fence_proxy_async_smem();
+                        __syncwarp();
+                    }
+                    const uint32_t bar = smem_addr(&full[st]);
+                    if (lane == 0) {
+                        const uint32_t bytes = __popc(loads) * (kToPage + (FP8 && !is_v ? 2 * kPage * 4 : 0));
+                        if (bytes) mbar_arrive_expect_tx(bar, bytes);
+                        else mbar_arrive(bar);
+                    }
+                    __syncwarp();
+                    if (load) {
+                        const uint32_t dst = to + st * kTo + lane * kToPage;
+                        if (FP8) {
+                            bulk_copy_g2s(dst, pool + from * kToPage, kToPage, bar);
+                            if (!is_v) {
+                                const uint32_t sc = smem_addr(scales + (tile + i) % kInfoSlots * 2 * kTileTok + lane * kPage);
+                                bulk_copy_g2s(sc, a.k_scale + from * kPage, kPage * 4, bar);
+                                bulk_copy_g2s(sc + kTileTok * 4, a.v_scale + from * kPage, kPage * 4, bar);
                             }
                         } else {
-                            // A value page with tokens that no row sees (they may hold anything) is
-                            // copied by the warp with zeros in their place, so that P = 0 never
-                            // meets a NaN; a page the table does not give is all zeros.
-                            const uint32_t seen = my_lp < 0 ? 0u : union_mask(my_lp * kPage, qlo, qhi, a.window, a.sink);
-                            const bool part = kv == 1 && my_lp >= 0 && (bad || seen != 0xffffu);
-                            const uint32_t parts = __ballot_sync(0xffffffffu, part);
-                            const uint32_t loads = __ballot_sync(0xffffffffu, load && !part);
-                            unsigned char* const stage = ring + st * kStageBytes;
-                            for (uint32_t rest = parts; rest; rest &= rest - 1) {
-                                const int p = __ffs(rest) - 1;
-                                const uint32_t m = __shfl_sync(0xffffffffu, bad ? 0u : seen, p);
-                                const int64_t from = __shfl_sync(0xffffffffu, at, p);
-                                const uint4* src = reinterpret_cast<const uint4*>(a.v_pool + from * kPageBytes);
-#pragma unroll
-                                for (int k = 0; k < 8; ++k) {
-                                    const int r = 2 * k + (lane >> 4), c = lane & 15;
-                                    const uint4 v = (m >> r) & 1u ? src[r * 16 + c] : make_uint4(0u, 0u, 0u, 0u);
-                                    *reinterpret_cast<uint4*>(stage + p * kPageBytes + (r >> 3) * 2048 + (c >> 3) * 1024 +
-                                                              (r & 7) * 128 + (((c & 7) ^ (r & 7)) << 4)) = v;
-                                }
-                            }
-                            if (parts) fence_proxy_async_smem();
-                            __syncwarp();
-                            if (lane == 0) {
-                                if (loads) mbar_arrive_expect_tx(bar, __popc(loads) * kPageBytes);
-                                else mbar_arrive(bar);
-                            }
-                            __syncwarp();
-                            if (load && !part)
-                                tma_load_4d(smem_addr(stage) + lane * kPageBytes,
-                                            kv == 0 ? static_cast<const void*>(&tmap_k) : static_cast<const void*>(&tmap_v),
-                                            static_cast<int>(at * 2), bar);
+                            tma_load_4d(dst, map, static_cast<int>(from * 2), bar);
                         }
-                        ++ld;
-                        if (kv == 0) ++tile;
                     }
-                    lp_prev = lp;
-                    ph_prev = ph;
+                    last[2] = last[1];
+                    last[1] = last[0];
+                    last[0] = at + 1;
                 }
+                base += 2 * n;
+                tile += n;
+                s = nx;
+                more = have_next;
+                nxt = seg;
             }
+            goto loads_done;   // every load has been waited for by the MMAs or the widening warps
         loads_end:
-            // The copies in flight land before the CTA (and its shared memory) retires.
-            for (uint32_t i = ld > kDepth ? ld - kDepth : 0; i < ld; ++i) {
-                uint64_t* const full = FP8 ? &ct->code_full[i % kDepth] : &ct->full[i % kDepth];
-                (void)mbar_wait_bounded(smem_addr(full), (i / kDepth) & 1);
-            }
+            // Gave up: the copies still in flight land before the CTA (and its shared memory)
+            // retires; at most three of the ring's loads are this warp's.
+            for (int k = 0; k < 3; ++k)
+                if (last[k]) (void)bar_wait(smem_addr(&full[(last[k] - 1) % kDepth]), ((last[k] - 1) / kDepth) & 1);
+        loads_done:;
         } else if (warp == 1) {
             // ---------------- MMAs (one thread)
+            reg_dec<C::kOtherRegs>();
             if (lane == 0) {
                 Walk walk(a, ct, count);
                 Seg s;
@@ -505,21 +605,17 @@ __global__ void __launch_bounds__(Cfg<FP8>::kThreads, 1)
                 while (walk.next(s)) {
                     const int n = s.t1 - s.t0;
                     const bool two = s.en.ntok * group > 128;   // two row halves; else even and odd tiles
-                    // Loads of the segment in order: K0 K1 V0 K2 V1 .. K(n-1) V(n-2) V(n-1).
-                    auto k_at = [&](int t) { return ld + (t == 0 ? 0u : 2u * t - 1u); };
-                    auto v_at = [&](int t) { return ld + (t == n - 1 ? 2u * n - 1u : 2u * t + 2u); };
+                    auto k_at = [&](int t) { return ld + k_load(t); };
+                    auto v_at = [&](int t) { return ld + v_load(t, n); };
                     auto wait_load = [&](uint32_t i) {
-                        return mbar_wait_bounded(smem_addr(&ct->full[i % C::kStages]), (i / C::kStages) & 1);
+                        return bar_wait(smem_addr(&ct->full[i % C::kStages]), (i / C::kStages) & 1);
                     };
                     auto qk = [&](int w, int t) {
                         if (!wait_load(k_at(t))) return false;
                         tc_fence_after();
                         const uint32_t ks = ring_s + (k_at(t) % C::kStages) * kStageBytes;
                         const uint32_t qw = qs_s + w * (128 * kHeadDim * 2);
-#pragma unroll
-                        for (int k = 0; k < 8; ++k)
-                            mma_ss(tmem + kColS + w * 128, smem_desc(qw + (k >> 2) * 16384 + (k & 3) * 32, 16, 1024),
-                                   smem_desc(ks + (k >> 2) * 1024 + (k & 3) * 32, 16, 2048), kIdescQK, k != 0);
+                        mma_qk(tmem + kColS + w * 128, desc_lo(qw, 16), desc_lo(ks, 16), kIdescQK);
                         mma_commit(smem_addr(&ct->s_full[w]));
                         return true;
                     };
@@ -528,9 +624,15 @@ __global__ void __launch_bounds__(Cfg<FP8>::kThreads, 1)
                         tc_fence_after();
                         const uint32_t vs = ring_s + (v_at(t) % C::kStages) * kStageBytes;
                         const int pages = min(kTilePages, s.en.npages - (s.t0 + t) * kTilePages);
-                        for (int k = 0; k < pages; ++k)
-                            mma_ts(tmem + kColO + w * 128, tmem + kColS + w * 128 + k * 8, smem_desc(vs + k * kPageBytes, 1024, 2048),
-                                   kIdescPV, acc || k != 0);
+                        const uint32_t o = tmem + kColO + w * 128, p = tmem + kColS + w * 128;
+                        // The two 64-channel halves of a value tile are 1 KB apart (N-major operand).
+                        const uint32_t lo = desc_lo(vs, 1024);
+                        if (pages == kTilePages) {
+                            mma_pv8(o, p, lo, kIdescPV, acc);
+                        } else {
+                            for (int k = 0; k < pages; ++k)
+                                mma_pv1(o, p + k * 8, lo + k * (kPageBytes >> 4), kIdescPV, acc || k != 0);
+                        }
                         return true;
                     };
                     auto release = [&](uint32_t i) { mma_commit(smem_addr(&ct->empty[i % C::kStages])); };
@@ -538,7 +640,7 @@ __global__ void __launch_bounds__(Cfg<FP8>::kThreads, 1)
                     for (int w = 0; w < 2 && ok; ++w) {
                         const int t = two ? 0 : w;
                         if (t >= n) break;
-                        ok = mbar_wait_bounded(smem_addr(&ct->q_full[w]), q_ph[w]) && qk(w, t);
+                        ok = bar_wait(smem_addr(&ct->q_full[w]), q_ph[w]) && qk(w, t);
                         q_ph[w] ^= 1;
                         if (ok && (!two || w == 1)) release(k_at(t));
                     }
@@ -547,7 +649,7 @@ __global__ void __launch_bounds__(Cfg<FP8>::kThreads, 1)
                             if (!two && v != (t & 1)) continue;
                             const int w = v;
                             const int step = two ? 1 : 2;
-                            ok = mbar_wait_bounded(smem_addr(&ct->p_full[w]), p_ph[w]);
+                            ok = bar_wait(smem_addr(&ct->p_full[w]), p_ph[w]);
                             p_ph[w] ^= 1;
                             ok = ok && pv(w, t, t >= step);
                             if (!ok) break;
@@ -567,11 +669,14 @@ __global__ void __launch_bounds__(Cfg<FP8>::kThreads, 1)
                     ld += 2 * n;
                 }
                 mma_commit(smem_addr(&ct->drain));   // nothing of this CTA's is in flight when TMEM is freed
-                (void)mbar_wait_bounded(smem_addr(&ct->drain), 0);
+                (void)bar_wait(smem_addr(&ct->drain), 0);
             }
             __syncwarp();
-        } else if (warp >= 4 && warp < 12) {
+        } else if (warp < 4) {
+            reg_dec<C::kOtherRegs>();
+        } else if (warp < 12) {
             // ---------------- softmax: warps 4-7 stream 0, warps 8-11 stream 1
+            reg_inc<C::kSoftmaxRegs>();
             const int w = (warp - 4) >> 2;
             const int row = (warp & 3) * 32 + lane;
             const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
@@ -652,100 +757,85 @@ __global__ void __launch_bounds__(Cfg<FP8>::kThreads, 1)
                             return bits;
                         };
                         const float4* ks = reinterpret_cast<const float4*>(scales + slot * 2 * kTileTok);
-                        const float4* vs = ks + kTileTok / 4;
-                        // Pass 1: the tile's maximum.
-                        float mx = -INFINITY;
+                        const float2* vs = reinterpret_cast<const float2*>(ks + kTileTok / 4);
+                        // The row's 128 logits stay in registers from here to P.
+                        float x[128];
 #pragma unroll
-                        for (int c = 0; c < 4; ++c) {
-                            uint32_t x[32];
-                            tc_ld32(s_col + c * 32, x);
-                            tc_wait_ld();
-                            if (FP8) {
+                        for (int c = 0; c < 4; ++c) tc_ld32(s_col + c * 32, reinterpret_cast<uint32_t(&)[32]>(x[c * 32]));
+                        tc_wait_ld();
+                        if (FP8) {
 #pragma unroll
-                                for (int u = 0; u < 8; ++u) {
-                                    const float4 k4 = ks[c * 8 + u];
-                                    x[4 * u] = __float_as_uint(__uint_as_float(x[4 * u]) * k4.x);
-                                    x[4 * u + 1] = __float_as_uint(__uint_as_float(x[4 * u + 1]) * k4.y);
-                                    x[4 * u + 2] = __float_as_uint(__uint_as_float(x[4 * u + 2]) * k4.z);
-                                    x[4 * u + 3] = __float_as_uint(__uint_as_float(x[4 * u + 3]) * k4.w);
-                                }
+                            for (int u = 0; u < 32; ++u) {
+                                const float4 k4 = ks[u];
+                                x[4 * u] *= k4.x;
+                                x[4 * u + 1] *= k4.y;
+                                x[4 * u + 2] *= k4.z;
+                                x[4 * u + 3] *= k4.w;
                             }
-                            if (plain) {
+                        }
+                        if (!plain) {
 #pragma unroll
-                                for (int u = 0; u < 32; u += 2)
-                                    mx = fmaxf(fmaxf(mx, __uint_as_float(x[u])), __uint_as_float(x[u + 1]));
-                            } else {
+                            for (int c = 0; c < 4; ++c) {
                                 const uint32_t bits = mask_of(c);
 #pragma unroll
                                 for (int u = 0; u < 32; ++u)
-                                    mx = fmaxf(mx, (bits >> u) & 1u ? __uint_as_float(x[u]) : -INFINITY);
+                                    if (!((bits >> u) & 1u)) x[c * 32 + u] = -INFINITY;
                             }
                         }
-                        mx *= a.scale_log2;
+                        float mx[4];
+#pragma unroll
+                        for (int c = 0; c < 4; ++c) {
+                            mx[c] = fmaxf(x[c * 32], x[c * 32 + 1]);
+#pragma unroll
+                            for (int u = 2; u < 32; u += 2) mx[c] = fmaxf(fmaxf(mx[c], x[c * 32 + u]), x[c * 32 + u + 1]);
+                        }
+                        const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * a.scale_log2;
                         // The base moves only when the maximum is more than kSlack above it; weights
                         // stay at most 2^kSlack, and sums and outputs share the base.
-                        if (__any_sync(0xffffffffu, mx > m + kSlack)) {
-                            const float mn = fmaxf(m, mx);
+                        if (__any_sync(0xffffffffu, top > m + kSlack)) {
+                            const float mn = fmaxf(m, top);
                             const float alpha = mn == -INFINITY ? 1.f : ex2(m - mn);
                             m = mn;
                             l *= alpha;
                             if (j > 0) {   // S of this tile is complete, so the MMAs into O before it are
 #pragma unroll
-                                for (int c = 0; c < 4; ++c) {
-                                    uint32_t x[32];
-                                    tc_ld32(o_col + c * 32, x);
+                                for (int c = 0; c < 8; ++c) {
+                                    uint32_t y[16];
+                                    tc_ld16(o_col + c * 16, y);
                                     tc_wait_ld();
 #pragma unroll
-                                    for (int u = 0; u < 32; ++u) x[u] = __float_as_uint(__uint_as_float(x[u]) * alpha);
-                                    tc_st32(o_col + c * 32, x);
+                                    for (int u = 0; u < 16; ++u) y[u] = __float_as_uint(__uint_as_float(y[u]) * alpha);
+                                    tc_st16(o_col + c * 16, y);
                                 }
                             }
                         }
                         const float base = m == -INFINITY ? 0.f : m;
-                        // Pass 2: weights, their sum, and P in bf16 over the columns already read.
+                        // Weights and their sum, two at a time, and P in bf16 over S (read already).
+                        const uint64_t scale2 = pack2(a.scale_log2, a.scale_log2), base2 = pack2(-base, -base);
+                        uint64_t sum[2] = {0ull, 0ull};
 #pragma unroll
                         for (int c = 0; c < 4; ++c) {
-                            uint32_t x[32], p[16];
-                            tc_ld32(s_col + c * 32, x);
-                            tc_wait_ld();
-                            if (FP8) {
+                            uint32_t p[16];
 #pragma unroll
-                                for (int u = 0; u < 8; ++u) {
-                                    const float4 k4 = ks[c * 8 + u];
-                                    x[4 * u] = __float_as_uint(__uint_as_float(x[4 * u]) * k4.x);
-                                    x[4 * u + 1] = __float_as_uint(__uint_as_float(x[4 * u + 1]) * k4.y);
-                                    x[4 * u + 2] = __float_as_uint(__uint_as_float(x[4 * u + 2]) * k4.z);
-                                    x[4 * u + 3] = __float_as_uint(__uint_as_float(x[4 * u + 3]) * k4.w);
+                            for (int u = 0; u < 16; ++u) {
+                                float e0, e1;
+                                unpack2(fma2(pack2(x[c * 32 + 2 * u], x[c * 32 + 2 * u + 1]), scale2, base2), e0, e1);
+                                e0 = ex2(e0);
+                                e1 = ex2(e1);
+                                sum[u & 1] = add2(sum[u & 1], pack2(e0, e1));
+                                if (FP8) {
+                                    const float2 v2 = vs[c * 16 + u];
+                                    e0 *= v2.x;
+                                    e1 *= v2.y;
                                 }
+                                p[u] = pack_bf16x2(e0, e1);
                             }
-                            float e[32];
-#pragma unroll
-                            for (int u = 0; u < 32; ++u) e[u] = ex2(fmaf(__uint_as_float(x[u]), a.scale_log2, -base));
-                            if (!plain) {
-                                const uint32_t bits = mask_of(c);
-#pragma unroll
-                                for (int u = 0; u < 32; ++u) e[u] = (bits >> u) & 1u ? e[u] : 0.f;
-                            }
-                            float s0 = 0.f, s1 = 0.f;
-#pragma unroll
-                            for (int u = 0; u < 32; u += 2) {
-                                s0 += e[u];
-                                s1 += e[u + 1];
-                            }
-                            l += s0 + s1;
-                            if (FP8) {
-#pragma unroll
-                                for (int u = 0; u < 8; ++u) {
-                                    const float4 v4 = vs[c * 8 + u];
-                                    e[4 * u] *= v4.x;
-                                    e[4 * u + 1] *= v4.y;
-                                    e[4 * u + 2] *= v4.z;
-                                    e[4 * u + 3] *= v4.w;
-                                }
-                            }
-#pragma unroll
-                            for (int u = 0; u < 16; ++u) p[u] = pack_bf16x2(e[2 * u], e[2 * u + 1]);
                             tc_st16(s_col + c * 16, p);
+                        }
+                        {
+                            float s0, s1;
+                            unpack2(add2(sum[0], sum[1]), s0, s1);
+                            l += s0 + s1;
                         }
                         tc_wait_st();
                     }
@@ -854,6 +944,7 @@ __global__ void __launch_bounds__(Cfg<FP8>::kThreads, 1)
         softmax_end:;
         } else if (FP8 && warp >= 12) {
             // ---------------- e4m3 codes -> bf16 tiles in the MMAs' layout
+            reg_dec<C::kOtherRegs>();
             Walk walk(a, ct, count);
             Seg s;
             const int tid = threadIdx.x - 384;
@@ -863,9 +954,8 @@ __global__ void __launch_bounds__(Cfg<FP8>::kThreads, 1)
                 const int n = s.t1 - s.t0;
                 const int qlo = s.en.pos0, qhi = last_pos(s.en);
                 for (int i = 0; i < 2 * n; ++i) {
-                    // The loads' order: K0 K1 V0 K2 V1 .. V(n-1).
-                    const bool is_k = i == 0 || (i != 2 * n - 1 && (i & 1));
-                    const int t = is_k ? (i + 1) / 2 : (i == 2 * n - 1 ? n - 1 : i / 2 - 1);
+                    const bool is_k = load_is_k(i, n);
+                    const int t = load_tile(i, n);
                     const int slot = (tile + t) % kInfoSlots;
                     const int cs = ld % kCodeDepth, st = ld % C::kStages;
                     SVQ_WAIT(ct->code_full[cs], (ld / kCodeDepth) & 1, widen_end);
@@ -873,30 +963,65 @@ __global__ void __launch_bounds__(Cfg<FP8>::kThreads, 1)
                     const unsigned char* src = codes + cs * (kTileTok * kHeadDim);
                     unsigned char* dst = ring + st * kStageBytes;
                     const int i0 = (s.t0 + t) * kTilePages;
+                    // Page k of the tile: thread -> row tid / 8, 16 codes at chunk tid % 8.
+                    const int r = tid >> 3, c = tid & 7;
+                    // Tokens no row sees may hold anything: they become zeros, scales too.  Bit k:
+                    // this thread's token of page k is seen; `clean`: every token of the tile is.
+                    const int base0 = logical_page(s.en, i0) * kPage, base7 = logical_page(s.en, i0 + 7) * kPage;
                     const int fault = ct->fault[slot];
+                    const bool clean = !fault && i0 + kTilePages <= s.en.npages && base7 - base0 == 7 * kPage &&
+                                       base7 + 15 <= qhi && (base0 > qlo - a.window || base7 + 15 < a.sink);
+                    uint32_t on = 0xffu;
+                    if (!clean) {
+                        on = 0u;
 #pragma unroll
-                    for (int k = 0; k < 8; ++k) {
-                        // Pass k is page k of the tile: thread -> row tid / 8, 16 codes at chunk tid % 8.
-                        const int r = tid >> 3, c = tid & 7;
-                        const int pi = i0 + k;
-                        uint32_t seen = 0;
-                        if (pi < s.en.npages && !((fault >> k) & 1))
-                            seen = union_mask(logical_page(s.en, pi) * kPage, qlo, qhi, a.window, a.sink);
-                        const bool on = (seen >> r) & 1u;
-                        uint4 v = *reinterpret_cast<const uint4*>(src + k * (kPage * kHeadDim) + r * kHeadDim + c * 16);
-                        if (!on) v = make_uint4(0u, 0u, 0u, 0u);   // tokens no row sees may hold anything
-                        uint4 lo, hi;
-                        widen4(v.x, lo.x, lo.y);
-                        widen4(v.y, lo.z, lo.w);
-                        widen4(v.z, hi.x, hi.y);
-                        widen4(v.w, hi.z, hi.w);
-                        unsigned char* o = dst + k * kPageBytes + (r >> 3) * 2048 + (c >> 2) * 1024 + (r & 7) * 128;
-                        *reinterpret_cast<uint4*>(o + ((((2 * c) & 7) ^ (r & 7)) << 4)) = lo;
-                        *reinterpret_cast<uint4*>(o + ((((2 * c + 1) & 7) ^ (r & 7)) << 4)) = hi;
-                        if (is_k && c == 0 && !on) {
-                            scales[slot * 2 * kTileTok + k * kPage + r] = 0.f;
-                            scales[slot * 2 * kTileTok + kTileTok + k * kPage + r] = 0.f;
+                        for (int k = 0; k < 8; ++k)
+                            if (i0 + k < s.en.npages && !((fault >> k) & 1))
+                                on |= ((union_mask(logical_page(s.en, i0 + k) * kPage, qlo, qhi, a.window, a.sink) >> r) & 1u) << k;
+                    }
+                    unsigned char* const o = dst + (r >> 3) * 2048 + (c >> 2) * 1024 + (r & 7) * 128;
+                    const int at0 = ((2 * c) & 7 ^ (r & 7)) << 4, at1 = ((2 * c + 1) & 7 ^ (r & 7)) << 4;
+#pragma unroll
+                    for (int k0 = 0; k0 < 8; k0 += 4) {
+                        uint4 v[4];
+                        uint32_t nan = 0;
+#pragma unroll
+                        for (int u = 0; u < 4; ++u) {
+                            v[u] = *reinterpret_cast<const uint4*>(src + (k0 + u) * (kPage * kHeadDim) + r * kHeadDim + c * 16);
+                            if (!((on >> (k0 + u)) & 1u)) v[u] = make_uint4(0u, 0u, 0u, 0u);
                         }
+#pragma unroll
+                        for (int u = 0; u < 4; ++u) nan |= has_nan(v[u].x) | has_nan(v[u].y) | has_nan(v[u].z) | has_nan(v[u].w);
+                        uint4 lo[4], hi[4];
+#pragma unroll
+                        for (int u = 0; u < 4; ++u) {
+                            widen4(v[u].x, lo[u].x, lo[u].y);
+                            widen4(v[u].y, lo[u].z, lo[u].w);
+                            widen4(v[u].z, hi[u].x, hi[u].y);
+                            widen4(v[u].w, hi[u].z, hi[u].w);
+                        }
+                        if (nan) {
+#pragma unroll
+                            for (int u = 0; u < 4; ++u) {
+                                keep_nan(v[u].x, lo[u].x, lo[u].y);
+                                keep_nan(v[u].y, lo[u].z, lo[u].w);
+                                keep_nan(v[u].z, hi[u].x, hi[u].y);
+                                keep_nan(v[u].w, hi[u].z, hi[u].w);
+                            }
+                        }
+#pragma unroll
+                        for (int u = 0; u < 4; ++u) {
+                            *reinterpret_cast<uint4*>(o + (k0 + u) * kPageBytes + at0) = lo[u];
+                            *reinterpret_cast<uint4*>(o + (k0 + u) * kPageBytes + at1) = hi[u];
+                        }
+                    }
+                    if (is_k && c == 0 && on != 0xffu) {
+#pragma unroll
+                        for (int k = 0; k < 8; ++k)
+                            if (!((on >> k) & 1u)) {
+                                scales[slot * 2 * kTileTok + k * kPage + r] = 0.f;
+                                scales[slot * 2 * kTileTok + kTileTok + k * kPage + r] = 0.f;
+                            }
                     }
                     fence_proxy_async_smem();
                     __syncwarp();
