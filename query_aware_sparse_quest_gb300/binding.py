@@ -313,7 +313,7 @@ def sv_sparse_decode_ex(cache: Cache, q: torch.Tensor, page_table: torch.Tensor,
 
 
 def _shape(t: torch.Tensor, shape, name: str) -> None:
-    if tuple(t.shape) != tuple(shape):
+    if t.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
 
 
@@ -322,12 +322,21 @@ def _channels(d: int) -> None:
         raise ValueError(f"q must have 128 channels, got {d}")
 
 
-def _here(*tensors: Optional[torch.Tensor]) -> None:
-    """The kernels run on the current device: every tensor has to be there."""
-    dev = torch.cuda.current_device()
-    for t in tensors:
-        if t is not None and t.is_cuda and t.device.index != dev:
-            raise ValueError(f"tensors on cuda:{t.device.index} while cuda:{dev} is current")
+def _at(t: Optional[torch.Tensor], dtype: Optional[torch.dtype], name: str, dev: int):
+    """_p for the current device `dev`, where the kernels run, in few calls: decode calls are made every few
+    microseconds, and their host time counts as much as their kernels'."""
+    if t is None:
+        return None
+    if t.get_device() == dev and (dtype is None or t.dtype is dtype) and t.is_contiguous():
+        return t.data_ptr()
+    p = _p(t, dtype, name)
+    if t.get_device() != dev:
+        raise ValueError(f"{name} is on cuda:{t.get_device()} while cuda:{dev} is current")
+    return p
+
+
+def _on(stream, dev: int):
+    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else _stream(stream)
 
 
 def sv_window_attention_workspace_size(batch: int, num_q_heads: int, num_kv_heads: int, total_q: int) -> int:
@@ -343,17 +352,17 @@ def sv_window_attention(cache: Cache, q: torch.Tensor, page_table: torch.Tensor,
     B, max_pages = page_table.shape
     _channels(D)
     _shape(seq_lens, (B,), "seq_lens")
-    _shape(out, q.shape, "out")
+    _shape(out, (T, Hq, D), "out")
     _shape(lse, (T, Hq), "lse")
     if q_start is not None:
         _shape(q_start, (B + 1,), "q_start")
-    _here(cache.k_pool, q, page_table, seq_lens, q_start, out, lse, workspace)
-    scale = float(D) ** -0.5 if softmax_scale is None else float(softmax_scale)
+    dev = torch.cuda.current_device()
+    _at(cache.k_pool, None, "the cache", dev)
     _check("sv_window_attention", _load().sv_window_attention(
-        cache.ref(), _p(q, _BF16, "q"), Hq, _p(q_start, _I32, "q_start"), T, _p(page_table, _I32, "page_table"),
-        _p(seq_lens, _I32, "seq_lens"), B, max_pages, int(window), int(sink_tokens), scale, _p(out, _BF16, "out"),
-        _p(lse, _F32, "lse"), _p(workspace, None, "workspace"), workspace.numel() * workspace.element_size(),
-        _stream(stream)))
+        cache.ref(), _at(q, _BF16, "q", dev), Hq, _at(q_start, _I32, "q_start", dev), T,
+        _at(page_table, _I32, "page_table", dev), _at(seq_lens, _I32, "seq_lens", dev), B, max_pages, window, sink_tokens,
+        D ** -0.5 if softmax_scale is None else softmax_scale, _at(out, _BF16, "out", dev), _at(lse, _F32, "lse", dev),
+        _at(workspace, None, "workspace", dev), workspace.nbytes, _on(stream, dev)))
 
 
 def sv_prefix_decode_workspace_size(batch: int, num_q_heads: int, num_kv_heads: int, num_groups: int) -> int:
@@ -365,20 +374,21 @@ def sv_prefix_decode(cache: Cache, q: torch.Tensor, page_table: torch.Tensor, se
                      workspace: torch.Tensor, softmax_scale: Optional[float] = None, stream=None) -> None:
     """Dense decode with the first shared_pages[g] pages of requests group_start[g] .. read once a group."""
     B, Hq, D = q.shape
-    groups = int(shared_pages.numel())
+    groups, max_pages = shared_pages.numel(), page_table.shape[-1]
     _channels(D)
-    _shape(page_table, (B, page_table.shape[-1]), "page_table")
+    _shape(page_table, (B, max_pages), "page_table")
     _shape(seq_lens, (B,), "seq_lens")
     _shape(group_start, (groups + 1,), "group_start")
-    _shape(out, q.shape, "out")
+    _shape(out, (B, Hq, D), "out")
     _shape(lse, (B, Hq), "lse")
-    _here(cache.k_pool, q, page_table, seq_lens, group_start, shared_pages, out, lse, workspace)
-    scale = float(D) ** -0.5 if softmax_scale is None else float(softmax_scale)
+    dev = torch.cuda.current_device()
+    _at(cache.k_pool, None, "the cache", dev)
     _check("sv_prefix_decode", _load().sv_prefix_decode(
-        cache.ref(), _p(q, _BF16, "q"), Hq, _p(page_table, _I32, "page_table"), _p(seq_lens, _I32, "seq_lens"), B,
-        int(page_table.shape[1]), _p(group_start, _I32, "group_start"), _p(shared_pages, _I32, "shared_pages"), groups,
-        scale, _p(out, _BF16, "out"), _p(lse, _F32, "lse"), _p(workspace, None, "workspace"),
-        workspace.numel() * workspace.element_size(), _stream(stream)))
+        cache.ref(), _at(q, _BF16, "q", dev), Hq, _at(page_table, _I32, "page_table", dev),
+        _at(seq_lens, _I32, "seq_lens", dev), B, max_pages, _at(group_start, _I32, "group_start", dev),
+        _at(shared_pages, _I32, "shared_pages", dev), groups, D ** -0.5 if softmax_scale is None else softmax_scale,
+        _at(out, _BF16, "out", dev), _at(lse, _F32, "lse", dev), _at(workspace, None, "workspace", dev),
+        workspace.nbytes, _on(stream, dev)))
 
 
 class CacheList:
@@ -401,14 +411,15 @@ def _cache_list(caches) -> CacheList:
     return CacheList([caches] if isinstance(caches, Cache) else caches)
 
 
-def _rows(page_table: torch.Tensor, seq_lens: torch.Tensor, ref_counts: torch.Tensor, pool: Optional[int] = None):
+def _rows(page_table: torch.Tensor, seq_lens: torch.Tensor, ref_counts: torch.Tensor, dev: int,
+          pool: Optional[int] = None):
     """The leading arguments of the sv_pages_* calls that go by rows."""
     rows, max_pages = page_table.shape
     _shape(seq_lens, (rows,), "seq_lens")
     if pool is not None:
         _shape(ref_counts, (pool,), "ref_counts")
-    return (_p(page_table, _I32, "page_table"), _p(seq_lens, _I32, "seq_lens"), rows, max_pages,
-            _p(ref_counts, _I32, "ref_counts"))
+    return (_at(page_table, _I32, "page_table", dev), _at(seq_lens, _I32, "seq_lens", dev), rows, max_pages,
+            _at(ref_counts, _I32, "ref_counts", dev))
 
 
 def sv_pages_workspace_size(num_phys_pages: int, num_rows: int, n: int) -> int:
@@ -419,31 +430,34 @@ def sv_pages_copy(caches, src: torch.Tensor, dst: torch.Tensor, stream=None) -> 
     """Copies page src[i] to page dst[i] in every cache (a Cache, several, or a CacheList)."""
     cl = _cache_list(caches)
     _shape(dst, src.shape, "dst")
-    _here(cl.caches[0].k_pool, src, dst)
-    _check("sv_pages_copy", _load().sv_pages_copy(cl.c, len(cl.c), _p(src, _I32, "src"), _p(dst, _I32, "dst"),
-                                                  src.numel(), _stream(stream)))
+    dev = torch.cuda.current_device()
+    _at(cl.caches[0].k_pool, None, "the cache", dev)
+    _check("sv_pages_copy", _load().sv_pages_copy(cl.c, len(cl.c), _at(src, _I32, "src", dev), _at(dst, _I32, "dst", dev),
+                                                  src.numel(), _on(stream, dev)))
 
 
 def sv_pages_fork(caches, page_table: torch.Tensor, seq_lens: torch.Tensor, ref_counts: torch.Tensor,
                   parents: torch.Tensor, children: torch.Tensor, workspace: torch.Tensor, stream=None) -> None:
+    """Row children[i] becomes a fork of row parents[i]."""
     cl = _cache_list(caches)
     _shape(children, parents.shape, "children")
-    _here(cl.caches[0].k_pool, page_table, seq_lens, ref_counts, parents, children, workspace)
+    dev = torch.cuda.current_device()
+    _at(cl.caches[0].k_pool, None, "the cache", dev)
     _check("sv_pages_fork", _load().sv_pages_fork(
-        cl.c, len(cl.c), *_rows(page_table, seq_lens, ref_counts, cl.num_phys_pages), _p(parents, _I32, "parents"),
-        _p(children, _I32, "children"), parents.numel(), _p(workspace, None, "workspace"),
-        workspace.numel() * workspace.element_size(), _stream(stream)))
+        cl.c, len(cl.c), *_rows(page_table, seq_lens, ref_counts, dev, cl.num_phys_pages),
+        _at(parents, _I32, "parents", dev), _at(children, _I32, "children", dev), parents.numel(),
+        _at(workspace, None, "workspace", dev), workspace.nbytes, _on(stream, dev)))
 
 
 def sv_pages_reserve(page_table: torch.Tensor, seq_lens: torch.Tensor, ref_counts: torch.Tensor, rows: torch.Tensor,
                      add_tokens: torch.Tensor, slot_mapping: torch.Tensor, workspace: torch.Tensor, stream=None) -> None:
     """Room for add_tokens[i] more tokens in row rows[i]; their slots go to slot_mapping."""
     _shape(add_tokens, rows.shape, "add_tokens")
-    _here(page_table, seq_lens, ref_counts, rows, add_tokens, slot_mapping, workspace)
+    dev = torch.cuda.current_device()
     _check("sv_pages_reserve", _load().sv_pages_reserve(
-        *_rows(page_table, seq_lens, ref_counts), ref_counts.numel(), _p(rows, _I32, "rows"),
-        _p(add_tokens, _I32, "add_tokens"), rows.numel(), _p(slot_mapping, _I32, "slot_mapping"), slot_mapping.numel(),
-        _p(workspace, None, "workspace"), workspace.numel() * workspace.element_size(), _stream(stream)))
+        *_rows(page_table, seq_lens, ref_counts, dev), ref_counts.numel(), _at(rows, _I32, "rows", dev),
+        _at(add_tokens, _I32, "add_tokens", dev), rows.numel(), _at(slot_mapping, _I32, "slot_mapping", dev),
+        slot_mapping.numel(), _at(workspace, None, "workspace", dev), workspace.nbytes, _on(stream, dev)))
 
 
 def sv_pages_free(page_table: torch.Tensor, seq_lens: torch.Tensor, ref_counts: torch.Tensor, rows: torch.Tensor,
@@ -453,10 +467,10 @@ def sv_pages_free(page_table: torch.Tensor, seq_lens: torch.Tensor, ref_counts: 
     for t, name in ((first_page, "first_page"), (end_page, "end_page")):
         if t is not None:
             _shape(t, rows.shape, name)
-    _here(page_table, seq_lens, ref_counts, rows, first_page, end_page)
+    dev = torch.cuda.current_device()
     _check("sv_pages_free", _load().sv_pages_free(
-        *_rows(page_table, seq_lens, ref_counts), ref_counts.numel(), _p(rows, _I32, "rows"),
-        _p(first_page, _I32, "first_page"), _p(end_page, _I32, "end_page"), rows.numel(), _stream(stream)))
+        *_rows(page_table, seq_lens, ref_counts, dev), ref_counts.numel(), _at(rows, _I32, "rows", dev),
+        _at(first_page, _I32, "first_page", dev), _at(end_page, _I32, "end_page", dev), rows.numel(), _on(stream, dev)))
 
 
 def sv_pages_compact(caches, page_table: torch.Tensor, seq_lens: torch.Tensor, ref_counts: torch.Tensor,
@@ -467,12 +481,12 @@ def sv_pages_compact(caches, page_table: torch.Tensor, seq_lens: torch.Tensor, r
     _shape(page_table_out, page_table.shape, "page_table_out")
     _shape(ref_counts_out, ref_counts.shape, "ref_counts_out")
     _shape(num_live, (1,), "num_live")
-    _here(cl.caches[0].k_pool, page_table, seq_lens, ref_counts, page_table_out, ref_counts_out, num_live, workspace)
+    dev = torch.cuda.current_device()
+    _at(cl.caches[0].k_pool, None, "the cache", dev)
     _check("sv_pages_compact", _load().sv_pages_compact(
-        cl.c, len(cl.c), *_rows(page_table, seq_lens, ref_counts, cl.num_phys_pages),
-        _p(page_table_out, _I32, "page_table_out"), _p(ref_counts_out, _I32, "ref_counts_out"),
-        _p(num_live, _I32, "num_live"), _p(workspace, None, "workspace"),
-        workspace.numel() * workspace.element_size(), _stream(stream)))
+        cl.c, len(cl.c), *_rows(page_table, seq_lens, ref_counts, dev, cl.num_phys_pages),
+        _at(page_table_out, _I32, "page_table_out", dev), _at(ref_counts_out, _I32, "ref_counts_out", dev),
+        _at(num_live, _I32, "num_live", dev), _at(workspace, None, "workspace", dev), workspace.nbytes, _on(stream, dev)))
 
 
 def sv_get_device_error(reset: bool = True) -> int:

@@ -758,36 +758,35 @@ __global__ void __launch_bounds__(Cfg<FP8>::kThreads, 1)
                         };
                         const float4* ks = reinterpret_cast<const float4*>(scales + slot * 2 * kTileTok);
                         const float2* vs = reinterpret_cast<const float2*>(ks + kTileTok / 4);
-                        // The row's 128 logits stay in registers from here to P.
-                        float x[128];
+                        // Pass 1: the tile's maximum.  Both passes are rolled loops over 32 columns
+                        // that read S from TMEM: straight code over 128 columns ran at the
+                        // rate its instructions were fetched.
+                        float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll 1
+                        for (int c = 0; c < 4; ++c) {
+                            float x[32];
+                            tc_ld32(s_col + c * 32, reinterpret_cast<uint32_t(&)[32]>(x));
+                            tc_wait_ld();
+                            if (FP8) {
 #pragma unroll
-                        for (int c = 0; c < 4; ++c) tc_ld32(s_col + c * 32, reinterpret_cast<uint32_t(&)[32]>(x[c * 32]));
-                        tc_wait_ld();
-                        if (FP8) {
-#pragma unroll
-                            for (int u = 0; u < 32; ++u) {
-                                const float4 k4 = ks[u];
-                                x[4 * u] *= k4.x;
-                                x[4 * u + 1] *= k4.y;
-                                x[4 * u + 2] *= k4.z;
-                                x[4 * u + 3] *= k4.w;
+                                for (int u = 0; u < 8; ++u) {
+                                    const float4 k4 = ks[c * 8 + u];
+                                    x[4 * u] *= k4.x;
+                                    x[4 * u + 1] *= k4.y;
+                                    x[4 * u + 2] *= k4.z;
+                                    x[4 * u + 3] *= k4.w;
+                                }
                             }
-                        }
-                        if (!plain) {
-#pragma unroll
-                            for (int c = 0; c < 4; ++c) {
+                            if (!plain) {
                                 const uint32_t bits = mask_of(c);
 #pragma unroll
                                 for (int u = 0; u < 32; ++u)
-                                    if (!((bits >> u) & 1u)) x[c * 32 + u] = -INFINITY;
+                                    if (!((bits >> u) & 1u)) x[u] = -INFINITY;
                             }
-                        }
-                        float mx[4];
 #pragma unroll
-                        for (int c = 0; c < 4; ++c) {
-                            mx[c] = fmaxf(x[c * 32], x[c * 32 + 1]);
+                            for (int u = 0; u < 32; u += 8)
 #pragma unroll
-                            for (int u = 2; u < 32; u += 2) mx[c] = fmaxf(fmaxf(mx[c], x[c * 32 + u]), x[c * 32 + u + 1]);
+                                for (int k = 0; k < 4; ++k) mx[k] = fmaxf(fmaxf(mx[k], x[u + 2 * k]), x[u + 2 * k + 1]);
                         }
                         const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * a.scale_log2;
                         // The base moves only when the maximum is more than kSlack above it; weights
@@ -798,7 +797,7 @@ __global__ void __launch_bounds__(Cfg<FP8>::kThreads, 1)
                             m = mn;
                             l *= alpha;
                             if (j > 0) {   // S of this tile is complete, so the MMAs into O before it are
-#pragma unroll
+#pragma unroll 1
                                 for (int c = 0; c < 8; ++c) {
                                     uint32_t y[16];
                                     tc_ld16(o_col + c * 16, y);
@@ -813,13 +812,32 @@ __global__ void __launch_bounds__(Cfg<FP8>::kThreads, 1)
                         // Weights and their sum, two at a time, and P in bf16 over S (read already).
                         const uint64_t scale2 = pack2(a.scale_log2, a.scale_log2), base2 = pack2(-base, -base);
                         uint64_t sum[2] = {0ull, 0ull};
-#pragma unroll
+#pragma unroll 1
                         for (int c = 0; c < 4; ++c) {
+                            float x[32];
                             uint32_t p[16];
+                            tc_ld32(s_col + c * 32, reinterpret_cast<uint32_t(&)[32]>(x));
+                            tc_wait_ld();
+                            if (FP8) {
+#pragma unroll
+                                for (int u = 0; u < 8; ++u) {
+                                    const float4 k4 = ks[c * 8 + u];
+                                    x[4 * u] *= k4.x;
+                                    x[4 * u + 1] *= k4.y;
+                                    x[4 * u + 2] *= k4.z;
+                                    x[4 * u + 3] *= k4.w;
+                                }
+                            }
+                            if (!plain) {
+                                const uint32_t bits = mask_of(c);
+#pragma unroll
+                                for (int u = 0; u < 32; ++u)
+                                    if (!((bits >> u) & 1u)) x[u] = -INFINITY;
+                            }
 #pragma unroll
                             for (int u = 0; u < 16; ++u) {
                                 float e0, e1;
-                                unpack2(fma2(pack2(x[c * 32 + 2 * u], x[c * 32 + 2 * u + 1]), scale2, base2), e0, e1);
+                                unpack2(fma2(pack2(x[2 * u], x[2 * u + 1]), scale2, base2), e0, e1);
                                 e0 = ex2(e0);
                                 e1 = ex2(e1);
                                 sum[u & 1] = add2(sum[u & 1], pack2(e0, e1));
@@ -981,20 +999,18 @@ __global__ void __launch_bounds__(Cfg<FP8>::kThreads, 1)
                     }
                     unsigned char* const o = dst + (r >> 3) * 2048 + (c >> 2) * 1024 + (r & 7) * 128;
                     const int at0 = ((2 * c) & 7 ^ (r & 7)) << 4, at1 = ((2 * c + 1) & 7 ^ (r & 7)) << 4;
-#pragma unroll
-                    for (int k0 = 0; k0 < 8; k0 += 4) {
-                        uint4 v[4];
+#pragma unroll 1
+                    for (int k0 = 0; k0 < 8; k0 += 2) {
+                        uint4 v[2], lo[2], hi[2];
                         uint32_t nan = 0;
 #pragma unroll
-                        for (int u = 0; u < 4; ++u) {
+                        for (int u = 0; u < 2; ++u) {
                             v[u] = *reinterpret_cast<const uint4*>(src + (k0 + u) * (kPage * kHeadDim) + r * kHeadDim + c * 16);
                             if (!((on >> (k0 + u)) & 1u)) v[u] = make_uint4(0u, 0u, 0u, 0u);
                         }
 #pragma unroll
-                        for (int u = 0; u < 4; ++u) nan |= has_nan(v[u].x) | has_nan(v[u].y) | has_nan(v[u].z) | has_nan(v[u].w);
-                        uint4 lo[4], hi[4];
-#pragma unroll
-                        for (int u = 0; u < 4; ++u) {
+                        for (int u = 0; u < 2; ++u) {
+                            nan |= has_nan(v[u].x) | has_nan(v[u].y) | has_nan(v[u].z) | has_nan(v[u].w);
                             widen4(v[u].x, lo[u].x, lo[u].y);
                             widen4(v[u].y, lo[u].z, lo[u].w);
                             widen4(v[u].z, hi[u].x, hi[u].y);
@@ -1002,7 +1018,7 @@ __global__ void __launch_bounds__(Cfg<FP8>::kThreads, 1)
                         }
                         if (nan) {
 #pragma unroll
-                            for (int u = 0; u < 4; ++u) {
+                            for (int u = 0; u < 2; ++u) {
                                 keep_nan(v[u].x, lo[u].x, lo[u].y);
                                 keep_nan(v[u].y, lo[u].z, lo[u].w);
                                 keep_nan(v[u].z, hi[u].x, hi[u].y);
@@ -1010,7 +1026,7 @@ __global__ void __launch_bounds__(Cfg<FP8>::kThreads, 1)
                             }
                         }
 #pragma unroll
-                        for (int u = 0; u < 4; ++u) {
+                        for (int u = 0; u < 2; ++u) {
                             *reinterpret_cast<uint4*>(o + (k0 + u) * kPageBytes + at0) = lo[u];
                             *reinterpret_cast<uint4*>(o + (k0 + u) * kPageBytes + at1) = hi[u];
                         }
