@@ -26,6 +26,7 @@ int decode_max_splits(int pages);
 size_t decode_workspace_bytes(int batch, int num_q_heads, int splits);
 int read_error_decode_fp8(uint32_t* flags, int reset);
 int read_error_attend(uint32_t* flags, int reset);
+int read_error_window_decode(uint32_t* flags, int reset);
 int read_error_pages(uint32_t* flags, int reset);
 size_t pages_workspace_bytes(int64_t num_pages, int num_rows, int n);
 int launch_pages_copy(const sv_cache* caches, int num_caches, const int32_t* src, const int32_t* dst, int n,
@@ -543,6 +544,7 @@ int sv_get_device_error(uint32_t* flags, int reset) {
     if ((st = read_error_select(flags, reset))) return st;
     if ((st = read_error_decode_fp8(flags, reset))) return st;
     if ((st = read_error_attend(flags, reset))) return st;
+    if ((st = read_error_window_decode(flags, reset))) return st;
     if ((st = read_error_pages(flags, reset))) return st;
     return read_error_decode(flags, reset);
 }

@@ -1,6 +1,6 @@
-// Attention of query rows over ranges of cached pages on the tcgen05 tensor
-// cores: sliding-window attention with sinks (chunks and single tokens) and
-// decode of requests that share a prefix.
+// Attention of many query rows over ranges of cached pages on the tcgen05
+// tensor cores: chunks of query tokens with a sliding window and sinks, and the
+// shared prefix of a decode batch.
 //
 // Mathematics.  A row tile is up to 256 (query token, query head) pairs that
 // read the same pages of one kv head; 128 of them are one MMA's M side, so the
@@ -32,16 +32,22 @@
 // two 128-row halves of a tile of more than 128 rows, each over every key
 // tile; or, for up to 128 rows, the even and the odd key tiles of the same
 // rows, joined at the end.
-#include <cuda.h>
-#include <cudaTypedefs.h>
-
 #include <climits>
 
-#include "svq_common.cuh"
+#include "svq_paged.cuh"
 
 namespace svq {
 
 SVQ_DEFINE_ERROR_WORD(read_error_attend)
+
+int window_decode_splits(bool fp8, int batch, int num_kv_heads, int64_t pages, int sm_count);
+int64_t window_decode_rows(int batch, int num_q_heads, int num_kv_heads);
+int launch_window_decode(const sv_cache* c, const void* q, int num_q_heads, const int32_t* page_table,
+                         const int32_t* seq_lens, int batch, int max_pages, int window, int sink,
+                         const int32_t* first_page, float softmax_scale, int splits, float* o_part, float2* ml_part,
+                         cudaStream_t stream);
+int launch_join_splits(const float* o_part, const float2* ml_part, int splits, int64_t rows, void* out, float* lse,
+                       cudaStream_t stream);
 
 namespace {
 
@@ -65,10 +71,9 @@ struct __align__(16) Entry {
     int sink_pages;
     int w0;
     int npages;       // pages in the list
-    int kind;         // kDirect, kPrefix or kSuffix
+    int unused;
 };
 constexpr int kAllVisible = 1 << 30;
-constexpr int kDirect = 0, kPrefix = 1, kSuffix = 2;
 
 __device__ __forceinline__ int tiles_of(int npages) { return (npages + kTilePages - 1) / kTilePages; }
 
@@ -76,8 +81,9 @@ struct Plan {
     Entry* entries;
     int64_t* cum;      // [E + 1] tiles per kv head before each entry
     int* num_entries;
-    int* req_entry;    // kPrefix mode: entry that holds each request's prefix rows, -1: none
-    int* req_offset;   // ragged chunks: first entry of each request
+    int* req_offset;   // first entry of each request (chunks) or group (prefixes)
+    int* req_entry;    // prefixes: entry that holds each request's rows, -1: none, -2: the request is not touched
+    int* first_page;   // prefixes: each request's first page behind the prefix, -1: none is read
 };
 
 struct AttendArgs {
@@ -99,8 +105,11 @@ struct AttendArgs {
     float* cut_o;      // [2 CTAs][slot_rows][128] partials of items that are cut
     float2* cut_ml;    // [2 CTAs][slot_rows] (base in log2 units, sum)
     int slot_rows;
-    float* whole_o[2];    // prefix / suffix parts of whole items, [B Hq][128]
-    float2* whole_ml[2];
+    float* whole_o;    // prefixes: the parts of whole items, [B Hq][128]; else null
+    float2* whole_ml;
+    float* split_o;    // prefixes: the parts behind the prefix, [B Hq][splits][128]
+    float2* split_ml;
+    int splits;
 };
 
 // The run of tiles of CTA c: total / ctas each, the first total % ctas one more.
@@ -242,12 +251,6 @@ template <int N>
 __device__ __forceinline__ void reg_dec() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
 template <int N>
 __device__ __forceinline__ void reg_inc() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
-__device__ __forceinline__ float ex2(float x) {
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
-
 // ---------------------------------------------------------------- shared memory
 template <bool FP8>
 struct Cfg {
@@ -324,18 +327,6 @@ struct Walk {
 
 __device__ __forceinline__ int logical_page(const Entry& en, int i) {
     return i < en.sink_pages ? i : en.w0 + i - en.sink_pages;
-}
-// Bit t: some row of the entry (positions qlo .. qhi) sees token t of the page.
-__device__ __forceinline__ uint32_t union_mask(int base, int qlo, int qhi, int window, int sink) {
-    const int hi = min(16, qhi - base + 1);
-    if (hi <= 0) return 0u;
-    const int lo = max(0, min(16, max(0, qlo - window + 1) - base));
-    const int sk = max(0, min(16, sink - base));
-    return ((1u << hi) - 1u) & (~((1u << lo) - 1u) | ((1u << sk) - 1u));
-}
-// Bit t: the row at position qpos does.
-__device__ __forceinline__ uint32_t page_mask(int base, int qpos, int window, int sink) {
-    return union_mask(base, qpos, qpos, window, sink);
 }
 __device__ __forceinline__ int last_pos(const Entry& en) {
     return en.pos0 == kAllVisible ? kAllVisible : en.pos0 + en.ntok - 1;
@@ -874,9 +865,9 @@ __global__ void __launch_bounds__(Cfg<FP8>::kThreads, 1)
                     const int64_t at = static_cast<int64_t>(blockIdx.x * 2 + (first_seg ? 0 : 1)) * a.slot_rows + r;
                     po = a.cut_o + at * kHeadDim;
                     pml = a.cut_ml + at;
-                } else if (s.en.kind != kDirect) {
-                    po = a.whole_o[s.en.kind - 1] + qrow * kHeadDim;
-                    pml = a.whole_ml[s.en.kind - 1] + qrow;
+                } else if (a.whole_o) {
+                    po = a.whole_o + qrow * kHeadDim;
+                    pml = a.whole_ml + qrow;
                 }
                 float f0 = 1.f, f1 = 0.f;   // factors of O0 and O1 (f0: of the own O when there are two row halves)
                 float M = m, L = l;
@@ -1062,7 +1053,7 @@ struct PlanArgs {
     Plan plan;
     int max_entries;
     int tok_per_entry;          // query tokens of a row tile: kRowTile / group
-    const int32_t* q_start;     // nullptr: one token a request
+    const int32_t* q_start;     // chunks
     int total_q;
     const int32_t* seq_lens;
     int batch;
@@ -1073,7 +1064,7 @@ struct PlanArgs {
     const int32_t* shared_pages;
     int num_groups;
     int num_q_heads;
-    __nv_bfloat16* out;         // window mode: rows that see nothing get 0 / -inf here
+    __nv_bfloat16* out;         // chunks: rows that see nothing get 0 / -inf here
     float* lse;
 };
 
@@ -1137,7 +1128,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const __grid_constan
     pdl_launch_dependents();
     // Row tiles before each request (or group): the entries of one are consecutive.
     int rows_entries = 0;   // entries of the row tiles
-    const int owners = PREFIX ? p.num_groups : (p.q_start ? p.batch : 0);
+    const int owners = PREFIX ? p.num_groups : p.batch;
     for (int i0 = 0; i0 < owners; i0 += kPlanThreads) {
         const int i = i0 + tid;
         int count = 0;
@@ -1160,20 +1151,44 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const __grid_constan
         rows_entries = static_cast<int>(min(sum, static_cast<int64_t>(INT_MAX / 2)));
     }
     // Overlapping (broken) starts could list more tiles than the workspace holds.
-    const int room = p.max_entries - (PREFIX ? p.batch : 0);
-    if (rows_entries > room) {
+    if (rows_entries > p.max_entries) {
         if (tid == 0) svq_flag(PREFIX ? SV_DEVERR_GROUP : SV_DEVERR_Q_START);
-        rows_entries = room;
+        rows_entries = p.max_entries;
     }
     __syncthreads();
-    const int n = PREFIX ? rows_entries + p.batch : (p.q_start ? rows_entries : p.batch);
+    const int n = rows_entries;
+    if (PREFIX) {
+        for (int b = tid; b < p.batch; b += kPlanThreads) {
+            int pre = -2, page = -1;
+            if (p.group_start[0] <= b && b < p.group_start[p.num_groups]) {
+                const int g = find_le(p.group_start, p.num_groups, b);
+                const int a = p.group_start[g], end = p.group_start[g + 1];
+                const int sp = p.shared_pages[g];
+                pre = -1;
+                if (a < 0 || a > b || b >= end || end > p.batch || sp < 0 || sp > p.max_pages) {
+                    svq_flag(SV_DEVERR_GROUP);
+                } else {
+                    const int len = checked_len(p, b);
+                    if (len < sp * kPage) {
+                        if (len > 0) svq_flag(SV_DEVERR_GROUP);
+                    } else if (len > 0) {
+                        const int pe = p.plan.req_offset[g] + (b - a) / p.tok_per_entry;
+                        if (sp > 0 && pe < n) pre = pe;
+                        page = sp;
+                    }
+                }
+            }
+            p.plan.req_entry[b] = pre;
+            p.plan.first_page[b] = page;
+        }
+    }
     int64_t base = 0;
     for (int e0 = 0; e0 < n; e0 += kPlanThreads) {
         const int e = e0 + tid;
-        Entry en = {0, 0, 0, 0, 0, 0, 0, kDirect};
-        bool empty = false;   // window mode: rows that see nothing
+        Entry en = {0, 0, 0, 0, 0, 0, 0, 0};
+        bool empty = false;   // chunks: rows that see nothing
         if (e < n) {
-            if (PREFIX && e < rows_entries) {
+            if (PREFIX) {
                 const int g = find_le(p.plan.req_offset, p.num_groups, e);
                 const int a = p.group_start[g], b = p.group_start[g + 1];
                 const int at = (e - p.plan.req_offset[g]) * p.tok_per_entry;
@@ -1182,45 +1197,14 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const __grid_constan
                 en.pos0 = kAllVisible;
                 en.req = a;
                 en.npages = p.shared_pages[g];
-                en.kind = kPrefix;
-            } else if (PREFIX) {
-                const int b = e - rows_entries;
-                en.row0 = en.req = b;
-                en.ntok = 1;
-                en.kind = kSuffix;
-                int pre = -2;     // -2: no group holds the request, -1: no prefix
-                if (p.group_start[0] <= b && b < p.group_start[p.num_groups]) {
-                    const int g = find_le(p.group_start, p.num_groups, b);
-                    const int a = p.group_start[g], end = p.group_start[g + 1];
-                    const int sp = p.shared_pages[g];
-                    pre = -1;
-                    if (a < 0 || a > b || b >= end || end > p.batch || sp < 0 || sp > p.max_pages) {
-                        svq_flag(SV_DEVERR_GROUP);
-                    } else {
-                        const int len = checked_len(p, b);
-                        if (len < sp * kPage) {
-                            if (len > 0) svq_flag(SV_DEVERR_GROUP);
-                        } else if (len > 0) {
-                            const int pe = p.plan.req_offset[g] + (b - a) / p.tok_per_entry;
-                            if (sp > 0 && pe < rows_entries) pre = pe;
-                            en.pos0 = len - 1;
-                            en.w0 = sp;
-                            en.npages = (len + kPage - 1) / kPage - sp;
-                        }
-                    }
-                }
-                p.plan.req_entry[b] = pre;
             } else {
-                int b = e, at = 0, size = 1, start = e;
-                if (p.q_start) {
-                    b = find_le(p.plan.req_offset, p.batch, e);
-                    start = p.q_start[b];
-                    size = p.q_start[b + 1] - start;
-                    at = (e - p.plan.req_offset[b]) * p.tok_per_entry;
-                }
+                const int b = find_le(p.plan.req_offset, p.batch, e);
+                const int start = p.q_start[b];
+                const int size = p.q_start[b + 1] - start;
+                const int at = (e - p.plan.req_offset[b]) * p.tok_per_entry;
                 int len = checked_len(p, b);
                 if (size > len) {
-                    if (len > 0 || size > 1) svq_flag(p.q_start ? SV_DEVERR_Q_START : SV_DEVERR_SEQ_LEN);
+                    if (len > 0) svq_flag(SV_DEVERR_Q_START);
                     len = 0;
                 }
                 en.row0 = start + at;
@@ -1230,7 +1214,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const __grid_constan
                     en.pos0 = len - size + at;
                     const int last = (en.pos0 + en.ntok - 1) / kPage + 1;
                     const int w0 = max(0, en.pos0 - p.window + 1) / kPage;
-                    en.sink_pages = min(w0, p.sink / kPage + (p.sink % kPage != 0));
+                    en.sink_pages = sink_pages_of(p.sink, w0);
                     en.w0 = w0;
                     en.npages = en.sink_pages + last - w0;
                 } else {
@@ -1260,18 +1244,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const __grid_constan
 }
 
 // ---------------------------------------------------------------- joining partials
-// The partials of one item, in tile order: those of CTAs c0 .. c0 + n - 1, or
-// (whole) the one of the CTA that had all of it.
-struct Pieces {
-    const float* o;
-    const float2* ml;
-    int64_t first;     // row of the first piece
-    int64_t second;    // row of the second; the others follow `stride` apart
-    int64_t stride;
-    int n;
-    __device__ __forceinline__ int64_t row(int k) const { return k == 0 ? first : second + (k - 1) * stride; }
-};
-
+// The partials of an item that is cut, those of consecutive CTAs in tile order.
 __device__ __forceinline__ Pieces cut_pieces(const AttendArgs& a, const Share& share, int64_t begin, int64_t end, int r) {
     Pieces p;
     const int c0 = share.cta_of(begin);
@@ -1284,82 +1257,7 @@ __device__ __forceinline__ Pieces cut_pieces(const AttendArgs& a, const Share& s
     return p;
 }
 
-constexpr int kJoinThreads = 128;
-
-// One row by the whole CTA: warps take pieces in turn, lane l channels 4 l .. 4 l + 3.
-__device__ __forceinline__ void join_row(const Pieces (&lists)[2], int nlists, __nv_bfloat16* out, float* lse) {
-    __shared__ float4 sm_o[kJoinThreads / 32][32];
-    __shared__ float2 sm_ml[kJoinThreads / 32];
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    constexpr int kWarps = kJoinThreads / 32;
-    float m = -INFINITY, l = 0.f;
-    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-    int k0 = warp;
-    for (int li = 0; li < nlists; ++li) {
-        const Pieces& p = lists[li];
-        int k = k0;
-        for (; k < p.n; k += 4 * kWarps) {
-            float2 ml[4];
-            float4 o[4];
-#pragma unroll
-            for (int u = 0; u < 4; ++u) {
-                const int j = k + u * kWarps;
-                ml[u] = j < p.n ? p.ml[p.row(j)] : make_float2(-INFINITY, 0.f);
-                o[u] = j < p.n ? *reinterpret_cast<const float4*>(p.o + p.row(j) * kHeadDim + 4 * lane)
-                               : make_float4(0.f, 0.f, 0.f, 0.f);
-            }
-            float mn = m;
-#pragma unroll
-            for (int u = 0; u < 4; ++u) mn = fmaxf(mn, ml[u].x);
-            const float base = mn == -INFINITY ? 0.f : mn;   // pieces without a visible token: weights 0
-            const float e = ex2(m - base);
-            l *= e;
-            acc.x *= e;
-            acc.y *= e;
-            acc.z *= e;
-            acc.w *= e;
-            m = mn;
-#pragma unroll
-            for (int u = 0; u < 4; ++u) {
-                const float f = ex2(ml[u].x - base);
-                l += ml[u].y * f;
-                acc.x += o[u].x * f;
-                acc.y += o[u].y * f;
-                acc.z += o[u].z * f;
-                acc.w += o[u].w * f;
-            }
-        }
-        k0 = (k0 + kWarps - p.n % kWarps) % kWarps;   // the next list goes on where this one ended
-    }
-    sm_o[warp][lane] = acc;
-    if (lane == 0) sm_ml[warp] = make_float2(m, l);
-    __syncthreads();
-    if (warp == 0) {
-        float M = -INFINITY;
-#pragma unroll
-        for (int u = 0; u < kWarps; ++u) M = fmaxf(M, sm_ml[u].x);
-        float L = 0.f;
-        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-        for (int u = 0; u < kWarps; ++u) {
-            const float f = ex2(sm_ml[u].x - (M == -INFINITY ? 0.f : M));
-            L += sm_ml[u].y * f;
-            o.x += sm_o[u][lane].x * f;
-            o.y += sm_o[u][lane].y * f;
-            o.z += sm_o[u][lane].z * f;
-            o.w += sm_o[u][lane].w * f;
-        }
-        const float inv = L > 0.f ? 1.f / L : (L == 0.f ? 0.f : L);
-        uint2 v;
-        v.x = pack_bf16x2(o.x * inv, o.y * inv);
-        v.y = pack_bf16x2(o.z * inv, o.w * inv);
-        *reinterpret_cast<uint2*>(out + 4 * lane) = v;
-        if (lane == 0) *lse = L > 0.f ? (M + log2f(L)) * 0.69314718055994531f : (L == 0.f ? -INFINITY : L);
-    }
-    __syncthreads();   // the shared arrays are written again for the next row
-}
-
-// Window mode: CTA (c, y) joins the item that attend CTA c goes on with, if c
+// Chunks: CTA (c, y) joins the item that attend CTA c goes on with, if c
 // is the first to do so; rows y, y + gridDim.y, ...
 __global__ void __launch_bounds__(kJoinThreads) join_cut_kernel(const __grid_constant__ AttendArgs a, int ctas) {
     pdl_wait();
@@ -1385,32 +1283,29 @@ __global__ void __launch_bounds__(kJoinThreads) join_cut_kernel(const __grid_con
     }
 }
 
-// Prefix mode: CTA per (request, query head) joins its prefix and its suffix.
+// Prefixes: CTA per (request, query head) joins its prefix and what is behind it.
 __global__ void __launch_bounds__(kJoinThreads) join_prefix_kernel(const __grid_constant__ AttendArgs a, int ctas) {
     pdl_wait();
     const int b = blockIdx.x / a.num_q_heads, hq = blockIdx.x % a.num_q_heads;
     const int n = *a.plan.num_entries;
     const int pre = a.plan.req_entry[b];
     if (pre == -2) return;
-    const int64_t total = a.plan.cum[n] * a.num_kv_heads;
-    const Share share(total, ctas);
-    const int h = hq / a.group, hr = hq - h * a.group;
     const int64_t q = blockIdx.x;
     Pieces lists[2];
     int nl = 0;
-    const int suf = n - static_cast<int>(gridDim.x / a.num_q_heads) + b;
-    for (int k = 0; k < 2; ++k) {
-        const int e = k == 0 ? pre : suf;
-        if (e < 0) continue;
-        const Entry en = a.plan.entries[e];
+    if (pre >= 0) {
+        const int64_t total = a.plan.cum[n] * a.num_kv_heads;
+        const Share share(total, ctas);
+        const int h = hq / a.group, hr = hq - h * a.group;
+        const Entry en = a.plan.entries[pre];
         const int tiles = tiles_of(en.npages);
-        if (tiles == 0) continue;
-        const int64_t begin = a.plan.cum[e] * a.num_kv_heads + static_cast<int64_t>(h) * tiles;
+        const int64_t begin = a.plan.cum[pre] * a.num_kv_heads + static_cast<int64_t>(h) * tiles;
         if (share.cta_of(begin) == share.cta_of(begin + tiles - 1))
-            lists[nl++] = Pieces{a.whole_o[k], a.whole_ml[k], q, q, 0, 1};
+            lists[nl++] = Pieces{a.whole_o, a.whole_ml, q, q, 0, 1};
         else
             lists[nl++] = cut_pieces(a, share, begin, begin + tiles, (b - en.row0) * a.group + hr);
     }
+    lists[nl++] = Pieces{a.split_o, a.split_ml, q * a.splits, q * a.splits + 1, 1, a.splits};
     join_row(lists, nl, a.out + q * kHeadDim, a.lse + q);
 }
 
@@ -1418,13 +1313,12 @@ __global__ void __launch_bounds__(kJoinThreads) join_prefix_kernel(const __grid_
 size_t up(size_t n) { return (n + 255) / 256 * 256; }
 
 struct Layout {
-    size_t entries, cum, num, req_entry, req_offset, cut_o, cut_ml, whole_o, whole_ml, total;
+    size_t entries, cum, num, req_offset, req_entry, first_page, cut_o, cut_ml, whole_o, whole_ml, split_o, split_ml, total;
     int max_entries, slot_rows;
-    // owners: requests (ragged chunks) or groups; rows: query tokens; prefix: room for whole parts
+    // owners: requests (chunks) or groups (prefixes); rows: query tokens
     Layout(int64_t batch, int64_t owners, int64_t rows, int num_q_heads, int num_kv_heads, bool prefix) {
         const int group = num_q_heads / num_kv_heads;
-        const int64_t per = kRowTile / group;
-        const int64_t e = rows / per + owners + (prefix ? batch : 0);
+        const int64_t e = rows / (kRowTile / group) + owners;
         max_entries = static_cast<int>(e);
         slot_rows = static_cast<int>(rows * group < kRowTile ? rows * group : kRowTile);
         size_t at = 0;
@@ -1432,34 +1326,20 @@ struct Layout {
         entries = take(e * sizeof(Entry));
         cum = take((e + 1) * sizeof(int64_t));
         num = take(sizeof(int));
-        req_entry = take(prefix ? batch * sizeof(int) : 0);
         req_offset = take(owners * sizeof(int));
         cut_o = take(2ull * kMaxCtas * slot_rows * kHeadDim * sizeof(float));
         cut_ml = take(2ull * kMaxCtas * slot_rows * sizeof(float2));
-        const size_t heads = prefix ? static_cast<size_t>(batch) * num_q_heads : 0;
-        whole_o = take(2 * heads * kHeadDim * sizeof(float));
-        whole_ml = take(2 * heads * sizeof(float2));
+        const size_t b = prefix ? batch : 0, heads = b * num_q_heads;
+        const size_t parts = prefix ? window_decode_rows(batch, num_q_heads, num_kv_heads) : 0;
+        req_entry = take(b * sizeof(int));
+        first_page = take(b * sizeof(int));
+        whole_o = take(heads * kHeadDim * sizeof(float));
+        whole_ml = take(heads * sizeof(float2));
+        split_o = take(parts * kHeadDim * sizeof(float));
+        split_ml = take(parts * sizeof(float2));
         total = at;
     }
 };
-
-// The K or V pool bf16 [pages][kv heads][16][128] as a 4-D tensor: 64 channels,
-// 8 rows (256 bytes apart), 2 channel halves (128 bytes apart), groups of 8
-// rows (2 KB apart).  A box of 64 x 8 x 2 x 2 is one page's tile of one kv head
-// and lands as [8-row group][half][8 rows of 128 bytes], each 1 KB block
-// 128-byte swizzled: 8-row groups 2 KB apart through the whole stage, the
-// uniform stride an MMA operand needs, with one copy a page.
-bool encode_map(CUtensorMap* map, const void* pool, int64_t row_groups) {
-    auto enc = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(tensor_map_encode_entry());
-    if (!enc) return false;
-    const cuuint64_t dims[4] = {64, 8, 2, static_cast<cuuint64_t>(row_groups)};
-    const cuuint64_t strides[3] = {256, 128, 2048};
-    const cuuint32_t box[4] = {64, 8, 2, 2};
-    const cuuint32_t ones[4] = {1, 1, 1, 1};
-    return enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(pool), dims, strides, box, ones,
-               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
 
 template <bool FP8>
 int launch_attend(const AttendArgs& a, const CUtensorMap& tk, const CUtensorMap& tv, int ctas, cudaStream_t stream) {
@@ -1477,10 +1357,10 @@ int launch_attend(const AttendArgs& a, const CUtensorMap& tk, const CUtensorMap&
                : SV_ERR_CUDA;
 }
 
-// What both calls do: arguments, plan, attention.
-int launch_common(const sv_cache* c, const void* q, int num_q_heads, const int32_t* page_table, int max_pages,
-                  const Layout& lay, int window, int sink, float softmax_scale, void* out, float* lse, void* workspace,
-                  PlanArgs& p, bool prefix, int batch, int ctas, AttendArgs& a, cudaStream_t stream) {
+// The arguments both calls share.
+void fill_args(const sv_cache* c, const void* q, int num_q_heads, const int32_t* page_table, int max_pages,
+               const Layout& lay, int window, int sink, float softmax_scale, void* out, float* lse, void* workspace,
+               int batch, AttendArgs& a, PlanArgs& p) {
     unsigned char* ws = static_cast<unsigned char*>(workspace);
     a.q = static_cast<const __nv_bfloat16*>(q);
     a.num_q_heads = num_q_heads;
@@ -1496,8 +1376,9 @@ int launch_common(const sv_cache* c, const void* q, int num_q_heads, const int32
     a.plan.entries = reinterpret_cast<Entry*>(ws + lay.entries);
     a.plan.cum = reinterpret_cast<int64_t*>(ws + lay.cum);
     a.plan.num_entries = reinterpret_cast<int*>(ws + lay.num);
-    a.plan.req_entry = reinterpret_cast<int*>(ws + lay.req_entry);
     a.plan.req_offset = reinterpret_cast<int*>(ws + lay.req_offset);
+    a.plan.req_entry = reinterpret_cast<int*>(ws + lay.req_entry);
+    a.plan.first_page = reinterpret_cast<int*>(ws + lay.first_page);
     a.window = window > 0 ? window : INT_MAX;
     a.sink = sink;
     a.scale_log2 = softmax_scale * 1.4426950408889634f;
@@ -1506,11 +1387,6 @@ int launch_common(const sv_cache* c, const void* q, int num_q_heads, const int32
     a.cut_o = reinterpret_cast<float*>(ws + lay.cut_o);
     a.cut_ml = reinterpret_cast<float2*>(ws + lay.cut_ml);
     a.slot_rows = lay.slot_rows;
-    const size_t heads = static_cast<size_t>(batch) * num_q_heads;
-    for (int k = 0; k < 2; ++k) {
-        a.whole_o[k] = reinterpret_cast<float*>(ws + lay.whole_o) + k * heads * kHeadDim;
-        a.whole_ml[k] = reinterpret_cast<float2*>(ws + lay.whole_ml) + k * heads;
-    }
     p.plan = a.plan;
     p.max_entries = lay.max_entries;
     p.tok_per_entry = kRowTile / a.group;
@@ -1521,24 +1397,28 @@ int launch_common(const sv_cache* c, const void* q, int num_q_heads, const int32
     p.num_q_heads = num_q_heads;
     p.out = a.out;
     p.lse = lse;
-    const bool fp8 = c->kv_format == SV_KV_FP8_E4M3;
-    CUtensorMap tk = {}, tv = {};
-    if (!fp8) {
-        // TMA coordinates are 32-bit.
-        const int64_t groups = c->num_phys_pages * c->num_kv_heads * 2;
-        if (groups > INT_MAX) return SV_ERR_UNSUPPORTED;
-        if (!encode_map(&tk, c->k_pool, groups) || !encode_map(&tv, c->v_pool, groups)) return SV_ERR_CUDA;
-    }
-    const cudaError_t err = prefix ? launch_pdl(plan_kernel<true>, dim3(1), dim3(kPlanThreads), 0, stream, p)
-                                   : launch_pdl(plan_kernel<false>, dim3(1), dim3(kPlanThreads), 0, stream, p);
-    if (err != cudaSuccess) return SV_ERR_CUDA;
-    return fp8 ? launch_attend<true>(a, tk, tv, ctas, stream) : launch_attend<false>(a, tk, tv, ctas, stream);
 }
+
+int launch_tiles(const sv_cache* c, const AttendArgs& a, int ctas, cudaStream_t stream) {
+    CUtensorMap tk = {}, tv = {};
+    if (c->kv_format == SV_KV_FP8_E4M3) return launch_attend<true>(a, tk, tv, ctas, stream);
+    // TMA coordinates are 32-bit.
+    const int64_t groups = c->num_phys_pages * c->num_kv_heads * 2;
+    if (groups > INT_MAX) return SV_ERR_UNSUPPORTED;
+    if (!encode_pages_map(&tk, c->k_pool, groups) || !encode_pages_map(&tv, c->v_pool, groups)) return SV_ERR_CUDA;
+    return launch_attend<false>(a, tk, tv, ctas, stream);
+}
+
+int cta_count(int sm_count) { return sm_count < kMaxCtas ? sm_count : kMaxCtas; }
 
 }  // namespace
 
+// One token a request goes to the decode kernel (partials of its splits); chunks to the tiles.
 size_t window_workspace_bytes(int batch, int num_q_heads, int num_kv_heads, int total_q) {
-    return Layout(batch, batch, total_q, num_q_heads, num_kv_heads, false).total;
+    const size_t chunks = Layout(batch, batch, total_q, num_q_heads, num_kv_heads, false).total;
+    const size_t rows = static_cast<size_t>(window_decode_rows(batch, num_q_heads, num_kv_heads));
+    const size_t decode = total_q == batch ? up(rows * kHeadDim * sizeof(float)) + up(rows * sizeof(float2)) : 0;
+    return chunks > decode ? chunks : decode;
 }
 size_t prefix_workspace_bytes(int batch, int num_q_heads, int num_kv_heads, int num_groups) {
     return Layout(batch, num_groups, batch, num_q_heads, num_kv_heads, true).total;
@@ -1547,15 +1427,28 @@ size_t prefix_workspace_bytes(int batch, int num_q_heads, int num_kv_heads, int 
 int launch_window(const sv_cache* c, const void* q, int num_q_heads, const int32_t* q_start, int total_q,
                   const int32_t* page_table, const int32_t* seq_lens, int batch, int max_pages, int window, int sink,
                   float softmax_scale, void* out, float* lse, void* workspace, int sm_count, cudaStream_t stream) {
+    const int ctas = cta_count(sm_count);
+    if (!q_start) {
+        // Pages of a window that starts anywhere in a page, and of the sinks.
+        const int64_t span = window > 0 ? (static_cast<int64_t>(window) + 14) / kPage + 1 + (sink + 15ll) / kPage : max_pages;
+        const int splits = window_decode_splits(c->kv_format == SV_KV_FP8_E4M3, batch, c->num_kv_heads,
+                                                span < max_pages ? span : max_pages, ctas);
+        const int64_t heads = static_cast<int64_t>(batch) * num_q_heads;
+        float* o = static_cast<float*>(workspace);
+        float2* ml = reinterpret_cast<float2*>(static_cast<unsigned char*>(workspace) + up(heads * splits * kHeadDim * sizeof(float)));
+        const int st = launch_window_decode(c, q, num_q_heads, page_table, seq_lens, batch, max_pages, window, sink, nullptr,
+                                            softmax_scale, splits, o, ml, stream);
+        return st ? st : launch_join_splits(o, ml, splits, heads, out, lse, stream);
+    }
     const Layout lay(batch, batch, total_q, num_q_heads, c->num_kv_heads, false);
-    const int ctas = sm_count < kMaxCtas ? sm_count : kMaxCtas;
     PlanArgs p = {};
+    AttendArgs a = {};
+    fill_args(c, q, num_q_heads, page_table, max_pages, lay, window, sink, softmax_scale, out, lse, workspace, batch, a, p);
     p.q_start = q_start;
     p.total_q = total_q;
     p.seq_lens = seq_lens;
-    AttendArgs a = {};
-    const int st = launch_common(c, q, num_q_heads, page_table, max_pages, lay, window, sink, softmax_scale, out, lse,
-                                 workspace, p, false, batch, ctas, a, stream);
+    if (launch_pdl(plan_kernel<false>, dim3(1), dim3(kPlanThreads), 0, stream, p) != cudaSuccess) return SV_ERR_CUDA;
+    const int st = launch_tiles(c, a, ctas, stream);
     if (st || ctas < 2) return st;
     const int y = lay.slot_rows < 32 ? lay.slot_rows : 32;
     return launch_pdl(join_cut_kernel, dim3(ctas - 1, y), dim3(kJoinThreads), 0, stream, a, ctas) == cudaSuccess
@@ -1568,16 +1461,25 @@ int launch_prefix(const sv_cache* c, const void* q, int num_q_heads, const int32
                   const int32_t* shared_pages, int num_groups, float softmax_scale, void* out, float* lse,
                   void* workspace, int sm_count, cudaStream_t stream) {
     const Layout lay(batch, num_groups, batch, num_q_heads, c->num_kv_heads, true);
-    const int ctas = sm_count < kMaxCtas ? sm_count : kMaxCtas;
+    const int ctas = cta_count(sm_count);
     PlanArgs p = {};
+    AttendArgs a = {};
+    fill_args(c, q, num_q_heads, page_table, max_pages, lay, 0, 0, softmax_scale, out, lse, workspace, batch, a, p);
     p.seq_lens = seq_lens;
     p.group_start = group_start;
     p.shared_pages = shared_pages;
     p.num_groups = num_groups;
-    AttendArgs a = {};
-    const int st = launch_common(c, q, num_q_heads, page_table, max_pages, lay, 0, 0, softmax_scale, out, lse, workspace,
-                                 p, true, batch, ctas, a, stream);
+    unsigned char* ws = static_cast<unsigned char*>(workspace);
+    a.whole_o = reinterpret_cast<float*>(ws + lay.whole_o);
+    a.whole_ml = reinterpret_cast<float2*>(ws + lay.whole_ml);
+    a.split_o = reinterpret_cast<float*>(ws + lay.split_o);
+    a.split_ml = reinterpret_cast<float2*>(ws + lay.split_ml);
+    a.splits = window_decode_splits(c->kv_format == SV_KV_FP8_E4M3, batch, c->num_kv_heads, max_pages, ctas);
+    if (launch_pdl(plan_kernel<true>, dim3(1), dim3(kPlanThreads), 0, stream, p) != cudaSuccess) return SV_ERR_CUDA;
+    int st = launch_window_decode(c, q, num_q_heads, page_table, seq_lens, batch, max_pages, 0, 0, a.plan.first_page,
+                                  softmax_scale, a.splits, a.split_o, a.split_ml, stream);
     if (st) return st;
+    if ((st = launch_tiles(c, a, ctas, stream))) return st;
     return launch_pdl(join_prefix_kernel, dim3(static_cast<unsigned>(batch) * num_q_heads), dim3(kJoinThreads), 0, stream,
                       a, ctas) == cudaSuccess
                ? SV_OK

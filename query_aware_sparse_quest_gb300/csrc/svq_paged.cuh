@@ -1,0 +1,142 @@
+// Helpers shared by the window / prefix attention kernels: what a row sees, the
+// pool's tensor map, and the joining of partial results.
+#pragma once
+
+#include <cuda.h>
+#include <cudaTypedefs.h>
+
+#include "svq_common.cuh"
+
+namespace svq {
+namespace {
+
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// Bit t: some row at positions qlo .. qhi sees token t of the page whose first
+// token is at `base`: token <= qhi, and token > qlo - window or token < sink.
+__device__ __forceinline__ uint32_t union_mask(int base, int qlo, int qhi, int window, int sink) {
+    const int hi = min(16, qhi - base + 1);
+    if (hi <= 0) return 0u;
+    const int lo = max(0, min(16, max(0, qlo - window + 1) - base));
+    const int sk = max(0, min(16, sink - base));
+    return ((1u << hi) - 1u) & (~((1u << lo) - 1u) | ((1u << sk) - 1u));
+}
+// Bit t: the row at position qpos does.
+__device__ __forceinline__ uint32_t page_mask(int base, int qpos, int window, int sink) {
+    return union_mask(base, qpos, qpos, window, sink);
+}
+// First page of a window that begins at token `lo`, and the sink pages before it.
+__device__ __forceinline__ int sink_pages_of(int sink, int w0) { return min(w0, sink / kPage + (sink % kPage != 0)); }
+
+// The K or V pool bf16 [pages][kv heads][16][128] as a 4-D tensor: 64 channels,
+// 8 rows (256 bytes apart), 2 channel halves (128 bytes apart), groups of 8
+// rows (2 KB apart).  A box of 64 x 8 x 2 x 2 is one page's tile of one kv head
+// and lands as [8-row group][half][8 rows of 128 bytes], each 1 KB block
+// 128-byte swizzled: 8-row groups 2 KB apart through a whole stage, the
+// uniform stride an MMA operand needs, with one copy a page.
+inline bool encode_pages_map(CUtensorMap* map, const void* pool, int64_t row_groups) {
+    auto enc = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(tensor_map_encode_entry());
+    if (!enc) return false;
+    const cuuint64_t dims[4] = {64, 8, 2, static_cast<cuuint64_t>(row_groups)};
+    const cuuint64_t strides[3] = {256, 128, 2048};
+    const cuuint32_t box[4] = {64, 8, 2, 2};
+    const cuuint32_t ones[4] = {1, 1, 1, 1};
+    return enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(pool), dims, strides, box, ones,
+               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// ---------------------------------------------------------------- joining partials
+// A list of partials (o, (base, sum)) of one row; the base is in log2 units, o
+// and the sum are relative to it.
+struct Pieces {
+    const float* o;
+    const float2* ml;
+    int64_t first;     // row of the first piece
+    int64_t second;    // row of the second; the others follow `stride` apart
+    int64_t stride;
+    int n;
+    __device__ __forceinline__ int64_t row(int k) const { return k == 0 ? first : second + (k - 1) * stride; }
+};
+
+constexpr int kJoinThreads = 128;
+
+// One row by the whole CTA: warps take pieces in turn, lane l channels 4 l .. 4 l + 3.
+__device__ __forceinline__ void join_row(const Pieces (&lists)[2], int nlists, __nv_bfloat16* out, float* lse) {
+    __shared__ float4 sm_o[kJoinThreads / 32][32];
+    __shared__ float2 sm_ml[kJoinThreads / 32];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    constexpr int kWarps = kJoinThreads / 32;
+    float m = -INFINITY, l = 0.f;
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    int k0 = warp;
+    for (int li = 0; li < nlists; ++li) {
+        const Pieces& p = lists[li];
+        int k = k0;
+        for (; k < p.n; k += 4 * kWarps) {
+            float2 ml[4];
+            float4 o[4];
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+                const int j = k + u * kWarps;
+                ml[u] = j < p.n ? p.ml[p.row(j)] : make_float2(-INFINITY, 0.f);
+                o[u] = j < p.n ? *reinterpret_cast<const float4*>(p.o + p.row(j) * kHeadDim + 4 * lane)
+                               : make_float4(0.f, 0.f, 0.f, 0.f);
+            }
+            float mn = m;
+#pragma unroll
+            for (int u = 0; u < 4; ++u) mn = fmaxf(mn, ml[u].x);
+            const float base = mn == -INFINITY ? 0.f : mn;   // pieces without a visible token: weights 0
+            const float e = ex2(m - base);
+            l *= e;
+            acc.x *= e;
+            acc.y *= e;
+            acc.z *= e;
+            acc.w *= e;
+            m = mn;
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+                const float f = ex2(ml[u].x - base);
+                l += ml[u].y * f;
+                acc.x += o[u].x * f;
+                acc.y += o[u].y * f;
+                acc.z += o[u].z * f;
+                acc.w += o[u].w * f;
+            }
+        }
+        k0 = (k0 + kWarps - p.n % kWarps) % kWarps;   // the next list goes on where this one ended
+    }
+    sm_o[warp][lane] = acc;
+    if (lane == 0) sm_ml[warp] = make_float2(m, l);
+    __syncthreads();
+    if (warp == 0) {
+        float M = -INFINITY;
+#pragma unroll
+        for (int u = 0; u < kWarps; ++u) M = fmaxf(M, sm_ml[u].x);
+        float L = 0.f;
+        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int u = 0; u < kWarps; ++u) {
+            const float f = ex2(sm_ml[u].x - (M == -INFINITY ? 0.f : M));
+            L += sm_ml[u].y * f;
+            o.x += sm_o[u][lane].x * f;
+            o.y += sm_o[u][lane].y * f;
+            o.z += sm_o[u][lane].z * f;
+            o.w += sm_o[u][lane].w * f;
+        }
+        const float inv = L > 0.f ? 1.f / L : (L == 0.f ? 0.f : L);
+        uint2 v;
+        v.x = pack_bf16x2(o.x * inv, o.y * inv);
+        v.y = pack_bf16x2(o.z * inv, o.w * inv);
+        *reinterpret_cast<uint2*>(out + 4 * lane) = v;
+        if (lane == 0) *lse = L > 0.f ? (M + log2f(L)) * 0.69314718055994531f : (L == 0.f ? -INFINITY : L);
+    }
+    __syncthreads();   // the shared arrays are written again for the next row
+}
+
+}  // namespace
+}  // namespace svq
