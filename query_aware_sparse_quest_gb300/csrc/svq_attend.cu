@@ -71,15 +71,21 @@ struct __align__(16) Entry {
     int sink_pages;
     int w0;
     int npages;       // pages in the list
-    int unused;
+    int tiles;        // key tiles of npages
 };
 constexpr int kAllVisible = 1 << 30;
 
 __device__ __forceinline__ int tiles_of(int npages) { return (npages + kTilePages - 1) / kTilePages; }
 
+// What an item costs beside its tiles (loading Q, filling the pipeline, writing
+// the rows), in tiles: shares of the work count it, so that a CTA with many
+// short items does not take longer than one with few long ones.
+constexpr int kItemCost = 2;
+__device__ __forceinline__ int cost_of(int tiles) { return tiles ? tiles + kItemCost : 0; }
+
 struct Plan {
     Entry* entries;
-    int64_t* cum;      // [E + 1] tiles per kv head before each entry
+    int64_t* cum;      // [E + 1] cost per kv head of the entries before each
     int* num_entries;
     int* req_offset;   // first entry of each request (chunks) or group (prefixes)
     int* req_entry;    // prefixes: entry that holds each request's rows, -1: none, -2: the request is not touched
@@ -112,7 +118,7 @@ struct AttendArgs {
     int splits;
 };
 
-// The run of tiles of CTA c: total / ctas each, the first total % ctas one more.
+// The share of CTA c: total / ctas of the cost each, the first total % ctas one more.
 struct Share {
     int64_t q, r;
     __device__ __forceinline__ Share(int64_t total, int ctas) : q(total / ctas), r(total % ctas) {}
@@ -270,60 +276,28 @@ struct Cfg {
 };
 static_assert(Cfg<false>::kSmem <= 227 * 1024 && Cfg<true>::kSmem <= 227 * 1024, "shared memory of one CTA");
 
+// A run of tiles of one item (entry, kv head); none: the CTA's work is over.
+struct __align__(16) Seg {
+    Entry en;
+    int h;            // kv head
+    int t0, t1;       // tiles of the item
+    int slot;         // where a partial goes; -1: the segment is the whole item
+};
+constexpr int kSegs = 4;
+
 struct Control {
     uint64_t full[5], empty[5];       // ring stages
     uint64_t code_full[3], code_empty[3];
+    uint64_t seg_full[kSegs], seg_empty[kSegs];
     uint64_t s_full[2], p_full[2], o_full[2], q_full[2];
     uint64_t join[2];                 // both streams have published their statistics / have read O0 and O1
     uint64_t drain;
     uint32_t tmem;
-    int start_e, start_h;
-    int64_t start_t;
     int fault[kInfoSlots];            // pages of a tile that the table does not give
+    Seg seg[kSegs];
     float2 ml[2][128];                // stream statistics of a joined tile
 };
 static_assert(sizeof(Control) <= 3072, "control block");
-
-// A run of tiles of one item (entry, kv head).
-struct Seg {
-    Entry en;
-    int h;        // kv head
-    int t0, t1;   // tiles of the item
-    int tiles;    // of the whole item
-};
-
-// The CTA's segments in order; every role walks its own copy.
-struct Walk {
-    const AttendArgs& a;
-    int e, h, t;
-    int64_t left;   // tiles still to walk
-    __device__ __forceinline__ Walk(const AttendArgs& args, const Control* c, int64_t n)
-        : a(args), e(c->start_e), h(c->start_h), t(static_cast<int>(c->start_t)), left(n) {}
-    __device__ __forceinline__ bool next(Seg& s) {
-        if (left <= 0) return false;
-        const int4* p = reinterpret_cast<const int4*>(a.plan.entries + e);
-        int4 x = p[0], y = p[1];
-        while (y.z == 0) {   // entries without pages
-            ++e;
-            p += 2;
-            x = p[0];
-            y = p[1];
-        }
-        s.en = Entry{x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
-        s.h = h;
-        s.tiles = tiles_of(y.z);
-        s.t0 = t;
-        const int64_t n = min(left, static_cast<int64_t>(s.tiles - t));
-        s.t1 = t + static_cast<int>(n);
-        left -= n;
-        t = 0;
-        if (s.t1 == s.tiles && ++h == a.num_kv_heads) {
-            h = 0;
-            ++e;
-        }
-        return true;
-    }
-};
 
 __device__ __forceinline__ int logical_page(const Entry& en, int i) {
     return i < en.sink_pages ? i : en.w0 + i - en.sink_pages;
@@ -424,6 +398,10 @@ __global__ void __launch_bounds__(Cfg<FP8>::kThreads, 1)
             mbar_init(smem_addr(&ct->o_full[w]), 1);
             mbar_init(smem_addr(&ct->q_full[w]), 128);
         }
+        for (int i = 0; i < kSegs; ++i) {
+            mbar_init(smem_addr(&ct->seg_full[i]), 1);
+            mbar_init(smem_addr(&ct->seg_empty[i]), 3 + 8 + (FP8 ? 4 : 0));   // loads, MMAs, softmax, widening warps
+        }
         mbar_init(smem_addr(&ct->join[0]), 256);
         mbar_init(smem_addr(&ct->join[1]), 256);
         mbar_init(smem_addr(&ct->drain), 1);
@@ -440,27 +418,18 @@ __global__ void __launch_bounds__(Cfg<FP8>::kThreads, 1)
     }
     pdl_wait();   // the plan comes from the kernel launched just before
     pdl_launch_dependents();
-    const int num_entries = *a.plan.num_entries;
-    const int64_t total = a.plan.cum[num_entries] * a.num_kv_heads;
-    const Share share(total, gridDim.x);
-    const int64_t first = share.start(blockIdx.x);
-    const int64_t count = share.start(blockIdx.x + 1) - first;
-    if (warp == 2 && count > 0) {
-        const int e = warp_find(a.plan.cum, num_entries, first / a.num_kv_heads);
-        if (lane == 0) {
-            const int tiles = tiles_of(a.plan.entries[e].npages);
-            const int64_t in = first - a.plan.cum[e] * a.num_kv_heads;
-            ct->start_e = e;
-            ct->start_h = static_cast<int>(in / tiles);
-            ct->start_t = in % tiles;
-        }
-    }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = ct->tmem;
+    // Every role takes the segments in order: the k-th is in slot k % kSegs.
+    auto seg_wait = [&](uint32_t k) { return bar_wait(smem_addr(&ct->seg_full[k % kSegs]), (k / kSegs) & 1); };
+    auto seg_done = [&](uint32_t k) {   // once a warp
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_addr(&ct->seg_empty[k % kSegs]));
+    };
 
-    if (count > 0) {
+    {
         if (warp == 0 || warp == 3) {
             // ---------------- loads: warp 0 keys, warp 3 values
             reg_dec<C::kOtherRegs>();
@@ -473,12 +442,10 @@ __global__ void __launch_bounds__(Cfg<FP8>::kThreads, 1)
             const uint32_t to = FP8 ? smem_addr(codes) : smem_addr(ring);
             constexpr uint32_t kTo = FP8 ? kTileTok * kHeadDim : kStageBytes;   // bytes of a stage, of a page
             constexpr uint32_t kToPage = kTo / kTilePages;
-            Walk walk(a, ct, count);
-            Seg s, nx;
             uint32_t base = 0, tile = 0;   // loads and key tiles before the segment
             uint32_t last[3] = {0, 0, 0};  // the last loads issued here, each plus 1
-            // Lane l resolves page i + l of the segment's list (four tiles at a time), well
-            // before the loads that need it: the row (page, kv head) of the pool, or -1.
+            // Lane l resolves page i + l of a segment's list (four tiles at a time), well before
+            // the loads that need it.
             auto fetch = [&](const Seg& g, int i0) {
                 const int i = i0 + lane;
                 int ph = -2;               // behind the segment's pages
@@ -486,17 +453,25 @@ __global__ void __launch_bounds__(Cfg<FP8>::kThreads, 1)
                     ph = a.page_table[static_cast<int64_t>(g.en.req) * a.max_pages + logical_page(g.en, i)];
                 return ph;
             };
-            bool more = walk.next(s);
-            int cur = -2, nxt = more ? fetch(s, s.t0 * kTilePages) : -2, seg = -2;
-            while (more) {
-                const bool have_next = walk.next(nx);
-                if (have_next) seg = fetch(nx, nx.t0 * kTilePages);
+            int cur = -2, nxt = -2;
+            for (uint32_t k = 0;; ++k) {
+                const Seg& s = ct->seg[k % kSegs];
+                if (k == 0) {
+                    SVQ_WAIT(ct->seg_full[0], 0, loads_end);
+                    nxt = fetch(s, s.t0 * kTilePages);
+                }
                 const int n = s.t1 - s.t0;
+                if (n == 0) break;
                 const int qlo = s.en.pos0, qhi = last_pos(s.en);
                 for (int i = 0; i < n; ++i) {
                     if (i % 4 == 0) {
                         cur = nxt;
-                        nxt = fetch(s, (s.t0 + i + 4) * kTilePages);
+                        if (i + 4 < n) nxt = fetch(s, (s.t0 + i + 4) * kTilePages);
+                    }
+                    if (i == n - 1) {      // the next segment's first pages
+                        SVQ_WAIT(ct->seg_full[(k + 1) % kSegs], ((k + 1) / kSegs) & 1, loads_end);
+                        const Seg& g = ct->seg[(k + 1) % kSegs];
+                        nxt = fetch(g, g.t0 * kTilePages);
                     }
                     const uint32_t at = base + (is_v ? v_load(i, n) : k_load(i));
                     const uint32_t st = at % kDepth;
@@ -573,9 +548,7 @@ __global__ void __launch_bounds__(Cfg<FP8>::kThreads, 1)
                 }
                 base += 2 * n;
                 tile += n;
-                s = nx;
-                more = have_next;
-                nxt = seg;
+                seg_done(k);
             }
             goto loads_done;   // every load has been waited for by the MMAs or the widening warps
         loads_end:
@@ -588,83 +561,132 @@ __global__ void __launch_bounds__(Cfg<FP8>::kThreads, 1)
             // ---------------- MMAs (one thread)
             reg_dec<C::kOtherRegs>();
             if (lane == 0) {
-                Walk walk(a, ct, count);
-                Seg s;
                 uint32_t ld = 0;
-                uint32_t q_ph[2] = {0, 0}, p_ph[2] = {0, 0};
+                uint32_t q_ph = 0, p_ph = 0;   // bit w: stream w's phase
                 const uint32_t ring_s = smem_addr(ring), qs_s = smem_addr(qs);
-                while (walk.next(s)) {
+                auto load_ready = [&](uint32_t i) {
+                    return bar_wait(smem_addr(&ct->full[i % C::kStages]), (i / C::kStages) & 1);
+                };
+                auto stage = [&](uint32_t i) { return ring_s + i % C::kStages * kStageBytes; };
+                auto release = [&](uint32_t i) { mma_commit(smem_addr(&ct->empty[i % C::kStages])); };
+                auto qk = [&](int w, uint32_t ks) {
+                    mma_qk(tmem + kColS + w * 128, desc_lo(qs_s + w * (128 * kHeadDim * 2), 16), desc_lo(ks, 16), kIdescQK);
+                    mma_commit(smem_addr(&ct->s_full[w]));
+                };
+                bool ok = true;
+                for (uint32_t k = 0; ok; ++k) {
+                    ok = seg_wait(k);
+                    const Seg& s = ct->seg[k % kSegs];
                     const int n = s.t1 - s.t0;
+                    if (!ok || n == 0) break;
                     const bool two = s.en.ntok * group > 128;   // two row halves; else even and odd tiles
-                    auto k_at = [&](int t) { return ld + k_load(t); };
-                    auto v_at = [&](int t) { return ld + v_load(t, n); };
-                    auto wait_load = [&](uint32_t i) {
-                        return bar_wait(smem_addr(&ct->full[i % C::kStages]), (i / C::kStages) & 1);
-                    };
-                    auto qk = [&](int w, int t) {
-                        if (!wait_load(k_at(t))) return false;
-                        tc_fence_after();
-                        const uint32_t ks = ring_s + (k_at(t) % C::kStages) * kStageBytes;
-                        const uint32_t qw = qs_s + w * (128 * kHeadDim * 2);
-                        mma_qk(tmem + kColS + w * 128, desc_lo(qw, 16), desc_lo(ks, 16), kIdescQK);
-                        mma_commit(smem_addr(&ct->s_full[w]));
-                        return true;
-                    };
-                    auto pv = [&](int w, int t, bool acc) {
-                        if (!wait_load(v_at(t))) return false;
-                        tc_fence_after();
-                        const uint32_t vs = ring_s + (v_at(t) % C::kStages) * kStageBytes;
-                        const int pages = min(kTilePages, s.en.npages - (s.t0 + t) * kTilePages);
-                        const uint32_t o = tmem + kColO + w * 128, p = tmem + kColS + w * 128;
-                        // The two 64-channel halves of a value tile are 1 KB apart (N-major operand).
-                        const uint32_t lo = desc_lo(vs, 1024);
-                        if (pages == kTilePages) {
-                            mma_pv8(o, p, lo, kIdescPV, acc);
-                        } else {
-                            for (int k = 0; k < pages; ++k)
-                                mma_pv1(o, p + k * 8, lo + k * (kPageBytes >> 4), kIdescPV, acc || k != 0);
-                        }
-                        return true;
-                    };
-                    auto release = [&](uint32_t i) { mma_commit(smem_addr(&ct->empty[i % C::kStages])); };
-                    bool ok = true;
+                    const int first_page = s.t0 * kTilePages, npages = s.en.npages;
                     for (int w = 0; w < 2 && ok; ++w) {
                         const int t = two ? 0 : w;
                         if (t >= n) break;
-                        ok = bar_wait(smem_addr(&ct->q_full[w]), q_ph[w]) && qk(w, t);
-                        q_ph[w] ^= 1;
-                        if (ok && (!two || w == 1)) release(k_at(t));
+                        const uint32_t kl = ld + k_load(t);
+                        ok = load_ready(kl) && bar_wait(smem_addr(&ct->q_full[w]), (q_ph >> w) & 1);
+                        q_ph ^= 1u << w;
+                        if (!ok) break;
+                        tc_fence_after();
+                        qk(w, stage(kl));
+                        if (!two || w == 1) release(kl);
                     }
-                    for (int t = 0; t < n && ok; ++t) {
-                        for (int v = 0; v < 2 && ok; ++v) {
-                            if (!two && v != (t & 1)) continue;
-                            const int w = v;
-                            const int step = two ? 1 : 2;
-                            ok = bar_wait(smem_addr(&ct->p_full[w]), p_ph[w]);
-                            p_ph[w] ^= 1;
-                            ok = ok && pv(w, t, t >= step);
-                            if (!ok) break;
-                            if (!two || w == 1) release(v_at(t));
-                            if (t + step < n) {
-                                ok = qk(w, t + step);
-                                if (ok && (!two || w == 1)) release(k_at(t + step));
-                            } else {
-                                mma_commit(smem_addr(&ct->o_full[w]));
-                            }
+                    const int step = two ? 1 : 2;
+                    for (int i = 0; i < (two ? 2 * n : n) && ok; ++i) {
+                        // The i-th (tile, stream) pair: everything but P is waited for and worked out first.
+                        const int t = two ? i >> 1 : i, w = i & 1;
+                        const bool next = t + step < n, done = !two || w == 1;   // done: the last use of the tiles
+                        const uint32_t vl = ld + v_load(t, n), kl = ld + k_load(t + step);
+                        const int pages = min(kTilePages, npages - first_page - t * kTilePages);
+                        // The two 64-channel halves of a value tile are 1 KB apart (N-major operand).
+                        const uint32_t v_lo = desc_lo(stage(vl), 1024), ks = stage(kl);
+                        const uint32_t o = tmem + kColO + w * 128, p = tmem + kColS + w * 128;
+                        ok = load_ready(vl) && (!next || load_ready(kl)) && bar_wait(smem_addr(&ct->p_full[w]), (p_ph >> w) & 1);
+                        p_ph ^= 1u << w;
+                        if (!ok) break;
+                        tc_fence_after();
+                        if (pages == kTilePages) {
+                            mma_pv8(o, p, v_lo, kIdescPV, t >= step);
+                        } else {
+                            for (int u = 0; u < pages; ++u)
+                                mma_pv1(o, p + u * 8, v_lo + u * (kPageBytes >> 4), kIdescPV, t >= step || u != 0);
+                        }
+                        if (next) qk(w, ks);
+                        else mma_commit(smem_addr(&ct->o_full[w]));
+                        if (done) {
+                            release(vl);
+                            if (next) release(kl);
                         }
                     }
-                    if (!ok) {
-                        svq_flag(SV_DEVERR_TIMEOUT);
-                        break;
-                    }
                     ld += 2 * n;
+                    if (ok) mbar_arrive(smem_addr(&ct->seg_empty[k % kSegs]));
                 }
+                if (!ok) svq_flag(SV_DEVERR_TIMEOUT);
                 mma_commit(smem_addr(&ct->drain));   // nothing of this CTA's is in flight when TMEM is freed
                 (void)bar_wait(smem_addr(&ct->drain), 0);
             }
             __syncwarp();
-        } else if (warp < 4) {
+        } else if (warp == 2) {
+            // ---------------- the CTA's share of the plan, segment by segment
             reg_dec<C::kOtherRegs>();
+            const int num_entries = *a.plan.num_entries;
+            const int64_t total = a.plan.cum[num_entries] * a.num_kv_heads;
+            const Share share(total, gridDim.x);
+            const int64_t first = share.start(blockIdx.x);
+            int64_t left = share.start(blockIdx.x + 1) - first;
+            int e = 0, h = 0;
+            int64_t off = 0;                 // into the item's cost
+            if (left > 0) {
+                e = warp_find(a.plan.cum, num_entries, first / a.num_kv_heads);
+                const int64_t in = first - a.plan.cum[e] * a.num_kv_heads;
+                const int cost = cost_of(a.plan.entries[e].tiles);
+                h = static_cast<int>(in / cost);
+                off = in - static_cast<int64_t>(h) * cost;
+            }
+            bool first_item = true;
+            Entry en;
+            int held = -1;
+            for (uint32_t k = 0;;) {
+                int t0 = 0, t1 = 0;
+                if (left > 0) {
+                    while (held != e) {
+                        const int4* p = reinterpret_cast<const int4*>(a.plan.entries + e);
+                        const int4 x = p[0], y = p[1];
+                        en = Entry{x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
+                        held = e;
+                        if (en.tiles == 0) ++e;   // rows that see nothing
+                    }
+                    const int64_t take = min(left, cost_of(en.tiles) - off);
+                    t0 = static_cast<int>(max(static_cast<int64_t>(0), off - kItemCost));
+                    t1 = static_cast<int>(max(static_cast<int64_t>(0), off + take - kItemCost));
+                    left -= take;
+                    off += take;
+                }
+                if (t1 > t0 || left <= 0) {
+                    SVQ_WAIT(ct->seg_empty[k % kSegs], ((k / kSegs) & 1) ^ 1, plan_end);
+                    if (lane == 0) {
+                        Seg& s = ct->seg[k % kSegs];
+                        s.en = en;
+                        s.h = h;
+                        s.t0 = t0;
+                        s.t1 = t1;
+                        s.slot = t0 == 0 && t1 == en.tiles ? -1 : static_cast<int>(blockIdx.x) * 2 + (first_item ? 0 : 1);
+                        mbar_arrive(smem_addr(&ct->seg_full[k % kSegs]));
+                    }
+                    ++k;
+                    if (t1 == t0) break;
+                }
+                first_item = false;
+                if (off == cost_of(en.tiles)) {
+                    off = 0;
+                    if (++h == a.num_kv_heads) {
+                        h = 0;
+                        ++e;
+                    }
+                }
+            }
+        plan_end:;
         } else if (warp < 12) {
             // ---------------- softmax: warps 4-7 stream 0, warps 8-11 stream 1
             reg_inc<C::kSoftmaxRegs>();
@@ -673,12 +695,8 @@ __global__ void __launch_bounds__(Cfg<FP8>::kThreads, 1)
             const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
             const uint32_t s_col = tmem + lanes + kColS + w * 128;
             const uint32_t o_col = tmem + lanes + kColO + w * 128;
-            Walk walk(a, ct, count);
-            Seg s, nx;
             uint32_t s_ph = 0, o_ph0 = 0, o_ph1 = 0, join_ph = 0;
             uint32_t tile0 = 0;          // key tiles of the CTA before the segment
-            bool more = walk.next(s);
-            bool first_seg = true;
             auto stream_tiles = [&](const Seg& g) {
                 const int n = g.t1 - g.t0;
                 return g.en.ntok * group > 128 ? n : (n - w + 1) / 2;
@@ -702,14 +720,20 @@ __global__ void __launch_bounds__(Cfg<FP8>::kThreads, 1)
                 fence_proxy_async_smem();
                 mbar_arrive(smem_addr(&ct->q_full[w]));
             };
-            if (more && stream_tiles(s) > 0) {
-                load_q(s);
-                q_ready();
-            }
-            while (more) {
-                const bool have_next = walk.next(nx);
-                const bool next_q = have_next && stream_tiles(nx) > 0;
+            for (uint32_t k = 0;; ++k) {
+                const Seg& s = ct->seg[k % kSegs];
+                if (k == 0) {
+                    SVQ_WAIT(ct->seg_full[0], 0, softmax_end);
+                    if (stream_tiles(s) > 0) {
+                        load_q(s);
+                        q_ready();
+                    }
+                }
                 const int n = s.t1 - s.t0;
+                if (n == 0) break;
+                SVQ_WAIT(ct->seg_full[(k + 1) % kSegs], ((k + 1) / kSegs) & 1, softmax_end);
+                const Seg& nx = ct->seg[(k + 1) % kSegs];
+                const bool next_q = stream_tiles(nx) > 0;
                 const int rows = s.en.ntok * group;
                 const bool two = rows > 128;
                 const int nt = stream_tiles(s);
@@ -727,16 +751,16 @@ __global__ void __launch_bounds__(Cfg<FP8>::kThreads, 1)
                     const int ti = two ? j : 2 * j + w;          // tile of the segment
                     const int i0 = (s.t0 + ti) * kTilePages;     // first page of the tile in the list
                     const int slot = (tile0 + ti) % kInfoSlots;
+                    const int base0 = logical_page(s.en, i0) * kPage, base7 = logical_page(s.en, i0 + 7) * kPage;
+                    bool plain = i0 + kTilePages <= s.en.npages && base7 - base0 == 7 * kPage && base7 + 15 <= qlo &&
+                                 (base0 > qhi - a.window || base7 + 15 < a.sink);
                     SVQ_WAIT(ct->s_full[w], s_ph, softmax_end);
                     s_ph ^= 1;
                     tc_fence_after();
                     if (j == nt - 1 && next_q) load_q(nx);       // the stream's last use of Q is over
                     if (warp_on) {
                         const int fault = ct->fault[slot];
-                        const int base0 = logical_page(s.en, i0) * kPage;
-                        const int base7 = logical_page(s.en, i0 + 7) * kPage;
-                        const bool plain = !fault && i0 + kTilePages <= s.en.npages && base7 - base0 == 7 * kPage &&
-                                           base7 + 15 <= qlo && (base0 > qhi - a.window || base7 + 15 < a.sink);
+                        plain = plain && !fault;
                         auto mask_of = [&](int c) {   // the 32 columns from 32 c on: two pages
                             uint32_t bits = 0;
 #pragma unroll
@@ -856,13 +880,12 @@ __global__ void __launch_bounds__(Cfg<FP8>::kThreads, 1)
                 if (next_q) q_ready();
 
                 // ---------------- the segment's end
-                const bool whole = s.t0 == 0 && s.t1 == s.tiles;
                 float* po = nullptr;        // this row's fp32 partial
                 float2* pml = nullptr;
                 const int hr = r - tok * group;
                 const int64_t qrow = static_cast<int64_t>(s.en.row0 + tok) * a.num_q_heads + s.h * group + hr;
-                if (!whole) {
-                    const int64_t at = static_cast<int64_t>(blockIdx.x * 2 + (first_seg ? 0 : 1)) * a.slot_rows + r;
+                if (s.slot >= 0) {
+                    const int64_t at = static_cast<int64_t>(s.slot) * a.slot_rows + r;
                     po = a.cut_o + at * kHeadDim;
                     pml = a.cut_ml + at;
                 } else if (a.whole_o) {
@@ -946,21 +969,20 @@ __global__ void __launch_bounds__(Cfg<FP8>::kThreads, 1)
                     join_ph ^= 1;
                 }
                 tile0 += n;
-                first_seg = false;
-                s = nx;
-                more = have_next;
+                seg_done(k);
             }
         softmax_end:;
         } else if (FP8 && warp >= 12) {
             // ---------------- e4m3 codes -> bf16 tiles in the MMAs' layout
             reg_dec<C::kOtherRegs>();
-            Walk walk(a, ct, count);
-            Seg s;
             const int tid = threadIdx.x - 384;
             uint32_t ld = 0, tile = 0;
             constexpr int kCodeDepth = FP8 ? C::kCodeStages : 1;
-            while (walk.next(s)) {
+            for (uint32_t k = 0;; ++k) {
+                SVQ_WAIT(ct->seg_full[k % kSegs], (k / kSegs) & 1, widen_end);
+                const Seg& s = ct->seg[k % kSegs];
                 const int n = s.t1 - s.t0;
+                if (n == 0) break;
                 const int qlo = s.en.pos0, qhi = last_pos(s.en);
                 for (int i = 0; i < 2 * n; ++i) {
                     const bool is_k = load_is_k(i, n);
@@ -1039,6 +1061,7 @@ __global__ void __launch_bounds__(Cfg<FP8>::kThreads, 1)
                     ++ld;
                 }
                 tile += n;
+                seg_done(k);
             }
         widen_end:;
         }
@@ -1222,7 +1245,8 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const __grid_constan
                 }
             }
         }
-        const int64_t before = base + block_scan(tiles_of(en.npages), warp_sums, total);
+        en.tiles = tiles_of(en.npages);
+        const int64_t before = base + block_scan(cost_of(en.tiles), warp_sums, total);
         base += total;
         if (e < n) {
             p.plan.entries[e] = en;
@@ -1244,16 +1268,23 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const __grid_constan
 }
 
 // ---------------------------------------------------------------- joining partials
-// The partials of an item that is cut, those of consecutive CTAs in tile order.
-__device__ __forceinline__ Pieces cut_pieces(const AttendArgs& a, const Share& share, int64_t begin, int64_t end, int r) {
+// An item's place in the shares: its cost begins at `begin`, its first tile
+// kItemCost later.
+struct Placed {
+    int64_t begin;
+    int tiles, c0, c1;   // the CTAs with its first and its last tile
+    __device__ __forceinline__ Placed(const Share& share, int64_t at, int n)
+        : begin(at), tiles(n), c0(share.cta_of(at + kItemCost)), c1(share.cta_of(at + kItemCost + n - 1)) {}
+};
+// The partials of row r of an item that is cut: one of each of its CTAs.
+__device__ __forceinline__ Pieces cut_pieces(const AttendArgs& a, const Share& share, const Placed& it, int r) {
     Pieces p;
-    const int c0 = share.cta_of(begin);
     p.o = a.cut_o;
     p.ml = a.cut_ml;
-    p.n = share.cta_of(end - 1) - c0 + 1;
+    p.n = it.c1 - it.c0 + 1;
     p.stride = 2ll * a.slot_rows;
-    p.first = (2ll * c0 + (begin == share.start(c0) ? 0 : 1)) * a.slot_rows + r;
-    p.second = 2ll * (c0 + 1) * a.slot_rows + r;
+    p.first = (2ll * it.c0 + (share.start(it.c0) >= it.begin ? 0 : 1)) * a.slot_rows + r;
+    p.second = 2ll * (it.c0 + 1) * a.slot_rows + r;
     return p;
 }
 
@@ -1269,14 +1300,13 @@ __global__ void __launch_bounds__(kJoinThreads) join_cut_kernel(const __grid_con
     if (x >= total) return;
     const int e = warp_find(a.plan.cum, n, x / a.num_kv_heads);
     const Entry en = a.plan.entries[e];
-    const int tiles = tiles_of(en.npages);
     const int64_t at = a.plan.cum[e] * a.num_kv_heads;
-    const int h = static_cast<int>((x - at) / tiles);
-    const int64_t begin = at + static_cast<int64_t>(h) * tiles;
-    if (begin == x || share.start(c - 1) > begin) return;
+    const int h = static_cast<int>((x - at) / cost_of(en.tiles));
+    const Placed it(share, at + static_cast<int64_t>(h) * cost_of(en.tiles), en.tiles);
+    if (c != it.c0 + 1) return;   // the item is not cut here, or was before
     const int rows = en.ntok * a.group;
     for (int r = blockIdx.y; r < rows; r += gridDim.y) {
-        const Pieces lists[2] = {cut_pieces(a, share, begin, begin + tiles, r), {}};
+        const Pieces lists[2] = {cut_pieces(a, share, it, r), {}};
         const int tok = r / a.group;
         const int64_t q = static_cast<int64_t>(en.row0 + tok) * a.num_q_heads + h * a.group + (r - tok * a.group);
         join_row(lists, 1, a.out + q * kHeadDim, a.lse + q);
@@ -1298,12 +1328,9 @@ __global__ void __launch_bounds__(kJoinThreads) join_prefix_kernel(const __grid_
         const Share share(total, ctas);
         const int h = hq / a.group, hr = hq - h * a.group;
         const Entry en = a.plan.entries[pre];
-        const int tiles = tiles_of(en.npages);
-        const int64_t begin = a.plan.cum[pre] * a.num_kv_heads + static_cast<int64_t>(h) * tiles;
-        if (share.cta_of(begin) == share.cta_of(begin + tiles - 1))
-            lists[nl++] = Pieces{a.whole_o, a.whole_ml, q, q, 0, 1};
-        else
-            lists[nl++] = cut_pieces(a, share, begin, begin + tiles, (b - en.row0) * a.group + hr);
+        const Placed it(share, a.plan.cum[pre] * a.num_kv_heads + static_cast<int64_t>(h) * cost_of(en.tiles), en.tiles);
+        if (it.c0 == it.c1) lists[nl++] = Pieces{a.whole_o, a.whole_ml, q, q, 0, 1};
+        else lists[nl++] = cut_pieces(a, share, it, (b - en.row0) * a.group + hr);
     }
     lists[nl++] = Pieces{a.split_o, a.split_ml, q * a.splits, q * a.splits + 1, 1, a.splits};
     join_row(lists, nl, a.out + q * kHeadDim, a.lse + q);
