@@ -27,7 +27,7 @@
 //   warp 1       issues the MMAs (one thread)
 //   warps 4-7    softmax of stream 0, one row a thread
 //   warps 8-11   softmax of stream 1
-//   warps 12-15  (e4m3 pools) widen the codes to bf16 tiles
+//   warps 12-19  (e4m3 pools) widen the codes to bf16 tiles
 // Two streams keep the tensor cores busy while the other's softmax runs: the
 // two 128-row halves of a tile of more than 128 rows, each over every key
 // tile; or, for up to 128 rows, the even and the odd key tiles of the same
@@ -262,16 +262,17 @@ template <bool FP8>
 struct Cfg {
     static constexpr int kStages = FP8 ? 3 : 5;
     static constexpr int kCodeStages = FP8 ? 3 : 0;             // 16 KB of e4m3 codes each
-    static constexpr int kThreads = FP8 ? 512 : 384;
+    static constexpr int kWiden = FP8 ? 8 : 0;                  // widening warps
+    static constexpr int kThreads = 384 + 32 * kWiden;
     static constexpr int kRing = kStages * kStageBytes;
     static constexpr int kQ = 2 * 128 * kHeadDim * 2;           // one 128-row tile a stream
     static constexpr int kCodes = kCodeStages * kTileTok * kHeadDim;
     static constexpr int kScales = FP8 ? kInfoSlots * 2 * kTileTok * 4 : 0;
     static constexpr int kControl = 3072;
-    // Registers a thread after the start (the block is launched with 168 or 128 for each):
-    // 128 x 88 + 256 x 208 = 384 x 168; 256 x 80 + 256 x 176 = 512 x 128.
-    static constexpr int kOtherRegs = FP8 ? 80 : 88;
-    static constexpr int kSoftmaxRegs = FP8 ? 176 : 208;
+    // Registers a thread after the start (the block is launched with 168 or 96 for each):
+    // 128 x 88 + 256 x 208 = 384 x 168; 384 x 72 + 256 x 128 < 640 x 96.
+    static constexpr int kOtherRegs = FP8 ? 72 : 88;
+    static constexpr int kSoftmaxRegs = FP8 ? 128 : 208;
     static constexpr int kSmem = kRing + kQ + kCodes + kScales + kControl;
 };
 static_assert(Cfg<false>::kSmem <= 227 * 1024 && Cfg<true>::kSmem <= 227 * 1024, "shared memory of one CTA");
@@ -385,12 +386,12 @@ __global__ void __launch_bounds__(Cfg<FP8>::kThreads, 1)
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < C::kStages; ++i) {
-            mbar_init(smem_addr(&ct->full[i]), FP8 ? 4 : 1);
+            mbar_init(smem_addr(&ct->full[i]), FP8 ? C::kWiden : 1);
             mbar_init(smem_addr(&ct->empty[i]), 1);
         }
         for (int i = 0; i < C::kCodeStages; ++i) {
             mbar_init(smem_addr(&ct->code_full[i]), 1);
-            mbar_init(smem_addr(&ct->code_empty[i]), 4);
+            mbar_init(smem_addr(&ct->code_empty[i]), C::kWiden);
         }
         for (int w = 0; w < 2; ++w) {
             mbar_init(smem_addr(&ct->s_full[w]), 1);
@@ -400,7 +401,7 @@ __global__ void __launch_bounds__(Cfg<FP8>::kThreads, 1)
         }
         for (int i = 0; i < kSegs; ++i) {
             mbar_init(smem_addr(&ct->seg_full[i]), 1);
-            mbar_init(smem_addr(&ct->seg_empty[i]), 3 + 8 + (FP8 ? 4 : 0));   // loads, MMAs, softmax, widening warps
+            mbar_init(smem_addr(&ct->seg_empty[i]), 3 + 8 + C::kWiden);   // loads, MMAs, softmax, widening warps
         }
         mbar_init(smem_addr(&ct->join[0]), 256);
         mbar_init(smem_addr(&ct->join[1]), 256);
@@ -994,8 +995,9 @@ __global__ void __launch_bounds__(Cfg<FP8>::kThreads, 1)
                     const unsigned char* src = codes + cs * (kTileTok * kHeadDim);
                     unsigned char* dst = ring + st * kStageBytes;
                     const int i0 = (s.t0 + t) * kTilePages;
-                    // Page k of the tile: thread -> row tid / 8, 16 codes at chunk tid % 8.
-                    const int r = tid >> 3, c = tid & 7;
+                    // Page k of the tile, every second one here: thread -> row tid / 8 % 16, 16 codes
+                    // at chunk tid % 8.
+                    const int r = (tid >> 3) & 15, c = tid & 7, odd = tid >> 7;
                     // Tokens no row sees may hold anything: they become zeros, scales too.  Bit k:
                     // this thread's token of page k is seen; `clean`: every token of the tile is.
                     const int base0 = logical_page(s.en, i0) * kPage, base7 = logical_page(s.en, i0 + 7) * kPage;
@@ -1013,13 +1015,13 @@ __global__ void __launch_bounds__(Cfg<FP8>::kThreads, 1)
                     unsigned char* const o = dst + (r >> 3) * 2048 + (c >> 2) * 1024 + (r & 7) * 128;
                     const int at0 = ((2 * c) & 7 ^ (r & 7)) << 4, at1 = ((2 * c + 1) & 7 ^ (r & 7)) << 4;
 #pragma unroll 1
-                    for (int k0 = 0; k0 < 8; k0 += 2) {
+                    for (int k0 = odd; k0 < 8; k0 += 4) {
                         uint4 v[2], lo[2], hi[2];
                         uint32_t nan = 0;
 #pragma unroll
                         for (int u = 0; u < 2; ++u) {
-                            v[u] = *reinterpret_cast<const uint4*>(src + (k0 + u) * (kPage * kHeadDim) + r * kHeadDim + c * 16);
-                            if (!((on >> (k0 + u)) & 1u)) v[u] = make_uint4(0u, 0u, 0u, 0u);
+                            v[u] = *reinterpret_cast<const uint4*>(src + (k0 + 2 * u) * (kPage * kHeadDim) + r * kHeadDim + c * 16);
+                            if (!((on >> (k0 + 2 * u)) & 1u)) v[u] = make_uint4(0u, 0u, 0u, 0u);
                         }
 #pragma unroll
                         for (int u = 0; u < 2; ++u) {
@@ -1040,13 +1042,12 @@ __global__ void __launch_bounds__(Cfg<FP8>::kThreads, 1)
                         }
 #pragma unroll
                         for (int u = 0; u < 2; ++u) {
-                            *reinterpret_cast<uint4*>(o + (k0 + u) * kPageBytes + at0) = lo[u];
-                            *reinterpret_cast<uint4*>(o + (k0 + u) * kPageBytes + at1) = hi[u];
+                            *reinterpret_cast<uint4*>(o + (k0 + 2 * u) * kPageBytes + at0) = lo[u];
+                            *reinterpret_cast<uint4*>(o + (k0 + 2 * u) * kPageBytes + at1) = hi[u];
                         }
                     }
                     if (is_k && c == 0 && on != 0xffu) {
-#pragma unroll
-                        for (int k = 0; k < 8; ++k)
+                        for (int k = odd; k < 8; k += 2)
                             if (!((on >> k) & 1u)) {
                                 scales[slot * 2 * kTileTok + k * kPage + r] = 0.f;
                                 scales[slot * 2 * kTileTok + kTileTok + k * kPage + r] = 0.f;
@@ -1305,11 +1306,18 @@ __global__ void __launch_bounds__(kJoinThreads) join_cut_kernel(const __grid_con
     const Placed it(share, at + static_cast<int64_t>(h) * cost_of(en.tiles), en.tiles);
     if (c != it.c0 + 1) return;   // the item is not cut here, or was before
     const int rows = en.ntok * a.group;
+    auto at_row = [&](int r) {
+        const int tok = r / a.group;
+        return static_cast<int64_t>(en.row0 + tok) * a.num_q_heads + h * a.group + (r - tok * a.group);
+    };
+    if (it.c1 - it.c0 < 8) {   // few pieces: a warp a row
+        for (int r = blockIdx.y * (kJoinThreads / 32) + (threadIdx.x >> 5); r < rows; r += gridDim.y * (kJoinThreads / 32))
+            join_row_warp(cut_pieces(a, share, it, r), a.out + at_row(r) * kHeadDim, a.lse + at_row(r));
+        return;
+    }
     for (int r = blockIdx.y; r < rows; r += gridDim.y) {
         const Pieces lists[2] = {cut_pieces(a, share, it, r), {}};
-        const int tok = r / a.group;
-        const int64_t q = static_cast<int64_t>(en.row0 + tok) * a.num_q_heads + h * a.group + (r - tok * a.group);
-        join_row(lists, 1, a.out + q * kHeadDim, a.lse + q);
+        join_row(lists, 1, a.out + at_row(r) * kHeadDim, a.lse + at_row(r));
     }
 }
 

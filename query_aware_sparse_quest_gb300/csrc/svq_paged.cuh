@@ -63,28 +63,20 @@ struct Pieces {
     __device__ __forceinline__ int64_t row(int k) const { return k == 0 ? first : second + (k - 1) * stride; }
 };
 
-constexpr int kJoinThreads = 128;
-
-// One row by the whole CTA: warps take pieces in turn, lane l channels 4 l .. 4 l + 3.
-__device__ __forceinline__ void join_row(const Pieces (&lists)[2], int nlists, __nv_bfloat16* out, float* lse) {
-    __shared__ float4 sm_o[kJoinThreads / 32][32];
-    __shared__ float2 sm_ml[kJoinThreads / 32];
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    constexpr int kWarps = kJoinThreads / 32;
+// A row's running (base, sum, four channels of the output) and the pieces
+// k, k + step, ... of a list, four at a time.
+struct RowSum {
     float m = -INFINITY, l = 0.f;
-    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-    int k0 = warp;
-    for (int li = 0; li < nlists; ++li) {
-        const Pieces& p = lists[li];
-        int k = k0;
-        for (; k < p.n; k += 4 * kWarps) {
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+    __device__ __forceinline__ void add(const Pieces& p, int k, int step, int lane) {
+        for (; k < p.n; k += 4 * step) {
             float2 ml[4];
-            float4 o[4];
+            float4 x[4];
 #pragma unroll
             for (int u = 0; u < 4; ++u) {
-                const int j = k + u * kWarps;
+                const int j = k + u * step;
                 ml[u] = j < p.n ? p.ml[p.row(j)] : make_float2(-INFINITY, 0.f);
-                o[u] = j < p.n ? *reinterpret_cast<const float4*>(p.o + p.row(j) * kHeadDim + 4 * lane)
+                x[u] = j < p.n ? *reinterpret_cast<const float4*>(p.o + p.row(j) * kHeadDim + 4 * lane)
                                : make_float4(0.f, 0.f, 0.f, 0.f);
             }
             float mn = m;
@@ -93,47 +85,68 @@ __device__ __forceinline__ void join_row(const Pieces (&lists)[2], int nlists, _
             const float base = mn == -INFINITY ? 0.f : mn;   // pieces without a visible token: weights 0
             const float e = ex2(m - base);
             l *= e;
-            acc.x *= e;
-            acc.y *= e;
-            acc.z *= e;
-            acc.w *= e;
+            o.x *= e, o.y *= e, o.z *= e, o.w *= e;
             m = mn;
 #pragma unroll
             for (int u = 0; u < 4; ++u) {
                 const float f = ex2(ml[u].x - base);
                 l += ml[u].y * f;
-                acc.x += o[u].x * f;
-                acc.y += o[u].y * f;
-                acc.z += o[u].z * f;
-                acc.w += o[u].w * f;
+                o.x += x[u].x * f;
+                o.y += x[u].y * f;
+                o.z += x[u].z * f;
+                o.w += x[u].w * f;
             }
         }
-        k0 = (k0 + kWarps - p.n % kWarps) % kWarps;   // the next list goes on where this one ended
     }
-    sm_o[warp][lane] = acc;
-    if (lane == 0) sm_ml[warp] = make_float2(m, l);
-    __syncthreads();
-    if (warp == 0) {
-        float M = -INFINITY;
-#pragma unroll
-        for (int u = 0; u < kWarps; ++u) M = fmaxf(M, sm_ml[u].x);
-        float L = 0.f;
-        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-        for (int u = 0; u < kWarps; ++u) {
-            const float f = ex2(sm_ml[u].x - (M == -INFINITY ? 0.f : M));
-            L += sm_ml[u].y * f;
-            o.x += sm_o[u][lane].x * f;
-            o.y += sm_o[u][lane].y * f;
-            o.z += sm_o[u][lane].z * f;
-            o.w += sm_o[u][lane].w * f;
-        }
-        const float inv = L > 0.f ? 1.f / L : (L == 0.f ? 0.f : L);
+    __device__ __forceinline__ void write(__nv_bfloat16* out, float* lse, int lane) const {
+        const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);
         uint2 v;
         v.x = pack_bf16x2(o.x * inv, o.y * inv);
         v.y = pack_bf16x2(o.z * inv, o.w * inv);
         *reinterpret_cast<uint2*>(out + 4 * lane) = v;
-        if (lane == 0) *lse = L > 0.f ? (M + log2f(L)) * 0.69314718055994531f : (L == 0.f ? -INFINITY : L);
+        if (lane == 0) *lse = l > 0.f ? (m + log2f(l)) * 0.69314718055994531f : (l == 0.f ? -INFINITY : l);
+    }
+};
+
+constexpr int kJoinThreads = 128;
+
+// One row by a warp, lane l channels 4 l .. 4 l + 3.
+__device__ __forceinline__ void join_row_warp(const Pieces& p, __nv_bfloat16* out, float* lse) {
+    const int lane = threadIdx.x & 31;
+    RowSum s;
+    s.add(p, 0, 1, lane);
+    s.write(out, lse, lane);
+}
+
+// One row by the whole CTA: the warps take the pieces in turn.
+__device__ __forceinline__ void join_row(const Pieces (&lists)[2], int nlists, __nv_bfloat16* out, float* lse) {
+    constexpr int kWarps = kJoinThreads / 32;
+    __shared__ float4 sm_o[kWarps][32];
+    __shared__ float2 sm_ml[kWarps];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    RowSum s;
+    int k0 = warp;
+    for (int li = 0; li < nlists; ++li) {
+        s.add(lists[li], k0, kWarps, lane);
+        k0 = (k0 + kWarps - lists[li].n % kWarps) % kWarps;   // the next list goes on where this one ended
+    }
+    sm_o[warp][lane] = s.o;
+    if (lane == 0) sm_ml[warp] = make_float2(s.m, s.l);
+    __syncthreads();
+    if (warp == 0) {
+        RowSum t;
+#pragma unroll
+        for (int u = 0; u < kWarps; ++u) t.m = fmaxf(t.m, sm_ml[u].x);
+#pragma unroll
+        for (int u = 0; u < kWarps; ++u) {
+            const float f = ex2(sm_ml[u].x - (t.m == -INFINITY ? 0.f : t.m));
+            t.l += sm_ml[u].y * f;
+            t.o.x += sm_o[u][lane].x * f;
+            t.o.y += sm_o[u][lane].y * f;
+            t.o.z += sm_o[u][lane].z * f;
+            t.o.w += sm_o[u][lane].w * f;
+        }
+        t.write(out, lse, lane);
     }
     __syncthreads();   // the shared arrays are written again for the next row
 }
