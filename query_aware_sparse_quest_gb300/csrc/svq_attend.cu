@@ -44,8 +44,8 @@ int window_decode_splits(bool fp8, int batch, int num_kv_heads, int64_t pages, i
 int64_t window_decode_rows(int batch, int num_q_heads, int num_kv_heads);
 int launch_window_decode(const sv_cache* c, const void* q, int num_q_heads, const int32_t* page_table,
                          const int32_t* seq_lens, int batch, int max_pages, int window, int sink,
-                         const int32_t* first_page, float softmax_scale, int splits, float* o_part, float2* ml_part,
-                         cudaStream_t stream);
+                         const int32_t* group_start, const int32_t* shared_pages, int num_groups, float softmax_scale,
+                         int splits, float* o_part, float2* ml_part, cudaStream_t stream);
 int launch_join_splits(const float* o_part, const float2* ml_part, int splits, int64_t rows, void* out, float* lse,
                        cudaStream_t stream);
 
@@ -89,7 +89,6 @@ struct Plan {
     int* num_entries;
     int* req_offset;   // first entry of each request (chunks) or group (prefixes)
     int* req_entry;    // prefixes: entry that holds each request's rows, -1: none, -2: the request is not touched
-    int* first_page;   // prefixes: each request's first page behind the prefix, -1: none is read
 };
 
 struct AttendArgs {
@@ -417,7 +416,9 @@ __global__ void __launch_bounds__(Cfg<FP8>::kThreads, 1)
                      : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
     }
-    pdl_wait();   // the plan comes from the kernel launched just before
+    // The plan comes from the kernel launched just before; or (prefixes) from the one before that,
+    // which that one has waited for before it let this one start, and this one reads nothing of its.
+    if (!a.whole_o) pdl_wait();
     pdl_launch_dependents();
     tc_fence_before();
     __syncthreads();
@@ -762,16 +763,24 @@ __global__ void __launch_bounds__(Cfg<FP8>::kThreads, 1)
                     if (warp_on) {
                         const int fault = ct->fault[slot];
                         plain = plain && !fault;
-                        auto mask_of = [&](int c) {   // the 32 columns from 32 c on: two pages
-                            uint32_t bits = 0;
+                        // Visible columns, 32 a word (two pages).
+                        uint32_t bits0 = ~0u, bits1 = ~0u, bits2 = ~0u, bits3 = ~0u;
+                        if (!plain) {
+                            auto two_pages = [&](int c) {
+                                uint32_t bits = 0;
 #pragma unroll
-                            for (int u = 0; u < 2; ++u) {
-                                const int i = i0 + 2 * c + u;
-                                if (i < s.en.npages && !((fault >> (2 * c + u)) & 1))
-                                    bits |= page_mask(logical_page(s.en, i) * kPage, qpos, a.window, a.sink) << (16 * u);
-                            }
-                            return bits;
-                        };
+                                for (int u = 0; u < 2; ++u) {
+                                    const int i = i0 + 2 * c + u;
+                                    if (i < s.en.npages && !((fault >> (2 * c + u)) & 1))
+                                        bits |= page_mask(logical_page(s.en, i) * kPage, qpos, a.window, a.sink) << (16 * u);
+                                }
+                                return bits;
+                            };
+                            bits0 = two_pages(0);
+                            bits1 = two_pages(1);
+                            bits2 = two_pages(2);
+                            bits3 = two_pages(3);
+                        }
                         const float4* ks = reinterpret_cast<const float4*>(scales + slot * 2 * kTileTok);
                         const float2* vs = reinterpret_cast<const float2*>(ks + kTileTok / 4);
                         // Pass 1: the tile's maximum.  Both passes are rolled loops over 32 columns
@@ -794,7 +803,7 @@ __global__ void __launch_bounds__(Cfg<FP8>::kThreads, 1)
                                 }
                             }
                             if (!plain) {
-                                const uint32_t bits = mask_of(c);
+                                const uint32_t bits = c == 0 ? bits0 : (c == 1 ? bits1 : (c == 2 ? bits2 : bits3));
 #pragma unroll
                                 for (int u = 0; u < 32; ++u)
                                     if (!((bits >> u) & 1u)) x[u] = -INFINITY;
@@ -845,7 +854,7 @@ __global__ void __launch_bounds__(Cfg<FP8>::kThreads, 1)
                                 }
                             }
                             if (!plain) {
-                                const uint32_t bits = mask_of(c);
+                                const uint32_t bits = c == 0 ? bits0 : (c == 1 ? bits1 : (c == 2 ? bits2 : bits3));
 #pragma unroll
                                 for (int u = 0; u < 32; ++u)
                                     if (!((bits >> u) & 1u)) x[u] = -INFINITY;
@@ -922,7 +931,7 @@ __global__ void __launch_bounds__(Cfg<FP8>::kThreads, 1)
                     f0 *= inv;
                     f1 *= inv;
                     // Two halves: the whole row of the own stream.  Joined: 64 channels of both.
-#pragma unroll
+#pragma unroll 1
                     for (int c = 0; c < 4; ++c) {
                         if (!two && (c >> 1) != w) continue;
                         uint32_t x[32];
@@ -973,7 +982,7 @@ __global__ void __launch_bounds__(Cfg<FP8>::kThreads, 1)
                 seg_done(k);
             }
         softmax_end:;
-        } else if (FP8 && warp >= 12) {
+        } else if (FP8) {
             // ---------------- e4m3 codes -> bf16 tiles in the MMAs' layout
             reg_dec<C::kOtherRegs>();
             const int tid = threadIdx.x - 384;
@@ -1068,6 +1077,7 @@ __global__ void __launch_bounds__(Cfg<FP8>::kThreads, 1)
         }
     }
     __syncthreads();
+    if (a.whole_o) pdl_wait();   // this kernel ends after the one before it
     if (warp == 1)
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem));
 }
@@ -1121,17 +1131,6 @@ __device__ __forceinline__ int64_t block_scan(int64_t v, int64_t* warp_sums, int
     return before + x - v;
 }
 
-// Largest i in [0, n) with a[i] <= v (a non-decreasing, a[0] <= v).
-__device__ __forceinline__ int find_le(const int32_t* a, int n, int v) {
-    int lo = 0, hi = n;
-    while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if (a[mid] <= v) lo = mid;
-        else hi = mid;
-    }
-    return lo;
-}
-
 // Pages of request b, checked: 0 for a length the page table cannot hold.
 __device__ __forceinline__ int checked_len(const PlanArgs& p, int b) {
     const int len = p.seq_lens[b];
@@ -1183,27 +1182,14 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const __grid_constan
     const int n = rows_entries;
     if (PREFIX) {
         for (int b = tid; b < p.batch; b += kPlanThreads) {
-            int pre = -2, page = -1;
-            if (p.group_start[0] <= b && b < p.group_start[p.num_groups]) {
-                const int g = find_le(p.group_start, p.num_groups, b);
-                const int a = p.group_start[g], end = p.group_start[g + 1];
-                const int sp = p.shared_pages[g];
-                pre = -1;
-                if (a < 0 || a > b || b >= end || end > p.batch || sp < 0 || sp > p.max_pages) {
-                    svq_flag(SV_DEVERR_GROUP);
-                } else {
-                    const int len = checked_len(p, b);
-                    if (len < sp * kPage) {
-                        if (len > 0) svq_flag(SV_DEVERR_GROUP);
-                    } else if (len > 0) {
-                        const int pe = p.plan.req_offset[g] + (b - a) / p.tok_per_entry;
-                        if (sp > 0 && pe < n) pre = pe;
-                        page = sp;
-                    }
-                }
+            const Grouped r = grouped(p.group_start, p.shared_pages, p.num_groups, p.batch, p.max_pages, b, p.seq_lens[b]);
+            if (r.fault) svq_flag(r.fault);
+            int pre = r.page == kNotTouched ? -2 : -1;
+            if (r.page > 0) {
+                const int pe = p.plan.req_offset[r.group] + (b - p.group_start[r.group]) / p.tok_per_entry;
+                if (pe < n) pre = pe;
             }
             p.plan.req_entry[b] = pre;
-            p.plan.first_page[b] = page;
         }
     }
     int64_t base = 0;
@@ -1348,7 +1334,7 @@ __global__ void __launch_bounds__(kJoinThreads) join_prefix_kernel(const __grid_
 size_t up(size_t n) { return (n + 255) / 256 * 256; }
 
 struct Layout {
-    size_t entries, cum, num, req_offset, req_entry, first_page, cut_o, cut_ml, whole_o, whole_ml, split_o, split_ml, total;
+    size_t entries, cum, num, req_offset, req_entry, cut_o, cut_ml, whole_o, whole_ml, split_o, split_ml, total;
     int max_entries, slot_rows;
     // owners: requests (chunks) or groups (prefixes); rows: query tokens
     Layout(int64_t batch, int64_t owners, int64_t rows, int num_q_heads, int num_kv_heads, bool prefix) {
@@ -1367,7 +1353,6 @@ struct Layout {
         const size_t b = prefix ? batch : 0, heads = b * num_q_heads;
         const size_t parts = prefix ? window_decode_rows(batch, num_q_heads, num_kv_heads) : 0;
         req_entry = take(b * sizeof(int));
-        first_page = take(b * sizeof(int));
         whole_o = take(heads * kHeadDim * sizeof(float));
         whole_ml = take(heads * sizeof(float2));
         split_o = take(parts * kHeadDim * sizeof(float));
@@ -1413,7 +1398,6 @@ void fill_args(const sv_cache* c, const void* q, int num_q_heads, const int32_t*
     a.plan.num_entries = reinterpret_cast<int*>(ws + lay.num);
     a.plan.req_offset = reinterpret_cast<int*>(ws + lay.req_offset);
     a.plan.req_entry = reinterpret_cast<int*>(ws + lay.req_entry);
-    a.plan.first_page = reinterpret_cast<int*>(ws + lay.first_page);
     a.window = window > 0 ? window : INT_MAX;
     a.sink = sink;
     a.scale_log2 = softmax_scale * 1.4426950408889634f;
@@ -1472,7 +1456,7 @@ int launch_window(const sv_cache* c, const void* q, int num_q_heads, const int32
         float* o = static_cast<float*>(workspace);
         float2* ml = reinterpret_cast<float2*>(static_cast<unsigned char*>(workspace) + up(heads * splits * kHeadDim * sizeof(float)));
         const int st = launch_window_decode(c, q, num_q_heads, page_table, seq_lens, batch, max_pages, window, sink, nullptr,
-                                            softmax_scale, splits, o, ml, stream);
+                                            nullptr, 0, softmax_scale, splits, o, ml, stream);
         return st ? st : launch_join_splits(o, ml, splits, heads, out, lse, stream);
     }
     const Layout lay(batch, batch, total_q, num_q_heads, c->num_kv_heads, false);
@@ -1511,8 +1495,8 @@ int launch_prefix(const sv_cache* c, const void* q, int num_q_heads, const int32
     a.split_ml = reinterpret_cast<float2*>(ws + lay.split_ml);
     a.splits = window_decode_splits(c->kv_format == SV_KV_FP8_E4M3, batch, c->num_kv_heads, max_pages, ctas);
     if (launch_pdl(plan_kernel<true>, dim3(1), dim3(kPlanThreads), 0, stream, p) != cudaSuccess) return SV_ERR_CUDA;
-    int st = launch_window_decode(c, q, num_q_heads, page_table, seq_lens, batch, max_pages, 0, 0, a.plan.first_page,
-                                  softmax_scale, a.splits, a.split_o, a.split_ml, stream);
+    int st = launch_window_decode(c, q, num_q_heads, page_table, seq_lens, batch, max_pages, 0, 0, group_start,
+                                  shared_pages, num_groups, softmax_scale, a.splits, a.split_o, a.split_ml, stream);
     if (st) return st;
     if ((st = launch_tiles(c, a, ctas, stream))) return st;
     return launch_pdl(join_prefix_kernel, dim3(static_cast<unsigned>(batch) * num_q_heads), dim3(kJoinThreads), 0, stream,

@@ -32,6 +32,39 @@ __device__ __forceinline__ uint32_t page_mask(int base, int qpos, int window, in
 // First page of a window that begins at token `lo`, and the sink pages before it.
 __device__ __forceinline__ int sink_pages_of(int sink, int w0) { return min(w0, sink / kPage + (sink % kPage != 0)); }
 
+// Largest i in [0, n) with a[i] <= v (a non-decreasing, a[0] <= v).
+__device__ __forceinline__ int find_le(const int32_t* a, int n, int v) {
+    int lo = 0, hi = n;
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (a[mid] <= v) lo = mid;
+        else hi = mid;
+    }
+    return lo;
+}
+
+// Request b of a batch in groups that share their first pages: its group, and
+// the first page behind those, or kNothing (no token, or invalid, with the
+// error bit) or kNotTouched (behind the last group).
+constexpr int kNothing = -1, kNotTouched = -2;
+struct Grouped {
+    int group, page;
+    uint32_t fault;
+};
+__device__ __forceinline__ Grouped grouped(const int32_t* group_start, const int32_t* shared_pages, int num_groups, int batch,
+                                           int max_pages, int b, int len) {
+    Grouped r = {0, kNotTouched, 0u};
+    if (b < group_start[0] || b >= group_start[num_groups]) return r;
+    r.page = kNothing;
+    r.group = find_le(group_start, num_groups, b);
+    const int a = group_start[r.group], end = group_start[r.group + 1], sp = shared_pages[r.group];
+    if (a < 0 || a > b || b >= end || end > batch || sp < 0 || sp > max_pages) r.fault = SV_DEVERR_GROUP;
+    else if (len < 0 || (static_cast<int64_t>(len) + kPage - 1) / kPage > max_pages) r.fault = SV_DEVERR_SEQ_LEN;
+    else if (len < sp * kPage) r.fault = len ? SV_DEVERR_GROUP : 0u;
+    else if (len > 0) r.page = sp;
+    return r;
+}
+
 // The K or V pool bf16 [pages][kv heads][16][128] as a 4-D tensor: 64 channels,
 // 8 rows (256 bytes apart), 2 channel halves (128 bytes apart), groups of 8
 // rows (2 KB apart).  A box of 64 x 8 x 2 x 2 is one page's tile of one kv head
