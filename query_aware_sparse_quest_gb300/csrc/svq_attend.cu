@@ -13,8 +13,9 @@
 // bases are fp32.  P is rounded to bf16 because one MMA takes both operands in
 // one type and V is bf16; the sum is taken of the unrounded weights.
 //
-// Work.  The plan lists entries (row tiles with their page ranges) and the
-// running count of 128-token tiles.  Every CTA takes an equal run of the
+// Work.  An entry is a row tile with its page range: a plan kernel lists those
+// of chunks, those of prefixes follow from the groups.  Every CTA takes an
+// equal run of the
 // (entry, kv head, tile) sequence, so ragged batches, short windows and long
 // contexts all fill the GPU without a choice of splits; a run that starts or
 // ends inside an item leaves a partial (O, base, sum) in the workspace, joined
@@ -87,8 +88,7 @@ struct Plan {
     Entry* entries;
     int64_t* cum;      // [E + 1] cost per kv head of the entries before each
     int* num_entries;
-    int* req_offset;   // first entry of each request (chunks) or group (prefixes)
-    int* req_entry;    // prefixes: entry that holds each request's rows, -1: none, -2: the request is not touched
+    int* req_offset;   // first entry of each request
 };
 
 struct AttendArgs {
@@ -101,7 +101,10 @@ struct AttendArgs {
     const unsigned char* v_pool;
     const float* k_scale;
     const float* v_scale;
-    Plan plan;
+    Plan plan;         // chunks
+    Groups groups;     // prefixes
+    int tok_per_entry; // query tokens of a row tile: kRowTile / group
+    const int32_t* seq_lens;   // prefixes
     int window;        // INT_MAX: none
     int sink;
     float scale_log2;  // softmax_scale * log2(e)
@@ -142,6 +145,69 @@ __device__ __forceinline__ int warp_find(const int64_t* cum, int n, int64_t u) {
         lo = nlo;
     }
     return lo;
+}
+
+// Prefixes: a group has `entries` row tiles of `tiles` key tiles each.  Groups
+// are sound only in ascending order (none begins before a sound one ends), so
+// that no row is in two of them.
+struct GroupAt {
+    int g, a, entries, tiles;
+    int64_t before;   // cost per kv head of the groups before it
+};
+// By the whole warp, 32 groups a round: the sum of the groups' costs per kv
+// head, and the group for which pick(a, end, before, cost) holds, if any (g < 0).
+template <typename F>
+__device__ __forceinline__ GroupAt warp_groups(const Groups& gr, int tok_per_entry, int64_t& total, bool report, F&& pick) {
+    const int lane = threadIdx.x & 31;
+    GroupAt found = {-1, 0, 0, 0, 0};
+    total = 0;
+    int reach = 0;   // where the sound groups so far end
+    for (int g0 = 0; g0 < gr.n; g0 += 32) {
+        const int g = g0 + lane;
+        int a = 0, end = 0, sp = 0;
+        bool ok = false;
+        if (g < gr.n) {
+            a = gr.start[g];
+            end = gr.start[g + 1];
+            sp = gr.pages[g];
+            ok = gr.sound(a, end, sp);
+        }
+        // The largest end of the sound groups before (an unsound one by order does not count).
+        for (int round = 0; round < 32; ++round) {
+            int far = ok ? end : 0;
+#pragma unroll
+            for (int d = 1; d < 32; d <<= 1) {
+                const int y = __shfl_up_sync(0xffffffffu, far, d);
+                if (lane >= d) far = max(far, y);
+            }
+            int prev = __shfl_up_sync(0xffffffffu, far, 1);
+            if (lane == 0) prev = 0;
+            const uint32_t out = __ballot_sync(0xffffffffu, ok && a < max(prev, reach));
+            if (!out) {
+                reach = max(reach, __shfl_sync(0xffffffffu, far, 31));
+                break;
+            }
+            if (lane == __ffs(out) - 1) ok = false;   // the first one out of order may have hidden others
+        }
+        if (report && g < gr.n && !ok) svq_flag(SV_DEVERR_GROUP);
+        const int entries = ok && sp > 0 ? (end - a + tok_per_entry - 1) / tok_per_entry : 0;
+        const int64_t cost = static_cast<int64_t>(entries) * cost_of(tiles_of(sp));
+        int64_t x = cost;
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+            const int64_t y = __shfl_up_sync(0xffffffffu, x, d);
+            if (lane >= d) x += y;
+        }
+        const int64_t before = total + x - cost;
+        const uint32_t hit = __ballot_sync(0xffffffffu, ok && pick(a, end, before, cost));
+        if (hit && found.g < 0) {
+            const int src = __ffs(hit) - 1;
+            found = {g0 + src, __shfl_sync(0xffffffffu, a, src), __shfl_sync(0xffffffffu, entries, src),
+                     __shfl_sync(0xffffffffu, tiles_of(sp), src), __shfl_sync(0xffffffffu, before, src)};
+        }
+        total += __shfl_sync(0xffffffffu, x, 31);
+    }
+    return found;
 }
 
 // ---------------------------------------------------------------- tcgen05
@@ -416,9 +482,10 @@ __global__ void __launch_bounds__(Cfg<FP8>::kThreads, 1)
                      : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
     }
-    // The plan comes from the kernel launched just before; or (prefixes) from the one before that,
-    // which that one has waited for before it let this one start, and this one reads nothing of its.
-    if (!a.whole_o) pdl_wait();
+    // Chunks: the plan comes from the kernel launched just before.  Prefixes: this kernel shares
+    // nothing with the one before (the parts behind the prefix), which let it start only after what
+    // came before both had ended; it waits for that one at its end.
+    if (!a.groups.start) pdl_wait();
     pdl_launch_dependents();
     tc_fence_before();
     __syncthreads();
@@ -632,17 +699,37 @@ __global__ void __launch_bounds__(Cfg<FP8>::kThreads, 1)
         } else if (warp == 2) {
             // ---------------- the CTA's share of the plan, segment by segment
             reg_dec<C::kOtherRegs>();
-            const int num_entries = *a.plan.num_entries;
-            const int64_t total = a.plan.cum[num_entries] * a.num_kv_heads;
-            const Share share(total, gridDim.x);
+            const bool prefix = a.groups.start != nullptr;
+            int num_entries = 0;
+            int64_t total;
+            GroupAt grp;
+            if (prefix) {
+                grp = warp_groups(a.groups, a.tok_per_entry, total, blockIdx.x == 0, [](int, int, int64_t, int64_t) { return false; });
+            } else {
+                num_entries = *a.plan.num_entries;
+                total = a.plan.cum[num_entries];
+            }
+            const Share share(total * a.num_kv_heads, gridDim.x);
             const int64_t first = share.start(blockIdx.x);
             int64_t left = share.start(blockIdx.x + 1) - first;
-            int e = 0, h = 0;
+            int e = 0, h = 0;                // entry (prefixes: of the group)
             int64_t off = 0;                 // into the item's cost
             if (left > 0) {
-                e = warp_find(a.plan.cum, num_entries, first / a.num_kv_heads);
-                const int64_t in = first - a.plan.cum[e] * a.num_kv_heads;
-                const int cost = cost_of(a.plan.entries[e].tiles);
+                const int64_t u = first / a.num_kv_heads;
+                int64_t before;
+                int cost;
+                if (prefix) {
+                    grp = warp_groups(a.groups, a.tok_per_entry, total, false,
+                                      [u](int, int, int64_t b, int64_t c) { return b <= u && u < b + c; });
+                    cost = cost_of(grp.tiles);
+                    e = static_cast<int>((u - grp.before) / cost);
+                    before = grp.before + static_cast<int64_t>(e) * cost;
+                } else {
+                    e = warp_find(a.plan.cum, num_entries, u);
+                    before = a.plan.cum[e];
+                    cost = cost_of(a.plan.entries[e].tiles);
+                }
+                const int64_t in = first - before * a.num_kv_heads;
                 h = static_cast<int>(in / cost);
                 off = in - static_cast<int64_t>(h) * cost;
             }
@@ -652,7 +739,20 @@ __global__ void __launch_bounds__(Cfg<FP8>::kThreads, 1)
             for (uint32_t k = 0;;) {
                 int t0 = 0, t1 = 0;
                 if (left > 0) {
-                    while (held != e) {
+                    if (prefix && held != e) {
+                        if (e == grp.entries) {   // the next group with something to read
+                            const int64_t u = grp.before + static_cast<int64_t>(grp.entries) * cost_of(grp.tiles);
+                            grp = warp_groups(a.groups, a.tok_per_entry, total, false,
+                                              [u](int, int, int64_t b, int64_t c) { return b == u && c > 0; });
+                            e = 0;
+                        }
+                        const int row0 = grp.a + e * a.tok_per_entry;
+                        const int pages = a.groups.pages[grp.g];
+                        en = Entry{row0, min(a.tok_per_entry, a.groups.start[grp.g + 1] - row0), kAllVisible, grp.a, 0, 0, pages,
+                                   grp.tiles};
+                        held = e;
+                    }
+                    while (!prefix && held != e) {
                         const int4* p = reinterpret_cast<const int4*>(a.plan.entries + e);
                         const int4 x = p[0], y = p[1];
                         en = Entry{x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
@@ -685,6 +785,7 @@ __global__ void __launch_bounds__(Cfg<FP8>::kThreads, 1)
                     if (++h == a.num_kv_heads) {
                         h = 0;
                         ++e;
+                        held = -1;
                     }
                 }
             }
@@ -1077,7 +1178,7 @@ __global__ void __launch_bounds__(Cfg<FP8>::kThreads, 1)
         }
     }
     __syncthreads();
-    if (a.whole_o) pdl_wait();   // this kernel ends after the one before it
+    if (a.groups.start) pdl_wait();
     if (warp == 1)
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem));
 }
@@ -1087,18 +1188,15 @@ struct PlanArgs {
     Plan plan;
     int max_entries;
     int tok_per_entry;          // query tokens of a row tile: kRowTile / group
-    const int32_t* q_start;     // chunks
+    const int32_t* q_start;
     int total_q;
     const int32_t* seq_lens;
     int batch;
     int max_pages;
     int window;                 // INT_MAX: none
     int sink;
-    const int32_t* group_start; // prefix mode
-    const int32_t* shared_pages;
-    int num_groups;
     int num_q_heads;
-    __nv_bfloat16* out;         // chunks: rows that see nothing get 0 / -inf here
+    __nv_bfloat16* out;         // rows that see nothing get 0 / -inf here
     float* lse;
 };
 
@@ -1141,95 +1239,60 @@ __device__ __forceinline__ int checked_len(const PlanArgs& p, int b) {
     return len;
 }
 
-// One CTA: the list of entries, and the running count of their key tiles.
-template <bool PREFIX>
+// One CTA: the list of the chunks' entries, and the running sum of their costs.
 __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const __grid_constant__ PlanArgs p) {
     __shared__ int64_t warp_sums[32];
     const int tid = threadIdx.x, lane = tid & 31;
     int64_t total;
     pdl_wait();   // the workspace may still be read by the call before
     pdl_launch_dependents();
-    // Row tiles before each request (or group): the entries of one are consecutive.
-    int rows_entries = 0;   // entries of the row tiles
-    const int owners = PREFIX ? p.num_groups : p.batch;
-    for (int i0 = 0; i0 < owners; i0 += kPlanThreads) {
+    // Row tiles before each request: the entries of one are consecutive.
+    int n = 0;
+    for (int i0 = 0; i0 < p.batch; i0 += kPlanThreads) {
         const int i = i0 + tid;
         int count = 0;
-        if (i < owners) {
-            const int32_t* start = PREFIX ? p.group_start : p.q_start;
-            const int a = start[i], b = start[i + 1], most = PREFIX ? p.batch : p.total_q;
-            if (a < 0 || b < a || b > most) {
-                svq_flag(PREFIX ? SV_DEVERR_GROUP : SV_DEVERR_Q_START);
-            } else if (PREFIX) {
-                const int sp = p.shared_pages[i];
-                if (sp < 0 || sp > p.max_pages) svq_flag(SV_DEVERR_GROUP);
-                else if (sp > 0) count = (b - a + p.tok_per_entry - 1) / p.tok_per_entry;
-            } else {
-                count = (b - a + p.tok_per_entry - 1) / p.tok_per_entry;
-            }
+        if (i < p.batch) {
+            const int a = p.q_start[i], b = p.q_start[i + 1];
+            if (a < 0 || b < a || b > p.total_q) svq_flag(SV_DEVERR_Q_START);
+            else count = (b - a + p.tok_per_entry - 1) / p.tok_per_entry;
         }
-        const int64_t before = rows_entries + block_scan(count, warp_sums, total);
-        if (i < owners) p.plan.req_offset[i] = static_cast<int>(min(before, static_cast<int64_t>(INT_MAX / 2)));
-        const int64_t sum = rows_entries + total;
-        rows_entries = static_cast<int>(min(sum, static_cast<int64_t>(INT_MAX / 2)));
+        const int64_t before = n + block_scan(count, warp_sums, total);
+        if (i < p.batch) p.plan.req_offset[i] = static_cast<int>(min(before, static_cast<int64_t>(INT_MAX / 2)));
+        n = static_cast<int>(min(n + total, static_cast<int64_t>(INT_MAX / 2)));
     }
     // Overlapping (broken) starts could list more tiles than the workspace holds.
-    if (rows_entries > p.max_entries) {
-        if (tid == 0) svq_flag(PREFIX ? SV_DEVERR_GROUP : SV_DEVERR_Q_START);
-        rows_entries = p.max_entries;
+    if (n > p.max_entries) {
+        if (tid == 0) svq_flag(SV_DEVERR_Q_START);
+        n = p.max_entries;
     }
     __syncthreads();
-    const int n = rows_entries;
-    if (PREFIX) {
-        for (int b = tid; b < p.batch; b += kPlanThreads) {
-            const Grouped r = grouped(p.group_start, p.shared_pages, p.num_groups, p.batch, p.max_pages, b, p.seq_lens[b]);
-            if (r.fault) svq_flag(r.fault);
-            int pre = r.page == kNotTouched ? -2 : -1;
-            if (r.page > 0) {
-                const int pe = p.plan.req_offset[r.group] + (b - p.group_start[r.group]) / p.tok_per_entry;
-                if (pe < n) pre = pe;
-            }
-            p.plan.req_entry[b] = pre;
-        }
-    }
     int64_t base = 0;
     for (int e0 = 0; e0 < n; e0 += kPlanThreads) {
         const int e = e0 + tid;
         Entry en = {0, 0, 0, 0, 0, 0, 0, 0};
-        bool empty = false;   // chunks: rows that see nothing
+        bool empty = false;   // rows that see nothing
         if (e < n) {
-            if (PREFIX) {
-                const int g = find_le(p.plan.req_offset, p.num_groups, e);
-                const int a = p.group_start[g], b = p.group_start[g + 1];
-                const int at = (e - p.plan.req_offset[g]) * p.tok_per_entry;
-                en.row0 = a + at;
-                en.ntok = min(p.tok_per_entry, b - en.row0);
-                en.pos0 = kAllVisible;
-                en.req = a;
-                en.npages = p.shared_pages[g];
+            const int b = find_le(p.plan.req_offset, p.batch, e);
+            const int start = p.q_start[b];
+            const int size = p.q_start[b + 1] - start;
+            const int at = (e - p.plan.req_offset[b]) * p.tok_per_entry;
+            int len = checked_len(p, b);
+            if (size > len) {
+                if (len > 0) svq_flag(SV_DEVERR_Q_START);
+                len = 0;
+            }
+            en.row0 = start + at;
+            en.ntok = min(p.tok_per_entry, size - at);
+            en.req = b;
+            if (len > 0) {
+                en.pos0 = len - size + at;
+                const int last = (en.pos0 + en.ntok - 1) / kPage + 1;
+                const int w0 = max(0, en.pos0 - p.window + 1) / kPage;
+                en.sink_pages = sink_pages_of(p.sink, w0);
+                en.w0 = w0;
+                en.npages = en.sink_pages + last - w0;
             } else {
-                const int b = find_le(p.plan.req_offset, p.batch, e);
-                const int start = p.q_start[b];
-                const int size = p.q_start[b + 1] - start;
-                const int at = (e - p.plan.req_offset[b]) * p.tok_per_entry;
-                int len = checked_len(p, b);
-                if (size > len) {
-                    if (len > 0) svq_flag(SV_DEVERR_Q_START);
-                    len = 0;
-                }
-                en.row0 = start + at;
-                en.ntok = min(p.tok_per_entry, size - at);
-                en.req = b;
-                if (len > 0) {
-                    en.pos0 = len - size + at;
-                    const int last = (en.pos0 + en.ntok - 1) / kPage + 1;
-                    const int w0 = max(0, en.pos0 - p.window + 1) / kPage;
-                    en.sink_pages = sink_pages_of(p.sink, w0);
-                    en.w0 = w0;
-                    en.npages = en.sink_pages + last - w0;
-                } else {
-                    empty = true;
-                }
+                empty = true;
             }
         }
         en.tiles = tiles_of(en.npages);
@@ -1309,24 +1372,32 @@ __global__ void __launch_bounds__(kJoinThreads) join_cut_kernel(const __grid_con
 
 // Prefixes: CTA per (request, query head) joins its prefix and what is behind it.
 __global__ void __launch_bounds__(kJoinThreads) join_prefix_kernel(const __grid_constant__ AttendArgs a, int ctas) {
-    pdl_wait();
     const int b = blockIdx.x / a.num_q_heads, hq = blockIdx.x % a.num_q_heads;
-    const int n = *a.plan.num_entries;
-    const int pre = a.plan.req_entry[b];
-    if (pre == -2) return;
+    uint32_t fault;
+    const int page = page_behind(a.groups, b, a.seq_lens[b], fault);
+    int64_t total;
+    const GroupAt grp = warp_groups(a.groups, a.tok_per_entry, total, false,
+                                    [b](int g0, int end, int64_t, int64_t) { return g0 <= b && b < end; });
+    pdl_wait();
+    if (b < a.groups.start[0] || b >= a.groups.start[a.groups.n]) return;   // not touched
+    if (grp.g < 0) fault = SV_DEVERR_GROUP;
+    if (fault && hq == 0 && threadIdx.x == 0) svq_flag(fault);
     const int64_t q = blockIdx.x;
     Pieces lists[2];
     int nl = 0;
-    if (pre >= 0) {
-        const int64_t total = a.plan.cum[n] * a.num_kv_heads;
-        const Share share(total, ctas);
-        const int h = hq / a.group, hr = hq - h * a.group;
-        const Entry en = a.plan.entries[pre];
-        const Placed it(share, a.plan.cum[pre] * a.num_kv_heads + static_cast<int64_t>(h) * cost_of(en.tiles), en.tiles);
-        if (it.c0 == it.c1) lists[nl++] = Pieces{a.whole_o, a.whole_ml, q, q, 0, 1};
-        else lists[nl++] = cut_pieces(a, share, it, (b - en.row0) * a.group + hr);
+    if (page >= 0 && grp.g >= 0) {
+        if (page > 0) {
+            const Share share(total * a.num_kv_heads, ctas);
+            const int h = hq / a.group, hr = hq - h * a.group;
+            const int e = (b - grp.a) / a.tok_per_entry, row = b - grp.a - e * a.tok_per_entry;
+            const int cost = cost_of(grp.tiles);
+            const Placed it(share, (grp.before + static_cast<int64_t>(e) * cost) * a.num_kv_heads + static_cast<int64_t>(h) * cost,
+                            grp.tiles);
+            if (it.c0 == it.c1) lists[nl++] = Pieces{a.whole_o, a.whole_ml, q, q, 0, 1};
+            else lists[nl++] = cut_pieces(a, share, it, row * a.group + hr);
+        }
+        lists[nl++] = Pieces{a.split_o, a.split_ml, q * a.splits, q * a.splits + 1, 1, a.splits};
     }
-    lists[nl++] = Pieces{a.split_o, a.split_ml, q * a.splits, q * a.splits + 1, 1, a.splits};
     join_row(lists, nl, a.out + q * kHeadDim, a.lse + q);
 }
 
@@ -1334,12 +1405,12 @@ __global__ void __launch_bounds__(kJoinThreads) join_prefix_kernel(const __grid_
 size_t up(size_t n) { return (n + 255) / 256 * 256; }
 
 struct Layout {
-    size_t entries, cum, num, req_offset, req_entry, cut_o, cut_ml, whole_o, whole_ml, split_o, split_ml, total;
+    size_t entries, cum, num, req_offset, cut_o, cut_ml, whole_o, whole_ml, split_o, split_ml, total;
     int max_entries, slot_rows;
-    // owners: requests (chunks) or groups (prefixes); rows: query tokens
-    Layout(int64_t batch, int64_t owners, int64_t rows, int num_q_heads, int num_kv_heads, bool prefix) {
+    // rows: query tokens
+    Layout(int64_t batch, int64_t rows, int num_q_heads, int num_kv_heads, bool prefix) {
         const int group = num_q_heads / num_kv_heads;
-        const int64_t e = rows / (kRowTile / group) + owners;
+        const int64_t e = prefix ? 0 : rows / (kRowTile / group) + batch;
         max_entries = static_cast<int>(e);
         slot_rows = static_cast<int>(rows * group < kRowTile ? rows * group : kRowTile);
         size_t at = 0;
@@ -1347,12 +1418,11 @@ struct Layout {
         entries = take(e * sizeof(Entry));
         cum = take((e + 1) * sizeof(int64_t));
         num = take(sizeof(int));
-        req_offset = take(owners * sizeof(int));
+        req_offset = take(prefix ? 0 : batch * sizeof(int));
         cut_o = take(2ull * kMaxCtas * slot_rows * kHeadDim * sizeof(float));
         cut_ml = take(2ull * kMaxCtas * slot_rows * sizeof(float2));
         const size_t b = prefix ? batch : 0, heads = b * num_q_heads;
         const size_t parts = prefix ? window_decode_rows(batch, num_q_heads, num_kv_heads) : 0;
-        req_entry = take(b * sizeof(int));
         whole_o = take(heads * kHeadDim * sizeof(float));
         whole_ml = take(heads * sizeof(float2));
         split_o = take(parts * kHeadDim * sizeof(float));
@@ -1378,10 +1448,11 @@ int launch_attend(const AttendArgs& a, const CUtensorMap& tk, const CUtensorMap&
 }
 
 // The arguments both calls share.
-void fill_args(const sv_cache* c, const void* q, int num_q_heads, const int32_t* page_table, int max_pages,
-               const Layout& lay, int window, int sink, float softmax_scale, void* out, float* lse, void* workspace,
-               int batch, AttendArgs& a, PlanArgs& p) {
+AttendArgs attend_args(const sv_cache* c, const void* q, int num_q_heads, const int32_t* page_table, int max_pages,
+                       const Layout& lay, int window, int sink, float softmax_scale, void* out, float* lse,
+                       void* workspace) {
     unsigned char* ws = static_cast<unsigned char*>(workspace);
+    AttendArgs a = {};
     a.q = static_cast<const __nv_bfloat16*>(q);
     a.num_q_heads = num_q_heads;
     a.num_kv_heads = c->num_kv_heads;
@@ -1397,7 +1468,7 @@ void fill_args(const sv_cache* c, const void* q, int num_q_heads, const int32_t*
     a.plan.cum = reinterpret_cast<int64_t*>(ws + lay.cum);
     a.plan.num_entries = reinterpret_cast<int*>(ws + lay.num);
     a.plan.req_offset = reinterpret_cast<int*>(ws + lay.req_offset);
-    a.plan.req_entry = reinterpret_cast<int*>(ws + lay.req_entry);
+    a.tok_per_entry = kRowTile / a.group;
     a.window = window > 0 ? window : INT_MAX;
     a.sink = sink;
     a.scale_log2 = softmax_scale * 1.4426950408889634f;
@@ -1406,16 +1477,7 @@ void fill_args(const sv_cache* c, const void* q, int num_q_heads, const int32_t*
     a.cut_o = reinterpret_cast<float*>(ws + lay.cut_o);
     a.cut_ml = reinterpret_cast<float2*>(ws + lay.cut_ml);
     a.slot_rows = lay.slot_rows;
-    p.plan = a.plan;
-    p.max_entries = lay.max_entries;
-    p.tok_per_entry = kRowTile / a.group;
-    p.batch = batch;
-    p.max_pages = max_pages;
-    p.window = a.window;
-    p.sink = sink;
-    p.num_q_heads = num_q_heads;
-    p.out = a.out;
-    p.lse = lse;
+    return a;
 }
 
 int launch_tiles(const sv_cache* c, const AttendArgs& a, int ctas, cudaStream_t stream) {
@@ -1434,13 +1496,13 @@ int cta_count(int sm_count) { return sm_count < kMaxCtas ? sm_count : kMaxCtas; 
 
 // One token a request goes to the decode kernel (partials of its splits); chunks to the tiles.
 size_t window_workspace_bytes(int batch, int num_q_heads, int num_kv_heads, int total_q) {
-    const size_t chunks = Layout(batch, batch, total_q, num_q_heads, num_kv_heads, false).total;
+    const size_t chunks = Layout(batch, total_q, num_q_heads, num_kv_heads, false).total;
     const size_t rows = static_cast<size_t>(window_decode_rows(batch, num_q_heads, num_kv_heads));
     const size_t decode = total_q == batch ? up(rows * kHeadDim * sizeof(float)) + up(rows * sizeof(float2)) : 0;
     return chunks > decode ? chunks : decode;
 }
 size_t prefix_workspace_bytes(int batch, int num_q_heads, int num_kv_heads, int num_groups) {
-    return Layout(batch, num_groups, batch, num_q_heads, num_kv_heads, true).total;
+    return Layout(batch, batch, num_q_heads, num_kv_heads, true).total;
 }
 
 int launch_window(const sv_cache* c, const void* q, int num_q_heads, const int32_t* q_start, int total_q,
@@ -1459,14 +1521,11 @@ int launch_window(const sv_cache* c, const void* q, int num_q_heads, const int32
                                             nullptr, 0, softmax_scale, splits, o, ml, stream);
         return st ? st : launch_join_splits(o, ml, splits, heads, out, lse, stream);
     }
-    const Layout lay(batch, batch, total_q, num_q_heads, c->num_kv_heads, false);
-    PlanArgs p = {};
-    AttendArgs a = {};
-    fill_args(c, q, num_q_heads, page_table, max_pages, lay, window, sink, softmax_scale, out, lse, workspace, batch, a, p);
-    p.q_start = q_start;
-    p.total_q = total_q;
-    p.seq_lens = seq_lens;
-    if (launch_pdl(plan_kernel<false>, dim3(1), dim3(kPlanThreads), 0, stream, p) != cudaSuccess) return SV_ERR_CUDA;
+    const Layout lay(batch, total_q, num_q_heads, c->num_kv_heads, false);
+    const AttendArgs a = attend_args(c, q, num_q_heads, page_table, max_pages, lay, window, sink, softmax_scale, out, lse, workspace);
+    const PlanArgs p = {a.plan, lay.max_entries, a.tok_per_entry, q_start, total_q, seq_lens, batch, max_pages,
+                        a.window, sink, num_q_heads, a.out, lse};
+    if (launch_pdl(plan_kernel, dim3(1), dim3(kPlanThreads), 0, stream, p) != cudaSuccess) return SV_ERR_CUDA;
     const int st = launch_tiles(c, a, ctas, stream);
     if (st || ctas < 2) return st;
     const int y = lay.slot_rows < 32 ? lay.slot_rows : 32;
@@ -1479,22 +1538,17 @@ int launch_prefix(const sv_cache* c, const void* q, int num_q_heads, const int32
                   const int32_t* seq_lens, int batch, int max_pages, const int32_t* group_start,
                   const int32_t* shared_pages, int num_groups, float softmax_scale, void* out, float* lse,
                   void* workspace, int sm_count, cudaStream_t stream) {
-    const Layout lay(batch, num_groups, batch, num_q_heads, c->num_kv_heads, true);
+    const Layout lay(batch, batch, num_q_heads, c->num_kv_heads, true);
     const int ctas = cta_count(sm_count);
-    PlanArgs p = {};
-    AttendArgs a = {};
-    fill_args(c, q, num_q_heads, page_table, max_pages, lay, 0, 0, softmax_scale, out, lse, workspace, batch, a, p);
-    p.seq_lens = seq_lens;
-    p.group_start = group_start;
-    p.shared_pages = shared_pages;
-    p.num_groups = num_groups;
+    AttendArgs a = attend_args(c, q, num_q_heads, page_table, max_pages, lay, 0, 0, softmax_scale, out, lse, workspace);
+    a.groups = Groups{group_start, shared_pages, num_groups, batch, max_pages};
+    a.seq_lens = seq_lens;
     unsigned char* ws = static_cast<unsigned char*>(workspace);
     a.whole_o = reinterpret_cast<float*>(ws + lay.whole_o);
     a.whole_ml = reinterpret_cast<float2*>(ws + lay.whole_ml);
     a.split_o = reinterpret_cast<float*>(ws + lay.split_o);
     a.split_ml = reinterpret_cast<float2*>(ws + lay.split_ml);
     a.splits = window_decode_splits(c->kv_format == SV_KV_FP8_E4M3, batch, c->num_kv_heads, max_pages, ctas);
-    if (launch_pdl(plan_kernel<true>, dim3(1), dim3(kPlanThreads), 0, stream, p) != cudaSuccess) return SV_ERR_CUDA;
     int st = launch_window_decode(c, q, num_q_heads, page_table, seq_lens, batch, max_pages, 0, 0, group_start,
                                   shared_pages, num_groups, softmax_scale, a.splits, a.split_o, a.split_ml, stream);
     if (st) return st;

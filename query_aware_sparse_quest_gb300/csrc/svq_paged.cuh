@@ -43,26 +43,31 @@ __device__ __forceinline__ int find_le(const int32_t* a, int n, int v) {
     return lo;
 }
 
-// Request b of a batch in groups that share their first pages: its group, and
-// the first page behind those, or kNothing (no token, or invalid, with the
-// error bit) or kNotTouched (behind the last group).
-constexpr int kNothing = -1, kNotTouched = -2;
-struct Grouped {
-    int group, page;
-    uint32_t fault;
+// Requests in groups that share their first pages: group g is requests
+// start[g] .. start[g + 1] - 1, its first pages[g] pages are shared.
+struct Groups {
+    const int32_t* start;   // nullptr: none
+    const int32_t* pages;
+    int n;
+    int batch;
+    int max_pages;
+    // Whether group g by itself is one.
+    __device__ __forceinline__ bool sound(int a, int end, int sp) const {
+        return a >= 0 && a <= end && end <= batch && sp >= 0 && sp <= max_pages;
+    }
 };
-__device__ __forceinline__ Grouped grouped(const int32_t* group_start, const int32_t* shared_pages, int num_groups, int batch,
-                                           int max_pages, int b, int len) {
-    Grouped r = {0, kNotTouched, 0u};
-    if (b < group_start[0] || b >= group_start[num_groups]) return r;
-    r.page = kNothing;
-    r.group = find_le(group_start, num_groups, b);
-    const int a = group_start[r.group], end = group_start[r.group + 1], sp = shared_pages[r.group];
-    if (a < 0 || a > b || b >= end || end > batch || sp < 0 || sp > max_pages) r.fault = SV_DEVERR_GROUP;
-    else if (len < 0 || (static_cast<int64_t>(len) + kPage - 1) / kPage > max_pages) r.fault = SV_DEVERR_SEQ_LEN;
-    else if (len < sp * kPage) r.fault = len ? SV_DEVERR_GROUP : 0u;
-    else if (len > 0) r.page = sp;
-    return r;
+// The page behind the shared ones of request b, which has `len` tokens (-1: none
+// is to be read), and what is wrong with it.
+__device__ __forceinline__ int page_behind(const Groups& gr, int b, int len, uint32_t& fault) {
+    fault = 0;
+    if (b < gr.start[0] || b >= gr.start[gr.n]) return -1;
+    const int g = find_le(gr.start, gr.n, b);
+    const int a = gr.start[g], end = gr.start[g + 1], sp = gr.pages[g];
+    if (!gr.sound(a, end, sp) || a > b || b >= end) fault = SV_DEVERR_GROUP;
+    else if (len < 0 || (static_cast<int64_t>(len) + kPage - 1) / kPage > gr.max_pages) fault = SV_DEVERR_SEQ_LEN;
+    else if (len < sp * kPage) fault = len ? SV_DEVERR_GROUP : 0u;
+    else if (len > 0) return sp;
+    return -1;
 }
 
 // The K or V pool bf16 [pages][kv heads][16][128] as a 4-D tensor: 64 channels,

@@ -55,10 +55,7 @@ struct Args {
     const int32_t* seq_lens;
     int max_pages;
     int64_t num_phys_pages;
-    const int32_t* group_start; // requests in groups that share pages: the pages behind those; nullptr: the window's
-    const int32_t* shared_pages;
-    int num_groups;
-    int batch;
+    Groups groups;              // requests that share pages: the pages behind those are read; none: the window's
     int window;                 // INT_MAX: none
     int sink;
     int num_splits;
@@ -107,8 +104,9 @@ struct View {
 __device__ __forceinline__ View view_of(const Args& a, int len, int b) {
     View v = {0, 0, 0};
     if (len <= 0) return v;
-    if (a.group_start) {
-        v.w0 = grouped(a.group_start, a.shared_pages, a.num_groups, a.batch, a.max_pages, b, len).page;
+    if (a.groups.start) {
+        uint32_t fault;   // the join of the parts reports it
+        v.w0 = page_behind(a.groups, b, len, fault);
         if (v.w0 < 0) return {0, 0, 0};
     } else {
         v.w0 = max(0, len - a.window) / kPage;
@@ -148,7 +146,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<FP8>::kPerSm)
 
     int len = a.seq_lens[b];
     if (len < 0 || (static_cast<int64_t>(len) + kPage - 1) / kPage > a.max_pages) {
-        if (threadIdx.x == 0 && split == 0 && !a.group_start) svq_flag(SV_DEVERR_SEQ_LEN);   // else the plan does
+        if (threadIdx.x == 0 && split == 0 && !a.groups.start) svq_flag(SV_DEVERR_SEQ_LEN);
         len = 0;
     }
     if (warp == kWarps) {
@@ -175,9 +173,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<FP8>::kPerSm)
             }
         }
     }
-    // The pools and the workspace, which the work before may still use.  Behind a prefix the kernel
-    // before has waited for that work and shares nothing with this one, which waits at its end.
-    if (!a.group_start) pdl_wait();
+    pdl_wait();   // the pools and the workspace, which the work before may still use
     const View v = view_of(a, len, b);
     const int chunk = (v.count + a.num_splits - 1) / a.num_splits;
     const int j0 = min(v.count, split * chunk);
@@ -252,7 +248,6 @@ __global__ void __launch_bounds__(kThreads, Cfg<FP8>::kPerSm)
         if (!ok) svq_flag(SV_DEVERR_TIMEOUT);
         // This lane's copies land before the CTA (and its shared memory) retires.
         if (last >= 0) (void)mbar_wait_bounded(fb, (last / kStages) & 1);
-        pdl_wait();
         pdl_launch_dependents();
         return;
     }
@@ -434,7 +429,6 @@ __global__ void __launch_bounds__(kThreads, Cfg<FP8>::kPerSm)
         a.o_part[((q0 + hh) * a.num_splits + split) * kHeadDim + d] = O;
         if (d == 0) a.ml_part[(q0 + hh) * a.num_splits + split] = make_float2(M, L);
     }
-    pdl_wait();
 }
 
 // CTA per (request, query head): joins its splits.
@@ -517,10 +511,7 @@ int launch_window_decode(const sv_cache* c, const void* q, int num_q_heads, cons
     a.seq_lens = seq_lens;
     a.max_pages = max_pages;
     a.num_phys_pages = c->num_phys_pages;
-    a.group_start = group_start;
-    a.shared_pages = shared_pages;
-    a.num_groups = num_groups;
-    a.batch = batch;
+    a.groups = Groups{group_start, shared_pages, num_groups, batch, max_pages};
     a.window = window > 0 ? window : INT_MAX;
     a.sink = sink;
     a.num_splits = splits;
