@@ -661,29 +661,56 @@ __global__ void __launch_bounds__(Cfg<FP8>::kThreads, 1)
                         qk(w, stage(kl));
                         if (!two || w == 1) release(kl);
                     }
-                    const int step = two ? 1 : 2;
-                    for (int i = 0; i < (two ? 2 * n : n) && ok; ++i) {
-                        // The i-th (tile, stream) pair: everything but P is waited for and worked out first.
-                        const int t = two ? i >> 1 : i, w = i & 1;
-                        const bool next = t + step < n, done = !two || w == 1;   // done: the last use of the tiles
-                        const uint32_t vl = ld + v_load(t, n), kl = ld + k_load(t + step);
-                        const int pages = min(kTilePages, npages - first_page - t * kTilePages);
+                    // P V of (stream w, tile t), whose values are in stage vl.
+                    auto pv = [&](int w, uint32_t vs, int pages, bool acc) {
                         // The two 64-channel halves of a value tile are 1 KB apart (N-major operand).
-                        const uint32_t v_lo = desc_lo(stage(vl), 1024), ks = stage(kl);
+                        const uint32_t v_lo = desc_lo(vs, 1024);
                         const uint32_t o = tmem + kColO + w * 128, p = tmem + kColS + w * 128;
-                        ok = load_ready(vl) && (!next || load_ready(kl)) && bar_wait(smem_addr(&ct->p_full[w]), (p_ph >> w) & 1);
-                        p_ph ^= 1u << w;
-                        if (!ok) break;
-                        tc_fence_after();
-                        if (pages == kTilePages) {
-                            mma_pv8(o, p, v_lo, kIdescPV, t >= step);
+                        if (pages >= kTilePages) {
+                            mma_pv8(o, p, v_lo, kIdescPV, acc);
                         } else {
                             for (int u = 0; u < pages; ++u)
-                                mma_pv1(o, p + u * 8, v_lo + u * (kPageBytes >> 4), kIdescPV, t >= step || u != 0);
+                                mma_pv1(o, p + u * 8, v_lo + u * (kPageBytes >> 4), kIdescPV, acc || u != 0);
                         }
-                        if (next) qk(w, ks);
-                        else mma_commit(smem_addr(&ct->o_full[w]));
-                        if (done) {
+                    };
+                    auto p_ready = [&](int w) {
+                        const bool r = bar_wait(smem_addr(&ct->p_full[w]), (p_ph >> w) & 1);
+                        p_ph ^= 1u << w;
+                        tc_fence_after();
+                        return r;
+                    };
+                    // The tensor pipe queues only a few MMAs, so what lies between the last of one
+                    // (tile, stream) pair and the first of the next is kept short: loads are waited
+                    // for once a tile, stages follow one another.
+                    int pages = npages - first_page;
+                    if (two) {
+                        for (int t = 0; t < n && ok; ++t, pages -= kTilePages) {
+                            const bool next = t + 1 < n;
+                            const uint32_t vl = ld + v_load(t, n), kl = ld + k_load(t + 1);
+                            const uint32_t vs = stage(vl), ks = stage(kl);
+                            ok = load_ready(vl) && (!next || load_ready(kl)) && p_ready(0);
+                            if (!ok) break;
+                            pv(0, vs, pages, t > 0);
+                            if (next) qk(0, ks);
+                            else mma_commit(smem_addr(&ct->o_full[0]));
+                            ok = p_ready(1);
+                            if (!ok) break;
+                            pv(1, vs, pages, t > 0);
+                            if (next) qk(1, ks);
+                            else mma_commit(smem_addr(&ct->o_full[1]));
+                            release(vl);
+                            if (next) release(kl);
+                        }
+                    } else {
+                        for (int t = 0; t < n && ok; ++t, pages -= kTilePages) {
+                            const int w = t & 1;
+                            const bool next = t + 2 < n;
+                            const uint32_t vl = ld + v_load(t, n), kl = ld + k_load(t + 2);
+                            ok = load_ready(vl) && (!next || load_ready(kl)) && p_ready(w);
+                            if (!ok) break;
+                            pv(w, stage(vl), pages, t > 1);
+                            if (next) qk(w, stage(kl));
+                            else mma_commit(smem_addr(&ct->o_full[w]));
                             release(vl);
                             if (next) release(kl);
                         }
@@ -884,35 +911,57 @@ __global__ void __launch_bounds__(Cfg<FP8>::kThreads, 1)
                         }
                         const float4* ks = reinterpret_cast<const float4*>(scales + slot * 2 * kTileTok);
                         const float2* vs = reinterpret_cast<const float2*>(ks + kTileTok / 4);
-                        // Pass 1: the tile's maximum.  Both passes are rolled loops over 32 columns
-                        // that read S from TMEM: straight code over 128 columns ran at the
-                        // rate its instructions were fetched.
+                        // The row's logits.  bf16: all 128 stay in registers from here to P.  e4m3 (fewer
+                        // registers a thread, and the widening warps' code beside it): rolled loops over 32
+                        // columns that read S from TMEM twice.
+                        float x[FP8 ? 1 : 128];
                         float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+                        if constexpr (FP8) {
 #pragma unroll 1
-                        for (int c = 0; c < 4; ++c) {
-                            float x[32];
-                            tc_ld32(s_col + c * 32, reinterpret_cast<uint32_t(&)[32]>(x));
-                            tc_wait_ld();
-                            if (FP8) {
+                            for (int c = 0; c < 4; ++c) {
+                                float x[32];
+                                tc_ld32(s_col + c * 32, reinterpret_cast<uint32_t(&)[32]>(x));
+                                tc_wait_ld();
+                                {
 #pragma unroll
-                                for (int u = 0; u < 8; ++u) {
-                                    const float4 k4 = ks[c * 8 + u];
-                                    x[4 * u] *= k4.x;
-                                    x[4 * u + 1] *= k4.y;
-                                    x[4 * u + 2] *= k4.z;
-                                    x[4 * u + 3] *= k4.w;
+                                    for (int u = 0; u < 8; ++u) {
+                                        const float4 k4 = ks[c * 8 + u];
+                                        x[4 * u] *= k4.x;
+                                        x[4 * u + 1] *= k4.y;
+                                        x[4 * u + 2] *= k4.z;
+                                        x[4 * u + 3] *= k4.w;
+                                    }
+                                }
+                                if (!plain) {
+                                    const uint32_t bits = c == 0 ? bits0 : (c == 1 ? bits1 : (c == 2 ? bits2 : bits3));
+#pragma unroll
+                                    for (int u = 0; u < 32; ++u)
+                                        if (!((bits >> u) & 1u)) x[u] = -INFINITY;
+                                }
+#pragma unroll
+                                for (int u = 0; u < 32; u += 8)
+#pragma unroll
+                                    for (int k = 0; k < 4; ++k) mx[k] = fmaxf(fmaxf(mx[k], x[u + 2 * k]), x[u + 2 * k + 1]);
+                            }
+                        } else {
+#pragma unroll
+                            for (int c = 0; c < 4; ++c) tc_ld32(s_col + c * 32, reinterpret_cast<uint32_t(&)[32]>(x[c * 32]));
+                            tc_wait_ld();
+                            if (!plain) {
+#pragma unroll
+                                for (int c = 0; c < 4; ++c) {
+                                    const uint32_t bits = c == 0 ? bits0 : (c == 1 ? bits1 : (c == 2 ? bits2 : bits3));
+#pragma unroll
+                                    for (int u = 0; u < 32; ++u)
+                                        if (!((bits >> u) & 1u)) x[c * 32 + u] = -INFINITY;
                                 }
                             }
-                            if (!plain) {
-                                const uint32_t bits = c == 0 ? bits0 : (c == 1 ? bits1 : (c == 2 ? bits2 : bits3));
 #pragma unroll
-                                for (int u = 0; u < 32; ++u)
-                                    if (!((bits >> u) & 1u)) x[u] = -INFINITY;
+                            for (int c = 0; c < 4; ++c) {
+                                mx[c] = fmaxf(x[c], x[c + 4]);
+#pragma unroll
+                                for (int u = 8; u < 128; u += 8) mx[c] = fmaxf(fmaxf(mx[c], x[u + c]), x[u + c + 4]);
                             }
-#pragma unroll
-                            for (int u = 0; u < 32; u += 8)
-#pragma unroll
-                                for (int k = 0; k < 4; ++k) mx[k] = fmaxf(fmaxf(mx[k], x[u + 2 * k]), x[u + 2 * k + 1]);
                         }
                         const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * a.scale_log2;
                         // The base moves only when the maximum is more than kSlack above it; weights
@@ -937,44 +986,63 @@ __global__ void __launch_bounds__(Cfg<FP8>::kThreads, 1)
                         const float base = m == -INFINITY ? 0.f : m;
                         // Weights and their sum, two at a time, and P in bf16 over S (read already).
                         const uint64_t scale2 = pack2(a.scale_log2, a.scale_log2), base2 = pack2(-base, -base);
-                        uint64_t sum[2] = {0ull, 0ull};
+                        uint64_t sum[4] = {0ull, 0ull, 0ull, 0ull};
+                        if constexpr (FP8) {
 #pragma unroll 1
-                        for (int c = 0; c < 4; ++c) {
-                            float x[32];
-                            uint32_t p[16];
-                            tc_ld32(s_col + c * 32, reinterpret_cast<uint32_t(&)[32]>(x));
-                            tc_wait_ld();
-                            if (FP8) {
+                            for (int c = 0; c < 4; ++c) {
+                                float x[32];
+                                uint32_t p[16];
+                                tc_ld32(s_col + c * 32, reinterpret_cast<uint32_t(&)[32]>(x));
+                                tc_wait_ld();
+                                {
 #pragma unroll
-                                for (int u = 0; u < 8; ++u) {
-                                    const float4 k4 = ks[c * 8 + u];
-                                    x[4 * u] *= k4.x;
-                                    x[4 * u + 1] *= k4.y;
-                                    x[4 * u + 2] *= k4.z;
-                                    x[4 * u + 3] *= k4.w;
+                                    for (int u = 0; u < 8; ++u) {
+                                        const float4 k4 = ks[c * 8 + u];
+                                        x[4 * u] *= k4.x;
+                                        x[4 * u + 1] *= k4.y;
+                                        x[4 * u + 2] *= k4.z;
+                                        x[4 * u + 3] *= k4.w;
+                                    }
                                 }
-                            }
-                            if (!plain) {
-                                const uint32_t bits = c == 0 ? bits0 : (c == 1 ? bits1 : (c == 2 ? bits2 : bits3));
+                                if (!plain) {
+                                    const uint32_t bits = c == 0 ? bits0 : (c == 1 ? bits1 : (c == 2 ? bits2 : bits3));
 #pragma unroll
-                                for (int u = 0; u < 32; ++u)
-                                    if (!((bits >> u) & 1u)) x[u] = -INFINITY;
-                            }
-#pragma unroll
-                            for (int u = 0; u < 16; ++u) {
-                                float e0, e1;
-                                unpack2(fma2(pack2(x[2 * u], x[2 * u + 1]), scale2, base2), e0, e1);
-                                e0 = ex2(e0);
-                                e1 = ex2(e1);
-                                sum[u & 1] = add2(sum[u & 1], pack2(e0, e1));
-                                if (FP8) {
-                                    const float2 v2 = vs[c * 16 + u];
-                                    e0 *= v2.x;
-                                    e1 *= v2.y;
+                                    for (int u = 0; u < 32; ++u)
+                                        if (!((bits >> u) & 1u)) x[u] = -INFINITY;
                                 }
-                                p[u] = pack_bf16x2(e0, e1);
+#pragma unroll
+                                for (int u = 0; u < 16; ++u) {
+                                    float e0, e1;
+                                    unpack2(fma2(pack2(x[2 * u], x[2 * u + 1]), scale2, base2), e0, e1);
+                                    e0 = ex2(e0);
+                                    e1 = ex2(e1);
+                                    sum[u & 1] = add2(sum[u & 1], pack2(e0, e1));
+                                    {
+                                        const float2 v2 = vs[c * 16 + u];
+                                        e0 *= v2.x;
+                                        e1 *= v2.y;
+                                    }
+                                    p[u] = pack_bf16x2(e0, e1);
+                                }
+                                tc_st16(s_col + c * 16, p);
                             }
-                            tc_st16(s_col + c * 16, p);
+                        } else {
+#pragma unroll
+                            for (int c = 0; c < 4; ++c) {
+                                uint32_t p[16];
+#pragma unroll
+                                for (int u = 0; u < 16; ++u) {
+                                    float e0, e1;
+                                    unpack2(fma2(pack2(x[c * 32 + 2 * u], x[c * 32 + 2 * u + 1]), scale2, base2), e0, e1);
+                                    e0 = ex2(e0);
+                                    e1 = ex2(e1);
+                                    sum[u & 3] = add2(sum[u & 3], pack2(e0, e1));
+                                    p[u] = pack_bf16x2(e0, e1);
+                                }
+                                tc_st16(s_col + c * 16, p);
+                            }
+                            sum[0] = add2(sum[0], sum[2]);
+                            sum[1] = add2(sum[1], sum[3]);
                         }
                         {
                             float s0, s1;
