@@ -81,7 +81,7 @@ __device__ __forceinline__ int tiles_of(int npages) { return (npages + kTilePage
 // What an item costs beside its tiles (loading Q, filling the pipeline, writing
 // the rows), in tiles: shares of the work count it, so that a CTA with many
 // short items does not take longer than one with few long ones.
-constexpr int kItemCost = 2;
+constexpr int kItemCost = 3;
 __device__ __forceinline__ int cost_of(int tiles) { return tiles ? tiles + kItemCost : 0; }
 
 struct Plan {
@@ -966,7 +966,8 @@ __global__ void __launch_bounds__(Cfg<FP8>::kThreads, 1)
                         const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * a.scale_log2;
                         // The base moves only when the maximum is more than kSlack above it; weights
                         // stay at most 2^kSlack, and sums and outputs share the base.
-                        if (__any_sync(0xffffffffu, top > m + kSlack)) {
+                        // Threads without a row hold whatever Q's memory held and have no say.
+                        if (__any_sync(0xffffffffu, valid && top > m + kSlack)) {
                             const float mn = fmaxf(m, top);
                             const float alpha = mn == -INFINITY ? 1.f : ex2(m - mn);
                             m = mn;

@@ -167,6 +167,23 @@ def test_bad_starts_are_skipped():
     assert binding.sv_get_device_error() == 0x20
 
 
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("group", [3, 7])
+def test_part_filled_row_tiles_repeat_exactly(group, fp8):
+    """Row tiles that leave threads without a row: what those hold changes nothing."""
+    lens, sizes = [700, 90, 1500, 33], [300, 1, 41, 33]
+    case = PagedCase(lens, 3, fp8=fp8)
+    q = torch.randn((sum(sizes), 3 * group, DIM), generator=torch.Generator().manual_seed(1)).bfloat16().to(DEV)
+    starts = [sum(sizes[:b]) for b in range(5)]
+    first = run(case, q, 200, 5, starts)
+    other = PagedCase([4000], 1)
+    for i in range(4):     # other work in between leaves other values in shared memory
+        run(other, torch.full((400, 8, DIM), 10.0 ** i, dtype=torch.bfloat16, device=DEV), 0, 0, [0, 400])
+        again = run(case, q, 200, 5, starts)
+        assert torch.equal(first[0], again[0]) and torch.equal(first[1], again[1])
+    assert binding.sv_get_device_error() == 0
+
+
 def test_repeats_are_identical_and_replays_in_a_graph():
     case = PagedCase([3000, 500], 2)
     cache, table = case.cache(), case.table.to(DEV)
