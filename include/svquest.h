@@ -334,6 +334,7 @@ size_t sv_quest_decode_step_workspace_size(int32_t batch, int32_t num_q_heads, i
  *            of q are the last tokens of request b's seq_lens[b] tokens.  An
  *            empty range is a request without query tokens.  NULL: one token a
  *            request, row b is request b's last (total_q == batch).
+ *  - out is 32-byte aligned (any whole row of an aligned tensor is).
  *  - Rows that no request's range holds (behind q_start[batch]) are not
  *    written.  total_q == 0 launches nothing.
  *  - A request with seq_lens 0 (a padded batch) gets out = 0, lse = -inf.  So

@@ -429,6 +429,7 @@ int sv_window_attention(const sv_cache* cache, const void* q, int32_t num_q_head
     int st = attend_checks(cache, q, num_q_heads, page_table, seq_lens, batch, max_pages, softmax_scale, out, lse);
     if (st) return st;
     if (window < 0 || sink_tokens < 0 || total_q < 0) return SV_ERR_INVALID_ARG;
+    if (reinterpret_cast<uintptr_t>(out) & 31u) return SV_ERR_INVALID_ARG;   // rows are written 32 bytes at a time
     if (!q_start && total_q != batch) return SV_ERR_INVALID_ARG;
     if (total_q > kMaxQueryTokens) return SV_ERR_UNSUPPORTED;
     if (!workspace || workspace_bytes < sv_window_attention_workspace_size(batch, num_q_heads, cache->num_kv_heads, total_q))

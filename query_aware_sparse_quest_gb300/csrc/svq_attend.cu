@@ -91,6 +91,13 @@ struct Plan {
     int* req_offset;   // first entry of each request
 };
 
+// A group as the join of its rows wants it.
+struct GroupRec {
+    int64_t before;    // cost per kv head of the groups before it
+    int tiles;         // 0: nothing is shared
+    int sound;
+};
+
 struct AttendArgs {
     const __nv_bfloat16* q;
     int num_q_heads, num_kv_heads, group;
@@ -112,6 +119,9 @@ struct AttendArgs {
     float* lse;
     float* cut_o;      // [2 CTAs][slot_rows][128] partials of items that are cut
     float2* cut_ml;    // [2 CTAs][slot_rows] (base in log2 units, sum)
+    struct GroupRec* group_rec;   // prefixes: [groups + 1], for the join; the last one's cost is the total
+    int4* cut_item;    // chunks: [CTAs][2] the item that goes on in a CTA: row0, ntok, kv head, pieces (0: none is to
+                       // be joined here); slot of the first piece, and of the second
     int slot_rows;
     float* whole_o;    // prefixes: the parts of whole items, [B Hq][128]; else null
     float2* whole_ml;
@@ -131,6 +141,14 @@ struct Share {
     }
 };
 
+// An item's place in the shares: its cost begins at `begin`, its first tile
+// kItemCost later.
+struct Placed {
+    int64_t begin;
+    int tiles, c0, c1;   // the CTAs with its first and its last tile
+    __device__ __forceinline__ Placed(const Share& share, int64_t at, int n)
+        : begin(at), tiles(n), c0(share.cta_of(at + kItemCost)), c1(share.cta_of(at + kItemCost + n - 1)) {}
+};
 // Largest e in [0, n) with cum[e] <= u, by the whole warp (32 probes a round trip).
 __device__ __forceinline__ int warp_find(const int64_t* cum, int n, int64_t u) {
     const int lane = threadIdx.x & 31;
@@ -155,9 +173,10 @@ struct GroupAt {
     int64_t before;   // cost per kv head of the groups before it
 };
 // By the whole warp, 32 groups a round: the sum of the groups' costs per kv
-// head, and the group for which pick(a, end, before, cost) holds, if any (g < 0).
+// head, and the group for which pick(before, cost) holds, if any (else g < 0).
+// rec: where the groups are written down, and what is wrong with them reported.
 template <typename F>
-__device__ __forceinline__ GroupAt warp_groups(const Groups& gr, int tok_per_entry, int64_t& total, bool report, F&& pick) {
+__device__ __forceinline__ GroupAt warp_groups(const Groups& gr, int tok_per_entry, int64_t& total, GroupRec* rec, F&& pick) {
     const int lane = threadIdx.x & 31;
     GroupAt found = {-1, 0, 0, 0, 0};
     total = 0;
@@ -189,7 +208,6 @@ __device__ __forceinline__ GroupAt warp_groups(const Groups& gr, int tok_per_ent
             }
             if (lane == __ffs(out) - 1) ok = false;   // the first one out of order may have hidden others
         }
-        if (report && g < gr.n && !ok) svq_flag(SV_DEVERR_GROUP);
         const int entries = ok && sp > 0 ? (end - a + tok_per_entry - 1) / tok_per_entry : 0;
         const int64_t cost = static_cast<int64_t>(entries) * cost_of(tiles_of(sp));
         int64_t x = cost;
@@ -199,7 +217,11 @@ __device__ __forceinline__ GroupAt warp_groups(const Groups& gr, int tok_per_ent
             if (lane >= d) x += y;
         }
         const int64_t before = total + x - cost;
-        const uint32_t hit = __ballot_sync(0xffffffffu, ok && pick(a, end, before, cost));
+        if (rec && g < gr.n) {
+            if (!ok) svq_flag(SV_DEVERR_GROUP);
+            rec[g] = GroupRec{before, ok ? tiles_of(sp) : 0, ok};
+        }
+        const uint32_t hit = __ballot_sync(0xffffffffu, ok && pick(before, cost));
         if (hit && found.g < 0) {
             const int src = __ffs(hit) - 1;
             found = {g0 + src, __shfl_sync(0xffffffffu, a, src), __shfl_sync(0xffffffffu, entries, src),
@@ -207,6 +229,7 @@ __device__ __forceinline__ GroupAt warp_groups(const Groups& gr, int tok_per_ent
         }
         total += __shfl_sync(0xffffffffu, x, 31);
     }
+    if (rec && lane == 0) rec[gr.n].before = total;
     return found;
 }
 
@@ -317,6 +340,13 @@ __device__ __forceinline__ void tma_load_4d(uint32_t dst, const void* tmap, int 
         "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %2, %2, %3}], [%4];"
         ::"r"(dst), "l"(tmap), "r"(0), "r"(y), "r"(bar)
         : "memory");
+}
+// 32 bytes of one thread, a whole sector: rows are written a thread each.
+__device__ __forceinline__ void st_v8(void* p, uint32_t a, uint32_t b, uint32_t c, uint32_t d, uint32_t e, uint32_t f,
+                                      uint32_t g, uint32_t h) {
+    asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(a), "r"(b), "r"(c), "r"(d), "r"(e),
+                 "r"(f), "r"(g), "r"(h)
+                 : "memory");
 }
 template <int N>
 __device__ __forceinline__ void reg_dec() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
@@ -731,7 +761,7 @@ __global__ void __launch_bounds__(Cfg<FP8>::kThreads, 1)
             int64_t total;
             GroupAt grp;
             if (prefix) {
-                grp = warp_groups(a.groups, a.tok_per_entry, total, blockIdx.x == 0, [](int, int, int64_t, int64_t) { return false; });
+                grp = warp_groups(a.groups, a.tok_per_entry, total, blockIdx.x == 0 ? a.group_rec : nullptr, [](int64_t, int64_t) { return false; });
             } else {
                 num_entries = *a.plan.num_entries;
                 total = a.plan.cum[num_entries];
@@ -746,8 +776,8 @@ __global__ void __launch_bounds__(Cfg<FP8>::kThreads, 1)
                 int64_t before;
                 int cost;
                 if (prefix) {
-                    grp = warp_groups(a.groups, a.tok_per_entry, total, false,
-                                      [u](int, int, int64_t b, int64_t c) { return b <= u && u < b + c; });
+                    grp = warp_groups(a.groups, a.tok_per_entry, total, nullptr,
+                                      [u](int64_t b, int64_t c) { return b <= u && u < b + c; });
                     cost = cost_of(grp.tiles);
                     e = static_cast<int>((u - grp.before) / cost);
                     before = grp.before + static_cast<int64_t>(e) * cost;
@@ -760,6 +790,8 @@ __global__ void __launch_bounds__(Cfg<FP8>::kThreads, 1)
                 h = static_cast<int>(in / cost);
                 off = in - static_cast<int64_t>(h) * cost;
             }
+            const bool go_on = off > 0;      // the share begins inside an item
+            if (left <= 0 && !prefix && lane == 0) a.cut_item[2 * blockIdx.x] = make_int4(0, 0, 0, 0);
             bool first_item = true;
             Entry en;
             int held = -1;
@@ -769,8 +801,8 @@ __global__ void __launch_bounds__(Cfg<FP8>::kThreads, 1)
                     if (prefix && held != e) {
                         if (e == grp.entries) {   // the next group with something to read
                             const int64_t u = grp.before + static_cast<int64_t>(grp.entries) * cost_of(grp.tiles);
-                            grp = warp_groups(a.groups, a.tok_per_entry, total, false,
-                                              [u](int, int, int64_t b, int64_t c) { return b == u && c > 0; });
+                            grp = warp_groups(a.groups, a.tok_per_entry, total, nullptr,
+                                              [u](int64_t b, int64_t c) { return b == u && c > 0; });
                             e = 0;
                         }
                         const int row0 = grp.a + e * a.tok_per_entry;
@@ -785,6 +817,20 @@ __global__ void __launch_bounds__(Cfg<FP8>::kThreads, 1)
                         en = Entry{x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
                         held = e;
                         if (en.tiles == 0) ++e;   // rows that see nothing
+                    }
+                    if (first_item && !prefix && lane == 0) {
+                        // The CTA after the one with an item's first tile names the item for the join.
+                        int4 what = make_int4(0, 0, 0, 0), where = make_int4(0, 0, 0, 0);
+                        if (go_on) {
+                            const Placed it(share, first - off, en.tiles);
+                            if (static_cast<int>(blockIdx.x) == it.c0 + 1) {
+                                what = make_int4(en.row0, en.ntok, h, it.c1 - it.c0 + 1);
+                                where.x = 2 * it.c0 + (share.start(it.c0) >= it.begin ? 0 : 1);
+                                where.y = 2 * (it.c0 + 1);
+                            }
+                        }
+                        a.cut_item[2 * blockIdx.x] = what;
+                        a.cut_item[2 * blockIdx.x + 1] = where;
                     }
                     const int64_t take = min(left, cost_of(en.tiles) - off);
                     t0 = static_cast<int>(max(static_cast<int64_t>(0), off - kItemCost));
@@ -1120,19 +1166,18 @@ __global__ void __launch_bounds__(Cfg<FP8>::kThreads, 1)
                         if (valid) {
                             if (po) {
 #pragma unroll
-                                for (int u = 0; u < 8; ++u)
-                                    *reinterpret_cast<uint4*>(po + c * 32 + 4 * u) =
-                                        make_uint4(x[4 * u], x[4 * u + 1], x[4 * u + 2], x[4 * u + 3]);
+                                for (int u = 0; u < 4; ++u)
+                                    st_v8(po + c * 32 + 8 * u, x[8 * u], x[8 * u + 1], x[8 * u + 2], x[8 * u + 3], x[8 * u + 4],
+                                          x[8 * u + 5], x[8 * u + 6], x[8 * u + 7]);
                             } else {
+                                uint32_t v[16];
 #pragma unroll
-                                for (int u = 0; u < 4; ++u) {
-                                    uint4 v;
-                                    v.x = pack_bf16x2(__uint_as_float(x[8 * u]), __uint_as_float(x[8 * u + 1]));
-                                    v.y = pack_bf16x2(__uint_as_float(x[8 * u + 2]), __uint_as_float(x[8 * u + 3]));
-                                    v.z = pack_bf16x2(__uint_as_float(x[8 * u + 4]), __uint_as_float(x[8 * u + 5]));
-                                    v.w = pack_bf16x2(__uint_as_float(x[8 * u + 6]), __uint_as_float(x[8 * u + 7]));
-                                    *reinterpret_cast<uint4*>(a.out + qrow * kHeadDim + c * 32 + 8 * u) = v;
-                                }
+                                for (int u = 0; u < 16; ++u)
+                                    v[u] = pack_bf16x2(__uint_as_float(x[2 * u]), __uint_as_float(x[2 * u + 1]));
+#pragma unroll
+                                for (int u = 0; u < 2; ++u)
+                                    st_v8(a.out + qrow * kHeadDim + c * 32 + 16 * u, v[8 * u], v[8 * u + 1], v[8 * u + 2],
+                                          v[8 * u + 3], v[8 * u + 4], v[8 * u + 5], v[8 * u + 6], v[8 * u + 7]);
                             }
                         }
                     }
@@ -1387,14 +1432,6 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const __grid_constan
 }
 
 // ---------------------------------------------------------------- joining partials
-// An item's place in the shares: its cost begins at `begin`, its first tile
-// kItemCost later.
-struct Placed {
-    int64_t begin;
-    int tiles, c0, c1;   // the CTAs with its first and its last tile
-    __device__ __forceinline__ Placed(const Share& share, int64_t at, int n)
-        : begin(at), tiles(n), c0(share.cta_of(at + kItemCost)), c1(share.cta_of(at + kItemCost + n - 1)) {}
-};
 // The partials of row r of an item that is cut: one of each of its CTAs.
 __device__ __forceinline__ Pieces cut_pieces(const AttendArgs& a, const Share& share, const Placed& it, int r) {
     Pieces p;
@@ -1407,77 +1444,116 @@ __device__ __forceinline__ Pieces cut_pieces(const AttendArgs& a, const Share& s
     return p;
 }
 
-// Chunks: CTA (c, y) joins the item that attend CTA c goes on with, if c
-// is the first to do so; rows y, y + gridDim.y, ...
-__global__ void __launch_bounds__(kJoinThreads) join_cut_kernel(const __grid_constant__ AttendArgs a, int ctas) {
+// Chunks: CTA (c, y) joins the item that attend CTA c + 1 goes on with; rows y,
+// y + gridDim.y, ... (of 8 warps each, when the pieces are few).
+constexpr int kCutThreads = 256;
+
+__global__ void __launch_bounds__(kCutThreads) join_cut_kernel(const __grid_constant__ AttendArgs a) {
+    constexpr int kWarps = kCutThreads / 32;
+    __shared__ float4 sm_o[kWarps][32];
+    __shared__ float2 sm_ml[kWarps];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     pdl_wait();
-    const int c = blockIdx.x + 1;
-    const int n = *a.plan.num_entries;
-    const int64_t total = a.plan.cum[n] * a.num_kv_heads;
-    const Share share(total, ctas);
-    const int64_t x = share.start(c);
-    if (x >= total) return;
-    const int e = warp_find(a.plan.cum, n, x / a.num_kv_heads);
-    const Entry en = a.plan.entries[e];
-    const int64_t at = a.plan.cum[e] * a.num_kv_heads;
-    const int h = static_cast<int>((x - at) / cost_of(en.tiles));
-    const Placed it(share, at + static_cast<int64_t>(h) * cost_of(en.tiles), en.tiles);
-    if (c != it.c0 + 1) return;   // the item is not cut here, or was before
-    const int rows = en.ntok * a.group;
+    const int4 what = a.cut_item[2 * (blockIdx.x + 1)];
+    const int n = what.w;
+    if (n == 0) return;
+    const int4 where = a.cut_item[2 * (blockIdx.x + 1) + 1];
+    const int rows = what.y * a.group;
     auto at_row = [&](int r) {
         const int tok = r / a.group;
-        return static_cast<int64_t>(en.row0 + tok) * a.num_q_heads + h * a.group + (r - tok * a.group);
+        return static_cast<int64_t>(what.x + tok) * a.num_q_heads + what.z * a.group + (r - tok * a.group);
     };
-    if (it.c1 - it.c0 < 8) {   // few pieces: a warp a row
-        for (int r = blockIdx.y * (kJoinThreads / 32) + (threadIdx.x >> 5); r < rows; r += gridDim.y * (kJoinThreads / 32))
-            join_row_warp(cut_pieces(a, share, it, r), a.out + at_row(r) * kHeadDim, a.lse + at_row(r));
+    auto pieces = [&](int r) {
+        return Pieces{a.cut_o, a.cut_ml, static_cast<int64_t>(where.x) * a.slot_rows + r,
+                      static_cast<int64_t>(where.y) * a.slot_rows + r, 2ll * a.slot_rows, n};
+    };
+    if (n <= 8) {   // few pieces: a warp a row, four rows at a time in flight when there are two
+        const int step = gridDim.y * kWarps;
+        for (int r0 = blockIdx.y * kWarps + warp; r0 < rows; r0 += 4 * step) {
+            if (n == 2) {
+                float2 ml[4][2];
+                float4 x[4][2];
+#pragma unroll
+                for (int u = 0; u < 4; ++u) {
+                    const Pieces p = pieces(min(r0 + u * step, rows - 1));
+#pragma unroll
+                    for (int k = 0; k < 2; ++k) {
+                        ml[u][k] = p.ml[p.row(k)];
+                        x[u][k] = *reinterpret_cast<const float4*>(p.o + p.row(k) * kHeadDim + 4 * lane);
+                    }
+                }
+#pragma unroll
+                for (int u = 0; u < 4; ++u) {
+                    const int r = r0 + u * step;
+                    RowSum s;
+                    s.add2(ml[u], x[u]);
+                    if (r < rows) s.write(a.out + at_row(r) * kHeadDim, a.lse + at_row(r), lane);
+                }
+            } else {
+                for (int u = 0; u < 4; ++u) {
+                    const int r = r0 + u * step;
+                    if (r >= rows) break;
+                    RowSum s;
+                    s.add(pieces(r), 0, 1, lane);
+                    s.write(a.out + at_row(r) * kHeadDim, a.lse + at_row(r), lane);
+                }
+            }
+        }
         return;
     }
     for (int r = blockIdx.y; r < rows; r += gridDim.y) {
-        const Pieces lists[2] = {cut_pieces(a, share, it, r), {}};
-        join_row(lists, 1, a.out + at_row(r) * kHeadDim, a.lse + at_row(r));
+        const Pieces lists[2] = {pieces(r), {}};
+        join_row<kWarps>(lists, 1, sm_o, sm_ml, a.out + at_row(r) * kHeadDim, a.lse + at_row(r));
     }
 }
 
 // Prefixes: CTA per (request, query head) joins its prefix and what is behind it.
-__global__ void __launch_bounds__(kJoinThreads) join_prefix_kernel(const __grid_constant__ AttendArgs a, int ctas) {
+constexpr int kPrefixThreads = 128;
+
+__global__ void __launch_bounds__(kPrefixThreads) join_prefix_kernel(const __grid_constant__ AttendArgs a, int ctas) {
+    __shared__ float4 sm_o[kPrefixThreads / 32][32];
+    __shared__ float2 sm_ml[kPrefixThreads / 32];
     const int b = blockIdx.x / a.num_q_heads, hq = blockIdx.x % a.num_q_heads;
+    // Inputs: before the kernels before this one have ended.
+    if (b < a.groups.start[0] || b >= a.groups.start[a.groups.n]) {   // not touched
+        pdl_wait();
+        return;
+    }
     uint32_t fault;
     const int page = page_behind(a.groups, b, a.seq_lens[b], fault);
-    int64_t total;
-    const GroupAt grp = warp_groups(a.groups, a.tok_per_entry, total, false,
-                                    [b](int g0, int end, int64_t, int64_t) { return g0 <= b && b < end; });
+    const int g = find_le(a.groups.start, a.groups.n, b);
+    const int e = (b - a.groups.start[g]) / a.tok_per_entry, row = b - a.groups.start[g] - e * a.tok_per_entry;
     pdl_wait();
-    if (b < a.groups.start[0] || b >= a.groups.start[a.groups.n]) return;   // not touched
-    if (grp.g < 0) fault = SV_DEVERR_GROUP;
+    const GroupRec rec = a.group_rec[g];
+    if (!rec.sound) fault = SV_DEVERR_GROUP;
     if (fault && hq == 0 && threadIdx.x == 0) svq_flag(fault);
     const int64_t q = blockIdx.x;
     Pieces lists[2];
     int nl = 0;
-    if (page >= 0 && grp.g >= 0) {
+    if (page >= 0 && rec.sound) {
         if (page > 0) {
-            const Share share(total * a.num_kv_heads, ctas);
+            const Share share(a.group_rec[a.groups.n].before * a.num_kv_heads, ctas);
             const int h = hq / a.group, hr = hq - h * a.group;
-            const int e = (b - grp.a) / a.tok_per_entry, row = b - grp.a - e * a.tok_per_entry;
-            const int cost = cost_of(grp.tiles);
-            const Placed it(share, (grp.before + static_cast<int64_t>(e) * cost) * a.num_kv_heads + static_cast<int64_t>(h) * cost,
-                            grp.tiles);
+            const int cost = cost_of(rec.tiles);
+            const Placed it(share, (rec.before + static_cast<int64_t>(e) * cost) * a.num_kv_heads + static_cast<int64_t>(h) * cost,
+                            rec.tiles);
             if (it.c0 == it.c1) lists[nl++] = Pieces{a.whole_o, a.whole_ml, q, q, 0, 1};
             else lists[nl++] = cut_pieces(a, share, it, row * a.group + hr);
         }
         lists[nl++] = Pieces{a.split_o, a.split_ml, q * a.splits, q * a.splits + 1, 1, a.splits};
     }
-    join_row(lists, nl, a.out + q * kHeadDim, a.lse + q);
+    join_row<kPrefixThreads / 32>(lists, nl, sm_o, sm_ml, a.out + q * kHeadDim, a.lse + q);
 }
 
 // ---------------------------------------------------------------- host side
 size_t up(size_t n) { return (n + 255) / 256 * 256; }
 
 struct Layout {
-    size_t entries, cum, num, req_offset, cut_o, cut_ml, whole_o, whole_ml, split_o, split_ml, total;
+    size_t entries, cum, num, req_offset, group_rec, cut_item, cut_o, cut_ml, whole_o, whole_ml, split_o, split_ml, total;
     int max_entries, slot_rows;
-    // rows: query tokens
-    Layout(int64_t batch, int64_t rows, int num_q_heads, int num_kv_heads, bool prefix) {
+    // rows: query tokens; num_groups: 0 for chunks
+    Layout(int64_t batch, int64_t rows, int num_q_heads, int num_kv_heads, int num_groups) {
+        const bool prefix = num_groups > 0;
         const int group = num_q_heads / num_kv_heads;
         const int64_t e = prefix ? 0 : rows / (kRowTile / group) + batch;
         max_entries = static_cast<int>(e);
@@ -1488,17 +1564,23 @@ struct Layout {
         cum = take((e + 1) * sizeof(int64_t));
         num = take(sizeof(int));
         req_offset = take(prefix ? 0 : batch * sizeof(int));
+        cut_item = take(prefix ? 0 : 2 * kMaxCtas * sizeof(int4));
         cut_o = take(2ull * kMaxCtas * slot_rows * kHeadDim * sizeof(float));
         cut_ml = take(2ull * kMaxCtas * slot_rows * sizeof(float2));
         const size_t b = prefix ? batch : 0, heads = b * num_q_heads;
         const size_t parts = prefix ? window_decode_rows(batch, num_q_heads, num_kv_heads) : 0;
+        group_rec = take(prefix ? (num_groups + 1) * sizeof(GroupRec) : 0);
         whole_o = take(heads * kHeadDim * sizeof(float));
         whole_ml = take(heads * sizeof(float2));
         split_o = take(parts * kHeadDim * sizeof(float));
         split_ml = take(parts * sizeof(float2));
-        total = at;
+        total = at + 256;   // the parts begin at the workspace's first multiple of 256 (rows are written 32 bytes at a time)
     }
 };
+
+unsigned char* base_of(void* workspace) {
+    return reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(workspace) + 255) & ~static_cast<uintptr_t>(255));
+}
 
 template <bool FP8>
 int launch_attend(const AttendArgs& a, const CUtensorMap& tk, const CUtensorMap& tv, int ctas, cudaStream_t stream) {
@@ -1520,7 +1602,7 @@ int launch_attend(const AttendArgs& a, const CUtensorMap& tk, const CUtensorMap&
 AttendArgs attend_args(const sv_cache* c, const void* q, int num_q_heads, const int32_t* page_table, int max_pages,
                        const Layout& lay, int window, int sink, float softmax_scale, void* out, float* lse,
                        void* workspace) {
-    unsigned char* ws = static_cast<unsigned char*>(workspace);
+    unsigned char* ws = base_of(workspace);
     AttendArgs a = {};
     a.q = static_cast<const __nv_bfloat16*>(q);
     a.num_q_heads = num_q_heads;
@@ -1545,6 +1627,7 @@ AttendArgs attend_args(const sv_cache* c, const void* q, int num_q_heads, const 
     a.lse = lse;
     a.cut_o = reinterpret_cast<float*>(ws + lay.cut_o);
     a.cut_ml = reinterpret_cast<float2*>(ws + lay.cut_ml);
+    a.cut_item = reinterpret_cast<int4*>(ws + lay.cut_item);
     a.slot_rows = lay.slot_rows;
     return a;
 }
@@ -1565,13 +1648,13 @@ int cta_count(int sm_count) { return sm_count < kMaxCtas ? sm_count : kMaxCtas; 
 
 // One token a request goes to the decode kernel (partials of its splits); chunks to the tiles.
 size_t window_workspace_bytes(int batch, int num_q_heads, int num_kv_heads, int total_q) {
-    const size_t chunks = Layout(batch, total_q, num_q_heads, num_kv_heads, false).total;
+    const size_t chunks = Layout(batch, total_q, num_q_heads, num_kv_heads, 0).total;
     const size_t rows = static_cast<size_t>(window_decode_rows(batch, num_q_heads, num_kv_heads));
     const size_t decode = total_q == batch ? up(rows * kHeadDim * sizeof(float)) + up(rows * sizeof(float2)) : 0;
     return chunks > decode ? chunks : decode;
 }
 size_t prefix_workspace_bytes(int batch, int num_q_heads, int num_kv_heads, int num_groups) {
-    return Layout(batch, batch, num_q_heads, num_kv_heads, true).total;
+    return Layout(batch, batch, num_q_heads, num_kv_heads, num_groups).total;
 }
 
 int launch_window(const sv_cache* c, const void* q, int num_q_heads, const int32_t* q_start, int total_q,
@@ -1590,31 +1673,31 @@ int launch_window(const sv_cache* c, const void* q, int num_q_heads, const int32
                                             nullptr, 0, softmax_scale, splits, o, ml, stream);
         return st ? st : launch_join_splits(o, ml, splits, heads, out, lse, stream);
     }
-    const Layout lay(batch, total_q, num_q_heads, c->num_kv_heads, false);
+    const Layout lay(batch, total_q, num_q_heads, c->num_kv_heads, 0);
     const AttendArgs a = attend_args(c, q, num_q_heads, page_table, max_pages, lay, window, sink, softmax_scale, out, lse, workspace);
     const PlanArgs p = {a.plan, lay.max_entries, a.tok_per_entry, q_start, total_q, seq_lens, batch, max_pages,
                         a.window, sink, num_q_heads, a.out, lse};
     if (launch_pdl(plan_kernel, dim3(1), dim3(kPlanThreads), 0, stream, p) != cudaSuccess) return SV_ERR_CUDA;
     const int st = launch_tiles(c, a, ctas, stream);
     if (st || ctas < 2) return st;
-    const int y = lay.slot_rows < 32 ? lay.slot_rows : 32;
-    return launch_pdl(join_cut_kernel, dim3(ctas - 1, y), dim3(kJoinThreads), 0, stream, a, ctas) == cudaSuccess
-               ? SV_OK
-               : SV_ERR_CUDA;
+    const int y = lay.slot_rows < 32 ? lay.slot_rows : (lay.slot_rows < 128 ? 32 : 8);
+    return launch_pdl(join_cut_kernel, dim3(ctas - 1, y), dim3(kCutThreads), 0, stream, a) == cudaSuccess ? SV_OK
+                                                                                                          : SV_ERR_CUDA;
 }
 
 int launch_prefix(const sv_cache* c, const void* q, int num_q_heads, const int32_t* page_table,
                   const int32_t* seq_lens, int batch, int max_pages, const int32_t* group_start,
                   const int32_t* shared_pages, int num_groups, float softmax_scale, void* out, float* lse,
                   void* workspace, int sm_count, cudaStream_t stream) {
-    const Layout lay(batch, batch, num_q_heads, c->num_kv_heads, true);
+    const Layout lay(batch, batch, num_q_heads, c->num_kv_heads, num_groups);
     const int ctas = cta_count(sm_count);
     AttendArgs a = attend_args(c, q, num_q_heads, page_table, max_pages, lay, 0, 0, softmax_scale, out, lse, workspace);
     a.groups = Groups{group_start, shared_pages, num_groups, batch, max_pages};
     a.seq_lens = seq_lens;
-    unsigned char* ws = static_cast<unsigned char*>(workspace);
+    unsigned char* ws = base_of(workspace);
     a.whole_o = reinterpret_cast<float*>(ws + lay.whole_o);
     a.whole_ml = reinterpret_cast<float2*>(ws + lay.whole_ml);
+    a.group_rec = reinterpret_cast<GroupRec*>(ws + lay.group_rec);
     a.split_o = reinterpret_cast<float*>(ws + lay.split_o);
     a.split_ml = reinterpret_cast<float2*>(ws + lay.split_ml);
     a.splits = window_decode_splits(c->kv_format == SV_KV_FP8_E4M3, batch, c->num_kv_heads, max_pages, ctas);
@@ -1622,7 +1705,7 @@ int launch_prefix(const sv_cache* c, const void* q, int num_q_heads, const int32
                                   shared_pages, num_groups, softmax_scale, a.splits, a.split_o, a.split_ml, stream);
     if (st) return st;
     if ((st = launch_tiles(c, a, ctas, stream))) return st;
-    return launch_pdl(join_prefix_kernel, dim3(static_cast<unsigned>(batch) * num_q_heads), dim3(kJoinThreads), 0, stream,
+    return launch_pdl(join_prefix_kernel, dim3(static_cast<unsigned>(batch) * num_q_heads), dim3(kPrefixThreads), 0, stream,
                       a, ctas) == cudaSuccess
                ? SV_OK
                : SV_ERR_CUDA;

@@ -136,6 +136,17 @@ struct RowSum {
             }
         }
     }
+    // The row of two pieces.
+    __device__ __forceinline__ void add2(const float2 (&ml)[2], const float4 (&x)[2]) {
+        m = fmaxf(ml[0].x, ml[1].x);
+        const float base = m == -INFINITY ? 0.f : m;
+        const float e = ex2(ml[0].x - base), f = ex2(ml[1].x - base);
+        l = ml[0].y * e + ml[1].y * f;
+        o.x = x[0].x * e + x[1].x * f;
+        o.y = x[0].y * e + x[1].y * f;
+        o.z = x[0].z * e + x[1].z * f;
+        o.w = x[0].w * e + x[1].w * f;
+    }
     __device__ __forceinline__ void write(__nv_bfloat16* out, float* lse, int lane) const {
         const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);
         uint2 v;
@@ -146,21 +157,10 @@ struct RowSum {
     }
 };
 
-constexpr int kJoinThreads = 128;
-
-// One row by a warp, lane l channels 4 l .. 4 l + 3.
-__device__ __forceinline__ void join_row_warp(const Pieces& p, __nv_bfloat16* out, float* lse) {
-    const int lane = threadIdx.x & 31;
-    RowSum s;
-    s.add(p, 0, 1, lane);
-    s.write(out, lse, lane);
-}
-
-// One row by the whole CTA: the warps take the pieces in turn.
-__device__ __forceinline__ void join_row(const Pieces (&lists)[2], int nlists, __nv_bfloat16* out, float* lse) {
-    constexpr int kWarps = kJoinThreads / 32;
-    __shared__ float4 sm_o[kWarps][32];
-    __shared__ float2 sm_ml[kWarps];
+// One row by a CTA of kWarps warps, which take the pieces in turn.
+template <int kWarps>
+__device__ __forceinline__ void join_row(const Pieces (&lists)[2], int nlists, float4 (&sm_o)[kWarps][32],
+                                         float2 (&sm_ml)[kWarps], __nv_bfloat16* out, float* lse) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     RowSum s;
     int k0 = warp;

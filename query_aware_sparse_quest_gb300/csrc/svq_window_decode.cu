@@ -432,13 +432,17 @@ __global__ void __launch_bounds__(kThreads, Cfg<FP8>::kPerSm)
 }
 
 // CTA per (request, query head): joins its splits.
+constexpr int kJoinThreads = 128;
+
 __global__ void __launch_bounds__(kJoinThreads) join_splits_kernel(const float* __restrict__ o_part,
                                                                    const float2* __restrict__ ml_part, int splits,
                                                                    __nv_bfloat16* __restrict__ out, float* __restrict__ lse) {
+    __shared__ float4 sm_o[kJoinThreads / 32][32];
+    __shared__ float2 sm_ml[kJoinThreads / 32];
     pdl_wait();
     const int64_t q = blockIdx.x;
     const Pieces lists[2] = {{o_part, ml_part, q * splits, q * splits + 1, 1, splits}, {}};
-    join_row(lists, 1, out + q * kHeadDim, lse + q);
+    join_row<kJoinThreads / 32>(lists, 1, sm_o, sm_ml, out + q * kHeadDim, lse + q);
 }
 
 // An e4m3 pool as bytes [pages * kv heads * 16][128], in 16 x 128 boxes with the 128-byte swizzle.

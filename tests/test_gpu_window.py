@@ -184,6 +184,20 @@ def test_part_filled_row_tiles_repeat_exactly(group, fp8):
     assert binding.sv_get_device_error() == 0
 
 
+def test_workspace_at_sixteen_bytes_and_rows_inside_a_tensor():
+    case = PagedCase([500, 77], 2)
+    q = torch.randn((60, 6, DIM), generator=torch.Generator().manual_seed(1)).bfloat16().to(DEV)
+    first = run(case, q, 100, 4, [0, 50, 60])
+    need = binding.sv_window_attention_workspace_size(2, 6, 2, 60)
+    whole = torch.full((need + 16,), 0xFF, dtype=torch.uint8, device=DEV)
+    out, lse = torch.full((64, 6, DIM), 7.0, dtype=torch.bfloat16, device=DEV), torch.full((64, 6), 7.0, device=DEV)
+    binding.sv_window_attention(case.cache(), q, case.table.to(DEV), torch.tensor(case.lens, dtype=torch.int32, device=DEV), 100, 4,
+                                out[1:61], lse[1:61], whole[16:], q_start=torch.tensor([0, 50, 60], dtype=torch.int32, device=DEV))
+    torch.cuda.synchronize()
+    assert torch.equal(out[1:61], first[0]) and torch.equal(lse[1:61], first[1])
+    assert (out[:1] == 7).all() and (out[61:] == 7).all() and (lse[61:] == 7).all()
+
+
 def test_repeats_are_identical_and_replays_in_a_graph():
     case = PagedCase([3000, 500], 2)
     cache, table = case.cache(), case.table.to(DEV)

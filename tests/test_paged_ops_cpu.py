@@ -46,6 +46,7 @@ def test_window_attention_refuses(lib):
         assert call(**{name: None}) == SV_ERR_INVALID_ARG, name
     for name in ("q", "out", "ws"):
         assert call(**{name: ODD}) == SV_ERR_INVALID_ARG, name
+    assert call(out=ctypes.c_void_p(0x20010)) == SV_ERR_INVALID_ARG   # 32-byte aligned
     assert call(window=-1) == SV_ERR_INVALID_ARG
     assert call(sink=-1) == SV_ERR_INVALID_ARG
     assert call(total=-1) == SV_ERR_INVALID_ARG
