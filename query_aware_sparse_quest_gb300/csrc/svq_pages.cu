@@ -14,6 +14,11 @@
 // over the whole pool and what depends on it are one launch.  Moving page
 // data is a second launch over the whole GPU, one CTA at a time per page and
 // layer (34 KB for 4 kv heads), bound by HBM.
+//
+// Kernels are launched to overlap the end of the one before (a beam step of
+// three calls 33 -> 24 us), but each waits for it before its first access and
+// lets none after it start early: tables and lengths are inputs that later
+// kernels read as soon as they start.
 #include <climits>
 
 #include "svq_common.cuh"
@@ -192,6 +197,7 @@ __device__ __forceinline__ void copy_page(const CacheDesc& c, int64_t src, int64
 __global__ void __launch_bounds__(kMoveThreads) copy_pages_kernel(const __grid_constant__ CacheSet set,
                                                                   const int32_t* __restrict__ src,
                                                                   const int32_t* __restrict__ dst, int num_pages) {
+    pdl_wait();
     const int s = src[blockIdx.x], d = dst[blockIdx.x];
     if (s < 0 || s >= num_pages || d < 0 || d >= num_pages) {
         if (threadIdx.x == 0) svq_flag(SV_DEVERR_PAGE_TABLE);
@@ -206,13 +212,18 @@ struct ForkArgs {
     const int32_t* parents;
     const int32_t* children;
     int n;
-    int32_t* owner;      // [num_rows] first fork of a child row
+    int32_t* owner;      // [num_rows] first fork of a child row (large tables)
     int32_t* is_parent;  // [num_rows]
-    int32_t* rank;       // [n] free page a fork takes: its place among the forks that take one
-    int32_t* free;       // [n]
+    int32_t* who;        // [n] the forks that take a page, in order
+    int32_t* rank;       // [n] a fork's place among those, -1: it takes none
     int32_t* take;       // [n] page the fork got, kNone: needs none, kSkip: not made
 };
 constexpr int kNone = -1, kSkip = -2;
+// Rows listed twice are found by letting every list entry name itself at its
+// row and the lowest win: for tables up to this many rows in the shared memory
+// of the CTA that walks the list, for others in global memory by the whole
+// cluster (two more of its barriers).
+constexpr int kRowsHere = 4096;
 
 __device__ __forceinline__ bool row_ok(const Rows& t, int r) { return r >= 0 && r < t.num_rows; }
 
@@ -221,32 +232,53 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kPlanThreads)
     __shared__ int warp_sums[32];
     __shared__ int frees[kCluster];
     __shared__ int needed;
+    __shared__ int owner[kRowsHere];
+    __shared__ uint32_t is_parent[kRowsHere / 32];
     const int rank = cluster_rank();
     const int me = rank * kPlanThreads + threadIdx.x;
     constexpr int kAll = kCluster * kPlanThreads;
-    for (int i = me; i < a.n; i += kAll) {
-        const int c = a.children[i], p = a.parents[i];
-        if (row_ok(a.t, c)) a.owner[c] = INT_MAX, a.is_parent[c] = 0;
-        if (row_ok(a.t, p)) a.is_parent[p] = 0;
-    }
-    cluster_sync();
-    for (int i = me; i < a.n; i += kAll) {
-        const int c = a.children[i], p = a.parents[i];
-        if (row_ok(a.t, c)) atomicMin(&a.owner[c], i);
-        if (row_ok(a.t, p)) a.is_parent[p] = 1;
+    const bool here = a.t.num_rows <= kRowsHere;
+    pdl_wait();
+    cluster_sync();   // every CTA of the cluster is there before another writes its shared memory
+    if (!here) {
+        for (int i = me; i < a.n; i += kAll) {
+            const int c = a.children[i], p = a.parents[i];
+            if (row_ok(a.t, c)) a.owner[c] = INT_MAX, a.is_parent[c] = 0;
+            if (row_ok(a.t, p)) a.is_parent[p] = 0;
+        }
+        cluster_sync();
+        for (int i = me; i < a.n; i += kAll) {
+            const int c = a.children[i], p = a.parents[i];
+            if (row_ok(a.t, c)) atomicMin(&a.owner[c], i);
+            if (row_ok(a.t, p)) a.is_parent[p] = 1;
+        }
+        cluster_sync();
     }
     int lo, hi;
     slice(a.t.num_pages, rank, lo, hi);
     publish(count_free(a.t.counts, lo, hi), rank, warp_sums, frees);
-    cluster_sync();
     if (rank == 0) {
+        if (here) {
+            for (int r = threadIdx.x; r < a.t.num_rows; r += kPlanThreads) owner[r] = INT_MAX;
+            for (int r = threadIdx.x; r < kRowsHere / 32; r += kPlanThreads) is_parent[r] = 0;
+            __syncthreads();
+            for (int i = threadIdx.x; i < a.n; i += kPlanThreads) {
+                const int c = a.children[i], p = a.parents[i];
+                if (row_ok(a.t, c)) atomicMin(&owner[c], i);
+                if (row_ok(a.t, p)) atomicOr(&is_parent[p / 32], 1u << (p % 32));
+            }
+            __syncthreads();
+        }
         int base = 0;
         for (int i0 = 0; i0 < a.n; i0 += kPlanThreads) {
             const int i = i0 + threadIdx.x;
             int need = 0, take = kSkip;
             if (i < a.n) {
                 const int c = a.children[i], p = a.parents[i];
-                if (!row_ok(a.t, c) || !row_ok(a.t, p) || a.owner[c] != i || a.is_parent[c]) {
+                bool fine = row_ok(a.t, c) && row_ok(a.t, p);
+                if (fine)
+                    fine = here ? owner[c] == i && !((is_parent[c / 32] >> (c % 32)) & 1u) : a.owner[c] == i && !a.is_parent[c];
+                if (!fine) {
                     svq_flag(SV_DEVERR_ROW);
                 } else {
                     const int len = a.t.lens[p];
@@ -267,6 +299,7 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kPlanThreads)
             if (i < a.n) {
                 a.take[i] = take;
                 a.rank[i] = need ? r : -1;
+                if (need) a.who[r] = i;
             }
             base += total;
         }
@@ -278,21 +311,17 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kPlanThreads)
         if (r < rank) before += frees[r];
         all += frees[r];
     }
-    each_free(a.t.counts, lo, hi, before, needed, warp_sums, [&](int r, int p) { a.free[r] = p; });
-    cluster_sync();
+    // The r-th free page goes to the r-th fork that takes one (a CTA's scan is past the counts it changes).
+    each_free(a.t.counts, lo, hi, before, needed, warp_sums, [&](int r, int p) {
+        a.take[a.who[r]] = p;
+        a.t.counts[p] = 1;
+    });
     for (int i = me; i < a.n; i += kAll) {
-        const int r = a.rank[i];
-        if (r < 0) continue;
-        if (r < all) {
-            const int p = a.free[r];
-            a.take[i] = p;
-            a.t.counts[p] = 1;
-        } else {
+        if (a.rank[i] >= all) {
             a.take[i] = kSkip;
             svq_flag(SV_DEVERR_NO_PAGE);
         }
     }
-    cluster_sync();   // no CTA leaves while another may still write its shared memory
 }
 
 // CTAs below n: the child's row and the counts of the pages it shares.  The
@@ -332,10 +361,10 @@ struct ReserveArgs {
     int n;
     int32_t* slots;
     int num_slots;
-    int32_t* owner;     // [num_rows]
+    int32_t* owner;     // [num_rows] (large tables)
     int32_t* need;      // [n + 1] pages taken before each request
     int32_t* tok;       // [n + 1] tokens before each request
-    int32_t* ok;        // [n]
+    int32_t* len;       // [n] the row's length, -1: refused
     int32_t* free;      // [num_pages]
 };
 
@@ -345,32 +374,47 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kPlanThreads)
     __shared__ int frees[kCluster];
     __shared__ int needed, tokens;
     __shared__ int64_t wide_sums[32];
+    __shared__ int owner[kRowsHere];
     constexpr int64_t kMost = INT_MAX;
     const int rank = cluster_rank();
     const int me = rank * kPlanThreads + threadIdx.x;
     constexpr int kAll = kCluster * kPlanThreads;
-    for (int i = me; i < a.n; i += kAll)
-        if (row_ok(a.t, a.rows[i])) a.owner[a.rows[i]] = INT_MAX;
-    cluster_sync();
-    for (int i = me; i < a.n; i += kAll)
-        if (row_ok(a.t, a.rows[i])) atomicMin(&a.owner[a.rows[i]], i);
+    const bool here = a.t.num_rows <= kRowsHere;
+    pdl_wait();
+    cluster_sync();   // every CTA of the cluster is there before another writes its shared memory
+    if (!here) {
+        for (int i = me; i < a.n; i += kAll)
+            if (row_ok(a.t, a.rows[i])) a.owner[a.rows[i]] = INT_MAX;
+        cluster_sync();
+        for (int i = me; i < a.n; i += kAll)
+            if (row_ok(a.t, a.rows[i])) atomicMin(&a.owner[a.rows[i]], i);
+        cluster_sync();
+    }
     int lo, hi;
     slice(a.t.num_pages, rank, lo, hi);
     publish(count_free(a.t.counts, lo, hi), rank, warp_sums, frees);
-    cluster_sync();
     if (rank == 0) {
+        if (here) {
+            for (int r = threadIdx.x; r < a.t.num_rows; r += kPlanThreads) owner[r] = INT_MAX;
+            __syncthreads();
+            for (int i = threadIdx.x; i < a.n; i += kPlanThreads)
+                if (row_ok(a.t, a.rows[i])) atomicMin(&owner[a.rows[i]], i);
+            __syncthreads();
+        }
         // 64-bit sums; what is stored saturates past everything that can be served.
         int64_t pages = 0, toks = 0, total;
         for (int i0 = 0; i0 < a.n; i0 += kPlanThreads) {
             const int i = i0 + threadIdx.x;
-            int need = 0, add = 0, ok = 0;
+            int need = 0, add = 0, ok = 0, len = 0;
             if (i < a.n) {
                 const int r = a.rows[i];
                 add = max(0, a.add[i]);
-                if (!row_ok(a.t, r) || a.owner[r] != i || a.add[i] < 0) {
+                bool fine = row_ok(a.t, r) && a.add[i] >= 0;
+                if (fine) fine = (here ? owner[r] : a.owner[r]) == i;
+                if (!fine) {
                     svq_flag(SV_DEVERR_ROW);
                 } else {
-                    const int len = a.t.lens[r];
+                    len = a.t.lens[r];
                     const int64_t end = static_cast<int64_t>(len) + add;
                     if (!len_ok(a.t, len) || (end + kPage - 1) / kPage > a.t.max_pages) {
                         svq_flag(SV_DEVERR_SEQ_LEN);
@@ -397,7 +441,7 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kPlanThreads)
             const int64_t p0 = pages + block_scan(static_cast<int64_t>(need), wide_sums, total);
             pages += total;
             if (i < a.n) {
-                a.ok[i] = ok;
+                a.len[i] = ok ? len : -1;
                 a.tok[i] = static_cast<int>(min(t0, kMost));
                 a.need[i] = static_cast<int>(min(p0, kMost));
             }
@@ -415,19 +459,20 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kPlanThreads)
         if (r < rank) before += frees[r];
         all += frees[r];
     }
-    each_free(a.t.counts, lo, hi, before, min(needed, all), warp_sums, [&](int r, int p) { a.free[r] = p; });
-    cluster_sync();
     // A request gets its pages if all that it and those before it need are there.
-    auto granted = [&](int i) { return a.ok[i] && (a.need[i + 1] == a.need[i] || a.need[i + 1] <= all); };
-    const int most = min(needed, all);
-    for (int k = me; k < most; k += kAll) {
+    auto granted = [&](int i) { return a.len[i] >= 0 && (a.need[i + 1] == a.need[i] || a.need[i + 1] <= all); };
+    // The k-th free page (a CTA's scan is past the counts it changes).
+    each_free(a.t.counts, lo, hi, before, min(needed, all), warp_sums, [&](int k, int p) {
+        a.free[k] = p;
         const int i = find_le(a.need, a.n, k);
-        if (!granted(i)) continue;
-        const int r = a.rows[i];
-        const int at = (a.t.lens[r] + kPage - 1) / kPage + k - a.need[i];
-        const int p = a.free[k];
-        a.t.table[static_cast<int64_t>(r) * a.t.max_pages + at] = p;
+        if (!granted(i)) return;
+        const int at = (a.len[i] + kPage - 1) / kPage + k - a.need[i];
+        a.t.table[static_cast<int64_t>(a.rows[i]) * a.t.max_pages + at] = p;
         a.t.counts[p] = 1;
+    });
+    for (int i = me; i < a.n; i += kAll) {
+        if (granted(i)) a.t.lens[a.rows[i]] = a.len[i] + a.add[i];
+        else if (a.len[i] >= 0) svq_flag(SV_DEVERR_NO_PAGE);
     }
     cluster_sync();
     const int ntok = min(tokens, a.num_slots);
@@ -435,16 +480,12 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kPlanThreads)
         const int i = find_le(a.tok, a.n, k);
         int slot = -1;
         if (granted(i)) {
-            const int r = a.rows[i];
-            const int pos = a.t.lens[r] + k - a.tok[i];
-            slot = a.t.table[static_cast<int64_t>(r) * a.t.max_pages + pos / kPage] * kPage + pos % kPage;
+            const int pos = a.len[i] + k - a.tok[i], fresh = pos / kPage - (a.len[i] + kPage - 1) / kPage;
+            const int page = fresh >= 0 ? a.free[a.need[i] + fresh]
+                                        : a.t.table[static_cast<int64_t>(a.rows[i]) * a.t.max_pages + pos / kPage];
+            slot = page * kPage + pos % kPage;
         }
         a.slots[k] = slot;
-    }
-    cluster_sync();
-    for (int i = me; i < a.n; i += kAll) {
-        if (granted(i)) a.t.lens[a.rows[i]] += a.add[i];
-        else if (a.ok[i]) svq_flag(SV_DEVERR_NO_PAGE);
     }
 }
 
@@ -455,6 +496,7 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kPlanThreads)
 __global__ void __launch_bounds__(kMoveThreads) free_kernel(const __grid_constant__ Rows t, const int32_t* __restrict__ rows,
                                                             const int32_t* __restrict__ first,
                                                             const int32_t* __restrict__ end) {
+    pdl_wait();
     const int i = blockIdx.x;
     const int r = rows[i];
     if (!row_ok(t, r)) {
@@ -505,6 +547,8 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kPlanThreads)
     const int n = a.t.num_pages;
     int lo, hi;
     slice(n, rank, lo, hi);
+    pdl_wait();
+    cluster_sync();   // every CTA of the cluster is there before another writes its shared memory
     publish(count_free(a.t.counts, lo, hi), rank, warp_sums, frees);
     cluster_sync();
     int live = n;
@@ -586,7 +630,7 @@ __global__ void __launch_bounds__(kMoveThreads) compact_move_kernel(const __grid
     }
 }
 
-bool fill_set(CacheSet* set, const sv_cache* caches, int n) {
+void fill_set(CacheSet* set, const sv_cache* caches, int n) {
     set->n = n;
     for (int i = 0; i < n; ++i) {
         const sv_cache& c = caches[i];
@@ -596,17 +640,16 @@ bool fill_set(CacheSet* set, const sv_cache* caches, int n) {
                               fp8 ? static_cast<unsigned char*>(c.k_scale) : nullptr,
                               fp8 ? static_cast<unsigned char*>(c.v_scale) : nullptr, c.num_kv_heads, fp8 ? 128 : 256};
     }
-    return true;
 }
 
-int status() { return cudaGetLastError() == cudaSuccess ? SV_OK : SV_ERR_CUDA; }
+int launched(cudaError_t e) { return e == cudaSuccess ? SV_OK : SV_ERR_CUDA; }
 
 size_t up(size_t n) { return (n + 255) / 256 * 256; }
 
 }  // namespace
 
-// owner, is_parent, then five lists of n + 1 (fork: rank, free, take; reserve:
-// need, tok, ok), then three of num_pages (reserve: free; compact: src, dst,
+// owner, is_parent, then three lists of n + 1 (fork: who, rank, take; reserve:
+// need, tok, len), then three of num_pages (reserve: free; compact: src, dst,
 // to) and a word.
 size_t pages_workspace_bytes(int64_t num_pages, int num_rows, int n) {
     return 2 * up(4ull * num_rows) + 3 * up(4ull * (static_cast<size_t>(n) + 1)) + 3 * up(4ull * num_pages) + 256;
@@ -635,9 +678,8 @@ int launch_pages_copy(const sv_cache* caches, int num_caches, const int32_t* src
                       cudaStream_t stream) {
     CacheSet set;
     fill_set(&set, caches, num_caches);
-    copy_pages_kernel<<<dim3(n, num_caches), kMoveThreads, 0, stream>>>(set, src, dst,
-                                                                        static_cast<int>(caches[0].num_phys_pages));
-    return status();
+    return launched(launch_pdl(copy_pages_kernel, dim3(n, num_caches), dim3(kMoveThreads), 0, stream, set, src, dst,
+                               static_cast<int>(caches[0].num_phys_pages)));
 }
 
 int launch_pages_fork(const sv_cache* caches, int num_caches, int32_t* table, int32_t* lens, int num_rows, int max_pages,
@@ -649,11 +691,9 @@ int launch_pages_fork(const sv_cache* caches, int num_caches, int32_t* table, in
     const Carve w(ws, num_pages, num_rows, n);
     ForkArgs a = {{table, lens, num_rows, max_pages, counts, num_pages}, parents, children, n, w.owner, w.is_parent,
                   w.a, w.b, w.c};
-    fork_plan_kernel<<<kCluster, kPlanThreads, 0, stream>>>(a);
-    if (status()) return SV_ERR_CUDA;
-    return launch_pdl(fork_move_kernel, dim3(n, num_caches + 1), dim3(kMoveThreads), 0, stream, set, a) == cudaSuccess
-               ? SV_OK
-               : SV_ERR_CUDA;
+    const int st = launched(launch_pdl(fork_plan_kernel, dim3(kCluster), dim3(kPlanThreads), 0, stream, a));
+    if (st) return st;
+    return launched(launch_pdl(fork_move_kernel, dim3(n, num_caches + 1), dim3(kMoveThreads), 0, stream, set, a));
 }
 
 int launch_pages_reserve(int32_t* table, int32_t* lens, int num_rows, int max_pages, int32_t* counts, int num_pages,
@@ -662,15 +702,13 @@ int launch_pages_reserve(int32_t* table, int32_t* lens, int num_rows, int max_pa
     const Carve w(ws, num_pages, num_rows, n);
     ReserveArgs a = {{table, lens, num_rows, max_pages, counts, num_pages}, rows, add, n, slots, num_slots, w.owner,
                      w.a, w.b, w.c, w.p};
-    reserve_kernel<<<kCluster, kPlanThreads, 0, stream>>>(a);
-    return status();
+    return launched(launch_pdl(reserve_kernel, dim3(kCluster), dim3(kPlanThreads), 0, stream, a));
 }
 
 int launch_pages_free(int32_t* table, int32_t* lens, int num_rows, int max_pages, int32_t* counts, int num_pages,
                       const int32_t* rows, const int32_t* first, const int32_t* end, int n, cudaStream_t stream) {
     const Rows t = {table, lens, num_rows, max_pages, counts, num_pages};
-    free_kernel<<<n, kMoveThreads, 0, stream>>>(t, rows, first, end);
-    return status();
+    return launched(launch_pdl(free_kernel, dim3(n), dim3(kMoveThreads), 0, stream, t, rows, first, end));
 }
 
 int launch_pages_compact(const sv_cache* caches, int num_caches, const int32_t* table, const int32_t* lens, int num_rows,
@@ -683,11 +721,9 @@ int launch_pages_compact(const sv_cache* caches, int num_caches, const int32_t* 
     CompactArgs a = {{const_cast<int32_t*>(table), const_cast<int32_t*>(lens), num_rows, max_pages,
                       const_cast<int32_t*>(counts), num_pages},
                      table_out, counts_out, live, w.p, w.q, w.r, w.word};
-    compact_plan_kernel<<<kCluster, kPlanThreads, 0, stream>>>(a);
-    if (status()) return SV_ERR_CUDA;
-    return launch_pdl(compact_move_kernel, dim3(sm_count * 6), dim3(kMoveThreads), 0, stream, set, a) == cudaSuccess
-               ? SV_OK
-               : SV_ERR_CUDA;
+    const int st = launched(launch_pdl(compact_plan_kernel, dim3(kCluster), dim3(kPlanThreads), 0, stream, a));
+    if (st) return st;
+    return launched(launch_pdl(compact_move_kernel, dim3(sm_count * 6), dim3(kMoveThreads), 0, stream, set, a));
 }
 
 }  // namespace svq

@@ -112,7 +112,7 @@ class Device:
                 self.caches.append(binding.Cache(k.bfloat16(), v.bfloat16(), meta))
         self.first = [[None if x is None else x.clone() for x in self.parts(c)] for c in self.caches]
         self.list = binding.CacheList(self.caches)
-        self.ws = torch.full((binding.sv_pages_workspace_size(m.pool, len(m.lens), 256),), 0xFF, dtype=torch.uint8, device=DEV)
+        self.ws = torch.full((binding.sv_pages_workspace_size(m.pool, len(m.lens), 3000),), 0xFF, dtype=torch.uint8, device=DEV)
 
     @staticmethod
     def parts(c):
@@ -221,6 +221,29 @@ def test_exhausted_pool():
     d.same()
     d.fork([1, 0], [3, 2])                          # row 1 ends inside a page and none is left
     d.same(0x200)
+
+
+@pytest.mark.parametrize("n,rows", [(128, 257), (1300, 4096), (1300, 4097)])
+def test_long_lists(n, rows):
+    """Lists past one block, tables around the size where the check for repeated rows changes."""
+    d = Device(Model(4 * n + 40, rows, 5), heads=(1,), fp8=(False,))
+    d.reserve(list(range(n)), [1 + (7 * i) % 40 for i in range(n)])
+    d.same()
+    d.fork([(3 * i) % n for i in range(n)], list(range(n, 2 * n)))
+    d.same()
+    d.reserve(list(range(2 * n - 1, -1, -1)), [i % 3 for i in range(2 * n)])
+    d.same()
+    # the same row twice, at both ends of the list
+    slots = torch.full((n,), -99, dtype=torch.int32, device=DEV)
+    rows = list(range(n - 1)) + [0]
+    binding.sv_pages_reserve(d.table, d.lens, d.counts, ints(rows), ints([1] * n), slots, d.ws)
+    want = d.m.reserve(rows[:-1], [1] * (n - 1)) + [-1]
+    assert slots.tolist() == want
+    d.same(0x80)
+    d.free(list(range(n, 2 * n)))
+    binding.sv_pages_fork(d.list, d.table, d.lens, d.counts, ints([0] * n), ints(list(range(n, 2 * n - 1)) + [n]), d.ws)
+    d.m.fork([0] * (n - 1), list(range(n, 2 * n - 1)))
+    d.same(0x80)
 
 
 def test_refused_entries():
