@@ -130,14 +130,21 @@ struct AttendArgs {
     int splits;
 };
 
+// a / b for non-negative values that mostly fit 32 bits (a 64-bit division takes
+// several times as long).
+__device__ __forceinline__ int64_t div64(int64_t a, int64_t b) {
+    if (((a | b) >> 32) == 0) return static_cast<uint32_t>(a) / static_cast<uint32_t>(b);
+    return a / b;
+}
+
 // The share of CTA c: total / ctas of the cost each, the first total % ctas one more.
 struct Share {
     int64_t q, r;
-    __device__ __forceinline__ Share(int64_t total, int ctas) : q(total / ctas), r(total % ctas) {}
+    __device__ __forceinline__ Share(int64_t total, int ctas) : q(div64(total, ctas)), r(total - q * ctas) {}
     __device__ __forceinline__ int64_t start(int c) const { return c * q + (c < r ? c : r); }
     __device__ __forceinline__ int cta_of(int64_t x) const {
         const int64_t head = r * (q + 1);
-        return static_cast<int>(x < head ? x / (q + 1) : r + (x - head) / q);
+        return static_cast<int>(x < head ? div64(x, q + 1) : r + div64(x - head, q));
     }
 };
 
@@ -772,14 +779,14 @@ __global__ void __launch_bounds__(Cfg<FP8>::kThreads, 1)
             int e = 0, h = 0;                // entry (prefixes: of the group)
             int64_t off = 0;                 // into the item's cost
             if (left > 0) {
-                const int64_t u = first / a.num_kv_heads;
+                const int64_t u = div64(first, a.num_kv_heads);
                 int64_t before;
                 int cost;
                 if (prefix) {
                     grp = warp_groups(a.groups, a.tok_per_entry, total, nullptr,
                                       [u](int64_t b, int64_t c) { return b <= u && u < b + c; });
                     cost = cost_of(grp.tiles);
-                    e = static_cast<int>((u - grp.before) / cost);
+                    e = static_cast<int>(div64(u - grp.before, cost));
                     before = grp.before + static_cast<int64_t>(e) * cost;
                 } else {
                     e = warp_find(a.plan.cum, num_entries, u);
@@ -787,7 +794,7 @@ __global__ void __launch_bounds__(Cfg<FP8>::kThreads, 1)
                     cost = cost_of(a.plan.entries[e].tiles);
                 }
                 const int64_t in = first - before * a.num_kv_heads;
-                h = static_cast<int>(in / cost);
+                h = static_cast<int>(div64(in, cost));
                 off = in - static_cast<int64_t>(h) * cost;
             }
             const bool go_on = off > 0;      // the share begins inside an item
@@ -1507,13 +1514,15 @@ __global__ void __launch_bounds__(kCutThreads) join_cut_kernel(const __grid_cons
     }
 }
 
-// Prefixes: CTA per (request, query head) joins its prefix and what is behind it.
-constexpr int kPrefixThreads = 128;
+// Prefixes: CTA per (request, kv head) joins the rows' prefixes and what is
+// behind them; a row's pieces go in turn to 16 / group warps.  (A CTA a row
+// spent most of its time finding the pieces.)
+constexpr int kPrefixThreads = 512;
 
 __global__ void __launch_bounds__(kPrefixThreads) join_prefix_kernel(const __grid_constant__ AttendArgs a, int ctas) {
-    __shared__ float4 sm_o[kPrefixThreads / 32][32];
-    __shared__ float2 sm_ml[kPrefixThreads / 32];
-    const int b = blockIdx.x / a.num_q_heads, hq = blockIdx.x % a.num_q_heads;
+    constexpr int kWarps = kPrefixThreads / 32;
+    __shared__ RowSum parts[kWarps][32];
+    const int b = blockIdx.x / a.num_kv_heads, h = blockIdx.x % a.num_kv_heads;
     // Inputs: before the kernels before this one have ended.
     if (b < a.groups.start[0] || b >= a.groups.start[a.groups.n]) {   // not touched
         pdl_wait();
@@ -1523,26 +1532,36 @@ __global__ void __launch_bounds__(kPrefixThreads) join_prefix_kernel(const __gri
     const int page = page_behind(a.groups, b, a.seq_lens[b], fault);
     const int g = find_le(a.groups.start, a.groups.n, b);
     const int e = (b - a.groups.start[g]) / a.tok_per_entry, row = b - a.groups.start[g] - e * a.tok_per_entry;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int per_row = kWarps / a.group;
+    const int hr = warp / per_row, part = warp - hr * per_row;   // query head of the group, share of its pieces
     pdl_wait();
     const GroupRec rec = a.group_rec[g];
+    const int64_t total = a.group_rec[a.groups.n].before * a.num_kv_heads;
     if (!rec.sound) fault = SV_DEVERR_GROUP;
-    if (fault && hq == 0 && threadIdx.x == 0) svq_flag(fault);
-    const int64_t q = blockIdx.x;
-    Pieces lists[2];
-    int nl = 0;
-    if (page >= 0 && rec.sound) {
+    if (fault && h == 0 && threadIdx.x == 0) svq_flag(fault);
+    const int64_t q = static_cast<int64_t>(b) * a.num_q_heads + h * a.group + hr;
+    RowSum s;
+    if (hr < a.group && page >= 0 && rec.sound) {
+        int k0 = part;
         if (page > 0) {
-            const Share share(a.group_rec[a.groups.n].before * a.num_kv_heads, ctas);
-            const int h = hq / a.group, hr = hq - h * a.group;
+            const Share share(total, ctas);
             const int cost = cost_of(rec.tiles);
             const Placed it(share, (rec.before + static_cast<int64_t>(e) * cost) * a.num_kv_heads + static_cast<int64_t>(h) * cost,
                             rec.tiles);
-            if (it.c0 == it.c1) lists[nl++] = Pieces{a.whole_o, a.whole_ml, q, q, 0, 1};
-            else lists[nl++] = cut_pieces(a, share, it, row * a.group + hr);
+            const Pieces p = it.c0 == it.c1 ? Pieces{a.whole_o, a.whole_ml, q, q, 0, 1}
+                                            : cut_pieces(a, share, it, row * a.group + hr);
+            s.add(p, k0, per_row, lane);
+            k0 = (k0 + per_row - p.n % per_row) % per_row;
         }
-        lists[nl++] = Pieces{a.split_o, a.split_ml, q * a.splits, q * a.splits + 1, 1, a.splits};
+        s.add(Pieces{a.split_o, a.split_ml, q * a.splits, q * a.splits + 1, 1, a.splits}, k0, per_row, lane);
     }
-    join_row<kPrefixThreads / 32>(lists, nl, sm_o, sm_ml, a.out + q * kHeadDim, a.lse + q);
+    parts[warp][lane] = s;
+    __syncthreads();
+    if (part == 0 && hr < a.group) {
+        for (int u = 1; u < per_row; ++u) s.join(parts[warp + u][lane]);
+        s.write(a.out + q * kHeadDim, a.lse + q, lane);
+    }
 }
 
 // ---------------------------------------------------------------- host side
@@ -1705,7 +1724,7 @@ int launch_prefix(const sv_cache* c, const void* q, int num_q_heads, const int32
                                   shared_pages, num_groups, softmax_scale, a.splits, a.split_o, a.split_ml, stream);
     if (st) return st;
     if ((st = launch_tiles(c, a, ctas, stream))) return st;
-    return launch_pdl(join_prefix_kernel, dim3(static_cast<unsigned>(batch) * num_q_heads), dim3(kPrefixThreads), 0, stream,
+    return launch_pdl(join_prefix_kernel, dim3(static_cast<unsigned>(batch) * c->num_kv_heads), dim3(kPrefixThreads), 0, stream,
                       a, ctas) == cudaSuccess
                ? SV_OK
                : SV_ERR_CUDA;

@@ -136,6 +136,16 @@ struct RowSum {
             }
         }
     }
+    __device__ __forceinline__ void join(const RowSum& t) {
+        const float mn = fmaxf(m, t.m), base = mn == -INFINITY ? 0.f : mn;
+        const float e = ex2(m - base), f = ex2(t.m - base);
+        m = mn;
+        l = l * e + t.l * f;
+        o.x = o.x * e + t.o.x * f;
+        o.y = o.y * e + t.o.y * f;
+        o.z = o.z * e + t.o.z * f;
+        o.w = o.w * e + t.o.w * f;
+    }
     // The row of two pieces.
     __device__ __forceinline__ void add2(const float2 (&ml)[2], const float4 (&x)[2]) {
         m = fmaxf(ml[0].x, ml[1].x);
