@@ -8,7 +8,11 @@
  *   on_kv_stored(...)      -> sv_quest_update_meta  (store K/V, refresh page metadata)
  *   build_decode_view(q)   -> sv_quest_select       (query-aware page selection)
  *   generic attention      -> sv_sparse_decode      (attention over the view)
- * and sv_quest_decode_step runs the last two in one call.
+ * and sv_quest_decode_step runs the last two in one call.  Around them, over
+ * the same cache, page tables and lengths: sv_window_attention (prefill chunks
+ * and decode, causal or with a sliding window and sinks), sv_prefix_decode
+ * (dense decode of requests that share their first pages) and sv_pages_* (who
+ * holds which page: fork, reserve, free, compact, copy).
  *
  * Conventions common to every call
  *  - Every buffer argument is a DEVICE pointer, allocated and owned by the
@@ -26,9 +30,9 @@
  *  - `stream` is a cudaStream_t passed as void* (NULL = legacy default
  *    stream).  Calls enqueue kernels and return; they never synchronise.
  *  - Kernels are launched with programmatic dependent launch.  The scoring,
- *    top-K and attention kernels read the call's q, page_table and seq_lens,
- *    and the append kernel its slot_mapping, k_new and v_new, as soon as
- *    they start, possibly while the kernel enqueued just before them is
+ *    top-K and attention kernels read the call's q, page_table, seq_lens,
+ *    group_start and shared_pages, and the append kernel its slot_mapping,
+ *    k_new and v_new, as soon as they start, possibly while the kernel enqueued just before them is
  *    still running.  Pools, metadata and workspace are touched only
  *    after that kernel has completed.  So the kernel that produces a
  *    call's inputs must not release its dependents early
@@ -85,7 +89,9 @@ enum sv_status {
 #define SV_DEVERR_SLOT       0x4u   /* slot_mapping entry outside the pool */
 #define SV_DEVERR_SEQ_LEN    0x8u   /* seq_lens[b] < 1 or needs more than max_pages pages */
 #define SV_DEVERR_TIMEOUT    0x10u  /* a kernel gave up a wait on its own bulk copies after
-                                       2^28 SM clock cycles */
+                                       2^28 SM clock cycles (the tiles of sv_window_attention
+                                       and sv_prefix_decode: on its copies or its other warps,
+                                       after half a second) */
 #define SV_DEVERR_Q_START    0x20u  /* q_start not ascending inside [0, total_q], or a chunk longer than its
                                        request */
 #define SV_DEVERR_GROUP      0x40u  /* group_start not ascending inside [0, batch], or shared_pages negative or

@@ -426,7 +426,11 @@ int sv_window_attention(const sv_cache* cache, const void* q, int32_t num_q_head
                         int32_t total_q, const int32_t* page_table, const int32_t* seq_lens, int32_t batch,
                         int32_t max_pages, int32_t window, int32_t sink_tokens, float softmax_scale, void* out,
                         float* lse, void* workspace, size_t workspace_bytes, void* stream) {
-    int st = attend_checks(cache, q, num_q_heads, page_table, seq_lens, batch, max_pages, softmax_scale, out, lse);
+    int st = check_cache(cache);
+    if (st) return st;
+    if ((st = check_heads(cache, num_q_heads))) return st;
+    if (q_start && total_q == 0) return SV_OK;   // nothing to do; an empty tensor has no address
+    st = attend_checks(cache, q, num_q_heads, page_table, seq_lens, batch, max_pages, softmax_scale, out, lse);
     if (st) return st;
     if (window < 0 || sink_tokens < 0 || total_q < 0) return SV_ERR_INVALID_ARG;
     if (reinterpret_cast<uintptr_t>(out) & 31u) return SV_ERR_INVALID_ARG;   // rows are written 32 bytes at a time
@@ -435,7 +439,6 @@ int sv_window_attention(const sv_cache* cache, const void* q, int32_t num_q_head
     if (!workspace || workspace_bytes < sv_window_attention_workspace_size(batch, num_q_heads, cache->num_kv_heads, total_q))
         return SV_ERR_WORKSPACE;
     if (!aligned16(workspace)) return SV_ERR_INVALID_ARG;
-    if (total_q == 0) return SV_OK;
     int sms = 0;
     if ((st = sm_count_of_current_device(&sms))) return st;
     return launch_window(cache, q, num_q_heads, q_start, total_q, page_table, seq_lens, batch, max_pages, window,
@@ -561,6 +564,6 @@ const char* sv_status_string(int status) {
     }
 }
 
-int sv_version(void) { return 100; }
+int sv_version(void) { return 110; }
 
 }  // extern "C"

@@ -127,3 +127,39 @@ def test_bad_page_is_masked():
     out, lse = run(case, q, [0, 2], [3])
     assert binding.sv_get_device_error() == 0x1
     check(out, lse, [torch.cat(x) for x in zip(*ref)])
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+def test_repeats_and_graph(fp8):
+    """Calls in a row on one workspace, and a captured one with other lengths, give what a call alone gives."""
+    starts, shared = [0, 20, 23], [30, 4]
+    lens = [30 * PAGE + 7 * i for i in range(20)] + [4 * PAGE + 3 * i for i in range(3)]
+    case = PagedCase(lens, 2, fp8=fp8, max_pages=50)
+    share(case, starts, shared)
+    q = queries(case, 7)
+    first = run(case, q, starts, shared)
+    cache, table, gs, sp, ls = case.cache(), case.table.to(DEV), ints(starts), ints(shared), ints(lens)
+    ws = torch.full((binding.sv_prefix_decode_workspace_size(23, 14, 2, 2),), 0xFF, dtype=torch.uint8, device=DEV)
+    out, lse = torch.empty_like(q), torch.empty((23, 14), device=DEV)
+
+    def call():
+        binding.sv_prefix_decode(cache, q, table, ls, gs, sp, out, lse, ws)
+    for _ in range(20):
+        call()
+    torch.cuda.synchronize()
+    assert torch.equal(out, first[0]) and torch.equal(lse, first[1])
+    side, graph = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.graph(graph, stream=side):
+        for _ in range(3):
+            call()
+    out.zero_()
+    graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(out, first[0]) and torch.equal(lse, first[1])
+    # other groups in the same graph: everyone for itself
+    sp.zero_()
+    graph.replay()
+    torch.cuda.synchronize()
+    check(out, lse, reference(case, q, range(23)))
+    assert binding.sv_get_device_error() == 0

@@ -229,3 +229,41 @@ def test_repeats_are_identical_and_replays_in_a_graph():
     torch.cuda.synchronize()
     assert torch.equal(out, first[0]) and torch.equal(lse, first[1])
     assert binding.sv_get_device_error() == 0
+
+
+def test_empty_calls():
+    case = PagedCase([50], 2)
+    q = torch.empty((0, 8, DIM), dtype=torch.bfloat16, device=DEV)
+    out, lse = run(case, q, 0, 0, [0, 0])
+    assert out.shape == (0, 8, DIM) and binding.sv_get_device_error() == 0
+
+
+def test_two_streams_at_once():
+    """Two calls with workspaces of their own, at the same time on two streams."""
+    cases = [PagedCase([3000, 70], 2, seed=1), PagedCase([900] * 20, 2, fp8=True, seed=2)]
+    sizes = [[500, 3], [30] * 20]
+    args = []
+    for case, size in zip(cases, sizes):
+        T, B = sum(size), len(size)
+        q = torch.randn((T, 8, DIM), device=DEV).bfloat16()
+        args.append(dict(cache=case.cache(), q=q, page_table=case.table.to(DEV), window=256, sink_tokens=4,
+                         seq_lens=torch.tensor(case.lens, dtype=torch.int32, device=DEV),
+                         q_start=torch.tensor([sum(size[:b]) for b in range(B + 1)], dtype=torch.int32, device=DEV),
+                         workspace=torch.empty(binding.sv_window_attention_workspace_size(B, 8, 2, T), dtype=torch.uint8, device=DEV)))
+    alone = []
+    for a in args:
+        o = torch.empty_like(a["q"]), torch.empty(a["q"].shape[:2], device=DEV)
+        binding.sv_window_attention(**a, out=o[0], lse=o[1])
+        alone.append(o)
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    for _ in range(5):
+        both = [(torch.empty_like(a["q"]), torch.empty(a["q"].shape[:2], device=DEV)) for a in args]
+        torch.cuda.synchronize()
+        for _ in range(4):
+            for a, o, st in zip(args, both, streams):
+                binding.sv_window_attention(**a, out=o[0], lse=o[1], stream=st)
+        torch.cuda.synchronize()
+        for o, r in zip(both, alone):
+            assert torch.equal(o[0], r[0]) and torch.equal(o[1], r[1])
+    assert binding.sv_get_device_error() == 0

@@ -66,6 +66,8 @@ def test_window_attention_refuses(lib):
     assert call(ws=None) == SV_ERR_WORKSPACE
     assert call(ws_bytes=binding.sv_window_attention_workspace_size(8, 32, 4, 100) - 1) == SV_ERR_WORKSPACE
     assert call(total=0) == SV_OK                                   # nothing to do, nothing launched
+    assert call(total=0, q=None, out=None, lse=None, ws=None) == SV_OK   # empty tensors have no address
+    assert call(total=0, hq=30) == SV_ERR_INVALID_ARG
 
 
 @host_only
