@@ -350,9 +350,10 @@ size_t sv_quest_decode_step_workspace_size(int32_t batch, int32_t num_q_heads, i
  *    as masked.
  *  - Only page table entries of visible tokens are read, so the pages behind a
  *    window may have been freed (sv_pages_free) and their entries be -1.
- *  - A K/V row that no query token of the call sees may hold anything.  One
- *    that some see has to be finite: an infinite or NaN value may also reach
- *    query tokens of the same request that do not see it.
+ *  - A K/V row may hold anything as far as the query tokens that do not see
+ *    it are concerned: infinite and NaN values reach only those that do.  (A
+ *    value seen by some query tokens of a row tile and not by others is put
+ *    right afterwards, a row at a time: slow, and only then.)
  *  - Rows of one request and kv head are processed 256 at a time
  *    (token, query head), on the tensor cores; work is divided evenly over
  *    the GPU whatever the lengths.  The result does not depend on timing.

@@ -121,7 +121,10 @@ struct AttendArgs {
     float2* cut_ml;    // [2 CTAs][slot_rows] (base in log2 units, sum)
     struct GroupRec* group_rec;   // prefixes: [groups + 1], for the join; the last one's cost is the total
     int4* cut_item;    // chunks: [CTAs][2] the item that goes on in a CTA: row0, ntok, kv head, pieces (0: none is to
-                       // be joined here); slot of the first piece, and of the second
+                       // be joined here); slot of the first piece, of the second, and the entry
+    int2* odd;         // chunks: 32-row parts of whole items with a channel that is not finite: entry, kv head * 256 + row
+    int* num_odd;
+    bool fp8;
     int slot_rows;
     float* whole_o;    // prefixes: the parts of whole items, [B Hq][128]; else null
     float2* whole_ml;
@@ -384,7 +387,7 @@ struct __align__(16) Seg {
     Entry en;
     int h;            // kv head
     int t0, t1;       // tiles of the item
-    int slot;         // where a partial goes; -1: the segment is the whole item
+    int slot;         // where a partial goes; -1 - entry: the segment is the whole item
 };
 constexpr int kSegs = 4;
 
@@ -834,6 +837,7 @@ __global__ void __launch_bounds__(Cfg<FP8>::kThreads, 1)
                                 what = make_int4(en.row0, en.ntok, h, it.c1 - it.c0 + 1);
                                 where.x = 2 * it.c0 + (share.start(it.c0) >= it.begin ? 0 : 1);
                                 where.y = 2 * (it.c0 + 1);
+                                where.z = e;
                             }
                         }
                         a.cut_item[2 * blockIdx.x] = what;
@@ -853,7 +857,7 @@ __global__ void __launch_bounds__(Cfg<FP8>::kThreads, 1)
                         s.h = h;
                         s.t0 = t0;
                         s.t1 = t1;
-                        s.slot = t0 == 0 && t1 == en.tiles ? -1 : static_cast<int>(blockIdx.x) * 2 + (first_item ? 0 : 1);
+                        s.slot = t0 == 0 && t1 == en.tiles ? -1 - e : static_cast<int>(blockIdx.x) * 2 + (first_item ? 0 : 1);
                         mbar_arrive(smem_addr(&ct->seg_full[k % kSegs]));
                     }
                     ++k;
@@ -1153,6 +1157,7 @@ __global__ void __launch_bounds__(Cfg<FP8>::kThreads, 1)
                     const float inv = po ? 1.f : (L > 0.f ? 1.f / L : (L == 0.f ? 0.f : L));
                     f0 *= inv;
                     f1 *= inv;
+                    float odd = 0.f;   // NaN once a channel of the row is not finite
                     // Two halves: the whole row of the own stream.  Joined: 64 channels of both.
 #pragma unroll 1
                     for (int c = 0; c < 4; ++c) {
@@ -1179,6 +1184,8 @@ __global__ void __launch_bounds__(Cfg<FP8>::kThreads, 1)
                             } else {
                                 uint32_t v[16];
 #pragma unroll
+                                for (int u = 0; u < 32; ++u) odd = fmaf(__uint_as_float(x[u]), 0.f, odd);
+#pragma unroll
                                 for (int u = 0; u < 16; ++u)
                                     v[u] = pack_bf16x2(__uint_as_float(x[2 * u]), __uint_as_float(x[2 * u + 1]));
 #pragma unroll
@@ -1188,6 +1195,8 @@ __global__ void __launch_bounds__(Cfg<FP8>::kThreads, 1)
                             }
                         }
                     }
+                    if (!po && __any_sync(0xffffffffu, odd != 0.f && L < INFINITY) && lane == 0)
+                        a.odd[atomicAdd(a.num_odd, 1)] = make_int2(-1 - s.slot, s.h * kRowTile + off + (warp & 3) * 32);
                     if (valid && (two || w == 0)) {
                         if (po) *pml = make_float2(M, L);
                         else a.lse[qrow] = L > 0.f ? (M + log2f(L)) * 0.69314718055994531f : (L == 0.f ? -INFINITY : L);
@@ -1307,6 +1316,7 @@ __global__ void __launch_bounds__(Cfg<FP8>::kThreads, 1)
 // ---------------------------------------------------------------- plan
 struct PlanArgs {
     Plan plan;
+    int* num_odd;
     int max_entries;
     int tok_per_entry;          // query tokens of a row tile: kRowTile / group
     const int32_t* q_start;
@@ -1435,6 +1445,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const __grid_constan
     if (tid == 0) {
         p.plan.cum[n] = base;
         *p.plan.num_entries = n;
+        *p.num_odd = 0;
     }
 }
 
@@ -1451,21 +1462,96 @@ __device__ __forceinline__ Pieces cut_pieces(const AttendArgs& a, const Share& s
     return p;
 }
 
+// A row of an entry whose outputs may not be finite, by one warp.  The tile's
+// product multiplies every value of the tile with a weight, and a weight 0 does
+// not hide an infinite or NaN value from the rows that do not see its token.  So
+// if the row's logits are finite, its outputs are not, and a token that other
+// rows of the entry see and this one does not holds such a value, the row is
+// computed again from its own tokens alone, at 10 us a page and row (loads four
+// tokens at a time would be no faster and their registers cost every join 2 us
+// of 212).  Finding such rows costs a call without them 1 to 1.5 us of 210.
+__device__ __noinline__ void look_at_row(const AttendArgs& a, int entry, int h, int r) {
+    const int lane = threadIdx.x & 31;
+    const Entry en = a.plan.entries[entry];
+    const int tok = r / a.group, pos = en.pos0 + tok, end = en.pos0 + en.ntok;
+    const int64_t qrow = static_cast<int64_t>(en.row0 + tok) * a.num_q_heads + h * a.group + (r - tok * a.group);
+    {
+        const uint2 w = *reinterpret_cast<const uint2*>(a.out + qrow * kHeadDim + 4 * lane);
+        const float odd = fmaf(bf16lo(w.x), 0.f, fmaf(bf16hi(w.x), 0.f, fmaf(bf16lo(w.y), 0.f, bf16hi(w.y) * 0.f)));
+        if (!(fabsf(a.lse[qrow]) < INFINITY) || !__any_sync(0xffffffffu, odd != 0.f)) return;
+    }
+    const int32_t* const pages = a.page_table + static_cast<int64_t>(en.req) * a.max_pages;
+    // Four channels of a token's row of a pool.
+    auto row_of = [&](const unsigned char* pool, const float* scale, int64_t at) {
+        uint2 w;
+        if (!a.fp8) {
+            w = *reinterpret_cast<const uint2*>(pool + at * (2 * kHeadDim) + 8 * lane);
+            return make_float4(bf16lo(w.x), bf16hi(w.x), bf16lo(w.y), bf16hi(w.y));
+        }
+        const uint32_t c = *reinterpret_cast<const uint32_t*>(pool + at * kHeadDim + 4 * lane);
+        widen4(c, w.x, w.y);
+        keep_nan(c, w.x, w.y);
+        const float f = scale[at];
+        return make_float4(bf16lo(w.x) * f, bf16hi(w.x) * f, bf16lo(w.y) * f, bf16hi(w.y) * f);
+    };
+    auto place_of = [&](int page) {   // the first token's row in the pools; -1: the table gives no page
+        const int ph = pages[page];
+        return ph < 0 || ph >= a.num_phys_pages ? -1ll : (static_cast<int64_t>(ph) * a.num_kv_heads + h) * kPage;
+    };
+    // Tokens [t0, t1) that other rows may see and this one does not.
+    auto finite = [&](int t0, int t1) {
+        float odd = 0.f;
+        for (int t = t0; t < t1; ++t) {
+            const int64_t at = place_of(t / kPage);
+            if (at < 0) continue;
+            const float4 v = row_of(a.v_pool, a.v_scale, at + t % kPage);
+            odd = fmaf(v.x, 0.f, fmaf(v.y, 0.f, fmaf(v.z, 0.f, fmaf(v.w, 0.f, odd))));
+        }
+        return !__any_sync(0xffffffffu, odd != 0.f);
+    };
+    const bool later = finite(pos + 1, end);
+    const bool passed = finite(max(a.sink, max(0, en.pos0 - a.window + 1)), max(0, pos - a.window + 1));
+    if (later && passed) return;   // the row's own tokens gave it
+    float4 q;
+    {
+        const uint2 w = *reinterpret_cast<const uint2*>(a.q + qrow * kHeadDim + 4 * lane);
+        q = make_float4(bf16lo(w.x), bf16hi(w.x), bf16lo(w.y), bf16hi(w.y));
+    }
+    RowSum s;
+    for (int i = 0; i < en.npages; ++i) {
+        const int page = logical_page(en, i);
+        const uint32_t seen = page_mask(page * kPage, pos, a.window, a.sink);
+        const int64_t at = place_of(page);
+        if (at < 0) continue;
+        for (uint32_t rest = seen; rest; rest &= rest - 1) {
+            const int t = __ffs(rest) - 1;
+            const float4 k = row_of(a.k_pool, a.k_scale, at + t), v = row_of(a.v_pool, a.v_scale, at + t);
+            float z = q.x * k.x + q.y * k.y + q.z * k.z + q.w * k.w;
+#pragma unroll
+            for (int d = 16; d; d >>= 1) z += __shfl_xor_sync(0xffffffffu, z, d);
+            s.join(RowSum{z * a.scale_log2, 1.f, v});
+        }
+    }
+    (void)s.write(a.out + qrow * kHeadDim, a.lse + qrow, lane);
+}
+
 // Chunks: CTA (c, y) joins the item that attend CTA c + 1 goes on with; rows y,
-// y + gridDim.y, ... (of 8 warps each, when the pieces are few).
+// y + gridDim.y, ... (of 8 warps each, when the pieces are few).  Then the parts
+// of whole items with rows that are not finite.
 constexpr int kCutThreads = 256;
 
-__global__ void __launch_bounds__(kCutThreads) join_cut_kernel(const __grid_constant__ AttendArgs a) {
+__global__ void __launch_bounds__(kCutThreads, 4) join_cut_kernel(const __grid_constant__ AttendArgs a) {
     constexpr int kWarps = kCutThreads / 32;
     __shared__ float4 sm_o[kWarps][32];
     __shared__ float2 sm_ml[kWarps];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     pdl_wait();
     const int4 what = a.cut_item[2 * (blockIdx.x + 1)];
+    const int num_odd = *a.num_odd;
     const int n = what.w;
-    if (n == 0) return;
-    const int4 where = a.cut_item[2 * (blockIdx.x + 1) + 1];
-    const int rows = what.y * a.group;
+    if (n == 0 && num_odd == 0) return;
+    const int4 where = n ? a.cut_item[2 * (blockIdx.x + 1) + 1] : what;
+    const int rows = n ? what.y * a.group : 0;
     auto at_row = [&](int r) {
         const int tok = r / a.group;
         return static_cast<int64_t>(what.x + tok) * a.num_q_heads + what.z * a.group + (r - tok * a.group);
@@ -1474,6 +1560,9 @@ __global__ void __launch_bounds__(kCutThreads) join_cut_kernel(const __grid_cons
         return Pieces{a.cut_o, a.cut_ml, static_cast<int64_t>(where.x) * a.slot_rows + r,
                       static_cast<int64_t>(where.y) * a.slot_rows + r, 2ll * a.slot_rows, n};
     };
+    // Rows that are not finite are looked at behind the loops (a call inside them costs 3 us of 212).
+    bool odd = false;
+    auto write = [&](const RowSum& s, int r) { odd |= s.write(a.out + at_row(r) * kHeadDim, a.lse + at_row(r), lane); };
     if (n <= 8) {   // few pieces: a warp a row, four rows at a time in flight when there are two
         const int step = gridDim.y * kWarps;
         for (int r0 = blockIdx.y * kWarps + warp; r0 < rows; r0 += 4 * step) {
@@ -1491,10 +1580,9 @@ __global__ void __launch_bounds__(kCutThreads) join_cut_kernel(const __grid_cons
                 }
 #pragma unroll
                 for (int u = 0; u < 4; ++u) {
-                    const int r = r0 + u * step;
                     RowSum s;
                     s.add2(ml[u], x[u]);
-                    if (r < rows) s.write(a.out + at_row(r) * kHeadDim, a.lse + at_row(r), lane);
+                    if (r0 + u * step < rows) write(s, r0 + u * step);
                 }
             } else {
                 for (int u = 0; u < 4; ++u) {
@@ -1502,15 +1590,23 @@ __global__ void __launch_bounds__(kCutThreads) join_cut_kernel(const __grid_cons
                     if (r >= rows) break;
                     RowSum s;
                     s.add(pieces(r), 0, 1, lane);
-                    s.write(a.out + at_row(r) * kHeadDim, a.lse + at_row(r), lane);
+                    write(s, r);
                 }
             }
         }
-        return;
+    } else {
+        for (int r = blockIdx.y; r < rows; r += gridDim.y)
+            odd |= join_row<kWarps>(pieces(r), sm_o, sm_ml, a.out + at_row(r) * kHeadDim, a.lse + at_row(r));
     }
-    for (int r = blockIdx.y; r < rows; r += gridDim.y) {
-        const Pieces lists[2] = {pieces(r), {}};
-        join_row<kWarps>(lists, 1, sm_o, sm_ml, a.out + at_row(r) * kHeadDim, a.lse + at_row(r));
+    if (__any_sync(0xffffffffu, odd)) {   // of the rows this warp wrote
+        for (int r = n <= 8 ? blockIdx.y * kWarps + warp : blockIdx.y; r < rows; r += n <= 8 ? gridDim.y * kWarps : gridDim.y)
+            look_at_row(a, where.z, what.z, r);
+    }
+    constexpr int kTurns = 32 / kWarps;   // a warp a row
+    for (int64_t i = blockIdx.y * gridDim.x + blockIdx.x; i < static_cast<int64_t>(num_odd) * kTurns; i += gridDim.x * gridDim.y) {
+        const int2 part = a.odd[i / kTurns];
+        const int r = part.y % kRowTile + static_cast<int>(i % kTurns) * kWarps + warp;
+        if (r < a.plan.entries[part.x].ntok * a.group) look_at_row(a, part.x, part.y / kRowTile, r);
     }
 }
 
@@ -1571,7 +1667,7 @@ __global__ void __launch_bounds__(kPrefixThreads) join_prefix_kernel(const __gri
 size_t up(size_t n) { return (n + 255) / 256 * 256; }
 
 struct Layout {
-    size_t entries, cum, num, req_offset, group_rec, cut_item, cut_o, cut_ml, whole_o, whole_ml, split_o, split_ml, total;
+    size_t entries, cum, num, req_offset, odd, num_odd, group_rec, cut_item, cut_o, cut_ml, whole_o, whole_ml, split_o, split_ml, total;
     int max_entries, slot_rows;
     // rows: query tokens; num_groups: 0 for chunks
     Layout(int64_t batch, int64_t rows, int num_q_heads, int num_kv_heads, int num_groups) {
@@ -1596,6 +1692,9 @@ struct Layout {
         whole_ml = take(heads * sizeof(float2));
         split_o = take(parts * kHeadDim * sizeof(float));
         split_ml = take(parts * sizeof(float2));
+        // A warp's 32 rows of an item each.  Behind all that every call touches (in front of it: 92.8 against 90.7 us).
+        odd = take(8 * e * num_kv_heads * sizeof(int2));
+        num_odd = take(sizeof(int));
         total = at + 256;   // the parts begin at the workspace's first multiple of 256 (rows are written 32 bytes at a time)
     }
 };
@@ -1650,6 +1749,9 @@ AttendArgs attend_args(const sv_cache* c, const void* q, int num_q_heads, const 
     a.cut_o = reinterpret_cast<float*>(ws + lay.cut_o);
     a.cut_ml = reinterpret_cast<float2*>(ws + lay.cut_ml);
     a.cut_item = reinterpret_cast<int4*>(ws + lay.cut_item);
+    a.odd = reinterpret_cast<int2*>(ws + lay.odd);
+    a.num_odd = reinterpret_cast<int*>(ws + lay.num_odd);
+    a.fp8 = c->kv_format == SV_KV_FP8_E4M3;
     a.slot_rows = lay.slot_rows;
     return a;
 }
@@ -1697,7 +1799,7 @@ int launch_window(const sv_cache* c, const void* q, int num_q_heads, const int32
     }
     const Layout lay(batch, total_q, num_q_heads, c->num_kv_heads, 0);
     const AttendArgs a = attend_args(c, q, num_q_heads, page_table, max_pages, lay, window, sink, softmax_scale, out, lse, workspace);
-    const PlanArgs p = {a.plan, lay.max_entries, a.tok_per_entry, q_start, total_q, seq_lens, batch, max_pages,
+    const PlanArgs p = {a.plan, a.num_odd, lay.max_entries, a.tok_per_entry, q_start, total_q, seq_lens, batch, max_pages,
                         a.window, sink, num_q_heads, a.out, lse};
     if (launch_pdl(plan_kernel, dim3(1), dim3(kPlanThreads), 0, stream, p) != cudaSuccess) return SV_ERR_CUDA;
     const int st = launch_tiles(c, a, ctas, stream);

@@ -157,27 +157,28 @@ struct RowSum {
         o.z = x[0].z * e + x[1].z * f;
         o.w = x[0].w * e + x[1].w * f;
     }
-    __device__ __forceinline__ void write(__nv_bfloat16* out, float* lse, int lane) const {
+    // Returns whether one of the lane's channels is not finite although the sum is.
+    __device__ __forceinline__ bool write(__nv_bfloat16* out, float* lse, int lane) const {
         const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);
         uint2 v;
         v.x = pack_bf16x2(o.x * inv, o.y * inv);
         v.y = pack_bf16x2(o.z * inv, o.w * inv);
         *reinterpret_cast<uint2*>(out + 4 * lane) = v;
         if (lane == 0) *lse = l > 0.f ? (m + log2f(l)) * 0.69314718055994531f : (l == 0.f ? -INFINITY : l);
+        const float odd = fmaf(o.x, 0.f, fmaf(o.y, 0.f, fmaf(o.z, 0.f, o.w * 0.f)));
+        return odd != 0.f && l < INFINITY;
     }
 };
 
-// One row by a CTA of kWarps warps, which take the pieces in turn.
+// One row by a CTA of kWarps warps, which take the pieces in turn.  Returns what
+// RowSum::write does, to the first warp.
 template <int kWarps>
-__device__ __forceinline__ void join_row(const Pieces (&lists)[2], int nlists, float4 (&sm_o)[kWarps][32],
-                                         float2 (&sm_ml)[kWarps], __nv_bfloat16* out, float* lse) {
+__device__ __forceinline__ bool join_row(const Pieces& pieces, float4 (&sm_o)[kWarps][32], float2 (&sm_ml)[kWarps],
+                                         __nv_bfloat16* out, float* lse) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    bool odd = false;
     RowSum s;
-    int k0 = warp;
-    for (int li = 0; li < nlists; ++li) {
-        s.add(lists[li], k0, kWarps, lane);
-        k0 = (k0 + kWarps - lists[li].n % kWarps) % kWarps;   // the next list goes on where this one ended
-    }
+    s.add(pieces, warp, kWarps, lane);
     sm_o[warp][lane] = s.o;
     if (lane == 0) sm_ml[warp] = make_float2(s.m, s.l);
     __syncthreads();
@@ -194,9 +195,10 @@ __device__ __forceinline__ void join_row(const Pieces (&lists)[2], int nlists, f
             t.o.z += sm_o[u][lane].z * f;
             t.o.w += sm_o[u][lane].w * f;
         }
-        t.write(out, lse, lane);
+        odd = t.write(out, lse, lane);
     }
     __syncthreads();   // the shared arrays are written again for the next row
+    return odd;
 }
 
 }  // namespace

@@ -441,8 +441,8 @@ __global__ void __launch_bounds__(kJoinThreads) join_splits_kernel(const float* 
     __shared__ float2 sm_ml[kJoinThreads / 32];
     pdl_wait();
     const int64_t q = blockIdx.x;
-    const Pieces lists[2] = {{o_part, ml_part, q * splits, q * splits + 1, 1, splits}, {}};
-    join_row<kJoinThreads / 32>(lists, 1, sm_o, sm_ml, out + q * kHeadDim, lse + q);
+    const Pieces pieces = {o_part, ml_part, q * splits, q * splits + 1, 1, splits};
+    (void)join_row<kJoinThreads / 32>(pieces, sm_o, sm_ml, out + q * kHeadDim, lse + q);
 }
 
 // An e4m3 pool as bytes [pages * kv heads * 16][128], in 16 x 128 boxes with the 128-byte swizzle.

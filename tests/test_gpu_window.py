@@ -267,3 +267,41 @@ def test_two_streams_at_once():
         for o, r in zip(both, alone):
             assert torch.equal(o[0], r[0]) and torch.equal(o[1], r[1])
     assert binding.sv_get_device_error() == 0
+
+
+@pytest.mark.parametrize("fp8,poison", [(False, "nan"), (False, "inf"), (True, "nan"), (True, "scale")])
+@pytest.mark.parametrize("lens,sizes,group,window,sink", [
+    ([300], [300], 8, 0, 0),
+    ([2000], [500], 4, 300, 37),
+    ([2000], [500], 1, 300, 37),
+    ([40] * 100, [40] * 100, 4, 0, 0),           # whole items
+    ([20000], [9], 8, 0, 0),                     # an item in many pieces
+    ([700, 5, 1, 333], [650, 5, 1, 64], 7, 128, 3),
+])
+def test_values_that_are_not_finite_stay_with_the_rows_that_see_them(lens, sizes, group, window, sink, fp8, poison):
+    case = PagedCase(lens, 2, fp8=fp8)
+    g = torch.Generator().manual_seed(3)
+    q = torch.randn((sum(sizes), 2 * group, DIM), generator=g).bfloat16().to(DEV)
+    seen = [window_seen(n, sizes[b], window, sink, DEV) for b, n in enumerate(lens)]
+    ref = [attend(q[sum(sizes[:b]):sum(sizes[:b + 1])], *case.tokens(b), seen[b], DIM ** -0.5) for b in range(len(lens))]
+    hit = []                                     # (row, channel) that see such a value
+    for b, (n, size) in enumerate(zip(lens, sizes)):
+        h = torch.zeros((size, DIM), dtype=torch.bool, device=DEV)
+        places = {n - 1: 3, n - size + size // 2: 64, max(0, n - size - window // 2): 127}
+        for t, channel in places.items():
+            page, at = case.table[b, t // PAGE], t % PAGE
+            if poison == "scale":
+                case.vs[page, :, at] = float("nan")
+                h |= seen[b][:, t, None]
+            else:
+                case.v[page, :, at, channel] = 0x7F if fp8 else float(poison)
+                h[:, channel] |= seen[b][:, t]
+        hit.append(h)
+    hit = torch.cat(hit)[:, None].expand(-1, 2 * group, -1)
+    out, lse = run(case, q, window, sink, [sum(sizes[:b]) for b in range(len(sizes) + 1)])
+    assert binding.sv_get_device_error() == 0
+    assert hit.any()
+    bad = out.isposinf() if poison == "inf" else out.isnan()
+    assert torch.equal(bad, hit)
+    o, ls, tol, tol_lse = (torch.cat(x) for x in zip(*ref))
+    check(torch.where(hit, 0, out), lse, (torch.where(hit, 0, o), ls, tol, tol_lse))
