@@ -66,6 +66,19 @@ class PagedCase:
         f = [None if x is None else x.to(dev).contiguous() for x in (self.k, self.v, self.ks, self.vs)]
         return binding.Cache(f[0], f[1], meta, f[2], f[3])
 
+    def spread(self, pages):
+        """The same cache in a pool of `pages` pages, from the last one down (the others hold whatever was there)."""
+        at = pages - 1 - 2 * torch.arange(self.k.shape[0])
+        self.table = torch.where(self.table >= 0, at[self.table.long()].int(), self.table)
+
+        def one(x):
+            if x is None:
+                return None
+            big = torch.empty((pages, *x.shape[1:]), dtype=x.dtype, device=self.device)
+            big[at.to(self.device)] = x.to(self.device)
+            return big
+        self.k, self.v, self.ks, self.vs = (one(x) for x in (self.k, self.v, self.ks, self.vs))
+
     def tokens(self, b, n=None):
         """K, V [Hkv, n, D] of request b in 64 bits, on the device."""
         n = self.lens[b] if n is None else n

@@ -164,7 +164,7 @@ def test_calls_in_turn(pool, rows, max_pages):
     most = min(max_pages * PAGE, 2 * pool * PAGE // rows)
     d.reserve(held, [int(torch.randint(0, most, (1,), generator=g)) for _ in held])
     d.same()
-    d.reserve(held[::-1], [0, 1] * len(held) if False else [i % 3 for i in range(len(held))])
+    d.reserve(held[::-1], [i % 3 for i in range(len(held))])
     d.same()
     kids = [held[-1] + 1 + i for i in range(rows // 4)]
     d.fork([held[i % 2] for i in range(len(kids))], kids)
@@ -404,4 +404,70 @@ def test_a_request_s_life(fp8):
     window(which, [1] * 6, 60, 5)
     binding.sv_pages_free(table, lens, counts, ints(list(range(rows))))
     assert (counts == 0).all() and (lens == 0).all()
+    assert binding.sv_get_device_error() == 0
+
+
+def test_as_many_caches_as_a_call_takes():
+    heads = [1 + i % 2 for i in range(128)]
+    d = Device(Model(40, 4, 6), heads=heads, fp8=[i % 3 == 0 for i in range(128)])
+    d.reserve([0, 1], [70, 33])
+    d.fork([0, 1], [2, 3])
+    d.same()
+    d.free([0])
+    d.compact()
+    d.same()
+
+
+def test_decode_steps_replay_as_a_graph():
+    """Reserve, append and both decodes of a step as one graph, over page boundaries: what the calls give one by one."""
+    rows, max_pages, hkv, group, pool = 5, 12, 2, 4, 60
+    hq = hkv * group
+    lens0 = [70, 70, 70, 15, 16]
+    g = torch.Generator().manual_seed(9)
+
+    def values(*shape):
+        return torch.randn(shape, generator=g).bfloat16().to(DEV)
+    prompt = values(sum(lens0), hkv, DIM), values(sum(lens0), hkv, DIM)
+    q, kv = values(rows, hq, DIM), [(values(rows, hkv, DIM), values(rows, hkv, DIM)) for _ in range(20)]
+
+    def state():
+        shape = (pool, hkv, PAGE, DIM)
+        s = dict(cache=binding.Cache(torch.zeros(shape, dtype=torch.bfloat16, device=DEV),
+                                     torch.zeros(shape, dtype=torch.bfloat16, device=DEV),
+                                     torch.zeros((pool, hkv, 2, DIM), dtype=torch.bfloat16, device=DEV)),
+                 table=torch.full((rows, max_pages), -1, dtype=torch.int32, device=DEV), lens=ints([0] * rows),
+                 counts=ints([0] * pool), which=ints(list(range(rows))), ones=ints([1] * rows), groups=ints([0, 3, 5]),
+                 shared=ints([0, 0]), slots=ints([0] * rows), k=torch.empty_like(kv[0][0]), v=torch.empty_like(kv[0][1]),
+                 ws=torch.empty(binding.sv_pages_workspace_size(pool, rows, rows), dtype=torch.uint8, device=DEV),
+                 pw=torch.empty(binding.sv_prefix_decode_workspace_size(rows, hq, hkv, 2), dtype=torch.uint8, device=DEV),
+                 aw=torch.empty(binding.sv_window_attention_workspace_size(rows, hq, hkv, rows), dtype=torch.uint8, device=DEV),
+                 got=[torch.zeros((rows, hq, DIM), dtype=torch.bfloat16, device=DEV) for _ in range(2)],
+                 lse=[torch.zeros((rows, hq), device=DEV) for _ in range(2)])
+        slots = torch.empty(sum(lens0), dtype=torch.int32, device=DEV)
+        binding.sv_pages_reserve(s["table"], s["lens"], s["counts"], s["which"], ints(lens0), slots, s["ws"])
+        binding.sv_quest_update_meta(s["cache"], *prompt, slots)
+        return s
+
+    def step(s):
+        binding.sv_pages_reserve(s["table"], s["lens"], s["counts"], s["which"], s["ones"], s["slots"], s["ws"])
+        binding.sv_quest_update_meta(s["cache"], s["k"], s["v"], s["slots"])
+        binding.sv_prefix_decode(s["cache"], q, s["table"], s["lens"], s["groups"], s["shared"], s["got"][0], s["lse"][0], s["pw"])
+        binding.sv_window_attention(s["cache"], q, s["table"], s["lens"], 40, 3, s["got"][1], s["lse"][1], s["aw"])
+
+    a, b = state(), state()
+    torch.cuda.synchronize()
+    side, graph = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.graph(graph, stream=side):
+        step(b)
+    for k, v in kv:
+        for s in (a, b):
+            s["k"].copy_(k)
+            s["v"].copy_(v)
+        step(a)
+        graph.replay()
+        for x, y in zip(a["got"] + a["lse"] + [a["slots"]], b["got"] + b["lse"] + [b["slots"]]):
+            assert torch.equal(x, y)
+    assert a["lens"].tolist() == b["lens"].tolist() == [n + 20 for n in lens0]
+    assert torch.equal(a["table"], b["table"]) and torch.equal(a["counts"], b["counts"])
     assert binding.sv_get_device_error() == 0

@@ -305,3 +305,37 @@ def test_values_that_are_not_finite_stay_with_the_rows_that_see_them(lens, sizes
     assert torch.equal(bad, hit)
     o, ls, tol, tol_lse = (torch.cat(x) for x in zip(*ref))
     check(torch.where(hit, 0, out), lse, (torch.where(hit, 0, o), ls, tol, tol_lse))
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+def test_offsets_past_32_bits(fp8):
+    """A pool of more than 2^31 elements, used at its end: chunks, single tokens, a shared prefix, and page copies."""
+    lens, sizes = [300, 77, 300], [100, 1, 40]
+    case = PagedCase(lens, 4, fp8=fp8)
+    case.table[2, :5] = case.table[0, :5]                                    # requests 0 and 2 share pages
+    g = torch.Generator().manual_seed(6)
+    q = torch.randn((sum(sizes), 8, DIM), generator=g).bfloat16().to(DEV)
+    ref = [attend(q[sum(sizes[:b]):sum(sizes[:b + 1])], *case.tokens(b), window_seen(n, sizes[b], 90, 5, DEV), DIM ** -0.5)
+           for b, n in enumerate(lens)]
+    every = [attend(q[b:b + 1], *case.tokens(b), torch.ones((1, n), dtype=torch.bool, device=DEV), DIM ** -0.5)
+             for b, n in enumerate(lens)]
+    case.spread(270000)
+    assert case.k.numel() > 2 ** 31
+    out, lse = run(case, q, 90, 5, [sum(sizes[:b]) for b in range(4)])
+    check(out, lse, [torch.cat(x) for x in zip(*ref)])
+    out, lse = run(case, q[:3], 0, 0)
+    check(out, lse, [torch.cat(x) for x in zip(*every)])
+    order = [0, 2, 1]
+    cache, table = case.cache(), case.table[order].to(DEV).contiguous()
+    ints = lambda x: torch.tensor(x, dtype=torch.int32, device=DEV)
+    ws = torch.empty(binding.sv_prefix_decode_workspace_size(3, 8, 4, 2), dtype=torch.uint8, device=DEV)
+    out, lse = torch.empty_like(q[:3]), torch.empty((3, 8), device=DEV)
+    binding.sv_prefix_decode(cache, q[order].contiguous(), table, ints([lens[b] for b in order]), ints([0, 2, 3]),
+                             ints([5, 0]), out, lse, ws)
+    check(out, lse, [torch.cat([x[b] for b in order]) for x in zip(*every)])
+    page = case.table[0, 3].item()
+    binding.sv_pages_copy(cache, ints([page, page]), ints([1, 260001]))
+    for to in (1, 260001):
+        for x in (cache.k_pool, cache.v_pool, cache.k_scale, cache.v_scale):
+            assert x is None or torch.equal(x[to], x[page])
+    assert binding.sv_get_device_error() == 0
