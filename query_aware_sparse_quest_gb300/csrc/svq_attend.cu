@@ -42,11 +42,13 @@ namespace svq {
 SVQ_DEFINE_ERROR_WORD(read_error_attend)
 
 int window_decode_splits(bool fp8, int batch, int num_kv_heads, int64_t pages, int sm_count);
+int window_decode_cluster(bool fp8, int batch, int num_kv_heads, int64_t pages, int sm_count, bool must);
+bool prefix_alone(bool fp8, int batch, int num_kv_heads, int64_t pages);
 int64_t window_decode_rows(int batch, int num_q_heads, int num_kv_heads);
 int launch_window_decode(const sv_cache* c, const void* q, int num_q_heads, const int32_t* page_table,
                          const int32_t* seq_lens, int batch, int max_pages, int window, int sink,
                          const int32_t* group_start, const int32_t* shared_pages, int num_groups, float softmax_scale,
-                         int splits, float* o_part, float2* ml_part, cudaStream_t stream);
+                         int splits, void* out, float* lse, float* o_part, float2* ml_part, cudaStream_t stream);
 int launch_join_splits(const float* o_part, const float2* ml_part, int splits, int64_t rows, void* out, float* lse,
                        cudaStream_t stream);
 
@@ -175,9 +177,7 @@ __device__ __forceinline__ int warp_find(const int64_t* cum, int n, int64_t u) {
     return lo;
 }
 
-// Prefixes: a group has `entries` row tiles of `tiles` key tiles each.  Groups
-// are sound only in ascending order (none begins before a sound one ends), so
-// that no row is in two of them.
+// Prefixes: a group has `entries` row tiles of `tiles` key tiles each.
 struct GroupAt {
     int g, a, entries, tiles;
     int64_t before;   // cost per kv head of the groups before it
@@ -201,23 +201,7 @@ __device__ __forceinline__ GroupAt warp_groups(const Groups& gr, int tok_per_ent
             sp = gr.pages[g];
             ok = gr.sound(a, end, sp);
         }
-        // The largest end of the sound groups before (an unsound one by order does not count).
-        for (int round = 0; round < 32; ++round) {
-            int far = ok ? end : 0;
-#pragma unroll
-            for (int d = 1; d < 32; d <<= 1) {
-                const int y = __shfl_up_sync(0xffffffffu, far, d);
-                if (lane >= d) far = max(far, y);
-            }
-            int prev = __shfl_up_sync(0xffffffffu, far, 1);
-            if (lane == 0) prev = 0;
-            const uint32_t out = __ballot_sync(0xffffffffu, ok && a < max(prev, reach));
-            if (!out) {
-                reach = max(reach, __shfl_sync(0xffffffffu, far, 31));
-                break;
-            }
-            if (lane == __ffs(out) - 1) ok = false;   // the first one out of order may have hidden others
-        }
+        ok = sound_in_order(ok, a, end, reach);
         const int entries = ok && sp > 0 ? (end - a + tok_per_entry - 1) / tok_per_entry : 0;
         const int64_t cost = static_cast<int64_t>(entries) * cost_of(tiles_of(sp));
         int64_t x = cost;
@@ -1626,8 +1610,8 @@ __global__ void __launch_bounds__(kPrefixThreads) join_prefix_kernel(const __gri
         return;
     }
     uint32_t fault;
-    const int page = page_behind(a.groups, b, a.seq_lens[b], fault);
-    const int g = find_le(a.groups.start, a.groups.n, b);
+    int g;
+    const int page = page_behind(a.groups, b, a.seq_lens[b], fault, g);
     const int e = (b - a.groups.start[g]) / a.tok_per_entry, row = b - a.groups.start[g] - e * a.tok_per_entry;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int rows = (a.group + gridDim.y - 1) / gridDim.y, per_row = kWarps / rows;
@@ -1788,13 +1772,18 @@ int launch_window(const sv_cache* c, const void* q, int num_q_heads, const int32
     if (!q_start) {
         // Pages of a window that starts anywhere in a page, and of the sinks.
         const int64_t span = window > 0 ? (static_cast<int64_t>(window) + 14) / kPage + 1 + (sink + 15ll) / kPage : max_pages;
-        const int splits = window_decode_splits(c->kv_format == SV_KV_FP8_E4M3, batch, c->num_kv_heads,
-                                                span < max_pages ? span : max_pages, ctas);
+        const bool fp8 = c->kv_format == SV_KV_FP8_E4M3;
+        const int64_t pages = span < max_pages ? span : max_pages;
+        const int cluster = window_decode_cluster(fp8, batch, c->num_kv_heads, pages, ctas, false);
+        if (cluster)
+            return launch_window_decode(c, q, num_q_heads, page_table, seq_lens, batch, max_pages, window, sink, nullptr,
+                                        nullptr, 0, softmax_scale, cluster, out, lse, nullptr, nullptr, stream);
+        const int splits = window_decode_splits(fp8, batch, c->num_kv_heads, pages, ctas);
         const int64_t heads = static_cast<int64_t>(batch) * num_q_heads;
         float* o = static_cast<float*>(workspace);
         float2* ml = reinterpret_cast<float2*>(static_cast<unsigned char*>(workspace) + up(heads * splits * kHeadDim * sizeof(float)));
         const int st = launch_window_decode(c, q, num_q_heads, page_table, seq_lens, batch, max_pages, window, sink, nullptr,
-                                            nullptr, 0, softmax_scale, splits, o, ml, stream);
+                                            nullptr, 0, softmax_scale, splits, nullptr, nullptr, o, ml, stream);
         return st ? st : launch_join_splits(o, ml, splits, heads, out, lse, stream);
     }
     const Layout lay(batch, total_q, num_q_heads, c->num_kv_heads, 0);
@@ -1815,6 +1804,12 @@ int launch_prefix(const sv_cache* c, const void* q, int num_q_heads, const int32
                   void* workspace, int sm_count, cudaStream_t stream) {
     const Layout lay(batch, batch, num_q_heads, c->num_kv_heads, num_groups);
     const int ctas = cta_count(sm_count);
+    const bool fp8 = c->kv_format == SV_KV_FP8_E4M3;
+    if (prefix_alone(fp8, batch, c->num_kv_heads, max_pages))
+        return launch_window_decode(c, q, num_q_heads, page_table, seq_lens, batch, max_pages, 0, 0, group_start,
+                                    shared_pages, num_groups, softmax_scale,
+                                    window_decode_cluster(fp8, batch, c->num_kv_heads, max_pages, ctas, true), out, lse,
+                                    nullptr, nullptr, stream);
     AttendArgs a = attend_args(c, q, num_q_heads, page_table, max_pages, lay, 0, 0, softmax_scale, out, lse, workspace);
     a.groups = Groups{group_start, shared_pages, num_groups, batch, max_pages};
     a.seq_lens = seq_lens;
@@ -1824,9 +1819,10 @@ int launch_prefix(const sv_cache* c, const void* q, int num_q_heads, const int32
     a.group_rec = reinterpret_cast<GroupRec*>(ws + lay.group_rec);
     a.split_o = reinterpret_cast<float*>(ws + lay.split_o);
     a.split_ml = reinterpret_cast<float2*>(ws + lay.split_ml);
-    a.splits = window_decode_splits(c->kv_format == SV_KV_FP8_E4M3, batch, c->num_kv_heads, max_pages, ctas);
+    a.splits = window_decode_splits(fp8, batch, c->num_kv_heads, max_pages, ctas);
     int st = launch_window_decode(c, q, num_q_heads, page_table, seq_lens, batch, max_pages, 0, 0, group_start,
-                                  shared_pages, num_groups, softmax_scale, a.splits, a.split_o, a.split_ml, stream);
+                                  shared_pages, num_groups, softmax_scale, a.splits, nullptr, nullptr, a.split_o, a.split_ml,
+                                  stream);
     if (st) return st;
     if ((st = launch_tiles(c, a, ctas, stream))) return st;
     const int rows = batch * c->num_kv_heads, fill = 2 * ctas / rows;   // two CTAs of 512 threads an SM

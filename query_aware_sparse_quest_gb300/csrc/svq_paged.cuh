@@ -56,12 +56,37 @@ struct Groups {
         return a >= 0 && a <= end && end <= batch && sp >= 0 && sp <= max_pages;
     }
 };
+// Groups are sound only in ascending order (none begins before a sound one
+// ends), so that no row is in two of them.  By a whole warp, a group a lane:
+// which of those that are sound by themselves are; `reach`: where the sound
+// groups so far end.
+__device__ __forceinline__ bool sound_in_order(bool ok, int a, int end, int& reach) {
+    const int lane = threadIdx.x & 31;
+    // The largest end of the sound groups before (an unsound one by order does not count).
+    for (int round = 0; round < 32; ++round) {
+        int far = ok ? end : 0;
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+            const int y = __shfl_up_sync(0xffffffffu, far, d);
+            if (lane >= d) far = max(far, y);
+        }
+        int prev = __shfl_up_sync(0xffffffffu, far, 1);
+        if (lane == 0) prev = 0;
+        const uint32_t out = __ballot_sync(0xffffffffu, ok && a < max(prev, reach));
+        if (!out) {
+            reach = max(reach, __shfl_sync(0xffffffffu, far, 31));
+            break;
+        }
+        if (lane == __ffs(out) - 1) ok = false;   // the first one out of order may have hidden others
+    }
+    return ok;
+}
 // The page behind the shared ones of request b, which has `len` tokens (-1: none
-// is to be read), and what is wrong with it.
-__device__ __forceinline__ int page_behind(const Groups& gr, int b, int len, uint32_t& fault) {
+// is to be read), what is wrong with it, and its group.
+__device__ __forceinline__ int page_behind(const Groups& gr, int b, int len, uint32_t& fault, int& g) {
     fault = 0;
     if (b < gr.start[0] || b >= gr.start[gr.n]) return -1;
-    const int g = find_le(gr.start, gr.n, b);
+    g = find_le(gr.start, gr.n, b);
     const int a = gr.start[g], end = gr.start[g + 1], sp = gr.pages[g];
     if (!gr.sound(a, end, sp) || a > b || b >= end) fault = SV_DEVERR_GROUP;
     else if (len < 0 || (static_cast<int64_t>(len) + kPage - 1) / kPage > gr.max_pages) fault = SV_DEVERR_SEQ_LEN;

@@ -11,7 +11,8 @@
 //
 // CTA (request x kv head, split): warp 4 loads the split's pages, warps 0-3
 // take them in turn, keep a softmax of their own and join through shared
-// memory; the splits' partials are joined by a second kernel.
+// memory.  Up to 8 splits of a row are one cluster and join through distributed
+// shared memory; the partials of more are joined by a second kernel.
 //
 // e4m3 pools: codes convert to f16 exactly and the products run in f16.  The
 // value weight of token t is exp(z_t) s_v(t).  It is formed as
@@ -34,10 +35,22 @@ constexpr int kThreads = (kWarps + 1) * 32;
 constexpr int kStages = 8;                         // pages in flight, four producer lanes each
 constexpr float kSlack = 8.f;                      // log2 units a base may lag behind the maximum
 constexpr int kMaxSplits = 64;
+constexpr int kMaxCluster = 8;                     // CTAs of a cluster at most (what every launch may have)
 // At least this many pages a split once every SM has work (a split costs its
 // start, its merge and its partial), and at least kFewPages before that.
 constexpr int kSplitPages[2] = {24, 16};           // bf16, e4m3
 constexpr int kFewPages = 8;
+// Rows of at most so many pages go to a cluster even where more than 8 splits would fill more SMs.
+constexpr int kClusterPages = 80;
+// Requests that share pages: each is read alone, shared pages and all, in one
+// launch, if the batch and kv heads have at most so many pages together and a
+// row so many.  Against sharing (three launches), us, 8 query heads a kv head,
+// device time alone: 16 rows of 135 pages bf16 9.4 / 18.5, e4m3 11.3 / 20.4; 64
+// rows of 407 21.8 / 27.7 and 30.2 / 27.8; 256 rows of 135 27.7 / 25.6 and 36.6 /
+// 28.7; 1 row of 519 14.6 / 17.4 and 20.6 / 20.3; 1 row of 1031 23.3 / 19.9 and
+// 34.4 / 22.2.
+constexpr int64_t kAlonePages[2] = {28000, 20000};   // bf16, e4m3
+constexpr int64_t kAloneRow[2] = {640, 480};
 
 template <bool FP8>
 struct Cfg {
@@ -46,7 +59,7 @@ struct Cfg {
     static constexpr int kSmem = 1024 + kStages * (2 * kTile + kScale);
     static constexpr int kPerSm = FP8 ? 4 : 3;
 };
-static_assert(kStages * 2 * Cfg<true>::kTile >= (kWarps * kMaxGroup * (kHeadDim + 3)) * 4, "the warps merge through the ring");
+static_assert(kStages * 2 * Cfg<true>::kTile >= (kWarps * kMaxGroup * (kHeadDim + 3) + 2 * kMaxGroup) * 4, "the warps merge through the ring");
 
 struct Args {
     const __nv_bfloat16* q;
@@ -55,13 +68,16 @@ struct Args {
     const int32_t* seq_lens;
     int max_pages;
     int64_t num_phys_pages;
-    Groups groups;              // requests that share pages: the pages behind those are read; none: the window's
+    Groups groups;              // requests that share pages; none: the window's are read
+    bool alone;                 // groups: all pages of a request are read, not only those behind the shared ones
     int window;                 // INT_MAX: none
     int sink;
     int num_splits;
     float scale_log2;           // softmax_scale * log2(e)
     const float* k_scale;
     const float* v_scale;
+    __nv_bfloat16* out;         // a row's splits are a cluster, which writes its result; null: partials
+    float* lse;
     float* o_part;              // [B][Hq][splits][128]
     float2* ml_part;            // [B][Hq][splits]
 };
@@ -97,17 +113,66 @@ __device__ __forceinline__ uint32_t bf16_at(int row, int chunk) {
 // 16-byte chunk (0 .. 7) of a row of an e4m3 tile (128-byte rows, 128-byte swizzle).
 __device__ __forceinline__ uint32_t f8_at(int row, int chunk) { return row * 128 + ((chunk ^ (row & 7)) << 4); }
 
+// All threads of the cluster; orders their shared accesses.
+__device__ __forceinline__ void cluster_sync() {
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// What lies at `addr` in the shared memory of the cluster's CTA `rank`.
+__device__ __forceinline__ uint32_t at_rank(uint32_t addr, int rank) {
+    uint32_t there;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(there) : "r"(addr), "r"(rank));
+    return there;
+}
+__device__ __forceinline__ float2 ld_cluster_f2(uint32_t addr, int rank) {
+    float2 v;
+    asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(at_rank(addr, rank)) : "memory");
+    return v;
+}
+__device__ __forceinline__ float4 ld_cluster_f4(uint32_t addr, int rank) {
+    float4 v;
+    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+                 : "r"(at_rank(addr, rank))
+                 : "memory");
+    return v;
+}
+
 // The pages of a request that are read: `sinks` first ones, then w0 on.
 struct View {
     int sinks, w0, count;
+    int shared, row;   // the first `shared` pages are read from this row of the table
 };
-__device__ __forceinline__ View view_of(const Args& a, int len, int b) {
-    View v = {0, 0, 0};
-    if (len <= 0) return v;
+// By whole warps; `report`: one of them says what is wrong.
+__device__ __forceinline__ View view_of(const Args& a, int len, int b, bool report) {
+    View v = {0, 0, 0, 0, b};
     if (a.groups.start) {
-        uint32_t fault;   // the join of the parts reports it
-        v.w0 = page_behind(a.groups, b, len, fault);
-        if (v.w0 < 0) return {0, 0, 0};
+        uint32_t fault;   // of parts behind a prefix: the join reports it
+        int g;
+        v.w0 = page_behind(a.groups, b, len, fault, g);
+        if (a.alone && v.w0 >= 0) {
+            int reach = 0;
+            bool sound = true;
+            for (int g0 = 0; g0 <= g && sound; g0 += 32) {
+                const int at = g0 + (threadIdx.x & 31);
+                int from = 0, end = 0;
+                bool ok = false;
+                if (at <= g) {
+                    from = a.groups.start[at];
+                    end = a.groups.start[at + 1];
+                    ok = a.groups.sound(from, end, a.groups.pages[at]);
+                }
+                ok = sound_in_order(ok, from, end, reach);
+                if (g < g0 + 32) sound = __shfl_sync(0xffffffffu, ok, g - g0);
+            }
+            v.shared = v.w0;
+            v.row = a.groups.start[g];
+            v.w0 = sound ? 0 : -1;
+            if (!sound) fault = SV_DEVERR_GROUP;
+        }
+        if (a.alone && fault && report) svq_flag(fault);
+        if (v.w0 < 0) return {0, 0, 0, 0, b};
+    } else if (len <= 0) {
+        return v;
     } else {
         v.w0 = max(0, len - a.window) / kPage;
         v.sinks = sink_pages_of(a.sink, v.w0);
@@ -145,7 +210,14 @@ __global__ void __launch_bounds__(kThreads, Cfg<FP8>::kPerSm)
     __syncthreads();
 
     int len = a.seq_lens[b];
-    if (len < 0 || (static_cast<int64_t>(len) + kPage - 1) / kPage > a.max_pages) {
+    bool touched = true;
+    if (a.alone) {
+        touched = b >= a.groups.start[0] && b < a.groups.start[a.groups.n];
+        // What is wrong with groups that hold no row.
+        if (blockIdx.x == 0 && split == 0)
+            for (int g = threadIdx.x; g < a.groups.n; g += kThreads)
+                if (!a.groups.sound(a.groups.start[g], a.groups.start[g + 1], a.groups.pages[g])) svq_flag(SV_DEVERR_GROUP);
+    } else if (len < 0 || (static_cast<int64_t>(len) + kPage - 1) / kPage > a.max_pages) {
         if (threadIdx.x == 0 && split == 0 && !a.groups.start) svq_flag(SV_DEVERR_SEQ_LEN);
         len = 0;
     }
@@ -173,8 +245,8 @@ __global__ void __launch_bounds__(kThreads, Cfg<FP8>::kPerSm)
             }
         }
     }
+    const View v = view_of(a, len, b, split == 0 && h == 0 && threadIdx.x == 0);
     pdl_wait();   // the pools and the workspace, which the work before may still use
-    const View v = view_of(a, len, b);
     const int chunk = (v.count + a.num_splits - 1) / a.num_splits;
     const int j0 = min(v.count, split * chunk);
     const int mine = min(v.count, j0 + chunk) - j0;
@@ -182,6 +254,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<FP8>::kPerSm)
     if (warp == kWarps) {
         // ---------------- loads: lanes 4u (K) and 4u + 2 (V) feed stage u with pages u, u + 8, ...
         const int32_t* const pages = a.page_table + static_cast<int64_t>(b) * a.max_pages;
+        const int32_t* const first = a.page_table + static_cast<int64_t>(v.row) * a.max_pages;
         const int u = lane >> 2, part = (lane & 3) >> 1;
         const bool mover = (lane & 1) == 0;
         const uint64_t policy = l2_evict_first_policy();
@@ -195,7 +268,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<FP8>::kPerSm)
             if (i < mine) {
                 const int j = j0 + i;
                 const int lp = j < v.sinks ? j : v.w0 + j - v.sinks;
-                const int ph = pages[lp];
+                const int ph = (lp < v.shared ? first : pages)[lp];
                 if (ph < 0 || ph >= a.num_phys_pages) {
                     svq_flag(SV_DEVERR_PAGE_TABLE);
                 } else {
@@ -248,7 +321,13 @@ __global__ void __launch_bounds__(kThreads, Cfg<FP8>::kPerSm)
         if (!ok) svq_flag(SV_DEVERR_TIMEOUT);
         // This lane's copies land before the CTA (and its shared memory) retires.
         if (last >= 0) (void)mbar_wait_bounded(fb, (last / kStages) & 1);
-        pdl_launch_dependents();
+        if (!a.out) {
+            pdl_launch_dependents();   // (results may be inputs of what comes next)
+            return;
+        }
+        __syncwarp();
+        cluster_sync();
+        cluster_sync();
         return;
     }
 
@@ -396,6 +475,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<FP8>::kPerSm)
     float* const sm_m = sm_o + kWarps * kMaxGroup * kHeadDim;       // [warp][8] bases, output bases, sums
     float* const sm_d = sm_m + kWarps * kMaxGroup;
     float* const sm_l = sm_d + kWarps * kMaxGroup;
+    float2* const sm_fin = reinterpret_cast<float2*>(sm_l + kWarps * kMaxGroup);   // [8] the CTA's
     {
         float* const ow = sm_o + warp * kMaxGroup * kHeadDim;
         const int h0 = 2 * quad, h1 = 2 * quad + 1;
@@ -426,9 +506,48 @@ __global__ void __launch_bounds__(kThreads, Cfg<FP8>::kPerSm)
             L += sm_l[w * kMaxGroup + hh] * ex2(sm_m[w * kMaxGroup + hh] - base);
             O += sm_o[(w * kMaxGroup + hh) * kHeadDim + d] * ex2(sm_d[w * kMaxGroup + hh] - base);
         }
-        a.o_part[((q0 + hh) * a.num_splits + split) * kHeadDim + d] = O;
-        if (d == 0) a.ml_part[(q0 + hh) * a.num_splits + split] = make_float2(M, L);
+        if (a.out) {   // over warp 0's part, which only this thread reads here
+            sm_o[idx] = O;
+            if (d == 0) sm_fin[hh] = make_float2(M, L);
+        } else {
+            a.o_part[((q0 + hh) * a.num_splits + split) * kHeadDim + d] = O;
+            if (d == 0) a.ml_part[(q0 + hh) * a.num_splits + split] = make_float2(M, L);
+        }
     }
+    if (!a.out) return;
+    __syncwarp();
+    cluster_sync();
+    // Four channels of a head a thread, over all CTAs of the cluster.
+    for (int at = split * kWarps * 32 + threadIdx.x; at < a.group * 32; at += a.num_splits * kWarps * 32) {
+        const int hh = at / 32;
+        float2 ml[kMaxCluster];
+        float4 x[kMaxCluster];
+#pragma unroll
+        for (int u = 0; u < kMaxCluster; ++u) {
+            ml[u] = make_float2(-INFINITY, 0.f);
+            x[u] = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (u < a.num_splits) {
+                ml[u] = ld_cluster_f2(smem_addr(sm_fin + hh), u);
+                x[u] = ld_cluster_f4(smem_addr(sm_o + 4 * at), u);
+            }
+        }
+        RowSum s;
+#pragma unroll
+        for (int u = 0; u < kMaxCluster; ++u) s.m = fmaxf(s.m, ml[u].x);
+        const float base = s.m == -INFINITY ? 0.f : s.m;
+#pragma unroll
+        for (int u = 0; u < kMaxCluster; ++u) {
+            const float f = ex2(ml[u].x - base);
+            s.l += ml[u].y * f;
+            s.o.x += x[u].x * f;
+            s.o.y += x[u].y * f;
+            s.o.z += x[u].z * f;
+            s.o.w += x[u].w * f;
+        }
+        if (touched) (void)s.write(a.out + (q0 + hh) * kHeadDim, a.lse + q0 + hh, lane);
+    }
+    __syncwarp();
+    cluster_sync();   // the others have read this CTA's shared memory
 }
 
 // CTA per (request, query head): joins its splits.
@@ -468,10 +587,21 @@ int launch(const Args& a, const CUtensorMap& tk, const CUtensorMap& tv, int batc
                    : SV_ERR_CUDA;
     });
     if (st) return st;
-    return launch_pdl(window_decode_kernel<FP8>, dim3(batch * a.num_kv_heads, a.num_splits), dim3(kThreads),
-                      Cfg<FP8>::kSmem, stream, a, tk, tv) == cudaSuccess
-               ? SV_OK
-               : SV_ERR_CUDA;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(batch * a.num_kv_heads, a.num_splits);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = Cfg<FP8>::kSmem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = 1;
+    attr[1].val.clusterDim.y = a.num_splits;
+    attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = a.out ? 2 : 1;
+    return cudaLaunchKernelEx(&cfg, window_decode_kernel<FP8>, a, tk, tv) == cudaSuccess ? SV_OK : SV_ERR_CUDA;
 }
 
 }  // namespace
@@ -487,6 +617,28 @@ int window_decode_splits(bool fp8, int batch, int num_kv_heads, int64_t pages, i
     return static_cast<int>(s < 1 ? 1 : (s > kMaxSplits ? kMaxSplits : s));
 }
 
+// The same, as a cluster that joins a row without a second launch (5 us of the
+// host's time; the GPU's is the same); 0: more splits than a cluster has CTAs
+// are faster (`must`: never).  With 8 instead of more: 32 rows bf16 of 256 pages
+// 14.0 against 13.9 us, 20 rows 10.8 / 9.5, 52 rows e4m3 20.5 / 17.9, 1 row of 64
+// pages 6.0 / 5.8, of 512 13.4 / 8.4.  Clusters of 7 and 8 CTAs, three to an SM,
+// do not fill the GPU: 64 rows of 256 pages 34.4 us with 7, 26.3 with 5.
+int window_decode_cluster(bool fp8, int batch, int num_kv_heads, int64_t pages, int sm_count, bool must) {
+    const int64_t rows = static_cast<int64_t>(batch) * num_kv_heads;
+    int s = window_decode_splits(fp8, batch, num_kv_heads, pages, sm_count);
+    if (s > kMaxCluster) {
+        if (!must && pages > kClusterPages && (fp8 || 2 * rows * kMaxCluster < 3 * sm_count)) return 0;
+        s = kMaxCluster;
+    }
+    if (!fp8 && s > 6 && 20 * rows * s > 17ll * sm_count * Cfg<false>::kPerSm) s = 6;
+    return s;
+}
+
+// Whether requests that share pages are each read alone.
+bool prefix_alone(bool fp8, int batch, int num_kv_heads, int64_t pages) {
+    return batch * pages * num_kv_heads <= kAlonePages[fp8] && pages <= kAloneRow[fp8];
+}
+
 // Partial rows a call can need: a row has one split, or all rows' splits fit one wave.
 int64_t window_decode_rows(int batch, int num_q_heads, int num_kv_heads) {
     const int64_t one = static_cast<int64_t>(batch) * num_q_heads;
@@ -497,7 +649,7 @@ int64_t window_decode_rows(int batch, int num_q_heads, int num_kv_heads) {
 int launch_window_decode(const sv_cache* c, const void* q, int num_q_heads, const int32_t* page_table,
                          const int32_t* seq_lens, int batch, int max_pages, int window, int sink,
                          const int32_t* group_start, const int32_t* shared_pages, int num_groups, float softmax_scale,
-                         int splits, float* o_part, float2* ml_part, cudaStream_t stream) {
+                         int splits, void* out, float* lse, float* o_part, float2* ml_part, cudaStream_t stream) {
     const bool fp8 = c->kv_format == SV_KV_FP8_E4M3;
     // TMA coordinates are 32-bit.
     const int64_t rows = c->num_phys_pages * c->num_kv_heads * kPage;
@@ -518,7 +670,10 @@ int launch_window_decode(const sv_cache* c, const void* q, int num_q_heads, cons
     a.groups = Groups{group_start, shared_pages, num_groups, batch, max_pages};
     a.window = window > 0 ? window : INT_MAX;
     a.sink = sink;
+    a.alone = group_start && out;
     a.num_splits = splits;
+    a.out = static_cast<__nv_bfloat16*>(out);
+    a.lse = lse;
     a.scale_log2 = softmax_scale * 1.4426950408889634f;
     a.k_scale = static_cast<const float*>(c->k_scale);
     a.v_scale = static_cast<const float*>(c->v_scale);

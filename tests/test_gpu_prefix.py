@@ -22,11 +22,22 @@ def share(case, starts, shared):
             case.table[b, :shared[g]] = case.table[starts[g], :shared[g]]
 
 
+@pytest.fixture(params=["narrow", "wide"], autouse=True)
+def width(request):
+    """Small batches over a narrow page table read every request alone, those over a wide one share the prefix's pages."""
+    run.wide = request.param == "wide"
+
+
+def table_of(case):
+    table = case.table.to(DEV)
+    return torch.nn.functional.pad(table, (0, 5000), value=-1) if run.wide else table
+
+
 def run(case, q, starts, shared, scale=None):
     B, Hq, _ = q.shape
     out, lse = torch.full_like(q, 7.0), torch.full((B, Hq), 7.0, device=DEV)
     ws = torch.full((binding.sv_prefix_decode_workspace_size(B, Hq, case.hkv, len(shared)),), 0xFF, dtype=torch.uint8, device=DEV)
-    binding.sv_prefix_decode(case.cache(), q, case.table.to(DEV), ints(case.lens), ints(starts), ints(shared), out, lse, ws,
+    binding.sv_prefix_decode(case.cache(), q, table_of(case), ints(case.lens), ints(starts), ints(shared), out, lse, ws,
                              softmax_scale=scale)
     torch.cuda.synchronize()
     return out, lse
@@ -86,7 +97,7 @@ def test_padded_and_invalid_requests():
     share(case, starts, shared)
     q = queries(case, 8)
     good = reference(case, q, [0, 2, 3, 4])
-    for n, flag in ((0, 0), (63, 0x40), (-1, 0x8), (6 * PAGE + 1, 0x8)):
+    for n, flag in ((0, 0), (63, 0x40), (-1, 0x8), (table_of(case).shape[1] * PAGE + 1, 0x8)):
         held, case.lens[1] = case.lens[1], n
         out, lse = run(case, q, starts, shared)
         case.lens[1] = held
@@ -138,7 +149,7 @@ def test_repeats_and_graph(fp8):
     share(case, starts, shared)
     q = queries(case, 7)
     first = run(case, q, starts, shared)
-    cache, table, gs, sp, ls = case.cache(), case.table.to(DEV), ints(starts), ints(shared), ints(lens)
+    cache, table, gs, sp, ls = case.cache(), table_of(case), ints(starts), ints(shared), ints(lens)
     ws = torch.full((binding.sv_prefix_decode_workspace_size(23, 14, 2, 2),), 0xFF, dtype=torch.uint8, device=DEV)
     out, lse = torch.empty_like(q), torch.empty((23, 14), device=DEV)
 

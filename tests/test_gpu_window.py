@@ -330,9 +330,10 @@ def test_offsets_past_32_bits(fp8):
     ints = lambda x: torch.tensor(x, dtype=torch.int32, device=DEV)
     ws = torch.empty(binding.sv_prefix_decode_workspace_size(3, 8, 4, 2), dtype=torch.uint8, device=DEV)
     out, lse = torch.empty_like(q[:3]), torch.empty((3, 8), device=DEV)
-    binding.sv_prefix_decode(cache, q[order].contiguous(), table, ints([lens[b] for b in order]), ints([0, 2, 3]),
-                             ints([5, 0]), out, lse, ws)
-    check(out, lse, [torch.cat([x[b] for b in order]) for x in zip(*every)])
+    for wide in (0, 5000):                                                    # each request alone; the prefix once
+        binding.sv_prefix_decode(cache, q[order].contiguous(), torch.nn.functional.pad(table, (0, wide), value=-1),
+                                 ints([lens[b] for b in order]), ints([0, 2, 3]), ints([5, 0]), out, lse, ws)
+        check(out, lse, [torch.cat([x[b] for b in order]) for x in zip(*every)])
     page = case.table[0, 3].item()
     binding.sv_pages_copy(cache, ints([page, page]), ints([1, 260001]))
     for to in (1, 260001):
