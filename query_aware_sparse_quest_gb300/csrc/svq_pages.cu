@@ -13,7 +13,11 @@
 // shared memory, and the cluster barrier orders its phases, so that a scan
 // over the whole pool and what depends on it are one launch.  Moving page
 // data is a second launch over the whole GPU, one CTA at a time per page and
-// layer (34 KB for 4 kv heads), bound by HBM.
+// layer (34 KB for 4 kv heads), bound by HBM.  Measured on a GB300 (a plain copy:
+// 6.8 TB/s): packing a pool of 16384 pages held to 60 per cent, 4 layers of 4 kv
+// heads, 181 us for 1.10 GB read and written (6.1 TB/s); fork, reserve and free
+// for 64 children of 16 parents in 8 layers 24 us, for 8 of 1 in one layer 22 us:
+// four launches and three calls of the host, with 34 MB and 0.1 MB moved.
 //
 // Kernels are launched to overlap the end of the one before (a beam step of
 // three calls 33 -> 24 us), but each waits for it before its first access and
