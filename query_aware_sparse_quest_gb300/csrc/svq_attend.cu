@@ -140,7 +140,8 @@ struct AttendArgs {
     struct GroupRec* group_rec;   // prefixes: [groups + 1], for the join; the last one's cost is the total
     int4* cut_item;    // chunks: [CTAs][2] the item that goes on in a CTA: row0, ntok, kv head, pieces (0: none is to
                        // be joined here); slot of the first piece, of the second, and the entry
-    int2* odd;         // chunks: 32-row parts of whole items with a channel that is not finite: entry, kv head * 256 + row
+    uint32_t* odd;     // chunks: 32-row parts of whole items with a channel that is not finite:
+                       // (entry * kv heads + kv head) * 8 + part
     int* num_odd;
     bool fp8;
     int slot_rows;
@@ -388,7 +389,7 @@ struct __align__(16) Seg {
     Entry en;
     int h;            // kv head
     int t0, t1;       // tiles of the item
-    int slot;         // where a partial goes; -1 - entry: the segment is the whole item
+    int slot;         // where a partial goes; -1 - (entry * kv heads + kv head): the segment is the whole item
 };
 constexpr int kSegs = 4;
 
@@ -858,7 +859,7 @@ __global__ void __launch_bounds__(Cfg<FP8>::kThreads, 1)
                         s.h = h;
                         s.t0 = t0;
                         s.t1 = t1;
-                        s.slot = t0 == 0 && t1 == en.tiles ? -1 - e : static_cast<int>(blockIdx.x) * 2 + (first_item ? 0 : 1);
+                        s.slot = t0 == 0 && t1 == en.tiles ? -1 - (e * a.num_kv_heads + h) : static_cast<int>(blockIdx.x) * 2 + (first_item ? 0 : 1);
                         mbar_arrive(smem_addr(&ct->seg_full[k % kSegs]));
                     }
                     ++k;
@@ -1199,7 +1200,7 @@ __global__ void __launch_bounds__(Cfg<FP8>::kThreads, 1)
                         }
                     }
                     if (!po && __any_sync(0xffffffffu, odd != 0.f && L < INFINITY) && lane == 0)
-                        a.odd[atomicAdd(a.num_odd, 1)] = make_int2(-1 - s.slot, s.h * kRowTile + off + (warp & 3) * 32);
+                        a.odd[atomicAdd(a.num_odd, 1)] = static_cast<uint32_t>(~s.slot) * 8 + (warp - 4 - (two ? 0 : w * 4));
                     if (valid && (two || w == 0)) {
                         if (po) *pml = make_float2(M, L);
                         else a.lse[qrow] = L > 0.f ? (M + log2f(L)) * 0.69314718055994531f : (L == 0.f ? -INFINITY : L);
@@ -1607,9 +1608,10 @@ __global__ void __launch_bounds__(kCutThreads, 4) join_cut_kernel(const __grid_c
     }
     constexpr int kTurns = 32 / kWarps;   // a warp a row
     for (int64_t i = blockIdx.y * gridDim.x + blockIdx.x; i < static_cast<int64_t>(num_odd) * kTurns; i += gridDim.x * gridDim.y) {
-        const int2 part = a.odd[i / kTurns];
-        const int r = part.y % kRowTile + static_cast<int>(i % kTurns) * kWarps + warp;
-        if (r < a.plan.entries[part.x].ntok * a.group) look_at_row(a, part.x, part.y / kRowTile, r);
+        const uint32_t part = a.odd[i / kTurns];
+        const int e = part / 8 / a.num_kv_heads, h = part / 8 % a.num_kv_heads;
+        const int r = part % 8 * 32 + static_cast<int>(i % kTurns) * kWarps + warp;
+        if (r < a.plan.entries[e].ntok * a.group) look_at_row(a, e, h, r);
     }
 }
 
@@ -1696,7 +1698,7 @@ struct Layout {
         split_o = take(parts * kHeadDim * sizeof(float));
         split_ml = take(parts * sizeof(float2));
         // A warp's 32 rows of an item each.  Behind all that every call touches (in front of it: 92.8 against 90.7 us).
-        odd = take(8 * e * num_kv_heads * sizeof(int2));
+        odd = take(8 * e * num_kv_heads * sizeof(uint32_t));
         num_odd = take(sizeof(int));
         total = at + 256;   // the parts begin at the workspace's first multiple of 256 (rows are written 32 bytes at a time)
     }
@@ -1752,7 +1754,7 @@ AttendArgs attend_args(const sv_cache* c, const void* q, int num_q_heads, const 
     a.cut_o = reinterpret_cast<float*>(ws + lay.cut_o);
     a.cut_ml = reinterpret_cast<float2*>(ws + lay.cut_ml);
     a.cut_item = reinterpret_cast<int4*>(ws + lay.cut_item);
-    a.odd = reinterpret_cast<int2*>(ws + lay.odd);
+    a.odd = reinterpret_cast<uint32_t*>(ws + lay.odd);
     a.num_odd = reinterpret_cast<int*>(ws + lay.num_odd);
     a.fp8 = c->kv_format == SV_KV_FP8_E4M3;
     a.slot_rows = lay.slot_rows;
