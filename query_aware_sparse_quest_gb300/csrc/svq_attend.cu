@@ -44,7 +44,7 @@
 // to 1.35 ms by the card's power (1530 to 1660 TFLOP/s, 81 to 88 % of the
 // product's), with a window of 4096 tokens 212 us (1300 TFLOP/s of visible work;
 // 12 % of the tiles' work is masked or item cost); 7 ragged e4m3 requests of up
-// to 4000 tokens 91 us (52 % of the issue slots, the tensor pipe 18 %); 32
+// to 4000 tokens 89 us (52 % of the issue slots, the tensor pipe 18 %); 32
 // requests behind 32768 shared tokens 45 us, of which these tiles 21, what is
 // behind the prefix 11 and the join 13.
 #include <climits>
@@ -73,7 +73,7 @@ constexpr int kTileTok = kTilePages * kPage;        // 128 tokens
 constexpr int kPageBytes = kPage * kHeadDim * 2;    // a page's bf16 tile of one kv head: 4 KB
 constexpr int kStageBytes = kTilePages * kPageBytes;
 constexpr int kRowTile = 256;                       // rows of an entry at most
-constexpr int kInfoSlots = 8;                       // tiles whose page faults / scales are kept (the loads run at most 3 ahead)
+constexpr int kInfoSlots = 8;                       // tiles whose page faults / scales are kept (loads run at most 5 tiles ahead)
 constexpr int kMaxCtas = 160;                       // partial slots in the workspace
 constexpr float kSlack = 8.f;                       // log2 units the base may lag behind the maximum
 constexpr int kColS = 0, kColO = 256;               // TMEM columns of S0 and O0; S1 and O1 lie 128 further
@@ -331,6 +331,11 @@ __device__ __forceinline__ void unpack2(uint64_t v, float& lo, float& hi) {
 __device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
     uint64_t r;
     asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
     return r;
 }
 __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
@@ -968,13 +973,15 @@ __global__ void __launch_bounds__(Cfg<FP8>::kThreads, 1)
                             bits2 = two_pages(2);
                             bits3 = two_pages(3);
                         }
-                        const float4* ks = reinterpret_cast<const float4*>(scales + slot * 2 * kTileTok);
-                        const float2* vs = reinterpret_cast<const float2*>(ks + kTileTok / 4);
+                        // Pairs of tokens: key scales times scale_log2, value scales.
+                        const ulonglong2* ks = reinterpret_cast<const ulonglong2*>(scales + slot * 2 * kTileTok);
+                        const ulonglong2* vs = ks + kTileTok / 4;
                         // The row's logits.  bf16: all 128 stay in registers from here to P (a causal chunk
                         // 1268 us; with the exponentials in a rolled loop 1363).  e4m3 (fewer registers a
                         // thread, and the widening warps' code beside it in the instruction cache): rolled
                         // loops over 32 columns that read S from TMEM twice (ragged chunks 89.0 us; logits in
-                        // registers, with half the widening warps, 90.7).
+                        // registers, with half the widening warps, 90.7).  Scales act on pairs of tokens,
+                        // the keys' with scale_log2 in them.
                         float x[FP8 ? 1 : 128];
                         float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
                         if constexpr (FP8) {
@@ -983,18 +990,14 @@ __global__ void __launch_bounds__(Cfg<FP8>::kThreads, 1)
                                 float x[32];
                                 tc_ld32(s_col + c * 32, reinterpret_cast<uint32_t(&)[32]>(x));
                                 tc_wait_ld();
-                                {
 #pragma unroll
-                                    for (int u = 0; u < 8; ++u) {
-                                        const float4 k4 = ks[c * 8 + u];
-                                        x[4 * u] *= k4.x;
-                                        x[4 * u + 1] *= k4.y;
-                                        x[4 * u + 2] *= k4.z;
-                                        x[4 * u + 3] *= k4.w;
-                                    }
+                                for (int u = 0; u < 8; ++u) {
+                                    const ulonglong2 k4 = ks[c * 8 + u];
+                                    unpack2(mul2(pack2(x[4 * u], x[4 * u + 1]), k4.x), x[4 * u], x[4 * u + 1]);
+                                    unpack2(mul2(pack2(x[4 * u + 2], x[4 * u + 3]), k4.y), x[4 * u + 2], x[4 * u + 3]);
                                 }
-                                if (!plain) {
-                                    const uint32_t bits = c == 0 ? bits0 : (c == 1 ? bits1 : (c == 2 ? bits2 : bits3));
+                                const uint32_t bits = c == 0 ? bits0 : (c == 1 ? bits1 : (c == 2 ? bits2 : bits3));
+                                if (__any_sync(0xffffffffu, bits != ~0u)) {
 #pragma unroll
                                     for (int u = 0; u < 32; ++u)
                                         if (!((bits >> u) & 1u)) x[u] = -INFINITY;
@@ -1024,7 +1027,7 @@ __global__ void __launch_bounds__(Cfg<FP8>::kThreads, 1)
                                 for (int u = 8; u < 128; u += 8) mx[c] = fmaxf(fmaxf(mx[c], x[u + c]), x[u + c + 4]);
                             }
                         }
-                        const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * a.scale_log2;
+                        const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * (FP8 ? 1.f : a.scale_log2);
                         // The base moves only when the maximum is more than kSlack above it; weights
                         // stay at most 2^kSlack, and sums and outputs share the base.
                         // Threads without a row hold whatever Q's memory held and have no say.
@@ -1056,35 +1059,30 @@ __global__ void __launch_bounds__(Cfg<FP8>::kThreads, 1)
                                 uint32_t p[16];
                                 tc_ld32(s_col + c * 32, reinterpret_cast<uint32_t(&)[32]>(x));
                                 tc_wait_ld();
-                                {
 #pragma unroll
-                                    for (int u = 0; u < 8; ++u) {
-                                        const float4 k4 = ks[c * 8 + u];
-                                        x[4 * u] *= k4.x;
-                                        x[4 * u + 1] *= k4.y;
-                                        x[4 * u + 2] *= k4.z;
-                                        x[4 * u + 3] *= k4.w;
-                                    }
+                                for (int u = 0; u < 8; ++u) {
+                                    const ulonglong2 k4 = ks[c * 8 + u];
+                                    unpack2(fma2(pack2(x[4 * u], x[4 * u + 1]), k4.x, base2), x[4 * u], x[4 * u + 1]);
+                                    unpack2(fma2(pack2(x[4 * u + 2], x[4 * u + 3]), k4.y, base2), x[4 * u + 2], x[4 * u + 3]);
                                 }
-                                if (!plain) {
-                                    const uint32_t bits = c == 0 ? bits0 : (c == 1 ? bits1 : (c == 2 ? bits2 : bits3));
+                                const uint32_t bits = c == 0 ? bits0 : (c == 1 ? bits1 : (c == 2 ? bits2 : bits3));
+                                if (__any_sync(0xffffffffu, bits != ~0u)) {
 #pragma unroll
                                     for (int u = 0; u < 32; ++u)
                                         if (!((bits >> u) & 1u)) x[u] = -INFINITY;
                                 }
 #pragma unroll
-                                for (int u = 0; u < 16; ++u) {
-                                    float e0, e1;
-                                    unpack2(fma2(pack2(x[2 * u], x[2 * u + 1]), scale2, base2), e0, e1);
-                                    e0 = ex2(e0);
-                                    e1 = ex2(e1);
-                                    sum[u & 1] = add2(sum[u & 1], pack2(e0, e1));
-                                    {
-                                        const float2 v2 = vs[c * 16 + u];
-                                        e0 *= v2.x;
-                                        e1 *= v2.y;
-                                    }
-                                    p[u] = pack_bf16x2(e0, e1);
+                                for (int u = 0; u < 8; ++u) {
+                                    const ulonglong2 v4 = vs[c * 8 + u];
+                                    const uint64_t e0 = pack2(ex2(x[4 * u]), ex2(x[4 * u + 1]));
+                                    const uint64_t e1 = pack2(ex2(x[4 * u + 2]), ex2(x[4 * u + 3]));
+                                    sum[0] = add2(sum[0], e0);
+                                    sum[1] = add2(sum[1], e1);
+                                    float w0, w1;
+                                    unpack2(mul2(e0, v4.x), w0, w1);
+                                    p[2 * u] = pack_bf16x2(w0, w1);
+                                    unpack2(mul2(e1, v4.y), w0, w1);
+                                    p[2 * u + 1] = pack_bf16x2(w0, w1);
                                 }
                                 tc_st16(s_col + c * 16, p);
                             }
@@ -1235,7 +1233,6 @@ __global__ void __launch_bounds__(Cfg<FP8>::kThreads, 1)
                     const int slot = (tile + t) % kInfoSlots;
                     const int cs = ld % kCodeDepth, st = ld % C::kStages;
                     SVQ_WAIT(ct->code_full[cs], (ld / kCodeDepth) & 1, widen_end);
-                    SVQ_WAIT(ct->empty[st], ((ld / C::kStages) & 1) ^ 1, widen_end);
                     const unsigned char* src = codes + cs * (kTileTok * kHeadDim);
                     unsigned char* dst = ring + st * kStageBytes;
                     const int i0 = (s.t0 + t) * kTilePages;
@@ -1256,17 +1253,23 @@ __global__ void __launch_bounds__(Cfg<FP8>::kThreads, 1)
                             if (i0 + k < s.en.npages && !((fault >> k) & 1))
                                 on |= ((union_mask(logical_page(s.en, i0 + k) * kPage, qlo, qhi, a.window, a.sink) >> r) & 1u) << k;
                     }
+                    const int pages = min(kTilePages, s.en.npages - i0);   // (products with pages behind are masked or left out)
                     unsigned char* const o = dst + (r >> 3) * 2048 + (c >> 2) * 1024 + (r & 7) * 128;
                     const int at0 = ((2 * c) & 7 ^ (r & 7)) << 4, at1 = ((2 * c + 1) & 7 ^ (r & 7)) << 4;
-#pragma unroll 1
-                    for (int k0 = odd; k0 < 8; k0 += 4) {
-                        uint4 v[2], lo[2], hi[2];
-                        uint32_t nan = 0;
+                    // All of a thread's codes first, so that the next copy into their slot starts early.
+                    uint4 v[4];
 #pragma unroll
-                        for (int u = 0; u < 2; ++u) {
-                            v[u] = *reinterpret_cast<const uint4*>(src + (k0 + 2 * u) * (kPage * kHeadDim) + r * kHeadDim + c * 16);
-                            if (!((on >> (k0 + 2 * u)) & 1u)) v[u] = make_uint4(0u, 0u, 0u, 0u);
-                        }
+                    for (int u = 0; u < 4; ++u) {
+                        v[u] = *reinterpret_cast<const uint4*>(src + (odd + 2 * u) * (kPage * kHeadDim) + r * kHeadDim + c * 16);
+                        if (!((on >> (odd + 2 * u)) & 1u)) v[u] = make_uint4(0u, 0u, 0u, 0u);
+                    }
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(smem_addr(&ct->code_empty[cs]));
+                    SVQ_WAIT(ct->empty[st], ((ld / C::kStages) & 1) ^ 1, widen_end);
+#pragma unroll 1
+                    for (int k0 = odd; k0 < pages; k0 += 4) {
+                        uint4 lo[2], hi[2];
+                        uint32_t nan = 0;
 #pragma unroll
                         for (int u = 0; u < 2; ++u) {
                             nan |= has_nan(v[u].x) | has_nan(v[u].y) | has_nan(v[u].z) | has_nan(v[u].w);
@@ -1289,20 +1292,20 @@ __global__ void __launch_bounds__(Cfg<FP8>::kThreads, 1)
                             *reinterpret_cast<uint4*>(o + (k0 + 2 * u) * kPageBytes + at0) = lo[u];
                             *reinterpret_cast<uint4*>(o + (k0 + 2 * u) * kPageBytes + at1) = hi[u];
                         }
+                        v[0] = v[2];
+                        v[1] = v[3];
                     }
-                    if (is_k && c == 0 && on != 0xffu) {
-                        for (int k = odd; k < 8; k += 2)
-                            if (!((on >> k) & 1u)) {
-                                scales[slot * 2 * kTileTok + k * kPage + r] = 0.f;
-                                scales[slot * 2 * kTileTok + kTileTok + k * kPage + r] = 0.f;
-                            }
+                    // Scales of the tile's tokens, with its keys: 0 for tokens that no row sees.
+                    if (is_k && c < 4) {
+                        const int k = odd + 2 * c;
+                        float* const sc = scales + slot * 2 * kTileTok + k * kPage + r;
+                        const bool seen = (on >> k) & 1u;
+                        *sc = seen ? *sc * a.scale_log2 : 0.f;
+                        if (!seen) sc[kTileTok] = 0.f;
                     }
                     fence_proxy_async_smem();
                     __syncwarp();
-                    if (lane == 0) {
-                        mbar_arrive(smem_addr(&ct->full[st]));
-                        mbar_arrive(smem_addr(&ct->code_empty[cs]));
-                    }
+                    if (lane == 0) mbar_arrive(smem_addr(&ct->full[st]));
                     ++ld;
                 }
                 tile += n;
