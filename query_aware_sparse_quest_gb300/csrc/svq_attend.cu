@@ -1482,9 +1482,10 @@ __device__ __noinline__ void look_at_row(const AttendArgs& a, int entry, int h, 
     const Entry en = a.plan.entries[entry];
     const int tok = r / a.group, pos = en.pos0 + tok, end = en.pos0 + en.ntok;
     const int64_t qrow = static_cast<int64_t>(en.row0 + tok) * a.num_q_heads + h * a.group + (r - tok * a.group);
+    const uint2 w = *reinterpret_cast<const uint2*>(a.out + qrow * kHeadDim + 4 * lane);
+    const float4 got = make_float4(bf16lo(w.x), bf16hi(w.x), bf16lo(w.y), bf16hi(w.y));
     {
-        const uint2 w = *reinterpret_cast<const uint2*>(a.out + qrow * kHeadDim + 4 * lane);
-        const float odd = fmaf(bf16lo(w.x), 0.f, fmaf(bf16hi(w.x), 0.f, fmaf(bf16lo(w.y), 0.f, bf16hi(w.y) * 0.f)));
+        const float odd = fmaf(got.x, 0.f, fmaf(got.y, 0.f, fmaf(got.z, 0.f, got.w * 0.f)));
         if (!(fabsf(a.lse[qrow]) < INFINITY) || !__any_sync(0xffffffffu, odd != 0.f)) return;
     }
     const int32_t* const pages = a.page_table + static_cast<int64_t>(en.req) * a.max_pages;
@@ -1505,6 +1506,13 @@ __device__ __noinline__ void look_at_row(const AttendArgs& a, int entry, int h, 
         const int ph = pages[page];
         return ph < 0 || ph >= a.num_phys_pages ? -1ll : (static_cast<int64_t>(ph) * a.num_kv_heads + h) * kPage;
     };
+    if (const int64_t at = place_of(pos / kPage); at >= 0) {
+        // The row's own token is NaN wherever the row is not finite (a whole cache of NaN): so is the result.
+        const float4 v = row_of(a.v_pool, a.v_scale, at + pos % kPage);
+        const bool known = (v.x != v.x || got.x * 0.f == 0.f) && (v.y != v.y || got.y * 0.f == 0.f) &&
+                           (v.z != v.z || got.z * 0.f == 0.f) && (v.w != v.w || got.w * 0.f == 0.f);
+        if (__all_sync(0xffffffffu, known)) return;
+    }
     // Tokens [t0, t1) that other rows may see and this one does not.
     auto finite = [&](int t0, int t1) {
         float odd = 0.f;
@@ -1519,11 +1527,8 @@ __device__ __noinline__ void look_at_row(const AttendArgs& a, int entry, int h, 
     const bool later = finite(pos + 1, end);
     const bool passed = finite(max(a.sink, max(0, en.pos0 - a.window + 1)), max(0, pos - a.window + 1));
     if (later && passed) return;   // the row's own tokens gave it
-    float4 q;
-    {
-        const uint2 w = *reinterpret_cast<const uint2*>(a.q + qrow * kHeadDim + 4 * lane);
-        q = make_float4(bf16lo(w.x), bf16hi(w.x), bf16lo(w.y), bf16hi(w.y));
-    }
+    const uint2 qw = *reinterpret_cast<const uint2*>(a.q + qrow * kHeadDim + 4 * lane);
+    const float4 q = make_float4(bf16lo(qw.x), bf16hi(qw.x), bf16lo(qw.y), bf16hi(qw.y));
     RowSum s;
     for (int i = 0; i < en.npages; ++i) {
         const int page = logical_page(en, i);
