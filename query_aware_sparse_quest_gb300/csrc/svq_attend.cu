@@ -45,8 +45,7 @@
 // product's), with a window of 4096 tokens 212 us (1300 TFLOP/s of visible work;
 // 12 % of the tiles' work is masked or item cost); 7 ragged e4m3 requests of up
 // to 4000 tokens 89 us (52 % of the issue slots, the tensor pipe 18 %); 32
-// requests behind 32768 shared tokens 45 us, of which these tiles 21, what is
-// behind the prefix 11 and the join 13.
+// requests behind 32768 shared tokens 39 us, of which these tiles 21 to 25.
 #include <climits>
 
 #include "svq_paged.cuh"
@@ -62,13 +61,13 @@ int64_t window_decode_rows(int batch, int num_q_heads, int num_kv_heads);
 int launch_window_decode(const sv_cache* c, const void* q, int num_q_heads, const int32_t* page_table,
                          const int32_t* seq_lens, int batch, int max_pages, int window, int sink,
                          const int32_t* group_start, const int32_t* shared_pages, int num_groups, float softmax_scale,
-                         int splits, void* out, float* lse, float* o_part, float2* ml_part, cudaStream_t stream);
+                         const PrefixParts* prefix, int splits, void* out, float* lse, float* o_part, float2* ml_part,
+                         cudaStream_t stream);
 int launch_join_splits(const float* o_part, const float2* ml_part, int splits, int64_t rows, void* out, float* lse,
                        cudaStream_t stream);
 
 namespace {
 
-constexpr int kTilePages = 8;                       // pages of a key tile
 constexpr int kTileTok = kTilePages * kPage;        // 128 tokens
 constexpr int kPageBytes = kPage * kHeadDim * 2;    // a page's bf16 tile of one kv head: 4 KB
 constexpr int kStageBytes = kTilePages * kPageBytes;
@@ -92,28 +91,11 @@ struct __align__(16) Entry {
 };
 constexpr int kAllVisible = 1 << 30;
 
-__device__ __forceinline__ int tiles_of(int npages) { return (npages + kTilePages - 1) / kTilePages; }
-
-// What an item costs beside its tiles (loading Q, filling the pipeline, writing
-// the rows), in tiles: shares of the work count it, so that a CTA with many
-// short items does not take longer than one with few long ones.  7 ragged e4m3
-// requests / 32 requests behind a prefix, us: 1: 117 / 53.4, 2: 103.6 / 50.6,
-// 3: 103.3 / 48.9, 4: 102.6 / 49.1.
-constexpr int kItemCost = 3;
-__device__ __forceinline__ int cost_of(int tiles) { return tiles ? tiles + kItemCost : 0; }
-
 struct Plan {
     Entry* entries;
     int64_t* cum;      // [E + 1] cost per kv head of the entries before each
     int* num_entries;
     int* req_offset;   // first entry of each request
-};
-
-// A group as the join of its rows wants it.
-struct GroupRec {
-    int64_t before;    // cost per kv head of the groups before it
-    int tiles;         // 0: nothing is shared
-    int sound;
 };
 
 struct AttendArgs {
@@ -137,7 +119,7 @@ struct AttendArgs {
     float* lse;
     float* cut_o;      // [2 CTAs][slot_rows][128] partials of items that are cut
     float2* cut_ml;    // [2 CTAs][slot_rows] (base in log2 units, sum)
-    struct GroupRec* group_rec;   // prefixes: [groups + 1], for the join; the last one's cost is the total
+    GroupRec* group_rec;   // prefixes: [groups + 1], for the join; the last one's cost is the total
     int4* cut_item;    // chunks: [CTAs][2] the item that goes on in a CTA: row0, ntok, kv head, pieces (0: none is to
                        // be joined here); slot of the first piece, of the second, and the entry
     uint32_t* odd;     // chunks: 32-row parts of whole items with a channel that is not finite:
@@ -152,32 +134,6 @@ struct AttendArgs {
     int splits;
 };
 
-// a / b for non-negative values that mostly fit 32 bits (a 64-bit division takes
-// several times as long).
-__device__ __forceinline__ int64_t div64(int64_t a, int64_t b) {
-    if (((a | b) >> 32) == 0) return static_cast<uint32_t>(a) / static_cast<uint32_t>(b);
-    return a / b;
-}
-
-// The share of CTA c: total / ctas of the cost each, the first total % ctas one more.
-struct Share {
-    int64_t q, r;
-    __device__ __forceinline__ Share(int64_t total, int ctas) : q(div64(total, ctas)), r(total - q * ctas) {}
-    __device__ __forceinline__ int64_t start(int c) const { return c * q + (c < r ? c : r); }
-    __device__ __forceinline__ int cta_of(int64_t x) const {
-        const int64_t head = r * (q + 1);
-        return static_cast<int>(x < head ? div64(x, q + 1) : r + div64(x - head, q));
-    }
-};
-
-// An item's place in the shares: its cost begins at `begin`, its first tile
-// kItemCost later.
-struct Placed {
-    int64_t begin;
-    int tiles, c0, c1;   // the CTAs with its first and its last tile
-    __device__ __forceinline__ Placed(const Share& share, int64_t at, int n)
-        : begin(at), tiles(n), c0(share.cta_of(at + kItemCost)), c1(share.cta_of(at + kItemCost + n - 1)) {}
-};
 // Largest e in [0, n) with cum[e] <= u, by the whole warp (32 probes a round trip).
 __device__ __forceinline__ int warp_find(const int64_t* cum, int n, int64_t u) {
     const int lane = threadIdx.x & 31;
@@ -529,10 +485,9 @@ __global__ void __launch_bounds__(Cfg<FP8>::kThreads, 1)
                      : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
     }
-    // Chunks: the plan comes from the kernel launched just before.  Prefixes: this kernel shares
-    // nothing with the one before (the parts behind the prefix), which let it start only after what
-    // came before both had ended; it waits for that one at its end.
-    if (!a.groups.start) pdl_wait();
+    // Prefixes: what is behind them shares nothing with this kernel but the join at its end, and may
+    // start when all CTAs are past this wait.
+    pdl_wait();
     pdl_launch_dependents();
     tc_fence_before();
     __syncthreads();
@@ -1315,7 +1270,6 @@ __global__ void __launch_bounds__(Cfg<FP8>::kThreads, 1)
         }
     }
     __syncthreads();
-    if (a.groups.start) pdl_wait();
     if (warp == 1)
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem));
 }
@@ -1457,18 +1411,6 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const __grid_constan
 }
 
 // ---------------------------------------------------------------- joining partials
-// The partials of row r of an item that is cut: one of each of its CTAs.
-__device__ __forceinline__ Pieces cut_pieces(const AttendArgs& a, const Share& share, const Placed& it, int r) {
-    Pieces p;
-    p.o = a.cut_o;
-    p.ml = a.cut_ml;
-    p.n = it.c1 - it.c0 + 1;
-    p.stride = 2ll * a.slot_rows;
-    p.first = (2ll * it.c0 + (share.start(it.c0) >= it.begin ? 0 : 1)) * a.slot_rows + r;
-    p.second = 2ll * (it.c0 + 1) * a.slot_rows + r;
-    return p;
-}
-
 // A row of an entry whose outputs may not be finite, by one warp.  The tile's
 // product multiplies every value of the tile with a weight, and a weight 0 does
 // not hide an infinite or NaN value from the rows that do not see its token.  So
@@ -1623,13 +1565,15 @@ __global__ void __launch_bounds__(kCutThreads, 4) join_cut_kernel(const __grid_c
     }
 }
 
-// Prefixes: CTA (request x kv head, y) joins the prefixes, and what is behind
-// them, of group / gridDim.y rows; a row's pieces go in turn to the warps it
-// has.  With as few CTAs as fill the GPU: finding the pieces takes a CTA as
-// long as adding them (a CTA a row: 50 against 45 us for 61 requests).
+// Prefixes of so few requests that more than 8 splits a row read what is behind
+// them: CTA (request x kv head, y) joins both for group / gridDim.y rows; a row's
+// pieces go in turn to the warps it has.  With as few CTAs as fill the GPU:
+// finding the pieces takes a CTA as long as adding them (a CTA a row: 50 against
+// 45 us for 61 requests).
 constexpr int kPrefixThreads = 512;
 
-__global__ void __launch_bounds__(kPrefixThreads) join_prefix_kernel(const __grid_constant__ AttendArgs a, int ctas) {
+__global__ void __launch_bounds__(kPrefixThreads) join_prefix_kernel(const __grid_constant__ AttendArgs a,
+                                                                     const __grid_constant__ PrefixParts prefix) {
     constexpr int kWarps = kPrefixThreads / 32;
     __shared__ RowSum parts[kWarps][32];
     const int b = blockIdx.x / a.num_kv_heads, h = blockIdx.x % a.num_kv_heads;
@@ -1649,7 +1593,7 @@ __global__ void __launch_bounds__(kPrefixThreads) join_prefix_kernel(const __gri
     const bool on = mine < rows && hr < a.group;
     pdl_wait();
     const GroupRec rec = a.group_rec[g];
-    const int64_t total = a.group_rec[a.groups.n].before * a.num_kv_heads;
+    const int64_t total = a.group_rec[a.groups.n].before;
     if (!rec.sound) fault = SV_DEVERR_GROUP;
     if (fault && h == 0 && blockIdx.y == 0 && threadIdx.x == 0) svq_flag(fault);
     const int64_t q = static_cast<int64_t>(b) * a.num_q_heads + h * a.group + hr;
@@ -1657,12 +1601,7 @@ __global__ void __launch_bounds__(kPrefixThreads) join_prefix_kernel(const __gri
     if (on && page >= 0 && rec.sound) {
         int k0 = part;
         if (page > 0) {
-            const Share share(total, ctas);
-            const int cost = cost_of(rec.tiles);
-            const Placed it(share, (rec.before + static_cast<int64_t>(e) * cost) * a.num_kv_heads + static_cast<int64_t>(h) * cost,
-                            rec.tiles);
-            const Pieces p = it.c0 == it.c1 ? Pieces{a.whole_o, a.whole_ml, q, q, 0, 1}
-                                            : cut_pieces(a, share, it, row * a.group + hr);
+            const Pieces p = prefix_pieces(prefix, rec, total, a.num_kv_heads, h, e, row * a.group + hr, q);
             s.add(p, k0, per_row, lane);
             k0 = (k0 + per_row - p.n % per_row) % per_row;
         }
@@ -1806,13 +1745,13 @@ int launch_window(const sv_cache* c, const void* q, int num_q_heads, const int32
         const int cluster = window_decode_cluster(fp8, batch, c->num_kv_heads, pages, ctas, false);
         if (cluster)
             return launch_window_decode(c, q, num_q_heads, page_table, seq_lens, batch, max_pages, window, sink, nullptr,
-                                        nullptr, 0, softmax_scale, cluster, out, lse, nullptr, nullptr, stream);
+                                        nullptr, 0, softmax_scale, nullptr, cluster, out, lse, nullptr, nullptr, stream);
         const int splits = window_decode_splits(fp8, batch, c->num_kv_heads, pages, ctas);
         const int64_t heads = static_cast<int64_t>(batch) * num_q_heads;
         float* o = static_cast<float*>(workspace);
         float2* ml = reinterpret_cast<float2*>(static_cast<unsigned char*>(workspace) + up(heads * splits * kHeadDim * sizeof(float)));
         const int st = launch_window_decode(c, q, num_q_heads, page_table, seq_lens, batch, max_pages, window, sink, nullptr,
-                                            nullptr, 0, softmax_scale, splits, nullptr, nullptr, o, ml, stream);
+                                            nullptr, 0, softmax_scale, nullptr, splits, nullptr, nullptr, o, ml, stream);
         return st ? st : launch_join_splits(o, ml, splits, heads, out, lse, stream);
     }
     const Layout lay(batch, total_q, num_q_heads, c->num_kv_heads, 0);
@@ -1836,7 +1775,7 @@ int launch_prefix(const sv_cache* c, const void* q, int num_q_heads, const int32
     const bool fp8 = c->kv_format == SV_KV_FP8_E4M3;
     if (prefix_alone(fp8, batch, c->num_kv_heads, max_pages))
         return launch_window_decode(c, q, num_q_heads, page_table, seq_lens, batch, max_pages, 0, 0, group_start,
-                                    shared_pages, num_groups, softmax_scale,
+                                    shared_pages, num_groups, softmax_scale, nullptr,
                                     window_decode_cluster(fp8, batch, c->num_kv_heads, max_pages, ctas, true), out, lse,
                                     nullptr, nullptr, stream);
     AttendArgs a = attend_args(c, q, num_q_heads, page_table, max_pages, lay, 0, 0, softmax_scale, out, lse, workspace);
@@ -1848,16 +1787,22 @@ int launch_prefix(const sv_cache* c, const void* q, int num_q_heads, const int32
     a.group_rec = reinterpret_cast<GroupRec*>(ws + lay.group_rec);
     a.split_o = reinterpret_cast<float*>(ws + lay.split_o);
     a.split_ml = reinterpret_cast<float2*>(ws + lay.split_ml);
-    a.splits = window_decode_splits(fp8, batch, c->num_kv_heads, max_pages, ctas);
-    int st = launch_window_decode(c, q, num_q_heads, page_table, seq_lens, batch, max_pages, 0, 0, group_start,
-                                  shared_pages, num_groups, softmax_scale, a.splits, nullptr, nullptr, a.split_o, a.split_ml,
-                                  stream);
+    int st = launch_tiles(c, a, ctas, stream);
     if (st) return st;
-    if ((st = launch_tiles(c, a, ctas, stream))) return st;
+    const PrefixParts prefix = {a.group_rec, a.cut_o, a.cut_ml, a.whole_o, a.whole_ml, a.slot_rows, a.tok_per_entry, ctas};
+    const int cluster = window_decode_cluster(fp8, batch, c->num_kv_heads, max_pages, ctas, false);
+    if (cluster)
+        return launch_window_decode(c, q, num_q_heads, page_table, seq_lens, batch, max_pages, 0, 0, group_start,
+                                    shared_pages, num_groups, softmax_scale, &prefix, cluster, out, lse, nullptr, nullptr,
+                                    stream);
+    a.splits = window_decode_splits(fp8, batch, c->num_kv_heads, max_pages, ctas);
+    st = launch_window_decode(c, q, num_q_heads, page_table, seq_lens, batch, max_pages, 0, 0, group_start, shared_pages,
+                              num_groups, softmax_scale, &prefix, a.splits, nullptr, nullptr, a.split_o, a.split_ml, stream);
+    if (st) return st;
     const int rows = batch * c->num_kv_heads, fill = 2 * ctas / rows;   // two CTAs of 512 threads an SM
     const int y = fill < 1 ? 1 : (fill < a.group ? fill : a.group);
     return launch_pdl(join_prefix_kernel, dim3(rows, y), dim3(kPrefixThreads), 0, stream,
-                      a, ctas) == cudaSuccess
+                      a, prefix) == cudaSuccess
                ? SV_OK
                : SV_ERR_CUDA;
 }

@@ -8,6 +8,26 @@
 #include "svq_common.cuh"
 
 namespace svq {
+
+// A group whose prefix the tiles work on, as the join of its rows wants it.
+struct GroupRec {
+    int64_t before;    // cost per kv head of the groups before it
+    int tiles;         // 0: nothing is shared
+    int sound;
+};
+
+// What the tiles leave of the prefixes.
+struct PrefixParts {
+    const GroupRec* rec;   // [groups + 1]; the last one's cost is the total
+    const float* cut_o;    // partials of items that are cut
+    const float2* cut_ml;
+    const float* whole_o;  // those of whole items, [B Hq][128]
+    const float2* whole_ml;
+    int slot_rows;
+    int tok_per_entry;     // requests of a row tile
+    int ctas;              // that shared the work
+};
+
 namespace {
 
 __device__ __forceinline__ float ex2(float x) {
@@ -113,6 +133,45 @@ inline bool encode_pages_map(CUtensorMap* map, const void* pool, int64_t row_gro
                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// ---------------------------------------------------------------- shares of the tiles' work
+constexpr int kTilePages = 8;                       // pages of a key tile
+__device__ __forceinline__ int tiles_of(int npages) { return (npages + kTilePages - 1) / kTilePages; }
+
+// What an item costs beside its tiles (loading Q, filling the pipeline, writing
+// the rows), in tiles: shares of the work count it, so that a CTA with many
+// short items does not take longer than one with few long ones.  7 ragged e4m3
+// requests / 32 requests behind a prefix, us: 1: 117 / 53.4, 2: 103.6 / 50.6,
+// 3: 103.3 / 48.9, 4: 102.6 / 49.1.
+constexpr int kItemCost = 3;
+__device__ __forceinline__ int cost_of(int tiles) { return tiles ? tiles + kItemCost : 0; }
+
+// a / b for non-negative values that mostly fit 32 bits (a 64-bit division takes
+// several times as long).
+__device__ __forceinline__ int64_t div64(int64_t a, int64_t b) {
+    if (((a | b) >> 32) == 0) return static_cast<uint32_t>(a) / static_cast<uint32_t>(b);
+    return a / b;
+}
+
+// The share of CTA c: total / ctas of the cost each, the first total % ctas one more.
+struct Share {
+    int64_t q, r;
+    __device__ __forceinline__ Share(int64_t total, int ctas) : q(div64(total, ctas)), r(total - q * ctas) {}
+    __device__ __forceinline__ int64_t start(int c) const { return c * q + (c < r ? c : r); }
+    __device__ __forceinline__ int cta_of(int64_t x) const {
+        const int64_t head = r * (q + 1);
+        return static_cast<int>(x < head ? div64(x, q + 1) : r + div64(x - head, q));
+    }
+};
+
+// An item's place in the shares: its cost begins at `begin`, its first tile
+// kItemCost later.
+struct Placed {
+    int64_t begin;
+    int tiles, c0, c1;   // the CTAs with its first and its last tile
+    __device__ __forceinline__ Placed(const Share& share, int64_t at, int n)
+        : begin(at), tiles(n), c0(share.cta_of(at + kItemCost)), c1(share.cta_of(at + kItemCost + n - 1)) {}
+};
+
 // ---------------------------------------------------------------- joining partials
 // A list of partials (o, (base, sum)) of one row; the base is in log2 units, o
 // and the sum are relative to it.
@@ -125,6 +184,28 @@ struct Pieces {
     int n;
     __device__ __forceinline__ int64_t row(int k) const { return k == 0 ? first : second + (k - 1) * stride; }
 };
+
+// The partials of row r of an item that is cut: one of each of its CTAs.
+__device__ __forceinline__ Pieces cut_pieces(const PrefixParts& a, const Share& share, const Placed& it, int r) {
+    Pieces p;
+    p.o = a.cut_o;
+    p.ml = a.cut_ml;
+    p.n = it.c1 - it.c0 + 1;
+    p.stride = 2ll * a.slot_rows;
+    p.first = (2ll * it.c0 + (share.start(it.c0) >= it.begin ? 0 : 1)) * a.slot_rows + r;
+    p.second = 2ll * (it.c0 + 1) * a.slot_rows + r;
+    return p;
+}
+
+// Those of a request's row in its prefix: entry e of group rec (whose entries
+// come behind rec.before), row r of it, row q of the batch.
+__device__ __forceinline__ Pieces prefix_pieces(const PrefixParts& a, const GroupRec& rec, int64_t total, int num_kv_heads,
+                                                int h, int e, int r, int64_t q) {
+    const Share share(total * num_kv_heads, a.ctas);
+    const int cost = cost_of(rec.tiles);
+    const Placed it(share, (rec.before + static_cast<int64_t>(e) * cost) * num_kv_heads + static_cast<int64_t>(h) * cost, rec.tiles);
+    return it.c0 == it.c1 ? Pieces{a.whole_o, a.whole_ml, q, q, 0, 1} : cut_pieces(a, share, it, r);
+}
 
 // A row's running (base, sum, four channels of the output) and the pieces
 // k, k + step, ... of a list, four at a time.

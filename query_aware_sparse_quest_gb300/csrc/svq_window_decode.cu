@@ -12,7 +12,10 @@
 // CTA (request x kv head, split): warp 4 loads the split's pages, warps 0-3
 // take them in turn, keep a softmax of their own and join through shared
 // memory.  Up to 8 splits of a row are one cluster and join through distributed
-// shared memory; the partials of more are joined by a second kernel.
+// shared memory; the partials of more are joined by a second kernel.  Behind a
+// prefix a cluster also joins what the tiles left of it, so the tiles and this
+// kernel, which starts while the last of them run, are the whole call (32
+// requests behind 32768 tokens 39.2 us; with a kernel for the join 44.2).
 //
 // e4m3 pools: codes convert to f16 exactly and the products run in f16.  The
 // value weight of token t is exp(z_t) s_v(t).  It is formed as
@@ -42,6 +45,7 @@ namespace {
 
 constexpr int kWarps = 4;                          // consumer warps; warp w takes pages w, w + 4, ...
 constexpr int kThreads = (kWarps + 1) * 32;
+constexpr int kParts = kWarps + 1;                 // what a CTA joins: its warps' and a prefix's part
 constexpr int kStages = 8;                         // pages in flight, four producer lanes each
 constexpr float kSlack = 8.f;                      // log2 units a base may lag behind the maximum
 constexpr int kMaxSplits = 64;
@@ -73,7 +77,7 @@ struct Cfg {
     static constexpr int kSmem = 1024 + kStages * (2 * kTile + kScale);
     static constexpr int kPerSm = FP8 ? 4 : 3;
 };
-static_assert(kStages * 2 * Cfg<true>::kTile >= (kWarps * kMaxGroup * (kHeadDim + 3) + 2 * kMaxGroup) * 4, "the warps merge through the ring");
+static_assert(kStages * 2 * Cfg<true>::kTile >= (kParts * kMaxGroup * (kHeadDim + 3) + 2 * kMaxGroup) * 4, "the warps merge through the ring");
 
 struct Args {
     const __nv_bfloat16* q;
@@ -83,7 +87,7 @@ struct Args {
     int max_pages;
     int64_t num_phys_pages;
     Groups groups;              // requests that share pages; none: the window's are read
-    bool alone;                 // groups: all pages of a request are read, not only those behind the shared ones
+    PrefixParts prefix;         // PREFIX: what a cluster joins with its part
     int window;                 // INT_MAX: none
     int sink;
     int num_splits;
@@ -155,15 +159,17 @@ __device__ __forceinline__ float4 ld_cluster_f4(uint32_t addr, int rank) {
 struct View {
     int sinks, w0, count;
     int shared, row;   // the first `shared` pages are read from this row of the table
+    int group;
 };
 // By whole warps; `report`: one of them says what is wrong.
+template <bool PREFIX>
 __device__ __forceinline__ View view_of(const Args& a, int len, int b, bool report) {
-    View v = {0, 0, 0, 0, b};
+    View v = {0, 0, 0, 0, b, 0};
     if (a.groups.start) {
         uint32_t fault;   // of parts behind a prefix: the join reports it
         int g;
         v.w0 = page_behind(a.groups, b, len, fault, g);
-        if (a.alone && v.w0 >= 0) {
+        if (!PREFIX && v.w0 >= 0) {
             int reach = 0;
             bool sound = true;
             for (int g0 = 0; g0 <= g && sound; g0 += 32) {
@@ -183,8 +189,9 @@ __device__ __forceinline__ View view_of(const Args& a, int len, int b, bool repo
             v.w0 = sound ? 0 : -1;
             if (!sound) fault = SV_DEVERR_GROUP;
         }
-        if (a.alone && fault && report) svq_flag(fault);
-        if (v.w0 < 0) return {0, 0, 0, 0, b};
+        if (a.out && fault && report) svq_flag(fault);
+        if (v.w0 < 0) return {0, 0, 0, 0, b, -1};
+        v.group = g;
     } else if (len <= 0) {
         return v;
     } else {
@@ -195,7 +202,9 @@ __device__ __forceinline__ View view_of(const Args& a, int len, int b, bool repo
     return v;
 }
 
-template <bool FP8>
+// PREFIX: requests that share pages, of which the tiles have read the shared ones:
+// only those behind are read here, and the cluster joins both.
+template <bool FP8, bool PREFIX>
 __global__ void __launch_bounds__(kThreads, Cfg<FP8>::kPerSm)
     window_decode_kernel(const __grid_constant__ Args a, const __grid_constant__ CUtensorMap tmap_k,
                          const __grid_constant__ CUtensorMap tmap_v) {
@@ -225,14 +234,14 @@ __global__ void __launch_bounds__(kThreads, Cfg<FP8>::kPerSm)
 
     int len = a.seq_lens[b];
     bool touched = true;
-    if (a.alone) {
+    if (a.groups.start) {
         touched = b >= a.groups.start[0] && b < a.groups.start[a.groups.n];
         // What is wrong with groups that hold no row.
-        if (blockIdx.x == 0 && split == 0)
+        if (!PREFIX && blockIdx.x == 0 && split == 0)
             for (int g = threadIdx.x; g < a.groups.n; g += kThreads)
                 if (!a.groups.sound(a.groups.start[g], a.groups.start[g + 1], a.groups.pages[g])) svq_flag(SV_DEVERR_GROUP);
     } else if (len < 0 || (static_cast<int64_t>(len) + kPage - 1) / kPage > a.max_pages) {
-        if (threadIdx.x == 0 && split == 0 && !a.groups.start) svq_flag(SV_DEVERR_SEQ_LEN);
+        if (threadIdx.x == 0 && split == 0) svq_flag(SV_DEVERR_SEQ_LEN);
         len = 0;
     }
     if (warp == kWarps) {
@@ -259,8 +268,10 @@ __global__ void __launch_bounds__(kThreads, Cfg<FP8>::kPerSm)
             }
         }
     }
-    const View v = view_of(a, len, b, split == 0 && h == 0 && threadIdx.x == 0);
-    pdl_wait();   // the pools and the workspace, which the work before may still use
+    const View v = view_of<PREFIX>(a, len, b, split == 0 && h == 0 && threadIdx.x == 0);
+    // The pools and the workspace, which the work before may still use.  Behind a prefix: the tiles,
+    // which let this kernel start when what came before them had ended.
+    if (!PREFIX) pdl_wait();
     const int chunk = (v.count + a.num_splits - 1) / a.num_splits;
     const int j0 = min(v.count, split * chunk);
     const int mine = min(v.count, j0 + chunk) - j0;
@@ -337,6 +348,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<FP8>::kPerSm)
         if (last >= 0) (void)mbar_wait_bounded(fb, (last / kStages) & 1);
         if (!a.out) {
             pdl_launch_dependents();   // (results may be inputs of what comes next)
+            if (PREFIX) pdl_wait();
             return;
         }
         __syncwarp();
@@ -485,11 +497,11 @@ __global__ void __launch_bounds__(kThreads, Cfg<FP8>::kPerSm)
     }
     // Join the warps through shared memory (every page has been consumed: no copy is in flight).
     asm volatile("bar.sync 1, %0;" ::"n"(kWarps * 32) : "memory");
-    float* const sm_o = reinterpret_cast<float*>(ring);             // [warp][8][128]
-    float* const sm_m = sm_o + kWarps * kMaxGroup * kHeadDim;       // [warp][8] bases, output bases, sums
-    float* const sm_d = sm_m + kWarps * kMaxGroup;
-    float* const sm_l = sm_d + kWarps * kMaxGroup;
-    float2* const sm_fin = reinterpret_cast<float2*>(sm_l + kWarps * kMaxGroup);   // [8] the CTA's
+    float* const sm_o = reinterpret_cast<float*>(ring);             // [warp, prefix][8][128]
+    float* const sm_m = sm_o + kParts * kMaxGroup * kHeadDim;       // [warp, prefix][8] bases, output bases, sums
+    float* const sm_d = sm_m + kParts * kMaxGroup;
+    float* const sm_l = sm_d + kParts * kMaxGroup;
+    float2* const sm_fin = reinterpret_cast<float2*>(sm_l + kParts * kMaxGroup);   // [8] the CTA's
     {
         float* const ow = sm_o + warp * kMaxGroup * kHeadDim;
         const int h0 = 2 * quad, h1 = 2 * quad + 1;
@@ -507,16 +519,66 @@ __global__ void __launch_bounds__(kThreads, Cfg<FP8>::kPerSm)
             sm_l[warp * kMaxGroup + hh] = row ? l[1] : l[0];
         }
     }
-    asm volatile("bar.sync 1, %0;" ::"n"(kWarps * 32) : "memory");
+    // What the tiles left of this row's prefix: the splits take the pieces in turn, warp w those of
+    // heads w and w + 4.  (Partials: the join wants the tiles to have ended before this kernel does.)
     const int64_t q0 = static_cast<int64_t>(b) * a.num_q_heads + h * a.group;
+    int parts = kWarps;   // what there is to join
+    bool dead = false;    // the row's group is not sound
+    if (PREFIX) pdl_wait();
+    if (PREFIX && a.out && v.group >= 0) {
+        const GroupRec rec = a.prefix.rec[v.group];
+        const int64_t total = a.prefix.rec[a.groups.n].before;
+        dead = !rec.sound;
+        if (rec.sound && v.w0 > 0) {
+            const int at = b - a.groups.start[v.group], e = at / a.prefix.tok_per_entry;
+            const Pieces p = prefix_pieces(a.prefix, rec, total, a.num_kv_heads, h, e,
+                                           (at - e * a.prefix.tok_per_entry) * a.group, q0);
+            parts = kParts;
+            const bool two = warp + kWarps < a.group;
+            const int h0 = min(warp, a.group - 1), h1 = two ? warp + kWarps : h0;
+            RowSum s0, s1;
+            for (int k = split; k < p.n; k += 4 * a.num_splits) {
+                float2 ml[8];
+                float4 x[8];
+#pragma unroll
+                for (int u = 0; u < 4; ++u) {
+                    const int piece = k + u * a.num_splits;
+                    ml[u] = ml[u + 4] = make_float2(-INFINITY, 0.f);
+                    x[u] = x[u + 4] = make_float4(0.f, 0.f, 0.f, 0.f);
+                    if (piece < p.n) {
+                        const int64_t row = p.row(piece);
+                        ml[u] = p.ml[row + h0];
+                        ml[u + 4] = p.ml[row + h1];
+                        x[u] = *reinterpret_cast<const float4*>(p.o + (row + h0) * kHeadDim + 4 * lane);
+                        x[u + 4] = *reinterpret_cast<const float4*>(p.o + (row + h1) * kHeadDim + 4 * lane);
+                    }
+                }
+#pragma unroll
+                for (int u = 0; u < 4; ++u) {
+                    s0.join(RowSum{ml[u].x, ml[u].y, x[u]});
+                    s1.join(RowSum{ml[u + 4].x, ml[u + 4].y, x[u + 4]});
+                }
+            }
+            auto put = [&](int hh, const RowSum& s) {
+                const int at = kWarps * kMaxGroup + hh;
+                *reinterpret_cast<float4*>(sm_o + at * kHeadDim + 4 * lane) = s.o;
+                if (lane == 0) sm_m[at] = sm_d[at] = s.m, sm_l[at] = s.l;
+            };
+            if (warp < a.group) put(warp, s0);
+            if (two) put(warp + kWarps, s1);
+        }
+    }
+    asm volatile("bar.sync 1, %0;" ::"n"(kWarps * 32) : "memory");
     for (int idx = threadIdx.x; idx < a.group * kHeadDim; idx += kWarps * 32) {
         const int hh = idx / kHeadDim, d = idx % kHeadDim;
         float M = -INFINITY, L = 0.f, O = 0.f;
 #pragma unroll
-        for (int w = 0; w < kWarps; ++w) M = fmaxf(M, sm_m[w * kMaxGroup + hh]);
+        for (int w = 0; w < (PREFIX ? kParts : kWarps); ++w)
+            if (w < parts) M = fmaxf(M, sm_m[w * kMaxGroup + hh]);
         const float base = M == -INFINITY ? 0.f : M;
 #pragma unroll
-        for (int w = 0; w < kWarps; ++w) {
+        for (int w = 0; w < (PREFIX ? kParts : kWarps); ++w) {
+            if (w >= parts) break;
             L += sm_l[w * kMaxGroup + hh] * ex2(sm_m[w * kMaxGroup + hh] - base);
             O += sm_o[(w * kMaxGroup + hh) * kHeadDim + d] * ex2(sm_d[w * kMaxGroup + hh] - base);
         }
@@ -558,6 +620,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<FP8>::kPerSm)
             s.o.z += x[u].z * f;
             s.o.w += x[u].w * f;
         }
+        if (dead) s = RowSum{};
         if (touched) (void)s.write(a.out + (q0 + hh) * kHeadDim, a.lse + q0 + hh, lane);
     }
     __syncwarp();
@@ -591,11 +654,11 @@ bool encode_codes_map(CUtensorMap* map, const void* pool, int64_t rows) {
                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <bool FP8>
+template <bool FP8, bool PREFIX>
 int launch(const Args& a, const CUtensorMap& tk, const CUtensorMap& tv, int batch, cudaStream_t stream) {
     static std::atomic<bool> attr_set[64];
     const int st = once_per_device(attr_set, [] {
-        return cudaFuncSetAttribute(window_decode_kernel<FP8>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+        return cudaFuncSetAttribute(window_decode_kernel<FP8, PREFIX>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                     Cfg<FP8>::kSmem) == cudaSuccess
                    ? SV_OK
                    : SV_ERR_CUDA;
@@ -615,7 +678,7 @@ int launch(const Args& a, const CUtensorMap& tk, const CUtensorMap& tv, int batc
     attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = a.out ? 2 : 1;
-    return cudaLaunchKernelEx(&cfg, window_decode_kernel<FP8>, a, tk, tv) == cudaSuccess ? SV_OK : SV_ERR_CUDA;
+    return cudaLaunchKernelEx(&cfg, window_decode_kernel<FP8, PREFIX>, a, tk, tv) == cudaSuccess ? SV_OK : SV_ERR_CUDA;
 }
 
 }  // namespace
@@ -663,7 +726,8 @@ int64_t window_decode_rows(int batch, int num_q_heads, int num_kv_heads) {
 int launch_window_decode(const sv_cache* c, const void* q, int num_q_heads, const int32_t* page_table,
                          const int32_t* seq_lens, int batch, int max_pages, int window, int sink,
                          const int32_t* group_start, const int32_t* shared_pages, int num_groups, float softmax_scale,
-                         int splits, void* out, float* lse, float* o_part, float2* ml_part, cudaStream_t stream) {
+                         const PrefixParts* prefix, int splits, void* out, float* lse, float* o_part, float2* ml_part,
+                         cudaStream_t stream) {
     const bool fp8 = c->kv_format == SV_KV_FP8_E4M3;
     // TMA coordinates are 32-bit.
     const int64_t rows = c->num_phys_pages * c->num_kv_heads * kPage;
@@ -684,7 +748,7 @@ int launch_window_decode(const sv_cache* c, const void* q, int num_q_heads, cons
     a.groups = Groups{group_start, shared_pages, num_groups, batch, max_pages};
     a.window = window > 0 ? window : INT_MAX;
     a.sink = sink;
-    a.alone = group_start && out;
+    a.prefix = prefix ? *prefix : PrefixParts{};
     a.num_splits = splits;
     a.out = static_cast<__nv_bfloat16*>(out);
     a.lse = lse;
@@ -693,7 +757,8 @@ int launch_window_decode(const sv_cache* c, const void* q, int num_q_heads, cons
     a.v_scale = static_cast<const float*>(c->v_scale);
     a.o_part = o_part;
     a.ml_part = ml_part;
-    return fp8 ? launch<true>(a, tk, tv, batch, stream) : launch<false>(a, tk, tv, batch, stream);
+    if (prefix) return fp8 ? launch<true, true>(a, tk, tv, batch, stream) : launch<false, true>(a, tk, tv, batch, stream);
+    return fp8 ? launch<true, false>(a, tk, tv, batch, stream) : launch<false, false>(a, tk, tv, batch, stream);
 }
 
 int launch_join_splits(const float* o_part, const float2* ml_part, int splits, int64_t rows, void* out, float* lse,

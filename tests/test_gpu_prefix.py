@@ -174,3 +174,37 @@ def test_repeats_and_graph(fp8):
     torch.cuda.synchronize()
     check(out, lse, reference(case, q, range(23)))
     assert binding.sv_get_device_error() == 0
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("group", [3, 8])
+def test_many_requests(group, fp8):
+    """Enough rows that the parts behind the prefixes join them: groups of all sizes, one without shared pages, padded
+    requests, one short of its group's pages, requests in no group, and one behind groups out of order."""
+    starts, shared = [0, 1, 20, 20, 43, 45], [7, 30, 5, 0, 2]
+    lens = []
+    for g in range(5):
+        lens += [shared[g] * PAGE + (17 * i) % 70 + (g == 3) for i in range(starts[g + 1] - starts[g])]
+    lens += [40, 50]
+    case = PagedCase(lens, 2, fp8=fp8)
+    share(case, starts, shared)
+    q = queries(case, group)
+    ref = reference(case, q, range(45))
+    out, lse = run(case, q, starts, shared)
+    assert binding.sv_get_device_error() == 0
+    check(out[:45], lse[:45], ref)
+    assert (out[45:] == 7).all() and (lse[45:] == 7).all()
+    good = [b for b in range(45) if b not in (5, 9, 30)]
+    case.lens[5], case.lens[9], case.lens[30] = 0, 30 * PAGE - 1, -4
+    out, lse = run(case, q, starts, shared)
+    assert binding.sv_get_device_error() == 0x48
+    check(out[good], lse[good], [x[good] for x in ref])
+    assert (out[[5, 9, 30]] == 0).all() and torch.isneginf(lse[[5, 9, 30]]).all()
+    # Group 1 ends behind where group 3 begins: group 3's rows that are not group 1's are empty.
+    case.lens = lens
+    out, lse = run(case, q, [0, 1, 20, 11, 43, 45], shared)
+    assert binding.sv_get_device_error() & 0x40
+    for b in range(45):
+        if not ((out[b] == 0).all() and torch.isneginf(lse[b]).all()):
+            check(out[b:b + 1], lse[b:b + 1], [x[b:b + 1] for x in ref])
+    assert (out[25] == 0).all() and torch.isneginf(lse[25]).all()
