@@ -41,10 +41,10 @@
 // short runs: the start, the first copies, and partials.  Measured on a GB300
 // (copy 6.8 TB/s, library bf16 product 1895 TFLOP/s), 32 query / 4 kv heads, time
 // of a call in a run of calls: a 4096-token chunk at 32768 tokens, causal, 1.24
-// to 1.35 ms by the card's power (1530 to 1660 TFLOP/s, 81 to 88 % of the
+// to 1.36 ms by the card's power (1520 to 1660 TFLOP/s, 80 to 88 % of the
 // product's), with a window of 4096 tokens 212 us (1300 TFLOP/s of visible work;
 // 12 % of the tiles' work is masked or item cost); 7 ragged e4m3 requests of up
-// to 4000 tokens 89 us (52 % of the issue slots, the tensor pipe 18 %); 32
+// to 4000 tokens 89 us (48 % of the issue slots, the tensor pipe 18 %); 32
 // requests behind 32768 shared tokens 39 us, of which these tiles 21 to 25.
 #include <climits>
 
