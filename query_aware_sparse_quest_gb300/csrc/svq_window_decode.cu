@@ -30,8 +30,8 @@
 // time of a call: 8 requests with a window of 4096 tokens 16.4 us (67.5 MB, 4.1
 // TB/s; 10 us at the copy's rate: 5 us are the kernel's start, the first copies
 // and the join), 32 e4m3 requests with a window of 2048 21.4 us (70.5 MB, 3.3
-// TB/s: 40 % of the issue slots go to widening codes, with 4 warps an SM's
-// quarter waiting on one another's pages), 32 requests at 32768 tokens without a
+// TB/s: 40 % of the issue slots are taken and DRAM is 35 % busy; latency within
+// a page's chain of conversions and products), 32 requests at 32768 tokens without a
 // window 308 us (2.15 GB, 7.0 TB/s).
 #include <climits>
 
