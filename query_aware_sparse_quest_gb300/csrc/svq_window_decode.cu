@@ -22,9 +22,11 @@
 // 2^(y_t - B), y_t = log2(e) z_t + log2 s_v(t), with a running base B of its own
 // beside the softmax's, so that it uses f16's range whatever the values' scale
 // (exp(z_t) s_v(t) itself would fall below f16's normal numbers for values
-// under 0.03 and above its largest one for values over 3e7).  P is rounded to
-// bf16 (e4m3 pools: f16), the type of the other operand of its product; sums and
-// outputs are fp32.
+// under 0.03 and above its largest one for values over 3e7).  P enters its
+// product in the other operand's type: f16 over e4m3 pools, and two bf16 parts
+// over bf16 pools (the weight's first 8 bits and the next 8), as one part's 2^-8
+// would be as large an error as the output's own rounding; sums and outputs are
+// fp32.
 //
 // Measured on a GB300 (a plain copy: 6.8 TB/s), 32 query / 4 kv heads, device
 // time of a call: 8 requests with a window of 4096 tokens 16.4 us (67.5 MB, 4.1
@@ -456,20 +458,24 @@ __global__ void __launch_bounds__(kThreads, Cfg<FP8>::kPerSm)
         l[0] += p0 + p2;
         l[1] += p1 + p3;
         // P^T as the B operand: lane needs tokens 2 quad + {0, 1} (+ 8) (k slots) of head `row`.
-        uint32_t lo, hi;
+        const int src0 = (2 * quad) * 4 + (row >> 1), src1 = (2 * quad + 1) * 4 + (row >> 1);
+        const uint32_t selector = (row & 1) ? 0x7632u : 0x5410u;
+        auto operand = [&](uint32_t heads) {   // tokens 2 quad, + 1 of head `row`, from the lanes with pairs of heads
+            return __byte_perm(__shfl_sync(0xffffffffu, heads, src0), __shfl_sync(0xffffffffu, heads, src1), selector);
+        };
+        uint32_t pb0, pb1, rb0 = 0, rb1 = 0;
         if (FP8) {
             const float d0 = mo[0] == -INFINITY ? 0.f : mo[0], d1 = mo[1] == -INFINITY ? 0.f : mo[1];
-            lo = pack_half2(ex2(y0 - d0), ex2(y1 - d1));
-            hi = pack_half2(ex2(y2 - d0), ex2(y3 - d1));
+            pb0 = operand(pack_half2(ex2(y0 - d0), ex2(y1 - d1)));
+            pb1 = operand(pack_half2(ex2(y2 - d0), ex2(y3 - d1)));
         } else {
-            lo = pack_bf16x2(p0, p1);
-            hi = pack_bf16x2(p2, p3);
+            // A weight cut to bf16, and what is left of it (not quite 0, so that an infinite value stays one).
+            auto rest = [](float p) { return fmaxf(p - __uint_as_float(__float_as_uint(p) & 0xffff0000u), 0x1p-126f); };
+            pb0 = operand(__byte_perm(__float_as_uint(p0), __float_as_uint(p1), 0x7632u));
+            pb1 = operand(__byte_perm(__float_as_uint(p2), __float_as_uint(p3), 0x7632u));
+            rb0 = operand(pack_bf16x2(rest(p0), rest(p1)));
+            rb1 = operand(pack_bf16x2(rest(p2), rest(p3)));
         }
-        const int src0 = (2 * quad) * 4 + (row >> 1), src1 = (2 * quad + 1) * 4 + (row >> 1);
-        const uint32_t lo0 = __shfl_sync(0xffffffffu, lo, src0), lo1 = __shfl_sync(0xffffffffu, lo, src1);
-        const uint32_t hi0 = __shfl_sync(0xffffffffu, hi, src0), hi1 = __shfl_sync(0xffffffffu, hi, src1);
-        const uint32_t selector = (row & 1) ? 0x7632u : 0x5410u;
-        const uint32_t pb0 = __byte_perm(lo0, lo1, selector), pb1 = __byte_perm(hi0, hi1, selector);
         // O^T (128 channels x 8) += V^T P^T
         if (FP8) {
 #pragma unroll
@@ -485,6 +491,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<FP8>::kPerSm)
                 uint32_t r0, r1, r2, r3;
                 ldmatrix_x4_trans(vs_s + bf16_at(vrow, 2 * mt + (mat & 1)), r0, r1, r2, r3);
                 mma_bf16_16816(o[mt], r0, r1, r2, r3, pb0, pb1);
+                mma_bf16_16816(o[mt], r0, r1, r2, r3, rb0, rb1);
             }
         }
         __syncwarp();   // every lane has read the stage before it is released

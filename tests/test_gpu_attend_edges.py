@@ -1,0 +1,38 @@
+"""sv_window_attention and sv_prefix_decode where a row sees nothing, over queries and weights of any size, and
+over values that are not finite."""
+from __future__ import annotations
+
+import pytest
+import torch
+
+import test_gpu_prefix as prefix
+from attend_ref import DIM, PAGE, PagedCase, attend, check, window_seen
+from query_aware_sparse_quest_gb300 import binding
+from test_gpu_window import compare, run
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda"
+
+
+def ints(x):
+    return torch.tensor(x, dtype=torch.int32, device=DEV)
+
+
+def gauss(*shape, seed=3):
+    return torch.randn(shape, generator=torch.Generator().manual_seed(seed))
+
+
+@pytest.mark.parametrize("lens,group,window,sink", [
+    ([2, 3, 5, 17], 8, 0, 0), ([300, 77], 7, 0, 0), ([5000, 1, 40], 4, 333, 5), ([3000], 1, 0, 0), ([20000] * 3, 2, 0, 0),
+])
+def test_single_tokens_over_bf16_keep_their_weights(lens, group, window, sink):
+    """Weights enter the product as two bf16 parts: the second is less than 2^-7 of a weight and off by 2^-8 of itself."""
+    case = PagedCase(lens, 2)
+    q = (3 * gauss(len(lens), 2 * group, DIM)).bfloat16().to(DEV)
+    seen = [window_seen(n, 1, window, sink, DEV) for n in lens]
+    tokens = [case.tokens(b) for b in range(len(lens))]
+    o, ls, tol, tol_lse = (torch.cat(x) for x in zip(*[attend(q[b:b + 1], *tokens[b], seen[b], DIM ** -0.5) for b in range(len(lens))]))
+    size = torch.cat([attend(q[b:b + 1], k, torch.nan_to_num(v).abs(), seen[b], DIM ** -0.5)[0] for b, (k, v) in enumerate(tokens)])
+    # attend()'s bound with 2^-15 in place of P's 2^-8, in the output's own rounding too
+    tol = tol - (2.0 ** -8 - 2.0 ** -15) * (1 + 2.0 ** -8) * size
+    check(*run(case, q, window, sink), (o, ls, tol, tol_lse))
