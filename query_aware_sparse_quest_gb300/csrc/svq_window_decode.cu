@@ -50,6 +50,9 @@ constexpr int kThreads = (kWarps + 1) * 32;
 constexpr int kParts = kWarps + 1;                 // what a CTA joins: its warps' and a prefix's part
 constexpr int kStages = 8;                         // pages in flight, four producer lanes each
 constexpr float kSlack = 8.f;                      // log2 units a base may lag behind the maximum
+// e4m3: a value weight is 2^(y - B + kF16Lift) in f16, at most 2^15 (below f16's 65504).  Its smallest step, 2^-24,
+// is then 2^-31 of a weight at the base.
+constexpr float kF16Lift = 7.f;
 constexpr int kMaxSplits = 64;
 constexpr int kMaxCluster = 8;                     // CTAs of a cluster at most (what every launch may have)
 // At least this many pages a split once every SM has work (a split costs its
@@ -465,7 +468,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<FP8>::kPerSm)
         };
         uint32_t pb0, pb1, rb0 = 0, rb1 = 0;
         if (FP8) {
-            const float d0 = mo[0] == -INFINITY ? 0.f : mo[0], d1 = mo[1] == -INFINITY ? 0.f : mo[1];
+            const float d0 = mo[0] == -INFINITY ? 0.f : mo[0] - kF16Lift, d1 = mo[1] == -INFINITY ? 0.f : mo[1] - kF16Lift;
             pb0 = operand(pack_half2(ex2(y0 - d0), ex2(y1 - d1)));
             pb1 = operand(pack_half2(ex2(y2 - d0), ex2(y3 - d1)));
         } else {
@@ -522,7 +525,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<FP8>::kPerSm)
         if (row < 2) {
             const int hh = row ? h1 : h0;
             sm_m[warp * kMaxGroup + hh] = row ? m[1] : m[0];
-            sm_d[warp * kMaxGroup + hh] = row ? mo[1] : mo[0];
+            sm_d[warp * kMaxGroup + hh] = (row ? mo[1] : mo[0]) - (FP8 ? kF16Lift : 0.f);
             sm_l[warp * kMaxGroup + hh] = row ? l[1] : l[0];
         }
     }

@@ -36,3 +36,24 @@ def test_single_tokens_over_bf16_keep_their_weights(lens, group, window, sink):
     # attend()'s bound with 2^-15 in place of P's 2^-8, in the output's own rounding too
     tol = tol - (2.0 ** -8 - 2.0 ** -15) * (1 + 2.0 ** -8) * size
     check(*run(case, q, window, sink), (o, ls, tol, tol_lse))
+
+
+def test_small_weights_over_e4m3_count_in_the_output():
+    """One token of value 0 outweighs the others of its page by 2^26; the output is theirs alone.
+
+    A weight is held in f16 relative to 2^-7 of the largest of its page, in steps of 2^-24 at least: off by at
+    most 2^-32 of the largest, and in 15 tokens of value 1 by 15 of those."""
+    case = PagedCase([PAGE], 1, fp8=True)
+    page = case.table[0, 0]
+    case.k[page], case.v[page] = 0, 0x7E                     # 448
+    case.v[page, 0, 0] = 0
+    case.ks[page], case.vs[page] = 1.0, 1 / 448
+    q = torch.zeros((1, 4, DIM), dtype=torch.bfloat16, device=DEV)
+    q[:, :, 0] = 1
+    lift = torch.tensor([26 * 0.6931471805599453 / 448])
+    case.k[page, 0, 1:, 0] = 0xFE                            # -448
+    case.ks[page, 0, 1:] = lift
+    ref = attend(q, *case.tokens(0), window_seen(PAGE, 1, 0, 0, DEV), 1.0)
+    assert (ref[0] - 15 * 2.0 ** -26).abs().max() < 1e-10
+    ref[2].add_(15 * 2.0 ** -32)
+    check(*run(case, q, 0, 0, scale=1.0), ref)
