@@ -354,8 +354,6 @@ size_t sv_quest_decode_step_workspace_size(int32_t batch, int32_t num_q_heads, i
  *    it are concerned: infinite and NaN values reach only those that do.  (A
  *    value seen by some query tokens of a row tile and not by others is put
  *    right afterwards, a row at a time: slow, and only then.)
- *  - e4m3 pools: a call with q_start NULL (and sv_prefix_decode, behind the
- *    prefix) takes q in fp16, so |q| <= 65504.
  *  - Rows of one request and kv head are processed 256 at a time
  *    (token, query head), on the tensor cores; work is divided evenly over
  *    the GPU whatever the lengths.  The result does not depend on timing.

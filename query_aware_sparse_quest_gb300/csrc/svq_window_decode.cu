@@ -254,9 +254,12 @@ __global__ void __launch_bounds__(kThreads, Cfg<FP8>::kPerSm)
         prefetch_tmap(&tmap_v);
     }
     // Q^T fragments (B operand): head `row` of the group.  bf16: channels 16 k + 2 quad (+ 8).  e4m3: f16,
-    // channels 16 k + 4 quad .. + 3 (a dot product does not depend on the channels' order).
+    // channels 16 k + 4 quad .. + 3 (a dot product does not depend on the channels' order), times a power of
+    // two that puts the head's largest channel into 2^14 .. 2^15: channels down to 2^-28 of it keep all their
+    // bits, whatever their size.  `back`: what undoes that for the heads of this lane's logits.
     const int quad = lane & 3, row = lane >> 2;
     uint32_t qf[8][2];
+    float back[2] = {1.f, 1.f};
     if (warp < kWarps) {
         const bool hv = row < a.group;
         const __nv_bfloat16* qh =
@@ -265,12 +268,28 @@ __global__ void __launch_bounds__(kThreads, Cfg<FP8>::kPerSm)
         for (int k = 0; k < 8; ++k) {
             if (FP8) {
                 const uint2 w = hv ? *reinterpret_cast<const uint2*>(qh + 16 * k + 4 * quad) : make_uint2(0u, 0u);
-                qf[k][0] = pack_half2(bf16lo(w.x), bf16hi(w.x));
-                qf[k][1] = pack_half2(bf16lo(w.y), bf16hi(w.y));
+                qf[k][0] = w.x;
+                qf[k][1] = w.y;
             } else {
                 qf[k][0] = hv ? *reinterpret_cast<const uint32_t*>(qh + 16 * k + 2 * quad) : 0u;
                 qf[k][1] = hv ? *reinterpret_cast<const uint32_t*>(qh + 16 * k + 8 + 2 * quad) : 0u;
             }
+        }
+        if (FP8) {
+            uint32_t top = 0;   // magnitudes of bf16 are in the order of their bits
+#pragma unroll
+            for (int k = 0; k < 8; ++k) top = __vmaxu2(top, __vmaxu2(qf[k][0] & 0x7fff7fffu, qf[k][1] & 0x7fff7fffu));
+            top = __vmaxu2(top, __shfl_xor_sync(0xffffffffu, top, 1));
+            top = __vmaxu2(top, __shfl_xor_sync(0xffffffffu, top, 2));
+            const int exponent = static_cast<int>(max(top >> 16, top & 0xffffu)) >> 7;
+            const int up = min(127 + 14 - exponent, 126);
+            const float scale = __int_as_float((127 + up) << 23), undo = __int_as_float((127 - up) << 23);
+            back[0] = __shfl_sync(0xffffffffu, undo, 8 * quad);
+            back[1] = __shfl_sync(0xffffffffu, undo, 8 * quad + 4);
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+#pragma unroll
+                for (int u = 0; u < 2; ++u) qf[k][u] = pack_half2(bf16lo(qf[k][u]) * scale, bf16hi(qf[k][u]) * scale);
         }
     }
     const View v = view_of<PREFIX>(a, len, b, split == 0 && h == 0 && threadIdx.x == 0);
@@ -421,10 +440,11 @@ __global__ void __launch_bounds__(kThreads, Cfg<FP8>::kPerSm)
         const float* const sc = scale_ring + st * (C::kScale / 4);
         const float f0 = FP8 && on0 ? sc[tok0] * a.scale_log2 : a.scale_log2;
         const float f1 = FP8 && on1 ? sc[tok1] * a.scale_log2 : a.scale_log2;
-        const float x0 = on0 ? (sa[0] + sb[0]) * f0 : -INFINITY;   // token tok0, head 2 quad
-        const float x1 = on0 ? (sa[1] + sb[1]) * f0 : -INFINITY;   // token tok0, head 2 quad + 1
-        const float x2 = on1 ? (sa[2] + sb[2]) * f1 : -INFINITY;   // token tok1, head 2 quad
-        const float x3 = on1 ? (sa[3] + sb[3]) * f1 : -INFINITY;   // token tok1, head 2 quad + 1
+        const float k0 = FP8 ? back[0] : 1.f, k1 = FP8 ? back[1] : 1.f;
+        const float x0 = on0 ? (sa[0] + sb[0]) * k0 * f0 : -INFINITY;   // token tok0, head 2 quad
+        const float x1 = on0 ? (sa[1] + sb[1]) * k1 * f0 : -INFINITY;   // token tok0, head 2 quad + 1
+        const float x2 = on1 ? (sa[2] + sb[2]) * k0 * f1 : -INFINITY;   // token tok1, head 2 quad
+        const float x3 = on1 ? (sa[3] + sb[3]) * k1 * f1 : -INFINITY;   // token tok1, head 2 quad + 1
         // e4m3: the logarithm of the value weights.
         const float lv0 = FP8 && on0 ? lg2(sc[kPage + tok0]) : 0.f, lv1 = FP8 && on1 ? lg2(sc[kPage + tok1]) : 0.f;
         const float y0 = FP8 ? x0 + lv0 : x0, y1 = FP8 ? x1 + lv0 : x1, y2 = FP8 ? x2 + lv1 : x2, y3 = FP8 ? x3 + lv1 : x3;

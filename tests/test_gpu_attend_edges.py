@@ -57,3 +57,49 @@ def test_small_weights_over_e4m3_count_in_the_output():
     assert (ref[0] - 15 * 2.0 ** -26).abs().max() < 1e-10
     ref[2].add_(15 * 2.0 ** -32)
     check(*run(case, q, 0, 0, scale=1.0), ref)
+
+
+# Queries of every size a bf16 has, with a scale that makes ordinary logits of them.
+SIZES = {"1e-6": (1e-6, 1e5), "1e-30": (1e-30, 1e28), "3e4": (3e4, 3e-6), "1e30": (1e30, 1e-31),
+         "mixed": (None, 1.0)}
+
+
+def sized(q, name):
+    size, scale = SIZES[name]
+    if size is None:                     # channels over 20 powers of two, the largest near 1
+        return (q * torch.exp2(-(torch.arange(DIM) * 7 % 20).float())).bfloat16(), scale
+    return (q * size).bfloat16(), scale
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("name", list(SIZES))
+def test_queries_of_any_size(name, fp8):
+    """A token alone, the same one as a chunk, and behind a prefix, read alone or in tiles."""
+    lens, group = [700, 33, 260], 4
+    case = PagedCase(lens, 2, fp8=fp8)
+    q, scale = sized(gauss(3, 2 * group, DIM), name)
+    q = q.to(DEV)
+    ref = [torch.cat(x) for x in zip(*[attend(q[b:b + 1], *case.tokens(b), window_seen(n, 1, 0, 0, DEV), scale)
+                                       for b, n in enumerate(lens)])]
+    for starts in (None, [0, 1, 2, 3]):
+        out, lse = run(case, q, 0, 0, starts, scale)
+        check(out, lse, ref)
+    cache, lens = case.cache(), ints(lens)
+    ws = torch.empty(binding.sv_prefix_decode_workspace_size(3, 2 * group, 2, 3), dtype=torch.uint8, device=DEV)
+    for wide in (0, 5000):
+        table = torch.nn.functional.pad(case.table, (0, wide), value=-1).to(DEV)
+        binding.sv_prefix_decode(cache, q, table, lens, ints([0, 1, 2, 3]), ints([20, 1, 0]), out, lse, ws, softmax_scale=scale)
+        check(out, lse, ref)
+    assert binding.sv_get_device_error() == 0
+
+
+def test_queries_of_infinity_and_nan_over_e4m3():
+    """They give NaN to their own heads alone."""
+    case = PagedCase([100], 2, fp8=True)
+    q = gauss(1, 8, DIM).bfloat16().to(DEV)
+    ref = attend(q, *case.tokens(0), window_seen(100, 1, 0, 0, DEV), DIM ** -0.5)
+    q[0, 2, 9], q[0, 5, 0] = float("inf"), float("nan")
+    out, lse = run(case, q, 0, 0)
+    good = [0, 1, 3, 4, 6, 7]
+    check(out[:, good], lse[:, good], [x[:, good] for x in ref])
+    assert out[:, [2, 5]].isnan().all() and not lse[:, [2, 5]].isfinite().any()
