@@ -1111,7 +1111,7 @@ __global__ void __launch_bounds__(Cfg<FP8>::kThreads, 1)
                 }
                 tc_fence_after();
                 if (warp_on) {
-                    const float inv = po ? 1.f : (L > 0.f ? 1.f / L : (L == 0.f ? 0.f : L));
+                    const float inv = po ? 1.f : (L > 0.f ? 1.f / L : L);
                     f0 *= inv;
                     f1 *= inv;
                     float odd = 0.f;   // NaN once a channel of the row is not finite
@@ -1143,8 +1143,8 @@ __global__ void __launch_bounds__(Cfg<FP8>::kThreads, 1)
 #pragma unroll
                                 for (int u = 0; u < 32; ++u) odd = fmaf(__uint_as_float(x[u]), 0.f, odd);
 #pragma unroll
-                                for (int u = 0; u < 16; ++u)
-                                    v[u] = pack_bf16x2(__uint_as_float(x[2 * u]), __uint_as_float(x[2 * u + 1]));
+                                for (int u = 0; u < 16; ++u)   // (a row that sees nothing is 0, whatever the others see)
+                                    v[u] = L == 0.f ? 0u : pack_bf16x2(__uint_as_float(x[2 * u]), __uint_as_float(x[2 * u + 1]));
 #pragma unroll
                                 for (int u = 0; u < 2; ++u)
                                     st_v8(a.out + qrow * kHeadDim + c * 32 + 16 * u, v[8 * u], v[8 * u + 1], v[8 * u + 2],
@@ -1152,7 +1152,7 @@ __global__ void __launch_bounds__(Cfg<FP8>::kThreads, 1)
                             }
                         }
                     }
-                    if (!po && __any_sync(0xffffffffu, odd != 0.f && L < INFINITY) && lane == 0)
+                    if (!po && __any_sync(0xffffffffu, odd != 0.f && L > 0.f && L < INFINITY) && lane == 0)
                         a.odd[atomicAdd(a.num_odd, 1)] = static_cast<uint32_t>(~s.slot) * 8 + (warp - 4 - (two ? 0 : w * 4));
                     if (valid && (two || w == 0)) {
                         if (po) *pml = make_float2(M, L);

@@ -263,16 +263,19 @@ struct RowSum {
         o.z = x[0].z * e + x[1].z * f;
         o.w = x[0].w * e + x[1].w * f;
     }
-    // Returns whether one of the lane's channels is not finite although the sum is.
+    // Returns whether one of the lane's channels is not finite although the sum is.  A row that sees nothing is
+    // 0, whatever its tile's other rows see.
     __device__ __forceinline__ bool write(__nv_bfloat16* out, float* lse, int lane) const {
-        const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);
-        uint2 v;
-        v.x = pack_bf16x2(o.x * inv, o.y * inv);
-        v.y = pack_bf16x2(o.z * inv, o.w * inv);
+        const float inv = l > 0.f ? 1.f / l : l;
+        uint2 v = make_uint2(0u, 0u);
+        if (l != 0.f) {
+            v.x = pack_bf16x2(o.x * inv, o.y * inv);
+            v.y = pack_bf16x2(o.z * inv, o.w * inv);
+        }
         *reinterpret_cast<uint2*>(out + 4 * lane) = v;
         if (lane == 0) *lse = l > 0.f ? (m + log2f(l)) * 0.69314718055994531f : (l == 0.f ? -INFINITY : l);
         const float odd = fmaf(o.x, 0.f, fmaf(o.y, 0.f, fmaf(o.z, 0.f, o.w * 0.f)));
-        return odd != 0.f && l < INFINITY;
+        return odd != 0.f && l > 0.f && l < INFINITY;
     }
 };
 

@@ -103,3 +103,30 @@ def test_queries_of_infinity_and_nan_over_e4m3():
     good = [0, 1, 3, 4, 6, 7]
     check(out[:, good], lse[:, good], [x[:, good] for x in ref])
     assert out[:, [2, 5]].isnan().all() and not lse[:, [2, 5]].isfinite().any()
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("requests", [1, 100])         # items that are cut; whole ones
+def test_rows_that_see_nothing_beside_a_nan(requests, fp8):
+    """A missing page empties some rows of a tile; others of the tile see a NaN.  The empty ones are 0, -inf."""
+    n, size, group, window = 200, 64, 4, 8
+    case = PagedCase([n] * requests, 2, fp8=fp8)
+    q = gauss(requests * size, 2 * group, DIM).bfloat16().to(DEV)
+    seen = window_seen(n, size, window, 0, DEV)
+    seen[:, 144:160] = False
+    ref = [attend(q[b * size:(b + 1) * size], *case.tokens(b), seen, DIM ** -0.5) for b in range(requests)]
+    nan = 163
+    for b in range(requests):
+        case.v[case.table[b, nan // PAGE], :, nan % PAGE, 5] = 0x7F if fp8 else float("nan")
+        case.table[b, 144 // PAGE] = -1
+    out, lse = run(case, q, window, 0, [b * size for b in range(requests + 1)])
+    assert binding.sv_get_device_error() == 0x1
+    empty = (~seen.any(1)).repeat(requests)
+    assert empty.sum() == 9 * requests
+    assert (out[empty] == 0).all() and torch.isneginf(lse[empty]).all()
+    hit = torch.zeros((n - (n - size), DIM), dtype=torch.bool, device=DEV)
+    hit[:, 5] = seen[:, nan]
+    hit = hit.repeat(requests, 1)[:, None].expand(-1, 2 * group, -1)
+    assert torch.equal(out.isnan(), hit)
+    o, ls, tol, tol_lse = (torch.cat(x) for x in zip(*ref))
+    check(torch.where(hit, 0, out), lse, (torch.where(hit, 0, o), ls, tol, tol_lse))
