@@ -1553,6 +1553,7 @@ __global__ void __launch_bounds__(kCutThreads, 4) join_cut_kernel(const __grid_c
             odd |= join_row<kWarps>(pieces(r), sm_o, sm_ml, a.out + at_row(r) * kHeadDim, a.lse + at_row(r));
     }
     if (__any_sync(0xffffffffu, odd)) {   // of the rows this warp wrote
+        __syncwarp();                     // (their lse by its first lane)
         for (int r = n <= 8 ? blockIdx.y * kWarps + warp : blockIdx.y; r < rows; r += n <= 8 ? gridDim.y * kWarps : gridDim.y)
             look_at_row(a, where.z, what.z, r);
     }
