@@ -513,8 +513,8 @@ __global__ void __launch_bounds__(kMoveThreads) free_kernel(const __grid_constan
         return;
     }
     const int pages = (len + kPage - 1) / kPage;
-    const int lo = first ? max(0, first[i]) : 0;
     const int hi = end ? min(pages, end[i]) : pages;
+    const int lo = first ? min(max(0, first[i]), pages) : 0;   // (so that lo + a thread's number does not wrap)
     int32_t* row = t.table + static_cast<int64_t>(r) * t.max_pages;
     for (int p = lo + threadIdx.x; p < hi; p += kMoveThreads) {
         const int e = atomicExch(&row[p], -1);
