@@ -480,8 +480,8 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kPlanThreads)
     }
     cluster_sync();
     const int ntok = min(tokens, a.num_slots);
-    for (int k = me; k < ntok; k += kAll) {
-        const int i = find_le(a.tok, a.n, k);
+    for (int64_t at = me; at < ntok; at += kAll) {   // (a list may have all the entries that 32 bits count)
+        const int k = static_cast<int>(at), i = find_le(a.tok, a.n, k);
         int slot = -1;
         if (granted(i)) {
             const int pos = a.len[i] + k - a.tok[i], fresh = pos / kPage - (a.len[i] + kPage - 1) / kPage;
