@@ -440,7 +440,10 @@ int sv_pages_copy(const sv_cache* caches, int32_t num_caches, const int32_t* src
  * themselves.  The shared pages are what sv_prefix_decode reads once.  Child
  * rows hold nothing before (their entries are overwritten).  A child listed
  * twice (its first mention counts), or one that is also a parent, is
- * SV_DEVERR_ROW; a fork for which no page is left is SV_DEVERR_NO_PAGE.
+ * SV_DEVERR_ROW; a fork for which no page is left is SV_DEVERR_NO_PAGE; one of a
+ * row that lists a page outside the pool, or whose partly filled page was freed,
+ * is SV_DEVERR_PAGE_TABLE, and one of a row that lists a free page
+ * SV_DEVERR_REF_COUNT.
  */
 int sv_pages_fork(const sv_cache* caches, int32_t num_caches, int32_t* page_table, int32_t* seq_lens, int32_t num_rows,
                   int32_t max_pages, int32_t* ref_counts, const int32_t* parents, const int32_t* children, int32_t n,

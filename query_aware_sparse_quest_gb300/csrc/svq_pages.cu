@@ -221,6 +221,7 @@ struct ForkArgs {
     int32_t* who;        // [n] the forks that take a page, in order
     int32_t* rank;       // [n] a fork's place among those, -1: it takes none
     int32_t* take;       // [n] page the fork got, kNone: needs none, kSkip: not made
+    uint32_t* wrong;     // [n] what is wrong with its parent's pages (error bits)
 };
 constexpr int kNone = -1, kSkip = -2;
 // Rows listed twice are found by letting every list entry name itself at its
@@ -230,6 +231,31 @@ constexpr int kNone = -1, kSkip = -2;
 constexpr int kRowsHere = 4096;
 
 __device__ __forceinline__ bool row_ok(const Rows& t, int r) { return r >= 0 && r < t.num_rows; }
+// What a CTA that finds something wrong adds to its count of free pages (at most 2^24 of them).
+constexpr int kWrong = 1 << 25;
+// What is wrong with the pages that row p of `len` tokens lists, by a warp (a lane's share): full ones may be -1,
+// let go of behind a window.  Spans `part`, part + parts, ... of them.
+__device__ __forceinline__ uint32_t pages_fault(const Rows& t, int p, int len, int part, int parts) {
+    constexpr int kLoads = 8;   // in flight
+    if (!row_ok(t, p) || !len_ok(t, len)) return 0u;
+    const int full = len / kPage, pages = (len + kPage - 1) / kPage;
+    const int32_t* row = t.table + static_cast<int64_t>(p) * t.max_pages;
+    uint32_t wrong = 0;
+    for (int p0 = part * kLoads * 32 + threadIdx.x % 32; p0 < pages; p0 += parts * kLoads * 32) {
+        int e[kLoads];
+#pragma unroll
+        for (int u = 0; u < kLoads; ++u) e[u] = p0 + 32 * u < pages ? row[p0 + 32 * u] : -1;
+#pragma unroll
+        for (int u = 0; u < kLoads; ++u) {
+            if (e[u] < 0 || e[u] >= t.num_pages) {
+                if (e[u] != -1 || (p0 + 32 * u == full && full < pages)) wrong |= SV_DEVERR_PAGE_TABLE;
+            } else if (t.counts[e[u]] <= 0) {
+                wrong |= SV_DEVERR_REF_COUNT;
+            }
+        }
+    }
+    return wrong;
+}
 
 __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kPlanThreads)
     fork_plan_kernel(const __grid_constant__ ForkArgs a) {
@@ -260,6 +286,10 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kPlanThreads)
     }
     int lo, hi;
     slice(a.t.num_pages, rank, lo, hi);
+    // The other CTAs look at the parents' pages while the first walks the list (no count changes before it is done).
+    const int checker = rank > 0 ? (threadIdx.x / 32) * (kCluster - 1) + rank - 1 : 0;
+    constexpr int kCheckers = (kCluster - 1) * (kPlanThreads / 32);
+    int parent = a.parents[checker % a.n], parent_len = row_ok(a.t, parent) ? a.t.lens[parent] : 0;   // (early)
     publish(count_free(a.t.counts, lo, hi), rank, warp_sums, frees);
     if (rank == 0) {
         if (here) {
@@ -290,11 +320,7 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kPlanThreads)
                         svq_flag(SV_DEVERR_SEQ_LEN);
                     } else {
                         take = kNone;
-                        if (len % kPage) {
-                            const int e = a.t.table[static_cast<int64_t>(p) * a.t.max_pages + len / kPage];
-                            if (e >= 0 && e < a.t.num_pages) need = 1;
-                            else svq_flag(SV_DEVERR_PAGE_TABLE);
-                        }
+                        need = len % kPage != 0;
                     }
                 }
             }
@@ -308,20 +334,49 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kPlanThreads)
             base += total;
         }
         if (threadIdx.x == 0) cluster_store(&needed, base);
+    } else {
+        uint32_t found = 0;
+        const int parts = max(1, kCheckers / a.n);
+        for (int w = checker; w < a.n * parts; w += kCheckers) {
+            if (w != checker) parent = a.parents[w % a.n], parent_len = row_ok(a.t, parent) ? a.t.lens[parent] : 0;
+            found |= pages_fault(a.t, parent, parent_len, w / a.n, parts);
+        }
+        if (__syncthreads_or(found) && threadIdx.x == 0) cluster_store(frees + rank, frees[rank] + kWrong);
     }
     cluster_sync();
     int before = 0, all = 0;
+    bool wrong = false;
     for (int r = 0; r < kCluster; ++r) {
-        if (r < rank) before += frees[r];
-        all += frees[r];
+        const int free = frees[r] % kWrong;
+        if (r < rank) before += free;
+        all += free;
+        wrong |= frees[r] >= kWrong;
     }
-    // The r-th free page goes to the r-th fork that takes one (a CTA's scan is past the counts it changes).
+    if (wrong) {   // which forks
+        for (int i = me; i < a.n; i += kAll) a.wrong[i] = 0;
+        cluster_sync();
+        for (int i = me / 32; i < a.n; i += kAll / 32) {
+            parent = a.parents[i];
+            const uint32_t fault = pages_fault(a.t, parent, row_ok(a.t, parent) ? a.t.lens[parent] : 0, 0, 1);
+            if (fault) atomicOr(&a.wrong[i], fault);
+        }
+        cluster_sync();
+    }
+    // The r-th free page goes to the r-th fork that takes one (a CTA's scan is past the counts it changes).  It
+    // stays free if something is wrong with the pages of that fork's parent.
     each_free(a.t.counts, lo, hi, before, needed, warp_sums, [&](int r, int p) {
-        a.take[a.who[r]] = p;
+        const int i = a.who[r];
+        if (wrong && a.wrong[i]) return;
+        a.take[i] = p;
         a.t.counts[p] = 1;
     });
     for (int i = me; i < a.n; i += kAll) {
-        if (a.rank[i] >= all) {
+        if (wrong && a.wrong[i]) {
+            if (a.rank[i] >= 0 || a.take[i] == kNone) {
+                a.take[i] = kSkip;
+                svq_flag(a.wrong[i]);
+            }
+        } else if (a.rank[i] >= all) {
             a.take[i] = kSkip;
             svq_flag(SV_DEVERR_NO_PAGE);
         }
@@ -348,8 +403,7 @@ __global__ void __launch_bounds__(kMoveThreads) fork_move_kernel(const __grid_co
     for (int p = threadIdx.x; p < full; p += kMoveThreads) {
         const int e = from[p];
         to[p] = e;
-        if (e >= 0 && e < a.t.num_pages) atomicAdd(&a.t.counts[e], 1);
-        else if (e != -1) svq_flag(SV_DEVERR_PAGE_TABLE);
+        if (e >= 0) atomicAdd(&a.t.counts[e], 1);   // (the plan has looked at them)
     }
     if (threadIdx.x == 0) {
         if (len % kPage) to[full] = take;
@@ -652,16 +706,16 @@ size_t up(size_t n) { return (n + 255) / 256 * 256; }
 
 }  // namespace
 
-// owner, is_parent, then three lists of n + 1 (fork: who, rank, take; reserve:
-// need, tok, len), then three of num_pages (reserve: free; compact: src, dst,
+// owner, is_parent, then four lists of n + 1 (fork: who, rank, take, wrong;
+// reserve: need, tok, len), then three of num_pages (reserve: free; compact: src, dst,
 // to) and a word.
 size_t pages_workspace_bytes(int64_t num_pages, int num_rows, int n) {
-    return 2 * up(4ull * num_rows) + 3 * up(4ull * (static_cast<size_t>(n) + 1)) + 3 * up(4ull * num_pages) + 256;
+    return 2 * up(4ull * num_rows) + 4 * up(4ull * (static_cast<size_t>(n) + 1)) + 3 * up(4ull * num_pages) + 256;
 }
 
 namespace {
 struct Carve {
-    int32_t *owner, *is_parent, *a, *b, *c, *p, *q, *r, *word;
+    int32_t *owner, *is_parent, *a, *b, *c, *d, *p, *q, *r, *word;
     Carve(void* ws, int64_t num_pages, int num_rows, int n) {
         unsigned char* at = static_cast<unsigned char*>(ws);
         auto take = [&](size_t ints) { int32_t* x = reinterpret_cast<int32_t*>(at); at += up(4 * ints); return x; };
@@ -670,6 +724,7 @@ struct Carve {
         a = take(static_cast<size_t>(n) + 1);
         b = take(static_cast<size_t>(n) + 1);
         c = take(static_cast<size_t>(n) + 1);
+        d = take(static_cast<size_t>(n) + 1);
         p = take(num_pages);
         q = take(num_pages);
         r = take(num_pages);
@@ -694,7 +749,7 @@ int launch_pages_fork(const sv_cache* caches, int num_caches, int32_t* table, in
     const int num_pages = static_cast<int>(caches[0].num_phys_pages);
     const Carve w(ws, num_pages, num_rows, n);
     ForkArgs a = {{table, lens, num_rows, max_pages, counts, num_pages}, parents, children, n, w.owner, w.is_parent,
-                  w.a, w.b, w.c};
+                  w.a, w.b, w.c, reinterpret_cast<uint32_t*>(w.d)};
     const int st = launched(launch_pdl(fork_plan_kernel, dim3(kCluster), dim3(kPlanThreads), 0, stream, a));
     if (st) return st;
     return launched(launch_pdl(fork_move_kernel, dim3(n, num_caches + 1), dim3(kMoveThreads), 0, stream, set, a));

@@ -33,3 +33,48 @@ def test_as_many_slots_as_an_index_counts():
     assert slots[:5].tolist() == d.m.reserve([0], [5])
     assert (slots[5:2 ** 30] == -1).all() and (slots[2 ** 30:] == -1).all()
     d.same(0x8)
+
+
+@pytest.mark.parametrize("page", [0, 2])
+@pytest.mark.parametrize("entry", [-1, 40, 2 ** 31 - 1, -2 ** 31])
+def test_a_row_with_a_page_that_is_none_is_not_forked(entry, page):
+    """Page 2 is partly filled, so a fork wants a copy of it; page 0 is shared, or was let go of behind a window."""
+    d = Device(Model(40, 6, 5))
+    d.reserve([0, 1], [40, 37])
+    d.table[0, page] = entry
+    d.m.table[0][page] = entry
+    binding.sv_pages_fork(d.list, d.table, d.lens, d.counts, ints([1, 0, 0]), ints([3, 2, 4]), d.ws)
+    made = page == 0 and entry == -1
+    d.m.fork([1, 0, 0] if made else [1], [3, 2, 4] if made else [3])
+    d.same(0 if made else 0x1)
+
+
+@pytest.mark.parametrize("count", [0, -3])
+@pytest.mark.parametrize("page", [0, 1, 2])
+@pytest.mark.parametrize("rows", [8, 5000])
+def test_a_row_with_a_free_page_is_not_forked(rows, page, count):
+    """Its pages could be another row's next."""
+    d = Device(Model(40, rows, 5))
+    d.reserve([0, 1], [40, 37])
+    p = d.m.table[0][page]
+    d.counts[p] = count
+    binding.sv_pages_fork(d.list, d.table, d.lens, d.counts, ints([1, 0, 0]), ints([3, 2, 4]), d.ws)
+    d.m.counts[p] = 0
+    d.m.fork([1], [3])                       # takes the free page, which is the lowest
+    d.same(0x100)
+
+
+@pytest.mark.parametrize("page", [0, 31, 32, 255, 256, 299])
+def test_one_free_page_among_many_is_found(page):
+    """Forks of every row but one, more than a cluster has warps; row 100 lists a free page."""
+    rows, per = 300, 300
+    d = Device(Model(rows + per + 9, 2 * rows, per), heads=(1,), fp8=(False,))
+    d.reserve(list(range(rows)), [PAGE] * rows)
+    d.reserve([100], [(per - 1) * PAGE])
+    p = d.m.table[100][page]
+    d.counts[p] = 0
+    d.m.counts[p] = 0
+    binding.sv_pages_fork(d.list, d.table, d.lens, d.counts, ints(list(range(rows))), ints(list(range(rows, 2 * rows))), d.ws)
+    others = [r for r in range(rows) if r != 100]
+    d.m.fork(others, [rows + r for r in others])
+    d.same(0x100)
