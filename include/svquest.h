@@ -412,7 +412,8 @@ size_t sv_prefix_decode_workspace_size(int32_t batch, int32_t num_q_heads, int32
  *                neither read nor written.
  *   ref_counts   int32 [num_phys_pages]: how many rows hold a page.  A page is
  *                free when its count is 0.  Whoever else keeps pages (a prefix
- *                cache) adds to their counts.  All start at 0.
+ *                cache) adds to their counts, and follows them through
+ *                sv_pages_compact_ex's page_map.  All start at 0.
  * New pages are always the lowest free ones, in the order of the list that
  * asks for them, so every result is determined by the arguments.  `caches` is
  * an array of num_caches (1 .. SV_MAX_CACHES) caches, one a layer, that share
@@ -481,11 +482,19 @@ int sv_pages_free(int32_t* page_table, int32_t* seq_lens, int32_t num_rows, int3
  * the device), and rewrites the tables of all rows and the counts.
  * page_table_out and ref_counts_out may be the inputs themselves; if they are
  * not, a step still running on the old table reads the old pages, whose data
- * stay until something new is written there.
+ * stay until something new is written there, and entries behind a row's pages
+ * are copied.
+ * Only rows are rewritten.  Whoever holds pages outside them (a prefix cache)
+ * calls sv_pages_compact_ex, whose page_map (int32 [num_phys_pages], or NULL)
+ * gets every page's new number, -1 for pages that were free.
  */
 int sv_pages_compact(const sv_cache* caches, int32_t num_caches, const int32_t* page_table, const int32_t* seq_lens,
                      int32_t num_rows, int32_t max_pages, const int32_t* ref_counts, int32_t* page_table_out,
                      int32_t* ref_counts_out, int32_t* num_live, void* workspace, size_t workspace_bytes, void* stream);
+int sv_pages_compact_ex(const sv_cache* caches, int32_t num_caches, const int32_t* page_table, const int32_t* seq_lens,
+                        int32_t num_rows, int32_t max_pages, const int32_t* ref_counts, int32_t* page_table_out,
+                        int32_t* ref_counts_out, int32_t* num_live, int32_t* page_map, void* workspace,
+                        size_t workspace_bytes, void* stream);
 
 /* Reads (and with reset != 0 clears) the current device's error word; the
  * read synchronises the device.  Returns SV_OK or SV_ERR_CUDA. */

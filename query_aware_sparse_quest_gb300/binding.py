@@ -73,6 +73,7 @@ def _load():
         "sv_pages_reserve": [vp, vp, i32, i32, vp, i64, vp, vp, i32, vp, i32, vp, sz, vp],
         "sv_pages_free": [vp, vp, i32, i32, vp, i64, vp, vp, vp, i32, vp],
         "sv_pages_compact": [cp, i32, vp, vp, i32, i32, vp, vp, vp, vp, vp, sz, vp],
+        "sv_pages_compact_ex": [cp, i32, vp, vp, i32, i32, vp, vp, vp, vp, vp, vp, sz, vp],
         "sv_get_device_error": [ctypes.POINTER(ctypes.c_uint32), ctypes.c_int],
     }
     for name, args in sig.items():
@@ -475,18 +476,22 @@ def sv_pages_free(page_table: torch.Tensor, seq_lens: torch.Tensor, ref_counts: 
 
 def sv_pages_compact(caches, page_table: torch.Tensor, seq_lens: torch.Tensor, ref_counts: torch.Tensor,
                      page_table_out: torch.Tensor, ref_counts_out: torch.Tensor, num_live: torch.Tensor,
-                     workspace: torch.Tensor, stream=None) -> None:
-    """Live pages to the front of the pool; the outputs may be the inputs themselves."""
+                     workspace: torch.Tensor, stream=None, page_map: Optional[torch.Tensor] = None) -> None:
+    """Live pages to the front of the pool; the outputs may be the inputs themselves.  page_map [pages]: every page's
+    new number, for those who hold pages outside the rows; -1: free."""
     cl = _cache_list(caches)
     _shape(page_table_out, page_table.shape, "page_table_out")
     _shape(ref_counts_out, ref_counts.shape, "ref_counts_out")
     _shape(num_live, (1,), "num_live")
+    if page_map is not None:
+        _shape(page_map, (cl.num_phys_pages,), "page_map")
     dev = torch.cuda.current_device()
     _at(cl.caches[0].k_pool, None, "the cache", dev)
-    _check("sv_pages_compact", _load().sv_pages_compact(
+    _check("sv_pages_compact", _load().sv_pages_compact_ex(
         cl.c, len(cl.c), *_rows(page_table, seq_lens, ref_counts, dev, cl.num_phys_pages),
         _at(page_table_out, _I32, "page_table_out", dev), _at(ref_counts_out, _I32, "ref_counts_out", dev),
-        _at(num_live, _I32, "num_live", dev), _at(workspace, None, "workspace", dev), workspace.nbytes, _on(stream, dev)))
+        _at(num_live, _I32, "num_live", dev), _at(page_map, _I32, "page_map", dev),
+        _at(workspace, None, "workspace", dev), workspace.nbytes, _on(stream, dev)))
 
 
 def sv_get_device_error(reset: bool = True) -> int:

@@ -41,7 +41,7 @@ int launch_pages_free(int32_t* table, int32_t* lens, int num_rows, int max_pages
                       const int32_t* rows, const int32_t* first, const int32_t* end, int n, cudaStream_t stream);
 int launch_pages_compact(const sv_cache* caches, int num_caches, const int32_t* table, const int32_t* lens, int num_rows,
                          int max_pages, const int32_t* counts, int32_t* table_out, int32_t* counts_out, int32_t* live,
-                         void* ws, int sm_count, cudaStream_t stream);
+                         int32_t* page_map, void* ws, int sm_count, cudaStream_t stream);
 size_t window_workspace_bytes(int batch, int num_q_heads, int num_kv_heads, int total_q);
 size_t prefix_workspace_bytes(int batch, int num_q_heads, int num_kv_heads, int num_groups);
 int launch_window(const sv_cache* c, const void* q, int num_q_heads, const int32_t* q_start, int total_q,
@@ -525,9 +525,10 @@ int sv_pages_free(int32_t* page_table, int32_t* seq_lens, int32_t num_rows, int3
                              first_page, end_page, n, static_cast<cudaStream_t>(stream));
 }
 
-int sv_pages_compact(const sv_cache* caches, int32_t num_caches, const int32_t* page_table, const int32_t* seq_lens,
-                     int32_t num_rows, int32_t max_pages, const int32_t* ref_counts, int32_t* page_table_out,
-                     int32_t* ref_counts_out, int32_t* num_live, void* workspace, size_t workspace_bytes, void* stream) {
+int sv_pages_compact_ex(const sv_cache* caches, int32_t num_caches, const int32_t* page_table, const int32_t* seq_lens,
+                        int32_t num_rows, int32_t max_pages, const int32_t* ref_counts, int32_t* page_table_out,
+                        int32_t* ref_counts_out, int32_t* num_live, int32_t* page_map, void* workspace,
+                        size_t workspace_bytes, void* stream) {
     int st = check_caches(caches, num_caches);
     if (st) return st;
     const int64_t pool = caches[0].num_phys_pages;
@@ -537,7 +538,14 @@ int sv_pages_compact(const sv_cache* caches, int32_t num_caches, const int32_t* 
     int sms = 0;
     if ((st = sm_count_of_current_device(&sms))) return st;
     return launch_pages_compact(caches, num_caches, page_table, seq_lens, num_rows, max_pages, ref_counts, page_table_out,
-                                ref_counts_out, num_live, workspace, sms, static_cast<cudaStream_t>(stream));
+                                ref_counts_out, num_live, page_map, workspace, sms, static_cast<cudaStream_t>(stream));
+}
+
+int sv_pages_compact(const sv_cache* caches, int32_t num_caches, const int32_t* page_table, const int32_t* seq_lens,
+                     int32_t num_rows, int32_t max_pages, const int32_t* ref_counts, int32_t* page_table_out,
+                     int32_t* ref_counts_out, int32_t* num_live, void* workspace, size_t workspace_bytes, void* stream) {
+    return sv_pages_compact_ex(caches, num_caches, page_table, seq_lens, num_rows, max_pages, ref_counts, page_table_out,
+                               ref_counts_out, num_live, nullptr, workspace, workspace_bytes, stream);
 }
 
 int sv_get_device_error(uint32_t* flags, int reset) {

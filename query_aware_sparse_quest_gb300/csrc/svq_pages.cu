@@ -772,14 +772,14 @@ int launch_pages_free(int32_t* table, int32_t* lens, int num_rows, int max_pages
 
 int launch_pages_compact(const sv_cache* caches, int num_caches, const int32_t* table, const int32_t* lens, int num_rows,
                          int max_pages, const int32_t* counts, int32_t* table_out, int32_t* counts_out, int32_t* live,
-                         void* ws, int sm_count, cudaStream_t stream) {
+                         int32_t* page_map, void* ws, int sm_count, cudaStream_t stream) {
     CacheSet set;
     fill_set(&set, caches, num_caches);
     const int num_pages = static_cast<int>(caches[0].num_phys_pages);
     const Carve w(ws, num_pages, num_rows, 0);
     CompactArgs a = {{const_cast<int32_t*>(table), const_cast<int32_t*>(lens), num_rows, max_pages,
                       const_cast<int32_t*>(counts), num_pages},
-                     table_out, counts_out, live, w.p, w.q, w.r, w.word};
+                     table_out, counts_out, live, w.p, w.q, page_map ? page_map : w.r, w.word};
     const int st = launched(launch_pdl(compact_plan_kernel, dim3(kCluster), dim3(kPlanThreads), 0, stream, a));
     if (st) return st;
     return launched(launch_pdl(compact_move_kernel, dim3(sm_count * 6), dim3(kMoveThreads), 0, stream, set, a));

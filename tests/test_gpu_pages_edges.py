@@ -78,3 +78,33 @@ def test_one_free_page_among_many_is_found(page):
     others = [r for r in range(rows) if r != 100]
     d.m.fork(others, [rows + r for r in others])
     d.same(0x100)
+
+
+@pytest.mark.parametrize("inplace", [True, False])
+@pytest.mark.parametrize("pool,rows,max_pages", [(24, 4, 3), (9001, 30, 200)])
+def test_pages_held_outside_the_rows_are_found_after_a_compaction(pool, rows, max_pages, inplace):
+    """A prefix cache holds pages by their counts alone: the map says where they, and all others, went."""
+    d = Device(Model(pool, rows, max_pages))
+    g = torch.Generator().manual_seed(pool)
+    most = min(max_pages * PAGE, 2 * pool * PAGE // rows)
+    d.reserve(list(range(rows)), [int(torch.randint(0, most, (1,), generator=g)) for _ in range(rows)])
+    kept = sorted({p for r in range(0, rows, 2) for p in d.m.table[r][-(-d.m.lens[r] // PAGE) // 2:-(-d.m.lens[r] // PAGE)]})
+    for p in kept:
+        d.counts[p] += 1
+        d.m.counts[p] += 1
+    d.free(list(range(0, rows, 2)) + [1])
+    d.same()
+    held = [p for p in range(pool) if d.m.counts[p]]
+    assert set(kept) <= set(held)
+    data = list(d.m.data)
+    live = d.m.compact()
+    assert any(p >= live for p in kept)
+    got, page_map = ints([0]), torch.full((pool,), -99, dtype=torch.int32, device=DEV)
+    table, counts = (d.table, d.counts) if inplace else (torch.empty_like(d.table), torch.empty_like(d.counts))
+    binding.sv_pages_compact(d.list, d.table, d.lens, d.counts, table, counts, got, d.ws, page_map=page_map)
+    d.table, d.counts = table, counts
+    d.same()
+    to = page_map.tolist()
+    assert [p for p in range(pool) if to[p] >= 0] == held and sorted(to[p] for p in held) == list(range(live))
+    assert all(t == -1 for p, t in enumerate(to) if p not in set(held))
+    assert [d.m.data[to[p]] for p in held] == [data[p] for p in held]
