@@ -362,6 +362,7 @@ struct Control {
     uint64_t join[2];                 // both streams have published their statistics / have read O0 and O1
     uint64_t drain;
     uint32_t tmem;
+    int gave_up;                      // a role's wait ran out
     int fault[kInfoSlots];            // pages of a tile that the table does not give
     Seg seg[kSegs];
     float2 ml[2][128];                // stream statistics of a joined tile
@@ -409,12 +410,19 @@ __device__ __forceinline__ void keep_nan(uint32_t c, uint32_t& lo, uint32_t& hi)
     if (n & 0x80000000u) hi |= 0x7fff0000u;
 }
 
-// Waits for a phase of an mbarrier, at most kPolls polls of at most kPollNs each
-// (0.5 s; no wait here comes near it: copies land in microseconds); false when
-// it gave up.  Few instructions, as every role's loop has several: the roles of
+// Waits for a phase of an mbarrier, at most kPolls polls; false when it gave up.
+// A poll that finds the phase open takes 4 us on a GB300 (3.95 measured, whatever
+// time limit the instruction is given; with none named a chunk of 4096 tokens at
+// 32768 takes 1348 us instead of 1255), so that is after half a second; the waits
+// that this bounds are for copies and for other warps' work on a few tiles,
+// microseconds.  Few instructions, as every role's loop has several: the roles of
 // a CTA share the instruction caches.
-constexpr uint32_t kPolls = 1u << 19;
+constexpr uint32_t kPolls = 1u << 17;
 constexpr uint32_t kPollNs = 1000;
+// The one wait that may be long is the scheduler's, for a slot whose segment is
+// done: 1.7 us a key tile, so 14 s for the 2^30 tokens that a row may have.  It
+// ends when another role gave up, and after so many rounds of kPolls (a minute).
+constexpr int kSegRounds = 128;
 __device__ __forceinline__ bool bar_wait(uint32_t bar, uint32_t parity) {
     uint32_t ok;
     asm volatile(
@@ -429,11 +437,15 @@ __device__ __forceinline__ bool bar_wait(uint32_t bar, uint32_t parity) {
         : "memory");
     return ok != 0;
 }
+__device__ __forceinline__ void gave_up(Control* ct) {
+    svq_flag(SV_DEVERR_TIMEOUT);
+    *static_cast<volatile int*>(&ct->gave_up) = 1;
+}
 // The same by a whole warp; all of it leaves for `out` when it gave up.
 #define SVQ_WAIT(bar, parity, out)                                                        \
     do {                                                                                  \
         if (__any_sync(0xffffffffu, !bar_wait(smem_addr(&(bar)), (parity)))) {   \
-            if (lane == 0) svq_flag(SV_DEVERR_TIMEOUT);                                   \
+            if (lane == 0) gave_up(ct);                                                   \
             goto out;                                                                     \
         }                                                                                 \
     } while (0)
@@ -453,6 +465,7 @@ __global__ void __launch_bounds__(Cfg<FP8>::kThreads, 1)
     const int group = a.group;
 
     if (threadIdx.x == 0) {
+        ct->gave_up = 0;
         for (int i = 0; i < C::kStages; ++i) {
             mbar_init(smem_addr(&ct->full[i]), FP8 ? C::kWiden : 1);
             mbar_init(smem_addr(&ct->empty[i]), 1);
@@ -720,7 +733,7 @@ __global__ void __launch_bounds__(Cfg<FP8>::kThreads, 1)
                     ld += 2 * n;
                     if (ok) mbar_arrive(smem_addr(&ct->seg_empty[k % kSegs]));
                 }
-                if (!ok) svq_flag(SV_DEVERR_TIMEOUT);
+                if (!ok) gave_up(ct);
                 mma_commit(smem_addr(&ct->drain));   // nothing of this CTA's is in flight when TMEM is freed
                 (void)bar_wait(smem_addr(&ct->drain), 0);
             }
@@ -812,7 +825,13 @@ __global__ void __launch_bounds__(Cfg<FP8>::kThreads, 1)
                     off += take;
                 }
                 if (t1 > t0 || left <= 0) {
-                    SVQ_WAIT(ct->seg_empty[k % kSegs], ((k / kSegs) & 1) ^ 1, plan_end);
+                    for (int round = 0;; ++round) {
+                        if (!__any_sync(0xffffffffu, !bar_wait(smem_addr(&ct->seg_empty[k % kSegs]), ((k / kSegs) & 1) ^ 1))) break;
+                        if (__any_sync(0xffffffffu, *static_cast<volatile int*>(&ct->gave_up)) || round == kSegRounds) {
+                            if (lane == 0) gave_up(ct);
+                            goto plan_end;
+                        }
+                    }
                     if (lane == 0) {
                         Seg& s = ct->seg[k % kSegs];
                         s.en = en;

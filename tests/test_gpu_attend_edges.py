@@ -130,3 +130,27 @@ def test_rows_that_see_nothing_beside_a_nan(requests, fp8):
     assert torch.equal(out.isnan(), hit)
     o, ls, tol, tol_lse = (torch.cat(x) for x in zip(*ref))
     check(torch.where(hit, 0, out), lse, (torch.where(hit, 0, o), ls, tol, tol_lse))
+
+
+def test_a_cta_waits_as_long_as_an_item_takes():
+    """Items of 1.35 million key tiles (173 million tokens, 2.3 s), with short requests behind the first, so that its
+    CTA's scheduler waits for all of it.  The first page outweighs the others by 2^184, so it is the answer."""
+    pages, group, tile = 1_350_000 * 8, 8, 32            # 32 tokens x 8 heads are a row tile
+    case = PagedCase([PAGE, PAGE], 1)
+    first, rest = (int(case.table[b, 0]) for b in range(2))
+    case.k[first, ..., 0], case.k[rest, ..., 0] = 8, -8
+    short = 5
+    table = torch.full((short + 2, pages), rest, dtype=torch.int32, device=DEV)
+    table[:, 0] = first
+    sizes = [tile] + [1] * short + [151 * tile]           # 152 CTAs: the last request's items fill the other 151
+    lens = [(pages - 64 * 8) * PAGE] + [PAGE] * short + [pages * PAGE]
+    q = gauss(sum(sizes), group, DIM).bfloat16().to(DEV)
+    q[..., 0] = 8
+    ref = attend(q, *case.tokens(0), torch.ones((sum(sizes), PAGE), dtype=torch.bool, device=DEV), 1.0)
+    out, lse = torch.empty_like(q), torch.empty(q.shape[:2], device=DEV)
+    ws = torch.empty(binding.sv_window_attention_workspace_size(len(sizes), group, 1, sum(sizes)), dtype=torch.uint8, device=DEV)
+    binding.sv_window_attention(case.cache(), q, table, ints(lens), 0, 0, out, lse, ws, softmax_scale=1.0,
+                                q_start=ints([sum(sizes[:b]) for b in range(len(sizes) + 1)]))
+    torch.cuda.synchronize()
+    assert binding.sv_get_device_error() == 0
+    check(out, lse, ref)
