@@ -1230,13 +1230,16 @@ __global__ void __launch_bounds__(Cfg<FP8>::kThreads, 1)
                     const int pages = min(kTilePages, s.en.npages - i0);   // (products with pages behind are masked or left out)
                     unsigned char* const o = dst + (r >> 3) * 2048 + (c >> 2) * 1024 + (r & 7) * 128;
                     const int at0 = ((2 * c) & 7 ^ (r & 7)) << 4, at1 = ((2 * c + 1) & 7 ^ (r & 7)) << 4;
-                    // All of a thread's codes first, so that the next copy into their slot starts early.
+                    // All of a thread's codes first, so that the next copy into their slot starts early.  The fence
+                    // keeps that copy behind these reads: without it an arrival overtook them while other warps'
+                    // stores filled the load and store unit, and rows of the tile held the next load's codes.
                     uint4 v[4];
 #pragma unroll
                     for (int u = 0; u < 4; ++u) {
                         v[u] = *reinterpret_cast<const uint4*>(src + (odd + 2 * u) * (kPage * kHeadDim) + r * kHeadDim + c * 16);
                         if (!((on >> (odd + 2 * u)) & 1u)) v[u] = make_uint4(0u, 0u, 0u, 0u);
                     }
+                    fence_proxy_async_smem();
                     __syncwarp();
                     if (lane == 0) mbar_arrive(smem_addr(&ct->code_empty[cs]));
                     SVQ_WAIT(ct->empty[st], ((ld / C::kStages) & 1) ^ 1, widen_end);

@@ -154,3 +154,32 @@ def test_a_cta_waits_as_long_as_an_item_takes():
     torch.cuda.synchronize()
     assert binding.sv_get_device_error() == 0
     check(out, lse, ref)
+
+
+@pytest.mark.parametrize("lens,sizes,group", [
+    ([500 + 7 * i % 100 for i in range(700)], [32] * 700, 8),        # whole items and cut ones, 256 rows each
+    ([900 + 7 * i % 100 for i in range(700)], [16] * 700, 8),        # 128 rows: both streams take tiles in turn
+    ([260] * 1500, [1 + i % 40 for i in range(1500)], 7),
+])
+def test_e4m3_tiles_repeat_exactly_while_rows_are_written(lens, sizes, group):
+    """Several items a CTA: rows of one are written while the next one's codes are widened."""
+    case = PagedCase(lens, 2, fp8=True)
+    q = gauss(sum(sizes), 2 * group, DIM).bfloat16().to(DEV)
+    starts = [0]
+    for n in sizes:
+        starts.append(starts[-1] + n)
+    cache, table, ls, qs = case.cache(), case.table.to(DEV), ints(lens), ints(starts)
+    ws = torch.empty(binding.sv_window_attention_workspace_size(len(lens), 2 * group, 2, len(q)), dtype=torch.uint8, device=DEV)
+
+    def call():
+        out, lse = torch.empty_like(q), torch.empty(q.shape[:2], device=DEV)
+        binding.sv_window_attention(cache, q, table, ls, 0, 0, out, lse, ws, q_start=qs)
+        return out, lse
+    first = call()
+    for b in range(0, len(lens), 97):
+        rows = slice(starts[b], starts[b + 1])
+        check(first[0][rows], first[1][rows], attend(q[rows], *case.tokens(b), window_seen(lens[b], sizes[b], 0, 0, DEV), DIM ** -0.5))
+    for _ in range(60):
+        out, lse = call()
+        assert torch.equal(out, first[0]) and torch.equal(lse, first[1])
+    assert binding.sv_get_device_error() == 0
