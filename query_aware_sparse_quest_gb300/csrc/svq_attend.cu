@@ -75,6 +75,10 @@ constexpr int kRowTile = 256;                       // rows of an entry at most
 constexpr int kInfoSlots = 8;                       // tiles whose page faults / scales are kept (loads run at most 5 tiles ahead)
 constexpr int kMaxCtas = 160;                       // partial slots in the workspace
 constexpr float kSlack = 8.f;                       // log2 units the base may lag behind the maximum
+// A stream's key tiles after which its O and sum move into fp32 sums of their own and start again from zero.  The
+// MMAs cut their sums off at fp32's last bit, eight times a tile, always towards zero: values of one sign lose 2^-20.4
+// of their sum a tile (0.4 % over a million tokens, 5 % over 8 million, measured).  512 tiles lose 2^-11.4.
+constexpr int kFoldTiles = 512;
 constexpr int kColS = 0, kColO = 256;               // TMEM columns of S0 and O0; S1 and O1 lie 128 further
 
 // One row tile and the pages that some row of it sees: the first `sink_pages`
@@ -450,6 +454,56 @@ __device__ __forceinline__ void gave_up(Control* ct) {
         }                                                                                 \
     } while (0)
 
+// A row's O so far goes to `to` and its sum to `held`, beside their base; `more`: onto what is there.  By whole
+// warps, a row a thread; threads without one (not `valid`) write nothing.
+__device__ __noinline__ void fold_out(uint32_t o_col, float* to, bool valid, bool more, float2& held, float m, float l) {
+    tc_fence_after();
+    const float f = !more || held.x == -INFINITY ? 0.f : ex2(held.x - m);   // bases only grow
+#pragma unroll 1
+    for (int c = 0; c < 8; ++c) {
+        uint32_t y[16];
+        tc_ld16(o_col + c * 16, y);
+        tc_wait_ld();
+        float4* const at = reinterpret_cast<float4*>(to + c * 16);
+#pragma unroll
+        for (int u = 0; u < 4 && valid; ++u) {
+            float4 v = make_float4(__uint_as_float(y[4 * u]), __uint_as_float(y[4 * u + 1]), __uint_as_float(y[4 * u + 2]),
+                                   __uint_as_float(y[4 * u + 3]));
+            if (more) {
+                const float4 x = at[u];
+                v = make_float4(fmaf(x.x, f, v.x), fmaf(x.y, f, v.y), fmaf(x.z, f, v.z), fmaf(x.w, f, v.w));
+            }
+            at[u] = v;
+        }
+    }
+    held = make_float2(m, more ? fmaf(held.y, f, l) : l);
+    tc_fence_before();
+}
+// The other way, at the segment's end: O gets what was folded; returns the whole sum.
+__device__ __noinline__ float fold_in(uint32_t o_col, const float* from, bool valid, const float2& held, float m, float l) {
+    tc_fence_after();
+    const float f = held.x == -INFINITY ? 0.f : ex2(held.x - m);
+#pragma unroll 1
+    for (int c = 0; c < 8; ++c) {
+        uint32_t y[16];
+        tc_ld16(o_col + c * 16, y);
+        tc_wait_ld();
+        const float4* const at = reinterpret_cast<const float4*>(from + c * 16);
+#pragma unroll
+        for (int u = 0; u < 4 && valid; ++u) {
+            const float4 x = at[u];
+            y[4 * u] = __float_as_uint(fmaf(x.x, f, __uint_as_float(y[4 * u])));
+            y[4 * u + 1] = __float_as_uint(fmaf(x.y, f, __uint_as_float(y[4 * u + 1])));
+            y[4 * u + 2] = __float_as_uint(fmaf(x.z, f, __uint_as_float(y[4 * u + 2])));
+            y[4 * u + 3] = __float_as_uint(fmaf(x.w, f, __uint_as_float(y[4 * u + 3])));
+        }
+        tc_st16(o_col + c * 16, y);
+    }
+    tc_wait_st();
+    tc_fence_before();
+    return fmaf(held.y, f, l);
+}
+
 template <bool FP8>
 __global__ void __launch_bounds__(Cfg<FP8>::kThreads, 1)
     attend_kernel(const __grid_constant__ AttendArgs a, const __grid_constant__ CUtensorMap tmap_k,
@@ -705,12 +759,12 @@ __global__ void __launch_bounds__(Cfg<FP8>::kThreads, 1)
                             const uint32_t vs = stage(vl), ks = stage(kl);
                             ok = load_ready(vl) && (!next || load_ready(kl)) && p_ready(0);
                             if (!ok) break;
-                            pv(0, vs, pages, t > 0);
+                            pv(0, vs, pages, (t & (kFoldTiles - 1)) != 0);
                             if (next) qk(0, ks);
                             else mma_commit(smem_addr(&ct->o_full[0]));
                             ok = p_ready(1);
                             if (!ok) break;
-                            pv(1, vs, pages, t > 0);
+                            pv(1, vs, pages, (t & (kFoldTiles - 1)) != 0);
                             if (next) qk(1, ks);
                             else mma_commit(smem_addr(&ct->o_full[1]));
                             release(vl);
@@ -723,7 +777,7 @@ __global__ void __launch_bounds__(Cfg<FP8>::kThreads, 1)
                             const uint32_t vl = ld + v_load(t, n), kl = ld + k_load(t + 2);
                             ok = load_ready(vl) && (!next || load_ready(kl)) && p_ready(w);
                             if (!ok) break;
-                            pv(w, stage(vl), pages, t > 1);
+                            pv(w, stage(vl), pages, ((t >> 1) & (kFoldTiles - 1)) != 0);
                             if (next) qk(w, stage(kl));
                             else mma_commit(smem_addr(&ct->o_full[w]));
                             release(vl);
@@ -915,179 +969,192 @@ __global__ void __launch_bounds__(Cfg<FP8>::kThreads, 1)
                 const int qlo = all ? kAllVisible : s.en.pos0 + off / group;
                 const int qhi = all ? kAllVisible : s.en.pos0 + (min(rows, off + 128) - 1) / group;
                 float m = -INFINITY, l = 0.f;
-                for (int j = 0; j < nt; ++j) {
-                    const int ti = two ? j : 2 * j + w;          // tile of the segment
-                    const int i0 = (s.t0 + ti) * kTilePages;     // first page of the tile in the list
-                    const int slot = (tile0 + ti) % kInfoSlots;
-                    const int base0 = logical_page(s.en, i0) * kPage, base7 = logical_page(s.en, i0 + 7) * kPage;
-                    bool plain = i0 + kTilePages <= s.en.npages && base7 - base0 == 7 * kPage && base7 + 15 <= qlo &&
-                                 (base0 > qhi - a.window || base7 + 15 < a.sink);
-                    SVQ_WAIT(ct->s_full[w], s_ph, softmax_end);
-                    s_ph ^= 1;
-                    tc_fence_after();
-                    if (j == nt - 1 && next_q) load_q(nx);       // the stream's last use of Q is over
-                    if (warp_on) {
-                        const int fault = ct->fault[slot];
-                        plain = plain && !fault;
-                        // Visible columns, 32 a word (two pages).
-                        uint32_t bits0 = ~0u, bits1 = ~0u, bits2 = ~0u, bits3 = ~0u;
-                        if (!plain) {
-                            auto two_pages = [&](int c) {
-                                uint32_t bits = 0;
-#pragma unroll
-                                for (int u = 0; u < 2; ++u) {
-                                    const int i = i0 + 2 * c + u;
-                                    if (i < s.en.npages && !((fault >> (2 * c + u)) & 1))
-                                        bits |= page_mask(logical_page(s.en, i) * kPage, qpos, a.window, a.sink) << (16 * u);
-                                }
-                                return bits;
-                            };
-                            bits0 = two_pages(0);
-                            bits1 = two_pages(1);
-                            bits2 = two_pages(2);
-                            bits3 = two_pages(3);
-                        }
-                        // Pairs of tokens: key scales times scale_log2, value scales.
-                        const ulonglong2* ks = reinterpret_cast<const ulonglong2*>(scales + slot * 2 * kTileTok);
-                        const ulonglong2* vs = ks + kTileTok / 4;
-                        // The row's logits.  bf16: all 128 stay in registers from here to P (a causal chunk
-                        // 1268 us; with the exponentials in a rolled loop 1363).  e4m3 (fewer registers a
-                        // thread, and the widening warps' code beside it in the instruction cache): rolled
-                        // loops over 32 columns that read S from TMEM twice (ragged chunks 89.0 us; logits in
-                        // registers, with half the widening warps, 90.7).  Scales act on pairs of tokens,
-                        // the keys' with scale_log2 in them.
-                        float x[FP8 ? 1 : 128];
-                        float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-                        if constexpr (FP8) {
-#pragma unroll 1
-                            for (int c = 0; c < 4; ++c) {
-                                float x[32];
-                                tc_ld32(s_col + c * 32, reinterpret_cast<uint32_t(&)[32]>(x));
-                                tc_wait_ld();
-#pragma unroll
-                                for (int u = 0; u < 8; ++u) {
-                                    const ulonglong2 k4 = ks[c * 8 + u];
-                                    unpack2(mul2(pack2(x[4 * u], x[4 * u + 1]), k4.x), x[4 * u], x[4 * u + 1]);
-                                    unpack2(mul2(pack2(x[4 * u + 2], x[4 * u + 3]), k4.y), x[4 * u + 2], x[4 * u + 3]);
-                                }
-                                const uint32_t bits = c == 0 ? bits0 : (c == 1 ? bits1 : (c == 2 ? bits2 : bits3));
-                                if (__any_sync(0xffffffffu, bits != ~0u)) {
-#pragma unroll
-                                    for (int u = 0; u < 32; ++u)
-                                        if (!((bits >> u) & 1u)) x[u] = -INFINITY;
-                                }
-#pragma unroll
-                                for (int u = 0; u < 32; u += 8)
-#pragma unroll
-                                    for (int k = 0; k < 4; ++k) mx[k] = fmaxf(fmaxf(mx[k], x[u + 2 * k]), x[u + 2 * k + 1]);
-                            }
-                        } else {
-#pragma unroll
-                            for (int c = 0; c < 4; ++c) tc_ld32(s_col + c * 32, reinterpret_cast<uint32_t(&)[32]>(x[c * 32]));
-                            tc_wait_ld();
+                // The row's place for what is folded: that of the segment's partial; a whole item's CTA has not
+                // written its second one yet.  (Base, sum) are kept in ct->ml.
+                auto folded = [&] {
+                    const int slot = s.slot >= 0 ? s.slot : 2 * static_cast<int>(blockIdx.x) + 1;
+                    return a.cut_o + (static_cast<int64_t>(slot) * a.slot_rows + (two ? r : w * (a.slot_rows / 2) + row)) * kHeadDim;
+                };
+                for (int j0 = 0; j0 < nt; j0 += kFoldTiles) {
+                    if (j0 > 0) {
+                        SVQ_WAIT(ct->s_full[w], s_ph, softmax_end);   // O is complete, and the next product into it starts anew
+                        if (warp_on) fold_out(o_col, folded(), valid, j0 > kFoldTiles, ct->ml[w][row], m, l);
+                        l = 0.f;
+                    }
+                    for (int j = j0; j < min(nt, j0 + kFoldTiles); ++j) {
+                        const int ti = two ? j : 2 * j + w;          // tile of the segment
+                        const int i0 = (s.t0 + ti) * kTilePages;     // first page of the tile in the list
+                        const int slot = (tile0 + ti) % kInfoSlots;
+                        const int base0 = logical_page(s.en, i0) * kPage, base7 = logical_page(s.en, i0 + 7) * kPage;
+                        bool plain = i0 + kTilePages <= s.en.npages && base7 - base0 == 7 * kPage && base7 + 15 <= qlo &&
+                                     (base0 > qhi - a.window || base7 + 15 < a.sink);
+                        SVQ_WAIT(ct->s_full[w], s_ph, softmax_end);
+                        s_ph ^= 1;
+                        tc_fence_after();
+                        if (j == nt - 1 && next_q) load_q(nx);       // the stream's last use of Q is over
+                        if (warp_on) {
+                            const int fault = ct->fault[slot];
+                            plain = plain && !fault;
+                            // Visible columns, 32 a word (two pages).
+                            uint32_t bits0 = ~0u, bits1 = ~0u, bits2 = ~0u, bits3 = ~0u;
                             if (!plain) {
+                                auto two_pages = [&](int c) {
+                                    uint32_t bits = 0;
 #pragma unroll
-                                for (int c = 0; c < 4; ++c) {
-                                    const uint32_t bits = c == 0 ? bits0 : (c == 1 ? bits1 : (c == 2 ? bits2 : bits3));
-#pragma unroll
-                                    for (int u = 0; u < 32; ++u)
-                                        if (!((bits >> u) & 1u)) x[c * 32 + u] = -INFINITY;
-                                }
+                                    for (int u = 0; u < 2; ++u) {
+                                        const int i = i0 + 2 * c + u;
+                                        if (i < s.en.npages && !((fault >> (2 * c + u)) & 1))
+                                            bits |= page_mask(logical_page(s.en, i) * kPage, qpos, a.window, a.sink) << (16 * u);
+                                    }
+                                    return bits;
+                                };
+                                bits0 = two_pages(0);
+                                bits1 = two_pages(1);
+                                bits2 = two_pages(2);
+                                bits3 = two_pages(3);
                             }
-#pragma unroll
-                            for (int c = 0; c < 4; ++c) {
-                                mx[c] = fmaxf(x[c], x[c + 4]);
-#pragma unroll
-                                for (int u = 8; u < 128; u += 8) mx[c] = fmaxf(fmaxf(mx[c], x[u + c]), x[u + c + 4]);
-                            }
-                        }
-                        const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * (FP8 ? 1.f : a.scale_log2);
-                        // The base moves only when the maximum is more than kSlack above it; weights
-                        // stay at most 2^kSlack, and sums and outputs share the base.
-                        // Threads without a row hold whatever Q's memory held and have no say.
-                        if (__any_sync(0xffffffffu, valid && top > m + kSlack)) {
-                            const float mn = fmaxf(m, top);
-                            const float alpha = mn == -INFINITY ? 1.f : ex2(m - mn);
-                            m = mn;
-                            l *= alpha;
-                            if (j > 0) {   // S of this tile is complete, so the MMAs into O before it are
+                            // Pairs of tokens: key scales times scale_log2, value scales.
+                            const ulonglong2* ks = reinterpret_cast<const ulonglong2*>(scales + slot * 2 * kTileTok);
+                            const ulonglong2* vs = ks + kTileTok / 4;
+                            // The row's logits.  bf16: all 128 stay in registers from here to P (a causal chunk
+                            // 1268 us; with the exponentials in a rolled loop 1363).  e4m3 (fewer registers a
+                            // thread, and the widening warps' code beside it in the instruction cache): rolled
+                            // loops over 32 columns that read S from TMEM twice (ragged chunks 89.0 us; logits in
+                            // registers, with half the widening warps, 90.7).  Scales act on pairs of tokens,
+                            // the keys' with scale_log2 in them.
+                            float x[FP8 ? 1 : 128];
+                            float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+                            if constexpr (FP8) {
 #pragma unroll 1
-                                for (int c = 0; c < 8; ++c) {
-                                    uint32_t y[16];
-                                    tc_ld16(o_col + c * 16, y);
+                                for (int c = 0; c < 4; ++c) {
+                                    float x[32];
+                                    tc_ld32(s_col + c * 32, reinterpret_cast<uint32_t(&)[32]>(x));
                                     tc_wait_ld();
 #pragma unroll
-                                    for (int u = 0; u < 16; ++u) y[u] = __float_as_uint(__uint_as_float(y[u]) * alpha);
-                                    tc_st16(o_col + c * 16, y);
+                                    for (int u = 0; u < 8; ++u) {
+                                        const ulonglong2 k4 = ks[c * 8 + u];
+                                        unpack2(mul2(pack2(x[4 * u], x[4 * u + 1]), k4.x), x[4 * u], x[4 * u + 1]);
+                                        unpack2(mul2(pack2(x[4 * u + 2], x[4 * u + 3]), k4.y), x[4 * u + 2], x[4 * u + 3]);
+                                    }
+                                    const uint32_t bits = c == 0 ? bits0 : (c == 1 ? bits1 : (c == 2 ? bits2 : bits3));
+                                    if (__any_sync(0xffffffffu, bits != ~0u)) {
+#pragma unroll
+                                        for (int u = 0; u < 32; ++u)
+                                            if (!((bits >> u) & 1u)) x[u] = -INFINITY;
+                                    }
+#pragma unroll
+                                    for (int u = 0; u < 32; u += 8)
+#pragma unroll
+                                        for (int k = 0; k < 4; ++k) mx[k] = fmaxf(fmaxf(mx[k], x[u + 2 * k]), x[u + 2 * k + 1]);
                                 }
-                            }
-                        }
-                        const float base = m == -INFINITY ? 0.f : m;
-                        // Weights and their sum, two at a time, and P in bf16 over S (read already).
-                        const uint64_t scale2 = pack2(a.scale_log2, a.scale_log2), base2 = pack2(-base, -base);
-                        uint64_t sum[4] = {0ull, 0ull, 0ull, 0ull};
-                        if constexpr (FP8) {
-#pragma unroll 1
-                            for (int c = 0; c < 4; ++c) {
-                                float x[32];
-                                uint32_t p[16];
-                                tc_ld32(s_col + c * 32, reinterpret_cast<uint32_t(&)[32]>(x));
+                            } else {
+#pragma unroll
+                                for (int c = 0; c < 4; ++c) tc_ld32(s_col + c * 32, reinterpret_cast<uint32_t(&)[32]>(x[c * 32]));
                                 tc_wait_ld();
+                                if (!plain) {
 #pragma unroll
-                                for (int u = 0; u < 8; ++u) {
-                                    const ulonglong2 k4 = ks[c * 8 + u];
-                                    unpack2(fma2(pack2(x[4 * u], x[4 * u + 1]), k4.x, base2), x[4 * u], x[4 * u + 1]);
-                                    unpack2(fma2(pack2(x[4 * u + 2], x[4 * u + 3]), k4.y, base2), x[4 * u + 2], x[4 * u + 3]);
-                                }
-                                const uint32_t bits = c == 0 ? bits0 : (c == 1 ? bits1 : (c == 2 ? bits2 : bits3));
-                                if (__any_sync(0xffffffffu, bits != ~0u)) {
+                                    for (int c = 0; c < 4; ++c) {
+                                        const uint32_t bits = c == 0 ? bits0 : (c == 1 ? bits1 : (c == 2 ? bits2 : bits3));
 #pragma unroll
-                                    for (int u = 0; u < 32; ++u)
-                                        if (!((bits >> u) & 1u)) x[u] = -INFINITY;
+                                        for (int u = 0; u < 32; ++u)
+                                            if (!((bits >> u) & 1u)) x[c * 32 + u] = -INFINITY;
+                                    }
                                 }
 #pragma unroll
-                                for (int u = 0; u < 8; ++u) {
-                                    const ulonglong2 v4 = vs[c * 8 + u];
-                                    const uint64_t e0 = pack2(ex2(x[4 * u]), ex2(x[4 * u + 1]));
-                                    const uint64_t e1 = pack2(ex2(x[4 * u + 2]), ex2(x[4 * u + 3]));
-                                    sum[0] = add2(sum[0], e0);
-                                    sum[1] = add2(sum[1], e1);
-                                    float w0, w1;
-                                    unpack2(mul2(e0, v4.x), w0, w1);
-                                    p[2 * u] = pack_bf16x2(w0, w1);
-                                    unpack2(mul2(e1, v4.y), w0, w1);
-                                    p[2 * u + 1] = pack_bf16x2(w0, w1);
+                                for (int c = 0; c < 4; ++c) {
+                                    mx[c] = fmaxf(x[c], x[c + 4]);
+#pragma unroll
+                                    for (int u = 8; u < 128; u += 8) mx[c] = fmaxf(fmaxf(mx[c], x[u + c]), x[u + c + 4]);
                                 }
-                                tc_st16(s_col + c * 16, p);
                             }
-                        } else {
+                            const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * (FP8 ? 1.f : a.scale_log2);
+                            // The base moves only when the maximum is more than kSlack above it; weights
+                            // stay at most 2^kSlack, and sums and outputs share the base.
+                            // Threads without a row hold whatever Q's memory held and have no say.
+                            if (__any_sync(0xffffffffu, valid && top > m + kSlack)) {
+                                const float mn = fmaxf(m, top);
+                                const float alpha = mn == -INFINITY ? 1.f : ex2(m - mn);
+                                m = mn;
+                                l *= alpha;
+                                if (j > 0) {   // S of this tile is complete, so the MMAs into O before it are
+#pragma unroll 1
+                                    for (int c = 0; c < 8; ++c) {
+                                        uint32_t y[16];
+                                        tc_ld16(o_col + c * 16, y);
+                                        tc_wait_ld();
 #pragma unroll
-                            for (int c = 0; c < 4; ++c) {
-                                uint32_t p[16];
-#pragma unroll
-                                for (int u = 0; u < 16; ++u) {
-                                    float e0, e1;
-                                    unpack2(fma2(pack2(x[c * 32 + 2 * u], x[c * 32 + 2 * u + 1]), scale2, base2), e0, e1);
-                                    e0 = ex2(e0);
-                                    e1 = ex2(e1);
-                                    sum[u & 3] = add2(sum[u & 3], pack2(e0, e1));
-                                    p[u] = pack_bf16x2(e0, e1);
+                                        for (int u = 0; u < 16; ++u) y[u] = __float_as_uint(__uint_as_float(y[u]) * alpha);
+                                        tc_st16(o_col + c * 16, y);
+                                    }
                                 }
-                                tc_st16(s_col + c * 16, p);
                             }
-                            sum[0] = add2(sum[0], sum[2]);
-                            sum[1] = add2(sum[1], sum[3]);
+                            const float base = m == -INFINITY ? 0.f : m;
+                            // Weights and their sum, two at a time, and P in bf16 over S (read already).
+                            const uint64_t scale2 = pack2(a.scale_log2, a.scale_log2), base2 = pack2(-base, -base);
+                            uint64_t sum[4] = {0ull, 0ull, 0ull, 0ull};
+                            if constexpr (FP8) {
+#pragma unroll 1
+                                for (int c = 0; c < 4; ++c) {
+                                    float x[32];
+                                    uint32_t p[16];
+                                    tc_ld32(s_col + c * 32, reinterpret_cast<uint32_t(&)[32]>(x));
+                                    tc_wait_ld();
+#pragma unroll
+                                    for (int u = 0; u < 8; ++u) {
+                                        const ulonglong2 k4 = ks[c * 8 + u];
+                                        unpack2(fma2(pack2(x[4 * u], x[4 * u + 1]), k4.x, base2), x[4 * u], x[4 * u + 1]);
+                                        unpack2(fma2(pack2(x[4 * u + 2], x[4 * u + 3]), k4.y, base2), x[4 * u + 2], x[4 * u + 3]);
+                                    }
+                                    const uint32_t bits = c == 0 ? bits0 : (c == 1 ? bits1 : (c == 2 ? bits2 : bits3));
+                                    if (__any_sync(0xffffffffu, bits != ~0u)) {
+#pragma unroll
+                                        for (int u = 0; u < 32; ++u)
+                                            if (!((bits >> u) & 1u)) x[u] = -INFINITY;
+                                    }
+#pragma unroll
+                                    for (int u = 0; u < 8; ++u) {
+                                        const ulonglong2 v4 = vs[c * 8 + u];
+                                        const uint64_t e0 = pack2(ex2(x[4 * u]), ex2(x[4 * u + 1]));
+                                        const uint64_t e1 = pack2(ex2(x[4 * u + 2]), ex2(x[4 * u + 3]));
+                                        sum[0] = add2(sum[0], e0);
+                                        sum[1] = add2(sum[1], e1);
+                                        float w0, w1;
+                                        unpack2(mul2(e0, v4.x), w0, w1);
+                                        p[2 * u] = pack_bf16x2(w0, w1);
+                                        unpack2(mul2(e1, v4.y), w0, w1);
+                                        p[2 * u + 1] = pack_bf16x2(w0, w1);
+                                    }
+                                    tc_st16(s_col + c * 16, p);
+                                }
+                            } else {
+#pragma unroll
+                                for (int c = 0; c < 4; ++c) {
+                                    uint32_t p[16];
+#pragma unroll
+                                    for (int u = 0; u < 16; ++u) {
+                                        float e0, e1;
+                                        unpack2(fma2(pack2(x[c * 32 + 2 * u], x[c * 32 + 2 * u + 1]), scale2, base2), e0, e1);
+                                        e0 = ex2(e0);
+                                        e1 = ex2(e1);
+                                        sum[u & 3] = add2(sum[u & 3], pack2(e0, e1));
+                                        p[u] = pack_bf16x2(e0, e1);
+                                    }
+                                    tc_st16(s_col + c * 16, p);
+                                }
+                                sum[0] = add2(sum[0], sum[2]);
+                                sum[1] = add2(sum[1], sum[3]);
+                            }
+                            {
+                                float s0, s1;
+                                unpack2(add2(sum[0], sum[1]), s0, s1);
+                                l += s0 + s1;
+                            }
+                            tc_wait_st();
                         }
-                        {
-                            float s0, s1;
-                            unpack2(add2(sum[0], sum[1]), s0, s1);
-                            l += s0 + s1;
-                        }
-                        tc_wait_st();
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(smem_addr(&ct->p_full[w]));
                     }
-                    tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(smem_addr(&ct->p_full[w]));
                 }
                 if (nt == 0 && next_q) load_q(nx);
                 if (next_q) q_ready();
@@ -1111,6 +1178,7 @@ __global__ void __launch_bounds__(Cfg<FP8>::kThreads, 1)
                     SVQ_WAIT(ct->o_full[w], w ? o_ph1 : o_ph0, softmax_end);
                     o_ph0 ^= 1;
                     o_ph1 ^= 1;
+                    if (nt > kFoldTiles && warp_on) L = l = fold_in(o_col, folded(), valid, ct->ml[w][row], m, l);
                 } else {
                     SVQ_WAIT(ct->o_full[0], o_ph0, softmax_end);
                     o_ph0 ^= 1;
@@ -1118,6 +1186,7 @@ __global__ void __launch_bounds__(Cfg<FP8>::kThreads, 1)
                         SVQ_WAIT(ct->o_full[1], o_ph1, softmax_end);
                         o_ph1 ^= 1;
                     }
+                    if (nt > kFoldTiles && warp_on) l = fold_in(o_col, folded(), valid, ct->ml[w][row], m, l);
                     ct->ml[w][row] = make_float2(m, l);
                     mbar_arrive(smem_addr(&ct->join[0]));
                     SVQ_WAIT(ct->join[0], join_ph, softmax_end);
@@ -1643,14 +1712,15 @@ size_t up(size_t n) { return (n + 255) / 256 * 256; }
 
 struct Layout {
     size_t entries, cum, num, req_offset, odd, num_odd, group_rec, cut_item, cut_o, cut_ml, whole_o, whole_ml, split_o, split_ml, total;
-    int max_entries, slot_rows;
+    int max_entries, item_rows, slot_rows;
     // rows: query tokens; num_groups: 0 for chunks
     Layout(int64_t batch, int64_t rows, int num_q_heads, int num_kv_heads, int num_groups) {
         const bool prefix = num_groups > 0;
         const int group = num_q_heads / num_kv_heads;
         const int64_t e = prefix ? 0 : rows / (kRowTile / group) + batch;
         max_entries = static_cast<int>(e);
-        slot_rows = static_cast<int>(rows * group < kRowTile ? rows * group : kRowTile);
+        item_rows = static_cast<int>(rows * group < kRowTile ? rows * group : kRowTile);
+        slot_rows = 2 * item_rows < kRowTile ? 2 * item_rows : kRowTile;   // (both streams of up to 128 rows fold theirs)
         size_t at = 0;
         auto take = [&](size_t bytes) { const size_t r = at; at += up(bytes); return r; };
         entries = take(e * sizeof(Entry));
@@ -1784,7 +1854,7 @@ int launch_window(const sv_cache* c, const void* q, int num_q_heads, const int32
     if (launch_pdl(plan_kernel, dim3(1), dim3(kPlanThreads), 0, stream, p) != cudaSuccess) return SV_ERR_CUDA;
     const int st = launch_tiles(c, a, ctas, stream);
     if (st || ctas < 2) return st;
-    const int y = lay.slot_rows < 32 ? lay.slot_rows : (lay.slot_rows < 128 ? 32 : 8);
+    const int y = lay.item_rows < 32 ? lay.item_rows : (lay.item_rows < 128 ? 32 : 8);
     return launch_pdl(join_cut_kernel, dim3(ctas - 1, y), dim3(kCutThreads), 0, stream, a) == cudaSuccess ? SV_OK
                                                                                                           : SV_ERR_CUDA;
 }

@@ -183,3 +183,114 @@ def test_e4m3_tiles_repeat_exactly_while_rows_are_written(lens, sizes, group):
         out, lse = call()
         assert torch.equal(out, first[0]) and torch.equal(lse, first[1])
     assert binding.sv_get_device_error() == 0
+def repeated(levels, step, seed=8):
+    """64 pages a level, whose logits rise by `step` nats a level (channel 0, where q is 1, at a scale of 0.1)."""
+    n = 64 * levels
+    k = gauss(n, 1, PAGE, DIM, seed=seed)
+    k[..., 0] = 10 * step * torch.arange(n).div(64, rounding_mode="floor")[:, None, None]
+    v = gauss(n, 1, PAGE, DIM, seed=seed + 1) + 2
+    return k, v
+
+
+def held(k, v, fp8):
+    """The cache of K and V (fp32), and what it holds, in 64 bits."""
+    meta = torch.zeros((k.shape[0], 1, 2, DIM), dtype=torch.bfloat16, device=DEV)
+    if not fp8:
+        k, v = k.bfloat16().to(DEV), v.bfloat16().to(DEV)
+        return binding.Cache(k, v, meta), k.double().view(-1, DIM), v.double().view(-1, DIM)
+    (kc, ks), (vc, vs) = PagedCase._code(k), PagedCase._code(v)
+    kc, ks, vc, vs = (x.to(DEV).contiguous() for x in (kc, ks, vc, vs))
+    wide = [(x.view(torch.float8_e4m3fn).double() * s.double()[..., None]).view(-1, DIM) for x, s in ((kc, ks), (vc, vs))]
+    return binding.Cache(kc, vc, meta, ks, vs), *wide
+
+
+def weighted(q, k, v, w, scale):
+    """attend() of tokens that a row sees w [n, L] times.  The sums: 512 tiles of 128 tokens at a time, cut off at
+    fp32's last bit by the MMAs 8 times a tile (2^-23 of the sum each), then those sums, rounded; l: rounded."""
+    z = torch.einsum("nhd,ld->nhl", q.double(), k) * scale
+    mag = (torch.einsum("nhd,ld->nhl", q.double().abs(), k.abs()) * scale).amax(-1)
+    z = z + w.double().log()[:, None]
+    ls = torch.logsumexp(z, -1)
+    p = torch.exp(z - ls[..., None])
+    o, a = p @ v, p @ v.abs()
+    ez = 130 * 2.0 ** -24 * mag
+    folds = w.sum(1).max().item() / 65536
+    tol = (2.0 ** -8 + 2 * ez[..., None] + 2.0 ** -11 + folds * 2.0 ** -24 + 2.0 ** -20) * a + 2.0 ** -8 * (o.abs() + 2.0 ** -8 * a)
+    return o, ls, tol, ez + 2.0 ** -21 + 2.0 ** -20 + (512 + folds) * 2.0 ** -24 + 2.0 ** -23 * ls.abs()
+
+
+LONG = 1 << 20
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("form", ["halves", "joined", "cut", "prefix"])
+def test_long_sums_of_one_sign_lose_nothing(form, fp8):
+    """A million values 1 a row: the average is 1.  Row tiles of 256 rows and of 128, whole and cut; prefixes."""
+    pages, group = LONG // PAGE, 8
+    k = gauss(64, 1, PAGE, DIM)
+    cache, k64, _ = held(k, torch.ones_like(k), fp8)
+    batch, size = {"halves": (1, 152 * 32), "joined": (152, 16), "cut": (1, 100 * 32), "prefix": (320, 1)}[form]
+    table = (torch.arange(pages + 1, dtype=torch.int32, device=DEV) % 64).repeat(batch, 1)
+    q = gauss(batch * size, group, DIM, seed=4).bfloat16().to(DEV)
+    out, lse = torch.empty_like(q), torch.empty(q.shape[:2], device=DEV)
+    length = LONG + (5 if form == "prefix" else 0)
+    lens = ints([length] * batch)
+    if form == "prefix":
+        ws = torch.empty(binding.sv_prefix_decode_workspace_size(batch, group, 1, 10), dtype=torch.uint8, device=DEV)
+        binding.sv_prefix_decode(cache, q, table, lens, ints([32 * g for g in range(11)]), ints([pages] * 10), out, lse, ws)
+    else:
+        ws = torch.empty(binding.sv_window_attention_workspace_size(batch, group, 1, batch * size), dtype=torch.uint8, device=DEV)
+        binding.sv_window_attention(cache, q, table, lens, 0, 0, out, lse, ws, q_start=ints([b * size for b in range(batch + 1)]))
+    assert binding.sv_get_device_error() == 0
+    assert (out == 1).all(), (out.double() - 1).abs().max().item()
+    rows = torch.tensor([0, size // 2, batch * size - 1], device=DEV)
+    pos = length - size + rows % size
+    w = (pos[:, None] + 1) // 1024 + (torch.arange(1024, device=DEV) < (pos[:, None] + 1) % 1024)
+    _, ls, _, tol = weighted(q[rows], k64, torch.ones_like(k64), w, DIM ** -0.5)
+    assert ((lse[rows] - ls).abs() <= tol).all()
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("form", ["halves", "joined"])
+@pytest.mark.parametrize("step", [3.0, -0.5])
+def test_long_contexts_whose_logits_rise_and_fall(step, form, fp8):
+    """16 levels of 65536 tokens each: the base moves between the sums that a row is folded into."""
+    levels, group = 16, 8
+    k, v = repeated(levels, step)
+    cache, k64, v64 = held(k, v, fp8)
+    pages = LONG // PAGE
+    at = torch.arange(pages, device=DEV)
+    batch, size = (1, 152 * 32) if form == "halves" else (152, 16)
+    table = (at // 4096 * 64 + at % 64).int().repeat(batch, 1)
+    q = gauss(batch * size, group, DIM, seed=5).bfloat16().to(DEV)
+    q[..., 0] = 1
+    out, lse = torch.empty_like(q), torch.empty(q.shape[:2], device=DEV)
+    ws = torch.empty(binding.sv_window_attention_workspace_size(batch, group, 1, batch * size), dtype=torch.uint8, device=DEV)
+    binding.sv_window_attention(cache, q, table, ints([LONG] * batch), 0, 0, out, lse, ws, softmax_scale=0.1,
+                                q_start=ints([b * size for b in range(batch + 1)]))
+    assert binding.sv_get_device_error() == 0
+    rows = torch.arange(0, batch * size, 37, device=DEV)
+    seen = LONG - size + rows % size + 1
+    level = torch.arange(levels, device=DEV).repeat_interleave(1024)
+    token = torch.arange(1024, device=DEV).repeat(levels)
+    inside = (seen[:, None] - 65536 * level).clamp(0, 65536)
+    check(out[rows], lse[rows], weighted(q[rows], k64, v64, inside // 1024 + (token < inside % 1024), 0.1))
+
+
+def test_a_nan_behind_a_long_context():
+    """Only the last token's rows see it; the others of its tile, which have folded sums, do not."""
+    length, size, group = 1 << 17, 152 * 32, 8
+    k = gauss(65, 1, PAGE, DIM)
+    v = torch.ones_like(k)
+    v[64, 0, 15, 5] = float("nan")
+    cache, _, _ = held(k, v, False)
+    table = (torch.arange(length // PAGE, dtype=torch.int32, device=DEV) % 64)[None].contiguous()
+    table[0, -1] = 64
+    q = gauss(size, group, DIM, seed=4).bfloat16().to(DEV)
+    out, lse = torch.empty_like(q), torch.empty(q.shape[:2], device=DEV)
+    ws = torch.empty(binding.sv_window_attention_workspace_size(1, group, 1, size), dtype=torch.uint8, device=DEV)
+    binding.sv_window_attention(cache, q, table, ints([length]), 0, 0, out, lse, ws, q_start=ints([0, size]))
+    assert binding.sv_get_device_error() == 0
+    assert out[-1, :, 5].isnan().all() and lse.isfinite().all()
+    out[-1, :, 5] = 1
+    assert (out == 1).all()
