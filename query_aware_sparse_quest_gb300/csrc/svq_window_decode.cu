@@ -499,22 +499,33 @@ __global__ void __launch_bounds__(kThreads, Cfg<FP8>::kPerSm)
             rb0 = operand(pack_bf16x2(rest(p0), rest(p1)));
             rb1 = operand(pack_bf16x2(rest(p2), rest(p3)));
         }
-        // O^T (128 channels x 8) += V^T P^T
+        // O^T (128 channels x 8) += V^T P^T.  A page's product starts from zero and is added in fp32: an MMA cuts its
+        // sum off towards zero, which over a long row would take as much as the output's rounding from values of one
+        // sign (a million tokens in one split: 0.2 %).
+        auto add = [](float (&to)[4], const float (&d)[4]) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) to[i] += d[i];
+        };
         if (FP8) {
 #pragma unroll
             for (int cb = 0; cb < 4; ++cb) {
                 uint32_t r0, r1, r2, r3;
                 ldmatrix_bytes_trans(vs_s + f8_at(lane & 15, 2 * cb + (lane >> 4)), r0, r1, r2, r3);
-                mma_f16_16816(o[2 * cb], f16x2_of(r0), f16x2_of(r1), f16x2_of(r0 >> 16), f16x2_of(r1 >> 16), pb0, pb1);
-                mma_f16_16816(o[2 * cb + 1], f16x2_of(r2), f16x2_of(r3), f16x2_of(r2 >> 16), f16x2_of(r3 >> 16), pb0, pb1);
+                float d0[4] = {0.f, 0.f, 0.f, 0.f}, d1[4] = {0.f, 0.f, 0.f, 0.f};
+                mma_f16_16816(d0, f16x2_of(r0), f16x2_of(r1), f16x2_of(r0 >> 16), f16x2_of(r1 >> 16), pb0, pb1);
+                mma_f16_16816(d1, f16x2_of(r2), f16x2_of(r3), f16x2_of(r2 >> 16), f16x2_of(r3 >> 16), pb0, pb1);
+                add(o[2 * cb], d0);
+                add(o[2 * cb + 1], d1);
             }
         } else {
 #pragma unroll
             for (int mt = 0; mt < 8; ++mt) {
                 uint32_t r0, r1, r2, r3;
                 ldmatrix_x4_trans(vs_s + bf16_at(vrow, 2 * mt + (mat & 1)), r0, r1, r2, r3);
-                mma_bf16_16816(o[mt], r0, r1, r2, r3, pb0, pb1);
-                mma_bf16_16816(o[mt], r0, r1, r2, r3, rb0, rb1);
+                float d[4] = {0.f, 0.f, 0.f, 0.f};
+                mma_bf16_16816(d, r0, r1, r2, r3, pb0, pb1);
+                mma_bf16_16816(d, r0, r1, r2, r3, rb0, rb1);
+                add(o[mt], d);
             }
         }
         __syncwarp();   // every lane has read the stage before it is released

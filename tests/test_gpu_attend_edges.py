@@ -294,3 +294,22 @@ def test_a_nan_behind_a_long_context():
     assert out[-1, :, 5].isnan().all() and lse.isfinite().all()
     out[-1, :, 5] = 1
     assert (out == 1).all()
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("length", [LONG, 4 * LONG])
+def test_long_sums_of_one_sign_in_single_tokens(length, fp8):
+    """Enough requests that one split reads all of a row: the average of 4 million values 1 is 1."""
+    batch, group = 152 * 4, 8
+    k = gauss(64, 1, PAGE, DIM)
+    cache, k64, _ = held(k, torch.ones_like(k), fp8)
+    table = (torch.arange(length // PAGE, dtype=torch.int32, device=DEV) % 64).repeat(batch, 1)
+    q = gauss(batch, group, DIM, seed=4).bfloat16().to(DEV)
+    out, lse = torch.empty_like(q), torch.empty((batch, group), device=DEV)
+    ws = torch.empty(binding.sv_window_attention_workspace_size(batch, group, 1, batch), dtype=torch.uint8, device=DEV)
+    binding.sv_window_attention(cache, q, table, ints([length] * batch), 0, 0, out, lse, ws)
+    assert binding.sv_get_device_error() == 0
+    assert (out == 1).all(), (out.double() - 1).abs().max().item()
+    _, ls, _, _ = weighted(q, k64, torch.ones_like(k64), torch.full((batch, 1024), length // 1024, device=DEV), DIM ** -0.5)
+    # a lane's sum of length / 64 pages' weights, each addition rounded
+    assert ((lse - ls).abs() <= 1e-5 + length / 64 * 2.0 ** -24).all()
