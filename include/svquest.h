@@ -30,14 +30,15 @@
  *  - `stream` is a cudaStream_t passed as void* (NULL = legacy default
  *    stream).  Calls enqueue kernels and return; they never synchronise.
  *  - Kernels are launched with programmatic dependent launch.  The scoring,
- *    top-K and attention kernels read the call's q, page_table, seq_lens,
- *    group_start and shared_pages, and the append kernel its slot_mapping,
- *    k_new and v_new, as soon as they start, possibly while the kernel enqueued just before them is
- *    still running.  Pools, metadata and workspace are touched only
+ *    top-K and sv_sparse_decode kernels read the call's q, page_table and
+ *    seq_lens, and the append kernel its slot_mapping, k_new and v_new, as
+ *    soon as they start, possibly while the kernel enqueued just before them
+ *    is still running.  Pools, metadata and workspace, and every input of
+ *    sv_window_attention, sv_prefix_decode and sv_pages_*, are touched only
  *    after that kernel has completed.  So the kernel that produces a
  *    call's inputs must not release its dependents early
- *    (griddepcontrol.launch_dependents): an ordinary kernel, a copy, or any
- *    work enqueued earlier is fine.
+ *    (griddepcontrol.launch_dependents): an ordinary kernel, a copy, a call
+ *    of this library, or any work enqueued earlier is fine.
  *  - The page metadata and the K/V tiles a call streams are read through an
  *    L2 evict-first policy, so that they displace little else: what a call
  *    reuses (page tables, scores, selections, split partials) and the

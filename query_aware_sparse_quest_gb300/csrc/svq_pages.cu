@@ -21,8 +21,9 @@
 //
 // Kernels are launched to overlap the end of the one before (a beam step of
 // three calls 33 -> 24 us), but each waits for it before its first access and
-// lets none after it start early: tables and lengths are inputs that later
-// kernels read as soon as they start.
+// lets none after it start early: tables, lengths and slots are inputs that
+// later kernels (append, page selection) read as soon as they start, without a
+// wait of their own.  So every thread ends with a fence behind what it wrote.
 #include <climits>
 
 #include "svq_common.cuh"
@@ -60,6 +61,9 @@ struct Rows {
     int32_t* counts;
     int num_pages;            // of the pool
 };
+
+// The last thing a thread does that has written tables, lengths or slots.
+__device__ __forceinline__ void release_writes() { __threadfence(); }
 
 __device__ __forceinline__ int cluster_rank() {
     int r;
@@ -409,6 +413,7 @@ __global__ void __launch_bounds__(kMoveThreads) fork_move_kernel(const __grid_co
         if (len % kPage) to[full] = take;
         a.t.lens[a.children[i]] = len;
     }
+    release_writes();
 }
 
 // ---------------------------------------------------------------- reserve
@@ -545,6 +550,7 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kPlanThreads)
         }
         a.slots[k] = slot;
     }
+    release_writes();
 }
 
 // ---------------------------------------------------------------- free
@@ -583,6 +589,7 @@ __global__ void __launch_bounds__(kMoveThreads) free_kernel(const __grid_constan
     }
     __syncthreads();   // every thread has read the length
     if (!first && threadIdx.x == 0) t.lens[r] = 0;
+    release_writes();
 }
 
 // ---------------------------------------------------------------- compact
@@ -686,6 +693,7 @@ __global__ void __launch_bounds__(kMoveThreads) compact_move_kernel(const __grid
         }
         a.table_out[i] = e;
     }
+    release_writes();
 }
 
 void fill_set(CacheSet* set, const sv_cache* caches, int n) {

@@ -235,8 +235,15 @@ __global__ void __launch_bounds__(kThreads, Cfg<FP8>::kPerSm)
         }
         mbar_init_fence();
     }
+    if (warp == kWarps) {
+        prefetch_tmap(&tmap_k);
+        prefetch_tmap(&tmap_v);
+    }
     __syncthreads();
 
+    // The inputs and pools, which the work before may still write.  Behind a prefix: the tiles have waited for it,
+    // and let this kernel start when they had.
+    if (!PREFIX) pdl_wait();
     int len = a.seq_lens[b];
     bool touched = true;
     if (a.groups.start) {
@@ -248,10 +255,6 @@ __global__ void __launch_bounds__(kThreads, Cfg<FP8>::kPerSm)
     } else if (len < 0 || (static_cast<int64_t>(len) + kPage - 1) / kPage > a.max_pages) {
         if (threadIdx.x == 0 && split == 0) svq_flag(SV_DEVERR_SEQ_LEN);
         len = 0;
-    }
-    if (warp == kWarps) {
-        prefetch_tmap(&tmap_k);
-        prefetch_tmap(&tmap_v);
     }
     // Q^T fragments (B operand): head `row` of the group.  bf16: channels 16 k + 2 quad (+ 8).  e4m3: f16,
     // channels 16 k + 4 quad .. + 3 (a dot product does not depend on the channels' order), times a power of
@@ -293,9 +296,6 @@ __global__ void __launch_bounds__(kThreads, Cfg<FP8>::kPerSm)
         }
     }
     const View v = view_of<PREFIX>(a, len, b, split == 0 && h == 0 && threadIdx.x == 0);
-    // The pools and the workspace, which the work before may still use.  Behind a prefix: the tiles,
-    // which let this kernel start when what came before them had ended.
-    if (!PREFIX) pdl_wait();
     const int chunk = (v.count + a.num_splits - 1) / a.num_splits;
     const int j0 = min(v.count, split * chunk);
     const int mine = min(v.count, j0 + chunk) - j0;

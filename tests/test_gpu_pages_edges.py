@@ -108,3 +108,49 @@ def test_pages_held_outside_the_rows_are_found_after_a_compaction(pool, rows, ma
     assert [p for p in range(pool) if to[p] >= 0] == held and sorted(to[p] for p in held) == list(range(live))
     assert all(t == -1 for p, t in enumerate(to) if p not in set(held))
     assert [d.m.data[to[p]] for p in held] == [data[p] for p in held]
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+def test_decodes_right_behind_the_calls_that_lengthen_rows(fp8):
+    """Nothing between sv_pages_reserve or sv_pages_fork and the decode that reads the lengths and pages they wrote:
+    the same as with the device idle in between."""
+    rows, max_pages, hkv, group, pool = 64, 64, 4, 8, 6000
+    hq = hkv * group
+    g = torch.Generator(device=DEV).manual_seed(2)
+    shape = (pool, hkv, PAGE, DIM)
+    meta = torch.zeros((pool, hkv, 2, DIM), dtype=torch.bfloat16, device=DEV)
+    if fp8:
+        scale = torch.full(shape[:3], 0.01, device=DEV)
+        codes = [torch.randint(0, 0x70, shape, generator=g, device=DEV, dtype=torch.uint8) for _ in range(2)]
+        cache = binding.Cache(*codes, meta, scale, scale.clone())
+    else:
+        cache = binding.Cache(*[torch.randn(shape, generator=g, device=DEV).bfloat16() for _ in range(2)], meta)
+    table = torch.full((rows, max_pages), -1, dtype=torch.int32, device=DEV)
+    lens, counts, all_rows = ints([0] * rows), ints([0] * pool), ints(list(range(rows)))
+    ws = torch.empty(binding.sv_pages_workspace_size(pool, rows, rows), dtype=torch.uint8, device=DEV)
+    aw = torch.empty(binding.sv_window_attention_workspace_size(rows, hq, hkv, rows), dtype=torch.uint8, device=DEV)
+    pw = torch.empty(binding.sv_prefix_decode_workspace_size(rows, hq, hkv, 1), dtype=torch.uint8, device=DEV)
+    add, slots = ints([13] * rows), torch.empty(13 * rows, dtype=torch.int32, device=DEV)
+    q = torch.randn((rows, hq, DIM), generator=g, device=DEV).bfloat16()
+    groups, none = ints([0, rows]), ints([0])
+
+    def both():
+        o = [(torch.empty_like(q), torch.empty((rows, hq), device=DEV)) for _ in range(2)]
+        binding.sv_window_attention(cache, q, table, lens, 200, 4, *o[0], aw)
+        binding.sv_prefix_decode(cache, q, table, lens, groups, none, *o[1], pw)
+        return [x for y in o for x in y]
+
+    for step in range(40):
+        torch.cuda.synchronize()
+        if step % 10 == 9:                   # forks of row 0 in place of the others
+            kids = all_rows[1:].contiguous()
+            binding.sv_pages_free(table, lens, counts, kids)
+            binding.sv_pages_fork(cache, table, lens, counts, ints([0] * (rows - 1)), kids, ws)
+        else:
+            binding.sv_pages_reserve(table, lens, counts, all_rows, add, slots, ws)
+        got = both()
+        torch.cuda.synchronize()
+        for x, y in zip(got, both()):
+            assert torch.equal(x, y), step
+    assert lens.tolist() == [13 * 36] * rows
+    assert binding.sv_get_device_error() == 0
