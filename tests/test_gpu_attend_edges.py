@@ -313,3 +313,75 @@ def test_long_sums_of_one_sign_in_single_tokens(length, fp8):
     _, ls, _, _ = weighted(q, k64, torch.ones_like(k64), torch.full((batch, 1024), length // 1024, device=DEV), DIM ** -0.5)
     # a lane's sum of length / 64 pages' weights, each addition rounded
     assert ((lse - ls).abs() <= 1e-5 + length / 64 * 2.0 ** -24).all()
+
+
+@pytest.mark.parametrize("wide", [0, 5000])
+@pytest.mark.parametrize("length,flag", [(70, 0), (64, 0), (0, 0), (63, 0x40), (1, 0x40), (-1, 0x8), (-2 ** 31, 0x8), (None, 0x8)])
+def test_prefix_decode_says_exactly_what_is_wrong(length, flag, wide):
+    """A request of a group with 4 shared pages, of every length."""
+    starts, shared = [0, 3, 5], [4, 0]
+    case = PagedCase([70, 70, 90, 20, 33, 40], 2)
+    prefix.share(case, starts, shared)
+    prefix.run.wide = False
+    q = prefix.queries(case, 8)
+    ref = prefix.reference(case, q, range(5))
+    table = torch.nn.functional.pad(case.table, (0, wide), value=-1).to(DEV)
+    lens = list(case.lens)
+    lens[1] = table.shape[1] * PAGE + 1 if length is None else length
+    if length == 64:
+        k, v = case.tokens(1, 64)
+        ref = [torch.cat([x[:1], y, x[2:]]) for x, y in zip(ref, attend(q[1:2], k, v, window_seen(64, 1, 0, 0, DEV), DIM ** -0.5))]
+    out, lse = torch.full_like(q, 7.0), torch.full((6, 16), 7.0, device=DEV)
+    ws = torch.empty(binding.sv_prefix_decode_workspace_size(6, 16, 2, 2), dtype=torch.uint8, device=DEV)
+    binding.sv_prefix_decode(case.cache(), q, table, ints(lens), ints(starts), ints(shared), out, lse, ws)
+    assert binding.sv_get_device_error() == flag
+    right = [0, 1, 2, 3, 4] if lens[1] in (70, 64) else [0, 2, 3, 4]
+    check(out[right], lse[right], [x[right] for x in ref])
+    if 1 not in right:
+        assert (out[1] == 0).all() and torch.isneginf(lse[1]).all()
+    assert (out[5] == 7).all() and (lse[5] == 7).all()
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("v_mean", [0.0, 3.0])        # outputs that are averages near 0, and that are not
+def test_many_short_requests_in_tiles(v_mean, fp8):
+    """More items than CTAs: whole items and cut ones in one call of the tiles."""
+    lens = [1 + (37 * i) % 400 for i in range(90)]
+    compare(PagedCase(lens, 4, spare=0, fp8=fp8, v_mean=v_mean), [1] * 90, 2, 90, 7)
+    lens = [1 + (337 * i) % 4000 for i in range(40)]
+    compare(PagedCase(lens, 4, spare=0, fp8=fp8, v_mean=v_mean), [min(n, 1 + 11 * i % 70) for i, n in enumerate(lens)], 8, 0, 0)
+
+
+@pytest.mark.parametrize("fp8,poison", [(False, "nan"), (False, "inf"), (True, "nan"), (True, "scale")])
+@pytest.mark.parametrize("form", ["window", "alone", "tiles"])
+def test_values_that_are_not_finite_in_single_tokens(form, fp8, poison):
+    """They reach the requests that see them: one token of a request's own, one of a shared prefix."""
+    starts, shared = [0, 3, 6], [4, 6]
+    case = PagedCase([100, 64, 90, 700, 96, 97], 2, fp8=fp8)
+    window, sink = (0, 0) if form != "window" else (60, 3)
+    if form != "window":
+        prefix.share(case, starts, shared)
+    q = prefix.queries(case, 4)
+    seen = [window_seen(n, 1, window, sink, DEV) for n in case.lens]
+    ref = [torch.cat(x) for x in zip(*[attend(q[b:b + 1], *case.tokens(b), seen[b], DIM ** -0.5) for b in range(6)])]
+    hit = torch.zeros((6, DIM), dtype=torch.bool, device=DEV)
+    for b, t, channel in ((2, 85, 3), (3, 690, 127), (0, 20, 64)):
+        page, at = case.table[b, t // PAGE], t % PAGE
+        if poison == "scale":
+            case.vs[page, :, at] = float("nan")
+        else:
+            case.v[page, :, at, channel] = 0x7F if fp8 else float(poison)
+        for r in range(6):
+            same = r == b or (form != "window" and t < PAGE * shared[0 if r < 3 else 1] and case.table[r, t // PAGE] == page)
+            if same and t < case.lens[r] and seen[r][0, t]:
+                hit[r, slice(None) if poison == "scale" else channel] = True
+    assert hit.any(1).sum() >= 2 and not hit.all(1).all()
+    if form == "window":
+        out, lse = run(case, q, window, sink)
+    else:
+        prefix.run.wide = form == "tiles"
+        out, lse = prefix.run(case, q, starts, shared)
+    assert binding.sv_get_device_error() == 0
+    hit = hit[:, None].expand(-1, 8, -1)
+    assert torch.equal(out.isposinf() if poison == "inf" else out.isnan(), hit)
+    check(torch.where(hit, 0, out), lse, (torch.where(hit, 0, ref[0]), *ref[1:]))
