@@ -328,12 +328,13 @@ namespace {
 // Query tokens of one call: the row count times 8 query heads, and the row
 // tiles of all of them, stay within 31 bits.
 constexpr int kMaxQueryTokens = 1 << 24;
+constexpr int kMaxGroups = 65535;
 // Tokens of a page table's row: positions are 32-bit, below 2^30.
 constexpr int kMaxRowPages = 1 << 26;
 
 bool attend_sizes_ok(int batch, int num_q_heads, int num_kv_heads) {
     return batch >= 1 && batch <= 65535 && num_kv_heads >= 1 && num_q_heads >= 1 && num_q_heads % num_kv_heads == 0 &&
-           num_q_heads / num_kv_heads <= kMaxGroup;
+           num_q_heads / num_kv_heads <= kMaxGroup && static_cast<int64_t>(batch) * num_q_heads <= INT_MAX;
 }
 
 int attend_checks(const sv_cache* cache, const void* q, int num_q_heads, const int32_t* page_table,
@@ -418,7 +419,7 @@ int sv_quest_decode_step(const sv_cache* cache, const void* q, int32_t num_q_hea
 }
 
 size_t sv_window_attention_workspace_size(int32_t batch, int32_t num_q_heads, int32_t num_kv_heads, int32_t total_q) {
-    if (!attend_sizes_ok(batch, num_q_heads, num_kv_heads) || total_q < 0) return 0;
+    if (!attend_sizes_ok(batch, num_q_heads, num_kv_heads) || total_q < 0 || total_q > kMaxQueryTokens) return 0;
     return window_workspace_bytes(batch, num_q_heads, num_kv_heads, total_q);
 }
 
@@ -446,7 +447,7 @@ int sv_window_attention(const sv_cache* cache, const void* q, int32_t num_q_head
 }
 
 size_t sv_prefix_decode_workspace_size(int32_t batch, int32_t num_q_heads, int32_t num_kv_heads, int32_t num_groups) {
-    if (!attend_sizes_ok(batch, num_q_heads, num_kv_heads) || num_groups < 1) return 0;
+    if (!attend_sizes_ok(batch, num_q_heads, num_kv_heads) || num_groups < 1 || num_groups > kMaxGroups) return 0;
     return prefix_workspace_bytes(batch, num_q_heads, num_kv_heads, num_groups);
 }
 
@@ -457,7 +458,7 @@ int sv_prefix_decode(const sv_cache* cache, const void* q, int32_t num_q_heads, 
     int st = attend_checks(cache, q, num_q_heads, page_table, seq_lens, batch, max_pages, softmax_scale, out, lse);
     if (st) return st;
     if (!group_start || !shared_pages || num_groups < 1) return SV_ERR_INVALID_ARG;
-    if (num_groups > 65535) return SV_ERR_UNSUPPORTED;
+    if (num_groups > kMaxGroups) return SV_ERR_UNSUPPORTED;
     if (!workspace || workspace_bytes < sv_prefix_decode_workspace_size(batch, num_q_heads, cache->num_kv_heads, num_groups))
         return SV_ERR_WORKSPACE;
     if (!aligned16(workspace)) return SV_ERR_INVALID_ARG;

@@ -38,3 +38,11 @@ def test_binding_checks_the_map():
     with pytest.raises(ValueError, match="page_map"):
         binding.sv_pages_compact(caches, table, cpu, cpu, table, cpu, torch.zeros(1, dtype=torch.int32), cpu,
                                  page_map=torch.zeros(5, dtype=torch.int32))
+
+
+def test_workspace_sizes_of_what_is_not_taken_are_zero(lib):
+    f, g = binding.sv_window_attention_workspace_size, binding.sv_prefix_decode_workspace_size
+    assert f(1, 32, 4, 1 << 24) > 0 and f(1, 32, 4, (1 << 24) + 1) == 0
+    assert f(65535, 1 << 15, 1 << 15, 1) > 0 and f(65535, 1 << 16, 1 << 16, 1) == 0
+    assert g(8, 32, 4, 65535) > 0 and g(8, 32, 4, 65536) == 0
+    assert g(65535, 1 << 16, 1 << 16, 1) == 0
