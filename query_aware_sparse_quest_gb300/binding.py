@@ -399,6 +399,8 @@ class CacheList:
         self.caches = tuple(caches)
         if not self.caches:
             raise ValueError("at least one cache")
+        if len({c.k_pool.get_device() for c in self.caches}) > 1:
+            raise ValueError("the caches of a list must be on one device")
         self.c = (sv_cache * len(self.caches))(*(c.c for c in self.caches))
 
     @property

@@ -46,3 +46,14 @@ def test_workspace_sizes_of_what_is_not_taken_are_zero(lib):
     assert f(65535, 1 << 15, 1 << 15, 1) > 0 and f(65535, 1 << 16, 1 << 16, 1) == 0
     assert g(8, 32, 4, 65535) > 0 and g(8, 32, 4, 65536) == 0
     assert g(65535, 1 << 16, 1 << 16, 1) == 0
+
+
+def test_caches_of_a_list_are_on_one_device():
+    """The calls look at the first one's device only."""
+    class On:
+        def __init__(self, device):
+            self.k_pool, self.c = self, _fake_cache()
+            self.get_device = lambda: device
+    assert len(binding.CacheList([On(1), On(1)]).caches) == 2
+    with pytest.raises(ValueError, match="one device"):
+        binding.CacheList([On(0), On(0), On(1)])
