@@ -374,7 +374,8 @@ size_t sv_window_attention_workspace_size(int32_t batch, int32_t num_q_heads, in
  * sv_prefix_decode -- dense decode attention of a batch in which groups of
  * requests hold the same first pages (what sv_pages_fork makes): the result of
  * sv_sparse_decode with sel_idx = NULL, with every shared page read once for
- * its whole group instead of once a request.  (Where batch * kv heads *
+ * 256 rows (request x query head of a kv head) of its group instead of once a
+ * request.  (Where batch * kv heads *
  * max_pages is small, at most 28000 pages in bf16 and 20000 in e4m3 and rows of
  * at most 640 and 480, requests are read each by itself: one launch, shared
  * pages from L2.)  max_pages decides, so a narrow page table pays.

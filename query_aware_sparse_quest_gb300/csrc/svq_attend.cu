@@ -8,10 +8,14 @@
 // tile K (128 tokens x 128) and a value tile V,
 //   S = Q K^T                  (fp32 in TMEM, 8 MMAs of k = 16 channels)
 //   P = exp2(S * scale - base) (bf16 in TMEM over S; base = a running maximum)
-//   O = O * 2^(old - new base) + P V   (fp32 in TMEM, one MMA of k = 16 per page)
+//   O = O * 2^(old - new base) + P V   (fp32 in TMEM, one MMA of k = 16 per page;
+//                               every kFoldTiles tiles it moves into sums in memory)
 // and at the end out = O / sum P, lse = ln 2 * (base + log2 sum P).  The sums and
 // bases are fp32.  P is rounded to bf16 because one MMA takes both operands in
-// one type and V is bf16; the sum is taken of the unrounded weights.
+// one type and V is bf16; the sum is taken of the unrounded weights.  That is off
+// by at most 2^-8 of each weight (outputs are 0.0023 from 64 bits where the
+// output's own rounding alone is 0.0017); P in two parts would be half as much
+// tensor work again.
 //
 // Work.  An entry is a row tile with its page range: a plan kernel lists those
 // of chunks, those of prefixes follow from the groups.  Every CTA takes an
@@ -38,14 +42,15 @@
 // products (8 MMAs of 64 cycles a product; 128 exponentials a row and tile on
 // 16 lanes a cycle take as long).  e4m3: instructions, of the softmax (the
 // scales, two passes over S) and of widening every tile's codes.  Few rows or
-// short runs: the start, the first copies, and partials.  Measured on a GB300
-// (copy 6.8 TB/s, library bf16 product 1895 TFLOP/s), 32 query / 4 kv heads, time
-// of a call in a run of calls: a 4096-token chunk at 32768 tokens, causal, 1.24
-// to 1.36 ms by the card's power (1520 to 1660 TFLOP/s, 80 to 88 % of the
-// product's), with a window of 4096 tokens 212 us (1300 TFLOP/s of visible work;
-// 12 % of the tiles' work is masked or item cost); 7 ragged e4m3 requests of up
-// to 4000 tokens 89 us (48 % of the issue slots, the tensor pipe 18 %); 32
-// requests behind 32768 shared tokens 39 us, of which these tiles 21 to 25.
+// short runs: the start, the first copies, and partials.  Measured on GB300s
+// (copy 6.8 TB/s, library bf16 product 1895 TFLOP/s), 32 query / 4 kv heads, on the
+// device in a graph and as a call in a run of calls: a 4096-token chunk at 32768
+// tokens, causal, 1.24 to 1.28 ms and 1.33 to 1.38, by the card's power (1490 to
+// 1650 TFLOP/s, 79 to 87 % of the product's), with a window of 4096 tokens 216 us
+// and 220 to 224 (1250 TFLOP/s of visible work; 12 % of the tiles' work is masked
+// or item cost); 7 ragged e4m3 requests of up to 4000 tokens 87 us and 92 (48 % of
+// the issue slots, the tensor pipe 18 %); 32 requests behind 32768 shared tokens
+// 38 to 40 us and 42 to 44, of which these tiles 21 to 25.
 #include <climits>
 
 #include "svq_paged.cuh"

@@ -140,8 +140,9 @@ __device__ __forceinline__ int tiles_of(int npages) { return (npages + kTilePage
 // What an item costs beside its tiles (loading Q, filling the pipeline, writing
 // the rows), in tiles: shares of the work count it, so that a CTA with many
 // short items does not take longer than one with few long ones.  7 ragged e4m3
-// requests / 32 requests behind a prefix, us: 1: 117 / 53.4, 2: 103.6 / 50.6,
-// 3: 103.3 / 48.9, 4: 102.6 / 49.1.
+// requests / 32 requests behind a prefix / 61 e4m3 ones / a 4096-token chunk with
+// a window, device us: 1: 96.6 / 41.2 / 43.4 / 216.4, 2: 88.6 / 41.5 / 43.9 / 215.3,
+// 3: 88.3 / 41.4 / 44.3 / 215.3, 4: 87.4 / 41.8 / 44.4 / 213.5.
 constexpr int kItemCost = 3;
 __device__ __forceinline__ int cost_of(int tiles) { return tiles ? tiles + kItemCost : 0; }
 

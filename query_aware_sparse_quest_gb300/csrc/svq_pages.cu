@@ -16,8 +16,9 @@
 // layer (34 KB for 4 kv heads), bound by HBM.  Measured on a GB300 (a plain copy:
 // 6.8 TB/s): packing a pool of 16384 pages held to 60 per cent, 4 layers of 4 kv
 // heads, 181 us for 1.10 GB read and written (6.1 TB/s); fork, reserve and free
-// for 64 children of 16 parents in 8 layers 24 us, for 8 of 1 in one layer 22 us:
-// four launches and three calls of the host, with 34 MB and 0.1 MB moved.
+// for 64 children of 16 parents in 8 layers 25 us on the device and 25.5 as calls,
+// for 8 of 1 in one layer 18.6 and 22 to 23: four launches and three calls of the
+// host, with 34 MB and 0.1 MB moved.
 //
 // Kernels are launched to overlap the end of the one before (a beam step of
 // three calls 33 -> 24 us), but each waits for it before its first access and

@@ -15,7 +15,8 @@
 // shared memory; the partials of more are joined by a second kernel.  Behind a
 // prefix a cluster also joins what the tiles left of it, so the tiles and this
 // kernel, which starts while the last of them run, are the whole call (32
-// requests behind 32768 tokens 39.2 us; with a kernel for the join 44.2).
+// requests behind 32768 tokens 38 to 40 us on the device; a kernel for the join took
+// 5 us more).
 //
 // e4m3 pools: codes convert to f16 exactly and the products run in f16.  The
 // value weight of token t is exp(z_t) s_v(t).  It is formed as
@@ -29,12 +30,12 @@
 // fp32.
 //
 // Measured on a GB300 (a plain copy: 6.8 TB/s), 32 query / 4 kv heads, device
-// time of a call: 8 requests with a window of 4096 tokens 16.4 us (67.5 MB, 4.1
+// time of a call: 8 requests with a window of 4096 tokens 16.7 us (67.5 MB, 4.0
 // TB/s; 10 us at the copy's rate: 5 us are the kernel's start, the first copies
-// and the join), 32 e4m3 requests with a window of 2048 21.4 us (70.5 MB, 3.3
-// TB/s: 40 % of the issue slots are taken and DRAM is 35 % busy; latency within
+// and the join), 32 e4m3 requests with a window of 2048 22.2 us (70.5 MB, 3.2
+// TB/s: 43 % of the issue slots are taken and DRAM is 34 % busy; latency within
 // a page's chain of conversions and products), 32 requests at 32768 tokens without a
-// window 308 us (2.15 GB, 7.0 TB/s).
+// window 309 us (2.15 GB, 7.0 TB/s).
 #include <climits>
 
 #include "svq_paged.cuh"
@@ -56,22 +57,24 @@ constexpr float kF16Lift = 7.f;
 constexpr int kMaxSplits = 64;
 constexpr int kMaxCluster = 8;                     // CTAs of a cluster at most (what every launch may have)
 // At least this many pages a split once every SM has work (a split costs its
-// start, its merge and its partial), and at least kFewPages before that.  Us, 32
-// query / 4 kv heads: 24 pages / 12 / 48 for 8 requests of 256 pages 11.8 / 11.8 /
-// 13.6, for 16 of 128 11.6 / 11.6 / 13.6; e4m3, 16 / 8 / 32 for 8 of 128 10.5 /
-// 11.6 / 11.6, for 32 of 32 10.3 / 11.0 / 11.1; 8 / 4 / 16 of few for 1 of 32 5.6
-// / 5.7 / 6.8, for 4 of 128 7.9 / 9.7 / 8.2, e4m3 8.7 / 10.5 / 9.8.
+// start, its merge and its partial), and at least kFewPages before that.  Device us
+// with the pages in L2, 32 query / 4 kv heads: 24 pages / 12 / 48 for 8 requests of
+// 256 pages 12.0 / 12.2 / 14.1, for 16 of 128 14.4 / 14.5 / 16.1; e4m3, 16 / 8 / 32
+// for 8 of 128 10.4 / 11.5 / 11.5, for 32 of 32 10.3 / 10.8 / 11.0; 8 / 4 / 16 of few
+// for 1 of 32 6.1 / 5.8 / 7.1, for 4 of 128 8.1 / 9.8 / 8.6, e4m3 8.8 / 10.5 / 10.2.
 constexpr int kSplitPages[2] = {24, 16};           // bf16, e4m3
 constexpr int kFewPages = 8;
 // Rows of at most so many pages go to a cluster even where more than 8 splits would fill more SMs.
 constexpr int kClusterPages = 80;
 // Requests that share pages: each is read alone, shared pages and all, in one
 // launch, if the batch and kv heads have at most so many pages together and a
-// row so many.  Against sharing (three launches), us, 8 query heads a kv head,
-// device time alone: 16 rows of 135 pages bf16 9.4 / 18.5, e4m3 11.3 / 20.4; 64
-// rows of 407 21.8 / 27.7 and 30.2 / 27.8; 256 rows of 135 27.7 / 25.6 and 36.6 /
-// 28.7; 1 row of 519 14.6 / 17.4 and 20.6 / 20.3; 1 row of 1031 23.3 / 19.9 and
-// 34.4 / 22.2.
+// row so many.  Alone / shared (tiles and this kernel; a join too where more than 8
+// splits read a row), 8 query heads a kv head, device us: 16 rows of 135 pages bf16
+// 9.3 / 18.1, e4m3 11.0 / 21.0; 64 rows of 407 21.3 / 21.7 and 30.6 / 27.3; 128 rows
+// of 200 21.0 / 23.0 and 30.0 / 26.4; 256 rows of 135 30.1 / 25.1 and 37.6 / 27.0;
+// 1 row of 519 15.5 / 17.9 and 20.5 / 20.1; 1 row of 1031 24.5 / 20.5 and 34.5 /
+// 22.4.  At the borders either way costs up to 2 us: 40 rows of 600 bf16 (alone)
+// 22.7 / 21.5, 16 rows of 500 e4m3 (shared) 22.8 / 24.5.
 constexpr int64_t kAlonePages[2] = {28000, 20000};   // bf16, e4m3
 constexpr int64_t kAloneRow[2] = {640, 480};
 
@@ -737,10 +740,15 @@ int window_decode_splits(bool fp8, int batch, int num_kv_heads, int64_t pages, i
 
 // The same, as a cluster that joins a row without a second launch (5 us of the
 // host's time; the GPU's is the same); 0: more splits than a cluster has CTAs
-// are faster (`must`: never).  With 8 instead of more: 32 rows bf16 of 256 pages
-// 14.0 against 13.9 us, 20 rows 10.8 / 9.5, 52 rows e4m3 20.5 / 17.9, 1 row of 64
-// pages 6.0 / 5.8, of 512 13.4 / 8.4.  Clusters of 7 and 8 CTAs, three to an SM,
-// do not fill the GPU: 64 rows of 256 pages 34.4 us with 7, 26.3 with 5.
+// are faster (`must`: never).  Device us with 8 splits / with more: 32 rows bf16 of
+// 256 pages 12.0 / 12.0, 20 rows 11.2 / 10.2, of 2048 pages 63.3 / 55.7; 52 rows e4m3
+// of 256 21.0 / 18.3; 1 row of 64 pages 6.3 / 6.5, of 96 6.9 / 6.7, of 512 14.2 / 9.3.
+// So bf16 rows that 8 splits would not bring to one and a half CTAs an SM take
+// more, e4m3 rows always, short rows never.
+// bf16 CTAs, three to an SM, in clusters of 7 or 8 do not fit a part of the GPU to
+// its last place: where they would take more than 85 % of all places, 6 are taken.
+// Of 256 pages: 40 rows with 8 (70 %) 15.2, with 6 16.1; 52 rows with 8 (91 %) 30.3,
+// with 6 22.1; 64 rows with 7 (98 %) 34.8, with 8 33.5, with 6 25.7, with 5 26.1.
 int window_decode_cluster(bool fp8, int batch, int num_kv_heads, int64_t pages, int sm_count, bool must) {
     const int64_t rows = static_cast<int64_t>(batch) * num_kv_heads;
     int s = window_decode_splits(fp8, batch, num_kv_heads, pages, sm_count);
