@@ -531,7 +531,10 @@ __global__ void __launch_bounds__(kThreads, Cfg<FP8>::kPerSm)
                 add(o[mt], d);
             }
         }
-        __syncwarp();   // every lane has read the stage before it is released
+        // Every lane has read the stage before it is released, and the next copy into it stays behind these reads
+        // (without the fence an arrival can overtake them where the load and store unit is busy with other stores).
+        fence_proxy_async_smem();
+        __syncwarp();
         if (lane == 0) mbar_arrive(empty0 + st * 8);
     }
 #pragma unroll
