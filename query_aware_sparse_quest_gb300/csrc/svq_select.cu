@@ -356,6 +356,7 @@ __global__ void __launch_bounds__(kScoreThreads, 1) score_pages_kernel(
                 acc[j] = s0 + s1;
             }
             const bool real = slot_ok[slot] != 0;
+            fence_proxy_async_smem();   // the next copy into the slot stays behind these reads
             __syncwarp();
             if (lane == 0) mbar_arrive(empty0 + slot * 8);
             const int lp = cta_begin + p;
@@ -394,6 +395,7 @@ __global__ void __launch_bounds__(kScoreThreads, 1) score_pages_kernel(
         for (int t = 0; t < C; ++t)
             w[t] = *reinterpret_cast<const uint4*>(lane_base + slot * S::kPageBytes + t * L * 16);
         const bool real = slot_ok[slot] != 0;
+        fence_proxy_async_smem();   // the next copy into the slot stays behind these reads
         __syncwarp();   // every lane has read the slot before it is released
         if (lane == 0) mbar_arrive(empty0 + slot * 8);
         float a0 = 0.f, a1 = 0.f;

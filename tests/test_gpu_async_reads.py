@@ -42,3 +42,28 @@ def test_window_attention_repeats_exactly_beside_scattered_stores(size, fp8):
         binding.sv_window_attention(cache, q, table, lens, 1000, 5, out, lse, ws, q_start=starts)
         return torch.cat([out.float().flatten(), lse.flatten()])
     repeats(call)
+
+
+@pytest.mark.parametrize("per_q_head", [0, 1])
+def test_scores_repeat_exactly_beside_scattered_stores(per_q_head):
+    B, Hkv, group, pages = 4, 4, 8, 3000
+    g = torch.Generator(device=DEV).manual_seed(1)
+    meta = torch.randn((B * pages, Hkv, 2, 128), generator=g, device=DEV).bfloat16()
+    pool = torch.zeros((B * pages, Hkv, 16, 128), dtype=torch.bfloat16, device=DEV)
+    cache = binding.Cache(pool, pool, meta)
+    table = torch.randperm(B * pages, generator=g, device=DEV).int().view(B, pages).contiguous()
+    lens = torch.full((B,), pages * 16, dtype=torch.int32, device=DEV)
+    q = torch.randn((B, Hkv * group, 128), generator=g, device=DEV).bfloat16()
+    rows = Hkv * (group if per_q_head else 1)
+    idx = torch.empty((B, rows, 64), dtype=torch.int32, device=DEV)
+    cnt = torch.empty((B, rows), dtype=torch.int32, device=DEV)
+    opts = binding.quest_opts(per_q_head=bool(per_q_head))
+
+    def score():
+        s = torch.empty((B, rows, pages), device=DEV)
+        if per_q_head:
+            binding.sv_quest_select_ex(cache, q, table, lens, 64, opts, idx, cnt, scores_out=s)
+        else:
+            binding.sv_quest_score(cache, q, table, lens, s)
+        return s
+    repeats(score)
