@@ -346,7 +346,8 @@ __global__ void __launch_bounds__(kDecodeThreads) flash_decode_split_kernel(cons
             ldmatrix_x4_trans(addr, a0, a1, a2, a3);
             mma_bf16_16816(o[mt], a0, a1, a2, a3, pb0, pb1);
         }
-        __syncwarp();   // every lane has read the stage before it is released
+        fence_proxy_async_smem();   // the next copy into the stage stays behind these reads
+        __syncwarp();               // every lane has read the stage before it is released
         if (lane == 0) mbar_arrive(empty0 + stage * 8);
     }
 

@@ -371,7 +371,8 @@ __global__ void __launch_bounds__(kF8Threads, 4) flash_decode_fp8_kernel(const _
             mma_f16_16816(o[2 * cb + 1], e4m3x2_to_f16x2(r2), e4m3x2_to_f16x2(r3), e4m3x2_to_f16x2(r2 >> 16),
                           e4m3x2_to_f16x2(r3 >> 16), pb0, pb1);
         }
-        __syncwarp();   // every lane has read the stage before it is released
+        fence_proxy_async_smem();   // the next copy into the stage stays behind these reads
+        __syncwarp();               // every lane has read the stage before it is released
         if (lane == 0) mbar_arrive(empty0 + stage * 8);
     }
 

@@ -67,3 +67,24 @@ def test_scores_repeat_exactly_beside_scattered_stores(per_q_head):
             binding.sv_quest_score(cache, q, table, lens, s)
         return s
     repeats(score)
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("budget", [0, 48])            # every page; selected ones
+def test_sparse_decode_repeats_exactly_beside_scattered_stores(budget, fp8):
+    case = PagedCase([1500 + 37 * i for i in range(24)], 2, fp8=fp8)
+    cache, table = case.cache(), case.table.clamp_min(0).to(DEV)
+    lens = torch.tensor(case.lens, dtype=torch.int32, device=DEV)
+    q = torch.randn((24, 16, DIM), device=DEV).bfloat16()
+    pages = budget or case.max_pages
+    sel = cnt = None
+    if budget:
+        sel = torch.stack([torch.randperm(90, device=DEV)[:budget].sort().values for _ in range(48)]).int().view(24, 2, budget).contiguous()
+        cnt = torch.full((24, 2), budget, dtype=torch.int32, device=DEV)
+    ws = torch.empty(binding.sv_sparse_decode_workspace_size(24, 16, 2, pages), dtype=torch.uint8, device=DEV)
+
+    def call():
+        out, lse = torch.empty_like(q), torch.empty((24, 16), device=DEV)
+        binding.sv_sparse_decode(cache, q, table, lens, sel, cnt, out, lse, ws)
+        return torch.cat([out.float().flatten(), lse.flatten()])
+    repeats(call)
