@@ -164,16 +164,16 @@ struct GroupAt {
     int g, a, entries, tiles;
     int64_t before;   // cost per kv head of the groups before it
 };
-// By the whole warp, 32 groups a round: the sum of the groups' costs per kv
-// head, and the group for which pick(before, cost) holds, if any (else g < 0).
-// rec: where the groups are written down, and what is wrong with them reported.
+// By the whole warp, 32 groups a round from group `from` on, before which lie groups of cost `total` per kv head that
+// end at request `reach`: the group for which pick(before, cost) holds, if any (else g < 0), and the cost up to the
+// last group looked at (all of them unless `stop`: the search ends with the group).  rec: where the groups are written
+// down, and what is wrong with them reported.
 template <typename F>
-__device__ __forceinline__ GroupAt warp_groups(const Groups& gr, int tok_per_entry, int64_t& total, GroupRec* rec, F&& pick) {
+__device__ __forceinline__ GroupAt warp_groups(const Groups& gr, int tok_per_entry, int from, int reach, int64_t& total,
+                                               bool stop, GroupRec* rec, F&& pick) {
     const int lane = threadIdx.x & 31;
     GroupAt found = {-1, 0, 0, 0, 0};
-    total = 0;
-    int reach = 0;   // where the sound groups so far end
-    for (int g0 = 0; g0 < gr.n; g0 += 32) {
+    for (int g0 = from; g0 < gr.n && !(stop && found.g >= 0); g0 += 32) {
         const int g = g0 + lane;
         int a = 0, end = 0, sp = 0;
         bool ok = false;
@@ -802,10 +802,11 @@ __global__ void __launch_bounds__(Cfg<FP8>::kThreads, 1)
             reg_dec<C::kOtherRegs>();
             const bool prefix = a.groups.start != nullptr;
             int num_entries = 0;
-            int64_t total;
+            int64_t total = 0;
             GroupAt grp;
             if (prefix) {
-                grp = warp_groups(a.groups, a.tok_per_entry, total, blockIdx.x == 0 ? a.group_rec : nullptr, [](int64_t, int64_t) { return false; });
+                grp = warp_groups(a.groups, a.tok_per_entry, 0, 0, total, false, blockIdx.x == 0 ? a.group_rec : nullptr,
+                                  [](int64_t, int64_t) { return false; });
             } else {
                 num_entries = *a.plan.num_entries;
                 total = a.plan.cum[num_entries];
@@ -820,7 +821,8 @@ __global__ void __launch_bounds__(Cfg<FP8>::kThreads, 1)
                 int64_t before;
                 int cost;
                 if (prefix) {
-                    grp = warp_groups(a.groups, a.tok_per_entry, total, nullptr,
+                    int64_t passed = 0;
+                    grp = warp_groups(a.groups, a.tok_per_entry, 0, 0, passed, true, nullptr,
                                       [u](int64_t b, int64_t c) { return b <= u && u < b + c; });
                     cost = cost_of(grp.tiles);
                     e = static_cast<int>(div64(u - grp.before, cost));
@@ -844,9 +846,9 @@ __global__ void __launch_bounds__(Cfg<FP8>::kThreads, 1)
                 if (left > 0) {
                     if (prefix && held != e) {
                         if (e == grp.entries) {   // the next group with something to read
-                            const int64_t u = grp.before + static_cast<int64_t>(grp.entries) * cost_of(grp.tiles);
-                            grp = warp_groups(a.groups, a.tok_per_entry, total, nullptr,
-                                              [u](int64_t b, int64_t c) { return b == u && c > 0; });
+                            int64_t passed = grp.before + static_cast<int64_t>(grp.entries) * cost_of(grp.tiles);
+                            grp = warp_groups(a.groups, a.tok_per_entry, grp.g + 1, a.groups.start[grp.g + 1], passed, true,
+                                              nullptr, [](int64_t, int64_t c) { return c > 0; });
                             e = 0;
                         }
                         const int row0 = grp.a + e * a.tok_per_entry;

@@ -385,3 +385,30 @@ def test_values_that_are_not_finite_in_single_tokens(form, fp8, poison):
     hit = hit[:, None].expand(-1, 8, -1)
     assert torch.equal(out.isposinf() if poison == "inf" else out.isnan(), hit)
     check(torch.where(hit, 0, out), lse, (torch.where(hit, 0, ref[0]), *ref[1:]))
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+def test_prefixes_of_many_groups(fp8):
+    """Groups in every round of 32 that the scheduler looks at: empty ones, ones that share nothing, ones out of order."""
+    rng = torch.Generator().manual_seed(9)
+    sizes = torch.randint(0, 7, (300,), generator=rng).tolist()
+    shared = [0 if i % 11 == 5 else 1 + i % 13 for i in range(300)]
+    sizes[64:96] = [0] * 32
+    starts = [sum(sizes[:g]) for g in range(301)]
+    of = [g for g in range(300) for _ in range(sizes[g])]
+    lens = [shared[g] * PAGE + 1 + 5 * b % 40 for b, g in enumerate(of)]
+    case = PagedCase(lens, 2, fp8=fp8)
+    prefix.share(case, starts, shared)
+    prefix.run.wide = True
+    q = prefix.queries(case, 4)
+    ref = prefix.reference(case, q, range(len(lens)))
+    out, lse = prefix.run(case, q, starts, shared)
+    assert binding.sv_get_device_error() == 0
+    check(out, lse, ref)
+    g = next(g for g in range(200, 290) if sizes[g] > 0 and sizes[g + 1] > 1)
+    broken = list(starts)
+    broken[g] = starts[g + 1] + 1          # group g ends before it begins, group g - 1 takes its requests and one more
+    out, lse = prefix.run(case, q, broken, shared)
+    assert binding.sv_get_device_error() & 0x40
+    right = [b for b in range(len(lens)) if of[b] not in (g - 1, g, g + 1)]
+    check(out[right], lse[right], [x[right] for x in ref])
