@@ -354,7 +354,9 @@ size_t sv_quest_decode_step_workspace_size(int32_t batch, int32_t num_q_heads, i
  *  - A K/V row may hold anything as far as the query tokens that do not see
  *    it are concerned: infinite and NaN values reach only those that do.  (A
  *    value seen by some query tokens of a row tile and not by others is put
- *    right afterwards, a row at a time: slow, and only then.)
+ *    right afterwards, a row at a time: slow, and only then.  A 4096-token
+ *    causal chunk at 32768 tokens, 1.3 ms: one NaN in it 50 ms, an infinity in
+ *    every token 600 ms, both growing with the context.)
  *  - Rows of one request and kv head are processed 256 at a time
  *    (token, query head), on the tensor cores; work is divided evenly over
  *    the GPU whatever the lengths.  The result does not depend on timing.
