@@ -12,7 +12,10 @@
  * the same cache, page tables and lengths: sv_window_attention (prefill chunks
  * and decode, causal or with a sliding window and sinks), sv_prefix_decode
  * (dense decode of requests that share their first pages) and sv_pages_* (who
- * holds which page: fork, reserve, free, compact, copy).
+ * holds which page: fork, reserve, free, compact, copy).  For caches that keep
+ * one latent vector a token in place of keys and values (the AttentionView's
+ * latent variant): sv_latent_append, sv_latent_attention, sv_latent_gather and
+ * sv_expanded_attention.
  *
  * Conventions common to every call
  *  - Every buffer argument is a DEVICE pointer, allocated and owned by the
@@ -34,8 +37,8 @@
  *    seq_lens, and the append kernel its slot_mapping, k_new and v_new, as
  *    soon as they start, possibly while the kernel enqueued just before them
  *    is still running.  Pools, metadata and workspace, and every input of
- *    sv_window_attention, sv_prefix_decode and sv_pages_*, are touched only
- *    after that kernel has completed.  So the kernel that produces a
+ *    sv_window_attention, sv_prefix_decode, sv_pages_*, sv_latent_* and
+ *    sv_expanded_attention, are touched only after that kernel has completed.  So the kernel that produces a
  *    call's inputs must not release its dependents early
  *    (griddepcontrol.launch_dependents): an ordinary kernel, a copy, a call
  *    of this library, or any work enqueued earlier is fine.
@@ -52,6 +55,7 @@
  *  - Geometry: page_size must be 16 and head_dim 128 (SV_ERR_UNSUPPORTED
  *    otherwise); num_q_heads must be a multiple of num_kv_heads with at most
  *    8 query heads per kv head; query head h reads kv head h / (Hq / Hkv).
+ *    (Caches of latents have a geometry of their own: see sv_latent_append.)
  *
  * Layouts (row-major, innermost last)
  *   k_pool, v_pool  bf16 [num_phys_pages][num_kv_heads][16][128]   (e4m3: see sv_cache)
@@ -106,6 +110,8 @@ enum sv_status {
 /* K/V pool formats (sv_cache.kv_format). */
 #define SV_KV_BF16     0   /* k_pool, v_pool bf16 [pages][Hkv][16][128] */
 #define SV_KV_FP8_E4M3 1   /* k_pool, v_pool e4m3 bytes [pages][Hkv][16][128], one fp32 scale per row */
+#define SV_KV_LATENT_BF16 2  /* latents: k_pool bf16 [pages][16][512], v_pool rotary keys bf16 [pages][16][64] */
+#define SV_KV_LATENT_E4M3 3  /* the same with k_pool e4m3 bytes [pages][16][512] and one fp32 scale a token */
 
 /*
  * The paged pool and its metadata: caller-owned device buffers.
@@ -119,7 +125,8 @@ enum sv_status {
  * back as value(code) * s.  The metadata stays bf16 and holds the min / max
  * of the keys as appended (before coding), so page selection is the same as
  * for bf16 pools; only attention reads the coded rows.  All calls accept both
- * formats.
+ * formats.  The latent formats are those of sv_latent_* and of sv_pages_*; other
+ * calls refuse them (SV_ERR_UNSUPPORTED).
  */
 typedef struct sv_cache {
     void* k_pool;             /* [num_phys_pages][num_kv_heads][16][128] of the format's element */
@@ -129,7 +136,7 @@ typedef struct sv_cache {
     int32_t num_kv_heads;
     int32_t page_size;        /* must be 16 */
     int32_t head_dim;         /* must be 128 */
-    int32_t kv_format;        /* SV_KV_BF16 (zero) or SV_KV_FP8_E4M3 */
+    int32_t kv_format;        /* SV_KV_BF16 (zero), SV_KV_FP8_E4M3, or a latent format */
     void* k_scale;            /* SV_KV_FP8_E4M3: fp32 [num_phys_pages][num_kv_heads][16]; else unused */
     void* v_scale;
 } sv_cache;
@@ -499,6 +506,123 @@ int sv_pages_compact_ex(const sv_cache* caches, int32_t num_caches, const int32_
                         int32_t num_rows, int32_t max_pages, const int32_t* ref_counts, int32_t* page_table_out,
                         int32_t* ref_counts_out, int32_t* num_live, int32_t* page_map, void* workspace,
                         size_t workspace_bytes, void* stream);
+
+/*
+ * Latent caches.  A token is kept as one latent vector of 512 channels and one
+ * rotary key of 64, which all query heads share.  Attention over them has two
+ * forms with the same result: the absorbed one, in which the query has been
+ * multiplied with the key expansion, so that it meets the latent itself, and the
+ * average is one of latents (sv_latent_attention); and the expanded one, in
+ * which every head's keys and values have been computed from the latents
+ * (sv_latent_gather reads them back for that product) and attention is that of
+ * ordinary heads (sv_expanded_attention): 3.4 times fewer operations a pair, so
+ * the form for long prefills, at the price of the expansion.
+ *   An sv_cache of a latent format:
+ *     k_pool   latents [num_phys_pages][16][512], bf16 or e4m3 codes
+ *     v_pool   rotary keys bf16 [num_phys_pages][16][64]
+ *     k_scale  SV_KV_LATENT_E4M3: fp32 [num_phys_pages][16], 16-byte aligned
+ *     num_kv_heads 1, page_size 16, head_dim 512; meta and v_scale are not used
+ * The codec is that of SV_KV_FP8_E4M3 over a token's 512 latent channels: scale =
+ * max |x| / 448, code = e4m3(x / scale); rotary keys stay bf16.  Page tables,
+ * lengths, slots and sv_pages_* are those of the other caches, and caches of all
+ * formats may share one page table.
+ */
+
+/*
+ * sv_latent_append -- writes T tokens' latents and rotary keys into the pool at
+ * slot = physical_page * 16 + offset, coded for SV_KV_LATENT_E4M3.
+ *   latent         bf16, row t at latent + t * latent_stride elements, 512 each
+ *   rope           bf16, row t at rope + t * rope_stride elements, 64 each
+ *   slot_mapping   int32 [T]; an entry outside the pool is SV_DEVERR_SLOT and
+ *                  its token is left out
+ *  - Strides are multiples of 8 and at least a row: both may be parts of one
+ *    projection's output [T][576].
+ *  - No slot is listed twice.  num_tokens == 0 launches nothing.
+ *  - A latent with an infinite or NaN channel reads back as NaN from a coded
+ *    cache.
+ */
+int sv_latent_append(const sv_cache* cache, const void* latent, int64_t latent_stride, const void* rope,
+                     int64_t rope_stride, const int32_t* slot_mapping, int64_t num_tokens, void* stream);
+
+/*
+ * sv_latent_gather -- reads cached tokens back as dense bf16 rows: row
+ * row_start[b] + i gets token first_token[b] + i of request b (the first tokens
+ * where first_token is NULL).
+ *   row_start    int32 [batch + 1], ascending inside [0, total_rows]
+ *   first_token  int32 [batch] or NULL
+ *   latent, rope bf16 rows as in sv_latent_append; codes read back as
+ *                value(code) * scale, rounded once to bf16
+ *  - Rows that no request's range holds are not written.  A range that is not
+ *    ascending inside [0, total_rows] is skipped (SV_DEVERR_Q_START).
+ *  - Rows of tokens that a request does not have (SV_DEVERR_SEQ_LEN), or whose
+ *    page the table does not give (SV_DEVERR_PAGE_TABLE), are 0.
+ *  - total_rows == 0 launches nothing.
+ */
+int sv_latent_gather(const sv_cache* cache, const int32_t* page_table, const int32_t* seq_lens, int32_t batch,
+                     int32_t max_pages, const int32_t* row_start, const int32_t* first_token, int64_t total_rows,
+                     void* latent, int64_t latent_stride, void* rope, int64_t rope_stride, void* stream);
+
+/*
+ * sv_latent_attention -- exact causal softmax attention in the absorbed form of
+ * query tokens over their own request's cached tokens: chunks of a prefill,
+ * single decode tokens, and both in one batch.  The query token at position p of
+ * its request sees the tokens j <= p, and over those, with the latent c_j, the
+ * rotary key r_j and z_j = (q_h[0..511] . c_j + q_h[512..575] . r_j) * softmax_scale,
+ *   out = sum_j softmax(z)_j c_j     bf16 [total_q][num_q_heads][512]
+ *   lse = ln(sum_j exp(z_j))         fp32 [total_q][num_q_heads]
+ *   q        bf16 [total_q][num_q_heads][576], 1 <= num_q_heads <= 128
+ *   q_start  as in sv_window_attention: rows q_start[b] .. q_start[b + 1] - 1 are
+ *            the last tokens of request b; NULL: one token a request
+ *  - q and out are 16-byte aligned.  The page table, lengths, rows that no
+ *    request holds, requests without tokens, errors, and what rows that are not
+ *    finite cost those that do not see them, are as in sv_window_attention.
+ *  - workspace: sv_latent_attention_workspace_size(...) bytes, not shared with a
+ *    call that may run at the same time; nothing in it needs to start at zero.
+ *    total_q * num_q_heads < 2^31, max_pages < 2^26.
+ */
+int sv_latent_attention(const sv_cache* cache, const void* q, int32_t num_q_heads, const int32_t* q_start,
+                        int32_t total_q, const int32_t* page_table, const int32_t* seq_lens, int32_t batch,
+                        int32_t max_pages, float softmax_scale, void* out, float* lse, void* workspace,
+                        size_t workspace_bytes, void* stream);
+
+/* Workspace bytes of sv_latent_attention (0 for sizes it does not take). */
+size_t sv_latent_attention_workspace_size(int32_t batch, int32_t num_q_heads, int32_t total_q);
+
+/*
+ * sv_expanded_attention -- exact softmax attention in the expanded form: heads
+ * with keys and values of their own and one rotary key a token for all of them,
+ * over ragged rows.  Request b's query tokens are rows q_start[b] ..
+ * q_start[b + 1] - 1 of q, its tokens rows kv_start[b] .. kv_start[b + 1] - 1 of
+ * k, rope and v.  With z_j = (q[0..127] . k_j + q[128..191] . rope_j) *
+ * softmax_scale over the tokens j that a query token sees,
+ *   out = sum_j softmax(z)_j v_j     bf16 [total_q][num_heads][128]
+ *   lse = ln(sum_j exp(z_j))         fp32 [total_q][num_heads]
+ *   q     bf16 [total_q][num_heads][192]
+ *   k, v  bf16, head h of token t at k + t * k_stride + h * k_head_stride elements,
+ *         128 each (the halves of one expansion's output [total_kv][num_heads][256],
+ *         for instance)
+ *   rope  bf16, token t at rope + t * rope_stride elements, 64 each
+ *  - causal != 0: the query tokens are the last of the request's tokens, and each
+ *    sees those up to itself; 0: every query token sees every token.
+ *  - Strides are multiples of 8 elements, at least a row and below 2^36; q, k,
+ *    rope, v and out are 16-byte aligned (out 32).
+ *  - A request without tokens gets out = 0, lse = -inf.  So does, with
+ *    SV_DEVERR_Q_START, one whose kv range is not ascending inside [0, total_kv]
+ *    or, if causal, holds fewer tokens than it has query tokens; a query range
+ *    outside [0, total_q] is skipped.  Rows that no request's range holds are not
+ *    written.  total_q == 0 launches nothing.
+ *  - Rows of k, rope and v that a query token does not see may hold anything, as
+ *    in sv_window_attention.
+ *  - workspace as above.  total_q * num_heads < 2^31, num_heads <= 65535.
+ */
+int sv_expanded_attention(const void* q, int32_t num_heads, const int32_t* q_start, int32_t total_q, const void* k,
+                          int64_t k_stride, int64_t k_head_stride, const void* rope, int64_t rope_stride,
+                          const void* v, int64_t v_stride, int64_t v_head_stride, const int32_t* kv_start,
+                          int32_t total_kv, int32_t batch, int32_t causal, float softmax_scale, void* out, float* lse,
+                          void* workspace, size_t workspace_bytes, void* stream);
+
+/* Workspace bytes of sv_expanded_attention (0 for sizes it does not take). */
+size_t sv_expanded_attention_workspace_size(int32_t batch, int32_t num_heads, int32_t total_q);
 
 /* Reads (and with reset != 0 clears) the current device's error word; the
  * read synchronises the device.  Returns SV_OK or SV_ERR_CUDA. */

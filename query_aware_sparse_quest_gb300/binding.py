@@ -31,7 +31,7 @@ class sv_quest_opts(ctypes.Structure):
                 ("layer", ctypes.c_int32), ("dense_layers", ctypes.c_int32)]
 
 
-SV_KV_BF16, SV_KV_FP8_E4M3 = 0, 1
+SV_KV_BF16, SV_KV_FP8_E4M3, SV_KV_LATENT_BF16, SV_KV_LATENT_E4M3 = 0, 1, 2, 3
 
 
 class sv_cache(ctypes.Structure):
@@ -74,6 +74,11 @@ def _load():
         "sv_pages_free": [vp, vp, i32, i32, vp, i64, vp, vp, vp, i32, vp],
         "sv_pages_compact": [cp, i32, vp, vp, i32, i32, vp, vp, vp, vp, vp, sz, vp],
         "sv_pages_compact_ex": [cp, i32, vp, vp, i32, i32, vp, vp, vp, vp, vp, vp, sz, vp],
+        "sv_latent_append": [cp, vp, i64, vp, i64, vp, i64, vp],
+        "sv_latent_gather": [cp, vp, vp, i32, i32, vp, vp, i64, vp, i64, vp, i64, vp],
+        "sv_latent_attention": [cp, vp, i32, vp, i32, vp, vp, i32, i32, f32, vp, vp, vp, sz, vp],
+        "sv_expanded_attention": [vp, i32, vp, i32, vp, i64, i64, vp, i64, vp, i64, i64, vp, i32, i32, i32, f32, vp, vp, vp,
+                                  sz, vp],
         "sv_get_device_error": [ctypes.POINTER(ctypes.c_uint32), ctypes.c_int],
     }
     for name, args in sig.items():
@@ -94,6 +99,10 @@ def _load():
     lib.sv_prefix_decode_workspace_size.restype = sz
     lib.sv_pages_workspace_size.argtypes = [i64, i32, i32]
     lib.sv_pages_workspace_size.restype = sz
+    lib.sv_latent_attention_workspace_size.argtypes = [i32, i32, i32]
+    lib.sv_latent_attention_workspace_size.restype = sz
+    lib.sv_expanded_attention_workspace_size.argtypes = [i32, i32, i32]
+    lib.sv_expanded_attention_workspace_size.restype = sz
     lib.sv_status_string.argtypes = [ctypes.c_int]
     lib.sv_status_string.restype = ctypes.c_char_p
     lib.sv_version.argtypes = []
@@ -494,6 +503,142 @@ def sv_pages_compact(caches, page_table: torch.Tensor, seq_lens: torch.Tensor, r
         _at(page_table_out, _I32, "page_table_out", dev), _at(ref_counts_out, _I32, "ref_counts_out", dev),
         _at(num_live, _I32, "num_live", dev), _at(page_map, _I32, "page_map", dev),
         _at(workspace, None, "workspace", dev), workspace.nbytes, _on(stream, dev)))
+
+
+LATENT_DIM, ROPE_DIM = 512, 64
+
+
+class LatentCache:
+    """A paged pool of latents on the device: latent [pages][16][512] (bf16, or uint8 e4m3 codes with one fp32 scale a
+    token, scale [pages][16]) and rope bf16 [pages][16][64].  The sv_pages_* calls and CacheList take it as any cache."""
+
+    def __init__(self, latent: torch.Tensor, rope: torch.Tensor, scale: Optional[torch.Tensor] = None):
+        self.latent, self.rope, self.scale = latent, rope, scale
+        n, p, d = latent.shape
+        fp8 = latent.dtype == torch.uint8
+        if (p, d) != (16, LATENT_DIM):
+            raise ValueError(f"latent must have shape [pages, 16, {LATENT_DIM}], got {tuple(latent.shape)}")
+        _shape(rope, (n, 16, ROPE_DIM), "rope")
+        _p(latent, torch.uint8 if fp8 else _BF16, "latent")
+        _p(rope, _BF16, "rope")
+        if fp8 != (scale is not None):
+            raise ValueError("e4m3 latents need scale, bf16 ones have none")
+        if fp8:
+            _shape(scale, (n, 16), "scale")
+            _p(scale, _F32, "scale")
+        if len({t.get_device() for t in (latent, rope, scale) if t is not None}) > 1:
+            raise ValueError("a cache's tensors must be on one device")
+        self.c = sv_cache(latent.data_ptr(), rope.data_ptr(), None, n, 1, p, d,
+                          SV_KV_LATENT_E4M3 if fp8 else SV_KV_LATENT_BF16, scale.data_ptr() if fp8 else None, None)
+
+    @classmethod
+    def empty(cls, num_phys_pages: int, fp8: bool = False, device="cuda") -> "LatentCache":
+        shape = (num_phys_pages, 16)
+        latent = torch.zeros((*shape, LATENT_DIM), dtype=torch.uint8 if fp8 else _BF16, device=device)
+        rope = torch.zeros((*shape, ROPE_DIM), dtype=_BF16, device=device)
+        return cls(latent, rope, torch.zeros(shape, dtype=_F32, device=device) if fp8 else None)
+
+    @property
+    def k_pool(self) -> torch.Tensor:
+        return self.latent
+
+    def ref(self):
+        return ctypes.byref(self.c)
+
+
+def _strided(t: torch.Tensor, shape, name: str, dev: int):
+    """The address and the element strides of all dimensions but the last, which is contiguous.  A dimension of one (or
+    of none) has no stride to speak of: it gets that of a packed tensor."""
+    _shape(t, shape, name)
+    if t.get_device() != dev or t.dtype is not _BF16:
+        _at(t.reshape(-1)[:0], _BF16, name, dev)
+    if t.numel() and t.stride(-1) != 1:
+        raise ValueError(f"{name} must be contiguous in its last dimension")
+    strides, packed = [], shape[-1]
+    for n, s in zip(reversed(shape[:-1]), reversed(t.stride()[:-1])):
+        strides.append(s if n > 1 else packed)
+        packed *= max(n, 1)
+    return (t.data_ptr(), *reversed(strides))
+
+
+def sv_latent_append(cache: LatentCache, latent: torch.Tensor, rope: torch.Tensor, slot_mapping: torch.Tensor,
+                     stream=None) -> None:
+    """latent [T][512] and rope [T][64], rows of any stride, to the slots of the pool."""
+    n = slot_mapping.numel()
+    dev = torch.cuda.current_device()
+    _at(cache.latent, None, "the cache", dev)
+    _check("sv_latent_append", _load().sv_latent_append(
+        cache.ref(), *_strided(latent, (n, LATENT_DIM), "latent", dev), *_strided(rope, (n, ROPE_DIM), "rope", dev),
+        _at(slot_mapping, _I32, "slot_mapping", dev), n, _on(stream, dev)))
+
+
+def sv_latent_gather(cache: LatentCache, page_table: torch.Tensor, seq_lens: torch.Tensor, row_start: torch.Tensor,
+                     latent: torch.Tensor, rope: torch.Tensor, first_token: Optional[torch.Tensor] = None,
+                     stream=None) -> None:
+    """Rows row_start[b] .. row_start[b + 1] - 1 of latent [N][512] and rope [N][64] get request b's tokens from
+    first_token[b] (0) on."""
+    B, max_pages = page_table.shape
+    N = latent.shape[0]
+    _shape(seq_lens, (B,), "seq_lens")
+    _shape(row_start, (B + 1,), "row_start")
+    if first_token is not None:
+        _shape(first_token, (B,), "first_token")
+    dev = torch.cuda.current_device()
+    _at(cache.latent, None, "the cache", dev)
+    _check("sv_latent_gather", _load().sv_latent_gather(
+        cache.ref(), _at(page_table, _I32, "page_table", dev), _at(seq_lens, _I32, "seq_lens", dev), B, max_pages,
+        _at(row_start, _I32, "row_start", dev), _at(first_token, _I32, "first_token", dev), N,
+        *_strided(latent, (N, LATENT_DIM), "latent", dev), *_strided(rope, (N, ROPE_DIM), "rope", dev), _on(stream, dev)))
+
+
+def sv_latent_attention_workspace_size(batch: int, num_q_heads: int, total_q: int) -> int:
+    return int(_load().sv_latent_attention_workspace_size(batch, num_q_heads, total_q))
+
+
+def sv_latent_attention(cache: LatentCache, q: torch.Tensor, page_table: torch.Tensor, seq_lens: torch.Tensor,
+                        out: torch.Tensor, lse: torch.Tensor, workspace: torch.Tensor, softmax_scale: float,
+                        q_start: Optional[torch.Tensor] = None, stream=None) -> None:
+    """q [total_q][Hq][576], out [total_q][Hq][512], lse [total_q][Hq]; q_start None: one token a request."""
+    T, Hq, D = q.shape
+    B, max_pages = page_table.shape
+    if D != LATENT_DIM + ROPE_DIM:
+        raise ValueError(f"q must have {LATENT_DIM + ROPE_DIM} channels, got {D}")
+    _shape(seq_lens, (B,), "seq_lens")
+    _shape(out, (T, Hq, LATENT_DIM), "out")
+    _shape(lse, (T, Hq), "lse")
+    if q_start is not None:
+        _shape(q_start, (B + 1,), "q_start")
+    dev = torch.cuda.current_device()
+    _at(cache.latent, None, "the cache", dev)
+    _check("sv_latent_attention", _load().sv_latent_attention(
+        cache.ref(), _at(q, _BF16, "q", dev), Hq, _at(q_start, _I32, "q_start", dev), T,
+        _at(page_table, _I32, "page_table", dev), _at(seq_lens, _I32, "seq_lens", dev), B, max_pages, softmax_scale,
+        _at(out, _BF16, "out", dev), _at(lse, _F32, "lse", dev), _at(workspace, None, "workspace", dev), workspace.nbytes,
+        _on(stream, dev)))
+
+
+def sv_expanded_attention_workspace_size(batch: int, num_heads: int, total_q: int) -> int:
+    return int(_load().sv_expanded_attention_workspace_size(batch, num_heads, total_q))
+
+
+def sv_expanded_attention(q: torch.Tensor, k: torch.Tensor, rope: torch.Tensor, v: torch.Tensor, q_start: torch.Tensor,
+                          kv_start: torch.Tensor, out: torch.Tensor, lse: torch.Tensor, workspace: torch.Tensor,
+                          causal: bool = True, softmax_scale: Optional[float] = None, stream=None) -> None:
+    """q [total_q][H][192]; k, v [total_kv][H][128] and rope [total_kv][64], of any strides; out [total_q][H][128],
+    lse [total_q][H]."""
+    T, H, D = q.shape
+    S, B = rope.shape[0], q_start.numel() - 1
+    if D != 128 + ROPE_DIM:
+        raise ValueError(f"q must have {128 + ROPE_DIM} channels, got {D}")
+    _shape(kv_start, (B + 1,), "kv_start")
+    _shape(out, (T, H, 128), "out")
+    _shape(lse, (T, H), "lse")
+    dev = torch.cuda.current_device()
+    _check("sv_expanded_attention", _load().sv_expanded_attention(
+        _at(q, _BF16, "q", dev), H, _at(q_start, _I32, "q_start", dev), T, *_strided(k, (S, H, 128), "k", dev),
+        *_strided(rope, (S, ROPE_DIM), "rope", dev), *_strided(v, (S, H, 128), "v", dev), _at(kv_start, _I32, "kv_start", dev),
+        S, B, int(causal), D ** -0.5 if softmax_scale is None else softmax_scale, _at(out, _BF16, "out", dev),
+        _at(lse, _F32, "lse", dev), _at(workspace, None, "workspace", dev), workspace.nbytes, _on(stream, dev)))
 
 
 def sv_get_device_error(reset: bool = True) -> int:

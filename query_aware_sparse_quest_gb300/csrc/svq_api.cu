@@ -28,6 +28,24 @@ int read_error_decode_fp8(uint32_t* flags, int reset);
 int read_error_attend(uint32_t* flags, int reset);
 int read_error_window_decode(uint32_t* flags, int reset);
 int read_error_pages(uint32_t* flags, int reset);
+int read_error_latent(uint32_t* flags, int reset);
+int read_error_latent_attend(uint32_t* flags, int reset);
+int read_error_expanded(uint32_t* flags, int reset);
+int launch_latent_append(const sv_cache* c, const void* latent, int64_t latent_stride, const void* rope,
+                         int64_t rope_stride, const int32_t* slot_mapping, int64_t num_tokens, cudaStream_t stream);
+int launch_latent_gather(const sv_cache* c, const int32_t* page_table, const int32_t* seq_lens, int batch, int max_pages,
+                         const int32_t* row_start, const int32_t* first_token, int64_t total_rows, void* latent,
+                         int64_t latent_stride, void* rope, int64_t rope_stride, int sm_count, cudaStream_t stream);
+size_t latent_workspace_bytes(int batch, int num_q_heads, int total_q);
+int launch_latent_attention(const sv_cache* c, const void* q, int num_q_heads, const int32_t* q_start, int total_q,
+                            const int32_t* page_table, const int32_t* seq_lens, int batch, int max_pages,
+                            float softmax_scale, void* out, float* lse, void* workspace, int sm_count,
+                            cudaStream_t stream);
+size_t expanded_workspace_bytes(int batch, int num_heads, int total_q);
+int launch_expanded(const void* q, int num_heads, const int32_t* q_start, int total_q, const void* k, int64_t k_stride,
+                    int64_t k_head_stride, const void* rope, int64_t rope_stride, const void* v, int64_t v_stride,
+                    int64_t v_head_stride, const int32_t* kv_start, int total_kv, int batch, bool causal,
+                    float softmax_scale, void* out, float* lse, void* workspace, int sm_count, cudaStream_t stream);
 size_t pages_workspace_bytes(int64_t num_pages, int num_rows, int n);
 int launch_pages_copy(const sv_cache* caches, int num_caches, const int32_t* src, const int32_t* dst, int n,
                       cudaStream_t stream);
@@ -77,8 +95,13 @@ int sm_count_of_current_device(int* out) {
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
+// Slots (page * 16 + offset) are 32-bit.
+constexpr int64_t kMaxPoolPages = 1ll << 27;
+
 int check_cache(const sv_cache* c) {
-    if (!c || !c->k_pool || !c->v_pool || !c->meta) return SV_ERR_INVALID_ARG;
+    if (!c || !c->k_pool || !c->v_pool) return SV_ERR_INVALID_ARG;
+    if (is_latent(c)) return SV_ERR_UNSUPPORTED;
+    if (!c->meta) return SV_ERR_INVALID_ARG;
     if (c->num_phys_pages < 1 || c->num_kv_heads < 1) return SV_ERR_INVALID_ARG;
     if (c->num_phys_pages > INT_MAX) return SV_ERR_UNSUPPORTED;
     if (c->page_size != kPage || c->head_dim != kHeadDim) return SV_ERR_UNSUPPORTED;
@@ -87,6 +110,17 @@ int check_cache(const sv_cache* c) {
     if (c->kv_format == SV_KV_FP8_E4M3 && (!c->k_scale || !c->v_scale || !aligned16(c->k_scale) ||
                                            !aligned16(c->v_scale)))
         return SV_ERR_INVALID_ARG;
+    return SV_OK;
+}
+
+int check_latent_cache(const sv_cache* c) {
+    if (!c || !c->k_pool || !c->v_pool) return SV_ERR_INVALID_ARG;
+    if (!is_latent(c)) return SV_ERR_UNSUPPORTED;
+    if (c->num_phys_pages < 1) return SV_ERR_INVALID_ARG;
+    if (c->num_phys_pages >= kMaxPoolPages) return SV_ERR_UNSUPPORTED;
+    if (c->page_size != kPage || c->head_dim != kLatentDim || c->num_kv_heads != 1) return SV_ERR_UNSUPPORTED;
+    if (!aligned16(c->k_pool) || !aligned16(c->v_pool)) return SV_ERR_INVALID_ARG;
+    if (c->kv_format == SV_KV_LATENT_E4M3 && (!c->k_scale || !aligned16(c->k_scale))) return SV_ERR_INVALID_ARG;
     return SV_OK;
 }
 
@@ -351,14 +385,29 @@ int attend_checks(const sv_cache* cache, const void* q, int num_q_heads, const i
     return SV_OK;
 }
 
-// Slots (page * 16 + offset) are 32-bit.
-constexpr int64_t kMaxPoolPages = 1ll << 27;
+constexpr int kMaxLatentHeads = 128;
+constexpr int kMaxKvRows = 1 << 30;   // positions are 32-bit
+
+// Query rows (token, head) of one call are 32-bit.
+bool rows_ok(int batch, int heads, int most_heads, int total_q) {
+    return batch >= 1 && batch <= 65535 && heads >= 1 && heads <= most_heads && total_q >= 0 &&
+           total_q <= kMaxQueryTokens && static_cast<int64_t>(total_q) * heads < INT_MAX;
+}
+
+// Elements between rows that are read 16 bytes at a time; tensor maps hold strides below 2^40 bytes.
+bool stride_ok(int64_t stride, int width) { return stride >= width && stride % 8 == 0 && stride < 1ll << 36; }
+
+int check_latent_rows(const void* latent, int64_t latent_stride, const void* rope, int64_t rope_stride, int64_t rows) {
+    if (!latent || !rope || !aligned16(latent) || !aligned16(rope)) return SV_ERR_INVALID_ARG;
+    if (!stride_ok(latent_stride, kLatentDim) || !stride_ok(rope_stride, kRopeDim)) return SV_ERR_INVALID_ARG;
+    return rows <= INT_MAX ? SV_OK : SV_ERR_UNSUPPORTED;
+}
 
 int check_caches(const sv_cache* caches, int n) {
     if (!caches || n < 1) return SV_ERR_INVALID_ARG;
     if (n > SV_MAX_CACHES) return SV_ERR_UNSUPPORTED;
     for (int i = 0; i < n; ++i) {
-        const int st = check_cache(caches + i);
+        const int st = is_latent(caches + i) ? check_latent_cache(caches + i) : check_cache(caches + i);
         if (st) return st;
         if (caches[i].num_phys_pages != caches[0].num_phys_pages) return SV_ERR_INVALID_ARG;
     }
@@ -549,6 +598,90 @@ int sv_pages_compact(const sv_cache* caches, int32_t num_caches, const int32_t* 
                                ref_counts_out, num_live, nullptr, workspace, workspace_bytes, stream);
 }
 
+int sv_latent_append(const sv_cache* cache, const void* latent, int64_t latent_stride, const void* rope,
+                     int64_t rope_stride, const int32_t* slot_mapping, int64_t num_tokens, void* stream) {
+    int st = check_latent_cache(cache);
+    if (st) return st;
+    if (num_tokens < 0) return SV_ERR_INVALID_ARG;
+    if (num_tokens == 0) return SV_OK;
+    if (!slot_mapping) return SV_ERR_INVALID_ARG;
+    if ((st = check_latent_rows(latent, latent_stride, rope, rope_stride, num_tokens))) return st;
+    return launch_latent_append(cache, latent, latent_stride, rope, rope_stride, slot_mapping, num_tokens,
+                                static_cast<cudaStream_t>(stream));
+}
+
+int sv_latent_gather(const sv_cache* cache, const int32_t* page_table, const int32_t* seq_lens, int32_t batch,
+                     int32_t max_pages, const int32_t* row_start, const int32_t* first_token, int64_t total_rows,
+                     void* latent, int64_t latent_stride, void* rope, int64_t rope_stride, void* stream) {
+    int st = check_latent_cache(cache);
+    if (st) return st;
+    if (total_rows < 0) return SV_ERR_INVALID_ARG;
+    if (total_rows == 0) return SV_OK;
+    if (!page_table || !seq_lens || !row_start || batch < 1 || max_pages < 1) return SV_ERR_INVALID_ARG;
+    if (batch > 65535 || max_pages >= kMaxRowPages || total_rows > INT_MAX) return SV_ERR_UNSUPPORTED;
+    if ((st = check_latent_rows(latent, latent_stride, rope, rope_stride, total_rows))) return st;
+    int sms = 0;
+    if ((st = sm_count_of_current_device(&sms))) return st;
+    return launch_latent_gather(cache, page_table, seq_lens, batch, max_pages, row_start, first_token, total_rows, latent,
+                                latent_stride, rope, rope_stride, sms, static_cast<cudaStream_t>(stream));
+}
+
+size_t sv_latent_attention_workspace_size(int32_t batch, int32_t num_q_heads, int32_t total_q) {
+    if (!rows_ok(batch, num_q_heads, kMaxLatentHeads, total_q)) return 0;
+    return latent_workspace_bytes(batch, num_q_heads, total_q);
+}
+
+int sv_latent_attention(const sv_cache* cache, const void* q, int32_t num_q_heads, const int32_t* q_start,
+                        int32_t total_q, const int32_t* page_table, const int32_t* seq_lens, int32_t batch,
+                        int32_t max_pages, float softmax_scale, void* out, float* lse, void* workspace,
+                        size_t workspace_bytes, void* stream) {
+    int st = check_latent_cache(cache);
+    if (st) return st;
+    if (num_q_heads < 1 || batch < 1 || total_q < 0) return SV_ERR_INVALID_ARG;
+    if (!rows_ok(batch, num_q_heads, kMaxLatentHeads, total_q)) return SV_ERR_UNSUPPORTED;
+    if (q_start && total_q == 0) return SV_OK;   // nothing to do; an empty tensor has no address
+    if ((st = check_batch(q, page_table, seq_lens, batch, max_pages))) return st;
+    if (max_pages >= kMaxRowPages) return SV_ERR_UNSUPPORTED;
+    if (!out || !lse || !aligned16(out)) return SV_ERR_INVALID_ARG;
+    if (!(softmax_scale > 0.f) || softmax_scale == INFINITY) return SV_ERR_INVALID_ARG;
+    if (!q_start && total_q != batch) return SV_ERR_INVALID_ARG;
+    if (!workspace || workspace_bytes < latent_workspace_bytes(batch, num_q_heads, total_q)) return SV_ERR_WORKSPACE;
+    if (!aligned16(workspace)) return SV_ERR_INVALID_ARG;
+    int sms = 0;
+    if ((st = sm_count_of_current_device(&sms))) return st;
+    return launch_latent_attention(cache, q, num_q_heads, q_start, total_q, page_table, seq_lens, batch, max_pages,
+                                   softmax_scale, out, lse, workspace, sms, static_cast<cudaStream_t>(stream));
+}
+
+size_t sv_expanded_attention_workspace_size(int32_t batch, int32_t num_heads, int32_t total_q) {
+    if (!rows_ok(batch, num_heads, 65535, total_q)) return 0;
+    return expanded_workspace_bytes(batch, num_heads, total_q);
+}
+
+int sv_expanded_attention(const void* q, int32_t num_heads, const int32_t* q_start, int32_t total_q, const void* k,
+                          int64_t k_stride, int64_t k_head_stride, const void* rope, int64_t rope_stride,
+                          const void* v, int64_t v_stride, int64_t v_head_stride, const int32_t* kv_start,
+                          int32_t total_kv, int32_t batch, int32_t causal, float softmax_scale, void* out, float* lse,
+                          void* workspace, size_t workspace_bytes, void* stream) {
+    if (num_heads < 1 || batch < 1 || total_q < 0 || total_kv < 0) return SV_ERR_INVALID_ARG;
+    if (!rows_ok(batch, num_heads, 65535, total_q) || total_kv > kMaxKvRows) return SV_ERR_UNSUPPORTED;
+    if (total_q == 0) return SV_OK;
+    if (!q || !q_start || !kv_start || !out || !lse || !aligned16(q)) return SV_ERR_INVALID_ARG;
+    if (reinterpret_cast<uintptr_t>(out) & 31u) return SV_ERR_INVALID_ARG;   // rows are written 32 bytes at a time
+    if (total_kv > 0 && (!k || !rope || !v || !aligned16(k) || !aligned16(rope) || !aligned16(v))) return SV_ERR_INVALID_ARG;
+    if (!stride_ok(k_stride, kHeadDim) || !stride_ok(k_head_stride, kHeadDim) || !stride_ok(v_stride, kHeadDim) ||
+        !stride_ok(v_head_stride, kHeadDim) || !stride_ok(rope_stride, kRopeDim))
+        return SV_ERR_INVALID_ARG;
+    if (!(softmax_scale > 0.f) || softmax_scale == INFINITY) return SV_ERR_INVALID_ARG;
+    if (!workspace || workspace_bytes < expanded_workspace_bytes(batch, num_heads, total_q)) return SV_ERR_WORKSPACE;
+    if (!aligned16(workspace)) return SV_ERR_INVALID_ARG;
+    int sms = 0, st;
+    if ((st = sm_count_of_current_device(&sms))) return st;
+    return launch_expanded(q, num_heads, q_start, total_q, k, k_stride, k_head_stride, rope, rope_stride, v, v_stride,
+                           v_head_stride, kv_start, total_kv, batch, causal != 0, softmax_scale, out, lse, workspace, sms,
+                           static_cast<cudaStream_t>(stream));
+}
+
 int sv_get_device_error(uint32_t* flags, int reset) {
     if (!flags) return SV_ERR_INVALID_ARG;
     *flags = 0;
@@ -559,6 +692,9 @@ int sv_get_device_error(uint32_t* flags, int reset) {
     if ((st = read_error_attend(flags, reset))) return st;
     if ((st = read_error_window_decode(flags, reset))) return st;
     if ((st = read_error_pages(flags, reset))) return st;
+    if ((st = read_error_latent(flags, reset))) return st;
+    if ((st = read_error_latent_attend(flags, reset))) return st;
+    if ((st = read_error_expanded(flags, reset))) return st;
     return read_error_decode(flags, reset);
 }
 
@@ -573,6 +709,6 @@ const char* sv_status_string(int status) {
     }
 }
 
-int sv_version(void) { return 110; }
+int sv_version(void) { return 120; }
 
 }  // extern "C"

@@ -17,6 +17,10 @@ namespace svq {
 constexpr int kPage = 16;      // tokens per page
 constexpr int kHeadDim = 128;  // channels per head
 constexpr int kMaxGroup = 8;   // query heads per kv head handled by one MMA n-tile
+constexpr int kLatentDim = 512;  // channels of a cached latent
+constexpr int kRopeDim = 64;     // and of its rotary key
+
+inline bool is_latent(const sv_cache* c) { return c->kv_format == SV_KV_LATENT_BF16 || c->kv_format == SV_KV_LATENT_E4M3; }
 
 // ---------------------------------------------------------------- error word
 // Each translation unit owns one device word; the host reads and clears it

@@ -44,9 +44,10 @@ struct CacheDesc {
     unsigned char* v;
     unsigned char* meta;
     unsigned char* k_scale;   // null for bf16 pools
-    unsigned char* v_scale;
-    int heads;
-    int row_chunks;           // 16-byte chunks of a page of one kv head: 256 (bf16) or 128 (e4m3)
+    unsigned char* v_scale;   // null for latents too
+    int k_chunks, v_chunks;   // 16-byte chunks of a page
+    int meta_chunks;          // 0 for latents
+    int scale_chunks;
 };
 struct CacheSet {
     CacheDesc c[SV_MAX_CACHES];
@@ -170,7 +171,13 @@ __device__ __forceinline__ void copy_span(unsigned char* base, int64_t src, int6
     for (int i = threadIdx.x; i < chunks; i += kMoveThreads) d[i] = ld_stream_v4(s + i);
 }
 __device__ __forceinline__ void copy_page(const CacheDesc& c, int64_t src, int64_t dst) {
-    const int chunks = c.heads * c.row_chunks;
+    if (c.v_chunks != c.k_chunks) {   // latents and their rotary keys
+        copy_span(c.k, src, dst, c.k_chunks);
+        copy_span(c.v, src, dst, c.v_chunks);
+        if (c.k_scale) copy_span(c.k_scale, src, dst, c.scale_chunks);
+        return;
+    }
+    const int chunks = c.k_chunks;
     const uint4* ks = reinterpret_cast<const uint4*>(c.k) + src * chunks;
     const uint4* vs = reinterpret_cast<const uint4*>(c.v) + src * chunks;
     uint4* kd = reinterpret_cast<uint4*>(c.k) + dst * chunks;
@@ -194,10 +201,10 @@ __device__ __forceinline__ void copy_page(const CacheDesc& c, int64_t src, int64
             }
         }
     }
-    copy_span(c.meta, src, dst, c.heads * 32);
+    copy_span(c.meta, src, dst, c.meta_chunks);
     if (c.k_scale) {
-        copy_span(c.k_scale, src, dst, c.heads * 4);
-        copy_span(c.v_scale, src, dst, c.heads * 4);
+        copy_span(c.k_scale, src, dst, c.scale_chunks);
+        copy_span(c.v_scale, src, dst, c.scale_chunks);
     }
 }
 
@@ -701,11 +708,22 @@ void fill_set(CacheSet* set, const sv_cache* caches, int n) {
     set->n = n;
     for (int i = 0; i < n; ++i) {
         const sv_cache& c = caches[i];
-        const bool fp8 = c.kv_format == SV_KV_FP8_E4M3;
-        set->c[i] = CacheDesc{static_cast<unsigned char*>(c.k_pool), static_cast<unsigned char*>(c.v_pool),
-                              static_cast<unsigned char*>(c.meta),
-                              fp8 ? static_cast<unsigned char*>(c.k_scale) : nullptr,
-                              fp8 ? static_cast<unsigned char*>(c.v_scale) : nullptr, c.num_kv_heads, fp8 ? 128 : 256};
+        const bool fp8 = c.kv_format == SV_KV_FP8_E4M3 || c.kv_format == SV_KV_LATENT_E4M3;
+        CacheDesc& d = set->c[i];
+        d = CacheDesc{};
+        d.k = static_cast<unsigned char*>(c.k_pool);
+        d.v = static_cast<unsigned char*>(c.v_pool);
+        d.scale_chunks = c.num_kv_heads * 4;
+        if (fp8) d.k_scale = static_cast<unsigned char*>(c.k_scale);
+        if (is_latent(&c)) {
+            d.k_chunks = kPage * kLatentDim * (fp8 ? 1 : 2) / 16;
+            d.v_chunks = kPage * kRopeDim * 2 / 16;
+        } else {
+            d.k_chunks = d.v_chunks = c.num_kv_heads * (fp8 ? 128 : 256);
+            d.meta = static_cast<unsigned char*>(c.meta);
+            d.meta_chunks = c.num_kv_heads * 32;
+            if (fp8) d.v_scale = static_cast<unsigned char*>(c.v_scale);
+        }
     }
 }
 
