@@ -613,7 +613,7 @@ size_t sv_latent_attention_workspace_size(int32_t batch, int32_t num_q_heads, in
  *    written.  total_q == 0 launches nothing.
  *  - Rows of k, rope and v that a query token does not see may hold anything, as
  *    in sv_window_attention.
- *  - workspace as above.  total_q * num_heads < 2^31, num_heads <= 65535.
+ *  - workspace as above.  total_q * num_heads < 2^31, batch * num_heads <= 2^24.
  */
 int sv_expanded_attention(const void* q, int32_t num_heads, const int32_t* q_start, int32_t total_q, const void* k,
                           int64_t k_stride, int64_t k_head_stride, const void* rope, int64_t rope_stride,

@@ -391,7 +391,8 @@ constexpr int kMaxKvRows = 1 << 30;   // positions are 32-bit
 // Query rows (token, head) of one call are 32-bit.
 bool rows_ok(int batch, int heads, int most_heads, int total_q) {
     return batch >= 1 && batch <= 65535 && heads >= 1 && heads <= most_heads && total_q >= 0 &&
-           total_q <= kMaxQueryTokens && static_cast<int64_t>(total_q) * heads < INT_MAX;
+           total_q <= kMaxQueryTokens && static_cast<int64_t>(total_q) * heads < INT_MAX &&
+           static_cast<int64_t>(batch) * heads <= kMaxQueryTokens;
 }
 
 // Elements between rows that are read 16 bytes at a time; tensor maps hold strides below 2^40 bytes.

@@ -53,7 +53,7 @@
 // 38 to 40 us and 42 to 44, of which these tiles 21 to 25.
 #include <climits>
 
-#include "svq_paged.cuh"
+#include "svq_fold.cuh"
 
 namespace svq {
 
@@ -214,17 +214,6 @@ __device__ __forceinline__ GroupAt warp_groups(const Groups& gr, int tok_per_ent
 constexpr uint32_t kIdescQK = (1u << 4) | (1u << 7) | (1u << 10) | ((128u / 8) << 17) | ((128u / 16) << 24);
 constexpr uint32_t kIdescPV = kIdescQK | (1u << 16);
 
-// Descriptors differ in their low words only; the high words (stride, version,
-// swizzle) are constants.  Eight k steps are issued from one statement, so that
-// the issuing thread keeps ahead of the tensor pipe (64 cycles a step): with a
-// descriptor built for each step it fell behind it.
-constexpr uint32_t desc_hi(uint32_t sbo) { return (sbo >> 4) | (1u << 14) | (2u << 29); }
-__device__ __forceinline__ uint32_t desc_lo(uint32_t addr, uint32_t lbo) { return (addr >> 4) | (lbo >> 4 << 16); }
-
-#define SVQ_MMA_SS(ao, bo, acc)                                                  \
-    "add.u32 al, %1, " #ao ";\n\tadd.u32 bl, %2, " #bo ";\n\t"                   \
-    "mov.b64 ad, {al, %3};\n\tmov.b64 bd, {bl, %4};\n\t"                         \
-    "tcgen05.mma.cta_group::1.kind::f16 [%0], ad, bd, %5, " #acc ";\n\t"
 // S = Q K^T: channels 16 k .. of both operands are 32 bytes further in a half's
 // rows (2 in the descriptor); the second half is 16 KB (Q) and 1 KB (K) on.
 __device__ __forceinline__ void mma_qk(uint32_t d, uint32_t q_lo, uint32_t k_lo, uint32_t idesc) {
@@ -236,10 +225,6 @@ __device__ __forceinline__ void mma_qk(uint32_t d, uint32_t q_lo, uint32_t k_lo,
         "}" ::"r"(d), "r"(q_lo), "r"(k_lo), "r"(desc_hi(1024)), "r"(desc_hi(2048)), "r"(idesc)
         : "memory");
 }
-#define SVQ_MMA_TS(ao, bo, acc)                                                  \
-    "add.u32 al, %1, " #ao ";\n\tadd.u32 bl, %2, " #bo ";\n\t"                   \
-    "mov.b64 bd, {bl, %3};\n\t"                                                  \
-    "tcgen05.mma.cta_group::1.kind::f16 [%0], [al], bd, %4, " #acc ";\n\t"
 // O (+)= P V over a whole tile: one step a page (8 TMEM columns, 4 KB).
 __device__ __forceinline__ void mma_pv8(uint32_t d, uint32_t p, uint32_t v_lo, uint32_t idesc, uint32_t acc) {
     asm volatile(
@@ -257,82 +242,12 @@ __device__ __forceinline__ void mma_pv1(uint32_t d, uint32_t p, uint32_t v_lo, u
         "}" ::"r"(d), "r"(p), "r"(v_lo), "r"(desc_hi(2048)), "r"(idesc), "r"(acc)
         : "memory");
 }
-__device__ __forceinline__ void mma_commit(uint32_t bar) {
-    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
-}
-__device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
-__device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
-__device__ __forceinline__ void tc_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
-__device__ __forceinline__ void tc_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
-
-__device__ __forceinline__ void tc_ld32(uint32_t addr, uint32_t (&r)[32]) {
-    asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
-        "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
-        "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
-        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
-          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
-          "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
-          "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
-        : "r"(addr));
-}
-__device__ __forceinline__ void tc_ld16(uint32_t addr, uint32_t (&r)[16]) {
-    asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
-        "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
-        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
-          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
-        : "r"(addr));
-}
-// Two fp32 values in one 64-bit register, for the paired fp32 instructions.
-__device__ __forceinline__ uint64_t pack2(float lo, float hi) {
-    uint64_t r;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
-    return r;
-}
-__device__ __forceinline__ void unpack2(uint64_t v, float& lo, float& hi) {
-    asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
-}
-__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
-    uint64_t r;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-    return r;
-}
-__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
-    uint64_t r;
-    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-    return r;
-}
-__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
-    uint64_t r;
-    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-    return r;
-}
-__device__ __forceinline__ void tc_st16(uint32_t addr, const uint32_t (&r)[16]) {
-    asm volatile(
-        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
-        "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(addr),
-        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
-        "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
-        : "memory");
-}
 __device__ __forceinline__ void tma_load_4d(uint32_t dst, const void* tmap, int y, uint32_t bar) {
     asm volatile(
         "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %2, %2, %3}], [%4];"
         ::"r"(dst), "l"(tmap), "r"(0), "r"(y), "r"(bar)
         : "memory");
 }
-// 32 bytes of one thread, a whole sector: rows are written a thread each.
-__device__ __forceinline__ void st_v8(void* p, uint32_t a, uint32_t b, uint32_t c, uint32_t d, uint32_t e, uint32_t f,
-                                      uint32_t g, uint32_t h) {
-    asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(a), "r"(b), "r"(c), "r"(d), "r"(e),
-                 "r"(f), "r"(g), "r"(h)
-                 : "memory");
-}
-template <int N>
-__device__ __forceinline__ void reg_dec() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
-template <int N>
-__device__ __forceinline__ void reg_inc() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
 // ---------------------------------------------------------------- shared memory
 template <bool FP8>
 struct Cfg {
@@ -394,121 +309,15 @@ __device__ __forceinline__ int load_tile(int i, int n) {
     return load_is_k(i, n) ? (i + 1) / 2 : (i == 2 * n - 1 ? n - 1 : i / 2 - 1);
 }
 
-// Four e4m3 codes -> two bf16 pairs, exactly: the code's exponent and mantissa
-// fields are moved under bf16's, which scales the value by 2^-120; the product
-// with 2^120 is exact, subnormal codes included.  The two NaN codes would read
-// as +-480: see has_nan.
-__device__ __forceinline__ void widen4(uint32_t c, uint32_t& lo, uint32_t& hi) {
-    const uint32_t a = __byte_perm(c, 0u, 0x1404);   // bytes 1, 0 of c in the high bytes of the halves
-    const uint32_t b = __byte_perm(c, 0u, 0x3424);
-    const uint32_t x = ((a & 0x7f007f00u) >> 4) | (a & 0x80008000u);
-    const uint32_t y = ((b & 0x7f007f00u) >> 4) | (b & 0x80008000u);
-    const __nv_bfloat162 two120 = __halves2bfloat162(__ushort_as_bfloat16(0x7b80), __ushort_as_bfloat16(0x7b80));
-    const __nv_bfloat162 xr = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&x), two120);
-    const __nv_bfloat162 yr = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&y), two120);
-    lo = *reinterpret_cast<const uint32_t*>(&xr);
-    hi = *reinterpret_cast<const uint32_t*>(&yr);
-}
-// Bit 7 of every byte of c that is a NaN code (0x7f or 0xff).
-__device__ __forceinline__ uint32_t has_nan(uint32_t c) { return ((c & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u; }
-__device__ __forceinline__ void keep_nan(uint32_t c, uint32_t& lo, uint32_t& hi) {
-    const uint32_t n = has_nan(c);
-    if (n & 0x00000080u) lo |= 0x00007fffu;
-    if (n & 0x00008000u) lo |= 0x7fff0000u;
-    if (n & 0x00800000u) hi |= 0x00007fffu;
-    if (n & 0x80000000u) hi |= 0x7fff0000u;
-}
 
-// Waits for a phase of an mbarrier, at most kPolls polls; false when it gave up.
-// A poll that finds the phase open takes 4 us on a GB300 (3.95 measured, whatever
-// time limit the instruction is given; with none named a chunk of 4096 tokens at
-// 32768 takes 1348 us instead of 1255), so that is after half a second; the waits
-// that this bounds are for copies and for other warps' work on a few tiles,
-// microseconds.  Few instructions, as every role's loop has several: the roles of
-// a CTA share the instruction caches.
-constexpr uint32_t kPolls = 1u << 17;
-constexpr uint32_t kPollNs = 1000;
 // The one wait that may be long is the scheduler's, for a slot whose segment is
 // done: 1.7 us a key tile, so 14 s for the 2^30 tokens that a row may have.  It
 // ends when another role gave up, and after so many rounds of kPolls (a minute).
 constexpr int kSegRounds = 128;
-__device__ __forceinline__ bool bar_wait(uint32_t bar, uint32_t parity) {
-    uint32_t ok;
-    asm volatile(
-        "{\n\t.reg .pred p, more;\n\t.reg .u32 i;\n\tmov.u32 i, 0;\n"
-        "again:\n\t"
-        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %4;\n\t"
-        "@p bra done;\n\t"
-        "add.u32 i, i, 1;\n\tsetp.lt.u32 more, i, %3;\n\t@more bra again;\n"
-        "done:\n\tselp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(ok)
-        : "r"(bar), "r"(parity), "n"(kPolls), "r"(kPollNs)
-        : "memory");
-    return ok != 0;
-}
 __device__ __forceinline__ void gave_up(Control* ct) {
     svq_flag(SV_DEVERR_TIMEOUT);
     *static_cast<volatile int*>(&ct->gave_up) = 1;
 }
-// The same by a whole warp; all of it leaves for `out` when it gave up.
-#define SVQ_WAIT(bar, parity, out)                                                        \
-    do {                                                                                  \
-        if (__any_sync(0xffffffffu, !bar_wait(smem_addr(&(bar)), (parity)))) {   \
-            if (lane == 0) gave_up(ct);                                                   \
-            goto out;                                                                     \
-        }                                                                                 \
-    } while (0)
-
-// A row's O so far goes to `to` and its sum to `held`, beside their base; `more`: onto what is there.  By whole
-// warps, a row a thread; threads without one (not `valid`) write nothing.
-__device__ __noinline__ void fold_out(uint32_t o_col, float* to, bool valid, bool more, float2& held, float m, float l) {
-    tc_fence_after();
-    const float f = !more || held.x == -INFINITY ? 0.f : ex2(held.x - m);   // bases only grow
-#pragma unroll 1
-    for (int c = 0; c < 8; ++c) {
-        uint32_t y[16];
-        tc_ld16(o_col + c * 16, y);
-        tc_wait_ld();
-        float4* const at = reinterpret_cast<float4*>(to + c * 16);
-#pragma unroll
-        for (int u = 0; u < 4 && valid; ++u) {
-            float4 v = make_float4(__uint_as_float(y[4 * u]), __uint_as_float(y[4 * u + 1]), __uint_as_float(y[4 * u + 2]),
-                                   __uint_as_float(y[4 * u + 3]));
-            if (more) {
-                const float4 x = at[u];
-                v = make_float4(fmaf(x.x, f, v.x), fmaf(x.y, f, v.y), fmaf(x.z, f, v.z), fmaf(x.w, f, v.w));
-            }
-            at[u] = v;
-        }
-    }
-    held = make_float2(m, more ? fmaf(held.y, f, l) : l);
-    tc_fence_before();
-}
-// The other way, at the segment's end: O gets what was folded; returns the whole sum.
-__device__ __noinline__ float fold_in(uint32_t o_col, const float* from, bool valid, const float2& held, float m, float l) {
-    tc_fence_after();
-    const float f = held.x == -INFINITY ? 0.f : ex2(held.x - m);
-#pragma unroll 1
-    for (int c = 0; c < 8; ++c) {
-        uint32_t y[16];
-        tc_ld16(o_col + c * 16, y);
-        tc_wait_ld();
-        const float4* const at = reinterpret_cast<const float4*>(from + c * 16);
-#pragma unroll
-        for (int u = 0; u < 4 && valid; ++u) {
-            const float4 x = at[u];
-            y[4 * u] = __float_as_uint(fmaf(x.x, f, __uint_as_float(y[4 * u])));
-            y[4 * u + 1] = __float_as_uint(fmaf(x.y, f, __uint_as_float(y[4 * u + 1])));
-            y[4 * u + 2] = __float_as_uint(fmaf(x.z, f, __uint_as_float(y[4 * u + 2])));
-            y[4 * u + 3] = __float_as_uint(fmaf(x.w, f, __uint_as_float(y[4 * u + 3])));
-        }
-        tc_st16(o_col + c * 16, y);
-    }
-    tc_wait_st();
-    tc_fence_before();
-    return fmaf(held.y, f, l);
-}
-
 template <bool FP8>
 __global__ void __launch_bounds__(Cfg<FP8>::kThreads, 1)
     attend_kernel(const __grid_constant__ AttendArgs a, const __grid_constant__ CUtensorMap tmap_k,
@@ -1392,32 +1201,6 @@ struct PlanArgs {
 
 constexpr int kPlanThreads = 1024;
 
-// Exclusive prefix sum over the block; `total` gets the block's sum.
-__device__ __forceinline__ int64_t block_scan(int64_t v, int64_t* warp_sums, int64_t& total) {
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
-    int64_t x = v;
-#pragma unroll
-    for (int d = 1; d < 32; d <<= 1) {
-        const int64_t y = __shfl_up_sync(0xffffffffu, x, d);
-        if (lane >= d) x += y;
-    }
-    if (lane == 31) warp_sums[warp] = x;
-    __syncthreads();
-    if (warp == 0) {
-        int64_t s = lane < warps ? warp_sums[lane] : 0;
-#pragma unroll
-        for (int d = 1; d < 32; d <<= 1) {
-            const int64_t y = __shfl_up_sync(0xffffffffu, s, d);
-            if (lane >= d) s += y;
-        }
-        if (lane < warps) warp_sums[lane] = s;
-    }
-    __syncthreads();
-    total = warp_sums[warps - 1];
-    const int64_t before = warp ? warp_sums[warp - 1] : 0;
-    __syncthreads();   // warp_sums may be written again
-    return before + x - v;
-}
 
 // Pages of request b, checked: 0 for a length the page table cannot hold.
 __device__ __forceinline__ int checked_len(const PlanArgs& p, int b) {

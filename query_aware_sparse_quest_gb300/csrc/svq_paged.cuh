@@ -173,6 +173,33 @@ struct Placed {
         : begin(at), tiles(n), c0(share.cta_of(at + kItemCost)), c1(share.cta_of(at + kItemCost + n - 1)) {}
 };
 
+// Exclusive prefix sum over the block; `total` gets the block's sum.
+__device__ __forceinline__ int64_t block_scan(int64_t v, int64_t* warp_sums, int64_t& total) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
+    int64_t x = v;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+        const int64_t y = __shfl_up_sync(0xffffffffu, x, d);
+        if (lane >= d) x += y;
+    }
+    if (lane == 31) warp_sums[warp] = x;
+    __syncthreads();
+    if (warp == 0) {
+        int64_t s = lane < warps ? warp_sums[lane] : 0;
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+            const int64_t y = __shfl_up_sync(0xffffffffu, s, d);
+            if (lane >= d) s += y;
+        }
+        if (lane < warps) warp_sums[lane] = s;
+    }
+    __syncthreads();
+    total = warp_sums[warps - 1];
+    const int64_t before = warp ? warp_sums[warp - 1] : 0;
+    __syncthreads();   // warp_sums may be written again
+    return before + x - v;
+}
+
 // ---------------------------------------------------------------- joining partials
 // A list of partials (o, (base, sum)) of one row; the base is in log2 units, o
 // and the sum are relative to it.

@@ -210,3 +210,20 @@ def test_rows_further_apart_than_2_31_elements():
     rope.copy_(r.rope)
     r.k, r.v, r.rope = k, v, rope
     r.check(*r.call())
+
+
+def test_sums_of_more_than_65536_tokens():
+    """Heads that overlap in memory (a token's row is the next head's of the token before) keep long rows small."""
+    n, heads, size = 140000, 160, 70
+    r = Rows([size], [n], 1, seed=5, mean=2.0, spare=heads)
+    r.heads = heads
+    g = torch.Generator().manual_seed(6)
+    r.q = torch.randn((size, heads, 192), generator=g).bfloat16().to(DEV)
+    flat_k, flat_v = (torch.nan_to_num(x.reshape(-1, 128).contiguous()) for x in (r.k, r.v))
+    r.k, r.v = (x.as_strided((n, heads, 128), (128, 128, 1)) for x in (flat_k, flat_v))
+    r.rope = r.rope[:n]
+    out, lse = r.call()
+    pick = [0, 1, 79, 159]
+    q, k, v = r.q[:, pick], r.k[:, pick], r.v[:, pick]
+    k = torch.cat((k.double(), r.rope[:, None].double().expand(-1, len(pick), -1)), -1)
+    check(out[:, pick], lse[:, pick], attend(q, k, v.double(), causal_seen(n, size, DEV), SCALE))
