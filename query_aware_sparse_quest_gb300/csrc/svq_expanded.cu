@@ -151,10 +151,10 @@ struct Control {
 };
 static_assert(sizeof(Control) <= kControlBytes, "control block");
 
-// The ring blocks of a segment of n tiles, in order: K0 K1 V0 K2 V1 .. K(n-1) V(n-2) V(n-1), three a key tile and two
-// a value tile.
-__device__ __forceinline__ uint32_t k_block(int t) { return t == 0 ? 0u : 5u * t - 2u; }
-__device__ __forceinline__ uint32_t v_block(int t, int n) { return t == n - 1 ? 5u * n - 2u : 5u * t + 6u; }
+// The ring blocks of a segment of n tiles, three a key tile and two a value tile, in the order of their use.  Two row
+// halves: K0 V0 K1 V1 ..; even and odd tiles: K0 K1 V0 K2 V1 .. K(n-1) V(n-2) V(n-1).
+__device__ __forceinline__ uint32_t k_block(bool two, int t) { return two ? 5u * t : (t == 0 ? 0u : 5u * t - 2u); }
+__device__ __forceinline__ uint32_t v_block(bool two, int t, int n) { return two ? 5u * t + 3u : (t == n - 1 ? 5u * n - 2u : 5u * t + 6u); }
 
 __device__ __forceinline__ void gave_up(Control* ct) {
     svq_flag(SV_DEVERR_TIMEOUT);
@@ -240,11 +240,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const Seg& s = ct->seg[k % kSegs];
                 const int n = s.t1 - s.t0;
                 if (n == 0) break;
+                const bool two = s.en.ntok > 128;
                 for (int i = 0; i < n; ++i) {
                     const int tok = s.en.kv0 + (s.t0 + i) * kTileTok;
 #pragma unroll
                     for (int c = 0; c < 3; ++c) {
-                        const uint32_t at = base + k_block(i) + c, st = at % kBlocks;
+                        const uint32_t at = base + k_block(two, i) + c, st = at % kBlocks;
                         SVQ_WAIT(ct->empty[st], ((at / kBlocks) & 1) ^ 1, keys_end);
                         if (lane == 0) {
                             const uint32_t bar = smem_addr(&ct->full[st]), dst = smem_addr(ring) + st * kBlock;
@@ -274,11 +275,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const Seg& s = ct->seg[k % kSegs];
                 const int n = s.t1 - s.t0;
                 if (n == 0) break;
+                const bool two = s.en.ntok > 128;
                 for (int i = 0; i < n; ++i) {
                     for (int c = 0; c < 2; ++c) {
                         const int first = (s.t0 + i) * kTileTok + c * 64;
                         const int here = s.en.len - first;          // tokens from here on
-                        const uint32_t at = base + v_block(i, n) + c, st = at % kBlocks;
+                        const uint32_t at = base + v_block(two, i, n) + c, st = at % kBlocks;
                         const uint32_t bar = smem_addr(&ct->full[st]), dst = smem_addr(ring) + st * kBlock;
                         SVQ_WAIT(ct->empty[st], ((at / kBlocks) & 1) ^ 1, values_end);
                         const bool whole = here >= 64, some = here > 0;
@@ -324,27 +326,33 @@ __global__ void __launch_bounds__(kThreads, 1)
                 auto ready = [&](uint32_t i) { return bar_wait(smem_addr(&ct->full[i % kBlocks]), (i / kBlocks) & 1); };
                 auto block = [&](uint32_t i) { return ring_s + i % kBlocks * kBlock; };
                 auto release = [&](uint32_t i) { mma_commit(smem_addr(&ct->empty[i % kBlocks])); };
-                auto k_ready = [&](uint32_t i) { return ready(i) && ready(i + 1) && ready(i + 2); };
-                auto k_release = [&](uint32_t i) { release(i); release(i + 1); release(i + 2); };
-                auto qk = [&](int w, uint32_t i) {
+                // Blocks are waited for where a stream is the first to read them, and freed where one is the last.
+                auto qk = [&](int w, uint32_t i, bool first, bool last) {
 #pragma unroll
-                    for (int c = 0; c < 3; ++c)
+                    for (int c = 0; c < 3; ++c) {
+                        if (first && !ready(i + c)) return false;
                         mma_qk4(tmem + kColS + w * 128, desc_lo(qs_s + w * kQBytes + c * kBlock, 16), desc_lo(block(i + c), 16),
                                 kIdescQK, c != 0);
+                        if (last) release(i + c);
+                    }
                     mma_commit(smem_addr(&ct->s_full[w]));
+                    return true;
                 };
                 // P V of stream w with the values in blocks i, i + 1, of which `steps` groups of 16 tokens count.
-                auto pv = [&](int w, uint32_t i, int steps, bool acc) {
+                auto pv = [&](int w, uint32_t i, int steps, bool acc, bool first, bool last) {
                     const uint32_t o = tmem + kColO + w * 128, p = tmem + kColS + w * 128;
 #pragma unroll
                     for (int c = 0; c < 2; ++c) {
+                        if (first && !ready(i + c)) return false;
                         const uint32_t v_lo = desc_lo(block(i + c), kBlock / 2);
                         if (steps >= 4 * c + 4) {
                             mma_pv4(o, p + c * 32, v_lo, kIdescPV, acc || c);
                         } else {
                             for (int u = 0; u < steps - 4 * c; ++u) mma_pv1(o, p + c * 32 + u * 8, v_lo + u * 128, kIdescPV, acc || c || u);
                         }
+                        if (last) release(i + c);
                     }
+                    return true;
                 };
                 auto p_ready = [&](int w) {
                     const bool r = bar_wait(smem_addr(&ct->p_full[w]), (p_ph >> w) & 1);
@@ -362,55 +370,35 @@ __global__ void __launch_bounds__(kThreads, 1)
                     for (int w = 0; w < 2 && ok; ++w) {
                         const int t = two ? 0 : w;
                         if (t >= n) break;
-                        const uint32_t kl = ld + k_block(t);
-                        ok = k_ready(kl) && bar_wait(smem_addr(&ct->q_full[w]), (q_ph >> w) & 1);
+                        ok = bar_wait(smem_addr(&ct->q_full[w]), (q_ph >> w) & 1);
                         q_ph ^= 1u << w;
                         if (!ok) break;
                         tc_fence_after();
-                        qk(w, kl);
-                        if (!two || w == 1) k_release(kl);
+                        ok = qk(w, ld + k_block(two, t), !two || w == 0, !two || w == 1);
                     }
                     int steps = (s.en.len - s.t0 * kTileTok + 15) / 16;   // groups of 16 tokens from the tile on
                     if (two) {
                         for (int t = 0; t < n && ok; ++t, steps -= 8) {
                             const bool next = t + 1 < n;
-                            const uint32_t vl = ld + v_block(t, n), kl = ld + k_block(t + 1);
-                            ok = ready(vl) && ready(vl + 1) && (!next || k_ready(kl)) && p_ready(0);
+                            const uint32_t vl = ld + v_block(true, t, n), kl = ld + k_block(true, t + 1);
+                            const bool acc = (t & (kFoldTiles - 1)) != 0;
+                            ok = p_ready(0) && pv(0, vl, steps, acc, true, false);
                             if (!ok) break;
-                            pv(0, vl, steps, (t & (kFoldTiles - 1)) != 0);
-                            if (next) qk(0, kl);
+                            if (next) ok = qk(0, kl, true, false);
                             else mma_commit(smem_addr(&ct->o_full[0]));
-                            ok = p_ready(1);
+                            ok = ok && p_ready(1);
                             if (!ok) break;
-                            pv(1, vl, steps, (t & (kFoldTiles - 1)) != 0);
-                            release(vl);
-                            release(vl + 1);
-                            if (next) {
-                                qk(1, kl);
-                                k_release(kl);
-                            } else {
-                                mma_commit(smem_addr(&ct->o_full[1]));
-                            }
+                            pv(1, vl, steps, acc, false, true);
+                            if (next) qk(1, kl, false, true);
+                            else mma_commit(smem_addr(&ct->o_full[1]));
                         }
                     } else {
                         for (int t = 0; t < n && ok; ++t, steps -= 8) {
                             const int w = t & 1;
-                            const bool next = t + 2 < n;
-                            const uint32_t vl = ld + v_block(t, n), kl = ld + k_block(t + 2);
-                            ok = ready(vl) && ready(vl + 1) && p_ready(w);
+                            ok = p_ready(w) && pv(w, ld + v_block(false, t, n), steps, ((t >> 1) & (kFoldTiles - 1)) != 0, true, true);
                             if (!ok) break;
-                            pv(w, vl, steps, ((t >> 1) & (kFoldTiles - 1)) != 0);
-                            release(vl);
-                            release(vl + 1);
-                            if (next) {
-                                ok = k_ready(kl);
-                                if (!ok) break;
-                                tc_fence_after();
-                                qk(w, kl);
-                                k_release(kl);
-                            } else {
-                                mma_commit(smem_addr(&ct->o_full[w]));
-                            }
+                            if (t + 2 < n) ok = qk(w, ld + k_block(false, t + 2), true, true);
+                            else mma_commit(smem_addr(&ct->o_full[w]));
                         }
                     }
                     ld += 5 * n;
