@@ -1,12 +1,44 @@
-// sv_latent_attention: attention in the absorbed form over the paged latents.
+// sv_latent_attention: attention in the absorbed form over the paged latents, on
+// the tcgen05 tensor cores.
 //
-// A warp computes one row (query token, head): lane l holds latent channels
-// 16 l .. 16 l + 15 and rotary channels 2 l, 2 l + 1 of the query, reads the
-// tokens the row sees one by one, and keeps the running maximum, sum and average
-// of the softmax in fp32.
+// Mathematics.  All query heads read the same token, so the query tokens of a
+// request times the heads are rows of one product, and a key tile's latents C (64
+// tokens x 512) are keys and values both.  With Q (rows x 576) and K = C beside the
+// rotary keys,
+//   S^T = K Q^T               (fp32 in TMEM: 64 tokens x rows, 36 MMAs of k = 16 channels)
+//   P^T = exp2(S^T * scale - base)   (bf16 in shared memory; base = a running maximum a row)
+//   O^T = O^T * 2^(old - new base) + C^T P^T   (fp32 in TMEM: 512 channels x rows,
+//                             4 MMAs of 128 channels for each 16 tokens)
+// The products are turned round, tokens and channels on the MMA's M side, rows on
+// its N side: O of 128 rows would take all of TMEM and Q of them 144 KB of shared
+// memory, while 64 rows leave room for two S and for a second key tile, and 16
+// rows of a single token need no padding to 128.
+//
+// P is rounded to bf16 because one MMA takes both operands in one type and C is
+// bf16 (off by at most 2^-8 of each weight); over bf16 latents the average is taken
+// over the sum of the rounded weights, so that rows of equal weights lose nothing.
+// Sums, bases and outputs are fp32.
+//
+// e4m3 latents: codes are widened to bf16 tiles, exactly; a token's scale acts on
+// its logits and on its weights, and the rotary part of the logits is a product of
+// its own (N more columns).
+//
+// Work.  An entry is up to kShare x N rows of a request with the pages they see;
+// every group of kShare CTAs takes an equal run of the (entry, key tile) sequence.
+// A run that starts or ends inside an entry leaves a partial (O, base, sum), joined
+// by a second kernel.
+//
+// Roles of a CTA (one per SM):
+//   warp 0       loads the pages: units of 64 tokens x 128 channels (16 KB), each
+//                freed when its part of the second product is done, and rotary keys
+//   warp 1       issues the MMAs (one thread)
+//   warp 2       walks the plan
+//   warps 4-7    softmax (16 tokens each), outputs
+//   warps 8-15   (e4m3) widen the codes
 #include <climits>
 
 #include "svq_paged.cuh"
+#include "svq_tcgen.cuh"
 
 namespace svq {
 
@@ -15,7 +47,46 @@ SVQ_DEFINE_ERROR_WORD(read_error_latent_attend)
 namespace {
 
 constexpr int kQueryDim = kLatentDim + kRopeDim;
-constexpr int kThreads = 256;
+constexpr int kPages = 4;                           // pages of a key tile
+constexpr int kTok = kPages * kPage;                // 64 tokens
+constexpr int kUnit = kTok * 128 * 2;               // bytes of 128 channels of a tile
+constexpr int kUnits = kLatentDim / 128;            // of a tile
+constexpr int kRopeBytes = kTok * kRopeDim * 2;
+constexpr int kInfoSlots = 8;                       // tiles whose page faults and scales are kept
+constexpr int kMaxCtas = 160;                       // partial slots in the workspace
+constexpr float kSlack = 8.f;                       // log2 units a base may lag behind the maximum
+// Key tiles after which O moves into fp32 sums and starts again from zero: the MMAs cut their sums off at fp32's last
+// bit, four times a tile, always towards zero (values of one sign lose 2^-21.4 of their sum a tile).
+constexpr int kFoldTiles = 1024;
+constexpr int kControlBytes = 3072;
+constexpr int kMaxRows = 64;                        // rows of a CTA's tile at most
+
+template <int N, bool FP8>
+struct Cfg {
+    static constexpr int kRing = FP8 ? (N == 64 ? 6 : 7) : (N == 64 ? 8 : (N == 32 ? 10 : 11));   // units
+    static constexpr int kRope = N == 64 ? 2 : 3;                                                 // rotary tiles
+    static constexpr int kCodes = FP8 ? (N == 64 ? 3 : (N == 32 ? 5 : 6)) : 0;                    // units of codes, 8 KB
+    static constexpr int kAhead = kRing >= 8 ? 4 : kRing - 4;   // units of a tile whose S is begun before the tile before is done
+    static constexpr int kThreads = FP8 ? 512 : 256;
+    static constexpr int kWiden = 8;                                                              // warps
+    static constexpr int kQ = N * kQueryDim * 2;
+    static constexpr int kP = N * kTok * 2;
+    static constexpr int kScales = FP8 ? kInfoSlots * kTok * 4 : 0;
+    static constexpr int kSmem = kRing * kUnit + kRope * kRopeBytes + kCodes * (kUnit / 2) + kQ + kP + kScales + kControlBytes;
+    static constexpr int kColS = 4 * N;                    // TMEM columns: O^T of channels 128 m .. at m N, then two S^T
+    static constexpr int kSCols = FP8 ? 2 * N : N;         // (latent | rotary)
+    static_assert(kSmem <= 227 * 1024, "shared memory of one CTA");
+};
+
+struct __align__(16) Entry {
+    int row0;      // first row: query token * heads + head
+    int nrows;
+    int posbase;   // a row's position is posbase + row / heads
+    int req;
+    int npages;    // pages that some row of it sees
+    int tiles;
+    int pad[2];
+};
 
 struct LatentArgs {
     const __nv_bfloat16* q;
@@ -29,11 +100,904 @@ struct LatentArgs {
     const unsigned char* pool;
     const __nv_bfloat16* rope;
     const float* scale;
+    bool fp8;
     float scale_log2;
     __nv_bfloat16* out;
     float* lse;
+    int share;           // CTAs that work on the rows of an entry side by side
+    int tile_rows;       // rows of each (N)
+    // Plan
+    Entry* entries;
+    int64_t* cum;        // [E + 1] cost of the entries before each
+    int* num_entries;
+    int* req_first;      // [batch]
+    int max_entries;
+    // Partials
+    float* cut_o;        // [2 CTAs][N][512]
+    float4* cut_ml;      // [2 CTAs][N] (base in log2 units, sum, sum of the rounded weights)
+    int4* cut_item;      // [groups][2]: row0, nrows, pieces, entry; slots of the first piece and the second (of part 0)
+    uint32_t* odd;       // CTAs' row tiles of whole entries that are not finite: entry * share + part
+    int* num_odd;
 };
 
+// ---------------------------------------------------------------- tensor cores
+constexpr uint32_t kF32FromBf16 = (1u << 4) | (1u << 7) | (1u << 10);
+constexpr uint32_t idesc(int m, int n) { return kF32FromBf16 | (static_cast<uint32_t>(n / 8) << 17) | (static_cast<uint32_t>(m / 16) << 24); }
+constexpr uint32_t kAIsMMajor = 1u << 15;
+
+// S^T (+)= K Q^T over a unit's 128 channels: 16 channels are 32 bytes further in the rows of both; the second 64 lie
+// 1 KB on (K) and a block of N rows on (Q: q_half in descriptor units).
+__device__ __forceinline__ void mma_qk8(uint32_t d, uint32_t k_lo, uint32_t q_lo, uint32_t q_half, uint32_t id, uint32_t acc) {
+    const uint32_t q2 = q_lo + q_half;
+    asm volatile(
+        "{\n\t.reg .pred acc, yes;\n\t.reg .b32 al, bl;\n\t.reg .b64 ad, bd;\n\t"
+        "setp.ne.u32 acc, %6, 0;\n\tsetp.eq.u32 yes, 0, 0;\n\t"
+        SVQ_MMA_SS(0, 0, acc) SVQ_MMA_SS(2, 2, yes) SVQ_MMA_SS(4, 4, yes) SVQ_MMA_SS(6, 6, yes)
+        "}" ::"r"(d), "r"(k_lo), "r"(q_lo), "r"(desc_hi(2048)), "r"(desc_hi(1024)), "r"(id), "r"(acc)
+        : "memory");
+    asm volatile(
+        "{\n\t.reg .pred yes;\n\t.reg .b32 al, bl;\n\t.reg .b64 ad, bd;\n\tsetp.eq.u32 yes, 0, 0;\n\t"
+        SVQ_MMA_SS(64, 0, yes) SVQ_MMA_SS(66, 2, yes) SVQ_MMA_SS(68, 4, yes) SVQ_MMA_SS(70, 6, yes)
+        "}" ::"r"(d), "r"(k_lo), "r"(q2), "r"(desc_hi(2048)), "r"(desc_hi(1024)), "r"(id)
+        : "memory");
+}
+// The rotary 64 channels.
+__device__ __forceinline__ void mma_rope4(uint32_t d, uint32_t k_lo, uint32_t q_lo, uint32_t id, uint32_t acc) {
+    asm volatile(
+        "{\n\t.reg .pred acc, yes;\n\t.reg .b32 al, bl;\n\t.reg .b64 ad, bd;\n\t"
+        "setp.ne.u32 acc, %6, 0;\n\tsetp.eq.u32 yes, 0, 0;\n\t"
+        SVQ_MMA_SS(0, 0, acc) SVQ_MMA_SS(2, 2, yes) SVQ_MMA_SS(4, 4, yes) SVQ_MMA_SS(6, 6, yes)
+        "}" ::"r"(d), "r"(k_lo), "r"(q_lo), "r"(desc_hi(1024)), "r"(desc_hi(1024)), "r"(id), "r"(acc)
+        : "memory");
+}
+// O^T (+)= C^T P^T of 128 channels: a page (16 tokens) is 4 KB of the unit and 32 bytes of P's rows.
+__device__ __forceinline__ void mma_pv4(uint32_t d, uint32_t c_lo, uint32_t p_lo, uint32_t id, uint32_t acc) {
+    asm volatile(
+        "{\n\t.reg .pred acc, yes;\n\t.reg .b32 al, bl;\n\t.reg .b64 ad, bd;\n\t"
+        "setp.ne.u32 acc, %6, 0;\n\tsetp.eq.u32 yes, 0, 0;\n\t"
+        SVQ_MMA_SS(0, 0, acc) SVQ_MMA_SS(256, 2, yes) SVQ_MMA_SS(512, 4, yes) SVQ_MMA_SS(768, 6, yes)
+        "}" ::"r"(d), "r"(c_lo), "r"(p_lo), "r"(desc_hi(2048)), "r"(desc_hi(1024)), "r"(id), "r"(acc)
+        : "memory");
+}
+__device__ __forceinline__ void mma_pv1(uint32_t d, uint32_t c_lo, uint32_t p_lo, uint32_t id, uint32_t acc) {
+    asm volatile(
+        "{\n\t.reg .pred acc;\n\t.reg .b32 al, bl;\n\t.reg .b64 ad, bd;\n\tsetp.ne.u32 acc, %6, 0;\n\t"
+        SVQ_MMA_SS(0, 0, acc)
+        "}" ::"r"(d), "r"(c_lo), "r"(p_lo), "r"(desc_hi(2048)), "r"(desc_hi(1024)), "r"(id), "r"(acc)
+        : "memory");
+}
+// 16 lanes x 8 columns a repeat: lane l of the warp gets row l / 4 (and + 8), columns 2 (l % 4), + 1.
+__device__ __forceinline__ void tc_ld_frag(uint32_t addr, float (&r)[8]) {
+    uint32_t(&u)[8] = reinterpret_cast<uint32_t(&)[8]>(r);
+    asm volatile("tcgen05.ld.sync.aligned.16x256b.x2.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                 : "=r"(u[0]), "=r"(u[1]), "=r"(u[2]), "=r"(u[3]), "=r"(u[4]), "=r"(u[5]), "=r"(u[6]), "=r"(u[7])
+                 : "r"(addr));
+}
+// Four 8 x 8 blocks of 16-bit values, turned round: lane l gives the address of row l % 8 of block l / 8.
+__device__ __forceinline__ void stmatrix_x4_trans(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+    asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1,%2,%3,%4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d)
+                 : "memory");
+}
+__device__ __forceinline__ void tma_page(uint32_t dst, const void* map, int half, int group, uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %2, %3, %4}], [%5];"
+        ::"r"(dst), "l"(map), "r"(0), "r"(half), "r"(group), "r"(bar)
+        : "memory");
+}
+// The softmax warps' barrier.
+__device__ __forceinline__ void softmax_sync() { asm volatile("barrier.cta.sync 1, 128;" ::: "memory"); }
+__device__ __forceinline__ bool softmax_any(bool mine) {
+    uint32_t any;
+    asm volatile(
+        "{\n\t.reg .pred p, r;\n\tsetp.ne.u32 p, %1, 0;\n\tbarrier.cta.red.or.pred r, 1, 128, p;\n\tselp.u32 %0, 1, 0, r;\n\t}"
+        : "=r"(any)
+        : "r"(static_cast<uint32_t>(mine))
+        : "memory");
+    return any != 0;
+}
+
+// The softmax warps meet at barriers, so they leave together: a warp whose wait ran out says so at the next one.
+#define LATENT_WAIT(bar, parity)                                                    \
+    do {                                                                            \
+        if (__any_sync(0xffffffffu, !bar_wait(smem_addr(&(bar)), (parity)))) {      \
+            if (lane == 0) gave_up(ct);                                             \
+            dead = true;                                                            \
+        }                                                                           \
+    } while (0)
+
+// A run of key tiles of one entry; none: the CTA's work is over.
+struct __align__(16) Seg {
+    Entry en;
+    int t0, t1;
+    int slot;         // where a partial goes; -1 - entry: the segment is the whole entry
+    int pad;
+};
+constexpr int kSegs = 4;
+
+struct Control {
+    uint64_t full[11], empty[11];          // units
+    uint64_t rope_full[3], rope_empty[3];
+    uint64_t code_full[6], code_empty[6];
+    uint64_t scale_full[kInfoSlots];
+    uint64_t seg_full[kSegs], seg_empty[kSegs];
+    uint64_t s_full[2], p_full, pv_done, q_full, drain;
+    uint32_t tmem;
+    int gave_up;
+    int fault[kInfoSlots];                 // pages of a tile that the table does not give
+    Seg seg[kSegs];
+    float red[4][kMaxRows];                // maxima (and, at a segment's end, sums) of each softmax warp
+    float base[kMaxRows], alpha[kMaxRows];
+};
+static_assert(sizeof(Control) <= kControlBytes, "control block");
+
+__device__ __forceinline__ void gave_up(Control* ct) {
+    svq_flag(SV_DEVERR_TIMEOUT);
+    *static_cast<volatile int*>(&ct->gave_up) = 1;
+}
+constexpr int kSegRounds = 128;   // of kPolls: what the plan waits for a slot whose segment may be long
+
+// Largest i in [0, n) with a[i] <= v (a ascending), by the whole warp (32 probes a round trip).
+__device__ __forceinline__ int warp_find_le(const int64_t* a, int n, int64_t v) {
+    const int lane = threadIdx.x & 31;
+    int lo = 0, len = n;
+    while (len > 1) {
+        const int step = (len + 31) / 32;
+        const int at = lo + lane * step;
+        const bool le = lane * step < len && a[at] <= v;
+        const int k = __popc(__ballot_sync(0xffffffffu, le)) - 1;
+        const int nlo = lo + max(k, 0) * step;
+        len = min(step, lo + len - nlo);
+        lo = nlo;
+    }
+    return lo;
+}
+
+// What an entry costs beside its tiles, in tiles, and the least share that is worth a CTA.
+constexpr int kEntryCost = 3, kMinShare = 4;
+__device__ __forceinline__ int cost_of_entry(int tiles) { return tiles ? tiles + kEntryCost : 0; }
+// Groups of CTAs that share the work.
+__device__ __forceinline__ int groups_of(int64_t total, int most) {
+    const int64_t n = (total + kMinShare - 1) / kMinShare;
+    return n < 1 ? 1 : (n < most ? static_cast<int>(n) : most);
+}
+struct PlacedEntry {
+    int64_t begin;
+    int c0, c1;
+    __device__ __forceinline__ PlacedEntry(const Share& share, int64_t at, int n)
+        : begin(at), c0(share.cta_of(at + kEntryCost)), c1(share.cta_of(at + kEntryCost + n - 1)) {}
+};
+
+template <int N, bool FP8>
+__global__ void __launch_bounds__(Cfg<N, FP8>::kThreads, 1)
+    latent_kernel(const __grid_constant__ LatentArgs a, const __grid_constant__ CUtensorMap tmap_q,
+                  const __grid_constant__ CUtensorMap tmap_c, const __grid_constant__ CUtensorMap tmap_r) {
+    using C = Cfg<N, FP8>;
+    extern __shared__ __align__(1024) unsigned char smem[];
+    unsigned char* const ring = smem;
+    unsigned char* const ropes = ring + C::kRing * kUnit;
+    unsigned char* const codes = ropes + C::kRope * kRopeBytes;
+    unsigned char* const qs = codes + C::kCodes * (kUnit / 2);
+    unsigned char* const ps = qs + C::kQ;
+    float* const scales = reinterpret_cast<float*>(ps + C::kP);
+    Control* const ct = reinterpret_cast<Control*>(ps + C::kP + C::kScales);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int part = blockIdx.x % a.share, group = blockIdx.x / a.share;
+
+    if (threadIdx.x == 0) {
+        ct->gave_up = 0;
+        for (int i = 0; i < C::kRing; ++i) {
+            mbar_init(smem_addr(&ct->full[i]), FP8 ? C::kWiden : 1);
+            mbar_init(smem_addr(&ct->empty[i]), 1);
+        }
+        for (int i = 0; i < C::kRope; ++i) {
+            mbar_init(smem_addr(&ct->rope_full[i]), 1);
+            mbar_init(smem_addr(&ct->rope_empty[i]), 1);
+        }
+        for (int i = 0; i < C::kCodes; ++i) {
+            mbar_init(smem_addr(&ct->code_full[i]), 1);
+            mbar_init(smem_addr(&ct->code_empty[i]), C::kWiden);
+        }
+        for (int i = 0; i < kInfoSlots; ++i) mbar_init(smem_addr(&ct->scale_full[i]), 1);
+        for (int i = 0; i < kSegs; ++i) {
+            mbar_init(smem_addr(&ct->seg_full[i]), 1);
+            mbar_init(smem_addr(&ct->seg_empty[i]), 2 + 4 + (FP8 ? C::kWiden : 0));   // loads, MMAs, softmax, widening
+        }
+        mbar_init(smem_addr(&ct->s_full[0]), 1);
+        mbar_init(smem_addr(&ct->s_full[1]), 1);
+        mbar_init(smem_addr(&ct->p_full), 4);
+        mbar_init(smem_addr(&ct->pv_done), 1);
+        mbar_init(smem_addr(&ct->q_full), 1);
+        mbar_init(smem_addr(&ct->drain), 1);
+        mbar_init_fence();
+        prefetch_tmap(&tmap_q);
+        prefetch_tmap(&tmap_c);
+        prefetch_tmap(&tmap_r);
+    }
+    if (warp == 1) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_addr(&ct->tmem))
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    }
+    pdl_wait();
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = ct->tmem;
+    // Every role takes the segments in order: the k-th is in slot k % kSegs.
+    auto seg_done = [&](uint32_t k) {   // once a warp
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_addr(&ct->seg_empty[k % kSegs]));
+    };
+
+    {
+        if (warp == 0) {
+            // ---------------- loads: lane p page p of a tile
+            uint32_t tile = 0, loaded = 0;
+            for (uint32_t k = 0;; ++k) {
+                SVQ_WAIT(ct->seg_full[k % kSegs], (k / kSegs) & 1, loads_end);
+                const Seg& s = ct->seg[k % kSegs];
+                const int n = s.t1 - s.t0;
+                if (n == 0) break;
+                const int32_t* const pages = a.page_table + static_cast<int64_t>(s.en.req) * a.max_pages;
+                // Lane l resolves page i + l of the segment (eight tiles at a time), well before the loads that need it.
+                auto fetch = [&](int i0) {
+                    const int i = i0 + lane;
+                    return i < min(s.en.npages, s.t1 * kPages) ? pages[i] : -2;
+                };
+                int cur = -2, nxt = fetch(s.t0 * kPages);
+                for (int i = 0; i < n; ++i, ++tile) {
+                    if (i % 8 == 0) {
+                        cur = nxt;
+                        if (i + 8 < n) nxt = fetch((s.t0 + i + 8) * kPages);
+                    }
+                    int ph = __shfl_sync(0xffffffffu, cur, (i % 8) * kPages + (lane & 3));
+                    if (lane >= kPages) ph = -2;
+                    const bool bad = ph != -2 && (ph < 0 || ph >= a.num_pages);
+                    const bool load = ph != -2 && !bad;
+                    const uint32_t faults = __ballot_sync(0xffffffffu, bad);
+                    const int loads = __popc(__ballot_sync(0xffffffffu, load));
+                    const int slot = tile % kInfoSlots;
+                    if (lane == 0) {
+                        if (faults) svq_flag(SV_DEVERR_PAGE_TABLE);
+                        ct->fault[slot] = static_cast<int>(faults);
+                    }
+                    if (FP8) {
+                        if (lane == 0) mbar_arrive_expect_tx(smem_addr(&ct->scale_full[slot]), loads * kPage * 4);
+                        __syncwarp();
+                        if (load)
+                            bulk_copy_g2s(smem_addr(scales + slot * kTok + lane * kPage), a.scale + static_cast<int64_t>(ph) * kPage,
+                                          kPage * 4, smem_addr(&ct->scale_full[slot]));
+                    }
+#pragma unroll 1
+                    for (int u = 0; u < kUnits; ++u) {
+                        const uint32_t at = tile * kUnits + u;
+                        if (FP8) {
+                            constexpr uint32_t kDepth = FP8 ? C::kCodes : 1;
+                            const uint32_t st = at % kDepth;
+                            SVQ_WAIT(ct->code_empty[st], ((at / kDepth) & 1) ^ 1, loads_end);
+                            const uint32_t bar = smem_addr(&ct->code_full[st]);
+                            if (lane == 0) mbar_arrive_expect_tx(bar, loads * (kPage * 128));
+                            __syncwarp();
+                            if (load)
+                                tma_load_2d(smem_addr(codes) + st * (kUnit / 2) + lane * (kPage * 128), &tmap_c, u * 128, ph * kPage, bar);
+                        } else {
+                            const uint32_t st = at % C::kRing;
+                            SVQ_WAIT(ct->empty[st], ((at / C::kRing) & 1) ^ 1, loads_end);
+                            const uint32_t bar = smem_addr(&ct->full[st]);
+                            if (lane == 0) mbar_arrive_expect_tx(bar, loads * (kPage * 256));
+                            __syncwarp();
+                            if (load) tma_page(smem_addr(ring) + st * kUnit + lane * (kPage * 256), &tmap_c, 2 * u, 2 * ph, bar);
+                        }
+                        loaded = at + 1;
+                    }
+                    const uint32_t st = tile % C::kRope;
+                    SVQ_WAIT(ct->rope_empty[st], ((tile / C::kRope) & 1) ^ 1, loads_end);
+                    const uint32_t bar = smem_addr(&ct->rope_full[st]);
+                    if (lane == 0) mbar_arrive_expect_tx(bar, loads * (kPage * kRopeDim * 2));
+                    __syncwarp();
+                    if (load) tma_load_2d(smem_addr(ropes) + st * kRopeBytes + lane * (kPage * kRopeDim * 2), &tmap_r, 0, ph * kPage, bar);
+                }
+                seg_done(k);
+            }
+            goto loads_done;   // every load has been waited for by the MMAs or the widening warps
+        loads_end:
+            // Gave up: the copies still in flight land before the CTA (and its shared memory) retires.
+            {
+                constexpr uint32_t kDepth = FP8 ? C::kCodes : C::kRing;
+                uint64_t* const full = FP8 ? ct->code_full : ct->full;
+                for (uint32_t x = loaded > kDepth ? loaded - kDepth : 0; x < loaded; ++x)
+                    (void)bar_wait(smem_addr(&full[x % kDepth]), (x / kDepth) & 1);
+                for (uint32_t x = tile > C::kRope ? tile - C::kRope : 0; x < tile; ++x)
+                    (void)bar_wait(smem_addr(&ct->rope_full[x % C::kRope]), (x / C::kRope) & 1);
+                if (FP8) (void)bar_wait(smem_addr(&ct->scale_full[tile % kInfoSlots]), (tile / kInfoSlots) & 1);
+            }
+        loads_done:;
+        } else if (warp == 1) {
+            // ---------------- MMAs (one thread)
+            if (lane == 0) {
+                uint32_t tile = 0, segs = 0;   // tiles before the segment; segments with tiles
+                const uint32_t ring_s = smem_addr(ring), q_s = smem_addr(qs), p_lo = desc_lo(smem_addr(ps), 16);
+                constexpr uint32_t kBlockQ = N * 128;
+                // S^T of tile t (counted over the CTA's work): units u0 .. u1 - 1, and the rotary part behind the last.
+                auto qk = [&](uint32_t t, int u0, int u1) {
+                    const uint32_t d = tmem + C::kColS + (t & 1) * C::kSCols;
+#pragma unroll 1
+                    for (int u = u0; u < u1; ++u) {
+                        const uint32_t at = t * kUnits + u, st = at % C::kRing;
+                        if (!bar_wait(smem_addr(&ct->full[st]), (at / C::kRing) & 1)) return false;
+                        tc_fence_after();
+                        mma_qk8(d, desc_lo(ring_s + st * kUnit, 16), desc_lo(q_s + 2 * u * kBlockQ, 16), kBlockQ >> 4, idesc(64, N), u != 0);
+                    }
+                    if (u1 < kUnits) return true;
+                    const uint32_t st = t % C::kRope;
+                    if (!bar_wait(smem_addr(&ct->rope_full[st]), (t / C::kRope) & 1)) return false;
+                    tc_fence_after();
+                    mma_rope4(FP8 ? d + N : d, desc_lo(smem_addr(ropes) + st * kRopeBytes, 16), desc_lo(q_s + 8 * kBlockQ, 16),
+                              idesc(64, N), !FP8);
+                    mma_commit(smem_addr(&ct->rope_empty[st]));
+                    mma_commit(smem_addr(&ct->s_full[t & 1]));
+                    return true;
+                };
+                bool ok = true;
+                for (uint32_t k = 0; ok; ++k) {
+                    ok = bar_wait(smem_addr(&ct->seg_full[k % kSegs]), (k / kSegs) & 1);
+                    const Seg& s = ct->seg[k % kSegs];
+                    const int n = s.t1 - s.t0;
+                    if (!ok || n == 0) break;
+                    ok = bar_wait(smem_addr(&ct->q_full), segs & 1);
+                    ++segs;
+                    if (!ok) break;
+                    tc_fence_after();
+                    ok = qk(tile, 0, kUnits);
+                    for (int i = 0; i < n && ok; ++i) {
+                        const uint32_t t = tile + i;
+                        if (i + 1 < n && !qk(t + 1, 0, C::kAhead)) {
+                            ok = false;
+                            break;
+                        }
+                        ok = bar_wait(smem_addr(&ct->p_full), t & 1);
+                        if (!ok) break;
+                        tc_fence_after();
+                        const int pages = min(kPages, s.en.npages - (s.t0 + i) * kPages);
+                        const bool acc = (i & (kFoldTiles - 1)) != 0;
+#pragma unroll 1
+                        for (int u = 0; u < kUnits; ++u) {
+                            const uint32_t st = (t * kUnits + u) % C::kRing;
+                            const uint32_t c_lo = desc_lo(ring_s + st * kUnit, 1024), d = tmem + u * N;
+                            if (pages == kPages) {
+                                mma_pv4(d, c_lo, p_lo, idesc(128, N) | kAIsMMajor, acc);
+                            } else {
+                                for (int p = 0; p < pages; ++p)
+                                    mma_pv1(d, c_lo + p * 256, p_lo + p * 2, idesc(128, N) | kAIsMMajor, acc || p != 0);
+                            }
+                            mma_commit(smem_addr(&ct->empty[st]));
+                        }
+                        mma_commit(smem_addr(&ct->pv_done));
+                        if (C::kAhead < kUnits && i + 1 < n) ok = qk(t + 1, C::kAhead, kUnits);
+                    }
+                    tile += n;
+                    if (ok) mbar_arrive(smem_addr(&ct->seg_empty[k % kSegs]));
+                }
+                if (!ok) gave_up(ct);
+                mma_commit(smem_addr(&ct->drain));   // nothing of this CTA's is in flight when TMEM is freed
+                (void)bar_wait(smem_addr(&ct->drain), 0);
+            }
+            __syncwarp();
+        } else if (warp == 2) {
+            // ---------------- the group's share of the plan, segment by segment
+            const int num_entries = *a.num_entries;
+            const int64_t total = a.cum[num_entries];
+            const int groups = groups_of(total, gridDim.x / a.share);
+            const Share share(total, groups);
+            const int64_t first = group < groups ? share.start(group) : total;
+            int64_t left = group < groups ? share.start(group + 1) - first : 0;
+            int e = 0;
+            int64_t off = 0;                 // into the entry's cost
+            if (left > 0) {
+                e = warp_find_le(a.cum, num_entries, first);
+                off = first - a.cum[e];
+            }
+            const bool go_on = off > 0;      // the share begins inside an entry
+            if (left <= 0 && lane == 0 && part == 0) a.cut_item[2 * group] = make_int4(0, 0, 0, 0);
+            bool first_item = true;
+            Entry en = {};
+            for (uint32_t k = 0;;) {
+                int t0 = 0, t1 = 0;
+                if (left > 0) {
+                    if (off == 0 || first_item) {
+                        do {   // (entries without tiles: rows that see nothing)
+                            const int4* p = reinterpret_cast<const int4*>(a.entries + e);
+                            const int4 x = p[0], y = p[1];
+                            en = Entry{x.x, x.y, x.z, x.w, y.x, y.y, {0, 0}};
+                        } while (en.tiles == 0 && ++e < num_entries);
+                    }
+                    if (first_item && lane == 0 && part == 0) {
+                        // The group after the one with an entry's first tile names the entry for the join.
+                        int4 what = make_int4(0, 0, 0, 0), where = make_int4(0, 0, 0, 0);
+                        if (go_on) {
+                            const PlacedEntry it(share, first - off, en.tiles);
+                            if (group == it.c0 + 1) {
+                                what = make_int4(en.row0, en.nrows, it.c1 - it.c0 + 1, e);
+                                where.x = 2 * it.c0 + (share.start(it.c0) >= it.begin ? 0 : 1);
+                                where.y = 2 * (it.c0 + 1);
+                            }
+                        }
+                        a.cut_item[2 * group] = what;
+                        a.cut_item[2 * group + 1] = where;
+                    }
+                    const int64_t take = min(left, cost_of_entry(en.tiles) - off);
+                    t0 = static_cast<int>(max(static_cast<int64_t>(0), off - kEntryCost));
+                    t1 = static_cast<int>(max(static_cast<int64_t>(0), off + take - kEntryCost));
+                    left -= take;
+                    off += take;
+                }
+                const int rows = min(N, en.nrows - part * N);
+                if ((t1 > t0 && rows > 0) || left <= 0) {
+                    for (int round = 0;; ++round) {
+                        if (!__any_sync(0xffffffffu, !bar_wait(smem_addr(&ct->seg_empty[k % kSegs]), ((k / kSegs) & 1) ^ 1))) break;
+                        if (__any_sync(0xffffffffu, *static_cast<volatile int*>(&ct->gave_up)) || round == kSegRounds) {
+                            if (lane == 0) gave_up(ct);
+                            goto plan_end;
+                        }
+                    }
+                    const bool over = t1 == t0 || rows <= 0;   // (the last one)
+                    if (lane == 0) {
+                        Seg& s = ct->seg[k % kSegs];
+                        s.en = en;
+                        s.en.row0 += part * N;
+                        s.en.nrows = rows;
+                        s.t0 = over ? 0 : t0;
+                        s.t1 = over ? 0 : t1;
+                        s.slot = t0 == 0 && t1 == en.tiles ? -1 - e : 2 * static_cast<int>(blockIdx.x) + (first_item ? 0 : 1);
+                        mbar_arrive(smem_addr(&ct->seg_full[k % kSegs]));
+                    }
+                    ++k;
+                    if (over) break;
+                }
+                first_item = false;
+                if (off == cost_of_entry(en.tiles)) {
+                    off = 0;
+                    ++e;
+                }
+            }
+        plan_end:;
+        } else if (warp >= 4 && warp < 8) {
+            // ---------------- softmax: warp w tokens 16 w .., lane l rows 8 c + 2 (l % 4), + 1 of tokens l / 4, + 8
+            const int w = warp - 4, tid = threadIdx.x - 128;
+            const int quad = lane & 3, row8 = lane >> 2;
+            const uint32_t lanes = static_cast<uint32_t>(w * 32) << 16;
+            constexpr int kGroups = N / 8;
+            uint32_t tile = 0, q_loads = 0;
+            bool dead = false;   // a wait of this warp's ran out
+            auto load_q = [&](const Seg& g) {
+                if (tid == 0) {
+                    const uint32_t bar = smem_addr(&ct->q_full);
+                    mbar_arrive_expect_tx(bar, C::kQ);
+                    ++q_loads;
+#pragma unroll 1
+                    for (int c = 0; c < kQueryDim / 64; ++c) tma_load_2d(smem_addr(qs) + c * (N * 128), &tmap_q, c * 64, g.en.row0, bar);
+                }
+            };
+            for (uint32_t k = 0;; ++k) {
+                const Seg& s = ct->seg[k % kSegs];
+                if (k == 0) {
+                    LATENT_WAIT(ct->seg_full[0], 0);
+                    if (softmax_any(dead)) goto softmax_end;
+                    if (s.t1 > s.t0) load_q(s);
+                }
+                const int n = s.t1 - s.t0;
+                if (n == 0) break;
+                LATENT_WAIT(ct->seg_full[(k + 1) % kSegs], ((k + 1) / kSegs) & 1);
+                if (softmax_any(dead)) goto softmax_end;
+                const Seg& nx = ct->seg[(k + 1) % kSegs];
+                const int rows = s.en.nrows;
+                // Tokens that a row sees.
+                auto see = [&](int r) { return s.en.posbase + (s.en.row0 + min(r, rows - 1)) / a.heads + 1; };
+                const int see_all = see(0), see_any = see(rows - 1);
+                float m = -INFINITY;                    // thread r < N: the base of row r
+                float base[2 * kGroups], l[2 * kGroups], lr[2 * kGroups];
+#pragma unroll
+                for (int c = 0; c < 2 * kGroups; ++c) base[c] = l[c] = lr[c] = 0.f;
+                float folded = -INFINITY;               // thread r < N: the base of what was folded
+                float* const fold_to = a.cut_o + static_cast<int64_t>(s.slot >= 0 ? s.slot : 2 * static_cast<int>(blockIdx.x) + 1) * N * kLatentDim;
+                for (int j = 0; j < n; ++j, ++tile) {
+                    const int first = (s.t0 + j) * kTok;
+                    const int slot = tile % kInfoSlots;
+                    LATENT_WAIT(ct->s_full[tile & 1], (tile >> 1) & 1);
+                    tc_fence_after();
+                    if (j == n - 1 && nx.t1 > nx.t0) load_q(nx);   // the segment's last use of Q is over
+                    const uint32_t s_col = tmem + lanes + C::kColS + (tile & 1) * C::kSCols;
+                    float x[4 * kGroups];
+#pragma unroll
+                    for (int c = 0; c < kGroups / 2; ++c) tc_ld_frag(s_col + c * 16, reinterpret_cast<float(&)[8]>(x[c * 8]));
+                    tc_wait_ld();
+                    const int tok0 = first + 16 * w + row8, tok1 = tok0 + 8;
+                    const int fault = ct->fault[slot];
+                    const bool gone = (fault >> w) & 1;     // the warp's tokens are one page
+                    float sc0 = 1.f, sc1 = 1.f;
+                    if (FP8) {
+                        LATENT_WAIT(ct->scale_full[slot], (tile / kInfoSlots) & 1);
+                        // (Scales of tokens that no row sees may hold anything.)
+                        sc0 = tok0 < see_any && !gone ? scales[slot * kTok + 16 * w + row8] : 0.f;
+                        sc1 = tok1 < see_any && !gone ? scales[slot * kTok + 16 * w + row8 + 8] : 0.f;
+#pragma unroll
+                        for (int c = 0; c < kGroups / 2; ++c) {
+                            float y[8];
+                            tc_ld_frag(s_col + N + c * 16, y);
+                            tc_wait_ld();
+#pragma unroll
+                            for (int g = 0; g < 2; ++g) {
+                                float* const z = &x[c * 8 + 4 * g];
+                                z[0] = fmaf(z[0], sc0, y[4 * g]);
+                                z[1] = fmaf(z[1], sc0, y[4 * g + 1]);
+                                z[2] = fmaf(z[2], sc1, y[4 * g + 2]);
+                                z[3] = fmaf(z[3], sc1, y[4 * g + 3]);
+                            }
+                        }
+                    }
+                    const bool plain = first + kTok <= see_all && !fault;
+                    if (!plain) {
+#pragma unroll
+                        for (int c = 0; c < kGroups; ++c)
+#pragma unroll
+                            for (int u = 0; u < 2; ++u) {
+                                const int lim = gone ? 0 : see(8 * c + 2 * quad + u);
+                                if (tok0 >= lim) x[4 * c + u] = -INFINITY;
+                                if (tok1 >= lim) x[4 * c + 2 + u] = -INFINITY;
+                            }
+                    }
+                    // Maxima of the warp's 16 tokens: after the exchanges lane l has those of 2 kGroups / 8 rows.
+                    float mx[2 * kGroups];
+#pragma unroll
+                    for (int c = 0; c < kGroups; ++c) {
+                        mx[2 * c] = fmaxf(x[4 * c], x[4 * c + 2]);
+                        mx[2 * c + 1] = fmaxf(x[4 * c + 1], x[4 * c + 3]);
+                    }
+#pragma unroll
+                    for (int c = 0; c < 2 * kGroups; ++c) {
+                        mx[c] = fmaxf(mx[c], __shfl_xor_sync(0xffffffffu, mx[c], 4));
+                        mx[c] = fmaxf(mx[c], __shfl_xor_sync(0xffffffffu, mx[c], 8));
+                        mx[c] = fmaxf(mx[c], __shfl_xor_sync(0xffffffffu, mx[c], 16));
+                    }
+                    if (row8 == 0) {
+#pragma unroll
+                        for (int c = 0; c < kGroups; ++c)
+                            *reinterpret_cast<float2*>(&ct->red[w][8 * c + 2 * quad]) = make_float2(mx[2 * c], mx[2 * c + 1]);
+                    }
+                    if (softmax_any(dead)) goto softmax_end;
+                    // The base of a row moves only when its maximum is more than kSlack above it; weights stay at most
+                    // 2^kSlack, and sums and outputs share the base.  Columns without a row have no say.
+                    bool move = false;
+                    if (tid < N) {
+                        const float top = fmaxf(fmaxf(ct->red[0][tid], ct->red[1][tid]), fmaxf(ct->red[2][tid], ct->red[3][tid])) * a.scale_log2;
+                        float alpha = 1.f;
+                        if (tid < rows && top > m + kSlack) {
+                            move = true;
+                            alpha = m == -INFINITY ? 0.f : ex2(m - top);   // (nothing was added yet)
+                            m = top;
+                            ct->base[tid] = m;
+                        } else if (j == 0) {
+                            ct->base[tid] = 0.f;   // a row that has seen nothing yet
+                        }
+                        ct->alpha[tid] = alpha;
+                    }
+                    const bool any = softmax_any(move);
+                    // P's memory and O are free when the product before is done.
+                    if (j > 0) LATENT_WAIT(ct->pv_done, (tile - 1) & 1);
+                    if (any || j == 0) {
+#pragma unroll
+                        for (int c = 0; c < 2 * kGroups; ++c) {
+                            const int r = 8 * (c >> 1) + 2 * quad + (c & 1);
+                            base[c] = ct->base[r];
+                            l[c] *= ct->alpha[r];
+                            lr[c] *= ct->alpha[r];
+                        }
+                        if (j > 0) {
+                            tc_fence_after();
+#pragma unroll 1
+                            for (int c = 0; c < 4 * N; c += 16) {
+                                uint32_t y[16];
+                                tc_ld16(tmem + lanes + c, y);
+                                tc_wait_ld();
+#pragma unroll
+                                for (int u = 0; u < 16; ++u) y[u] = __float_as_uint(__uint_as_float(y[u]) * ct->alpha[(c + u) % N]);
+                                tc_st16(tmem + lanes + c, y);
+                            }
+                            tc_wait_st();
+                        }
+                    }
+                    if (j > 0 && (j & (kFoldTiles - 1)) == 0) {
+                        // O moves to the fp32 sums: thread's channel 128 u + tid, row after row.
+                        tc_fence_after();
+                        softmax_sync();   // (alpha has been read)
+                        if (tid < N) {
+                            ct->alpha[tid] = folded == -INFINITY ? 0.f : ex2(folded - m);
+                            folded = m;
+                        }
+                        softmax_sync();
+#pragma unroll 1
+                        for (int c = 0; c < 4 * N; c += 16) {
+                            uint32_t y[16];
+                            tc_ld16(tmem + lanes + c, y);
+                            tc_wait_ld();
+#pragma unroll
+                            for (int u = 0; u < 16; ++u) {
+                                const int r = (c + u) % N;
+                                if (r < rows) {
+                                    float* const at = fold_to + r * kLatentDim + (c + u) / N * 128 + tid;
+                                    *at = j > kFoldTiles ? fmaf(*at, ct->alpha[r], __uint_as_float(y[u])) : __uint_as_float(y[u]);
+                                }
+                            }
+                        }
+                        softmax_sync();   // (alpha is written again)
+                    }
+                    // Weights, their sums, and P^T, a row of 64 tokens each.
+#pragma unroll
+                    for (int c = 0; c < kGroups; c += 2) {
+                        uint32_t p[4];
+#pragma unroll
+                        for (int g = 0; g < 2; ++g) {
+                            float e[4];
+#pragma unroll
+                            for (int u = 0; u < 4; ++u) e[u] = ex2(fmaf(x[4 * (c + g) + u], a.scale_log2, -base[2 * (c + g) + (u & 1)]));
+                            l[2 * (c + g)] += e[0] + e[2];
+                            l[2 * (c + g) + 1] += e[1] + e[3];
+                            if (FP8) {
+                                e[0] *= sc0;
+                                e[1] *= sc0;
+                                e[2] *= sc1;
+                                e[3] *= sc1;
+                            }
+                            p[2 * g] = pack_bf16x2(e[0], e[1]);
+                            p[2 * g + 1] = pack_bf16x2(e[2], e[3]);
+                            if (!FP8) {
+                                lr[2 * (c + g)] += bf16lo(p[2 * g]) + bf16lo(p[2 * g + 1]);
+                                lr[2 * (c + g) + 1] += bf16hi(p[2 * g]) + bf16hi(p[2 * g + 1]);
+                            }
+                        }
+                        // Blocks: tokens 16 w .. + 7 and + 8 .. + 15 of rows 8 c .., then of rows 8 (c + 1) ..
+                        const int r = 8 * (c + (lane >> 4)) + (lane & 7), chunk = 2 * w + ((lane >> 3) & 1);
+                        stmatrix_x4_trans(smem_addr(ps) + r * 128 + ((chunk ^ (r & 7)) << 4), p[0], p[1], p[2], p[3]);
+                    }
+                    // Tokens that no row sees may hold anything: their channels become zeros (P = 0 must not meet a
+                    // NaN) in the pages that the product reads.
+                    const int pages = min(kPages, s.en.npages - (s.t0 + j) * kPages);
+                    if (fault || first + pages * kPage > see_any) {
+                        for (int i = tid; i < pages * kPage * kUnits * 16; i += 128) {
+                            const int r = i >> 6, u = (i >> 4) & 3, c = i & 15;
+                            if (first + r >= see_any || ((fault >> (r / kPage)) & 1))
+                                *reinterpret_cast<uint4*>(ring + (tile * kUnits + u) % C::kRing * kUnit + (r >> 3) * 2048 + (c >> 3) * 1024 +
+                                                          (r & 7) * 128 + (c & 7) * 16) = make_uint4(0u, 0u, 0u, 0u);
+                        }
+                    }
+                    fence_proxy_async_smem();
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(smem_addr(&ct->p_full));
+                }
+
+                // ---------------- the segment's end
+                // The rows' sums: over the lanes of a row, then over the warps.
+#pragma unroll
+                for (int c = 0; c < 2 * kGroups; ++c) {
+#pragma unroll
+                    for (int d = 4; d < 32; d <<= 1) {
+                        l[c] += __shfl_xor_sync(0xffffffffu, l[c], d);
+                        lr[c] += __shfl_xor_sync(0xffffffffu, lr[c], d);
+                    }
+                }
+                float L = 0.f, R = 0.f;   // thread r < N: those of row r
+#pragma unroll
+                for (int pass = 0; pass < 2; ++pass) {
+                    softmax_sync();
+                    if (row8 == 0) {
+#pragma unroll
+                        for (int c = 0; c < kGroups; ++c)
+                            *reinterpret_cast<float2*>(&ct->red[w][8 * c + 2 * quad]) =
+                                pass ? make_float2(lr[2 * c], lr[2 * c + 1]) : make_float2(l[2 * c], l[2 * c + 1]);
+                    }
+                    softmax_sync();
+                    if (tid < N) {
+                        const float sum = ct->red[0][tid] + ct->red[1][tid] + (ct->red[2][tid] + ct->red[3][tid]);
+                        (pass ? R : L) = sum;
+                    }
+                }
+                if (FP8) R = L;
+                LATENT_WAIT(ct->pv_done, (tile - 1) & 1);
+                tc_fence_after();
+                const bool whole = s.slot < 0;
+                if (tid < N) {
+                    // A row that sees nothing is 0, whatever the others see.
+                    ct->base[tid] = whole ? (R > 0.f ? 1.f / R : R) : 1.f;
+                    ct->alpha[tid] = folded == -INFINITY ? 0.f : ex2(folded - m);
+                    if (tid < rows) {
+                        if (whole) a.lse[s.en.row0 + tid] = L > 0.f ? (m + log2f(L)) * 0.69314718055994531f : (L == 0.f ? -INFINITY : L);
+                        else a.cut_ml[static_cast<int64_t>(s.slot) * N + tid] = make_float4(m, L, R, 0.f);
+                    }
+                }
+                softmax_sync();
+                float odd = 0.f;   // NaN once a channel of a row that sees something is not finite
+#pragma unroll 1
+                for (int c = 0; c < 4 * N; c += 16) {
+                    uint32_t y[16];
+                    tc_ld16(tmem + lanes + c, y);
+                    tc_wait_ld();
+#pragma unroll
+                    for (int u = 0; u < 16; ++u) {
+                        const int r = (c + u) % N;
+                        if (r >= rows) continue;
+                        const int channel = (c + u) / N * 128 + tid;
+                        float v = __uint_as_float(y[u]);
+                        if (n > kFoldTiles) v = fmaf(fold_to[r * kLatentDim + channel], ct->alpha[r], v);
+                        const float f = ct->base[r];
+                        v = f == 0.f ? 0.f : v * f;
+                        if (whole) {
+                            odd = fmaf(v, 0.f, odd);
+                            a.out[static_cast<int64_t>(s.en.row0 + r) * kLatentDim + channel] = __float2bfloat16_rn(v);
+                        } else {
+                            a.cut_o[(static_cast<int64_t>(s.slot) * N + r) * kLatentDim + channel] = v;
+                        }
+                    }
+                }
+                // (Rows of one token see the same.)
+                if (whole && softmax_any(odd != 0.f) && tid == 0 && see_all != see_any)
+                    a.odd[atomicAdd(a.num_odd, 1)] = static_cast<uint32_t>(~s.slot) * a.share + part;
+                tc_fence_before();
+                softmax_sync();   // all have read O before the next segment's first product writes it
+                seg_done(k);
+            }
+        softmax_end:
+            // (Gave up: the rows in flight land before the CTA retires.)
+            if (tid == 0 && q_loads) (void)bar_wait(smem_addr(&ct->q_full), (q_loads - 1) & 1);
+        } else if (FP8 && warp >= 8) {
+            // ---------------- e4m3 codes -> bf16 units in the MMAs' layout
+            const int tid = threadIdx.x - 256;
+            uint32_t at = 0;
+            constexpr uint32_t kDepth = FP8 ? C::kCodes : 1;
+            for (uint32_t k = 0;; ++k) {
+                SVQ_WAIT(ct->seg_full[k % kSegs], (k / kSegs) & 1, widen_end);
+                const Seg& s = ct->seg[k % kSegs];
+                const int n = s.t1 - s.t0;
+                if (n == 0) break;
+                for (int i = 0; i < n * kUnits; ++i, ++at) {
+                    const uint32_t cs = at % kDepth, st = at % C::kRing;
+                    SVQ_WAIT(ct->code_full[cs], (at / kDepth) & 1, widen_end);
+                    // 16 codes at chunk tid % 8 of rows tid / 8 and + 32.  The fence keeps the next copy into the slot
+                    // behind these reads.
+                    const int r = tid >> 3, c = tid & 7;
+                    uint4 v[2];
+#pragma unroll
+                    for (int u = 0; u < 2; ++u)
+                        v[u] = *reinterpret_cast<const uint4*>(codes + cs * (kUnit / 2) + (r + 32 * u) * 128 + c * 16);
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(smem_addr(&ct->code_empty[cs]));
+                    uint4 lo[2], hi[2];
+                    uint32_t nan = 0;
+#pragma unroll
+                    for (int u = 0; u < 2; ++u) {
+                        nan |= has_nan(v[u].x) | has_nan(v[u].y) | has_nan(v[u].z) | has_nan(v[u].w);
+                        widen4(v[u].x, lo[u].x, lo[u].y);
+                        widen4(v[u].y, lo[u].z, lo[u].w);
+                        widen4(v[u].z, hi[u].x, hi[u].y);
+                        widen4(v[u].w, hi[u].z, hi[u].w);
+                    }
+                    if (nan) {
+#pragma unroll
+                        for (int u = 0; u < 2; ++u) {
+                            keep_nan(v[u].x, lo[u].x, lo[u].y);
+                            keep_nan(v[u].y, lo[u].z, lo[u].w);
+                            keep_nan(v[u].z, hi[u].x, hi[u].y);
+                            keep_nan(v[u].w, hi[u].z, hi[u].w);
+                        }
+                    }
+                    SVQ_WAIT(ct->empty[st], ((at / C::kRing) & 1) ^ 1, widen_end);
+#pragma unroll
+                    for (int u = 0; u < 2; ++u) {
+                        const int rr = r + 32 * u;
+                        unsigned char* const o = ring + st * kUnit + (rr >> 3) * 2048 + (c >> 2) * 1024 + (rr & 7) * 128;
+                        *reinterpret_cast<uint4*>(o + (((2 * c) & 7 ^ (rr & 7)) << 4)) = lo[u];
+                        *reinterpret_cast<uint4*>(o + (((2 * c + 1) & 7 ^ (rr & 7)) << 4)) = hi[u];
+                    }
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(smem_addr(&ct->full[st]));
+                }
+                seg_done(k);
+            }
+        widen_end:;
+        }
+    }
+    __threadfence();
+    __syncthreads();
+    if (warp == 1)
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem));
+}
+
+// ---------------------------------------------------------------- plan
+constexpr int kPlanThreads = 1024;
+
+// One CTA: the list of entries, and the running sum of their costs.
+__global__ void __launch_bounds__(kPlanThreads) latent_plan_kernel(const __grid_constant__ LatentArgs a) {
+    __shared__ int64_t warp_sums[32];
+    const int tid = threadIdx.x, lane = tid & 31;
+    int64_t total;
+    pdl_wait();   // the workspace may still be read by the call before
+    pdl_launch_dependents();
+    const int rows_per = a.share * a.tile_rows;
+    auto range = [&](int b, int& q0, int& q1) {
+        q0 = a.q_start ? a.q_start[b] : b;
+        q1 = a.q_start ? a.q_start[b + 1] : b + 1;
+        return q0 >= 0 && q1 >= q0 && q1 <= a.total_q;
+    };
+    int n = 0;
+    for (int i0 = 0; i0 < a.batch; i0 += kPlanThreads) {
+        const int i = i0 + tid;
+        int count = 0;
+        if (i < a.batch) {
+            int q0, q1;
+            if (!range(i, q0, q1)) svq_flag(SV_DEVERR_Q_START);
+            else count = static_cast<int>((static_cast<int64_t>(q1 - q0) * a.heads + rows_per - 1) / rows_per);
+        }
+        const int64_t before = n + block_scan(count, warp_sums, total);
+        // (Broken starts that overlap could list more entries than the workspace holds.)
+        if (i < a.batch) a.req_first[i] = static_cast<int>(min(before, static_cast<int64_t>(a.max_entries)));
+        n = static_cast<int>(min(n + total, static_cast<int64_t>(INT_MAX / 2)));
+    }
+    if (n > a.max_entries) {
+        if (tid == 0) svq_flag(SV_DEVERR_Q_START);
+        n = a.max_entries;
+    }
+    __syncthreads();
+    int64_t base = 0;
+    for (int e0 = 0; e0 < n; e0 += kPlanThreads) {
+        const int e = e0 + tid;
+        Entry en = {0, 0, 0, 0, 0, 0, {0, 0}};
+        bool empty = false;   // rows that see nothing
+        if (e < n) {
+            const int b = find_le(a.req_first, a.batch, e);
+            int q0, q1;
+            (void)range(b, q0, q1);
+            int len = a.seq_lens[b];
+            if (len < 0 || (static_cast<int64_t>(len) + kPage - 1) / kPage > a.max_pages) {
+                svq_flag(SV_DEVERR_SEQ_LEN);
+                len = 0;
+            } else if (len > 0 && q1 - q0 > len) {
+                svq_flag(SV_DEVERR_Q_START);
+                len = 0;
+            }
+            const int64_t row0 = static_cast<int64_t>(q0) * a.heads + static_cast<int64_t>(e - a.req_first[b]) * rows_per;
+            en.row0 = static_cast<int>(row0);
+            en.nrows = static_cast<int>(min(static_cast<int64_t>(rows_per), static_cast<int64_t>(q1) * a.heads - row0));
+            en.posbase = len - q1;
+            en.req = b;
+            if (len > 0) en.npages = (en.posbase + (en.row0 + en.nrows - 1) / a.heads) / kPage + 1;
+            empty = len == 0;
+        }
+        en.tiles = (en.npages + kPages - 1) / kPages;
+        const int64_t before = base + block_scan(cost_of_entry(en.tiles), warp_sums, total);
+        base += total;
+        if (e < n) {
+            a.entries[e] = en;
+            a.cum[e] = before;
+        }
+        for (uint32_t rest = __ballot_sync(0xffffffffu, empty); rest; rest &= rest - 1) {
+            const int src = __ffs(rest) - 1;
+            const int64_t r0 = __shfl_sync(0xffffffffu, en.row0, src);
+            const int64_t r1 = r0 + __shfl_sync(0xffffffffu, en.nrows, src);
+            uint4* o = reinterpret_cast<uint4*>(a.out + r0 * kLatentDim);
+            for (int64_t i = lane; i < (r1 - r0) * (kLatentDim / 8); i += 32) o[i] = make_uint4(0u, 0u, 0u, 0u);
+            for (int64_t i = r0 + lane; i < r1; i += 32) a.lse[i] = -INFINITY;
+        }
+    }
+    if (tid == 0) {
+        a.cum[n] = base;
+        *a.num_entries = n;
+        *a.num_odd = 0;
+    }
+}
+
+// ---------------------------------------------------------------- joining partials
 __device__ __forceinline__ void unpack8(const uint4& v, float* f) {
     const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
@@ -43,118 +1007,315 @@ __device__ __forceinline__ void unpack8(const uint4& v, float* f) {
     }
 }
 
-template <bool FP8>
-__global__ void __launch_bounds__(kThreads) latent_rows_kernel(const __grid_constant__ LatentArgs a) {
+// A row whose outputs may not be finite, by one warp (lane l: channels 16 l .. and
+// rotary channels 2 l, 2 l + 1).  The tile's product multiplies every latent of
+// the tile with a weight, and a weight 0 does not hide an infinite or NaN latent
+// from the rows that do not see its token.  So if the row's logits are finite, its
+// outputs are not, and a token that other rows of the entry see and this one does
+// not holds such a value, the row is computed again from its own tokens alone.
+__device__ __noinline__ void look_at_row(const LatentArgs& a, int entry, int row) {
     const int lane = threadIdx.x & 31;
-    pdl_wait();
-    const int64_t rows = static_cast<int64_t>(a.total_q) * a.heads;
-    if (blockIdx.x == 0) {
-        for (int b = threadIdx.x; b < a.batch; b += kThreads) {
-            const int q0 = a.q_start ? a.q_start[b] : b, q1 = a.q_start ? a.q_start[b + 1] : b + 1;
-            const int len = a.seq_lens[b];
-            if (q0 < 0 || q1 < q0 || q1 > a.total_q) svq_flag(SV_DEVERR_Q_START);
-            else if (len < 0 || (static_cast<int64_t>(len) + kPage - 1) / kPage > a.max_pages) svq_flag(SV_DEVERR_SEQ_LEN);
-            else if (len > 0 && q1 - q0 > len) svq_flag(SV_DEVERR_Q_START);
-        }
+    const Entry en = a.entries[entry];
+    const int end = en.posbase + row / a.heads + 1;
+    const int last = en.posbase + (en.row0 + en.nrows - 1) / a.heads + 1;
+    float got[16];
+    uint4* const to = reinterpret_cast<uint4*>(a.out + static_cast<int64_t>(row) * kLatentDim + 16 * lane);
+    unpack8(to[0], got);
+    unpack8(to[1], got + 8);
+    {
+        float odd = 0.f;
+#pragma unroll
+        for (int e = 0; e < 16; ++e) odd = fmaf(got[e], 0.f, odd);
+        if (!(fabsf(a.lse[row]) < INFINITY) || !__any_sync(0xffffffffu, odd != 0.f)) return;
     }
-    for (int64_t row = static_cast<int64_t>(blockIdx.x) * (kThreads / 32) + (threadIdx.x >> 5); row < rows;
-         row += static_cast<int64_t>(gridDim.x) * (kThreads / 32)) {
-        const int tok = static_cast<int>(row / a.heads);
-        const int b = a.q_start ? find_le(a.q_start, a.batch, tok) : tok;
-        const int q0 = a.q_start ? a.q_start[b] : b, q1 = a.q_start ? a.q_start[b + 1] : b + 1;
-        if (q0 < 0 || tok < q0 || tok >= q1 || q1 > a.total_q) continue;
-        const int len = a.seq_lens[b];
-        int end = 0;   // tokens seen
-        if (len > 0 && (static_cast<int64_t>(len) + kPage - 1) / kPage <= a.max_pages && q1 - q0 <= len) end = len - (q1 - tok) + 1;
-        float q[18], o[16], m = -INFINITY, l = 0.f;
-        const __nv_bfloat16* const qr = a.q + row * kQueryDim;
-        unpack8(*reinterpret_cast<const uint4*>(qr + 16 * lane), q);
-        unpack8(*reinterpret_cast<const uint4*>(qr + 16 * lane + 8), q + 8);
-        const uint32_t qw = *reinterpret_cast<const uint32_t*>(qr + kLatentDim + 2 * lane);
-        q[16] = bf16lo(qw);
-        q[17] = bf16hi(qw);
+    const int32_t* const pages = a.page_table + static_cast<int64_t>(en.req) * a.max_pages;
+    auto place_of = [&](int t) {
+        const int64_t ph = pages[t / kPage];
+        return ph < 0 || ph >= a.num_pages ? -1ll : ph * kPage + t % kPage;
+    };
+    auto latent = [&](int64_t s, float (&c)[16]) {
+        if (a.fp8) {
+            const uint4 v = *reinterpret_cast<const uint4*>(a.pool + s * kLatentDim + 16 * lane);
+            const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+            const float sc = a.scale[s];
 #pragma unroll
-        for (int e = 0; e < 16; ++e) o[e] = 0.f;
-        for (int j = 0; j < end; ++j) {
-            const int64_t page = a.page_table[static_cast<int64_t>(b) * a.max_pages + j / kPage];
-            if (page < 0 || page >= a.num_pages) {
-                if (lane == 0) svq_flag(SV_DEVERR_PAGE_TABLE);
-                continue;
+            for (int e = 0; e < 4; ++e) {
+                uint32_t lo, hi;
+                widen4(w[e], lo, hi);
+                keep_nan(w[e], lo, hi);
+                c[4 * e] = bf16lo(lo) * sc;
+                c[4 * e + 1] = bf16hi(lo) * sc;
+                c[4 * e + 2] = bf16lo(hi) * sc;
+                c[4 * e + 3] = bf16hi(hi) * sc;
             }
-            const int64_t s = page * kPage + j % kPage;
-            float c[16];
-            if (FP8) {
-                const uint4 v = *reinterpret_cast<const uint4*>(a.pool + s * kLatentDim + 16 * lane);
-                const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-                const float sc = a.scale[s];
-#pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(
-                        static_cast<__nv_fp8x2_storage_t>((w[e >> 1] >> (16 * (e & 1))) & 0xffffu), __NV_E4M3);
-                    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h));
-                    c[2 * e] = f.x * sc;
-                    c[2 * e + 1] = f.y * sc;
-                }
-            } else {
-                const uint4* const from = reinterpret_cast<const uint4*>(a.pool + s * (2 * kLatentDim) + 32 * lane);
-                unpack8(from[0], c);
-                unpack8(from[1], c + 8);
-            }
-            const uint32_t rw = *reinterpret_cast<const uint32_t*>(a.rope + s * kRopeDim + 2 * lane);
-            float z = q[16] * bf16lo(rw) + q[17] * bf16hi(rw);
-#pragma unroll
-            for (int e = 0; e < 16; ++e) z = fmaf(q[e], c[e], z);
-#pragma unroll
-            for (int d = 16; d; d >>= 1) z += __shfl_xor_sync(0xffffffffu, z, d);
-            z *= a.scale_log2;
-            const float mn = fmaxf(m, z), base = mn == -INFINITY ? 0.f : mn;
-            const float e = ex2(m - base), p = ex2(z - base);
-            m = mn;
-            l = l * e + p;
-#pragma unroll
-            for (int k = 0; k < 16; ++k) o[k] = fmaf(p, c[k], o[k] * e);
+        } else {
+            const uint4* const from = reinterpret_cast<const uint4*>(a.pool + s * (2 * kLatentDim) + 32 * lane);
+            unpack8(from[0], c);
+            unpack8(from[1], c + 8);
         }
-        const float inv = l != 0.f ? 1.f / l : 0.f;
-        uint32_t w[8];
+    };
+    float c[16];
+    if (const int64_t s = place_of(end - 1); s >= 0) {
+        // The row's own token is NaN wherever the row is not finite (a whole cache of NaN): so is the result.
+        latent(s, c);
+        bool known = true;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) w[e] = l != 0.f ? pack_bf16x2(o[2 * e] * inv, o[2 * e + 1] * inv) : 0u;
-        uint4* const to = reinterpret_cast<uint4*>(a.out + row * kLatentDim + 16 * lane);
-        to[0] = make_uint4(w[0], w[1], w[2], w[3]);
-        to[1] = make_uint4(w[4], w[5], w[6], w[7]);
-        if (lane == 0) a.lse[row] = l > 0.f ? (m + log2f(l)) * 0.69314718055994531f : (l == 0.f ? -INFINITY : l);
+        for (int e = 0; e < 16; ++e) known &= c[e] != c[e] || got[e] * 0.f == 0.f;
+        if (__all_sync(0xffffffffu, known)) return;
+    }
+    float odd = 0.f;   // of the tokens that other rows see and this one does not
+    for (int t = end; t < last; ++t) {
+        const int64_t s = place_of(t);
+        if (s < 0) continue;
+        latent(s, c);
+#pragma unroll
+        for (int e = 0; e < 16; ++e) odd = fmaf(c[e], 0.f, odd);
+    }
+    if (!__any_sync(0xffffffffu, odd != 0.f)) return;   // the row's own tokens gave it
+    float q[16], o[16], m = -INFINITY, l = 0.f;
+    const __nv_bfloat16* const qr = a.q + static_cast<int64_t>(row) * kQueryDim;
+    unpack8(*reinterpret_cast<const uint4*>(qr + 16 * lane), q);
+    unpack8(*reinterpret_cast<const uint4*>(qr + 16 * lane + 8), q + 8);
+    const uint32_t qw = *reinterpret_cast<const uint32_t*>(qr + kLatentDim + 2 * lane);
+#pragma unroll
+    for (int e = 0; e < 16; ++e) o[e] = 0.f;
+    for (int t = 0; t < end; ++t) {
+        const int64_t s = place_of(t);
+        if (s < 0) continue;
+        latent(s, c);
+        const uint32_t rw = *reinterpret_cast<const uint32_t*>(a.rope + s * kRopeDim + 2 * lane);
+        float z = bf16lo(qw) * bf16lo(rw) + bf16hi(qw) * bf16hi(rw);
+#pragma unroll
+        for (int e = 0; e < 16; ++e) z = fmaf(q[e], c[e], z);
+#pragma unroll
+        for (int d = 16; d; d >>= 1) z += __shfl_xor_sync(0xffffffffu, z, d);
+        z *= a.scale_log2;
+        const float mn = fmaxf(m, z), base = mn == -INFINITY ? 0.f : mn;
+        const float f = ex2(m - base), p = ex2(z - base);
+        m = mn;
+        l = l * f + p;
+#pragma unroll
+        for (int e = 0; e < 16; ++e) o[e] = fmaf(p, c[e], o[e] * f);
+    }
+    const float inv = l != 0.f ? 1.f / l : 0.f;
+    uint32_t w[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) w[e] = l != 0.f ? pack_bf16x2(o[2 * e] * inv, o[2 * e + 1] * inv) : 0u;
+    to[0] = make_uint4(w[0], w[1], w[2], w[3]);
+    to[1] = make_uint4(w[4], w[5], w[6], w[7]);
+    if (lane == 0) a.lse[row] = l > 0.f ? (m + log2f(l)) * 0.69314718055994531f : (l == 0.f ? -INFINITY : l);
+}
+
+// CTA (c, y) joins the entry that group c + 1 goes on with, a row at a time (rows
+// y, y + gridDim.y, ...): thread i channels 4 i .. 4 i + 3.  Then the row tiles of
+// whole entries with values that are not finite.
+constexpr int kJoinThreads = 128;
+
+__global__ void __launch_bounds__(kJoinThreads) latent_join_kernel(const __grid_constant__ LatentArgs a) {
+    const int tid = threadIdx.x, warp = tid >> 5;
+    pdl_wait();
+    const int N = a.tile_rows;
+    const int64_t total = a.cum[*a.num_entries];
+    const int groups = groups_of(total, gridDim.x + 1);
+    const int c = blockIdx.x + 1;
+    const int4 what = c < groups ? a.cut_item[2 * c] : make_int4(0, 0, 0, 0);
+    const int num_odd = *a.num_odd;
+    const int pieces = what.z;
+    const int4 where = pieces ? a.cut_item[2 * c + 1] : what;
+    for (int r = blockIdx.y; pieces && r < what.y; r += gridDim.y) {
+        const int part = r / N, tr = r - part * N;
+        // Slots count CTAs: group g's part p is CTA g * share + p.
+        auto row_of = [&](int k) {
+            const int slot = k == 0 ? where.x : where.y + 2 * (k - 1);
+            return (static_cast<int64_t>(2 * ((slot >> 1) * a.share + part) + (slot & 1))) * N + tr;
+        };
+        float m = -INFINITY, l = 0.f, lr = 0.f;
+        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int k0 = 0; k0 < pieces; k0 += 4) {
+            float4 ml[4], x[4];
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+                const bool on = k0 + u < pieces;
+                ml[u] = on ? a.cut_ml[row_of(k0 + u)] : make_float4(-INFINITY, 0.f, 0.f, 0.f);
+                x[u] = on ? *reinterpret_cast<const float4*>(a.cut_o + row_of(k0 + u) * kLatentDim + 4 * tid) : make_float4(0.f, 0.f, 0.f, 0.f);
+            }
+            float mn = m;
+#pragma unroll
+            for (int u = 0; u < 4; ++u) mn = fmaxf(mn, ml[u].x);
+            const float base = mn == -INFINITY ? 0.f : mn;   // pieces without a visible token: weights 0
+            const float e = ex2(m - base);
+            m = mn;
+            l *= e;
+            lr *= e;
+            o.x *= e, o.y *= e, o.z *= e, o.w *= e;
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+                const float f = ex2(ml[u].x - base);
+                l = fmaf(ml[u].y, f, l);
+                lr = fmaf(ml[u].z, f, lr);
+                o.x = fmaf(x[u].x, f, o.x);
+                o.y = fmaf(x[u].y, f, o.y);
+                o.z = fmaf(x[u].z, f, o.z);
+                o.w = fmaf(x[u].w, f, o.w);
+            }
+        }
+        const float inv = lr > 0.f ? 1.f / lr : lr;
+        uint2 v = make_uint2(0u, 0u);
+        if (lr != 0.f) {
+            v.x = pack_bf16x2(o.x * inv, o.y * inv);
+            v.y = pack_bf16x2(o.z * inv, o.w * inv);
+        }
+        const int row = what.x + r;
+        *reinterpret_cast<uint2*>(a.out + static_cast<int64_t>(row) * kLatentDim + 4 * tid) = v;
+        if (tid == 0) a.lse[row] = l > 0.f ? (m + log2f(l)) * 0.69314718055994531f : (l == 0.f ? -INFINITY : l);
+        const float odd = fmaf(o.x, 0.f, fmaf(o.y, 0.f, fmaf(o.z, 0.f, o.w * 0.f)));
+        if (__syncthreads_or(odd != 0.f && l > 0.f && l < INFINITY) && warp == 0) look_at_row(a, what.w, row);
+    }
+    for (int64_t i = blockIdx.y * gridDim.x + blockIdx.x; i < static_cast<int64_t>(num_odd) * (N / 4); i += gridDim.x * gridDim.y) {
+        const uint32_t id = a.odd[i / (N / 4)];
+        const int e = id / a.share, r = static_cast<int>(id % a.share) * N + static_cast<int>(i % (N / 4)) * 4 + warp;
+        if (r < a.entries[e].nrows) look_at_row(a, e, a.entries[e].row0 + r);
     }
     __threadfence();
 }
 
+// ---------------------------------------------------------------- host side
+size_t up(size_t n) { return (n + 255) / 256 * 256; }
+
+struct Layout {
+    size_t entries, cum, num, req_first, cut_item, cut_o, cut_ml, odd, num_odd, total;
+    int tile_rows, share, max_entries;
+    Layout(int64_t batch, int64_t total_q, int heads) {
+        // Rows of a CTA: as many as a request has at the most if each has one query token, else 64; two CTAs side by
+        // side take the rows of a token or a chunk that has more.
+        const int64_t rows = total_q <= batch ? heads : static_cast<int64_t>(total_q) * heads;
+        tile_rows = rows <= 16 ? 16 : (rows <= 32 ? 32 : 64);
+        share = rows <= 64 ? 1 : 2;
+        const int64_t e = total_q * heads / (share * tile_rows) + batch;
+        max_entries = static_cast<int>(e);
+        size_t at = 0;
+        auto take = [&](size_t bytes) { const size_t r = at; at += up(bytes); return r; };
+        entries = take(e * sizeof(Entry));
+        cum = take((e + 1) * sizeof(int64_t));
+        num = take(sizeof(int));
+        req_first = take(batch * sizeof(int));
+        cut_item = take(2 * kMaxCtas * sizeof(int4));
+        cut_o = take(2ull * kMaxCtas * tile_rows * kLatentDim * sizeof(float));
+        cut_ml = take(2ull * kMaxCtas * tile_rows * sizeof(float4));
+        odd = take(e * share * sizeof(uint32_t));
+        num_odd = take(sizeof(int));
+        total = at + 256;   // the parts begin at the workspace's first multiple of 256
+    }
+};
+
+bool encode(CUtensorMap* map, CUtensorMapDataType type, const void* p, int rank, const cuuint64_t* dims, const cuuint64_t* strides,
+            const cuuint32_t* box, CUtensorMapSwizzle swizzle) {
+    auto enc = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(tensor_map_encode_entry());
+    const cuuint32_t ones[4] = {1, 1, 1, 1};
+    return enc && enc(map, type, rank, const_cast<void*>(p), dims, strides, box, ones, CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle,
+                      CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// Rows of 64 bf16 channels blocks, `rows` of them a box.
+bool encode_rows(CUtensorMap* map, const void* p, int channels, int64_t n, int rows) {
+    const cuuint64_t dims[2] = {static_cast<cuuint64_t>(channels), static_cast<cuuint64_t>(n)};
+    const cuuint64_t strides[1] = {static_cast<cuuint64_t>(channels) * 2};
+    const cuuint32_t box[2] = {64, static_cast<cuuint32_t>(rows)};
+    return encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, p, 2, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B);
+}
+// A page's latents: bf16 in boxes of 128 channels that land as [8-row group][64-channel half][8 rows of 128 bytes], each
+// 1 KB swizzled; codes in boxes of 128.
+bool encode_latents(CUtensorMap* map, const void* p, int64_t pages, bool fp8) {
+    if (fp8) {
+        const cuuint64_t dims[2] = {kLatentDim, static_cast<cuuint64_t>(pages) * kPage};
+        const cuuint64_t strides[1] = {kLatentDim};
+        const cuuint32_t box[2] = {128, kPage};
+        return encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, p, 2, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_NONE);
+    }
+    const cuuint64_t dims[4] = {64, 8, kLatentDim / 64, static_cast<cuuint64_t>(pages) * 2};
+    const cuuint64_t strides[3] = {2 * kLatentDim, 128, 16 * kLatentDim};
+    const cuuint32_t box[4] = {64, 8, 2, 2};
+    return encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, p, 4, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B);
+}
+
+template <int N, bool FP8>
+int launch_tiles(const LatentArgs& a, const CUtensorMap& tq, const CUtensorMap& tc, const CUtensorMap& tr, int ctas, cudaStream_t stream) {
+    static std::atomic<bool> attr_set[64];
+    const int st = once_per_device(attr_set, [] {
+        return cudaFuncSetAttribute(latent_kernel<N, FP8>, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<N, FP8>::kSmem) ==
+                       cudaSuccess
+                   ? SV_OK
+                   : SV_ERR_CUDA;
+    });
+    if (st) return st;
+    return launch_pdl(latent_kernel<N, FP8>, dim3(ctas), dim3(Cfg<N, FP8>::kThreads), Cfg<N, FP8>::kSmem, stream, a, tq, tc, tr) ==
+                   cudaSuccess
+               ? SV_OK
+               : SV_ERR_CUDA;
+}
+
 }  // namespace
 
-size_t latent_workspace_bytes(int, int, int) { return 256; }
+size_t latent_workspace_bytes(int batch, int num_q_heads, int total_q) { return Layout(batch, total_q, num_q_heads).total; }
 
 int launch_latent_attention(const sv_cache* c, const void* q, int num_q_heads, const int32_t* q_start, int total_q,
                             const int32_t* page_table, const int32_t* seq_lens, int batch, int max_pages,
-                            float softmax_scale, void* out, float* lse, void* /*workspace*/, int sm_count,
+                            float softmax_scale, void* out, float* lse, void* workspace, int sm_count,
                             cudaStream_t stream) {
-    const LatentArgs a = {static_cast<const __nv_bfloat16*>(q),
-                          num_q_heads,
-                          q_start,
-                          total_q,
-                          page_table,
-                          seq_lens,
-                          batch,
-                          max_pages,
-                          c->num_phys_pages,
-                          static_cast<const unsigned char*>(c->k_pool),
-                          static_cast<const __nv_bfloat16*>(c->v_pool),
-                          static_cast<const float*>(c->k_scale),
-                          softmax_scale * 1.4426950408889634f,
-                          static_cast<__nv_bfloat16*>(out),
-                          lse};
-    const int64_t want = (static_cast<int64_t>(total_q) * num_q_heads + kThreads / 32 - 1) / (kThreads / 32);
-    const dim3 grid(static_cast<unsigned>(want < sm_count * 8 ? want : sm_count * 8));
-    const cudaError_t e = c->kv_format == SV_KV_LATENT_E4M3
-                              ? launch_pdl(latent_rows_kernel<true>, grid, dim3(kThreads), 0, stream, a)
-                              : launch_pdl(latent_rows_kernel<false>, grid, dim3(kThreads), 0, stream, a);
-    return e == cudaSuccess ? SV_OK : SV_ERR_CUDA;
+    const Layout lay(batch, total_q, num_q_heads);
+    unsigned char* const ws =
+        reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(workspace) + 255) & ~static_cast<uintptr_t>(255));
+    LatentArgs a = {};
+    a.q = static_cast<const __nv_bfloat16*>(q);
+    a.heads = num_q_heads;
+    a.q_start = q_start;
+    a.total_q = total_q;
+    a.page_table = page_table;
+    a.seq_lens = seq_lens;
+    a.batch = batch;
+    a.max_pages = max_pages;
+    a.num_pages = c->num_phys_pages;
+    a.pool = static_cast<const unsigned char*>(c->k_pool);
+    a.rope = static_cast<const __nv_bfloat16*>(c->v_pool);
+    a.scale = static_cast<const float*>(c->k_scale);
+    a.fp8 = c->kv_format == SV_KV_LATENT_E4M3;
+    a.scale_log2 = softmax_scale * 1.4426950408889634f;
+    a.out = static_cast<__nv_bfloat16*>(out);
+    a.lse = lse;
+    a.share = lay.share;
+    a.tile_rows = lay.tile_rows;
+    a.entries = reinterpret_cast<Entry*>(ws + lay.entries);
+    a.cum = reinterpret_cast<int64_t*>(ws + lay.cum);
+    a.num_entries = reinterpret_cast<int*>(ws + lay.num);
+    a.req_first = reinterpret_cast<int*>(ws + lay.req_first);
+    a.max_entries = lay.max_entries;
+    a.cut_o = reinterpret_cast<float*>(ws + lay.cut_o);
+    a.cut_ml = reinterpret_cast<float4*>(ws + lay.cut_ml);
+    a.cut_item = reinterpret_cast<int4*>(ws + lay.cut_item);
+    a.odd = reinterpret_cast<uint32_t*>(ws + lay.odd);
+    a.num_odd = reinterpret_cast<int*>(ws + lay.num_odd);
+    CUtensorMap tq, tc, tr;
+    if (!encode_rows(&tq, q, kQueryDim, static_cast<int64_t>(total_q) * num_q_heads, lay.tile_rows) ||
+        !encode_latents(&tc, c->k_pool, c->num_phys_pages, a.fp8) ||
+        !encode_rows(&tr, c->v_pool, kRopeDim, c->num_phys_pages * kPage, kPage))
+        return SV_ERR_CUDA;
+    if (launch_pdl(latent_plan_kernel, dim3(1), dim3(kPlanThreads), 0, stream, a) != cudaSuccess) return SV_ERR_CUDA;
+    const int groups = (sm_count < kMaxCtas ? sm_count : kMaxCtas) / lay.share;
+    const int ctas = groups * lay.share;
+    int st;
+    if (a.fp8)
+        st = lay.tile_rows == 16   ? launch_tiles<16, true>(a, tq, tc, tr, ctas, stream)
+             : lay.tile_rows == 32 ? launch_tiles<32, true>(a, tq, tc, tr, ctas, stream)
+                                   : launch_tiles<64, true>(a, tq, tc, tr, ctas, stream);
+    else
+        st = lay.tile_rows == 16   ? launch_tiles<16, false>(a, tq, tc, tr, ctas, stream)
+             : lay.tile_rows == 32 ? launch_tiles<32, false>(a, tq, tc, tr, ctas, stream)
+                                   : launch_tiles<64, false>(a, tq, tc, tr, ctas, stream);
+    if (st || groups < 2) return st;
+    const int rows = lay.share * lay.tile_rows;
+    return launch_pdl(latent_join_kernel, dim3(groups - 1, rows < 16 ? rows : 16), dim3(kJoinThreads), 0, stream, a) == cudaSuccess
+               ? SV_OK
+               : SV_ERR_CUDA;
 }
 
 }  // namespace svq
