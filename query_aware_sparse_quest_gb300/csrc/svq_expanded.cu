@@ -21,7 +21,7 @@
 //   warp 0       loads keys, warp 3 values: a ring of 8 blocks of 16 KB (TMA), of
 //                64 channels x 128 tokens (keys) and 128 channels x 64 tokens
 //                (values), so that each is freed when its products are done
-//   warp 1       issues the MMAs (one thread)
+//   warp 1       issues the MMAs
 //   warp 2       walks the plan
 //   warps 4-7    softmax of stream 0, one row a thread; warps 8-11 of stream 1
 // Two streams keep the tensor cores busy while the other's softmax runs: the two
@@ -100,29 +100,29 @@ struct ExpandedArgs {
     int slot_rows;
 };
 
-// S (+)= Q K^T over 64 channels: 16 of them are 32 bytes further in the rows.
-__device__ __forceinline__ void mma_qk4(uint32_t d, uint32_t q_lo, uint32_t k_lo, uint32_t idesc, uint32_t acc) {
+// S (+)= Q K^T over 64 channels: 16 of them are 32 bytes further in the rows.  By the whole warp, as the others.
+__device__ __forceinline__ void mma_qk4(uint32_t d, uint32_t q_lo, uint32_t k_lo, uint32_t idesc, uint32_t acc, uint32_t go) {
     asm volatile(
-        "{\n\t.reg .pred acc, yes;\n\t.reg .b32 al, bl;\n\t.reg .b64 ad, bd;\n\t"
-        "setp.ne.u32 acc, %6, 0;\n\tsetp.eq.u32 yes, 0, 0;\n\t"
-        SVQ_MMA_SS(0, 0, acc) SVQ_MMA_SS(2, 2, yes) SVQ_MMA_SS(4, 4, yes) SVQ_MMA_SS(6, 6, yes)
-        "}" ::"r"(d), "r"(q_lo), "r"(k_lo), "r"(desc_hi(1024)), "r"(desc_hi(1024)), "r"(idesc), "r"(acc)
+        "{\n\t.reg .pred acc, yes, go;\n\t.reg .b32 al, bl;\n\t.reg .b64 ad, bd;\n\t"
+        "setp.ne.u32 acc, %6, 0;\n\tsetp.ne.u32 go, %7, 0;\n\tsetp.eq.u32 yes, 0, 0;\n\t"
+        SVQ_MMA_SS_IF(0, 0, acc) SVQ_MMA_SS_IF(2, 2, yes) SVQ_MMA_SS_IF(4, 4, yes) SVQ_MMA_SS_IF(6, 6, yes)
+        "}" ::"r"(d), "r"(q_lo), "r"(k_lo), "r"(desc_hi(1024)), "r"(desc_hi(1024)), "r"(idesc), "r"(acc), "r"(go)
         : "memory");
 }
 // O (+)= P V over 64 tokens: 16 of them are 8 TMEM columns and 2 KB.
-__device__ __forceinline__ void mma_pv4(uint32_t d, uint32_t p, uint32_t v_lo, uint32_t idesc, uint32_t acc) {
+__device__ __forceinline__ void mma_pv4(uint32_t d, uint32_t p, uint32_t v_lo, uint32_t idesc, uint32_t acc, uint32_t go) {
     asm volatile(
-        "{\n\t.reg .pred acc, yes;\n\t.reg .b32 al, bl;\n\t.reg .b64 bd;\n\t"
-        "setp.ne.u32 acc, %5, 0;\n\tsetp.eq.u32 yes, 0, 0;\n\t"
-        SVQ_MMA_TS(0, 0, acc) SVQ_MMA_TS(8, 128, yes) SVQ_MMA_TS(16, 256, yes) SVQ_MMA_TS(24, 384, yes)
-        "}" ::"r"(d), "r"(p), "r"(v_lo), "r"(desc_hi(1024)), "r"(idesc), "r"(acc)
+        "{\n\t.reg .pred acc, yes, go;\n\t.reg .b32 al, bl;\n\t.reg .b64 bd;\n\t"
+        "setp.ne.u32 acc, %5, 0;\n\tsetp.ne.u32 go, %6, 0;\n\tsetp.eq.u32 yes, 0, 0;\n\t"
+        SVQ_MMA_TS_IF(0, 0, acc) SVQ_MMA_TS_IF(8, 128, yes) SVQ_MMA_TS_IF(16, 256, yes) SVQ_MMA_TS_IF(24, 384, yes)
+        "}" ::"r"(d), "r"(p), "r"(v_lo), "r"(desc_hi(1024)), "r"(idesc), "r"(acc), "r"(go)
         : "memory");
 }
-__device__ __forceinline__ void mma_pv1(uint32_t d, uint32_t p, uint32_t v_lo, uint32_t idesc, uint32_t acc) {
+__device__ __forceinline__ void mma_pv1(uint32_t d, uint32_t p, uint32_t v_lo, uint32_t idesc, uint32_t acc, uint32_t go) {
     asm volatile(
-        "{\n\t.reg .pred acc;\n\t.reg .b32 al, bl;\n\t.reg .b64 bd;\n\tsetp.ne.u32 acc, %5, 0;\n\t"
-        SVQ_MMA_TS(0, 0, acc)
-        "}" ::"r"(d), "r"(p), "r"(v_lo), "r"(desc_hi(1024)), "r"(idesc), "r"(acc)
+        "{\n\t.reg .pred acc, go;\n\t.reg .b32 al, bl;\n\t.reg .b64 bd;\n\tsetp.ne.u32 acc, %5, 0;\n\tsetp.ne.u32 go, %6, 0;\n\t"
+        SVQ_MMA_TS_IF(0, 0, acc)
+        "}" ::"r"(d), "r"(p), "r"(v_lo), "r"(desc_hi(1024)), "r"(idesc), "r"(acc), "r"(go)
         : "memory");
 }
 // bf16 x bf16 -> fp32, M = 128, N = 128, A K-major; B K-major (keys) or N-major (values).
@@ -222,9 +222,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    const uint32_t tmem = ct->tmem;
+    const uint32_t tmem = uniform(ct->tmem);
     // Every role takes the segments in order: the k-th is in slot k % kSegs.
-    auto seg_wait = [&](uint32_t k) { return bar_wait(smem_addr(&ct->seg_full[k % kSegs]), (k / kSegs) & 1); };
     auto seg_done = [&](uint32_t k) {   // once a warp
         __syncwarp();
         if (lane == 0) mbar_arrive(smem_addr(&ct->seg_empty[k % kSegs]));
@@ -317,25 +316,30 @@ __global__ void __launch_bounds__(kThreads, 1)
                 (void)bar_wait(smem_addr(&ct->full[x % kBlocks]), (x / kBlocks) & 1);
         values_done:;
         } else if (warp == 1) {
-            // ---------------- MMAs (one thread)
+            // ---------------- MMAs: the whole warp, in step
             reg_dec<kOtherRegs>();
-            if (lane == 0) {
+            {
+                const uint32_t go = elected();
                 uint32_t ld = 0;
                 uint32_t q_ph = 0, p_ph = 0;   // bit w: stream w's phase
                 const uint32_t ring_s = smem_addr(ring), qs_s = smem_addr(qs);
-                auto ready = [&](uint32_t i) { return bar_wait(smem_addr(&ct->full[i % kBlocks]), (i / kBlocks) & 1); };
+                auto wait = [&](uint64_t& bar, uint32_t parity) { return __all_sync(0xffffffffu, bar_wait(smem_addr(&bar), parity)) != 0; };
+                auto commit = [&](uint64_t& bar) {
+                    if (go) mma_commit(smem_addr(&bar));
+                };
+                auto ready = [&](uint32_t i) { return wait(ct->full[i % kBlocks], (i / kBlocks) & 1); };
                 auto block = [&](uint32_t i) { return ring_s + i % kBlocks * kBlock; };
-                auto release = [&](uint32_t i) { mma_commit(smem_addr(&ct->empty[i % kBlocks])); };
+                auto release = [&](uint32_t i) { commit(ct->empty[i % kBlocks]); };
                 // Blocks are waited for where a stream is the first to read them, and freed where one is the last.
                 auto qk = [&](int w, uint32_t i, bool first, bool last) {
 #pragma unroll
                     for (int c = 0; c < 3; ++c) {
                         if (first && !ready(i + c)) return false;
                         mma_qk4(tmem + kColS + w * 128, desc_lo(qs_s + w * kQBytes + c * kBlock, 16), desc_lo(block(i + c), 16),
-                                kIdescQK, c != 0);
+                                kIdescQK, c != 0, go);
                         if (last) release(i + c);
                     }
-                    mma_commit(smem_addr(&ct->s_full[w]));
+                    commit(ct->s_full[w]);
                     return true;
                 };
                 // P V of stream w with the values in blocks i, i + 1, of which `steps` groups of 16 tokens count.
@@ -346,37 +350,37 @@ __global__ void __launch_bounds__(kThreads, 1)
                         if (first && !ready(i + c)) return false;
                         const uint32_t v_lo = desc_lo(block(i + c), kBlock / 2);
                         if (steps >= 4 * c + 4) {
-                            mma_pv4(o, p + c * 32, v_lo, kIdescPV, acc || c);
+                            mma_pv4(o, p + c * 32, v_lo, kIdescPV, acc || c, go);
                         } else {
-                            for (int u = 0; u < steps - 4 * c; ++u) mma_pv1(o, p + c * 32 + u * 8, v_lo + u * 128, kIdescPV, acc || c || u);
+                            for (int u = 0; u < steps - 4 * c; ++u) mma_pv1(o, p + c * 32 + u * 8, v_lo + u * 128, kIdescPV, acc || c || u, go);
                         }
                         if (last) release(i + c);
                     }
                     return true;
                 };
                 auto p_ready = [&](int w) {
-                    const bool r = bar_wait(smem_addr(&ct->p_full[w]), (p_ph >> w) & 1);
+                    const bool r = wait(ct->p_full[w], (p_ph >> w) & 1);
                     p_ph ^= 1u << w;
                     tc_fence_after();
                     return r;
                 };
                 bool ok = true;
                 for (uint32_t k = 0; ok; ++k) {
-                    ok = seg_wait(k);
+                    ok = wait(ct->seg_full[k % kSegs], (k / kSegs) & 1);
                     const Seg& s = ct->seg[k % kSegs];
-                    const int n = s.t1 - s.t0;
+                    const int n = uniform(s.t1 - s.t0);
                     if (!ok || n == 0) break;
-                    const bool two = s.en.ntok > 128;   // two row halves; else even and odd tiles
+                    const bool two = uniform(s.en.ntok) > 128;   // two row halves; else even and odd tiles
                     for (int w = 0; w < 2 && ok; ++w) {
                         const int t = two ? 0 : w;
                         if (t >= n) break;
-                        ok = bar_wait(smem_addr(&ct->q_full[w]), (q_ph >> w) & 1);
+                        ok = wait(ct->q_full[w], (q_ph >> w) & 1);
                         q_ph ^= 1u << w;
                         if (!ok) break;
                         tc_fence_after();
                         ok = qk(w, ld + k_block(two, t), !two || w == 0, !two || w == 1);
                     }
-                    int steps = (s.en.len - s.t0 * kTileTok + 15) / 16;   // groups of 16 tokens from the tile on
+                    int steps = uniform((s.en.len - s.t0 * kTileTok + 15) / 16);   // groups of 16 tokens from the tile on
                     if (two) {
                         for (int t = 0; t < n && ok; ++t, steps -= 8) {
                             const bool next = t + 1 < n;
@@ -385,12 +389,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                             ok = p_ready(0) && pv(0, vl, steps, acc, true, false);
                             if (!ok) break;
                             if (next) ok = qk(0, kl, true, false);
-                            else mma_commit(smem_addr(&ct->o_full[0]));
+                            else commit(ct->o_full[0]);
                             ok = ok && p_ready(1);
                             if (!ok) break;
                             pv(1, vl, steps, acc, false, true);
                             if (next) qk(1, kl, false, true);
-                            else mma_commit(smem_addr(&ct->o_full[1]));
+                            else commit(ct->o_full[1]);
                         }
                     } else {
                         for (int t = 0; t < n && ok; ++t, steps -= 8) {
@@ -398,15 +402,15 @@ __global__ void __launch_bounds__(kThreads, 1)
                             ok = p_ready(w) && pv(w, ld + v_block(false, t, n), steps, ((t >> 1) & (kFoldTiles - 1)) != 0, true, true);
                             if (!ok) break;
                             if (t + 2 < n) ok = qk(w, ld + k_block(false, t + 2), true, true);
-                            else mma_commit(smem_addr(&ct->o_full[w]));
+                            else commit(ct->o_full[w]);
                         }
                     }
                     ld += 5 * n;
-                    if (ok) mbar_arrive(smem_addr(&ct->seg_empty[k % kSegs]));
+                    if (ok && go) mbar_arrive(smem_addr(&ct->seg_empty[k % kSegs]));
                 }
-                if (!ok) gave_up(ct);
-                mma_commit(smem_addr(&ct->drain));   // nothing of this CTA's is in flight when TMEM is freed
-                (void)bar_wait(smem_addr(&ct->drain), 0);
+                if (!ok && go) gave_up(ct);
+                commit(ct->drain);   // nothing of this CTA's is in flight when TMEM is freed
+                (void)wait(ct->drain, 0);
             }
             __syncwarp();
         } else if (warp == 2) {

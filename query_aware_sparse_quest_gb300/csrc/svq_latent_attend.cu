@@ -31,7 +31,7 @@
 // Roles of a CTA (one per SM):
 //   warp 0       loads the pages: units of 64 tokens x 128 channels (16 KB), each
 //                freed when its part of the second product is done, and rotary keys
-//   warp 1       issues the MMAs (one thread)
+//   warp 1       issues the MMAs
 //   warp 2       walks the plan
 //   warps 4-7    softmax (16 tokens each), outputs
 //   warps 8-15   (e4m3) widen the codes
@@ -125,45 +125,38 @@ constexpr uint32_t kF32FromBf16 = (1u << 4) | (1u << 7) | (1u << 10);
 constexpr uint32_t idesc(int m, int n) { return kF32FromBf16 | (static_cast<uint32_t>(n / 8) << 17) | (static_cast<uint32_t>(m / 16) << 24); }
 constexpr uint32_t kAIsMMajor = 1u << 15;
 
+#define LATENT_MMA_REGS "{\n\t.reg .pred acc, yes, go;\n\t.reg .b32 al, bl;\n\t.reg .b64 ad, bd;\n\t" \
+    "setp.ne.u32 acc, %6, 0;\n\tsetp.ne.u32 go, %7, 0;\n\tsetp.eq.u32 yes, 0, 0;\n\t"
 // S^T (+)= K Q^T over a unit's 128 channels: 16 channels are 32 bytes further in the rows of both; the second 64 lie
-// 1 KB on (K) and a block of N rows on (Q: q_half in descriptor units).
-__device__ __forceinline__ void mma_qk8(uint32_t d, uint32_t k_lo, uint32_t q_lo, uint32_t q_half, uint32_t id, uint32_t acc) {
-    const uint32_t q2 = q_lo + q_half;
-    asm volatile(
-        "{\n\t.reg .pred acc, yes;\n\t.reg .b32 al, bl;\n\t.reg .b64 ad, bd;\n\t"
-        "setp.ne.u32 acc, %6, 0;\n\tsetp.eq.u32 yes, 0, 0;\n\t"
-        SVQ_MMA_SS(0, 0, acc) SVQ_MMA_SS(2, 2, yes) SVQ_MMA_SS(4, 4, yes) SVQ_MMA_SS(6, 6, yes)
-        "}" ::"r"(d), "r"(k_lo), "r"(q_lo), "r"(desc_hi(2048)), "r"(desc_hi(1024)), "r"(id), "r"(acc)
+// 1 KB on (K) and a block of N rows on (Q: q_half in descriptor units).  By the whole warp, as the others.
+__device__ __forceinline__ void mma_qk8(uint32_t d, uint32_t k_lo, uint32_t q_lo, uint32_t q_half, uint32_t id, uint32_t acc, uint32_t go) {
+    asm volatile(LATENT_MMA_REGS
+        SVQ_MMA_SS_IF(0, 0, acc) SVQ_MMA_SS_IF(2, 2, yes) SVQ_MMA_SS_IF(4, 4, yes) SVQ_MMA_SS_IF(6, 6, yes)
+        "}" ::"r"(d), "r"(k_lo), "r"(q_lo), "r"(desc_hi(2048)), "r"(desc_hi(1024)), "r"(id), "r"(acc), "r"(go)
         : "memory");
-    asm volatile(
-        "{\n\t.reg .pred yes;\n\t.reg .b32 al, bl;\n\t.reg .b64 ad, bd;\n\tsetp.eq.u32 yes, 0, 0;\n\t"
-        SVQ_MMA_SS(64, 0, yes) SVQ_MMA_SS(66, 2, yes) SVQ_MMA_SS(68, 4, yes) SVQ_MMA_SS(70, 6, yes)
-        "}" ::"r"(d), "r"(k_lo), "r"(q2), "r"(desc_hi(2048)), "r"(desc_hi(1024)), "r"(id)
+    asm volatile(LATENT_MMA_REGS
+        SVQ_MMA_SS_IF(64, 0, yes) SVQ_MMA_SS_IF(66, 2, yes) SVQ_MMA_SS_IF(68, 4, yes) SVQ_MMA_SS_IF(70, 6, yes)
+        "}" ::"r"(d), "r"(k_lo), "r"(q_lo + q_half), "r"(desc_hi(2048)), "r"(desc_hi(1024)), "r"(id), "r"(acc), "r"(go)
         : "memory");
 }
 // The rotary 64 channels.
-__device__ __forceinline__ void mma_rope4(uint32_t d, uint32_t k_lo, uint32_t q_lo, uint32_t id, uint32_t acc) {
-    asm volatile(
-        "{\n\t.reg .pred acc, yes;\n\t.reg .b32 al, bl;\n\t.reg .b64 ad, bd;\n\t"
-        "setp.ne.u32 acc, %6, 0;\n\tsetp.eq.u32 yes, 0, 0;\n\t"
-        SVQ_MMA_SS(0, 0, acc) SVQ_MMA_SS(2, 2, yes) SVQ_MMA_SS(4, 4, yes) SVQ_MMA_SS(6, 6, yes)
-        "}" ::"r"(d), "r"(k_lo), "r"(q_lo), "r"(desc_hi(1024)), "r"(desc_hi(1024)), "r"(id), "r"(acc)
+__device__ __forceinline__ void mma_rope4(uint32_t d, uint32_t k_lo, uint32_t q_lo, uint32_t id, uint32_t acc, uint32_t go) {
+    asm volatile(LATENT_MMA_REGS
+        SVQ_MMA_SS_IF(0, 0, acc) SVQ_MMA_SS_IF(2, 2, yes) SVQ_MMA_SS_IF(4, 4, yes) SVQ_MMA_SS_IF(6, 6, yes)
+        "}" ::"r"(d), "r"(k_lo), "r"(q_lo), "r"(desc_hi(1024)), "r"(desc_hi(1024)), "r"(id), "r"(acc), "r"(go)
         : "memory");
 }
 // O^T (+)= C^T P^T of 128 channels: a page (16 tokens) is 4 KB of the unit and 32 bytes of P's rows.
-__device__ __forceinline__ void mma_pv4(uint32_t d, uint32_t c_lo, uint32_t p_lo, uint32_t id, uint32_t acc) {
-    asm volatile(
-        "{\n\t.reg .pred acc, yes;\n\t.reg .b32 al, bl;\n\t.reg .b64 ad, bd;\n\t"
-        "setp.ne.u32 acc, %6, 0;\n\tsetp.eq.u32 yes, 0, 0;\n\t"
-        SVQ_MMA_SS(0, 0, acc) SVQ_MMA_SS(256, 2, yes) SVQ_MMA_SS(512, 4, yes) SVQ_MMA_SS(768, 6, yes)
-        "}" ::"r"(d), "r"(c_lo), "r"(p_lo), "r"(desc_hi(2048)), "r"(desc_hi(1024)), "r"(id), "r"(acc)
+__device__ __forceinline__ void mma_pv4(uint32_t d, uint32_t c_lo, uint32_t p_lo, uint32_t id, uint32_t acc, uint32_t go) {
+    asm volatile(LATENT_MMA_REGS
+        SVQ_MMA_SS_IF(0, 0, acc) SVQ_MMA_SS_IF(256, 2, yes) SVQ_MMA_SS_IF(512, 4, yes) SVQ_MMA_SS_IF(768, 6, yes)
+        "}" ::"r"(d), "r"(c_lo), "r"(p_lo), "r"(desc_hi(2048)), "r"(desc_hi(1024)), "r"(id), "r"(acc), "r"(go)
         : "memory");
 }
-__device__ __forceinline__ void mma_pv1(uint32_t d, uint32_t c_lo, uint32_t p_lo, uint32_t id, uint32_t acc) {
-    asm volatile(
-        "{\n\t.reg .pred acc;\n\t.reg .b32 al, bl;\n\t.reg .b64 ad, bd;\n\tsetp.ne.u32 acc, %6, 0;\n\t"
-        SVQ_MMA_SS(0, 0, acc)
-        "}" ::"r"(d), "r"(c_lo), "r"(p_lo), "r"(desc_hi(2048)), "r"(desc_hi(1024)), "r"(id), "r"(acc)
+__device__ __forceinline__ void mma_pv1(uint32_t d, uint32_t c_lo, uint32_t p_lo, uint32_t id, uint32_t acc, uint32_t go) {
+    asm volatile(LATENT_MMA_REGS
+        SVQ_MMA_SS_IF(0, 0, acc)
+        "}" ::"r"(d), "r"(c_lo), "r"(p_lo), "r"(desc_hi(2048)), "r"(desc_hi(1024)), "r"(id), "r"(acc), "r"(go)
         : "memory");
 }
 // 16 lanes x 8 columns a repeat: lane l of the warp gets row l / 4 (and + 8), columns 2 (l % 4), + 1.
@@ -322,7 +315,7 @@ __global__ void __launch_bounds__(Cfg<N, FP8>::kThreads, 1)
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    const uint32_t tmem = ct->tmem;
+    const uint32_t tmem = uniform(ct->tmem);
     // Every role takes the segments in order: the k-th is in slot k % kSegs.
     auto seg_done = [&](uint32_t k) {   // once a warp
         __syncwarp();
@@ -413,74 +406,79 @@ __global__ void __launch_bounds__(Cfg<N, FP8>::kThreads, 1)
             }
         loads_done:;
         } else if (warp == 1) {
-            // ---------------- MMAs (one thread)
-            if (lane == 0) {
+            // ---------------- MMAs: the whole warp, in step
+            {
+                const uint32_t go = elected();
                 uint32_t tile = 0, segs = 0;   // tiles before the segment; segments with tiles
                 const uint32_t ring_s = smem_addr(ring), q_s = smem_addr(qs), p_lo = desc_lo(smem_addr(ps), 16);
                 constexpr uint32_t kBlockQ = N * 128;
+                auto wait = [&](uint64_t& bar, uint32_t parity) {
+                    const bool all = __all_sync(0xffffffffu, bar_wait(smem_addr(&bar), parity));
+                    tc_fence_after();
+                    return all;
+                };
+                auto commit = [&](uint64_t& bar) {
+                    if (go) mma_commit(smem_addr(&bar));
+                };
                 // S^T of tile t (counted over the CTA's work): units u0 .. u1 - 1, and the rotary part behind the last.
                 auto qk = [&](uint32_t t, int u0, int u1) {
                     const uint32_t d = tmem + C::kColS + (t & 1) * C::kSCols;
-#pragma unroll 1
+#pragma unroll
                     for (int u = u0; u < u1; ++u) {
                         const uint32_t at = t * kUnits + u, st = at % C::kRing;
-                        if (!bar_wait(smem_addr(&ct->full[st]), (at / C::kRing) & 1)) return false;
-                        tc_fence_after();
-                        mma_qk8(d, desc_lo(ring_s + st * kUnit, 16), desc_lo(q_s + 2 * u * kBlockQ, 16), kBlockQ >> 4, idesc(64, N), u != 0);
+                        if (!wait(ct->full[st], (at / C::kRing) & 1)) return false;
+                        mma_qk8(d, desc_lo(ring_s + st * kUnit, 16), desc_lo(q_s + 2 * u * kBlockQ, 16), kBlockQ >> 4, idesc(64, N), u != 0, go);
                     }
                     if (u1 < kUnits) return true;
                     const uint32_t st = t % C::kRope;
-                    if (!bar_wait(smem_addr(&ct->rope_full[st]), (t / C::kRope) & 1)) return false;
-                    tc_fence_after();
+                    if (!wait(ct->rope_full[st], (t / C::kRope) & 1)) return false;
                     mma_rope4(FP8 ? d + N : d, desc_lo(smem_addr(ropes) + st * kRopeBytes, 16), desc_lo(q_s + 8 * kBlockQ, 16),
-                              idesc(64, N), !FP8);
-                    mma_commit(smem_addr(&ct->rope_empty[st]));
-                    mma_commit(smem_addr(&ct->s_full[t & 1]));
+                              idesc(64, N), !FP8, go);
+                    commit(ct->rope_empty[st]);
+                    commit(ct->s_full[t & 1]);
                     return true;
                 };
                 bool ok = true;
                 for (uint32_t k = 0; ok; ++k) {
-                    ok = bar_wait(smem_addr(&ct->seg_full[k % kSegs]), (k / kSegs) & 1);
+                    ok = wait(ct->seg_full[k % kSegs], (k / kSegs) & 1);
                     const Seg& s = ct->seg[k % kSegs];
-                    const int n = s.t1 - s.t0;
+                    const int n = uniform(s.t1 - s.t0);
                     if (!ok || n == 0) break;
-                    ok = bar_wait(smem_addr(&ct->q_full), segs & 1);
+                    int pages = uniform(s.en.npages - s.t0 * kPages);   // from the tile on
+                    ok = wait(ct->q_full, segs & 1);
                     ++segs;
                     if (!ok) break;
-                    tc_fence_after();
                     ok = qk(tile, 0, kUnits);
-                    for (int i = 0; i < n && ok; ++i) {
+                    for (int i = 0; i < n && ok; ++i, pages -= kPages) {
                         const uint32_t t = tile + i;
                         if (i + 1 < n && !qk(t + 1, 0, C::kAhead)) {
                             ok = false;
                             break;
                         }
-                        ok = bar_wait(smem_addr(&ct->p_full), t & 1);
+                        ok = wait(ct->p_full, t & 1);
                         if (!ok) break;
-                        tc_fence_after();
-                        const int pages = min(kPages, s.en.npages - (s.t0 + i) * kPages);
                         const bool acc = (i & (kFoldTiles - 1)) != 0;
-#pragma unroll 1
+#pragma unroll
                         for (int u = 0; u < kUnits; ++u) {
                             const uint32_t st = (t * kUnits + u) % C::kRing;
                             const uint32_t c_lo = desc_lo(ring_s + st * kUnit, 1024), d = tmem + u * N;
-                            if (pages == kPages) {
-                                mma_pv4(d, c_lo, p_lo, idesc(128, N) | kAIsMMajor, acc);
+                            if (pages >= kPages) {
+                                mma_pv4(d, c_lo, p_lo, idesc(128, N) | kAIsMMajor, acc, go);
                             } else {
                                 for (int p = 0; p < pages; ++p)
-                                    mma_pv1(d, c_lo + p * 256, p_lo + p * 2, idesc(128, N) | kAIsMMajor, acc || p != 0);
+                                    mma_pv1(d, c_lo + p * 256, p_lo + p * 2, idesc(128, N) | kAIsMMajor, acc || p != 0, go);
                             }
-                            mma_commit(smem_addr(&ct->empty[st]));
+                            commit(ct->empty[st]);
                         }
-                        mma_commit(smem_addr(&ct->pv_done));
+                        commit(ct->pv_done);
                         if (C::kAhead < kUnits && i + 1 < n) ok = qk(t + 1, C::kAhead, kUnits);
                     }
                     tile += n;
-                    if (ok) mbar_arrive(smem_addr(&ct->seg_empty[k % kSegs]));
+                    if (ok && go) mbar_arrive(smem_addr(&ct->seg_empty[k % kSegs]));
                 }
-                if (!ok) gave_up(ct);
-                mma_commit(smem_addr(&ct->drain));   // nothing of this CTA's is in flight when TMEM is freed
-                (void)bar_wait(smem_addr(&ct->drain), 0);
+                if (!ok && go) gave_up(ct);
+                commit(ct->drain);   // nothing of this CTA's is in flight when TMEM is freed
+                (void)wait(ct->drain, 0);
             }
             __syncwarp();
         } else if (warp == 2) {

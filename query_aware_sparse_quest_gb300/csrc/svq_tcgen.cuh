@@ -22,6 +22,24 @@ __device__ __forceinline__ uint32_t desc_lo(uint32_t addr, uint32_t lbo) { retur
     "add.u32 al, %1, " #ao ";\n\tadd.u32 bl, %2, " #bo ";\n\t"                   \
     "mov.b64 bd, {bl, %3};\n\t"                                                  \
     "tcgen05.mma.cta_group::1.kind::f16 [%0], [al], bd, %4, " #acc ";\n\t"
+// The same by a whole warp that runs in step, one elected lane of which issues (predicate `go`): operands that all lanes
+// share stay in uniform registers, where the MMA wants them.  From a branch of one thread each is moved there first,
+// 48 cycles an MMA (measured), more than one of 64 x 64 or of 128 x 16 takes.
+#define SVQ_MMA_SS_IF(ao, bo, acc)                                               \
+    "add.u32 al, %1, " #ao ";\n\tadd.u32 bl, %2, " #bo ";\n\t"                   \
+    "mov.b64 ad, {al, %3};\n\tmov.b64 bd, {bl, %4};\n\t"                         \
+    "@go tcgen05.mma.cta_group::1.kind::f16 [%0], ad, bd, %5, " #acc ";\n\t"
+#define SVQ_MMA_TS_IF(ao, bo, acc)                                               \
+    "add.u32 al, %1, " #ao ";\n\tadd.u32 bl, %2, " #bo ";\n\t"                   \
+    "mov.b64 bd, {bl, %3};\n\t"                                                  \
+    "@go tcgen05.mma.cta_group::1.kind::f16 [%0], [al], bd, %4, " #acc ";\n\t"
+__device__ __forceinline__ uint32_t elected() {
+    uint32_t e;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(e));
+    return e;
+}
+// A value that all lanes of the warp hold, as the compiler cannot see.
+__device__ __forceinline__ int uniform(int v) { return __shfl_sync(0xffffffffu, v, 0); }
 __device__ __forceinline__ void mma_commit(uint32_t bar) {
     asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
 }
