@@ -65,8 +65,13 @@ template <int N, bool FP8>
 struct Cfg {
     static constexpr int kRing = FP8 ? (N == 64 ? 6 : 7) : (N == 64 ? 8 : (N == 32 ? 10 : 11));   // units
     static constexpr int kRope = N == 64 ? 2 : 3;                                                 // rotary tiles
-    static constexpr int kCodes = FP8 ? (N == 64 ? 3 : (N == 32 ? 5 : 6)) : 0;                    // units of codes, 8 KB
-    static constexpr int kAhead = kRing >= 8 ? 4 : kRing - 4;   // units of a tile whose S is begun before the tile before is done
+    static constexpr int kCodes = FP8 ? (N == 64 ? 3 : (N == 32 ? 4 : 8)) : 0;                    // units of codes, 8 KB
+    // Pairs of warps that widen a unit each, in turn.  (A pair sees every phase of the slots it reads: kCodes % kPairs is 0.)
+    static constexpr int kPairs = N == 64 ? 3 : 4;
+    static_assert(kCodes % kPairs == 0, "code slots");
+    // Units of a tile that the first of the two loading warps takes.  Pairs free code slots out of order, so a slot is
+    // one warp's: with slots that are not a multiple of the units, all are the first's.
+    static constexpr int kFirst = kCodes % 4 ? 4 : 2;
     static constexpr int kThreads = FP8 ? 512 : 256;
     static constexpr int kWiden = 8;                                                              // warps
     static constexpr int kQ = N * kQueryDim * 2;
@@ -171,10 +176,19 @@ __device__ __forceinline__ void stmatrix_x4_trans(uint32_t addr, uint32_t a, uin
     asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1,%2,%3,%4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d)
                  : "memory");
 }
-__device__ __forceinline__ void tma_page(uint32_t dst, const void* map, int half, int group, uint32_t bar) {
+// Copies by a whole warp in step, of which the elected lane issues (go): from four lanes at once each takes 130 cycles.
+__device__ __forceinline__ void tma_page_if(uint32_t go, uint32_t dst, const void* map, int half, int group, uint32_t bar) {
     asm volatile(
-        "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %2, %3, %4}], [%5];"
-        ::"r"(dst), "l"(map), "r"(0), "r"(half), "r"(group), "r"(bar)
+        "{\n\t.reg .pred go;\n\tsetp.ne.u32 go, %6, 0;\n\t"
+        "@go cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %2, %3, %4}], [%5];\n\t}"
+        ::"r"(dst), "l"(map), "r"(0), "r"(half), "r"(group), "r"(bar), "r"(go)
+        : "memory");
+}
+__device__ __forceinline__ void tma_2d_if(uint32_t go, uint32_t dst, const void* map, int x, int y, uint32_t bar) {
+    asm volatile(
+        "{\n\t.reg .pred go;\n\tsetp.ne.u32 go, %5, 0;\n\t"
+        "@go cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];\n\t}"
+        ::"r"(dst), "l"(map), "r"(x), "r"(y), "r"(bar), "r"(go)
         : "memory");
 }
 // The softmax warps' barrier.
@@ -210,7 +224,7 @@ constexpr int kSegs = 4;
 struct Control {
     uint64_t full[11], empty[11];          // units
     uint64_t rope_full[3], rope_empty[3];
-    uint64_t code_full[6], code_empty[6];
+    uint64_t code_full[8], code_empty[8];
     uint64_t scale_full[kInfoSlots];
     uint64_t seg_full[kSegs], seg_empty[kSegs];
     uint64_t s_full[2], p_full, pv_done, q_full, drain;
@@ -279,7 +293,7 @@ __global__ void __launch_bounds__(Cfg<N, FP8>::kThreads, 1)
     if (threadIdx.x == 0) {
         ct->gave_up = 0;
         for (int i = 0; i < C::kRing; ++i) {
-            mbar_init(smem_addr(&ct->full[i]), FP8 ? C::kWiden : 1);
+            mbar_init(smem_addr(&ct->full[i]), FP8 ? 2 : 1);
             mbar_init(smem_addr(&ct->empty[i]), 1);
         }
         for (int i = 0; i < C::kRope; ++i) {
@@ -288,12 +302,12 @@ __global__ void __launch_bounds__(Cfg<N, FP8>::kThreads, 1)
         }
         for (int i = 0; i < C::kCodes; ++i) {
             mbar_init(smem_addr(&ct->code_full[i]), 1);
-            mbar_init(smem_addr(&ct->code_empty[i]), C::kWiden);
+            mbar_init(smem_addr(&ct->code_empty[i]), 2);
         }
         for (int i = 0; i < kInfoSlots; ++i) mbar_init(smem_addr(&ct->scale_full[i]), 1);
         for (int i = 0; i < kSegs; ++i) {
             mbar_init(smem_addr(&ct->seg_full[i]), 1);
-            mbar_init(smem_addr(&ct->seg_empty[i]), 2 + 4 + (FP8 ? C::kWiden : 0));   // loads, MMAs, softmax, widening
+            mbar_init(smem_addr(&ct->seg_empty[i]), 3 + 4 + (FP8 ? C::kWiden : 0));   // loads, MMAs, softmax, widening
         }
         mbar_init(smem_addr(&ct->s_full[0]), 1);
         mbar_init(smem_addr(&ct->s_full[1]), 1);
@@ -323,72 +337,83 @@ __global__ void __launch_bounds__(Cfg<N, FP8>::kThreads, 1)
     };
 
     {
-        if (warp == 0) {
-            // ---------------- loads: lane p page p of a tile
+        if (warp == 0 || warp == 3) {
+            // ---------------- loads: warp 0 scales and the first kFirst units, warp 3 the rest; each in step
+            const bool rest = warp == 3;
+            const uint32_t go = elected();
             uint32_t tile = 0, loaded = 0;
             for (uint32_t k = 0;; ++k) {
                 SVQ_WAIT(ct->seg_full[k % kSegs], (k / kSegs) & 1, loads_end);
                 const Seg& s = ct->seg[k % kSegs];
-                const int n = s.t1 - s.t0;
+                const int t0 = uniform(s.t0), n = uniform(s.t1) - t0;
                 if (n == 0) break;
+                const int end = min(s.en.npages, s.t1 * kPages);
                 const int32_t* const pages = a.page_table + static_cast<int64_t>(s.en.req) * a.max_pages;
-                // Lane l resolves page i + l of the segment (eight tiles at a time), well before the loads that need it.
+                // Lane l resolves page i + l of the segment (eight tiles at a time), well before the loads that need it:
+                // -2 behind the last page, -1 what the table does not give.
                 auto fetch = [&](int i0) {
                     const int i = i0 + lane;
-                    return i < min(s.en.npages, s.t1 * kPages) ? pages[i] : -2;
+                    const int ph = i < end ? pages[i] : -2;
+                    return ph >= a.num_pages || ph < -2 || (ph == -2 && i < end) ? -1 : ph;
                 };
-                int cur = -2, nxt = fetch(s.t0 * kPages);
+                int cur = -2, nxt = fetch(t0 * kPages);
                 for (int i = 0; i < n; ++i, ++tile) {
                     if (i % 8 == 0) {
                         cur = nxt;
-                        if (i + 8 < n) nxt = fetch((s.t0 + i + 8) * kPages);
+                        if (i + 8 < n) nxt = fetch((t0 + i + 8) * kPages);
                     }
-                    int ph = __shfl_sync(0xffffffffu, cur, (i % 8) * kPages + (lane & 3));
-                    if (lane >= kPages) ph = -2;
-                    const bool bad = ph != -2 && (ph < 0 || ph >= a.num_pages);
-                    const bool load = ph != -2 && !bad;
-                    const uint32_t faults = __ballot_sync(0xffffffffu, bad);
-                    const int loads = __popc(__ballot_sync(0xffffffffu, load));
-                    const int slot = tile % kInfoSlots;
-                    if (lane == 0) {
+                    int ph[kPages];
+                    uint32_t faults = 0, loads = 0;
+#pragma unroll
+                    for (int p = 0; p < kPages; ++p) {
+                        ph[p] = uniform(__shfl_sync(0xffffffffu, cur, (i % 8) * kPages + p));
+                        faults |= ph[p] == -1 ? 1u << p : 0u;
+                        loads += ph[p] >= 0;
+                    }
+                    const uint32_t slot = tile % kInfoSlots;
+                    if (go) {
                         if (faults) svq_flag(SV_DEVERR_PAGE_TABLE);
-                        ct->fault[slot] = static_cast<int>(faults);
+                        if (!rest) ct->fault[slot] = static_cast<int>(faults);
                     }
-                    if (FP8) {
-                        if (lane == 0) mbar_arrive_expect_tx(smem_addr(&ct->scale_full[slot]), loads * kPage * 4);
+                    if (FP8 && !rest) {
+                        const uint32_t bar = smem_addr(&ct->scale_full[slot]);
+                        if (go) mbar_arrive_expect_tx(bar, loads * kPage * 4);
                         __syncwarp();
-                        if (load)
-                            bulk_copy_g2s(smem_addr(scales + slot * kTok + lane * kPage), a.scale + static_cast<int64_t>(ph) * kPage,
-                                          kPage * 4, smem_addr(&ct->scale_full[slot]));
+                        const int mine = lane == 0 ? ph[0] : (lane == 1 ? ph[1] : (lane == 2 ? ph[2] : ph[3]));
+                        if (lane < kPages && mine >= 0)
+                            bulk_copy_g2s(smem_addr(scales + slot * kTok + lane * kPage), a.scale + static_cast<int64_t>(mine) * kPage, kPage * 4, bar);
+                        __syncwarp();
                     }
-#pragma unroll 1
+#pragma unroll
                     for (int u = 0; u < kUnits; ++u) {
+                        if ((u >= C::kFirst) != rest) continue;
                         const uint32_t at = tile * kUnits + u;
-                        if (FP8) {
-                            constexpr uint32_t kDepth = FP8 ? C::kCodes : 1;
-                            const uint32_t st = at % kDepth;
-                            SVQ_WAIT(ct->code_empty[st], ((at / kDepth) & 1) ^ 1, loads_end);
-                            const uint32_t bar = smem_addr(&ct->code_full[st]);
-                            if (lane == 0) mbar_arrive_expect_tx(bar, loads * (kPage * 128));
-                            __syncwarp();
-                            if (load)
-                                tma_load_2d(smem_addr(codes) + st * (kUnit / 2) + lane * (kPage * 128), &tmap_c, u * 128, ph * kPage, bar);
-                        } else {
-                            const uint32_t st = at % C::kRing;
-                            SVQ_WAIT(ct->empty[st], ((at / C::kRing) & 1) ^ 1, loads_end);
-                            const uint32_t bar = smem_addr(&ct->full[st]);
-                            if (lane == 0) mbar_arrive_expect_tx(bar, loads * (kPage * 256));
-                            __syncwarp();
-                            if (load) tma_page(smem_addr(ring) + st * kUnit + lane * (kPage * 256), &tmap_c, 2 * u, 2 * ph, bar);
+                        constexpr uint32_t kDepth = FP8 ? (C::kCodes ? C::kCodes : 1) : C::kRing;
+                        uint64_t* const empty = FP8 ? ct->code_empty : ct->empty;
+                        uint64_t* const full = FP8 ? ct->code_full : ct->full;
+                        constexpr uint32_t kPageBytes = kPage * (FP8 ? 128 : 256);
+                        const uint32_t st = at % kDepth;
+                        SVQ_WAIT(empty[st], ((at / kDepth) & 1) ^ 1, loads_end);
+                        const uint32_t bar = smem_addr(&full[st]), dst = smem_addr(FP8 ? codes : ring) + st * (kPageBytes * kPages);
+                        if (go) mbar_arrive_expect_tx(bar, loads * kPageBytes);
+                        __syncwarp();
+#pragma unroll
+                        for (int p = 0; p < kPages; ++p) {
+                            const uint32_t on = ph[p] >= 0 ? go : 0u;
+                            if (FP8) tma_2d_if(on, dst + p * kPageBytes, &tmap_c, u * 128, ph[p] * kPage, bar);
+                            else tma_page_if(on, dst + p * kPageBytes, &tmap_c, 2 * u, 2 * ph[p], bar);
                         }
                         loaded = at + 1;
                     }
+                    if (!rest) continue;
                     const uint32_t st = tile % C::kRope;
                     SVQ_WAIT(ct->rope_empty[st], ((tile / C::kRope) & 1) ^ 1, loads_end);
                     const uint32_t bar = smem_addr(&ct->rope_full[st]);
-                    if (lane == 0) mbar_arrive_expect_tx(bar, loads * (kPage * kRopeDim * 2));
+                    if (go) mbar_arrive_expect_tx(bar, loads * (kPage * kRopeDim * 2));
                     __syncwarp();
-                    if (load) tma_load_2d(smem_addr(ropes) + st * kRopeBytes + lane * (kPage * kRopeDim * 2), &tmap_r, 0, ph * kPage, bar);
+#pragma unroll
+                    for (int p = 0; p < kPages; ++p)
+                        tma_2d_if(ph[p] >= 0 ? go : 0u, smem_addr(ropes) + st * kRopeBytes + p * (kPage * kRopeDim * 2), &tmap_r, 0, ph[p] * kPage, bar);
                 }
                 seg_done(k);
             }
@@ -396,7 +421,7 @@ __global__ void __launch_bounds__(Cfg<N, FP8>::kThreads, 1)
         loads_end:
             // Gave up: the copies still in flight land before the CTA (and its shared memory) retires.
             {
-                constexpr uint32_t kDepth = FP8 ? C::kCodes : C::kRing;
+                constexpr uint32_t kDepth = FP8 ? (C::kCodes ? C::kCodes : 1) : C::kRing;
                 uint64_t* const full = FP8 ? ct->code_full : ct->full;
                 for (uint32_t x = loaded > kDepth ? loaded - kDepth : 0; x < loaded; ++x)
                     (void)bar_wait(smem_addr(&full[x % kDepth]), (x / kDepth) & 1);
@@ -420,21 +445,50 @@ __global__ void __launch_bounds__(Cfg<N, FP8>::kThreads, 1)
                 auto commit = [&](uint64_t& bar) {
                     if (go) mma_commit(smem_addr(&bar));
                 };
-                // S^T of tile t (counted over the CTA's work): units u0 .. u1 - 1, and the rotary part behind the last.
-                auto qk = [&](uint32_t t, int u0, int u1) {
-                    const uint32_t d = tmem + C::kColS + (t & 1) * C::kSCols;
-#pragma unroll
-                    for (int u = u0; u < u1; ++u) {
-                        const uint32_t at = t * kUnits + u, st = at % C::kRing;
-                        if (!wait(ct->full[st], (at / C::kRing) & 1)) return false;
-                        mma_qk8(d, desc_lo(ring_s + st * kUnit, 16), desc_lo(q_s + 2 * u * kBlockQ, 16), kBlockQ >> 4, idesc(64, N), u != 0, go);
+                auto poll = [&](uint64_t& bar, uint32_t parity) { return __all_sync(0xffffffffu, bar_test(smem_addr(&bar), parity)) != 0; };
+                // O^T of the tile whose P is ready: `pv_pages` pages of tile pv_tile, onto what there is if pv_acc.
+                bool pv_due = false, pv_acc = false;
+                uint32_t pv_tile = 0;
+                int pv_pages = 0;
+                auto pv = [&] {
+                    tc_fence_after();
+#pragma unroll 1
+                    for (int u = 0; u < kUnits; ++u) {
+                        const uint32_t st = (pv_tile * kUnits + u) % C::kRing;
+                        const uint32_t c_lo = desc_lo(ring_s + st * kUnit, 1024), d = tmem + u * N;
+                        if (pv_pages >= kPages) {
+                            mma_pv4(d, c_lo, p_lo, idesc(128, N) | kAIsMMajor, pv_acc, go);
+                        } else {
+                            for (int p = 0; p < pv_pages; ++p)
+                                mma_pv1(d, c_lo + p * 256, p_lo + p * 2, idesc(128, N) | kAIsMMajor, pv_acc || p != 0, go);
+                        }
+                        commit(ct->empty[st]);
                     }
-                    if (u1 < kUnits) return true;
-                    const uint32_t st = t % C::kRope;
-                    if (!wait(ct->rope_full[st], (t / C::kRope) & 1)) return false;
-                    mma_rope4(FP8 ? d + N : d, desc_lo(smem_addr(ropes) + st * kRopeBytes, 16), desc_lo(q_s + 8 * kBlockQ, 16),
-                              idesc(64, N), !FP8, go);
-                    commit(ct->rope_empty[st]);
+                    commit(ct->pv_done);
+                    pv_due = false;
+                };
+                // S^T of tile t (counted over the CTA's work), unit after unit as they land, then the rotary part.  The
+                // product of the tile before goes in between as soon as its P is ready: it frees the memory that later
+                // units wait for.
+                auto qk = [&](uint32_t t) {
+                    const uint32_t d = tmem + C::kColS + (t & 1) * C::kSCols;
+#pragma unroll 1
+                    for (int u = 0; u <= kUnits; ++u) {
+                        const uint32_t at = t * kUnits + u, st = at % C::kRing, rt = t % C::kRope;
+                        uint64_t& bar = u < kUnits ? ct->full[st] : ct->rope_full[rt];
+                        const uint32_t parity = (u < kUnits ? at / C::kRing : t / C::kRope) & 1;
+                        for (uint32_t tests = 0; !poll(bar, parity); ++tests) {
+                            if (pv_due && poll(ct->p_full, pv_tile & 1)) pv();
+                            if (tests == kTests) return false;
+                        }
+                        tc_fence_after();
+                        if (u < kUnits)
+                            mma_qk8(d, desc_lo(ring_s + st * kUnit, 16), desc_lo(q_s + 2 * u * kBlockQ, 16), kBlockQ >> 4, idesc(64, N), u != 0, go);
+                        else
+                            mma_rope4(FP8 ? d + N : d, desc_lo(smem_addr(ropes) + rt * kRopeBytes, 16), desc_lo(q_s + 8 * kBlockQ, 16),
+                                      idesc(64, N), !FP8, go);
+                    }
+                    commit(ct->rope_empty[t % C::kRope]);
                     commit(ct->s_full[t & 1]);
                     return true;
                 };
@@ -448,30 +502,17 @@ __global__ void __launch_bounds__(Cfg<N, FP8>::kThreads, 1)
                     ok = wait(ct->q_full, segs & 1);
                     ++segs;
                     if (!ok) break;
-                    ok = qk(tile, 0, kUnits);
+                    ok = qk(tile);
                     for (int i = 0; i < n && ok; ++i, pages -= kPages) {
-                        const uint32_t t = tile + i;
-                        if (i + 1 < n && !qk(t + 1, 0, C::kAhead)) {
-                            ok = false;
-                            break;
+                        pv_due = true;
+                        pv_tile = tile + i;
+                        pv_pages = pages;
+                        pv_acc = (i & (kFoldTiles - 1)) != 0;
+                        if (i + 1 < n) ok = qk(tile + i + 1);
+                        if (ok && pv_due) {
+                            ok = wait(ct->p_full, pv_tile & 1);
+                            if (ok) pv();
                         }
-                        ok = wait(ct->p_full, t & 1);
-                        if (!ok) break;
-                        const bool acc = (i & (kFoldTiles - 1)) != 0;
-#pragma unroll
-                        for (int u = 0; u < kUnits; ++u) {
-                            const uint32_t st = (t * kUnits + u) % C::kRing;
-                            const uint32_t c_lo = desc_lo(ring_s + st * kUnit, 1024), d = tmem + u * N;
-                            if (pages >= kPages) {
-                                mma_pv4(d, c_lo, p_lo, idesc(128, N) | kAIsMMajor, acc, go);
-                            } else {
-                                for (int p = 0; p < pages; ++p)
-                                    mma_pv1(d, c_lo + p * 256, p_lo + p * 2, idesc(128, N) | kAIsMMajor, acc || p != 0, go);
-                            }
-                            commit(ct->empty[st]);
-                        }
-                        commit(ct->pv_done);
-                        if (C::kAhead < kUnits && i + 1 < n) ok = qk(t + 1, C::kAhead, kUnits);
                     }
                     tile += n;
                     if (ok && go) mbar_arrive(smem_addr(&ct->seg_empty[k % kSegs]));
@@ -644,45 +685,52 @@ __global__ void __launch_bounds__(Cfg<N, FP8>::kThreads, 1)
                                 if (tok1 >= lim) x[4 * c + 2 + u] = -INFINITY;
                             }
                     }
-                    // Maxima of the warp's 16 tokens: after the exchanges lane l has those of 2 kGroups / 8 rows.
-                    float mx[2 * kGroups];
+                    // Weights go by the rows' bases as they are, unless a logit is more than kSlack above its row's: then
+                    // (at a run's first tile, and seldom behind it) the tile's maxima move the bases.  Columns without a
+                    // row have no say.
+                    float over = -INFINITY;
 #pragma unroll
-                    for (int c = 0; c < kGroups; ++c) {
-                        mx[2 * c] = fmaxf(x[4 * c], x[4 * c + 2]);
-                        mx[2 * c + 1] = fmaxf(x[4 * c + 1], x[4 * c + 3]);
-                    }
+                    for (int c = 0; c < kGroups; ++c)
 #pragma unroll
-                    for (int c = 0; c < 2 * kGroups; ++c) {
-                        mx[c] = fmaxf(mx[c], __shfl_xor_sync(0xffffffffu, mx[c], 4));
-                        mx[c] = fmaxf(mx[c], __shfl_xor_sync(0xffffffffu, mx[c], 8));
-                        mx[c] = fmaxf(mx[c], __shfl_xor_sync(0xffffffffu, mx[c], 16));
-                    }
-                    if (row8 == 0) {
+                        for (int u = 0; u < 2; ++u)
+                            if (8 * c + 2 * quad + u < rows)
+                                over = fmaxf(over, fmaf(fmaxf(x[4 * c + u], x[4 * c + 2 + u]), a.scale_log2, -base[2 * c + u]));
+                    const bool any = softmax_any(dead || j == 0 || over > kSlack);
+                    if (any) {
+                        if (softmax_any(dead)) goto softmax_end;
+                        float mx[2 * kGroups];
 #pragma unroll
-                        for (int c = 0; c < kGroups; ++c)
-                            *reinterpret_cast<float2*>(&ct->red[w][8 * c + 2 * quad]) = make_float2(mx[2 * c], mx[2 * c + 1]);
-                    }
-                    if (softmax_any(dead)) goto softmax_end;
-                    // The base of a row moves only when its maximum is more than kSlack above it; weights stay at most
-                    // 2^kSlack, and sums and outputs share the base.  Columns without a row have no say.
-                    bool move = false;
-                    if (tid < N) {
-                        const float top = fmaxf(fmaxf(ct->red[0][tid], ct->red[1][tid]), fmaxf(ct->red[2][tid], ct->red[3][tid])) * a.scale_log2;
-                        float alpha = 1.f;
-                        if (tid < rows && top > m + kSlack) {
-                            move = true;
-                            alpha = m == -INFINITY ? 0.f : ex2(m - top);   // (nothing was added yet)
-                            m = top;
-                            ct->base[tid] = m;
-                        } else if (j == 0) {
-                            ct->base[tid] = 0.f;   // a row that has seen nothing yet
+                        for (int c = 0; c < kGroups; ++c) {
+                            mx[2 * c] = fmaxf(x[4 * c], x[4 * c + 2]);
+                            mx[2 * c + 1] = fmaxf(x[4 * c + 1], x[4 * c + 3]);
                         }
-                        ct->alpha[tid] = alpha;
+#pragma unroll
+                        for (int c = 0; c < 2 * kGroups; ++c) {
+                            mx[c] = fmaxf(mx[c], __shfl_xor_sync(0xffffffffu, mx[c], 4));
+                            mx[c] = fmaxf(mx[c], __shfl_xor_sync(0xffffffffu, mx[c], 8));
+                            mx[c] = fmaxf(mx[c], __shfl_xor_sync(0xffffffffu, mx[c], 16));
+                        }
+                        if (row8 == 0) {
+#pragma unroll
+                            for (int c = 0; c < kGroups; ++c)
+                                *reinterpret_cast<float2*>(&ct->red[w][8 * c + 2 * quad]) = make_float2(mx[2 * c], mx[2 * c + 1]);
+                        }
+                        softmax_sync();
+                        if (tid < N) {
+                            const float top = fmaxf(fmaxf(ct->red[0][tid], ct->red[1][tid]), fmaxf(ct->red[2][tid], ct->red[3][tid])) * a.scale_log2;
+                            float alpha = 1.f;
+                            if (tid < rows && top > m) {
+                                alpha = m == -INFINITY ? 0.f : ex2(m - top);   // (nothing was added yet)
+                                m = top;
+                            }
+                            ct->base[tid] = m == -INFINITY ? 0.f : m;   // (0: a row that has seen nothing yet)
+                            ct->alpha[tid] = alpha;
+                        }
+                        softmax_sync();
                     }
-                    const bool any = softmax_any(move);
                     // P's memory and O are free when the product before is done.
                     if (j > 0) LATENT_WAIT(ct->pv_done, (tile - 1) & 1);
-                    if (any || j == 0) {
+                    if (any) {
 #pragma unroll
                         for (int c = 0; c < 2 * kGroups; ++c) {
                             const int r = 8 * (c >> 1) + 2 * quad + (c & 1);
@@ -848,54 +896,47 @@ __global__ void __launch_bounds__(Cfg<N, FP8>::kThreads, 1)
             // (Gave up: the rows in flight land before the CTA retires.)
             if (tid == 0 && q_loads) (void)bar_wait(smem_addr(&ct->q_full), (q_loads - 1) & 1);
         } else if (FP8 && warp >= 8) {
-            // ---------------- e4m3 codes -> bf16 units in the MMAs' layout
-            const int tid = threadIdx.x - 256;
-            uint32_t at = 0;
+            // ---------------- e4m3 codes -> bf16 units in the MMAs' layout, two warps a unit
+            const int tid = threadIdx.x & 63, mine = (warp - 8) >> 1;
+            uint32_t at = mine, until = 0;
             constexpr uint32_t kDepth = FP8 ? C::kCodes : 1;
             for (uint32_t k = 0;; ++k) {
                 SVQ_WAIT(ct->seg_full[k % kSegs], (k / kSegs) & 1, widen_end);
                 const Seg& s = ct->seg[k % kSegs];
                 const int n = s.t1 - s.t0;
                 if (n == 0) break;
-                for (int i = 0; i < n * kUnits; ++i, ++at) {
+                until += n * kUnits;
+                for (; mine < C::kPairs && at < until; at += C::kPairs) {
                     const uint32_t cs = at % kDepth, st = at % C::kRing;
                     SVQ_WAIT(ct->code_full[cs], (at / kDepth) & 1, widen_end);
-                    // 16 codes at chunk tid % 8 of rows tid / 8 and + 32.  The fence keeps the next copy into the slot
-                    // behind these reads.
-                    const int r = tid >> 3, c = tid & 7;
-                    uint4 v[2];
+                    // 16 codes at chunk tid / 8 of rows tid % 8, + 8, ...: eight lanes read, and write, eight rows' bytes in
+                    // different banks.  The fence keeps the next copy into the slot behind these reads.
+                    const int r = tid & 7, c = tid >> 3;
+                    uint4 v[8];
 #pragma unroll
-                    for (int u = 0; u < 2; ++u)
-                        v[u] = *reinterpret_cast<const uint4*>(codes + cs * (kUnit / 2) + (r + 32 * u) * 128 + c * 16);
+                    for (int u = 0; u < 8; ++u)
+                        v[u] = *reinterpret_cast<const uint4*>(codes + cs * (kUnit / 2) + (r + 8 * u) * 128 + ((c ^ r) << 4));
                     fence_proxy_async_smem();
                     __syncwarp();
                     if (lane == 0) mbar_arrive(smem_addr(&ct->code_empty[cs]));
-                    uint4 lo[2], hi[2];
-                    uint32_t nan = 0;
-#pragma unroll
-                    for (int u = 0; u < 2; ++u) {
-                        nan |= has_nan(v[u].x) | has_nan(v[u].y) | has_nan(v[u].z) | has_nan(v[u].w);
-                        widen4(v[u].x, lo[u].x, lo[u].y);
-                        widen4(v[u].y, lo[u].z, lo[u].w);
-                        widen4(v[u].z, hi[u].x, hi[u].y);
-                        widen4(v[u].w, hi[u].z, hi[u].w);
-                    }
-                    if (nan) {
-#pragma unroll
-                        for (int u = 0; u < 2; ++u) {
-                            keep_nan(v[u].x, lo[u].x, lo[u].y);
-                            keep_nan(v[u].y, lo[u].z, lo[u].w);
-                            keep_nan(v[u].z, hi[u].x, hi[u].y);
-                            keep_nan(v[u].w, hi[u].z, hi[u].w);
-                        }
-                    }
                     SVQ_WAIT(ct->empty[st], ((at / C::kRing) & 1) ^ 1, widen_end);
+                    unsigned char* const o = ring + st * kUnit + (c >> 2) * 1024 + r * 128;
+                    const int at0 = ((2 * c) & 7 ^ r) << 4, at1 = ((2 * c + 1) & 7 ^ r) << 4;
 #pragma unroll
-                    for (int u = 0; u < 2; ++u) {
-                        const int rr = r + 32 * u;
-                        unsigned char* const o = ring + st * kUnit + (rr >> 3) * 2048 + (c >> 2) * 1024 + (rr & 7) * 128;
-                        *reinterpret_cast<uint4*>(o + (((2 * c) & 7 ^ (rr & 7)) << 4)) = lo[u];
-                        *reinterpret_cast<uint4*>(o + (((2 * c + 1) & 7 ^ (rr & 7)) << 4)) = hi[u];
+                    for (int u = 0; u < 8; ++u) {
+                        uint4 lo, hi;
+                        widen4(v[u].x, lo.x, lo.y);
+                        widen4(v[u].y, lo.z, lo.w);
+                        widen4(v[u].z, hi.x, hi.y);
+                        widen4(v[u].w, hi.z, hi.w);
+                        if (has_nan(v[u].x) | has_nan(v[u].y) | has_nan(v[u].z) | has_nan(v[u].w)) {
+                            keep_nan(v[u].x, lo.x, lo.y);
+                            keep_nan(v[u].y, lo.z, lo.w);
+                            keep_nan(v[u].z, hi.x, hi.y);
+                            keep_nan(v[u].w, hi.z, hi.w);
+                        }
+                        *reinterpret_cast<uint4*>(o + u * 2048 + at0) = lo;
+                        *reinterpret_cast<uint4*>(o + u * 2048 + at1) = hi;
                     }
                     fence_proxy_async_smem();
                     __syncwarp();
@@ -1228,7 +1269,7 @@ bool encode_latents(CUtensorMap* map, const void* p, int64_t pages, bool fp8) {
         const cuuint64_t dims[2] = {kLatentDim, static_cast<cuuint64_t>(pages) * kPage};
         const cuuint64_t strides[1] = {kLatentDim};
         const cuuint32_t box[2] = {128, kPage};
-        return encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, p, 2, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_NONE);
+        return encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, p, 2, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B);
     }
     const cuuint64_t dims[4] = {64, 8, kLatentDim / 64, static_cast<cuuint64_t>(pages) * 2};
     const cuuint64_t strides[3] = {2 * kLatentDim, 128, 16 * kLatentDim};

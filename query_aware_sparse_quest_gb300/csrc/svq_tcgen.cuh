@@ -38,8 +38,8 @@ __device__ __forceinline__ uint32_t elected() {
     asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(e));
     return e;
 }
-// A value that all lanes of the warp hold, as the compiler cannot see.
-__device__ __forceinline__ int uniform(int v) { return __shfl_sync(0xffffffffu, v, 0); }
+// A value that all lanes of the warp hold, as the compiler cannot see: a reduction leaves it in a uniform register.
+__device__ __forceinline__ int uniform(int v) { return static_cast<int>(__reduce_or_sync(0xffffffffu, static_cast<unsigned>(v))); }
 __device__ __forceinline__ void mma_commit(uint32_t bar) {
     asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
 }
@@ -130,6 +130,17 @@ __device__ __forceinline__ bool bar_wait(uint32_t bar, uint32_t parity) {
         "done:\n\tselp.u32 %0, 1, 0, p;\n\t}"
         : "=r"(ok)
         : "r"(bar), "r"(parity), "n"(kPolls), "r"(kPollNs)
+        : "memory");
+    return ok != 0;
+}
+// Whether the phase is over, without waiting; and how often a warp may ask before it gives up (about half a second).
+constexpr uint32_t kTests = 1u << 24;
+__device__ __forceinline__ bool bar_test(uint32_t bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tmbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity)
         : "memory");
     return ok != 0;
 }
