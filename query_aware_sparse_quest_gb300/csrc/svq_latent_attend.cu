@@ -72,6 +72,8 @@ struct Cfg {
     // Units of a tile that the first of the two loading warps takes.  Pairs free code slots out of order, so a slot is
     // one warp's: with slots that are not a multiple of the units, all are the first's.
     static constexpr int kFirst = kCodes % 4 ? 4 : 2;
+    // (e4m3: 128 registers a thread at launch, then 88 for the first four warps, 216 for the softmax, 104 for widening:
+    // 128 x (88 + 216 + 2 x 104) = 512 x 128.)
     static constexpr int kThreads = FP8 ? 512 : 256;
     static constexpr int kWiden = 8;                                                              // warps
     static constexpr int kQ = N * kQueryDim * 2;
@@ -227,10 +229,11 @@ struct Control {
     uint64_t code_full[8], code_empty[8];
     uint64_t scale_full[kInfoSlots];
     uint64_t seg_full[kSegs], seg_empty[kSegs];
-    uint64_t s_full[2], p_full, pv_done, q_full, drain;
+    uint64_t s_full[2], p_full, pv_done, q_full, vote, drain;
     uint32_t tmem;
     int gave_up;
     int fault[kInfoSlots];                 // pages of a tile that the table does not give
+    int over[4];                           // a logit of the tile is too far above its row's base
     Seg seg[kSegs];
     float red[4][kMaxRows];                // maxima (and, at a segment's end, sums) of each softmax warp
     float base[kMaxRows], alpha[kMaxRows];
@@ -314,6 +317,8 @@ __global__ void __launch_bounds__(Cfg<N, FP8>::kThreads, 1)
         mbar_init(smem_addr(&ct->p_full), 4);
         mbar_init(smem_addr(&ct->pv_done), 1);
         mbar_init(smem_addr(&ct->q_full), 1);
+        mbar_init(smem_addr(&ct->vote), 4);
+        for (int i = 0; i < 4; ++i) ct->over[i] = 0;
         mbar_init(smem_addr(&ct->drain), 1);
         mbar_init_fence();
         prefetch_tmap(&tmap_q);
@@ -339,6 +344,7 @@ __global__ void __launch_bounds__(Cfg<N, FP8>::kThreads, 1)
     {
         if (warp == 0 || warp == 3) {
             // ---------------- loads: warp 0 scales and the first kFirst units, warp 3 the rest; each in step
+            if (FP8) reg_dec<88>();
             const bool rest = warp == 3;
             const uint32_t go = elected();
             uint32_t tile = 0, loaded = 0;
@@ -432,6 +438,7 @@ __global__ void __launch_bounds__(Cfg<N, FP8>::kThreads, 1)
         loads_done:;
         } else if (warp == 1) {
             // ---------------- MMAs: the whole warp, in step
+            if (FP8) reg_dec<88>();
             {
                 const uint32_t go = elected();
                 uint32_t tile = 0, segs = 0;   // tiles before the segment; segments with tiles
@@ -445,7 +452,6 @@ __global__ void __launch_bounds__(Cfg<N, FP8>::kThreads, 1)
                 auto commit = [&](uint64_t& bar) {
                     if (go) mma_commit(smem_addr(&bar));
                 };
-                auto poll = [&](uint64_t& bar, uint32_t parity) { return __all_sync(0xffffffffu, bar_test(smem_addr(&bar), parity)) != 0; };
                 // O^T of the tile whose P is ready: `pv_pages` pages of tile pv_tile, onto what there is if pv_acc.
                 bool pv_due = false, pv_acc = false;
                 uint32_t pv_tile = 0;
@@ -469,26 +475,34 @@ __global__ void __launch_bounds__(Cfg<N, FP8>::kThreads, 1)
                 };
                 // S^T of tile t (counted over the CTA's work), unit after unit as they land, then the rotary part.  The
                 // product of the tile before goes in between as soon as its P is ready: it frees the memory that later
-                // units wait for.
+                // units wait for.  One look asks for all of them, a barrier a lane: a look takes as long as five MMAs, and
+                // the tensor pipe queues only a few.
                 auto qk = [&](uint32_t t) {
                     const uint32_t d = tmem + C::kColS + (t & 1) * C::kSCols;
-#pragma unroll 1
-                    for (int u = 0; u <= kUnits; ++u) {
-                        const uint32_t at = t * kUnits + u, st = at % C::kRing, rt = t % C::kRope;
-                        uint64_t& bar = u < kUnits ? ct->full[st] : ct->rope_full[rt];
-                        const uint32_t parity = (u < kUnits ? at / C::kRing : t / C::kRope) & 1;
-                        for (uint32_t tests = 0; !poll(bar, parity); ++tests) {
-                            if (pv_due && poll(ct->p_full, pv_tile & 1)) pv();
-                            if (tests == kTests) return false;
+                    const uint32_t at = t * kUnits + lane, rt = t % C::kRope;
+                    const uint32_t bar = lane < kUnits ? smem_addr(&ct->full[at % C::kRing]) : (lane == kUnits ? smem_addr(&ct->rope_full[rt]) : smem_addr(&ct->p_full));
+                    const uint32_t parity = (lane < kUnits ? at / C::kRing : (lane == kUnits ? t / C::kRope : t - 1)) & 1;
+                    uint32_t tests = 0;
+                    for (int u = 0; u <= kUnits;) {
+                        const uint32_t done = __ballot_sync(0xffffffffu, lane <= kUnits + 1 && bar_test(bar, parity));
+                        if (pv_due && (done >> (kUnits + 1))) pv();
+                        if (!((done >> u) & 1u)) {
+                            if (++tests == kTests) return false;
+                            continue;
                         }
                         tc_fence_after();
-                        if (u < kUnits)
+#pragma unroll 1
+                        for (; u < kUnits && ((done >> u) & 1u); ++u) {
+                            const uint32_t st = (t * kUnits + u) % C::kRing;
                             mma_qk8(d, desc_lo(ring_s + st * kUnit, 16), desc_lo(q_s + 2 * u * kBlockQ, 16), kBlockQ >> 4, idesc(64, N), u != 0, go);
-                        else
+                        }
+                        if (u == kUnits && ((done >> kUnits) & 1u)) {
                             mma_rope4(FP8 ? d + N : d, desc_lo(smem_addr(ropes) + rt * kRopeBytes, 16), desc_lo(q_s + 8 * kBlockQ, 16),
                                       idesc(64, N), !FP8, go);
+                            ++u;
+                        }
                     }
-                    commit(ct->rope_empty[t % C::kRope]);
+                    commit(ct->rope_empty[rt]);
                     commit(ct->s_full[t & 1]);
                     return true;
                 };
@@ -524,6 +538,7 @@ __global__ void __launch_bounds__(Cfg<N, FP8>::kThreads, 1)
             __syncwarp();
         } else if (warp == 2) {
             // ---------------- the group's share of the plan, segment by segment
+            if (FP8) reg_dec<88>();
             const int num_entries = *a.num_entries;
             const int64_t total = a.cum[num_entries];
             const int groups = groups_of(total, gridDim.x / a.share);
@@ -602,6 +617,7 @@ __global__ void __launch_bounds__(Cfg<N, FP8>::kThreads, 1)
         plan_end:;
         } else if (warp >= 4 && warp < 8) {
             // ---------------- softmax: warp w tokens 16 w .., lane l rows 8 c + 2 (l % 4), + 1 of tokens l / 4, + 8
+            if (FP8) reg_inc<216>();
             const int w = warp - 4, tid = threadIdx.x - 128;
             const int quad = lane & 3, row8 = lane >> 2;
             const uint32_t lanes = static_cast<uint32_t>(w * 32) << 16;
@@ -686,16 +702,47 @@ __global__ void __launch_bounds__(Cfg<N, FP8>::kThreads, 1)
                             }
                     }
                     // Weights go by the rows' bases as they are, unless a logit is more than kSlack above its row's: then
-                    // (at a run's first tile, and seldom behind it) the tile's maxima move the bases.  Columns without a
-                    // row have no say.
+                    // (at a run's first tile, and seldom behind it) the tile's maxima move the bases.  The warps say so to
+                    // one another while they work out the weights.  Columns without a row have an infinite base.
+                    uint32_t p[kGroups][2];
+                    float add[2 * kGroups], add_r[2 * kGroups];
                     float over = -INFINITY;
+                    auto weights = [&] {
 #pragma unroll
-                    for (int c = 0; c < kGroups; ++c)
-#pragma unroll
-                        for (int u = 0; u < 2; ++u)
-                            if (8 * c + 2 * quad + u < rows)
-                                over = fmaxf(over, fmaf(fmaxf(x[4 * c + u], x[4 * c + 2 + u]), a.scale_log2, -base[2 * c + u]));
-                    const bool any = softmax_any(dead || j == 0 || over > kSlack);
+                        for (int c = 0; c < kGroups; ++c) {
+                            const uint64_t scale2 = pack2(a.scale_log2, a.scale_log2), base2 = pack2(-base[2 * c], -base[2 * c + 1]);
+                            float y[4];
+                            unpack2(fma2(pack2(x[4 * c], x[4 * c + 1]), scale2, base2), y[0], y[1]);
+                            unpack2(fma2(pack2(x[4 * c + 2], x[4 * c + 3]), scale2, base2), y[2], y[3]);
+                            over = fmaxf(over, fmaxf(fmaxf(y[0], y[1]), fmaxf(y[2], y[3])));
+                            uint64_t e0 = pack2(ex2(y[0]), ex2(y[1])), e1 = pack2(ex2(y[2]), ex2(y[3]));
+                            unpack2(add2(e0, e1), add[2 * c], add[2 * c + 1]);
+                            if (FP8) {
+                                e0 = mul2(e0, pack2(sc0, sc0));
+                                e1 = mul2(e1, pack2(sc1, sc1));
+                            }
+                            unpack2(e0, y[0], y[1]);
+                            unpack2(e1, y[2], y[3]);
+                            p[c][0] = pack_bf16x2(y[0], y[1]);
+                            p[c][1] = pack_bf16x2(y[2], y[3]);
+                            if (!FP8) {
+                                add_r[2 * c] = bf16lo(p[c][0]) + bf16lo(p[c][1]);
+                                add_r[2 * c + 1] = bf16hi(p[c][0]) + bf16hi(p[c][1]);
+                            }
+                        }
+                    };
+                    if (j > 0) {
+                        weights();
+                        if (dead || over > kSlack) *static_cast<volatile int*>(&ct->over[tile & 3]) = 1;
+                    } else if (lane == 0) {
+                        *static_cast<volatile int*>(&ct->over[tile & 3]) = 1;
+                    }
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(smem_addr(&ct->vote));
+                    LATENT_WAIT(ct->vote, tile & 1);
+                    const bool any = *static_cast<volatile int*>(&ct->over[tile & 3]) != 0;
+                    // (The slot of the tile after the next: all have read it, and none is there yet.)
+                    if (tid == 0) *static_cast<volatile int*>(&ct->over[(tile + 2) & 3]) = 0;
                     if (any) {
                         if (softmax_any(dead)) goto softmax_end;
                         float mx[2 * kGroups];
@@ -723,7 +770,7 @@ __global__ void __launch_bounds__(Cfg<N, FP8>::kThreads, 1)
                                 alpha = m == -INFINITY ? 0.f : ex2(m - top);   // (nothing was added yet)
                                 m = top;
                             }
-                            ct->base[tid] = m == -INFINITY ? 0.f : m;   // (0: a row that has seen nothing yet)
+                            ct->base[tid] = tid >= rows ? INFINITY : (m == -INFINITY ? 0.f : m);   // (0: a row that has seen nothing yet)
                             ct->alpha[tid] = alpha;
                         }
                         softmax_sync();
@@ -751,6 +798,7 @@ __global__ void __launch_bounds__(Cfg<N, FP8>::kThreads, 1)
                             }
                             tc_wait_st();
                         }
+                        weights();
                     }
                     if (j > 0 && (j & (kFoldTiles - 1)) == 0) {
                         // O moves to the fp32 sums: thread's channel 128 u + tid, row after row.
@@ -777,33 +825,17 @@ __global__ void __launch_bounds__(Cfg<N, FP8>::kThreads, 1)
                         }
                         softmax_sync();   // (alpha is written again)
                     }
-                    // Weights, their sums, and P^T, a row of 64 tokens each.
+                    // Sums, and P^T, a row of 64 tokens each: blocks of tokens 16 w .. + 7 and + 8 .. + 15 of rows 8 c ..,
+                    // then of rows 8 (c + 1) ..
 #pragma unroll
                     for (int c = 0; c < kGroups; c += 2) {
-                        uint32_t p[4];
-#pragma unroll
-                        for (int g = 0; g < 2; ++g) {
-                            float e[4];
-#pragma unroll
-                            for (int u = 0; u < 4; ++u) e[u] = ex2(fmaf(x[4 * (c + g) + u], a.scale_log2, -base[2 * (c + g) + (u & 1)]));
-                            l[2 * (c + g)] += e[0] + e[2];
-                            l[2 * (c + g) + 1] += e[1] + e[3];
-                            if (FP8) {
-                                e[0] *= sc0;
-                                e[1] *= sc0;
-                                e[2] *= sc1;
-                                e[3] *= sc1;
-                            }
-                            p[2 * g] = pack_bf16x2(e[0], e[1]);
-                            p[2 * g + 1] = pack_bf16x2(e[2], e[3]);
-                            if (!FP8) {
-                                lr[2 * (c + g)] += bf16lo(p[2 * g]) + bf16lo(p[2 * g + 1]);
-                                lr[2 * (c + g) + 1] += bf16hi(p[2 * g]) + bf16hi(p[2 * g + 1]);
-                            }
-                        }
-                        // Blocks: tokens 16 w .. + 7 and + 8 .. + 15 of rows 8 c .., then of rows 8 (c + 1) ..
                         const int r = 8 * (c + (lane >> 4)) + (lane & 7), chunk = 2 * w + ((lane >> 3) & 1);
-                        stmatrix_x4_trans(smem_addr(ps) + r * 128 + ((chunk ^ (r & 7)) << 4), p[0], p[1], p[2], p[3]);
+                        stmatrix_x4_trans(smem_addr(ps) + r * 128 + ((chunk ^ (r & 7)) << 4), p[c][0], p[c][1], p[c + 1][0], p[c + 1][1]);
+                    }
+#pragma unroll
+                    for (int c = 0; c < 2 * kGroups; ++c) {
+                        l[c] += add[c];
+                        if (!FP8) lr[c] += add_r[c];
                     }
                     // Tokens that no row sees may hold anything: their channels become zeros (P = 0 must not meet a
                     // NaN) in the pages that the product reads.
@@ -897,6 +929,7 @@ __global__ void __launch_bounds__(Cfg<N, FP8>::kThreads, 1)
             if (tid == 0 && q_loads) (void)bar_wait(smem_addr(&ct->q_full), (q_loads - 1) & 1);
         } else if (FP8 && warp >= 8) {
             // ---------------- e4m3 codes -> bf16 units in the MMAs' layout, two warps a unit
+            reg_dec<104>();
             const int tid = threadIdx.x & 63, mine = (warp - 8) >> 1;
             uint32_t at = mine, until = 0;
             constexpr uint32_t kDepth = FP8 ? C::kCodes : 1;
