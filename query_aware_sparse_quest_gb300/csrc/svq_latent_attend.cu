@@ -29,12 +29,13 @@
 // by a second kernel.
 //
 // Roles of a CTA (one per SM):
-//   warp 0       loads the pages: units of 64 tokens x 128 channels (16 KB), each
-//                freed when its part of the second product is done, and rotary keys
 //   warp 1       issues the MMAs
 //   warp 2       walks the plan
 //   warps 4-7    softmax (16 tokens each), outputs
-//   warps 8-15   (e4m3) widen the codes
+//   warps 8-11   load a page of the tile each: units of 64 tokens x 128 channels (16
+//                KB), each freed when its part of the second product is done, and
+//                rotary keys
+//   warps 12-19  (e4m3) widen the codes
 #include <climits>
 
 #include "svq_paged.cuh"
@@ -69,12 +70,11 @@ struct Cfg {
     // Pairs of warps that widen a unit each, in turn.  (A pair sees every phase of the slots it reads: kCodes % kPairs is 0.)
     static constexpr int kPairs = N == 64 ? 3 : 4;
     static_assert(kCodes % kPairs == 0, "code slots");
-    // Units of a tile that the first of the two loading warps takes.  Pairs free code slots out of order, so a slot is
-    // one warp's: with slots that are not a multiple of the units, all are the first's.
-    static constexpr int kFirst = kCodes % 4 ? 4 : 2;
-    // (e4m3: 128 registers a thread at launch, then 88 for the first four warps, 216 for the softmax, 104 for widening:
-    // 128 x (88 + 216 + 2 x 104) = 512 x 128.)
-    static constexpr int kThreads = FP8 ? 512 : 256;
+    // Registers a thread: bf16 168 at launch, then 96 for the first four warps and the loads and 248 for the softmax
+    // (128 x (96 + 248 + 96) < 384 x 168); e4m3 96, then 72, 184 and 64, and 80 for widening (128 x (72 + 184 + 64 + 2 x 80)
+    // = 640 x 96).
+    static constexpr int kThreads = FP8 ? 640 : 384;
+    static constexpr int kMmaRegs = FP8 ? 72 : 96, kSoftmaxRegs = FP8 ? 184 : 248, kLoadRegs = FP8 ? 64 : 96, kWidenRegs = 80;
     static constexpr int kWiden = 8;                                                              // warps
     static constexpr int kQ = N * kQueryDim * 2;
     static constexpr int kP = N * kTok * 2;
@@ -232,7 +232,7 @@ struct Control {
     uint64_t s_full[2], p_full, pv_done, q_full, vote, drain;
     uint32_t tmem;
     int gave_up;
-    int fault[kInfoSlots];                 // pages of a tile that the table does not give
+    uint8_t fault[kInfoSlots][kPages];     // pages of a tile that the table does not give
     int over[4];                           // a logit of the tile is too far above its row's base
     Seg seg[kSegs];
     float red[4][kMaxRows];                // maxima (and, at a segment's end, sums) of each softmax warp
@@ -296,21 +296,21 @@ __global__ void __launch_bounds__(Cfg<N, FP8>::kThreads, 1)
     if (threadIdx.x == 0) {
         ct->gave_up = 0;
         for (int i = 0; i < C::kRing; ++i) {
-            mbar_init(smem_addr(&ct->full[i]), FP8 ? 2 : 1);
+            mbar_init(smem_addr(&ct->full[i]), FP8 ? 2 : kPages);
             mbar_init(smem_addr(&ct->empty[i]), 1);
         }
         for (int i = 0; i < C::kRope; ++i) {
-            mbar_init(smem_addr(&ct->rope_full[i]), 1);
+            mbar_init(smem_addr(&ct->rope_full[i]), kPages);
             mbar_init(smem_addr(&ct->rope_empty[i]), 1);
         }
         for (int i = 0; i < C::kCodes; ++i) {
-            mbar_init(smem_addr(&ct->code_full[i]), 1);
+            mbar_init(smem_addr(&ct->code_full[i]), kPages);
             mbar_init(smem_addr(&ct->code_empty[i]), 2);
         }
-        for (int i = 0; i < kInfoSlots; ++i) mbar_init(smem_addr(&ct->scale_full[i]), 1);
+        for (int i = 0; i < kInfoSlots; ++i) mbar_init(smem_addr(&ct->scale_full[i]), kPages);
         for (int i = 0; i < kSegs; ++i) {
             mbar_init(smem_addr(&ct->seg_full[i]), 1);
-            mbar_init(smem_addr(&ct->seg_empty[i]), 3 + 4 + (FP8 ? C::kWiden : 0));   // loads, MMAs, softmax, widening
+            mbar_init(smem_addr(&ct->seg_empty[i]), kPages + 1 + 4 + (FP8 ? C::kWiden : 0));   // loads, MMAs, softmax, widening
         }
         mbar_init(smem_addr(&ct->s_full[0]), 1);
         mbar_init(smem_addr(&ct->s_full[1]), 1);
@@ -342,103 +342,9 @@ __global__ void __launch_bounds__(Cfg<N, FP8>::kThreads, 1)
     };
 
     {
-        if (warp == 0 || warp == 3) {
-            // ---------------- loads: warp 0 scales and the first kFirst units, warp 3 the rest; each in step
-            if (FP8) reg_dec<88>();
-            const bool rest = warp == 3;
-            const uint32_t go = elected();
-            uint32_t tile = 0, loaded = 0;
-            for (uint32_t k = 0;; ++k) {
-                SVQ_WAIT(ct->seg_full[k % kSegs], (k / kSegs) & 1, loads_end);
-                const Seg& s = ct->seg[k % kSegs];
-                const int t0 = uniform(s.t0), n = uniform(s.t1) - t0;
-                if (n == 0) break;
-                const int end = min(s.en.npages, s.t1 * kPages);
-                const int32_t* const pages = a.page_table + static_cast<int64_t>(s.en.req) * a.max_pages;
-                // Lane l resolves page i + l of the segment (eight tiles at a time), well before the loads that need it:
-                // -2 behind the last page, -1 what the table does not give.
-                auto fetch = [&](int i0) {
-                    const int i = i0 + lane;
-                    const int ph = i < end ? pages[i] : -2;
-                    return ph >= a.num_pages || ph < -2 || (ph == -2 && i < end) ? -1 : ph;
-                };
-                int cur = -2, nxt = fetch(t0 * kPages);
-                for (int i = 0; i < n; ++i, ++tile) {
-                    if (i % 8 == 0) {
-                        cur = nxt;
-                        if (i + 8 < n) nxt = fetch((t0 + i + 8) * kPages);
-                    }
-                    int ph[kPages];
-                    uint32_t faults = 0, loads = 0;
-#pragma unroll
-                    for (int p = 0; p < kPages; ++p) {
-                        ph[p] = uniform(__shfl_sync(0xffffffffu, cur, (i % 8) * kPages + p));
-                        faults |= ph[p] == -1 ? 1u << p : 0u;
-                        loads += ph[p] >= 0;
-                    }
-                    const uint32_t slot = tile % kInfoSlots;
-                    if (go) {
-                        if (faults) svq_flag(SV_DEVERR_PAGE_TABLE);
-                        if (!rest) ct->fault[slot] = static_cast<int>(faults);
-                    }
-                    if (FP8 && !rest) {
-                        const uint32_t bar = smem_addr(&ct->scale_full[slot]);
-                        if (go) mbar_arrive_expect_tx(bar, loads * kPage * 4);
-                        __syncwarp();
-                        const int mine = lane == 0 ? ph[0] : (lane == 1 ? ph[1] : (lane == 2 ? ph[2] : ph[3]));
-                        if (lane < kPages && mine >= 0)
-                            bulk_copy_g2s(smem_addr(scales + slot * kTok + lane * kPage), a.scale + static_cast<int64_t>(mine) * kPage, kPage * 4, bar);
-                        __syncwarp();
-                    }
-#pragma unroll
-                    for (int u = 0; u < kUnits; ++u) {
-                        if ((u >= C::kFirst) != rest) continue;
-                        const uint32_t at = tile * kUnits + u;
-                        constexpr uint32_t kDepth = FP8 ? (C::kCodes ? C::kCodes : 1) : C::kRing;
-                        uint64_t* const empty = FP8 ? ct->code_empty : ct->empty;
-                        uint64_t* const full = FP8 ? ct->code_full : ct->full;
-                        constexpr uint32_t kPageBytes = kPage * (FP8 ? 128 : 256);
-                        const uint32_t st = at % kDepth;
-                        SVQ_WAIT(empty[st], ((at / kDepth) & 1) ^ 1, loads_end);
-                        const uint32_t bar = smem_addr(&full[st]), dst = smem_addr(FP8 ? codes : ring) + st * (kPageBytes * kPages);
-                        if (go) mbar_arrive_expect_tx(bar, loads * kPageBytes);
-                        __syncwarp();
-#pragma unroll
-                        for (int p = 0; p < kPages; ++p) {
-                            const uint32_t on = ph[p] >= 0 ? go : 0u;
-                            if (FP8) tma_2d_if(on, dst + p * kPageBytes, &tmap_c, u * 128, ph[p] * kPage, bar);
-                            else tma_page_if(on, dst + p * kPageBytes, &tmap_c, 2 * u, 2 * ph[p], bar);
-                        }
-                        loaded = at + 1;
-                    }
-                    if (!rest) continue;
-                    const uint32_t st = tile % C::kRope;
-                    SVQ_WAIT(ct->rope_empty[st], ((tile / C::kRope) & 1) ^ 1, loads_end);
-                    const uint32_t bar = smem_addr(&ct->rope_full[st]);
-                    if (go) mbar_arrive_expect_tx(bar, loads * (kPage * kRopeDim * 2));
-                    __syncwarp();
-#pragma unroll
-                    for (int p = 0; p < kPages; ++p)
-                        tma_2d_if(ph[p] >= 0 ? go : 0u, smem_addr(ropes) + st * kRopeBytes + p * (kPage * kRopeDim * 2), &tmap_r, 0, ph[p] * kPage, bar);
-                }
-                seg_done(k);
-            }
-            goto loads_done;   // every load has been waited for by the MMAs or the widening warps
-        loads_end:
-            // Gave up: the copies still in flight land before the CTA (and its shared memory) retires.
-            {
-                constexpr uint32_t kDepth = FP8 ? (C::kCodes ? C::kCodes : 1) : C::kRing;
-                uint64_t* const full = FP8 ? ct->code_full : ct->full;
-                for (uint32_t x = loaded > kDepth ? loaded - kDepth : 0; x < loaded; ++x)
-                    (void)bar_wait(smem_addr(&full[x % kDepth]), (x / kDepth) & 1);
-                for (uint32_t x = tile > C::kRope ? tile - C::kRope : 0; x < tile; ++x)
-                    (void)bar_wait(smem_addr(&ct->rope_full[x % C::kRope]), (x / C::kRope) & 1);
-                if (FP8) (void)bar_wait(smem_addr(&ct->scale_full[tile % kInfoSlots]), (tile / kInfoSlots) & 1);
-            }
-        loads_done:;
-        } else if (warp == 1) {
+        if (warp == 1) {
             // ---------------- MMAs: the whole warp, in step
-            if (FP8) reg_dec<88>();
+            reg_dec<C::kMmaRegs>();
             {
                 const uint32_t go = elected();
                 uint32_t tile = 0, segs = 0;   // tiles before the segment; segments with tiles
@@ -538,7 +444,7 @@ __global__ void __launch_bounds__(Cfg<N, FP8>::kThreads, 1)
             __syncwarp();
         } else if (warp == 2) {
             // ---------------- the group's share of the plan, segment by segment
-            if (FP8) reg_dec<88>();
+            reg_dec<C::kMmaRegs>();
             const int num_entries = *a.num_entries;
             const int64_t total = a.cum[num_entries];
             const int groups = groups_of(total, gridDim.x / a.share);
@@ -617,7 +523,7 @@ __global__ void __launch_bounds__(Cfg<N, FP8>::kThreads, 1)
         plan_end:;
         } else if (warp >= 4 && warp < 8) {
             // ---------------- softmax: warp w tokens 16 w .., lane l rows 8 c + 2 (l % 4), + 1 of tokens l / 4, + 8
-            if (FP8) reg_inc<216>();
+            reg_inc<C::kSoftmaxRegs>();
             const int w = warp - 4, tid = threadIdx.x - 128;
             const int quad = lane & 3, row8 = lane >> 2;
             const uint32_t lanes = static_cast<uint32_t>(w * 32) << 16;
@@ -667,8 +573,8 @@ __global__ void __launch_bounds__(Cfg<N, FP8>::kThreads, 1)
                     for (int c = 0; c < kGroups / 2; ++c) tc_ld_frag(s_col + c * 16, reinterpret_cast<float(&)[8]>(x[c * 8]));
                     tc_wait_ld();
                     const int tok0 = first + 16 * w + row8, tok1 = tok0 + 8;
-                    const int fault = ct->fault[slot];
-                    const bool gone = (fault >> w) & 1;     // the warp's tokens are one page
+                    const uint32_t fault = *reinterpret_cast<const uint32_t*>(ct->fault[slot]);
+                    const bool gone = (fault >> (8 * w)) & 1u;     // the warp's tokens are one page
                     float sc0 = 1.f, sc1 = 1.f;
                     if (FP8) {
                         LATENT_WAIT(ct->scale_full[slot], (tile / kInfoSlots) & 1);
@@ -739,7 +645,15 @@ __global__ void __launch_bounds__(Cfg<N, FP8>::kThreads, 1)
                     }
                     __syncwarp();
                     if (lane == 0) mbar_arrive(smem_addr(&ct->vote));
-                    LATENT_WAIT(ct->vote, tile & 1);
+                    // (P's memory and O are free when the product before is done: the same look asks for that.)
+                    {
+                        const bool first = lane == 0 || j == 0;
+                        const uint32_t bar = first ? smem_addr(&ct->vote) : smem_addr(&ct->pv_done), parity = (first ? tile : tile - 1) & 1;
+                        if (!__all_sync(0xffffffffu, bar_test(bar, parity)) && __any_sync(0xffffffffu, !bar_wait(bar, parity))) {
+                            if (lane == 0) gave_up(ct);
+                            dead = true;
+                        }
+                    }
                     const bool any = *static_cast<volatile int*>(&ct->over[tile & 3]) != 0;
                     // (The slot of the tile after the next: all have read it, and none is there yet.)
                     if (tid == 0) *static_cast<volatile int*>(&ct->over[(tile + 2) & 3]) = 0;
@@ -775,8 +689,6 @@ __global__ void __launch_bounds__(Cfg<N, FP8>::kThreads, 1)
                         }
                         softmax_sync();
                     }
-                    // P's memory and O are free when the product before is done.
-                    if (j > 0) LATENT_WAIT(ct->pv_done, (tile - 1) & 1);
                     if (any) {
 #pragma unroll
                         for (int c = 0; c < 2 * kGroups; ++c) {
@@ -825,17 +737,12 @@ __global__ void __launch_bounds__(Cfg<N, FP8>::kThreads, 1)
                         }
                         softmax_sync();   // (alpha is written again)
                     }
-                    // Sums, and P^T, a row of 64 tokens each: blocks of tokens 16 w .. + 7 and + 8 .. + 15 of rows 8 c ..,
+                    // P^T, a row of 64 tokens each: blocks of tokens 16 w .. + 7 and + 8 .. + 15 of rows 8 c ..,
                     // then of rows 8 (c + 1) ..
 #pragma unroll
                     for (int c = 0; c < kGroups; c += 2) {
                         const int r = 8 * (c + (lane >> 4)) + (lane & 7), chunk = 2 * w + ((lane >> 3) & 1);
                         stmatrix_x4_trans(smem_addr(ps) + r * 128 + ((chunk ^ (r & 7)) << 4), p[c][0], p[c][1], p[c + 1][0], p[c + 1][1]);
-                    }
-#pragma unroll
-                    for (int c = 0; c < 2 * kGroups; ++c) {
-                        l[c] += add[c];
-                        if (!FP8) lr[c] += add_r[c];
                     }
                     // Tokens that no row sees may hold anything: their channels become zeros (P = 0 must not meet a
                     // NaN) in the pages that the product reads.
@@ -843,7 +750,7 @@ __global__ void __launch_bounds__(Cfg<N, FP8>::kThreads, 1)
                     if (fault || first + pages * kPage > see_any) {
                         for (int i = tid; i < pages * kPage * kUnits * 16; i += 128) {
                             const int r = i >> 6, u = (i >> 4) & 3, c = i & 15;
-                            if (first + r >= see_any || ((fault >> (r / kPage)) & 1))
+                            if (first + r >= see_any || ((fault >> (r / kPage * 8)) & 1u))
                                 *reinterpret_cast<uint4*>(ring + (tile * kUnits + u) % C::kRing * kUnit + (r >> 3) * 2048 + (c >> 3) * 1024 +
                                                           (r & 7) * 128 + (c & 7) * 16) = make_uint4(0u, 0u, 0u, 0u);
                         }
@@ -852,6 +759,11 @@ __global__ void __launch_bounds__(Cfg<N, FP8>::kThreads, 1)
                     tc_fence_before();
                     __syncwarp();
                     if (lane == 0) mbar_arrive(smem_addr(&ct->p_full));
+#pragma unroll
+                    for (int c = 0; c < 2 * kGroups; ++c) {
+                        l[c] += add[c];
+                        if (!FP8) lr[c] += add_r[c];
+                    }
                 }
 
                 // ---------------- the segment's end
@@ -927,10 +839,96 @@ __global__ void __launch_bounds__(Cfg<N, FP8>::kThreads, 1)
         softmax_end:
             // (Gave up: the rows in flight land before the CTA retires.)
             if (tid == 0 && q_loads) (void)bar_wait(smem_addr(&ct->q_full), (q_loads - 1) & 1);
-        } else if (FP8 && warp >= 8) {
+        } else if (warp >= 8 && warp < 12) {
+            // ---------------- loads: warp 8 + p page p of every tile, in step
+            reg_dec<C::kLoadRegs>();
+            const uint32_t go = elected();
+            const int p = warp - 8;
+            uint32_t tile = 0, loaded = 0;
+            constexpr uint32_t kDepth = FP8 ? (C::kCodes ? C::kCodes : 1) : C::kRing;
+            constexpr uint32_t kPageBytes = kPage * (FP8 ? 128 : 256);
+            uint64_t* const empty = FP8 ? ct->code_empty : ct->empty;
+            uint64_t* const full = FP8 ? ct->code_full : ct->full;
+            const uint32_t to = smem_addr(FP8 ? codes : ring) + p * kPageBytes;
+            const uint32_t rope_to = smem_addr(ropes) + p * (kPage * kRopeDim * 2);
+            for (uint32_t k = 0;; ++k) {
+                SVQ_WAIT(ct->seg_full[k % kSegs], (k / kSegs) & 1, loads_end);
+                const Seg& s = ct->seg[k % kSegs];
+                const int t0 = uniform(s.t0), n = uniform(s.t1) - t0;
+                if (n == 0) break;
+                const int end = min(s.en.npages, s.t1 * kPages);
+                const int32_t* const pages = a.page_table + static_cast<int64_t>(s.en.req) * a.max_pages;
+                // Lane l resolves the page of tile i + l, well before the loads that need it: -2 behind the last page, -1
+                // what the table does not give.
+                auto fetch = [&](int i0) {
+                    const int i = (t0 + i0 + lane) * kPages + p;
+                    if (i0 + lane >= n || i >= end) return -2;
+                    const int ph = pages[i];
+                    return ph < 0 || ph >= a.num_pages ? -1 : ph;
+                };
+                int cur = -2, nxt = fetch(0);
+                for (int i = 0; i < n; ++i, ++tile) {
+                    if (i % 32 == 0) {
+                        cur = nxt;
+                        if (i + 32 < n) nxt = fetch(i + 32);
+                    }
+                    const int ph = uniform(__shfl_sync(0xffffffffu, cur, i % 32));
+                    const uint32_t on = ph >= 0 ? go : 0u;
+                    const uint32_t slot = tile % kInfoSlots;
+                    if (go) {
+                        if (ph == -1) svq_flag(SV_DEVERR_PAGE_TABLE);
+                        ct->fault[slot][p] = ph == -1;
+                    }
+                    if (FP8) {
+                        const uint32_t bar = smem_addr(&ct->scale_full[slot]);
+                        if (go) {
+                            if (ph >= 0) {
+                                mbar_arrive_expect_tx(bar, kPage * 4);
+                                bulk_copy_g2s(smem_addr(scales + slot * kTok + p * kPage), a.scale + static_cast<int64_t>(ph) * kPage, kPage * 4, bar);
+                            } else {
+                                mbar_arrive(bar);
+                            }
+                        }
+                    }
+#pragma unroll
+                    for (int u = 0; u < kUnits; ++u) {
+                        const uint32_t at = tile * kUnits + u, st = at % kDepth;
+                        SVQ_WAIT(empty[st], ((at / kDepth) & 1) ^ 1, loads_end);
+                        const uint32_t bar = smem_addr(&full[st]), dst = to + st * (kPageBytes * kPages);
+                        if (go) {
+                            if (ph >= 0) mbar_arrive_expect_tx(bar, kPageBytes);
+                            else mbar_arrive(bar);
+                        }
+                        __syncwarp();
+                        if (FP8) tma_2d_if(on, dst, &tmap_c, u * 128, ph * kPage, bar);
+                        else tma_page_if(on, dst, &tmap_c, 2 * u, 2 * ph, bar);
+                        loaded = at + 1;
+                    }
+                    const uint32_t st = tile % C::kRope;
+                    SVQ_WAIT(ct->rope_empty[st], ((tile / C::kRope) & 1) ^ 1, loads_end);
+                    const uint32_t bar = smem_addr(&ct->rope_full[st]);
+                    if (go) {
+                        if (ph >= 0) mbar_arrive_expect_tx(bar, kPage * kRopeDim * 2);
+                        else mbar_arrive(bar);
+                    }
+                    __syncwarp();
+                    tma_2d_if(on, rope_to + st * kRopeBytes, &tmap_r, 0, ph * kPage, bar);
+                }
+                seg_done(k);
+            }
+            goto loads_done;   // every load has been waited for by the MMAs or the widening warps
+        loads_end:
+            // Gave up: the copies still in flight land before the CTA (and its shared memory) retires.
+            for (uint32_t x = loaded > kDepth ? loaded - kDepth : 0; x < loaded; ++x)
+                (void)bar_wait(smem_addr(&full[x % kDepth]), (x / kDepth) & 1);
+            for (uint32_t x = tile > C::kRope ? tile - C::kRope : 0; x < tile; ++x)
+                (void)bar_wait(smem_addr(&ct->rope_full[x % C::kRope]), (x / C::kRope) & 1);
+            if (FP8) (void)bar_wait(smem_addr(&ct->scale_full[tile % kInfoSlots]), (tile / kInfoSlots) & 1);
+        loads_done:;
+        } else if (FP8 && warp >= 12) {
             // ---------------- e4m3 codes -> bf16 units in the MMAs' layout, two warps a unit
-            reg_dec<104>();
-            const int tid = threadIdx.x & 63, mine = (warp - 8) >> 1;
+            reg_dec<C::kWidenRegs>();
+            const int tid = threadIdx.x & 63, mine = (warp - 12) >> 1;
             uint32_t at = mine, until = 0;
             constexpr uint32_t kDepth = FP8 ? C::kCodes : 1;
             for (uint32_t k = 0;; ++k) {
@@ -978,6 +976,8 @@ __global__ void __launch_bounds__(Cfg<N, FP8>::kThreads, 1)
                 seg_done(k);
             }
         widen_end:;
+        } else {
+            reg_dec<C::kMmaRegs>();   // (warps 0 and 3)
         }
     }
     __threadfence();
