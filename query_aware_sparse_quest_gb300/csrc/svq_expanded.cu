@@ -235,7 +235,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             reg_dec<kOtherRegs>();
             uint32_t base = 0, issued = 0;   // blocks before the segment; the last one loaded here, plus 1
             for (uint32_t k = 0;; ++k) {
-                SVQ_WAIT(ct->seg_full[k % kSegs], (k / kSegs) & 1, keys_end);
+                TEST_WAIT(ct->seg_full[k % kSegs], (k / kSegs) & 1, keys_end);
                 const Seg& s = ct->seg[k % kSegs];
                 const int n = s.t1 - s.t0;
                 if (n == 0) break;
@@ -245,7 +245,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                     for (int c = 0; c < 3; ++c) {
                         const uint32_t at = base + k_block(two, i) + c, st = at % kBlocks;
-                        SVQ_WAIT(ct->empty[st], ((at / kBlocks) & 1) ^ 1, keys_end);
+                        TEST_WAIT(ct->empty[st], ((at / kBlocks) & 1) ^ 1, keys_end);
                         if (lane == 0) {
                             const uint32_t bar = smem_addr(&ct->full[st]), dst = smem_addr(ring) + st * kBlock;
                             mbar_arrive_expect_tx(bar, kBlock);
@@ -270,7 +270,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             reg_dec<kOtherRegs>();
             uint32_t base = 0, issued = 0, part_ph = 0;
             for (uint32_t k = 0;; ++k) {
-                SVQ_WAIT(ct->seg_full[k % kSegs], (k / kSegs) & 1, values_end);
+                TEST_WAIT(ct->seg_full[k % kSegs], (k / kSegs) & 1, values_end);
                 const Seg& s = ct->seg[k % kSegs];
                 const int n = s.t1 - s.t0;
                 if (n == 0) break;
@@ -281,7 +281,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         const int here = s.en.len - first;          // tokens from here on
                         const uint32_t at = base + v_block(two, i, n) + c, st = at % kBlocks;
                         const uint32_t bar = smem_addr(&ct->full[st]), dst = smem_addr(ring) + st * kBlock;
-                        SVQ_WAIT(ct->empty[st], ((at / kBlocks) & 1) ^ 1, values_end);
+                        TEST_WAIT(ct->empty[st], ((at / kBlocks) & 1) ^ 1, values_end);
                         const bool whole = here >= 64, some = here > 0;
                         const uint32_t on = whole ? bar : smem_addr(&ct->part);
                         if (lane == 0 && some) {
@@ -294,7 +294,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                             // Rows behind the last token may hold anything; those that its product reads become
                             // zeros (P = 0 must not meet a NaN).
                             if (some) {
-                                SVQ_WAIT(ct->part, part_ph, values_end);
+                                TEST_WAIT(ct->part, part_ph, values_end);
                                 part_ph ^= 1;
                                 const int end = (here + 15) / 16 * 16;
                                 for (int x = here * 16 + lane; x < end * 16; x += 32)
@@ -323,7 +323,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 uint32_t ld = 0;
                 uint32_t q_ph = 0, p_ph = 0;   // bit w: stream w's phase
                 const uint32_t ring_s = smem_addr(ring), qs_s = smem_addr(qs);
-                auto wait = [&](uint64_t& bar, uint32_t parity) { return __all_sync(0xffffffffu, bar_wait(smem_addr(&bar), parity)) != 0; };
+                auto wait = [&](uint64_t& bar, uint32_t parity) { return __all_sync(0xffffffffu, bar_ready(smem_addr(&bar), parity)) != 0; };
                 auto commit = [&](uint64_t& bar) {
                     if (go) mma_commit(smem_addr(&bar));
                 };
@@ -532,12 +532,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (uint32_t k = 0;; ++k) {
                 const Seg& s = ct->seg[k % kSegs];
                 if (k == 0) {
-                    SVQ_WAIT(ct->seg_full[0], 0, softmax_end);
+                    TEST_WAIT(ct->seg_full[0], 0, softmax_end);
                     if (stream_tiles(s) > 0) load_q(s);
                 }
                 const int n = s.t1 - s.t0;
                 if (n == 0) break;
-                SVQ_WAIT(ct->seg_full[(k + 1) % kSegs], ((k + 1) / kSegs) & 1, softmax_end);
+                TEST_WAIT(ct->seg_full[(k + 1) % kSegs], ((k + 1) / kSegs) & 1, softmax_end);
                 const Seg& nx = ct->seg[(k + 1) % kSegs];
                 const bool next_q = stream_tiles(nx) > 0;
                 const int rows = s.en.ntok;
@@ -560,14 +560,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                 };
                 for (int j0 = 0; j0 < nt; j0 += kFoldTiles) {
                     if (j0 > 0) {
-                        SVQ_WAIT(ct->s_full[w], s_ph, softmax_end);   // O is complete, and the next product into it starts anew
+                        TEST_WAIT(ct->s_full[w], s_ph, softmax_end);   // O is complete, and the next product into it starts anew
                         if (warp_on) fold_out(o_col, folded(), valid, j0 > kFoldTiles, ct->ml[w][row], m, l);
                         l = 0.f;
                     }
                     for (int j = j0; j < min(nt, j0 + kFoldTiles); ++j) {
                         const int ti = two ? j : 2 * j + w;          // tile of the segment
                         const int base_tok = (s.t0 + ti) * kTileTok;
-                        SVQ_WAIT(ct->s_full[w], s_ph, softmax_end);
+                        TEST_WAIT(ct->s_full[w], s_ph, softmax_end);
                         s_ph ^= 1;
                         tc_fence_after();
                         if (j == nt - 1 && next_q) load_q(nx);       // the stream's last use of Q is over
@@ -651,21 +651,21 @@ __global__ void __launch_bounds__(kThreads, 1)
                 float f0 = 1.f, f1 = 0.f;   // factors of O0 and O1 (f0: of the own O when there are two row halves)
                 float M = m, L = l;
                 if (two) {
-                    SVQ_WAIT(ct->o_full[w], w ? o_ph1 : o_ph0, softmax_end);
+                    TEST_WAIT(ct->o_full[w], w ? o_ph1 : o_ph0, softmax_end);
                     o_ph0 ^= 1;
                     o_ph1 ^= 1;
                     if (nt > kFoldTiles && warp_on) L = l = fold_in(o_col, folded(), valid, ct->ml[w][row], m, l);
                 } else {
-                    SVQ_WAIT(ct->o_full[0], o_ph0, softmax_end);
+                    TEST_WAIT(ct->o_full[0], o_ph0, softmax_end);
                     o_ph0 ^= 1;
                     if (n > 1) {
-                        SVQ_WAIT(ct->o_full[1], o_ph1, softmax_end);
+                        TEST_WAIT(ct->o_full[1], o_ph1, softmax_end);
                         o_ph1 ^= 1;
                     }
                     if (nt > kFoldTiles && warp_on) l = fold_in(o_col, folded(), valid, ct->ml[w][row], m, l);
                     ct->ml[w][row] = make_float2(m, l);
                     mbar_arrive(smem_addr(&ct->join[0]));
-                    SVQ_WAIT(ct->join[0], join_ph, softmax_end);
+                    TEST_WAIT(ct->join[0], join_ph, softmax_end);
                     const float2 other = ct->ml[1 - w][row];
                     M = fmaxf(m, other.x);
                     const float mine = M == -INFINITY ? 0.f : ex2(m - M), theirs = M == -INFINITY ? 0.f : ex2(other.x - M);
@@ -727,7 +727,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 tc_fence_before();
                 if (!two) {
                     mbar_arrive(smem_addr(&ct->join[1]));
-                    SVQ_WAIT(ct->join[1], join_ph, softmax_end);
+                    TEST_WAIT(ct->join[1], join_ph, softmax_end);
                     join_ph ^= 1;
                 }
                 seg_done(k);

@@ -5,14 +5,15 @@
 // request times the heads are rows of one product, and a key tile's latents C (64
 // tokens x 512) are keys and values both.  With Q (rows x 576) and K = C beside the
 // rotary keys,
-//   S^T = K Q^T               (fp32 in TMEM: 64 tokens x rows, 36 MMAs of k = 16 channels)
-//   P^T = exp2(S^T * scale - base)   (bf16 in shared memory; base = a running maximum a row)
+//   S = Q K^T                 (fp32 in TMEM: 64 rows x 64 tokens, 36 MMAs of k = 16 channels)
+//   P = exp2(S * scale - base)   (bf16 in shared memory; base = a running maximum a row)
 //   O^T = O^T * 2^(old - new base) + C^T P^T   (fp32 in TMEM: 512 channels x rows,
 //                             4 MMAs of 128 channels for each 16 tokens)
-// The products are turned round, tokens and channels on the MMA's M side, rows on
-// its N side: O of 128 rows would take all of TMEM and Q of them 144 KB of shared
-// memory, while 64 rows leave room for two S and for a second key tile, and 16
-// rows of a single token need no padding to 128.
+// The second product is turned round, channels on the MMA's M side and rows on its
+// N side: O of 128 rows would take all of TMEM, O^T of 64 takes half of it, and 16
+// rows of a single token need no padding to 64.  The other half holds most of Q,
+// the first product's M side: from shared memory Q would take 72 KB and as much of
+// its bandwidth as K (a tile then moves 327 KB through it, 2555 cycles; 276 KB now).
 //
 // P is rounded to bf16 because one MMA takes both operands in one type and C is
 // bf16 (off by at most 2^-8 of each weight); over bf16 latents the average is taken
@@ -21,7 +22,7 @@
 //
 // e4m3 latents: codes are widened to bf16 tiles, exactly; a token's scale acts on
 // its logits and on its weights, and the rotary part of the logits is a product of
-// its own (N more columns).
+// its own (64 more columns).
 //
 // Work.  An entry is up to kShare x N rows of a request with the pages they see;
 // every group of kShare CTAs takes an equal run of the (entry, key tile) sequence.
@@ -31,7 +32,7 @@
 // Roles of a CTA (one per SM):
 //   warp 1       issues the MMAs
 //   warp 2       walks the plan
-//   warps 4-7    softmax (16 tokens each), outputs
+//   warps 4-7    softmax (16 rows each), outputs
 //   warps 8-11   load a page of the tile each: units of 64 tokens x 128 channels (16
 //                KB), each freed when its part of the second product is done, and
 //                rotary keys
@@ -53,6 +54,7 @@ constexpr int kTok = kPages * kPage;                // 64 tokens
 constexpr int kUnit = kTok * 128 * 2;               // bytes of 128 channels of a tile
 constexpr int kUnits = kLatentDim / 128;            // of a tile
 constexpr int kRopeBytes = kTok * kRopeDim * 2;
+constexpr int kBlockQ = 64 * 128;                   // bytes of 64 rows x 64 channels
 constexpr int kInfoSlots = 8;                       // tiles whose page faults and scales are kept
 constexpr int kMaxCtas = 160;                       // partial slots in the workspace
 constexpr float kSlack = 8.f;                       // log2 units a base may lag behind the maximum
@@ -64,9 +66,9 @@ constexpr int kMaxRows = 64;                        // rows of a CTA's tile at m
 
 template <int N, bool FP8>
 struct Cfg {
-    static constexpr int kRing = FP8 ? (N == 64 ? 6 : 7) : (N == 64 ? 8 : (N == 32 ? 10 : 11));   // units
-    static constexpr int kRope = N == 64 ? 2 : 3;                                                 // rotary tiles
-    static constexpr int kCodes = FP8 ? (N == 64 ? 3 : (N == 32 ? 4 : 8)) : 0;                    // units of codes, 8 KB
+    static constexpr int kRing = FP8 ? 8 : 11;                             // units: two tiles at least
+    static constexpr int kRope = FP8 || N == 64 ? 2 : 3;                   // rotary tiles
+    static constexpr int kCodes = FP8 ? (N == 64 ? 3 : 8) : 0;             // units of codes, 8 KB
     // Pairs of warps that widen a unit each, in turn.  (A pair sees every phase of the slots it reads: kCodes % kPairs is 0.)
     static constexpr int kPairs = N == 64 ? 3 : 4;
     static_assert(kCodes % kPairs == 0, "code slots");
@@ -75,13 +77,17 @@ struct Cfg {
     // = 640 x 96).
     static constexpr int kThreads = FP8 ? 640 : 384;
     static constexpr int kMmaRegs = FP8 ? 72 : 96, kSoftmaxRegs = FP8 ? 184 : 248, kLoadRegs = FP8 ? 64 : 96, kWidenRegs = 80;
-    static constexpr int kWiden = 8;                                                              // warps
-    static constexpr int kQ = N * kQueryDim * 2;
+    static constexpr int kWiden = 8;                                       // warps
+    // TMEM columns: O^T of channels 128 m .. at m N, then S (e4m3: its latent and its rotary part), then the first
+    // kQUnits units of Q's channels, two a column.  The others and the rotary ones are in shared memory.
+    static constexpr int kSCols = FP8 ? 2 * kTok : kTok;
+    static constexpr int kColS = 4 * N, kColQ = kColS + kSCols;
+    static constexpr int kQUnits = (512 - kColQ) / 64 < kUnits ? (512 - kColQ) / 64 : kUnits;
+    static constexpr int kQBlocks = 2 * (kUnits - kQUnits) + 1;            // of 64 rows x 64 channels
+    static constexpr int kQ = kQBlocks * kBlockQ;
     static constexpr int kP = N * kTok * 2;
     static constexpr int kScales = FP8 ? kInfoSlots * kTok * 4 : 0;
     static constexpr int kSmem = kRing * kUnit + kRope * kRopeBytes + kCodes * (kUnit / 2) + kQ + kP + kScales + kControlBytes;
-    static constexpr int kColS = 4 * N;                    // TMEM columns: O^T of channels 128 m .. at m N, then two S^T
-    static constexpr int kSCols = FP8 ? 2 * N : N;         // (latent | rotary)
     static_assert(kSmem <= 227 * 1024, "shared memory of one CTA");
 };
 
@@ -134,23 +140,30 @@ constexpr uint32_t kAIsMMajor = 1u << 15;
 
 #define LATENT_MMA_REGS "{\n\t.reg .pred acc, yes, go;\n\t.reg .b32 al, bl;\n\t.reg .b64 ad, bd;\n\t" \
     "setp.ne.u32 acc, %6, 0;\n\tsetp.ne.u32 go, %7, 0;\n\tsetp.eq.u32 yes, 0, 0;\n\t"
-// S^T (+)= K Q^T over a unit's 128 channels: 16 channels are 32 bytes further in the rows of both; the second 64 lie
-// 1 KB on (K) and a block of N rows on (Q: q_half in descriptor units).  By the whole warp, as the others.
-__device__ __forceinline__ void mma_qk8(uint32_t d, uint32_t k_lo, uint32_t q_lo, uint32_t q_half, uint32_t id, uint32_t acc, uint32_t go) {
+// S (+)= Q K^T over a unit's 128 channels, Q in TMEM or in shared memory: 16 channels are 8 columns of the one and 32
+// bytes further in the rows of the other two; the second 64 lie 1 KB on (K) and a block on (Q).  By the whole warp, as
+// the others.
+__device__ __forceinline__ void mma_qk8_tmem(uint32_t d, uint32_t q, uint32_t k_lo, uint32_t id, uint32_t acc, uint32_t go) {
+    asm volatile(
+        "{\n\t.reg .pred acc, yes, go;\n\t.reg .b32 al, bl;\n\t.reg .b64 bd;\n\t"
+        "setp.ne.u32 acc, %5, 0;\n\tsetp.ne.u32 go, %6, 0;\n\tsetp.eq.u32 yes, 0, 0;\n\t"
+        SVQ_MMA_TS_IF(0, 0, acc) SVQ_MMA_TS_IF(8, 2, yes) SVQ_MMA_TS_IF(16, 4, yes) SVQ_MMA_TS_IF(24, 6, yes)
+        SVQ_MMA_TS_IF(32, 64, yes) SVQ_MMA_TS_IF(40, 66, yes) SVQ_MMA_TS_IF(48, 68, yes) SVQ_MMA_TS_IF(56, 70, yes)
+        "}" ::"r"(d), "r"(q), "r"(k_lo), "r"(desc_hi(2048)), "r"(id), "r"(acc), "r"(go)
+        : "memory");
+}
+__device__ __forceinline__ void mma_qk8(uint32_t d, uint32_t q_lo, uint32_t k_lo, uint32_t id, uint32_t acc, uint32_t go) {
     asm volatile(LATENT_MMA_REGS
         SVQ_MMA_SS_IF(0, 0, acc) SVQ_MMA_SS_IF(2, 2, yes) SVQ_MMA_SS_IF(4, 4, yes) SVQ_MMA_SS_IF(6, 6, yes)
-        "}" ::"r"(d), "r"(k_lo), "r"(q_lo), "r"(desc_hi(2048)), "r"(desc_hi(1024)), "r"(id), "r"(acc), "r"(go)
-        : "memory");
-    asm volatile(LATENT_MMA_REGS
-        SVQ_MMA_SS_IF(64, 0, yes) SVQ_MMA_SS_IF(66, 2, yes) SVQ_MMA_SS_IF(68, 4, yes) SVQ_MMA_SS_IF(70, 6, yes)
-        "}" ::"r"(d), "r"(k_lo), "r"(q_lo + q_half), "r"(desc_hi(2048)), "r"(desc_hi(1024)), "r"(id), "r"(acc), "r"(go)
+        SVQ_MMA_SS_IF(512, 64, yes) SVQ_MMA_SS_IF(514, 66, yes) SVQ_MMA_SS_IF(516, 68, yes) SVQ_MMA_SS_IF(518, 70, yes)
+        "}" ::"r"(d), "r"(q_lo), "r"(k_lo), "r"(desc_hi(1024)), "r"(desc_hi(2048)), "r"(id), "r"(acc), "r"(go)
         : "memory");
 }
 // The rotary 64 channels.
-__device__ __forceinline__ void mma_rope4(uint32_t d, uint32_t k_lo, uint32_t q_lo, uint32_t id, uint32_t acc, uint32_t go) {
+__device__ __forceinline__ void mma_rope4(uint32_t d, uint32_t q_lo, uint32_t k_lo, uint32_t id, uint32_t acc, uint32_t go) {
     asm volatile(LATENT_MMA_REGS
         SVQ_MMA_SS_IF(0, 0, acc) SVQ_MMA_SS_IF(2, 2, yes) SVQ_MMA_SS_IF(4, 4, yes) SVQ_MMA_SS_IF(6, 6, yes)
-        "}" ::"r"(d), "r"(k_lo), "r"(q_lo), "r"(desc_hi(1024)), "r"(desc_hi(1024)), "r"(id), "r"(acc), "r"(go)
+        "}" ::"r"(d), "r"(q_lo), "r"(k_lo), "r"(desc_hi(1024)), "r"(desc_hi(1024)), "r"(id), "r"(acc), "r"(go)
         : "memory");
 }
 // O^T (+)= C^T P^T of 128 channels: a page (16 tokens) is 4 KB of the unit and 32 bytes of P's rows.
@@ -166,16 +179,22 @@ __device__ __forceinline__ void mma_pv1(uint32_t d, uint32_t c_lo, uint32_t p_lo
         "}" ::"r"(d), "r"(c_lo), "r"(p_lo), "r"(desc_hi(2048)), "r"(desc_hi(1024)), "r"(id), "r"(acc), "r"(go)
         : "memory");
 }
-// 16 lanes x 8 columns a repeat: lane l of the warp gets row l / 4 (and + 8), columns 2 (l % 4), + 1.
-__device__ __forceinline__ void tc_ld_frag(uint32_t addr, float (&r)[8]) {
-    uint32_t(&u)[8] = reinterpret_cast<uint32_t(&)[8]>(r);
-    asm volatile("tcgen05.ld.sync.aligned.16x256b.x2.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
-                 : "=r"(u[0]), "=r"(u[1]), "=r"(u[2]), "=r"(u[3]), "=r"(u[4]), "=r"(u[5]), "=r"(u[6]), "=r"(u[7])
-                 : "r"(addr));
+// 16 rows x 64 columns: lane l gets rows l / 4 and + 8 of columns 8 c + 2 (l % 4), + 1, at r[4 c ..] and r[4 c + 2 ..].
+__device__ __forceinline__ void tc_ld_rows(uint32_t addr, float (&x)[32]) {
+    uint32_t(&r)[32] = reinterpret_cast<uint32_t(&)[32]>(x);
+    asm volatile(
+        "tcgen05.ld.sync.aligned.16x256b.x8.b32 "
+        "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+        "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
+          "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+          "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+        : "r"(addr));
 }
-// Four 8 x 8 blocks of 16-bit values, turned round: lane l gives the address of row l % 8 of block l / 8.
-__device__ __forceinline__ void stmatrix_x4_trans(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
-    asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1,%2,%3,%4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d)
+// Four 8 x 8 blocks of 16-bit values: lane l gives the address of row l % 8 of block l / 8.
+__device__ __forceinline__ void stmatrix_x4(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+    asm volatile("stmatrix.sync.aligned.m8n8.x4.shared.b16 [%0], {%1,%2,%3,%4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d)
                  : "memory");
 }
 // Copies by a whole warp in step, of which the elected lane issues (go): from four lanes at once each takes 130 cycles.
@@ -208,7 +227,7 @@ __device__ __forceinline__ bool softmax_any(bool mine) {
 // The softmax warps meet at barriers, so they leave together: a warp whose wait ran out says so at the next one.
 #define LATENT_WAIT(bar, parity)                                                    \
     do {                                                                            \
-        if (__any_sync(0xffffffffu, !bar_wait(smem_addr(&(bar)), (parity)))) {      \
+        if (__any_sync(0xffffffffu, !bar_ready(smem_addr(&(bar)), (parity)))) {      \
             if (lane == 0) gave_up(ct);                                             \
             dead = true;                                                            \
         }                                                                           \
@@ -229,14 +248,13 @@ struct Control {
     uint64_t code_full[8], code_empty[8];
     uint64_t scale_full[kInfoSlots];
     uint64_t seg_full[kSegs], seg_empty[kSegs];
-    uint64_t s_full[2], p_full, pv_done, q_full, vote, drain;
+    uint64_t s_full, s_read, p_full, pv_done, q_full, vote, drain;
     uint32_t tmem;
     int gave_up;
     uint8_t fault[kInfoSlots][kPages];     // pages of a tile that the table does not give
     int over[4];                           // a logit of the tile is too far above its row's base
     Seg seg[kSegs];
-    float red[4][kMaxRows];                // maxima (and, at a segment's end, sums) of each softmax warp
-    float base[kMaxRows], alpha[kMaxRows];
+    float alpha[kMaxRows], factor[kMaxRows];   // of a row's O: where its base moves, and at a segment's end
 };
 static_assert(sizeof(Control) <= kControlBytes, "control block");
 
@@ -312,11 +330,11 @@ __global__ void __launch_bounds__(Cfg<N, FP8>::kThreads, 1)
             mbar_init(smem_addr(&ct->seg_full[i]), 1);
             mbar_init(smem_addr(&ct->seg_empty[i]), kPages + 1 + 4 + (FP8 ? C::kWiden : 0));   // loads, MMAs, softmax, widening
         }
-        mbar_init(smem_addr(&ct->s_full[0]), 1);
-        mbar_init(smem_addr(&ct->s_full[1]), 1);
+        mbar_init(smem_addr(&ct->s_full), 1);
+        mbar_init(smem_addr(&ct->s_read), 4);
         mbar_init(smem_addr(&ct->p_full), 4);
         mbar_init(smem_addr(&ct->pv_done), 1);
-        mbar_init(smem_addr(&ct->q_full), 1);
+        mbar_init(smem_addr(&ct->q_full), 5);   // the copy of its part in shared memory, and the softmax warps
         mbar_init(smem_addr(&ct->vote), 4);
         for (int i = 0; i < 4; ++i) ct->over[i] = 0;
         mbar_init(smem_addr(&ct->drain), 1);
@@ -349,89 +367,74 @@ __global__ void __launch_bounds__(Cfg<N, FP8>::kThreads, 1)
                 const uint32_t go = elected();
                 uint32_t tile = 0, segs = 0;   // tiles before the segment; segments with tiles
                 const uint32_t ring_s = smem_addr(ring), q_s = smem_addr(qs), p_lo = desc_lo(smem_addr(ps), 16);
-                constexpr uint32_t kBlockQ = N * 128;
                 auto wait = [&](uint64_t& bar, uint32_t parity) {
-                    const bool all = __all_sync(0xffffffffu, bar_wait(smem_addr(&bar), parity));
+                    const bool all = __all_sync(0xffffffffu, bar_ready(smem_addr(&bar), parity));
                     tc_fence_after();
                     return all;
                 };
                 auto commit = [&](uint64_t& bar) {
                     if (go) mma_commit(smem_addr(&bar));
                 };
-                // O^T of the tile whose P is ready: `pv_pages` pages of tile pv_tile, onto what there is if pv_acc.
-                bool pv_due = false, pv_acc = false;
-                uint32_t pv_tile = 0;
-                int pv_pages = 0;
-                auto pv = [&] {
-                    tc_fence_after();
-#pragma unroll 1
-                    for (int u = 0; u < kUnits; ++u) {
-                        const uint32_t st = (pv_tile * kUnits + u) % C::kRing;
-                        const uint32_t c_lo = desc_lo(ring_s + st * kUnit, 1024), d = tmem + u * N;
-                        if (pv_pages >= kPages) {
-                            mma_pv4(d, c_lo, p_lo, idesc(128, N) | kAIsMMajor, pv_acc, go);
-                        } else {
-                            for (int p = 0; p < pv_pages; ++p)
-                                mma_pv1(d, c_lo + p * 256, p_lo + p * 2, idesc(128, N) | kAIsMMajor, pv_acc || p != 0, go);
-                        }
-                        commit(ct->empty[st]);
-                    }
-                    commit(ct->pv_done);
-                    pv_due = false;
-                };
-                // S^T of tile t (counted over the CTA's work), unit after unit as they land, then the rotary part.  The
-                // product of the tile before goes in between as soon as its P is ready: it frees the memory that later
-                // units wait for.  One look asks for all of them, a barrier a lane: a look takes as long as five MMAs, and
-                // the tensor pipe queues only a few.
-                auto qk = [&](uint32_t t) {
-                    const uint32_t d = tmem + C::kColS + (t & 1) * C::kSCols;
-                    const uint32_t at = t * kUnits + lane, rt = t % C::kRope;
-                    const uint32_t bar = lane < kUnits ? smem_addr(&ct->full[at % C::kRing]) : (lane == kUnits ? smem_addr(&ct->rope_full[rt]) : smem_addr(&ct->p_full));
-                    const uint32_t parity = (lane < kUnits ? at / C::kRing : (lane == kUnits ? t / C::kRope : t - 1)) & 1;
-                    uint32_t tests = 0;
-                    for (int u = 0; u <= kUnits;) {
-                        const uint32_t done = __ballot_sync(0xffffffffu, lane <= kUnits + 1 && bar_test(bar, parity));
-                        if (pv_due && (done >> (kUnits + 1))) pv();
-                        if (!((done >> u) & 1u)) {
-                            if (++tests == kTests) return false;
-                            continue;
-                        }
-                        tc_fence_after();
-#pragma unroll 1
-                        for (; u < kUnits && ((done >> u) & 1u); ++u) {
-                            const uint32_t st = (t * kUnits + u) % C::kRing;
-                            mma_qk8(d, desc_lo(ring_s + st * kUnit, 16), desc_lo(q_s + 2 * u * kBlockQ, 16), kBlockQ >> 4, idesc(64, N), u != 0, go);
-                        }
-                        if (u == kUnits && ((done >> kUnits) & 1u)) {
-                            mma_rope4(FP8 ? d + N : d, desc_lo(smem_addr(ropes) + rt * kRopeBytes, 16), desc_lo(q_s + 8 * kBlockQ, 16),
-                                      idesc(64, N), !FP8, go);
-                            ++u;
-                        }
-                    }
-                    commit(ct->rope_empty[rt]);
-                    commit(ct->s_full[t & 1]);
-                    return true;
-                };
+                // S of tile t, then the product with P of the tile before: while the softmax works on one tile the tensor
+                // cores work on the next.  One copy of each in the code: the roles share the instruction caches, and with
+                // the product inlined at every wait a tile took 400 cycles longer.
+                uint32_t qk_slot = 0, qk_ph = 0, rope_slot = 0, rope_ph = 0, pv_slot = 0;
                 bool ok = true;
                 for (uint32_t k = 0; ok; ++k) {
                     ok = wait(ct->seg_full[k % kSegs], (k / kSegs) & 1);
                     const Seg& s = ct->seg[k % kSegs];
                     const int n = uniform(s.t1 - s.t0);
                     if (!ok || n == 0) break;
-                    int pages = uniform(s.en.npages - s.t0 * kPages);   // from the tile on
+                    int pages = uniform(s.en.npages - s.t0 * kPages);   // from the tile of the second product on
                     ok = wait(ct->q_full, segs & 1);
                     ++segs;
-                    if (!ok) break;
-                    ok = qk(tile);
-                    for (int i = 0; i < n && ok; ++i, pages -= kPages) {
-                        pv_due = true;
-                        pv_tile = tile + i;
-                        pv_pages = pages;
-                        pv_acc = (i & (kFoldTiles - 1)) != 0;
-                        if (i + 1 < n) ok = qk(tile + i + 1);
-                        if (ok && pv_due) {
-                            ok = wait(ct->p_full, pv_tile & 1);
-                            if (ok) pv();
+#pragma unroll 1
+                    for (int i = 0; i <= n && ok; ++i) {
+                        const uint32_t t = tile + i;
+                        if (i < n) {
+                            const uint32_t d = tmem + C::kColS;
+                            if (t > 0) ok = wait(ct->s_read, (t - 1) & 1);   // S of the tile before
+#pragma unroll 1
+                            for (int u = 0; u < kUnits && ok; ++u) {
+                                ok = wait(ct->full[qk_slot], qk_ph);
+                                if (!ok) break;
+                                const uint32_t k_lo = desc_lo(ring_s + qk_slot * kUnit, 16);
+                                if (u < C::kQUnits) mma_qk8_tmem(d, tmem + C::kColQ + u * 64, k_lo, idesc(64, kTok), u != 0, go);
+                                else mma_qk8(d, desc_lo(q_s + 2 * (u - C::kQUnits) * kBlockQ, 16), k_lo, idesc(64, kTok), u != 0, go);
+                                if (++qk_slot == C::kRing) {
+                                    qk_slot = 0;
+                                    qk_ph ^= 1;
+                                }
+                            }
+                            ok = ok && wait(ct->rope_full[rope_slot], rope_ph);
+                            if (!ok) break;
+                            mma_rope4(FP8 ? d + kTok : d, desc_lo(q_s + (C::kQBlocks - 1) * kBlockQ, 16),
+                                      desc_lo(smem_addr(ropes) + rope_slot * kRopeBytes, 16), idesc(64, kTok), !FP8, go);
+                            commit(ct->s_full);
+                            commit(ct->rope_empty[rope_slot]);
+                            if (++rope_slot == C::kRope) {
+                                rope_slot = 0;
+                                rope_ph ^= 1;
+                            }
+                        }
+                        if (i > 0) {
+                            ok = wait(ct->p_full, (t - 1) & 1);
+                            if (!ok) break;
+                            const bool acc = ((i - 1) & (kFoldTiles - 1)) != 0;
+#pragma unroll 1
+                            for (int u = 0; u < kUnits; ++u) {
+                                const uint32_t c_lo = desc_lo(ring_s + pv_slot * kUnit, 1024), d = tmem + u * N;
+                                if (pages >= kPages) {
+                                    mma_pv4(d, c_lo, p_lo, idesc(128, N) | kAIsMMajor, acc, go);
+                                } else {
+                                    for (int p = 0; p < pages; ++p)
+                                        mma_pv1(d, c_lo + p * 256, p_lo + p * 2, idesc(128, N) | kAIsMMajor, acc || p != 0, go);
+                                }
+                                commit(ct->empty[pv_slot]);
+                                pv_slot = pv_slot + 1 == C::kRing ? 0 : pv_slot + 1;
+                            }
+                            commit(ct->pv_done);
+                            pages -= kPages;
                         }
                     }
                     tile += n;
@@ -522,22 +525,39 @@ __global__ void __launch_bounds__(Cfg<N, FP8>::kThreads, 1)
             }
         plan_end:;
         } else if (warp >= 4 && warp < 8) {
-            // ---------------- softmax: warp w tokens 16 w .., lane l rows 8 c + 2 (l % 4), + 1 of tokens l / 4, + 8
+            // ---------------- softmax: warp w rows 16 w .., lane l rows l / 4 and + 8 of those, tokens 8 c + 2 (l % 4), + 1
             reg_inc<C::kSoftmaxRegs>();
             const int w = warp - 4, tid = threadIdx.x - 128;
-            const int quad = lane & 3, row8 = lane >> 2;
+            const int quad = lane & 3;
             const uint32_t lanes = static_cast<uint32_t>(w * 32) << 16;
-            constexpr int kGroups = N / 8;
             uint32_t tile = 0, q_loads = 0;
             bool dead = false;   // a wait of this warp's ran out
+            // Q of a segment's rows: the first units to TMEM, where row r is lane 32 (r / 16) + r % 16 (and 16 further, which
+            // no product reads), the rest to shared memory.
             auto load_q = [&](const Seg& g) {
                 if (tid == 0) {
                     const uint32_t bar = smem_addr(&ct->q_full);
                     mbar_arrive_expect_tx(bar, C::kQ);
                     ++q_loads;
 #pragma unroll 1
-                    for (int c = 0; c < kQueryDim / 64; ++c) tma_load_2d(smem_addr(qs) + c * (N * 128), &tmap_q, c * 64, g.en.row0, bar);
+                    for (int c = 0; c < C::kQBlocks; ++c)
+                        tma_load_2d(smem_addr(qs) + c * kBlockQ, &tmap_q, (2 * C::kQUnits + c) * 64, g.en.row0, bar);
                 }
+                if (16 * w < g.en.nrows) {
+                    const int r = min(16 * w + (lane & 15), g.en.nrows - 1);
+                    const uint4* const from = reinterpret_cast<const uint4*>(a.q + static_cast<int64_t>(g.en.row0 + r) * kQueryDim);
+#pragma unroll 1
+                    for (int c = 0; c < C::kQUnits * 64; c += 32) {   // columns, two channels each
+                        uint32_t x[32];
+#pragma unroll
+                        for (int u = 0; u < 8; ++u) *reinterpret_cast<uint4*>(&x[4 * u]) = from[c / 4 + u];
+                        tc_st32(tmem + lanes + C::kColQ + c, x);
+                    }
+                    tc_wait_st();
+                }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(smem_addr(&ct->q_full));
             };
             for (uint32_t k = 0;; ++k) {
                 const Seg& s = ct->seg[k % kSegs];
@@ -555,90 +575,110 @@ __global__ void __launch_bounds__(Cfg<N, FP8>::kThreads, 1)
                 // Tokens that a row sees.
                 auto see = [&](int r) { return s.en.posbase + (s.en.row0 + min(r, rows - 1)) / a.heads + 1; };
                 const int see_all = see(0), see_any = see(rows - 1);
-                float m = -INFINITY;                    // thread r < N: the base of row r
-                float base[2 * kGroups], l[2 * kGroups], lr[2 * kGroups];
-#pragma unroll
-                for (int c = 0; c < 2 * kGroups; ++c) base[c] = l[c] = lr[c] = 0.f;
-                float folded = -INFINITY;               // thread r < N: the base of what was folded
+                const int r0 = 16 * w + (lane >> 2), r1 = r0 + 8;
+                const int lim0 = see(r0), lim1 = see(r1);
+                const bool on = 16 * w < rows;          // (warps without rows have no logits, but their share of O)
+                float m0 = -INFINITY, m1 = -INFINITY;   // the rows' bases
+                float l0 = 0.f, l1 = 0.f, lr0 = 0.f, lr1 = 0.f;
+                float folded0 = -INFINITY, folded1 = -INFINITY;   // the bases of what was folded
                 float* const fold_to = a.cut_o + static_cast<int64_t>(s.slot >= 0 ? s.slot : 2 * static_cast<int>(blockIdx.x) + 1) * N * kLatentDim;
+                // The rows' factors, by the lane that has them first; all read them behind a barrier.
+                auto publish = [&](float* to, float f0, float f1) {
+                    if (quad == 0) {
+                        to[r0] = f0;
+                        to[r1] = f1;
+                    }
+                };
                 for (int j = 0; j < n; ++j, ++tile) {
                     const int first = (s.t0 + j) * kTok;
                     const int slot = tile % kInfoSlots;
-                    LATENT_WAIT(ct->s_full[tile & 1], (tile >> 1) & 1);
+                    LATENT_WAIT(ct->s_full, tile & 1);
                     tc_fence_after();
-                    if (j == n - 1 && nx.t1 > nx.t0) load_q(nx);   // the segment's last use of Q is over
-                    const uint32_t s_col = tmem + lanes + C::kColS + (tile & 1) * C::kSCols;
-                    float x[4 * kGroups];
-#pragma unroll
-                    for (int c = 0; c < kGroups / 2; ++c) tc_ld_frag(s_col + c * 16, reinterpret_cast<float(&)[8]>(x[c * 8]));
-                    tc_wait_ld();
-                    const int tok0 = first + 16 * w + row8, tok1 = tok0 + 8;
                     const uint32_t fault = *reinterpret_cast<const uint32_t*>(ct->fault[slot]);
-                    const bool gone = (fault >> (8 * w)) & 1u;     // the warp's tokens are one page
-                    float sc0 = 1.f, sc1 = 1.f;
-                    if (FP8) {
-                        LATENT_WAIT(ct->scale_full[slot], (tile / kInfoSlots) & 1);
-                        // (Scales of tokens that no row sees may hold anything.)
-                        sc0 = tok0 < see_any && !gone ? scales[slot * kTok + 16 * w + row8] : 0.f;
-                        sc1 = tok1 < see_any && !gone ? scales[slot * kTok + 16 * w + row8 + 8] : 0.f;
-#pragma unroll
-                        for (int c = 0; c < kGroups / 2; ++c) {
-                            float y[8];
-                            tc_ld_frag(s_col + N + c * 16, y);
+                    float x[32];
+                    if (on) {
+                        tc_ld_rows(tmem + lanes + C::kColS, x);
+                        tc_wait_ld();
+                        if (FP8) {
+                            float y[32];
+                            tc_ld_rows(tmem + lanes + C::kColS + kTok, y);
                             tc_wait_ld();
+                            LATENT_WAIT(ct->scale_full[slot], (tile / kInfoSlots) & 1);
 #pragma unroll
-                            for (int g = 0; g < 2; ++g) {
-                                float* const z = &x[c * 8 + 4 * g];
-                                z[0] = fmaf(z[0], sc0, y[4 * g]);
-                                z[1] = fmaf(z[1], sc0, y[4 * g + 1]);
-                                z[2] = fmaf(z[2], sc1, y[4 * g + 2]);
-                                z[3] = fmaf(z[3], sc1, y[4 * g + 3]);
+                            for (int c = 0; c < 8; ++c) {
+                                const float2 sc = *reinterpret_cast<const float2*>(&scales[slot * kTok + 8 * c + 2 * quad]);
+                                x[4 * c] = fmaf(x[4 * c], sc.x, y[4 * c]);
+                                x[4 * c + 1] = fmaf(x[4 * c + 1], sc.y, y[4 * c + 1]);
+                                x[4 * c + 2] = fmaf(x[4 * c + 2], sc.x, y[4 * c + 2]);
+                                x[4 * c + 3] = fmaf(x[4 * c + 3], sc.y, y[4 * c + 3]);
                             }
                         }
                     }
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(smem_addr(&ct->s_read));
                     const bool plain = first + kTok <= see_all && !fault;
-                    if (!plain) {
+                    if (on && !plain) {
 #pragma unroll
-                        for (int c = 0; c < kGroups; ++c)
+                        for (int c = 0; c < 8; ++c) {
+                            const bool gone = (fault >> (c / 2 * 8)) & 1u;
 #pragma unroll
                             for (int u = 0; u < 2; ++u) {
-                                const int lim = gone ? 0 : see(8 * c + 2 * quad + u);
-                                if (tok0 >= lim) x[4 * c + u] = -INFINITY;
-                                if (tok1 >= lim) x[4 * c + 2 + u] = -INFINITY;
+                                const int tok = first + 8 * c + 2 * quad + u;
+                                if (gone || tok >= lim0) x[4 * c + u] = -INFINITY;
+                                if (gone || tok >= lim1) x[4 * c + 2 + u] = -INFINITY;
                             }
+                        }
                     }
                     // Weights go by the rows' bases as they are, unless a logit is more than kSlack above its row's: then
                     // (at a run's first tile, and seldom behind it) the tile's maxima move the bases.  The warps say so to
-                    // one another while they work out the weights.  Columns without a row have an infinite base.
-                    uint32_t p[kGroups][2];
-                    float add[2 * kGroups], add_r[2 * kGroups];
-                    float over = -INFINITY;
+                    // one another while they work out the weights, as each holds channels of all rows' O.
+                    uint32_t p[8][2];
+                    float add0, add1, add_r0, add_r1, over = -INFINITY;
                     auto weights = [&] {
+                        const float b0 = m0 == -INFINITY ? 0.f : m0, b1 = m1 == -INFINITY ? 0.f : m1;
+                        const uint64_t scale2 = pack2(a.scale_log2, a.scale_log2), base0 = pack2(-b0, -b0), base1 = pack2(-b1, -b1);
+                        uint64_t sum0 = 0ull, sum1 = 0ull, sumr0 = 0ull, sumr1 = 0ull;
 #pragma unroll
-                        for (int c = 0; c < kGroups; ++c) {
-                            const uint64_t scale2 = pack2(a.scale_log2, a.scale_log2), base2 = pack2(-base[2 * c], -base[2 * c + 1]);
+                        for (int c = 0; c < 8; ++c) {
                             float y[4];
-                            unpack2(fma2(pack2(x[4 * c], x[4 * c + 1]), scale2, base2), y[0], y[1]);
-                            unpack2(fma2(pack2(x[4 * c + 2], x[4 * c + 3]), scale2, base2), y[2], y[3]);
+                            unpack2(fma2(pack2(x[4 * c], x[4 * c + 1]), scale2, base0), y[0], y[1]);
+                            unpack2(fma2(pack2(x[4 * c + 2], x[4 * c + 3]), scale2, base1), y[2], y[3]);
                             over = fmaxf(over, fmaxf(fmaxf(y[0], y[1]), fmaxf(y[2], y[3])));
                             uint64_t e0 = pack2(ex2(y[0]), ex2(y[1])), e1 = pack2(ex2(y[2]), ex2(y[3]));
-                            unpack2(add2(e0, e1), add[2 * c], add[2 * c + 1]);
+                            sum0 = add2(sum0, e0);
+                            sum1 = add2(sum1, e1);
                             if (FP8) {
-                                e0 = mul2(e0, pack2(sc0, sc0));
-                                e1 = mul2(e1, pack2(sc1, sc1));
+                                // (Scales of tokens that no row sees may hold anything.)
+                                const float2 sc = *reinterpret_cast<const float2*>(&scales[slot * kTok + 8 * c + 2 * quad]);
+                                const int tok = first + 8 * c + 2 * quad;
+                                const bool gone = (fault >> (c / 2 * 8)) & 1u;
+                                const uint64_t s2 = plain ? pack2(sc.x, sc.y)
+                                                          : pack2(gone || tok >= see_any ? 0.f : sc.x, gone || tok + 1 >= see_any ? 0.f : sc.y);
+                                e0 = mul2(e0, s2);
+                                e1 = mul2(e1, s2);
                             }
                             unpack2(e0, y[0], y[1]);
                             unpack2(e1, y[2], y[3]);
                             p[c][0] = pack_bf16x2(y[0], y[1]);
                             p[c][1] = pack_bf16x2(y[2], y[3]);
                             if (!FP8) {
-                                add_r[2 * c] = bf16lo(p[c][0]) + bf16lo(p[c][1]);
-                                add_r[2 * c + 1] = bf16hi(p[c][0]) + bf16hi(p[c][1]);
+                                sumr0 = add2(sumr0, pack2(bf16lo(p[c][0]), bf16hi(p[c][0])));
+                                sumr1 = add2(sumr1, pack2(bf16lo(p[c][1]), bf16hi(p[c][1])));
                             }
                         }
+                        float u, v;
+                        unpack2(sum0, u, v);
+                        add0 = u + v;
+                        unpack2(sum1, u, v);
+                        add1 = u + v;
+                        unpack2(sumr0, u, v);
+                        add_r0 = u + v;
+                        unpack2(sumr1, u, v);
+                        add_r1 = u + v;
                     };
                     if (j > 0) {
-                        weights();
+                        if (on) weights();
                         if (dead || over > kSlack) *static_cast<volatile int*>(&ct->over[tile & 3]) = 1;
                     } else if (lane == 0) {
                         *static_cast<volatile int*>(&ct->over[tile & 3]) = 1;
@@ -647,8 +687,8 @@ __global__ void __launch_bounds__(Cfg<N, FP8>::kThreads, 1)
                     if (lane == 0) mbar_arrive(smem_addr(&ct->vote));
                     // (P's memory and O are free when the product before is done: the same look asks for that.)
                     {
-                        const bool first = lane == 0 || j == 0;
-                        const uint32_t bar = first ? smem_addr(&ct->vote) : smem_addr(&ct->pv_done), parity = (first ? tile : tile - 1) & 1;
+                        const bool vote = lane == 0 || j == 0;
+                        const uint32_t bar = vote ? smem_addr(&ct->vote) : smem_addr(&ct->pv_done), parity = (vote ? tile : tile - 1) & 1;
                         if (!__all_sync(0xffffffffu, bar_test(bar, parity)) && __any_sync(0xffffffffu, !bar_wait(bar, parity))) {
                             if (lane == 0) gave_up(ct);
                             dead = true;
@@ -659,46 +699,32 @@ __global__ void __launch_bounds__(Cfg<N, FP8>::kThreads, 1)
                     if (tid == 0) *static_cast<volatile int*>(&ct->over[(tile + 2) & 3]) = 0;
                     if (any) {
                         if (softmax_any(dead)) goto softmax_end;
-                        float mx[2 * kGroups];
+                        float top0 = -INFINITY, top1 = -INFINITY;
+                        if (on) {
 #pragma unroll
-                        for (int c = 0; c < kGroups; ++c) {
-                            mx[2 * c] = fmaxf(x[4 * c], x[4 * c + 2]);
-                            mx[2 * c + 1] = fmaxf(x[4 * c + 1], x[4 * c + 3]);
-                        }
-#pragma unroll
-                        for (int c = 0; c < 2 * kGroups; ++c) {
-                            mx[c] = fmaxf(mx[c], __shfl_xor_sync(0xffffffffu, mx[c], 4));
-                            mx[c] = fmaxf(mx[c], __shfl_xor_sync(0xffffffffu, mx[c], 8));
-                            mx[c] = fmaxf(mx[c], __shfl_xor_sync(0xffffffffu, mx[c], 16));
-                        }
-                        if (row8 == 0) {
-#pragma unroll
-                            for (int c = 0; c < kGroups; ++c)
-                                *reinterpret_cast<float2*>(&ct->red[w][8 * c + 2 * quad]) = make_float2(mx[2 * c], mx[2 * c + 1]);
-                        }
-                        softmax_sync();
-                        if (tid < N) {
-                            const float top = fmaxf(fmaxf(ct->red[0][tid], ct->red[1][tid]), fmaxf(ct->red[2][tid], ct->red[3][tid])) * a.scale_log2;
-                            float alpha = 1.f;
-                            if (tid < rows && top > m) {
-                                alpha = m == -INFINITY ? 0.f : ex2(m - top);   // (nothing was added yet)
-                                m = top;
+                            for (int c = 0; c < 8; ++c) {
+                                top0 = fmaxf(top0, fmaxf(x[4 * c], x[4 * c + 1]));
+                                top1 = fmaxf(top1, fmaxf(x[4 * c + 2], x[4 * c + 3]));
                             }
-                            ct->base[tid] = tid >= rows ? INFINITY : (m == -INFINITY ? 0.f : m);   // (0: a row that has seen nothing yet)
-                            ct->alpha[tid] = alpha;
                         }
-                        softmax_sync();
-                    }
-                    if (any) {
 #pragma unroll
-                        for (int c = 0; c < 2 * kGroups; ++c) {
-                            const int r = 8 * (c >> 1) + 2 * quad + (c & 1);
-                            base[c] = ct->base[r];
-                            l[c] *= ct->alpha[r];
-                            lr[c] *= ct->alpha[r];
+                        for (int d = 1; d < 4; d <<= 1) {
+                            top0 = fmaxf(top0, __shfl_xor_sync(0xffffffffu, top0, d));
+                            top1 = fmaxf(top1, __shfl_xor_sync(0xffffffffu, top1, d));
                         }
+                        const float n0 = fmaxf(m0, top0 * a.scale_log2), n1 = fmaxf(m1, top1 * a.scale_log2);
+                        // (A row that has seen nothing yet has added nothing.)
+                        const float alpha0 = m0 == -INFINITY ? 0.f : ex2(m0 - n0), alpha1 = m1 == -INFINITY ? 0.f : ex2(m1 - n1);
+                        m0 = n0;
+                        m1 = n1;
+                        l0 *= alpha0;
+                        lr0 *= alpha0;
+                        l1 *= alpha1;
+                        lr1 *= alpha1;
                         if (j > 0) {
+                            publish(ct->alpha, alpha0, alpha1);
                             tc_fence_after();
+                            softmax_sync();
 #pragma unroll 1
                             for (int c = 0; c < 4 * N; c += 16) {
                                 uint32_t y[16];
@@ -710,16 +736,14 @@ __global__ void __launch_bounds__(Cfg<N, FP8>::kThreads, 1)
                             }
                             tc_wait_st();
                         }
-                        weights();
+                        if (on) weights();
                     }
                     if (j > 0 && (j & (kFoldTiles - 1)) == 0) {
                         // O moves to the fp32 sums: thread's channel 128 u + tid, row after row.
                         tc_fence_after();
-                        softmax_sync();   // (alpha has been read)
-                        if (tid < N) {
-                            ct->alpha[tid] = folded == -INFINITY ? 0.f : ex2(folded - m);
-                            folded = m;
-                        }
+                        publish(ct->factor, folded0 == -INFINITY ? 0.f : ex2(folded0 - m0), folded1 == -INFINITY ? 0.f : ex2(folded1 - m1));
+                        folded0 = m0;
+                        folded1 = m1;
                         softmax_sync();
 #pragma unroll 1
                         for (int c = 0; c < 4 * N; c += 16) {
@@ -731,18 +755,19 @@ __global__ void __launch_bounds__(Cfg<N, FP8>::kThreads, 1)
                                 const int r = (c + u) % N;
                                 if (r < rows) {
                                     float* const at = fold_to + r * kLatentDim + (c + u) / N * 128 + tid;
-                                    *at = j > kFoldTiles ? fmaf(*at, ct->alpha[r], __uint_as_float(y[u])) : __uint_as_float(y[u]);
+                                    *at = j > kFoldTiles ? fmaf(*at, ct->factor[r], __uint_as_float(y[u])) : __uint_as_float(y[u]);
                                 }
                             }
                         }
-                        softmax_sync();   // (alpha is written again)
+                        softmax_sync();   // (the factors are written again)
                     }
-                    // P^T, a row of 64 tokens each: blocks of tokens 16 w .. + 7 and + 8 .. + 15 of rows 8 c ..,
-                    // then of rows 8 (c + 1) ..
+                    // P, a row of 64 tokens each: blocks of 8 rows x 8 tokens.
+                    if (on) {
 #pragma unroll
-                    for (int c = 0; c < kGroups; c += 2) {
-                        const int r = 8 * (c + (lane >> 4)) + (lane & 7), chunk = 2 * w + ((lane >> 3) & 1);
-                        stmatrix_x4_trans(smem_addr(ps) + r * 128 + ((chunk ^ (r & 7)) << 4), p[c][0], p[c][1], p[c + 1][0], p[c + 1][1]);
+                        for (int c = 0; c < 8; c += 2) {
+                            const int r = 16 * w + (lane & 15), chunk = c + (lane >> 4);
+                            stmatrix_x4(smem_addr(ps) + r * 128 + ((chunk ^ (r & 7)) << 4), p[c][0], p[c][1], p[c + 1][0], p[c + 1][1]);
+                        }
                     }
                     // Tokens that no row sees may hold anything: their channels become zeros (P = 0 must not meet a
                     // NaN) in the pages that the product reads.
@@ -759,50 +784,42 @@ __global__ void __launch_bounds__(Cfg<N, FP8>::kThreads, 1)
                     tc_fence_before();
                     __syncwarp();
                     if (lane == 0) mbar_arrive(smem_addr(&ct->p_full));
-#pragma unroll
-                    for (int c = 0; c < 2 * kGroups; ++c) {
-                        l[c] += add[c];
-                        if (!FP8) lr[c] += add_r[c];
+                    if (on) {
+                        l0 += add0;
+                        l1 += add1;
+                        lr0 += add_r0;
+                        lr1 += add_r1;
                     }
                 }
+                if (nx.t1 > nx.t0) load_q(nx);   // the segment's last use of Q is over
 
                 // ---------------- the segment's end
-                // The rows' sums: over the lanes of a row, then over the warps.
 #pragma unroll
-                for (int c = 0; c < 2 * kGroups; ++c) {
-#pragma unroll
-                    for (int d = 4; d < 32; d <<= 1) {
-                        l[c] += __shfl_xor_sync(0xffffffffu, l[c], d);
-                        lr[c] += __shfl_xor_sync(0xffffffffu, lr[c], d);
-                    }
+                for (int d = 1; d < 4; d <<= 1) {
+                    l0 += __shfl_xor_sync(0xffffffffu, l0, d);
+                    l1 += __shfl_xor_sync(0xffffffffu, l1, d);
+                    lr0 += __shfl_xor_sync(0xffffffffu, lr0, d);
+                    lr1 += __shfl_xor_sync(0xffffffffu, lr1, d);
                 }
-                float L = 0.f, R = 0.f;   // thread r < N: those of row r
-#pragma unroll
-                for (int pass = 0; pass < 2; ++pass) {
-                    softmax_sync();
-                    if (row8 == 0) {
-#pragma unroll
-                        for (int c = 0; c < kGroups; ++c)
-                            *reinterpret_cast<float2*>(&ct->red[w][8 * c + 2 * quad]) =
-                                pass ? make_float2(lr[2 * c], lr[2 * c + 1]) : make_float2(l[2 * c], l[2 * c + 1]);
-                    }
-                    softmax_sync();
-                    if (tid < N) {
-                        const float sum = ct->red[0][tid] + ct->red[1][tid] + (ct->red[2][tid] + ct->red[3][tid]);
-                        (pass ? R : L) = sum;
-                    }
+                if (FP8) {
+                    lr0 = l0;
+                    lr1 = l1;
                 }
-                if (FP8) R = L;
-                LATENT_WAIT(ct->pv_done, (tile - 1) & 1);
-                tc_fence_after();
                 const bool whole = s.slot < 0;
-                if (tid < N) {
-                    // A row that sees nothing is 0, whatever the others see.
-                    ct->base[tid] = whole ? (R > 0.f ? 1.f / R : R) : 1.f;
-                    ct->alpha[tid] = folded == -INFINITY ? 0.f : ex2(folded - m);
-                    if (tid < rows) {
-                        if (whole) a.lse[s.en.row0 + tid] = L > 0.f ? (m + log2f(L)) * 0.69314718055994531f : (L == 0.f ? -INFINITY : L);
-                        else a.cut_ml[static_cast<int64_t>(s.slot) * N + tid] = make_float4(m, L, R, 0.f);
+                LATENT_WAIT(ct->pv_done, (tile - 1) & 1);   // (all warps have read the factors of their last tile, too)
+                tc_fence_after();
+                // A row that sees nothing is 0, whatever the others see.
+                if (on) {
+                    publish(ct->factor, whole ? (lr0 > 0.f ? 1.f / lr0 : lr0) : 1.f, whole ? (lr1 > 0.f ? 1.f / lr1 : lr1) : 1.f);
+                    publish(ct->alpha, folded0 == -INFINITY ? 0.f : ex2(folded0 - m0), folded1 == -INFINITY ? 0.f : ex2(folded1 - m1));
+                    if (quad == 0) {
+                        auto result = [&](int r, float m, float l, float lr) {
+                            if (r >= rows) return;
+                            if (whole) a.lse[s.en.row0 + r] = l > 0.f ? (m + log2f(l)) * 0.69314718055994531f : (l == 0.f ? -INFINITY : l);
+                            else a.cut_ml[static_cast<int64_t>(s.slot) * N + r] = make_float4(m, l, lr, 0.f);
+                        };
+                        result(r0, m0, l0, lr0);
+                        result(r1, m1, l1, lr1);
                     }
                 }
                 softmax_sync();
@@ -819,7 +836,7 @@ __global__ void __launch_bounds__(Cfg<N, FP8>::kThreads, 1)
                         const int channel = (c + u) / N * 128 + tid;
                         float v = __uint_as_float(y[u]);
                         if (n > kFoldTiles) v = fmaf(fold_to[r * kLatentDim + channel], ct->alpha[r], v);
-                        const float f = ct->base[r];
+                        const float f = ct->factor[r];
                         v = f == 0.f ? 0.f : v * f;
                         if (whole) {
                             odd = fmaf(v, 0.f, odd);
@@ -852,7 +869,7 @@ __global__ void __launch_bounds__(Cfg<N, FP8>::kThreads, 1)
             const uint32_t to = smem_addr(FP8 ? codes : ring) + p * kPageBytes;
             const uint32_t rope_to = smem_addr(ropes) + p * (kPage * kRopeDim * 2);
             for (uint32_t k = 0;; ++k) {
-                SVQ_WAIT(ct->seg_full[k % kSegs], (k / kSegs) & 1, loads_end);
+                TEST_WAIT(ct->seg_full[k % kSegs], (k / kSegs) & 1, loads_end);
                 const Seg& s = ct->seg[k % kSegs];
                 const int t0 = uniform(s.t0), n = uniform(s.t1) - t0;
                 if (n == 0) break;
@@ -893,7 +910,7 @@ __global__ void __launch_bounds__(Cfg<N, FP8>::kThreads, 1)
 #pragma unroll
                     for (int u = 0; u < kUnits; ++u) {
                         const uint32_t at = tile * kUnits + u, st = at % kDepth;
-                        SVQ_WAIT(empty[st], ((at / kDepth) & 1) ^ 1, loads_end);
+                        TEST_WAIT(empty[st], ((at / kDepth) & 1) ^ 1, loads_end);
                         const uint32_t bar = smem_addr(&full[st]), dst = to + st * (kPageBytes * kPages);
                         if (go) {
                             if (ph >= 0) mbar_arrive_expect_tx(bar, kPageBytes);
@@ -905,7 +922,7 @@ __global__ void __launch_bounds__(Cfg<N, FP8>::kThreads, 1)
                         loaded = at + 1;
                     }
                     const uint32_t st = tile % C::kRope;
-                    SVQ_WAIT(ct->rope_empty[st], ((tile / C::kRope) & 1) ^ 1, loads_end);
+                    TEST_WAIT(ct->rope_empty[st], ((tile / C::kRope) & 1) ^ 1, loads_end);
                     const uint32_t bar = smem_addr(&ct->rope_full[st]);
                     if (go) {
                         if (ph >= 0) mbar_arrive_expect_tx(bar, kPage * kRopeDim * 2);
@@ -932,14 +949,14 @@ __global__ void __launch_bounds__(Cfg<N, FP8>::kThreads, 1)
             uint32_t at = mine, until = 0;
             constexpr uint32_t kDepth = FP8 ? C::kCodes : 1;
             for (uint32_t k = 0;; ++k) {
-                SVQ_WAIT(ct->seg_full[k % kSegs], (k / kSegs) & 1, widen_end);
+                TEST_WAIT(ct->seg_full[k % kSegs], (k / kSegs) & 1, widen_end);
                 const Seg& s = ct->seg[k % kSegs];
                 const int n = s.t1 - s.t0;
                 if (n == 0) break;
                 until += n * kUnits;
                 for (; mine < C::kPairs && at < until; at += C::kPairs) {
                     const uint32_t cs = at % kDepth, st = at % C::kRing;
-                    SVQ_WAIT(ct->code_full[cs], (at / kDepth) & 1, widen_end);
+                    TEST_WAIT(ct->code_full[cs], (at / kDepth) & 1, widen_end);
                     // 16 codes at chunk tid / 8 of rows tid % 8, + 8, ...: eight lanes read, and write, eight rows' bytes in
                     // different banks.  The fence keeps the next copy into the slot behind these reads.
                     const int r = tid & 7, c = tid >> 3;
@@ -950,7 +967,7 @@ __global__ void __launch_bounds__(Cfg<N, FP8>::kThreads, 1)
                     fence_proxy_async_smem();
                     __syncwarp();
                     if (lane == 0) mbar_arrive(smem_addr(&ct->code_empty[cs]));
-                    SVQ_WAIT(ct->empty[st], ((at / C::kRing) & 1) ^ 1, widen_end);
+                    TEST_WAIT(ct->empty[st], ((at / C::kRing) & 1) ^ 1, widen_end);
                     unsigned char* const o = ring + st * kUnit + (c >> 2) * 1024 + r * 128;
                     const int at0 = ((2 * c) & 7 ^ r) << 4, at1 = ((2 * c + 1) & 7 ^ r) << 4;
 #pragma unroll
@@ -1367,7 +1384,7 @@ int launch_latent_attention(const sv_cache* c, const void* q, int num_q_heads, c
     a.odd = reinterpret_cast<uint32_t*>(ws + lay.odd);
     a.num_odd = reinterpret_cast<int*>(ws + lay.num_odd);
     CUtensorMap tq, tc, tr;
-    if (!encode_rows(&tq, q, kQueryDim, static_cast<int64_t>(total_q) * num_q_heads, lay.tile_rows) ||
+    if (!encode_rows(&tq, q, kQueryDim, static_cast<int64_t>(total_q) * num_q_heads, 64) ||
         !encode_latents(&tc, c->k_pool, c->num_phys_pages, a.fp8) ||
         !encode_rows(&tr, c->v_pool, kRopeDim, c->num_phys_pages * kPage, kPage))
         return SV_ERR_CUDA;
