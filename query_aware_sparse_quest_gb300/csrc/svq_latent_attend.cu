@@ -66,8 +66,8 @@ constexpr int kMaxRows = 64;                        // rows of a CTA's tile at m
 
 template <int N, bool FP8>
 struct Cfg {
-    static constexpr int kRing = FP8 ? 8 : 11;                             // units: two tiles at least
-    static constexpr int kRope = FP8 || N == 64 ? 2 : 3;                   // rotary tiles
+    static constexpr int kRing = FP8 ? 8 : (N == 64 ? 11 : 12);            // units: two tiles at least
+    static constexpr int kRope = 2;                                        // rotary tiles
     static constexpr int kCodes = FP8 ? (N == 64 ? 3 : 8) : 0;             // units of codes, 8 KB
     // Pairs of warps that widen a unit each, in turn.  (A pair sees every phase of the slots it reads: kCodes % kPairs is 0.)
     static constexpr int kPairs = N == 64 ? 3 : 4;
@@ -243,8 +243,8 @@ struct __align__(16) Seg {
 constexpr int kSegs = 4;
 
 struct Control {
-    uint64_t full[11], empty[11];          // units
-    uint64_t rope_full[3], rope_empty[3];
+    uint64_t full[12], empty[12];          // units
+    uint64_t rope_full[2], rope_empty[2];
     uint64_t code_full[8], code_empty[8];
     uint64_t scale_full[kInfoSlots];
     uint64_t seg_full[kSegs], seg_empty[kSegs];
@@ -361,89 +361,103 @@ __global__ void __launch_bounds__(Cfg<N, FP8>::kThreads, 1)
 
     {
         if (warp == 1) {
-            // ---------------- MMAs: the whole warp, in step
+            // ---------------- MMAs: the whole warp, in step.  The tensor pipe queues next to nothing, so whatever the warp
+            // does between two MMAs is lost: a tile is waited for once, its MMAs follow one another, and there is one
+            // copy of each product in the code (the roles share the instruction caches).
             reg_dec<C::kMmaRegs>();
-            {
-                const uint32_t go = elected();
-                uint32_t tile = 0, segs = 0;   // tiles before the segment; segments with tiles
-                const uint32_t ring_s = smem_addr(ring), q_s = smem_addr(qs), p_lo = desc_lo(smem_addr(ps), 16);
-                auto wait = [&](uint64_t& bar, uint32_t parity) {
-                    const bool all = __all_sync(0xffffffffu, bar_ready(smem_addr(&bar), parity));
-                    tc_fence_after();
-                    return all;
-                };
-                auto commit = [&](uint64_t& bar) {
-                    if (go) mma_commit(smem_addr(&bar));
-                };
+            const uint32_t go = elected();
+            uint32_t tile = 0, segs = 0;   // tiles before the segment; segments with tiles
+            const uint32_t ring_s = smem_addr(ring), q_s = smem_addr(qs), p_lo = desc_lo(smem_addr(ps), 16);
+            auto wait = [&](uint64_t& bar, uint32_t parity) { return __all_sync(0xffffffffu, bar_ready(smem_addr(&bar), parity)) != 0; };
+            auto test = [&](uint64_t& bar, uint32_t parity) { return __all_sync(0xffffffffu, bar_test(smem_addr(&bar), parity)) != 0; };
+            auto commit = [&](uint64_t& bar) {
+                if (go) mma_commit(smem_addr(&bar));
+            };
+            uint32_t qk_slot = 0, qk_ph = 0, pv_slot = 0, rope = 0, rope_ph = 0;   // places in the rings, and their phases
+            auto next = [](uint32_t slot, uint32_t by) { return slot + by >= C::kRing ? slot + by - C::kRing : slot + by; };
+            bool ok = true;
+            for (uint32_t k = 0; ok; ++k) {
+                ok = wait(ct->seg_full[k % kSegs], (k / kSegs) & 1);
+                const Seg& s = ct->seg[k % kSegs];
+                const int n = uniform(s.t1 - s.t0);
+                if (!ok || n == 0) break;
+                int pages = uniform(s.en.npages - s.t0 * kPages);   // from the tile of the second product on
+                ok = wait(ct->q_full, segs & 1);
+                ++segs;
                 // S of tile t, then the product with P of the tile before: while the softmax works on one tile the tensor
-                // cores work on the next.  One copy of each in the code: the roles share the instruction caches, and with
-                // the product inlined at every wait a tile took 400 cycles longer.
-                uint32_t qk_slot = 0, qk_ph = 0, rope_slot = 0, rope_ph = 0, pv_slot = 0;
-                bool ok = true;
-                for (uint32_t k = 0; ok; ++k) {
-                    ok = wait(ct->seg_full[k % kSegs], (k / kSegs) & 1);
-                    const Seg& s = ct->seg[k % kSegs];
-                    const int n = uniform(s.t1 - s.t0);
-                    if (!ok || n == 0) break;
-                    int pages = uniform(s.en.npages - s.t0 * kPages);   // from the tile of the second product on
-                    ok = wait(ct->q_full, segs & 1);
-                    ++segs;
+                // cores work on the next.  What the one needs is asked for between the MMAs of the other, which the
+                // queue covers (`seen`: a unit each, the rotary keys, S of the tile before read; and P).
+                uint32_t seen = 0;
+                bool p_seen = false;
 #pragma unroll 1
-                    for (int i = 0; i <= n && ok; ++i) {
-                        const uint32_t t = tile + i;
-                        if (i < n) {
-                            const uint32_t d = tmem + C::kColS;
-                            if (t > 0) ok = wait(ct->s_read, (t - 1) & 1);   // S of the tile before
-#pragma unroll 1
-                            for (int u = 0; u < kUnits && ok; ++u) {
-                                ok = wait(ct->full[qk_slot], qk_ph);
-                                if (!ok) break;
-                                const uint32_t k_lo = desc_lo(ring_s + qk_slot * kUnit, 16);
-                                if (u < C::kQUnits) mma_qk8_tmem(d, tmem + C::kColQ + u * 64, k_lo, idesc(64, kTok), u != 0, go);
-                                else mma_qk8(d, desc_lo(q_s + 2 * (u - C::kQUnits) * kBlockQ, 16), k_lo, idesc(64, kTok), u != 0, go);
-                                if (++qk_slot == C::kRing) {
-                                    qk_slot = 0;
-                                    qk_ph ^= 1;
-                                }
-                            }
-                            ok = ok && wait(ct->rope_full[rope_slot], rope_ph);
+                for (int i = 0; i <= n && ok; ++i) {
+                    const uint32_t t = tile + i;
+                    if (i < n) {
+                        const uint32_t d = tmem + C::kColS;
+                        if (t > 0 && !((seen >> (kUnits + 1)) & 1u)) ok = wait(ct->s_read, (t - 1) & 1);
+#pragma unroll
+                        for (int u = 0; u < kUnits; ++u) {
+                            const uint32_t slot = next(qk_slot, u);
+                            if (!((seen >> u) & 1u)) ok = ok && wait(ct->full[slot], qk_ph ^ (slot < qk_slot));
                             if (!ok) break;
-                            mma_rope4(FP8 ? d + kTok : d, desc_lo(q_s + (C::kQBlocks - 1) * kBlockQ, 16),
-                                      desc_lo(smem_addr(ropes) + rope_slot * kRopeBytes, 16), idesc(64, kTok), !FP8, go);
-                            commit(ct->s_full);
-                            commit(ct->rope_empty[rope_slot]);
-                            if (++rope_slot == C::kRope) {
-                                rope_slot = 0;
-                                rope_ph ^= 1;
-                            }
+                            if (u == 0 || !((seen >> u) & 1u)) tc_fence_after();
+                            const uint32_t k_lo = desc_lo(ring_s + slot * kUnit, 16);
+                            if (u < C::kQUnits) mma_qk8_tmem(d, tmem + C::kColQ + u * 64, k_lo, idesc(64, kTok), u != 0, go);
+                            else mma_qk8(d, desc_lo(q_s + 2 * (u - C::kQUnits) * kBlockQ, 16), k_lo, idesc(64, kTok), u != 0, go);
                         }
-                        if (i > 0) {
-                            ok = wait(ct->p_full, (t - 1) & 1);
-                            if (!ok) break;
-                            const bool acc = ((i - 1) & (kFoldTiles - 1)) != 0;
+                        if (ok && !((seen >> kUnits) & 1u)) ok = wait(ct->rope_full[rope], rope_ph);
+                        if (!ok) break;
+                        tc_fence_after();
+                        mma_rope4(FP8 ? d + kTok : d, desc_lo(q_s + (C::kQBlocks - 1) * kBlockQ, 16),
+                                  desc_lo(smem_addr(ropes) + rope * kRopeBytes, 16), idesc(64, kTok), !FP8, go);
+                        p_seen = i > 0 && test(ct->p_full, (t - 1) & 1);
+                        commit(ct->s_full);
+                        commit(ct->rope_empty[rope]);
+                        qk_ph ^= qk_slot + kUnits >= C::kRing;
+                        qk_slot = next(qk_slot, kUnits);
+                        rope_ph ^= rope + 1 == C::kRope;
+                        rope = rope + 1 == C::kRope ? 0 : rope + 1;
+                    }
+                    seen = 0;
+                    if (i > 0) {
+                        if (!p_seen || i == n) ok = wait(ct->p_full, (t - 1) & 1);
+                        if (!ok) break;
+                        tc_fence_after();
+                        const bool acc = ((i - 1) & (kFoldTiles - 1)) != 0;
+                        if (pages >= kPages) {
+#pragma unroll
+                            for (int u = 0; u < kUnits; ++u) {
+                                const uint32_t slot = next(pv_slot, u);
+                                mma_pv4(tmem + u * N, desc_lo(ring_s + slot * kUnit, 1024), p_lo, idesc(128, N) | kAIsMMajor, acc, go);
+                                if (u == kUnits - 1) {
+                                    seen |= test(ct->rope_full[rope], rope_ph) ? 1u << kUnits : 0u;
+                                    seen |= test(ct->s_read, t & 1) ? 2u << kUnits : 0u;
+                                } else {
+                                    const uint32_t ahead = next(qk_slot, u);
+                                    seen |= test(ct->full[ahead], qk_ph ^ (ahead < qk_slot)) ? 1u << u : 0u;
+                                }
+                                commit(ct->empty[slot]);
+                            }
+                        } else {
 #pragma unroll 1
                             for (int u = 0; u < kUnits; ++u) {
-                                const uint32_t c_lo = desc_lo(ring_s + pv_slot * kUnit, 1024), d = tmem + u * N;
-                                if (pages >= kPages) {
-                                    mma_pv4(d, c_lo, p_lo, idesc(128, N) | kAIsMMajor, acc, go);
-                                } else {
-                                    for (int p = 0; p < pages; ++p)
-                                        mma_pv1(d, c_lo + p * 256, p_lo + p * 2, idesc(128, N) | kAIsMMajor, acc || p != 0, go);
-                                }
-                                commit(ct->empty[pv_slot]);
-                                pv_slot = pv_slot + 1 == C::kRing ? 0 : pv_slot + 1;
+                                const uint32_t slot = next(pv_slot, u), c_lo = desc_lo(ring_s + slot * kUnit, 1024);
+                                for (int p = 0; p < pages; ++p)
+                                    mma_pv1(tmem + u * N, c_lo + p * 256, p_lo + p * 2, idesc(128, N) | kAIsMMajor, acc || p != 0, go);
+                                commit(ct->empty[slot]);
                             }
-                            commit(ct->pv_done);
-                            pages -= kPages;
                         }
+                        commit(ct->pv_done);
+                        pv_slot = next(pv_slot, kUnits);
+                        pages -= kPages;
                     }
-                    tile += n;
-                    if (ok && go) mbar_arrive(smem_addr(&ct->seg_empty[k % kSegs]));
                 }
-                if (!ok && go) gave_up(ct);
-                commit(ct->drain);   // nothing of this CTA's is in flight when TMEM is freed
-                (void)wait(ct->drain, 0);
+                tile += n;
+                if (ok && go) mbar_arrive(smem_addr(&ct->seg_empty[k % kSegs]));
             }
+            if (!ok && go) gave_up(ct);
+            commit(ct->drain);   // nothing of this CTA's is in flight when TMEM is freed
+            (void)wait(ct->drain, 0);
             __syncwarp();
         } else if (warp == 2) {
             // ---------------- the group's share of the plan, segment by segment
@@ -863,9 +877,8 @@ __global__ void __launch_bounds__(Cfg<N, FP8>::kThreads, 1)
             const int p = warp - 8;
             uint32_t tile = 0, loaded = 0;
             constexpr uint32_t kDepth = FP8 ? (C::kCodes ? C::kCodes : 1) : C::kRing;
-            constexpr uint32_t kPageBytes = kPage * (FP8 ? 128 : 256);
+            constexpr uint32_t kPageBytes = kPage * (FP8 ? 128 : 256);   // of a unit
             uint64_t* const empty = FP8 ? ct->code_empty : ct->empty;
-            uint64_t* const full = FP8 ? ct->code_full : ct->full;
             const uint32_t to = smem_addr(FP8 ? codes : ring) + p * kPageBytes;
             const uint32_t rope_to = smem_addr(ropes) + p * (kPage * kRopeDim * 2);
             for (uint32_t k = 0;; ++k) {
@@ -911,14 +924,14 @@ __global__ void __launch_bounds__(Cfg<N, FP8>::kThreads, 1)
                     for (int u = 0; u < kUnits; ++u) {
                         const uint32_t at = tile * kUnits + u, st = at % kDepth;
                         TEST_WAIT(empty[st], ((at / kDepth) & 1) ^ 1, loads_end);
-                        const uint32_t bar = smem_addr(&full[st]), dst = to + st * (kPageBytes * kPages);
+                        const uint32_t bar = smem_addr(FP8 ? &ct->code_full[st] : &ct->full[st]);
                         if (go) {
                             if (ph >= 0) mbar_arrive_expect_tx(bar, kPageBytes);
                             else mbar_arrive(bar);
                         }
                         __syncwarp();
-                        if (FP8) tma_2d_if(on, dst, &tmap_c, u * 128, ph * kPage, bar);
-                        else tma_page_if(on, dst, &tmap_c, 2 * u, 2 * ph, bar);
+                        if (FP8) tma_2d_if(on, to + st * (kPageBytes * kPages), &tmap_c, u * 128, ph * kPage, bar);
+                        else tma_page_if(on, to + st * (kPageBytes * kPages), &tmap_c, 2 * u, 2 * ph, bar);
                         loaded = at + 1;
                     }
                     const uint32_t st = tile % C::kRope;
@@ -937,7 +950,7 @@ __global__ void __launch_bounds__(Cfg<N, FP8>::kThreads, 1)
         loads_end:
             // Gave up: the copies still in flight land before the CTA (and its shared memory) retires.
             for (uint32_t x = loaded > kDepth ? loaded - kDepth : 0; x < loaded; ++x)
-                (void)bar_wait(smem_addr(&full[x % kDepth]), (x / kDepth) & 1);
+                (void)bar_wait(smem_addr(FP8 ? &ct->code_full[x % kDepth] : &ct->full[x % kDepth]), (x / kDepth) & 1);
             for (uint32_t x = tile > C::kRope ? tile - C::kRope : 0; x < tile; ++x)
                 (void)bar_wait(smem_addr(&ct->rope_full[x % C::kRope]), (x / C::kRope) & 1);
             if (FP8) (void)bar_wait(smem_addr(&ct->scale_full[tile % kInfoSlots]), (tile / kInfoSlots) & 1);
