@@ -549,16 +549,18 @@ class LatentCache:
 def _strided(t: torch.Tensor, shape, name: str, dev: int):
     """The address and the element strides of all dimensions but the last, which is contiguous.  A dimension of one (or
     of none) has no stride to speak of: it gets that of a packed tensor."""
-    _shape(t, shape, name)
+    if t.shape != shape:
+        _shape(t, shape, name)
     if t.get_device() != dev or t.dtype is not _BF16:
         _at(t.reshape(-1)[:0], _BF16, name, dev)
-    if t.numel() and t.stride(-1) != 1:
+    strides = t.stride()
+    if strides[-1] != 1 and t.numel():
         raise ValueError(f"{name} must be contiguous in its last dimension")
-    strides, packed = [], shape[-1]
-    for n, s in zip(reversed(shape[:-1]), reversed(t.stride()[:-1])):
-        strides.append(s if n > 1 else packed)
-        packed *= max(n, 1)
-    return (t.data_ptr(), *reversed(strides))
+    if len(shape) == 2:
+        return t.data_ptr(), strides[0] if shape[0] > 1 else shape[1]
+    n, h, d = shape
+    inner = strides[1] if h > 1 else d
+    return t.data_ptr(), strides[0] if n > 1 else max(h, 1) * d, inner
 
 
 def sv_latent_append(cache: LatentCache, latent: torch.Tensor, rope: torch.Tensor, slot_mapping: torch.Tensor,

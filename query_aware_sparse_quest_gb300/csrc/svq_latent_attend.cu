@@ -122,6 +122,8 @@ struct LatentArgs {
     // Plan
     Entry* entries;
     int64_t* cum;        // [E + 1] cost of the entries before each
+    int64_t* total;      // of all
+    bool planned;        // by a kernel before; else single tokens of few requests, which every CTA goes through itself
     int* num_entries;
     int* req_first;      // [batch]
     int max_entries;
@@ -241,6 +243,9 @@ struct __align__(16) Seg {
     int pad;
 };
 constexpr int kSegs = 4;
+// Single tokens of at most so many requests: an entry is a request, and every CTA sums up their costs by itself (a plan
+// kernel before takes 3 us; one request of 4096 tokens 25.5 -> 22 us).
+constexpr int kOwnPlan = 256;
 
 struct Control {
     uint64_t full[12], empty[12];          // units
@@ -253,6 +258,7 @@ struct Control {
     int gave_up;
     uint8_t fault[kInfoSlots][kPages];     // pages of a tile that the table does not give
     int over[4];                           // a logit of the tile is too far above its row's base
+    int lens[kOwnPlan];                       // of the requests, where the CTA plans by itself
     Seg seg[kSegs];
     float alpha[kMaxRows], factor[kMaxRows];   // of a row's O: where its base moves, and at a segment's end
 };
@@ -462,8 +468,33 @@ __global__ void __launch_bounds__(Cfg<N, FP8>::kThreads, 1)
         } else if (warp == 2) {
             // ---------------- the group's share of the plan, segment by segment
             reg_dec<C::kMmaRegs>();
-            const int num_entries = *a.num_entries;
-            const int64_t total = a.cum[num_entries];
+            int num_entries;
+            int64_t total = 0;
+            auto own_cost = [&](int b) { return cost_of_entry((ct->lens[b] + kTok - 1) / kTok); };
+            if (a.planned) {
+                num_entries = *a.num_entries;
+                total = *a.total;
+            } else {
+                num_entries = a.batch;
+                for (int b0 = 0; b0 < a.batch; b0 += 32) {
+                    const int b = b0 + lane;
+                    int64_t cost = 0;
+                    if (b < a.batch) {
+                        int len = a.seq_lens[b];
+                        if (len < 0 || (static_cast<int64_t>(len) + kPage - 1) / kPage > a.max_pages) {
+                            if (blockIdx.x == 0) svq_flag(SV_DEVERR_SEQ_LEN);
+                            len = 0;
+                        }
+                        ct->lens[b] = len;
+                        cost = own_cost(b);
+                    }
+#pragma unroll
+                    for (int d = 16; d; d >>= 1) cost += __shfl_xor_sync(0xffffffffu, cost, d);
+                    total += cost;
+                }
+                if (blockIdx.x == 0 && lane == 0) *a.total = total;   // for the join
+                __syncwarp();
+            }
             const int groups = groups_of(total, gridDim.x / a.share);
             const Share share(total, groups);
             const int64_t first = group < groups ? share.start(group) : total;
@@ -471,9 +502,40 @@ __global__ void __launch_bounds__(Cfg<N, FP8>::kThreads, 1)
             int e = 0;
             int64_t off = 0;                 // into the entry's cost
             if (left > 0) {
-                e = warp_find_le(a.cum, num_entries, first);
-                off = first - a.cum[e];
+                if (a.planned) {
+                    e = warp_find_le(a.cum, num_entries, first);
+                    off = first - a.cum[e];
+                } else {
+                    int64_t before = 0;
+                    for (int b0 = 0;; b0 += 32) {
+                        const int b = b0 + lane;
+                        const int64_t cost = b < a.batch ? own_cost(b) : 0;
+                        int64_t x = cost;
+#pragma unroll
+                        for (int d = 1; d < 32; d <<= 1) {
+                            const int64_t y = __shfl_up_sync(0xffffffffu, x, d);
+                            if (lane >= d) x += y;
+                        }
+                        const uint32_t here = __ballot_sync(0xffffffffu, before + x > first);
+                        if (here) {
+                            const int src = __ffs(here) - 1;
+                            e = b0 + src;
+                            off = first - __shfl_sync(0xffffffffu, before + x - cost, src);
+                            break;
+                        }
+                        before += __shfl_sync(0xffffffffu, x, 31);
+                    }
+                }
             }
+            auto entry = [&](int e) {
+                if (a.planned) {
+                    const int4* p = reinterpret_cast<const int4*>(a.entries + e);
+                    const int4 x = p[0], y = p[1];
+                    return Entry{x.x, x.y, x.z, x.w, y.x, y.y, {0, 0}};
+                }
+                const int pages = (ct->lens[e] + kPage - 1) / kPage;
+                return Entry{e * a.heads, a.heads, ct->lens[e] - e - 1, e, pages, (pages + kPages - 1) / kPages, {0, 0}};
+            };
             const bool go_on = off > 0;      // the share begins inside an entry
             if (left <= 0 && lane == 0 && part == 0) a.cut_item[2 * group] = make_int4(0, 0, 0, 0);
             bool first_item = true;
@@ -482,11 +544,8 @@ __global__ void __launch_bounds__(Cfg<N, FP8>::kThreads, 1)
                 int t0 = 0, t1 = 0;
                 if (left > 0) {
                     if (off == 0 || first_item) {
-                        do {   // (entries without tiles: rows that see nothing)
-                            const int4* p = reinterpret_cast<const int4*>(a.entries + e);
-                            const int4 x = p[0], y = p[1];
-                            en = Entry{x.x, x.y, x.z, x.w, y.x, y.y, {0, 0}};
-                        } while (en.tiles == 0 && ++e < num_entries);
+                        do en = entry(e);   // (entries without tiles: rows that see nothing)
+                        while (en.tiles == 0 && ++e < num_entries);
                     }
                     if (first_item && lane == 0 && part == 0) {
                         // The group after the one with an entry's first tile names the entry for the join.
@@ -537,7 +596,15 @@ __global__ void __launch_bounds__(Cfg<N, FP8>::kThreads, 1)
                     ++e;
                 }
             }
-        plan_end:;
+        plan_end:
+            // Requests without tokens: a group takes those at its distance.
+            for (int b = group; !a.planned && part == 0 && b < a.batch; b += gridDim.x / a.share) {
+                if (ct->lens[b]) continue;
+                const int64_t r0 = static_cast<int64_t>(b) * a.heads;
+                uint4* const o = reinterpret_cast<uint4*>(a.out + r0 * kLatentDim);
+                for (int i = lane; i < a.heads * (kLatentDim / 8); i += 32) o[i] = make_uint4(0u, 0u, 0u, 0u);
+                for (int i = lane; i < a.heads; i += 32) a.lse[r0 + i] = -INFINITY;
+            }
         } else if (warp >= 4 && warp < 8) {
             // ---------------- softmax: warp w rows 16 w .., lane l rows l / 4 and + 8 of those, tokens 8 c + 2 (l % 4), + 1
             reg_inc<C::kSoftmaxRegs>();
@@ -1094,6 +1161,7 @@ __global__ void __launch_bounds__(kPlanThreads) latent_plan_kernel(const __grid_
     }
     if (tid == 0) {
         a.cum[n] = base;
+        *a.total = base;
         *a.num_entries = n;
         *a.num_odd = 0;
     }
@@ -1217,11 +1285,10 @@ __global__ void __launch_bounds__(kJoinThreads) latent_join_kernel(const __grid_
     const int tid = threadIdx.x, warp = tid >> 5;
     pdl_wait();
     const int N = a.tile_rows;
-    const int64_t total = a.cum[*a.num_entries];
-    const int groups = groups_of(total, gridDim.x + 1);
+    const int groups = groups_of(*a.total, gridDim.x + 1);
     const int c = blockIdx.x + 1;
     const int4 what = c < groups ? a.cut_item[2 * c] : make_int4(0, 0, 0, 0);
-    const int num_odd = *a.num_odd;
+    const int num_odd = a.planned ? *a.num_odd : 0;   // (rows of one token see the same)
     const int pieces = what.z;
     const int4 where = pieces ? a.cut_item[2 * c + 1] : what;
     for (int r = blockIdx.y; pieces && r < what.y; r += gridDim.y) {
@@ -1271,7 +1338,7 @@ __global__ void __launch_bounds__(kJoinThreads) latent_join_kernel(const __grid_
         *reinterpret_cast<uint2*>(a.out + static_cast<int64_t>(row) * kLatentDim + 4 * tid) = v;
         if (tid == 0) a.lse[row] = l > 0.f ? (m + log2f(l)) * 0.69314718055994531f : (l == 0.f ? -INFINITY : l);
         const float odd = fmaf(o.x, 0.f, fmaf(o.y, 0.f, fmaf(o.z, 0.f, o.w * 0.f)));
-        if (__syncthreads_or(odd != 0.f && l > 0.f && l < INFINITY) && warp == 0) look_at_row(a, what.w, row);
+        if (a.planned && __syncthreads_or(odd != 0.f && l > 0.f && l < INFINITY) && warp == 0) look_at_row(a, what.w, row);
     }
     for (int64_t i = blockIdx.y * gridDim.x + blockIdx.x; i < static_cast<int64_t>(num_odd) * (N / 4); i += gridDim.x * gridDim.y) {
         const uint32_t id = a.odd[i / (N / 4)];
@@ -1285,7 +1352,7 @@ __global__ void __launch_bounds__(kJoinThreads) latent_join_kernel(const __grid_
 size_t up(size_t n) { return (n + 255) / 256 * 256; }
 
 struct Layout {
-    size_t entries, cum, num, req_first, cut_item, cut_o, cut_ml, odd, num_odd, total;
+    size_t entries, cum, num, all, req_first, cut_item, cut_o, cut_ml, odd, num_odd, total;
     int tile_rows, share, max_entries;
     Layout(int64_t batch, int64_t total_q, int heads) {
         // Rows of a CTA: as many as a request has at the most if each has one query token, else 64; two CTAs side by
@@ -1300,6 +1367,7 @@ struct Layout {
         entries = take(e * sizeof(Entry));
         cum = take((e + 1) * sizeof(int64_t));
         num = take(sizeof(int));
+        all = take(sizeof(int64_t));
         req_first = take(batch * sizeof(int));
         cut_item = take(2 * kMaxCtas * sizeof(int4));
         cut_o = take(2ull * kMaxCtas * tile_rows * kLatentDim * sizeof(float));
@@ -1389,6 +1457,8 @@ int launch_latent_attention(const sv_cache* c, const void* q, int num_q_heads, c
     a.entries = reinterpret_cast<Entry*>(ws + lay.entries);
     a.cum = reinterpret_cast<int64_t*>(ws + lay.cum);
     a.num_entries = reinterpret_cast<int*>(ws + lay.num);
+    a.total = reinterpret_cast<int64_t*>(ws + lay.all);
+    a.planned = q_start || batch > kOwnPlan;
     a.req_first = reinterpret_cast<int*>(ws + lay.req_first);
     a.max_entries = lay.max_entries;
     a.cut_o = reinterpret_cast<float*>(ws + lay.cut_o);
@@ -1401,7 +1471,7 @@ int launch_latent_attention(const sv_cache* c, const void* q, int num_q_heads, c
         !encode_latents(&tc, c->k_pool, c->num_phys_pages, a.fp8) ||
         !encode_rows(&tr, c->v_pool, kRopeDim, c->num_phys_pages * kPage, kPage))
         return SV_ERR_CUDA;
-    if (launch_pdl(latent_plan_kernel, dim3(1), dim3(kPlanThreads), 0, stream, a) != cudaSuccess) return SV_ERR_CUDA;
+    if (a.planned && launch_pdl(latent_plan_kernel, dim3(1), dim3(kPlanThreads), 0, stream, a) != cudaSuccess) return SV_ERR_CUDA;
     const int groups = (sm_count < kMaxCtas ? sm_count : kMaxCtas) / lay.share;
     const int ctas = groups * lay.share;
     int st;
