@@ -260,7 +260,7 @@ struct Control {
     int over[4];                           // a logit of the tile is too far above its row's base
     int lens[kOwnPlan];                       // of the requests, where the CTA plans by itself
     Seg seg[kSegs];
-    float alpha[kMaxRows], factor[kMaxRows];   // of a row's O: where its base moves, and at a segment's end
+    alignas(16) float alpha[kMaxRows], factor[kMaxRows];   // of a row's O: where its base moves, and at a segment's end
 };
 static_assert(sizeof(Control) <= kControlBytes, "control block");
 
@@ -627,12 +627,18 @@ __global__ void __launch_bounds__(Cfg<N, FP8>::kThreads, 1)
                 if (16 * w < g.en.nrows) {
                     const int r = min(16 * w + (lane & 15), g.en.nrows - 1);
                     const uint4* const from = reinterpret_cast<const uint4*>(a.q + static_cast<int64_t>(g.en.row0 + r) * kQueryDim);
+                    constexpr int kBatch = FP8 || N == 64 ? 2 : 4;   // groups of 32 columns (two channels each) on their way at a time
+                    constexpr int kGroups = C::kQUnits * 2;
 #pragma unroll 1
-                    for (int c = 0; c < C::kQUnits * 64; c += 32) {   // columns, two channels each
-                        uint32_t x[32];
+                    for (int c0 = 0; c0 < kGroups; c0 += kBatch) {
+                        uint32_t x[kBatch][32];
 #pragma unroll
-                        for (int u = 0; u < 8; ++u) *reinterpret_cast<uint4*>(&x[4 * u]) = from[c / 4 + u];
-                        tc_st32(tmem + lanes + C::kColQ + c, x);
+                        for (int c = 0; c < kBatch; ++c)
+#pragma unroll
+                            for (int u = 0; u < 8 && c0 + c < kGroups; ++u) *reinterpret_cast<uint4*>(&x[c][4 * u]) = from[(c0 + c) * 8 + u];
+#pragma unroll
+                        for (int c = 0; c < kBatch; ++c)
+                            if (c0 + c < kGroups) tc_st32(tmem + lanes + C::kColQ + (c0 + c) * 32, x[c]);
                     }
                     tc_wait_st();
                 }
@@ -905,26 +911,40 @@ __global__ void __launch_bounds__(Cfg<N, FP8>::kThreads, 1)
                 }
                 softmax_sync();
                 float odd = 0.f;   // NaN once a channel of a row that sees something is not finite
+                const bool fold = n > kFoldTiles;
 #pragma unroll 1
-                for (int c = 0; c < 4 * N; c += 16) {
+                for (int c = 0; c < 4 * N; c += 16) {   // channel 128 (c / N) + tid of 16 rows
                     uint32_t y[16];
                     tc_ld16(tmem + lanes + c, y);
-                    tc_wait_ld();
+                    const int first_row = c % N, channel = c / N * 128 + tid, left = rows - first_row;
+                    float f[16];
 #pragma unroll
-                    for (int u = 0; u < 16; ++u) {
-                        const int r = (c + u) % N;
-                        if (r >= rows) continue;
-                        const int channel = (c + u) / N * 128 + tid;
-                        float v = __uint_as_float(y[u]);
-                        if (n > kFoldTiles) v = fmaf(fold_to[r * kLatentDim + channel], ct->alpha[r], v);
-                        const float f = ct->factor[r];
-                        v = f == 0.f ? 0.f : v * f;
-                        if (whole) {
-                            odd = fmaf(v, 0.f, odd);
-                            a.out[static_cast<int64_t>(s.en.row0 + r) * kLatentDim + channel] = __float2bfloat16_rn(v);
-                        } else {
-                            a.cut_o[(static_cast<int64_t>(s.slot) * N + r) * kLatentDim + channel] = v;
-                        }
+                    for (int u = 0; u < 16; u += 4) *reinterpret_cast<float4*>(&f[u]) = *reinterpret_cast<const float4*>(&ct->factor[first_row + u]);
+                    tc_wait_ld();
+                    if (fold) {
+                        const float* const from = fold_to + first_row * kLatentDim + channel;
+#pragma unroll
+                        for (int u = 0; u < 16; ++u)
+                            if (u < left) y[u] = __float_as_uint(fmaf(from[u * kLatentDim], ct->alpha[first_row + u], __uint_as_float(y[u])));
+                    }
+                    if (!whole) {
+                        float* const to = a.cut_o + (static_cast<int64_t>(s.slot) * N + first_row) * kLatentDim + channel;
+#pragma unroll
+                        for (int u = 0; u < 16; ++u)
+                            if (u < left) to[u * kLatentDim] = __uint_as_float(y[u]);
+                        continue;
+                    }
+                    // Pairs of lanes change values, so that each has two channels of one of two rows.
+                    const bool high = tid & 1;
+                    __nv_bfloat16* const to = a.out + static_cast<int64_t>(s.en.row0 + first_row + high) * kLatentDim + (channel & ~1);
+#pragma unroll
+                    for (int u = 0; u < 16; u += 2) {
+                        const float v0 = f[u] == 0.f || u >= left ? 0.f : __uint_as_float(y[u]) * f[u];
+                        const float v1 = f[u + 1] == 0.f || u + 1 >= left ? 0.f : __uint_as_float(y[u + 1]) * f[u + 1];
+                        odd = fmaf(v0, 0.f, fmaf(v1, 0.f, odd));
+                        const float other = __shfl_xor_sync(0xffffffffu, high ? v0 : v1, 1);
+                        if (u + high < left)
+                            *reinterpret_cast<uint32_t*>(to + u * kLatentDim) = high ? pack_bf16x2(other, v1) : pack_bf16x2(v0, other);
                     }
                 }
                 // (Rows of one token see the same.)
