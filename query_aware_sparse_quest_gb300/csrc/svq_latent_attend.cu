@@ -57,7 +57,9 @@ constexpr int kRopeBytes = kTok * kRopeDim * 2;
 constexpr int kBlockQ = 64 * 128;                   // bytes of 64 rows x 64 channels
 constexpr int kInfoSlots = 8;                       // tiles whose page faults and scales are kept
 constexpr int kMaxCtas = 160;                       // partial slots in the workspace
+constexpr int kQueryTop = 10;                       // e4m3: the exponent that a row of Q is scaled to for fp16
 constexpr float kSlack = 8.f;                       // log2 units a base may lag behind the maximum
+constexpr float kBig = 256.f;                       // e4m3: weights times scales, in O's unit, that its unit moves at (fp16 ends at 65504)
 // Key tiles after which O moves into fp32 sums and starts again from zero: the MMAs cut their sums off at fp32's last
 // bit, four times a tile, always towards zero (values of one sign lose 2^-21.4 of their sum a tile).
 constexpr int kFoldTiles = 1024;
@@ -137,7 +139,10 @@ struct LatentArgs {
 
 // ---------------------------------------------------------------- tensor cores
 constexpr uint32_t kF32FromBf16 = (1u << 4) | (1u << 7) | (1u << 10);
-constexpr uint32_t idesc(int m, int n) { return kF32FromBf16 | (static_cast<uint32_t>(n / 8) << 17) | (static_cast<uint32_t>(m / 16) << 24); }
+constexpr uint32_t kF32FromF16 = 1u << 4;
+// (types: of the latents, which e4m3 codes are widened to, and of what is multiplied with them)
+template <bool FP8>
+constexpr uint32_t idesc(int m, int n) { return (FP8 ? kF32FromF16 : kF32FromBf16) | (static_cast<uint32_t>(n / 8) << 17) | (static_cast<uint32_t>(m / 16) << 24); }
 constexpr uint32_t kAIsMMajor = 1u << 15;
 
 #define LATENT_MMA_REGS "{\n\t.reg .pred acc, yes, go;\n\t.reg .b32 al, bl;\n\t.reg .b64 ad, bd;\n\t" \
@@ -408,14 +413,14 @@ __global__ void __launch_bounds__(Cfg<N, FP8>::kThreads, 1)
                             if (!ok) break;
                             if (u == 0 || !((seen >> u) & 1u)) tc_fence_after();
                             const uint32_t k_lo = desc_lo(ring_s + slot * kUnit, 16);
-                            if (u < C::kQUnits) mma_qk8_tmem(d, tmem + C::kColQ + u * 64, k_lo, idesc(64, kTok), u != 0, go);
-                            else mma_qk8(d, desc_lo(q_s + 2 * (u - C::kQUnits) * kBlockQ, 16), k_lo, idesc(64, kTok), u != 0, go);
+                            if (u < C::kQUnits) mma_qk8_tmem(d, tmem + C::kColQ + u * 64, k_lo, idesc<FP8>(64, kTok), u != 0, go);
+                            else mma_qk8(d, desc_lo(q_s + 2 * (u - C::kQUnits) * kBlockQ, 16), k_lo, idesc<FP8>(64, kTok), u != 0, go);
                         }
                         if (ok && !((seen >> kUnits) & 1u)) ok = wait(ct->rope_full[rope], rope_ph);
                         if (!ok) break;
                         tc_fence_after();
                         mma_rope4(FP8 ? d + kTok : d, desc_lo(q_s + (C::kQBlocks - 1) * kBlockQ, 16),
-                                  desc_lo(smem_addr(ropes) + rope * kRopeBytes, 16), idesc(64, kTok), !FP8, go);
+                                  desc_lo(smem_addr(ropes) + rope * kRopeBytes, 16), idesc<false>(64, kTok), !FP8, go);
                         p_seen = i > 0 && test(ct->p_full, (t - 1) & 1);
                         commit(ct->s_full);
                         commit(ct->rope_empty[rope]);
@@ -434,7 +439,7 @@ __global__ void __launch_bounds__(Cfg<N, FP8>::kThreads, 1)
 #pragma unroll
                             for (int u = 0; u < kUnits; ++u) {
                                 const uint32_t slot = next(pv_slot, u);
-                                mma_pv4(tmem + u * N, desc_lo(ring_s + slot * kUnit, 1024), p_lo, idesc(128, N) | kAIsMMajor, acc, go);
+                                mma_pv4(tmem + u * N, desc_lo(ring_s + slot * kUnit, 1024), p_lo, idesc<FP8>(128, N) | kAIsMMajor, acc, go);
                                 if (u == kUnits - 1) {
                                     seen |= test(ct->rope_full[rope], rope_ph) ? 1u << kUnits : 0u;
                                     seen |= test(ct->s_read, t & 1) ? 2u << kUnits : 0u;
@@ -449,7 +454,7 @@ __global__ void __launch_bounds__(Cfg<N, FP8>::kThreads, 1)
                             for (int u = 0; u < kUnits; ++u) {
                                 const uint32_t slot = next(pv_slot, u), c_lo = desc_lo(ring_s + slot * kUnit, 1024);
                                 for (int p = 0; p < pages; ++p)
-                                    mma_pv1(tmem + u * N, c_lo + p * 256, p_lo + p * 2, idesc(128, N) | kAIsMMajor, acc || p != 0, go);
+                                    mma_pv1(tmem + u * N, c_lo + p * 256, p_lo + p * 2, idesc<FP8>(128, N) | kAIsMMajor, acc || p != 0, go);
                                 commit(ct->empty[slot]);
                             }
                         }
@@ -615,20 +620,51 @@ __global__ void __launch_bounds__(Cfg<N, FP8>::kThreads, 1)
             bool dead = false;   // a wait of this warp's ran out
             // Q of a segment's rows: the first units to TMEM, where row r is lane 32 (r / 16) + r % 16 (and 16 further, which
             // no product reads), the rest to shared memory.
+            float qs0 = 1.f, qs1 = 1.f;   // e4m3: what the lane's rows of Q are in units of
             auto load_q = [&](const Seg& g) {
+                constexpr int kCopied = FP8 ? 1 : C::kQBlocks;   // blocks that shared memory holds as they are
                 if (tid == 0) {
                     const uint32_t bar = smem_addr(&ct->q_full);
-                    mbar_arrive_expect_tx(bar, C::kQ);
+                    mbar_arrive_expect_tx(bar, kCopied * kBlockQ);
                     ++q_loads;
 #pragma unroll 1
-                    for (int c = 0; c < C::kQBlocks; ++c)
+                    for (int c = C::kQBlocks - kCopied; c < C::kQBlocks; ++c)
                         tma_load_2d(smem_addr(qs) + c * kBlockQ, &tmap_q, (2 * C::kQUnits + c) * 64, g.en.row0, bar);
                 }
                 if (16 * w < g.en.nrows) {
                     const int r = min(16 * w + (lane & 15), g.en.nrows - 1);
                     const uint4* const from = reinterpret_cast<const uint4*>(a.q + static_cast<int64_t>(g.en.row0 + r) * kQueryDim);
-                    constexpr int kBatch = FP8 || N == 64 ? 2 : 4;   // groups of 32 columns (two channels each) on their way at a time
+                    constexpr int kBatch = FP8 ? 1 : N == 64 ? 2 : 4;   // groups of 32 columns (two channels each) on their way at a time
                     constexpr int kGroups = C::kQUnits * 2;
+                    float shrink = 1.f;
+                    if (FP8) {
+                        // The row's largest exponent (of its finite values), by two lanes of half the channels each.
+                        uint32_t top = 0;
+#pragma unroll 1
+                        for (int c = 0; c < 32; c += 8) {
+                            uint4 v[8];
+#pragma unroll
+                            for (int u = 0; u < 8; ++u) v[u] = from[(lane >> 4) * 32 + c + u];
+#pragma unroll
+                            for (int u = 0; u < 8; ++u) {
+                                const uint32_t x[4] = {v[u].x, v[u].y, v[u].z, v[u].w};
+#pragma unroll
+                                for (int e = 0; e < 4; ++e) top = __vmaxu2(top, x[e] & 0x7f807f80u);
+                            }
+                        }
+                        top = max(top >> 16, top & 0xffffu);
+                        top = max(top, __shfl_xor_sync(0xffffffffu, top, 16)) >> 7;
+                        const int up = max(static_cast<int>(min(top, 254u)) - 127 - kQueryTop, -126);
+                        shrink = __uint_as_float(static_cast<uint32_t>(127 - up) << 23);
+                        const float unit = __uint_as_float(static_cast<uint32_t>(127 + up) << 23);
+                        qs0 = __shfl_sync(0xffffffffu, unit, lane >> 2);
+                        qs1 = __shfl_sync(0xffffffffu, unit, (lane >> 2) + 8);
+                    }
+                    auto half2 = [&](uint32_t v) {   // two bf16 in the row's unit, as fp16
+                        float x, y;
+                        unpack2(mul2(pack2(bf16lo(v), bf16hi(v)), pack2(shrink, shrink)), x, y);
+                        return pack_f16x2(x, y);
+                    };
 #pragma unroll 1
                     for (int c0 = 0; c0 < kGroups; c0 += kBatch) {
                         uint32_t x[kBatch][32];
@@ -636,9 +672,27 @@ __global__ void __launch_bounds__(Cfg<N, FP8>::kThreads, 1)
                         for (int c = 0; c < kBatch; ++c)
 #pragma unroll
                             for (int u = 0; u < 8 && c0 + c < kGroups; ++u) *reinterpret_cast<uint4*>(&x[c][4 * u]) = from[(c0 + c) * 8 + u];
+                        if (FP8) {
+#pragma unroll
+                            for (int e = 0; e < 32; ++e) x[0][e] = half2(x[0][e]);
+                        }
 #pragma unroll
                         for (int c = 0; c < kBatch; ++c)
                             if (c0 + c < kGroups) tc_st32(tmem + lanes + C::kColQ + (c0 + c) * 32, x[c]);
+                    }
+                    if (FP8) {
+#pragma unroll 1
+                        for (int c = 0; c < C::kQBlocks - 1; ++c) {
+                            const int row = 16 * w + (lane & 15);
+#pragma unroll
+                            for (int u = 0; u < 4; ++u) {
+                                const int chunk = (lane >> 4) * 4 + u;
+                                uint4 v = from[(kGroups + c) * 8 + chunk];
+                                v = make_uint4(half2(v.x), half2(v.y), half2(v.z), half2(v.w));
+                                *reinterpret_cast<uint4*>(qs + c * kBlockQ + row * 128 + ((chunk ^ (row & 7)) << 4)) = v;
+                            }
+                        }
+                        fence_proxy_async_smem();
                     }
                     tc_wait_st();
                 }
@@ -666,6 +720,8 @@ __global__ void __launch_bounds__(Cfg<N, FP8>::kThreads, 1)
                 const int lim0 = see(r0), lim1 = see(r1);
                 const bool on = 16 * w < rows;          // (warps without rows have no logits, but their share of O)
                 float m0 = -INFINITY, m1 = -INFINITY;   // the rows' bases
+                // e4m3: O is in units of 2^up, so that the largest weight times its token's scale is about 1 in fp16.
+                float up0 = -126.f, up1 = -126.f;
                 float l0 = 0.f, l1 = 0.f, lr0 = 0.f, lr1 = 0.f;
                 float folded0 = -INFINITY, folded1 = -INFINITY;   // the bases of what was folded
                 float* const fold_to = a.cut_o + static_cast<int64_t>(s.slot >= 0 ? s.slot : 2 * static_cast<int>(blockIdx.x) + 1) * N * kLatentDim;
@@ -694,10 +750,11 @@ __global__ void __launch_bounds__(Cfg<N, FP8>::kThreads, 1)
 #pragma unroll
                             for (int c = 0; c < 8; ++c) {
                                 const float2 sc = *reinterpret_cast<const float2*>(&scales[slot * kTok + 8 * c + 2 * quad]);
-                                x[4 * c] = fmaf(x[4 * c], sc.x, y[4 * c]);
-                                x[4 * c + 1] = fmaf(x[4 * c + 1], sc.y, y[4 * c + 1]);
-                                x[4 * c + 2] = fmaf(x[4 * c + 2], sc.x, y[4 * c + 2]);
-                                x[4 * c + 3] = fmaf(x[4 * c + 3], sc.y, y[4 * c + 3]);
+                                const uint64_t s2 = pack2(sc.x, sc.y);
+                                unpack2(fma2(mul2(pack2(x[4 * c], x[4 * c + 1]), pack2(qs0, qs0)), s2, pack2(y[4 * c], y[4 * c + 1])),
+                                        x[4 * c], x[4 * c + 1]);
+                                unpack2(fma2(mul2(pack2(x[4 * c + 2], x[4 * c + 3]), pack2(qs1, qs1)), s2, pack2(y[4 * c + 2], y[4 * c + 3])),
+                                        x[4 * c + 2], x[4 * c + 3]);
                             }
                         }
                     }
@@ -722,7 +779,9 @@ __global__ void __launch_bounds__(Cfg<N, FP8>::kThreads, 1)
                     // one another while they work out the weights, as each holds channels of all rows' O.
                     uint32_t p[8][2];
                     float add0, add1, add_r0, add_r1, over = -INFINITY;
-                    auto weights = [&] {
+                    float big0, big1;   // e4m3: the largest weight times scale, in O's unit
+                    auto weights = [&](float g0, float g1) {
+                        big0 = big1 = 0.f;
                         const float b0 = m0 == -INFINITY ? 0.f : m0, b1 = m1 == -INFINITY ? 0.f : m1;
                         const uint64_t scale2 = pack2(a.scale_log2, a.scale_log2), base0 = pack2(-b0, -b0), base1 = pack2(-b1, -b1);
                         uint64_t sum0 = 0ull, sum1 = 0ull, sumr0 = 0ull, sumr1 = 0ull;
@@ -742,13 +801,17 @@ __global__ void __launch_bounds__(Cfg<N, FP8>::kThreads, 1)
                                 const bool gone = (fault >> (c / 2 * 8)) & 1u;
                                 const uint64_t s2 = plain ? pack2(sc.x, sc.y)
                                                           : pack2(gone || tok >= see_any ? 0.f : sc.x, gone || tok + 1 >= see_any ? 0.f : sc.y);
-                                e0 = mul2(e0, s2);
-                                e1 = mul2(e1, s2);
+                                e0 = mul2(mul2(e0, s2), pack2(g0, g0));
+                                e1 = mul2(mul2(e1, s2), pack2(g1, g1));
                             }
                             unpack2(e0, y[0], y[1]);
                             unpack2(e1, y[2], y[3]);
-                            p[c][0] = pack_bf16x2(y[0], y[1]);
-                            p[c][1] = pack_bf16x2(y[2], y[3]);
+                            if (FP8) {
+                                big0 = fmaxf(big0, fmaxf(y[0], y[1]));
+                                big1 = fmaxf(big1, fmaxf(y[2], y[3]));
+                            }
+                            p[c][0] = FP8 ? pack_f16x2(y[0], y[1]) : pack_bf16x2(y[0], y[1]);
+                            p[c][1] = FP8 ? pack_f16x2(y[2], y[3]) : pack_bf16x2(y[2], y[3]);
                             if (!FP8) {
                                 sumr0 = add2(sumr0, pack2(bf16lo(p[c][0]), bf16hi(p[c][0])));
                                 sumr1 = add2(sumr1, pack2(bf16lo(p[c][1]), bf16hi(p[c][1])));
@@ -765,8 +828,8 @@ __global__ void __launch_bounds__(Cfg<N, FP8>::kThreads, 1)
                         add_r1 = u + v;
                     };
                     if (j > 0) {
-                        if (on) weights();
-                        if (dead || over > kSlack) *static_cast<volatile int*>(&ct->over[tile & 3]) = 1;
+                        if (on) weights(FP8 ? ex2(-up0) : 1.f, FP8 ? ex2(-up1) : 1.f);
+                        if (dead || over > kSlack || (FP8 && on && fmaxf(big0, big1) > kBig)) *static_cast<volatile int*>(&ct->over[tile & 3]) = 1;
                     } else if (lane == 0) {
                         *static_cast<volatile int*>(&ct->over[tile & 3]) = 1;
                     }
@@ -801,13 +864,38 @@ __global__ void __launch_bounds__(Cfg<N, FP8>::kThreads, 1)
                         }
                         const float n0 = fmaxf(m0, top0 * a.scale_log2), n1 = fmaxf(m1, top1 * a.scale_log2);
                         // (A row that has seen nothing yet has added nothing.)
-                        const float alpha0 = m0 == -INFINITY ? 0.f : ex2(m0 - n0), alpha1 = m1 == -INFINITY ? 0.f : ex2(m1 - n1);
-                        m0 = n0;
-                        m1 = n1;
+                        float alpha0 = m0 == -INFINITY ? 0.f : ex2(m0 - n0), alpha1 = m1 == -INFINITY ? 0.f : ex2(m1 - n1);
                         l0 *= alpha0;
                         lr0 *= alpha0;
                         l1 *= alpha1;
                         lr1 *= alpha1;
+                        if (FP8) {
+                            // (The unit of what has been added moves with the base, unless the tile has more.)
+                            const float by0 = m0 - n0, by1 = m1 - n1, was0 = m0 == -INFINITY ? -126.f : up0 + by0,
+                                        was1 = m1 == -INFINITY ? -126.f : up1 + by1;
+                            const bool none0 = m0 == -INFINITY, none1 = m1 == -INFINITY;
+                            m0 = n0;
+                            m1 = n1;
+                            if (on) weights(1.f, 1.f);
+                            else big0 = big1 = 0.f;
+#pragma unroll
+                            for (int d = 1; d < 4; d <<= 1) {
+                                big0 = fmaxf(big0, __shfl_xor_sync(0xffffffffu, big0, d));
+                                big1 = fmaxf(big1, __shfl_xor_sync(0xffffffffu, big1, d));
+                            }
+                            auto unit = [](float big, float before) {
+                                const float e = static_cast<float>(static_cast<int>(__float_as_uint(big) >> 23) - 127);
+                                return fminf(fmaxf(fmaxf(e, before), -126.f), 126.f);
+                            };
+                            const float to0 = unit(big0, was0), to1 = unit(big1, was1);
+                            alpha0 = none0 ? 0.f : ex2(by0 + (up0 - to0));
+                            alpha1 = none1 ? 0.f : ex2(by1 + (up1 - to1));
+                            up0 = to0;
+                            up1 = to1;
+                        } else {
+                            m0 = n0;
+                            m1 = n1;
+                        }
                         if (j > 0) {
                             publish(ct->alpha, alpha0, alpha1);
                             tc_fence_after();
@@ -823,14 +911,15 @@ __global__ void __launch_bounds__(Cfg<N, FP8>::kThreads, 1)
                             }
                             tc_wait_st();
                         }
-                        if (on) weights();
+                        if (on) weights(FP8 ? ex2(-up0) : 1.f, FP8 ? ex2(-up1) : 1.f);
                     }
                     if (j > 0 && (j & (kFoldTiles - 1)) == 0) {
                         // O moves to the fp32 sums: thread's channel 128 u + tid, row after row.
                         tc_fence_after();
-                        publish(ct->factor, folded0 == -INFINITY ? 0.f : ex2(folded0 - m0), folded1 == -INFINITY ? 0.f : ex2(folded1 - m1));
-                        folded0 = m0;
-                        folded1 = m1;
+                        const float o0 = FP8 ? m0 + up0 : m0, o1 = FP8 ? m1 + up1 : m1;
+                        publish(ct->factor, folded0 == -INFINITY ? 0.f : ex2(folded0 - o0), folded1 == -INFINITY ? 0.f : ex2(folded1 - o1));
+                        folded0 = o0;
+                        folded1 = o1;
                         softmax_sync();
 #pragma unroll 1
                         for (int c = 0; c < 4 * N; c += 16) {
@@ -897,8 +986,10 @@ __global__ void __launch_bounds__(Cfg<N, FP8>::kThreads, 1)
                 tc_fence_after();
                 // A row that sees nothing is 0, whatever the others see.
                 if (on) {
-                    publish(ct->factor, whole ? (lr0 > 0.f ? 1.f / lr0 : lr0) : 1.f, whole ? (lr1 > 0.f ? 1.f / lr1 : lr1) : 1.f);
-                    publish(ct->alpha, folded0 == -INFINITY ? 0.f : ex2(folded0 - m0), folded1 == -INFINITY ? 0.f : ex2(folded1 - m1));
+                    const float g0 = FP8 ? ex2(up0) : 1.f, g1 = FP8 ? ex2(up1) : 1.f;
+                    publish(ct->factor, whole ? (lr0 > 0.f ? 1.f / lr0 * g0 : lr0) : g0, whole ? (lr1 > 0.f ? 1.f / lr1 * g1 : lr1) : g1);
+                    publish(ct->alpha, folded0 == -INFINITY ? 0.f : ex2(folded0 - (FP8 ? m0 + up0 : m0)),
+                            folded1 == -INFINITY ? 0.f : ex2(folded1 - (FP8 ? m1 + up1 : m1)));
                     if (quad == 0) {
                         auto result = [&](int r, float m, float l, float lr) {
                             if (r >= rows) return;
@@ -931,7 +1022,7 @@ __global__ void __launch_bounds__(Cfg<N, FP8>::kThreads, 1)
                         float* const to = a.cut_o + (static_cast<int64_t>(s.slot) * N + first_row) * kLatentDim + channel;
 #pragma unroll
                         for (int u = 0; u < 16; ++u)
-                            if (u < left) to[u * kLatentDim] = __uint_as_float(y[u]);
+                            if (u < left) to[u * kLatentDim] = FP8 ? __uint_as_float(y[u]) * f[u] : __uint_as_float(y[u]);
                         continue;
                     }
                     // Pairs of lanes change values, so that each has two channels of one of two rows.
@@ -1043,7 +1134,7 @@ __global__ void __launch_bounds__(Cfg<N, FP8>::kThreads, 1)
             if (FP8) (void)bar_wait(smem_addr(&ct->scale_full[tile % kInfoSlots]), (tile / kInfoSlots) & 1);
         loads_done:;
         } else if (FP8 && warp >= 12) {
-            // ---------------- e4m3 codes -> bf16 units in the MMAs' layout, two warps a unit
+            // ---------------- e4m3 codes -> fp16 units in the MMAs' layout, two warps a unit
             reg_dec<C::kWidenRegs>();
             const int tid = threadIdx.x & 63, mine = (warp - 12) >> 1;
             uint32_t at = mine, until = 0;
@@ -1073,16 +1164,10 @@ __global__ void __launch_bounds__(Cfg<N, FP8>::kThreads, 1)
 #pragma unroll
                     for (int u = 0; u < 8; ++u) {
                         uint4 lo, hi;
-                        widen4(v[u].x, lo.x, lo.y);
-                        widen4(v[u].y, lo.z, lo.w);
-                        widen4(v[u].z, hi.x, hi.y);
-                        widen4(v[u].w, hi.z, hi.w);
-                        if (has_nan(v[u].x) | has_nan(v[u].y) | has_nan(v[u].z) | has_nan(v[u].w)) {
-                            keep_nan(v[u].x, lo.x, lo.y);
-                            keep_nan(v[u].y, lo.z, lo.w);
-                            keep_nan(v[u].z, hi.x, hi.y);
-                            keep_nan(v[u].w, hi.z, hi.w);
-                        }
+                        widen4_f16(v[u].x, lo.x, lo.y);
+                        widen4_f16(v[u].y, lo.z, lo.w);
+                        widen4_f16(v[u].z, hi.x, hi.y);
+                        widen4_f16(v[u].w, hi.z, hi.w);
                         *reinterpret_cast<uint4*>(o + u * 2048 + at0) = lo;
                         *reinterpret_cast<uint4*>(o + u * 2048 + at1) = hi;
                     }

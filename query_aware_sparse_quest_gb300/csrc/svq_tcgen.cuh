@@ -190,6 +190,17 @@ __device__ __forceinline__ void widen4(uint32_t c, uint32_t& lo, uint32_t& hi) {
     lo = *reinterpret_cast<const uint32_t*>(&xr);
     hi = *reinterpret_cast<const uint32_t*>(&yr);
 }
+// The same to fp16 by the conversion unit (77 codes a cycle and SM; widen4 28), NaN codes to NaN.
+__device__ __forceinline__ void widen4_f16(uint32_t c, uint32_t& lo, uint32_t& hi) {
+    asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, l;\n\tcvt.rn.f16x2.e4m3x2 %1, h;\n\t}"
+        : "=r"(lo), "=r"(hi)
+        : "r"(c));
+}
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
+    uint32_t r;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
 // Bit 7 of every byte of c that is a NaN code (0x7f or 0xff).
 __device__ __forceinline__ uint32_t has_nan(uint32_t c) { return ((c & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u; }
 __device__ __forceinline__ void keep_nan(uint32_t c, uint32_t& lo, uint32_t& hi) {
