@@ -32,7 +32,7 @@
 // Roles of a CTA (one per SM):
 //   warp 1       issues the MMAs
 //   warp 2       walks the plan
-//   warps 4-7    softmax (16 rows each), outputs
+//   warps 4-7    softmax (16 rows each, or a part of the tokens where there are fewer than 64), outputs
 //   warps 8-11   load a page of the tile each: units of 64 tokens x 128 channels (16
 //                KB), each freed when its part of the second product is done, and
 //                rotary keys
@@ -80,6 +80,9 @@ struct Cfg {
     static constexpr int kThreads = FP8 ? 640 : 384;
     static constexpr int kMmaRegs = FP8 ? 72 : 96, kSoftmaxRegs = FP8 ? 184 : 248, kLoadRegs = FP8 ? 64 : 96, kWidenRegs = 80;
     static constexpr int kWiden = 8;                                       // warps
+    // Softmax warps that share 16 rows, kCols tokens each.  (Q's rows are repeated on the M side, so every warp's quarter
+    // of TMEM holds its rows' logits.)
+    static constexpr int kGroups = N / 16, kSplit = 4 / kGroups, kCols = kTok / kSplit;
     // TMEM columns: O^T of channels 128 m .. at m N, then S (e4m3: its latent and its rotary part), then the first
     // kQUnits units of Q's channels, two a column.  The others and the rotary ones are in shared memory.
     static constexpr int kSCols = FP8 ? 2 * kTok : kTok;
@@ -186,18 +189,31 @@ __device__ __forceinline__ void mma_pv1(uint32_t d, uint32_t c_lo, uint32_t p_lo
         "}" ::"r"(d), "r"(c_lo), "r"(p_lo), "r"(desc_hi(2048)), "r"(desc_hi(1024)), "r"(id), "r"(acc), "r"(go)
         : "memory");
 }
-// 16 rows x 64 columns: lane l gets rows l / 4 and + 8 of columns 8 c + 2 (l % 4), + 1, at r[4 c ..] and r[4 c + 2 ..].
-__device__ __forceinline__ void tc_ld_rows(uint32_t addr, float (&x)[32]) {
-    uint32_t(&r)[32] = reinterpret_cast<uint32_t(&)[32]>(x);
-    asm volatile(
-        "tcgen05.ld.sync.aligned.16x256b.x8.b32 "
-        "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
-        "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
-        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
-          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
-          "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
-          "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
-        : "r"(addr));
+// 16 rows x 2 K columns: lane l gets rows l / 4 and + 8 of columns 8 c + 2 (l % 4), + 1, at x[4 c ..] and x[4 c + 2 ..].
+template <int K>
+__device__ __forceinline__ void tc_ld_rows(uint32_t addr, float (&x)[K]) {
+    uint32_t(&r)[K] = reinterpret_cast<uint32_t(&)[K]>(x);
+    static_assert(K == 8 || K == 16 || K == 32);
+    if constexpr (K == 8)
+        asm volatile("tcgen05.ld.sync.aligned.16x256b.x2.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                     : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+                     : "r"(addr));
+    else if constexpr (K == 16)
+        asm volatile(
+            "tcgen05.ld.sync.aligned.16x256b.x4.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+            : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+              "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+            : "r"(addr));
+    else
+        asm volatile(
+            "tcgen05.ld.sync.aligned.16x256b.x8.b32 "
+            "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+            "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+            : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+              "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
+              "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+              "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+            : "r"(addr));
 }
 // Four 8 x 8 blocks of 16-bit values: lane l gives the address of row l % 8 of block l / 8.
 __device__ __forceinline__ void stmatrix_x4(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
@@ -265,6 +281,13 @@ struct Control {
     int over[4];                           // a logit of the tile is too far above its row's base
     int lens[kOwnPlan];                       // of the requests, where the CTA plans by itself
     Seg seg[kSegs];
+    // Rows' maxima of the warps that share them, and at a segment's end their sums.
+    union {
+        struct {
+            float top[kMaxRows], big[kMaxRows];
+        };
+        float2 sum[kMaxRows];
+    };
     alignas(16) float alpha[kMaxRows], factor[kMaxRows];   // of a row's O: where its base moves, and at a segment's end
 };
 static_assert(sizeof(Control) <= kControlBytes, "control block");
@@ -611,9 +634,12 @@ __global__ void __launch_bounds__(Cfg<N, FP8>::kThreads, 1)
                 for (int i = lane; i < a.heads; i += 32) a.lse[r0 + i] = -INFINITY;
             }
         } else if (warp >= 4 && warp < 8) {
-            // ---------------- softmax: warp w rows 16 w .., lane l rows l / 4 and + 8 of those, tokens 8 c + 2 (l % 4), + 1
+            // ---------------- softmax: warp w rows 16 (w % kGroups) .. and kCols tokens from tok0 on, lane l rows l / 4 and
+            // + 8 of those and tokens 8 c + 2 (l % 4), + 1
+            constexpr int kC = C::kCols / 8;
             reg_inc<C::kSoftmaxRegs>();
             const int w = warp - 4, tid = threadIdx.x - 128;
+            const int rg = w % C::kGroups, tp = w / C::kGroups, tok0 = tp * C::kCols;
             const int quad = lane & 3;
             const uint32_t lanes = static_cast<uint32_t>(w * 32) << 16;
             uint32_t tile = 0, q_loads = 0;
@@ -629,10 +655,11 @@ __global__ void __launch_bounds__(Cfg<N, FP8>::kThreads, 1)
                     ++q_loads;
 #pragma unroll 1
                     for (int c = C::kQBlocks - kCopied; c < C::kQBlocks; ++c)
-                        tma_load_2d(smem_addr(qs) + c * kBlockQ, &tmap_q, (2 * C::kQUnits + c) * 64, g.en.row0, bar);
+                        for (int i = 0; i < C::kSplit; ++i)
+                            tma_load_2d(smem_addr(qs) + c * kBlockQ + i * (N * 128), &tmap_q, (2 * C::kQUnits + c) * 64, g.en.row0, bar);
                 }
-                if (16 * w < g.en.nrows) {
-                    const int r = min(16 * w + (lane & 15), g.en.nrows - 1);
+                if (16 * rg < g.en.nrows) {
+                    const int r = min(16 * rg + (lane & 15), g.en.nrows - 1);
                     const uint4* const from = reinterpret_cast<const uint4*>(a.q + static_cast<int64_t>(g.en.row0 + r) * kQueryDim);
                     constexpr int kBatch = FP8 ? 1 : N == 64 ? 2 : 4;   // groups of 32 columns (two channels each) on their way at a time
                     constexpr int kGroups = C::kQUnits * 2;
@@ -716,9 +743,9 @@ __global__ void __launch_bounds__(Cfg<N, FP8>::kThreads, 1)
                 // Tokens that a row sees.
                 auto see = [&](int r) { return s.en.posbase + (s.en.row0 + min(r, rows - 1)) / a.heads + 1; };
                 const int see_all = see(0), see_any = see(rows - 1);
-                const int r0 = 16 * w + (lane >> 2), r1 = r0 + 8;
+                const int r0 = 16 * rg + (lane >> 2), r1 = r0 + 8;
                 const int lim0 = see(r0), lim1 = see(r1);
-                const bool on = 16 * w < rows;          // (warps without rows have no logits, but their share of O)
+                const bool on = 16 * rg < rows;         // (warps without rows have no logits, but their share of O)
                 float m0 = -INFINITY, m1 = -INFINITY;   // the rows' bases
                 // e4m3: O is in units of 2^up, so that the largest weight times its token's scale is about 1 in fp16.
                 float up0 = -126.f, up1 = -126.f;
@@ -727,9 +754,22 @@ __global__ void __launch_bounds__(Cfg<N, FP8>::kThreads, 1)
                 float* const fold_to = a.cut_o + static_cast<int64_t>(s.slot >= 0 ? s.slot : 2 * static_cast<int>(blockIdx.x) + 1) * N * kLatentDim;
                 // The rows' factors, by the lane that has them first; all read them behind a barrier.
                 auto publish = [&](float* to, float f0, float f1) {
-                    if (quad == 0) {
+                    if (quad == 0 && tp == 0) {
                         to[r0] = f0;
                         to[r1] = f1;
+                    }
+                };
+                // Maxima over the warps that share the rows, in `at`, a warp's 16 rows each.
+                auto across = [&](float* at, float& v0, float& v1) {
+                    if (quad == 0) {
+                        at[16 * w + (lane >> 2)] = v0;
+                        at[16 * w + 8 + (lane >> 2)] = v1;
+                    }
+                    softmax_sync();
+#pragma unroll
+                    for (int i = 0; i < C::kSplit; ++i) {
+                        v0 = fmaxf(v0, at[i * N + r0]);
+                        v1 = fmaxf(v1, at[i * N + r1]);
                     }
                 };
                 for (int j = 0; j < n; ++j, ++tile) {
@@ -738,18 +778,18 @@ __global__ void __launch_bounds__(Cfg<N, FP8>::kThreads, 1)
                     LATENT_WAIT(ct->s_full, tile & 1);
                     tc_fence_after();
                     const uint32_t fault = *reinterpret_cast<const uint32_t*>(ct->fault[slot]);
-                    float x[32];
+                    float x[4 * kC];
                     if (on) {
-                        tc_ld_rows(tmem + lanes + C::kColS, x);
+                        tc_ld_rows(tmem + lanes + C::kColS + tok0, x);
                         tc_wait_ld();
                         if (FP8) {
-                            float y[32];
-                            tc_ld_rows(tmem + lanes + C::kColS + kTok, y);
+                            float y[4 * kC];
+                            tc_ld_rows(tmem + lanes + C::kColS + kTok + tok0, y);
                             tc_wait_ld();
                             LATENT_WAIT(ct->scale_full[slot], (tile / kInfoSlots) & 1);
 #pragma unroll
-                            for (int c = 0; c < 8; ++c) {
-                                const float2 sc = *reinterpret_cast<const float2*>(&scales[slot * kTok + 8 * c + 2 * quad]);
+                            for (int c = 0; c < kC; ++c) {
+                                const float2 sc = *reinterpret_cast<const float2*>(&scales[slot * kTok + tok0 + 8 * c + 2 * quad]);
                                 const uint64_t s2 = pack2(sc.x, sc.y);
                                 unpack2(fma2(mul2(pack2(x[4 * c], x[4 * c + 1]), pack2(qs0, qs0)), s2, pack2(y[4 * c], y[4 * c + 1])),
                                         x[4 * c], x[4 * c + 1]);
@@ -764,11 +804,11 @@ __global__ void __launch_bounds__(Cfg<N, FP8>::kThreads, 1)
                     const bool plain = first + kTok <= see_all && !fault;
                     if (on && !plain) {
 #pragma unroll
-                        for (int c = 0; c < 8; ++c) {
-                            const bool gone = (fault >> (c / 2 * 8)) & 1u;
+                        for (int c = 0; c < kC; ++c) {
+                            const bool gone = (fault >> ((tok0 / 16 + c / 2) * 8)) & 1u;
 #pragma unroll
                             for (int u = 0; u < 2; ++u) {
-                                const int tok = first + 8 * c + 2 * quad + u;
+                                const int tok = first + tok0 + 8 * c + 2 * quad + u;
                                 if (gone || tok >= lim0) x[4 * c + u] = -INFINITY;
                                 if (gone || tok >= lim1) x[4 * c + 2 + u] = -INFINITY;
                             }
@@ -777,7 +817,7 @@ __global__ void __launch_bounds__(Cfg<N, FP8>::kThreads, 1)
                     // Weights go by the rows' bases as they are, unless a logit is more than kSlack above its row's: then
                     // (at a run's first tile, and seldom behind it) the tile's maxima move the bases.  The warps say so to
                     // one another while they work out the weights, as each holds channels of all rows' O.
-                    uint32_t p[8][2];
+                    uint32_t p[kC][2];
                     float add0, add1, add_r0, add_r1, over = -INFINITY;
                     float big0, big1;   // e4m3: the largest weight times scale, in O's unit
                     auto weights = [&](float g0, float g1) {
@@ -786,7 +826,7 @@ __global__ void __launch_bounds__(Cfg<N, FP8>::kThreads, 1)
                         const uint64_t scale2 = pack2(a.scale_log2, a.scale_log2), base0 = pack2(-b0, -b0), base1 = pack2(-b1, -b1);
                         uint64_t sum0 = 0ull, sum1 = 0ull, sumr0 = 0ull, sumr1 = 0ull;
 #pragma unroll
-                        for (int c = 0; c < 8; ++c) {
+                        for (int c = 0; c < kC; ++c) {
                             float y[4];
                             unpack2(fma2(pack2(x[4 * c], x[4 * c + 1]), scale2, base0), y[0], y[1]);
                             unpack2(fma2(pack2(x[4 * c + 2], x[4 * c + 3]), scale2, base1), y[2], y[3]);
@@ -796,9 +836,9 @@ __global__ void __launch_bounds__(Cfg<N, FP8>::kThreads, 1)
                             sum1 = add2(sum1, e1);
                             if (FP8) {
                                 // (Scales of tokens that no row sees may hold anything.)
-                                const float2 sc = *reinterpret_cast<const float2*>(&scales[slot * kTok + 8 * c + 2 * quad]);
-                                const int tok = first + 8 * c + 2 * quad;
-                                const bool gone = (fault >> (c / 2 * 8)) & 1u;
+                                const float2 sc = *reinterpret_cast<const float2*>(&scales[slot * kTok + tok0 + 8 * c + 2 * quad]);
+                                const int tok = first + tok0 + 8 * c + 2 * quad;
+                                const bool gone = (fault >> ((tok0 / 16 + c / 2) * 8)) & 1u;
                                 const uint64_t s2 = plain ? pack2(sc.x, sc.y)
                                                           : pack2(gone || tok >= see_any ? 0.f : sc.x, gone || tok + 1 >= see_any ? 0.f : sc.y);
                                 e0 = mul2(mul2(e0, s2), pack2(g0, g0));
@@ -852,7 +892,7 @@ __global__ void __launch_bounds__(Cfg<N, FP8>::kThreads, 1)
                         float top0 = -INFINITY, top1 = -INFINITY;
                         if (on) {
 #pragma unroll
-                            for (int c = 0; c < 8; ++c) {
+                            for (int c = 0; c < kC; ++c) {
                                 top0 = fmaxf(top0, fmaxf(x[4 * c], x[4 * c + 1]));
                                 top1 = fmaxf(top1, fmaxf(x[4 * c + 2], x[4 * c + 3]));
                             }
@@ -862,6 +902,7 @@ __global__ void __launch_bounds__(Cfg<N, FP8>::kThreads, 1)
                             top0 = fmaxf(top0, __shfl_xor_sync(0xffffffffu, top0, d));
                             top1 = fmaxf(top1, __shfl_xor_sync(0xffffffffu, top1, d));
                         }
+                        if (C::kSplit > 1) across(ct->top, top0, top1);
                         const float n0 = fmaxf(m0, top0 * a.scale_log2), n1 = fmaxf(m1, top1 * a.scale_log2);
                         // (A row that has seen nothing yet has added nothing.)
                         float alpha0 = m0 == -INFINITY ? 0.f : ex2(m0 - n0), alpha1 = m1 == -INFINITY ? 0.f : ex2(m1 - n1);
@@ -883,6 +924,7 @@ __global__ void __launch_bounds__(Cfg<N, FP8>::kThreads, 1)
                                 big0 = fmaxf(big0, __shfl_xor_sync(0xffffffffu, big0, d));
                                 big1 = fmaxf(big1, __shfl_xor_sync(0xffffffffu, big1, d));
                             }
+                            if (C::kSplit > 1) across(ct->big, big0, big1);
                             auto unit = [](float big, float before) {
                                 const float e = static_cast<float>(static_cast<int>(__float_as_uint(big) >> 23) - 127);
                                 return fminf(fmaxf(fmaxf(e, before), -126.f), 126.f);
@@ -940,8 +982,8 @@ __global__ void __launch_bounds__(Cfg<N, FP8>::kThreads, 1)
                     // P, a row of 64 tokens each: blocks of 8 rows x 8 tokens.
                     if (on) {
 #pragma unroll
-                        for (int c = 0; c < 8; c += 2) {
-                            const int r = 16 * w + (lane & 15), chunk = c + (lane >> 4);
+                        for (int c = 0; c < kC; c += 2) {
+                            const int r = 16 * rg + (lane & 15), chunk = tok0 / 8 + c + (lane >> 4);
                             stmatrix_x4(smem_addr(ps) + r * 128 + ((chunk ^ (r & 7)) << 4), p[c][0], p[c][1], p[c + 1][0], p[c + 1][1]);
                         }
                     }
@@ -982,15 +1024,31 @@ __global__ void __launch_bounds__(Cfg<N, FP8>::kThreads, 1)
                     lr1 = l1;
                 }
                 const bool whole = s.slot < 0;
-                LATENT_WAIT(ct->pv_done, (tile - 1) & 1);   // (all warps have read the factors of their last tile, too)
+                LATENT_WAIT(ct->pv_done, (tile - 1) & 1);   // (all warps have read the factors and maxima of their last tile, too)
                 tc_fence_after();
+                if (C::kSplit > 1) {
+                    if (quad == 0) {
+                        ct->sum[16 * w + (lane >> 2)] = make_float2(l0, lr0);
+                        ct->sum[16 * w + 8 + (lane >> 2)] = make_float2(l1, lr1);
+                    }
+                    softmax_sync();
+                    l0 = l1 = lr0 = lr1 = 0.f;
+#pragma unroll
+                    for (int i = 0; i < C::kSplit; ++i) {
+                        const float2 a0 = ct->sum[i * N + r0], a1 = ct->sum[i * N + r1];
+                        l0 += a0.x;
+                        lr0 += a0.y;
+                        l1 += a1.x;
+                        lr1 += a1.y;
+                    }
+                }
                 // A row that sees nothing is 0, whatever the others see.
                 if (on) {
                     const float g0 = FP8 ? ex2(up0) : 1.f, g1 = FP8 ? ex2(up1) : 1.f;
                     publish(ct->factor, whole ? (lr0 > 0.f ? 1.f / lr0 * g0 : lr0) : g0, whole ? (lr1 > 0.f ? 1.f / lr1 * g1 : lr1) : g1);
                     publish(ct->alpha, folded0 == -INFINITY ? 0.f : ex2(folded0 - (FP8 ? m0 + up0 : m0)),
                             folded1 == -INFINITY ? 0.f : ex2(folded1 - (FP8 ? m1 + up1 : m1)));
-                    if (quad == 0) {
+                    if (quad == 0 && tp == 0) {
                         auto result = [&](int r, float m, float l, float lr) {
                             if (r >= rows) return;
                             if (whole) a.lse[s.en.row0 + r] = l > 0.f ? (m + log2f(l)) * 0.69314718055994531f : (l == 0.f ? -INFINITY : l);
@@ -1572,7 +1630,7 @@ int launch_latent_attention(const sv_cache* c, const void* q, int num_q_heads, c
     a.odd = reinterpret_cast<uint32_t*>(ws + lay.odd);
     a.num_odd = reinterpret_cast<int*>(ws + lay.num_odd);
     CUtensorMap tq, tc, tr;
-    if (!encode_rows(&tq, q, kQueryDim, static_cast<int64_t>(total_q) * num_q_heads, 64) ||
+    if (!encode_rows(&tq, q, kQueryDim, static_cast<int64_t>(total_q) * num_q_heads, lay.tile_rows) ||
         !encode_latents(&tc, c->k_pool, c->num_phys_pages, a.fp8) ||
         !encode_rows(&tr, c->v_pool, kRopeDim, c->num_phys_pages * kPage, kPage))
         return SV_ERR_CUDA;
