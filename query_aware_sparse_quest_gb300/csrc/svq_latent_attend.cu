@@ -36,8 +36,9 @@
 //   warps 8-11   load a page of the tile each: units of 64 tokens x 128 channels (16
 //                KB), each freed when its part of the second product is done, and
 //                rotary keys
-//   warps 12-19  (e4m3) widen the codes
+//   warps 12-15  (e4m3) widen the codes
 #include <climits>
+#include <type_traits>
 
 #include "svq_paged.cuh"
 #include "svq_tcgen.cuh"
@@ -68,18 +69,18 @@ constexpr int kMaxRows = 64;                        // rows of a CTA's tile at m
 
 template <int N, bool FP8>
 struct Cfg {
-    static constexpr int kRing = FP8 ? 8 : (N == 64 ? 11 : 12);            // units: two tiles at least
+    static constexpr int kRing = FP8 ? (N == 64 ? 8 : 10) : (N == 64 ? 11 : 12);           // units: two tiles at least
     static constexpr int kRope = 2;                                        // rotary tiles
-    static constexpr int kCodes = FP8 ? (N == 64 ? 3 : 8) : 0;             // units of codes, 8 KB
+    static constexpr int kCodes = FP8 ? (N == 64 ? 2 : 4) : 0;             // units of codes, 8 KB
     // Pairs of warps that widen a unit each, in turn.  (A pair sees every phase of the slots it reads: kCodes % kPairs is 0.)
-    static constexpr int kPairs = N == 64 ? 3 : 4;
+    static constexpr int kPairs = 2, kWiden = 2 * kPairs;
     static_assert(kCodes % kPairs == 0, "code slots");
     // Registers a thread: bf16 168 at launch, then 96 for the first four warps and the loads and 248 for the softmax
-    // (128 x (96 + 248 + 96) < 384 x 168); e4m3 96, then 72, 184 and 64, and 80 for widening (128 x (72 + 184 + 64 + 2 x 80)
-    // = 640 x 96).
-    static constexpr int kThreads = FP8 ? 640 : 384;
-    static constexpr int kMmaRegs = FP8 ? 72 : 96, kSoftmaxRegs = FP8 ? 184 : 248, kLoadRegs = FP8 ? 64 : 96, kWidenRegs = 80;
-    static constexpr int kWiden = 8;                                       // warps
+    // (128 x (96 + 248 + 96) < 384 x 168); e4m3 128, then 72, 232, 64 and 128 (128 x (72 + 232 + 64 + 128) < 512 x 128).
+    // (The compiler keeps every role's code near the count at launch: with eight warps that widen, 640 threads of 96, the
+    // softmax takes half as long again, 7 requests' chunks 935 us for 800.)
+    static constexpr int kThreads = FP8 ? 512 : 384;
+    static constexpr int kMmaRegs = FP8 ? 72 : 96, kSoftmaxRegs = FP8 ? 232 : 248, kLoadRegs = FP8 ? 64 : 96, kWidenRegs = 128;
     // Softmax warps that share 16 rows, kCols tokens each.  (Q's rows are repeated on the M side, so every warp's quarter
     // of TMEM holds its rows' logits.)
     static constexpr int kGroups = N / 16, kSplit = 4 / kGroups, kCols = kTok / kSplit;
@@ -215,6 +216,14 @@ __device__ __forceinline__ void tc_ld_rows(uint32_t addr, float (&x)[K]) {
               "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
             : "r"(addr));
 }
+// 16 rows of 32 columns: lanes 0 .. 15 have the rows' first 16, lanes 16 .. 31 the others.
+__device__ __forceinline__ void tc_st_halves(uint32_t addr, const uint32_t (&r)[16]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.16x32bx2.x16.b32 [%0], 16, {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(addr),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]),
+        "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+        : "memory");
+}
 // Four 8 x 8 blocks of 16-bit values: lane l gives the address of row l % 8 of block l / 8.
 __device__ __forceinline__ void stmatrix_x4(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
     asm volatile("stmatrix.sync.aligned.m8n8.x4.shared.b16 [%0], {%1,%2,%3,%4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d)
@@ -331,8 +340,8 @@ struct PlacedEntry {
 
 template <int N, bool FP8>
 __global__ void __launch_bounds__(Cfg<N, FP8>::kThreads, 1)
-    latent_kernel(const __grid_constant__ LatentArgs a, const __grid_constant__ CUtensorMap tmap_q,
-                  const __grid_constant__ CUtensorMap tmap_c, const __grid_constant__ CUtensorMap tmap_r) {
+    latent_kernel(const __grid_constant__ LatentArgs a, const __grid_constant__ CUtensorMap tmap_c,
+                  const __grid_constant__ CUtensorMap tmap_r) {
     using C = Cfg<N, FP8>;
     extern __shared__ __align__(1024) unsigned char smem[];
     unsigned char* const ring = smem;
@@ -368,12 +377,11 @@ __global__ void __launch_bounds__(Cfg<N, FP8>::kThreads, 1)
         mbar_init(smem_addr(&ct->s_read), 4);
         mbar_init(smem_addr(&ct->p_full), 4);
         mbar_init(smem_addr(&ct->pv_done), 1);
-        mbar_init(smem_addr(&ct->q_full), 5);   // the copy of its part in shared memory, and the softmax warps
+        mbar_init(smem_addr(&ct->q_full), 4);
         mbar_init(smem_addr(&ct->vote), 4);
         for (int i = 0; i < 4; ++i) ct->over[i] = 0;
         mbar_init(smem_addr(&ct->drain), 1);
         mbar_init_fence();
-        prefetch_tmap(&tmap_q);
         prefetch_tmap(&tmap_c);
         prefetch_tmap(&tmap_r);
     }
@@ -642,85 +650,81 @@ __global__ void __launch_bounds__(Cfg<N, FP8>::kThreads, 1)
             const int rg = w % C::kGroups, tp = w / C::kGroups, tok0 = tp * C::kCols;
             const int quad = lane & 3;
             const uint32_t lanes = static_cast<uint32_t>(w * 32) << 16;
-            uint32_t tile = 0, q_loads = 0;
+            uint32_t tile = 0;
             bool dead = false;   // a wait of this warp's ran out
-            // Q of a segment's rows: the first units to TMEM, where row r is lane 32 (r / 16) + r % 16 (and 16 further, which
-            // no product reads), the rest to shared memory.
+            // Q of a segment's rows: the first units to TMEM, where row r is lane 32 (r / 16) + r % 16, the rest to shared
+            // memory.  Eight lanes read a row, rows 4 i + lane / 8 and chunks of 8 channels (a row a lane would touch 32
+            // lines a load), and the way to TMEM leads through the warp's rows of the last block.
             float qs0 = 1.f, qs1 = 1.f;   // e4m3: what the lane's rows of Q are in units of
             auto load_q = [&](const Seg& g) {
-                constexpr int kCopied = FP8 ? 1 : C::kQBlocks;   // blocks that shared memory holds as they are
-                if (tid == 0) {
-                    const uint32_t bar = smem_addr(&ct->q_full);
-                    mbar_arrive_expect_tx(bar, kCopied * kBlockQ);
-                    ++q_loads;
-#pragma unroll 1
-                    for (int c = C::kQBlocks - kCopied; c < C::kQBlocks; ++c)
-                        for (int i = 0; i < C::kSplit; ++i)
-                            tma_load_2d(smem_addr(qs) + c * kBlockQ + i * (N * 128), &tmap_q, (2 * C::kQUnits + c) * 64, g.en.row0, bar);
-                }
                 if (16 * rg < g.en.nrows) {
-                    const int r = min(16 * rg + (lane & 15), g.en.nrows - 1);
-                    const uint4* const from = reinterpret_cast<const uint4*>(a.q + static_cast<int64_t>(g.en.row0 + r) * kQueryDim);
-                    constexpr int kBatch = FP8 ? 1 : N == 64 ? 2 : 4;   // groups of 32 columns (two channels each) on their way at a time
-                    constexpr int kGroups = C::kQUnits * 2;
-                    float shrink = 1.f;
+                    constexpr int kBlocks = kQueryDim / 64;
+                    const uint4* from[4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        from[i] = reinterpret_cast<const uint4*>(a.q + static_cast<int64_t>(g.en.row0 + min(16 * rg + 4 * i + (lane >> 3), g.en.nrows - 1)) * kQueryDim) + (lane & 7);
+                    float shrink[4];
                     if (FP8) {
-                        // The row's largest exponent (of its finite values), by two lanes of half the channels each.
-                        uint32_t top = 0;
-#pragma unroll 1
-                        for (int c = 0; c < 32; c += 8) {
-                            uint4 v[8];
+                        // The rows' largest exponents (of their finite values).
+                        uint32_t top[4] = {0, 0, 0, 0};
 #pragma unroll
-                            for (int u = 0; u < 8; ++u) v[u] = from[(lane >> 4) * 32 + c + u];
+                        for (int c = 0; c < kBlocks - 1; ++c)
 #pragma unroll
-                            for (int u = 0; u < 8; ++u) {
-                                const uint32_t x[4] = {v[u].x, v[u].y, v[u].z, v[u].w};
+                            for (int i = 0; i < 4; ++i) {
+                                const uint4 v = from[i][8 * c];
+                                top[i] = __vmaxu2(top[i], __vmaxu2(__vmaxu2(v.x & 0x7f807f80u, v.y & 0x7f807f80u), __vmaxu2(v.z & 0x7f807f80u, v.w & 0x7f807f80u)));
+                            }
+                        float of[4];
 #pragma unroll
-                                for (int e = 0; e < 4; ++e) top = __vmaxu2(top, x[e] & 0x7f807f80u);
+                        for (int i = 0; i < 4; ++i) {
+                            uint32_t t = max(top[i] >> 16, top[i] & 0xffffu);
+#pragma unroll
+                            for (int d = 1; d < 8; d <<= 1) t = max(t, __shfl_xor_sync(0xffffffffu, t, d));
+                            const int up = max(static_cast<int>(min(t >> 7, 254u)) - 127 - kQueryTop, -126);
+                            shrink[i] = __uint_as_float(static_cast<uint32_t>(127 - up) << 23);
+                            of[i] = __shfl_sync(0xffffffffu, __uint_as_float(static_cast<uint32_t>(127 + up) << 23), 8 * ((lane >> 2) & 3));
+                        }
+                        // (Row l / 4 is held as i = l / 16, row l / 4 + 8 as i + 2.)
+                        qs0 = lane & 16 ? of[1] : of[0];
+                        qs1 = lane & 16 ? of[3] : of[2];
+                    }
+                    constexpr int kBatch = 5;   // blocks on their way at a time
+                    unsigned char* const to = qs + w * 2048, * const way = to + (C::kQBlocks - 1) * kBlockQ;
+                    auto put = [](unsigned char* at, int r, int chunk) { return reinterpret_cast<uint4*>(at + r * 128 + ((chunk ^ (r & 7)) << 4)); };
+#pragma unroll
+                    for (int c0 = 0; c0 < kBlocks; c0 += kBatch) {
+                        uint4 x[kBatch][4];
+#pragma unroll
+                        for (int c = c0; c < c0 + kBatch && c < kBlocks; ++c)
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) x[c - c0][i] = from[i][8 * c];
+#pragma unroll
+                        for (int c = c0; c < c0 + kBatch && c < kBlocks; ++c) {
+                            const bool to_tmem = c < 2 * C::kQUnits;
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) {
+                                uint4 v = x[c - c0][i];
+                                if (FP8 && c < kBlocks - 1) {
+                                    auto half2 = [&](uint32_t e) {
+                                        float y, z;
+                                        unpack2(mul2(pack2(bf16lo(e), bf16hi(e)), pack2(shrink[i], shrink[i])), y, z);
+                                        return pack_f16x2(y, z);
+                                    };
+                                    v = make_uint4(half2(v.x), half2(v.y), half2(v.z), half2(v.w));
+                                }
+                                *put(to_tmem ? way : to + (c - 2 * C::kQUnits) * kBlockQ, 4 * i + (lane >> 3), lane & 7) = v;
+                            }
+                            if (to_tmem) {
+                                __syncwarp();
+                                uint32_t y[16];   // half of row l % 16
+#pragma unroll
+                                for (int u = 0; u < 4; ++u) *reinterpret_cast<uint4*>(&y[4 * u]) = *put(way, lane & 15, (lane >> 4) * 4 + u);
+                                tc_st_halves(tmem + lanes + C::kColQ + c * 32, y);
+                                __syncwarp();
                             }
                         }
-                        top = max(top >> 16, top & 0xffffu);
-                        top = max(top, __shfl_xor_sync(0xffffffffu, top, 16)) >> 7;
-                        const int up = max(static_cast<int>(min(top, 254u)) - 127 - kQueryTop, -126);
-                        shrink = __uint_as_float(static_cast<uint32_t>(127 - up) << 23);
-                        const float unit = __uint_as_float(static_cast<uint32_t>(127 + up) << 23);
-                        qs0 = __shfl_sync(0xffffffffu, unit, lane >> 2);
-                        qs1 = __shfl_sync(0xffffffffu, unit, (lane >> 2) + 8);
                     }
-                    auto half2 = [&](uint32_t v) {   // two bf16 in the row's unit, as fp16
-                        float x, y;
-                        unpack2(mul2(pack2(bf16lo(v), bf16hi(v)), pack2(shrink, shrink)), x, y);
-                        return pack_f16x2(x, y);
-                    };
-#pragma unroll 1
-                    for (int c0 = 0; c0 < kGroups; c0 += kBatch) {
-                        uint32_t x[kBatch][32];
-#pragma unroll
-                        for (int c = 0; c < kBatch; ++c)
-#pragma unroll
-                            for (int u = 0; u < 8 && c0 + c < kGroups; ++u) *reinterpret_cast<uint4*>(&x[c][4 * u]) = from[(c0 + c) * 8 + u];
-                        if (FP8) {
-#pragma unroll
-                            for (int e = 0; e < 32; ++e) x[0][e] = half2(x[0][e]);
-                        }
-#pragma unroll
-                        for (int c = 0; c < kBatch; ++c)
-                            if (c0 + c < kGroups) tc_st32(tmem + lanes + C::kColQ + (c0 + c) * 32, x[c]);
-                    }
-                    if (FP8) {
-#pragma unroll 1
-                        for (int c = 0; c < C::kQBlocks - 1; ++c) {
-                            const int row = 16 * w + (lane & 15);
-#pragma unroll
-                            for (int u = 0; u < 4; ++u) {
-                                const int chunk = (lane >> 4) * 4 + u;
-                                uint4 v = from[(kGroups + c) * 8 + chunk];
-                                v = make_uint4(half2(v.x), half2(v.y), half2(v.z), half2(v.w));
-                                *reinterpret_cast<uint4*>(qs + c * kBlockQ + row * 128 + ((chunk ^ (row & 7)) << 4)) = v;
-                            }
-                        }
-                        fence_proxy_async_smem();
-                    }
+                    fence_proxy_async_smem();
                     tc_wait_st();
                 }
                 tc_fence_before();
@@ -1076,25 +1080,30 @@ __global__ void __launch_bounds__(Cfg<N, FP8>::kThreads, 1)
                         for (int u = 0; u < 16; ++u)
                             if (u < left) y[u] = __float_as_uint(fmaf(from[u * kLatentDim], ct->alpha[first_row + u], __uint_as_float(y[u])));
                     }
-                    if (!whole) {
-                        float* const to = a.cut_o + (static_cast<int64_t>(s.slot) * N + first_row) * kLatentDim + channel;
+                    // (The rows mostly are all there: without the tests a partial's 16 take 340 cycles instead of 1070.)
+                    auto write = [&](auto all) {
+                        if (!whole) {
+                            float* const to = a.cut_o + (static_cast<int64_t>(s.slot) * N + first_row) * kLatentDim + channel;
 #pragma unroll
-                        for (int u = 0; u < 16; ++u)
-                            if (u < left) to[u * kLatentDim] = FP8 ? __uint_as_float(y[u]) * f[u] : __uint_as_float(y[u]);
-                        continue;
-                    }
-                    // Pairs of lanes change values, so that each has two channels of one of two rows.
-                    const bool high = tid & 1;
-                    __nv_bfloat16* const to = a.out + static_cast<int64_t>(s.en.row0 + first_row + high) * kLatentDim + (channel & ~1);
+                            for (int u = 0; u < 16; ++u)
+                                if (all || u < left) to[u * kLatentDim] = FP8 ? __uint_as_float(y[u]) * f[u] : __uint_as_float(y[u]);
+                            return;
+                        }
+                        // Pairs of lanes change values, so that each has two channels of one of two rows.
+                        const bool high = tid & 1;
+                        __nv_bfloat16* const to = a.out + static_cast<int64_t>(s.en.row0 + first_row + high) * kLatentDim + (channel & ~1);
 #pragma unroll
-                    for (int u = 0; u < 16; u += 2) {
-                        const float v0 = f[u] == 0.f || u >= left ? 0.f : __uint_as_float(y[u]) * f[u];
-                        const float v1 = f[u + 1] == 0.f || u + 1 >= left ? 0.f : __uint_as_float(y[u + 1]) * f[u + 1];
-                        odd = fmaf(v0, 0.f, fmaf(v1, 0.f, odd));
-                        const float other = __shfl_xor_sync(0xffffffffu, high ? v0 : v1, 1);
-                        if (u + high < left)
-                            *reinterpret_cast<uint32_t*>(to + u * kLatentDim) = high ? pack_bf16x2(other, v1) : pack_bf16x2(v0, other);
-                    }
+                        for (int u = 0; u < 16; u += 2) {
+                            const float v0 = f[u] == 0.f || !(all || u < left) ? 0.f : __uint_as_float(y[u]) * f[u];
+                            const float v1 = f[u + 1] == 0.f || !(all || u + 1 < left) ? 0.f : __uint_as_float(y[u + 1]) * f[u + 1];
+                            odd = fmaf(v0, 0.f, fmaf(v1, 0.f, odd));
+                            const float other = __shfl_xor_sync(0xffffffffu, high ? v0 : v1, 1);
+                            if (all || u + high < left)
+                                *reinterpret_cast<uint32_t*>(to + u * kLatentDim) = high ? pack_bf16x2(other, v1) : pack_bf16x2(v0, other);
+                        }
+                    };
+                    if (left >= 16) write(std::true_type{});
+                    else write(std::false_type{});
                 }
                 // (Rows of one token see the same.)
                 if (whole && softmax_any(odd != 0.f) && tid == 0 && see_all != see_any)
@@ -1103,9 +1112,7 @@ __global__ void __launch_bounds__(Cfg<N, FP8>::kThreads, 1)
                 softmax_sync();   // all have read O before the next segment's first product writes it
                 seg_done(k);
             }
-        softmax_end:
-            // (Gave up: the rows in flight land before the CTA retires.)
-            if (tid == 0 && q_loads) (void)bar_wait(smem_addr(&ct->q_full), (q_loads - 1) & 1);
+        softmax_end:;
         } else if (warp >= 8 && warp < 12) {
             // ---------------- loads: warp 8 + p page p of every tile, in step
             reg_dec<C::kLoadRegs>();
@@ -1572,7 +1579,7 @@ bool encode_latents(CUtensorMap* map, const void* p, int64_t pages, bool fp8) {
 }
 
 template <int N, bool FP8>
-int launch_tiles(const LatentArgs& a, const CUtensorMap& tq, const CUtensorMap& tc, const CUtensorMap& tr, int ctas, cudaStream_t stream) {
+int launch_tiles(const LatentArgs& a, const CUtensorMap& tc, const CUtensorMap& tr, int ctas, cudaStream_t stream) {
     static std::atomic<bool> attr_set[64];
     const int st = once_per_device(attr_set, [] {
         return cudaFuncSetAttribute(latent_kernel<N, FP8>, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<N, FP8>::kSmem) ==
@@ -1581,7 +1588,7 @@ int launch_tiles(const LatentArgs& a, const CUtensorMap& tq, const CUtensorMap& 
                    : SV_ERR_CUDA;
     });
     if (st) return st;
-    return launch_pdl(latent_kernel<N, FP8>, dim3(ctas), dim3(Cfg<N, FP8>::kThreads), Cfg<N, FP8>::kSmem, stream, a, tq, tc, tr) ==
+    return launch_pdl(latent_kernel<N, FP8>, dim3(ctas), dim3(Cfg<N, FP8>::kThreads), Cfg<N, FP8>::kSmem, stream, a, tc, tr) ==
                    cudaSuccess
                ? SV_OK
                : SV_ERR_CUDA;
@@ -1629,9 +1636,8 @@ int launch_latent_attention(const sv_cache* c, const void* q, int num_q_heads, c
     a.cut_item = reinterpret_cast<int4*>(ws + lay.cut_item);
     a.odd = reinterpret_cast<uint32_t*>(ws + lay.odd);
     a.num_odd = reinterpret_cast<int*>(ws + lay.num_odd);
-    CUtensorMap tq, tc, tr;
-    if (!encode_rows(&tq, q, kQueryDim, static_cast<int64_t>(total_q) * num_q_heads, lay.tile_rows) ||
-        !encode_latents(&tc, c->k_pool, c->num_phys_pages, a.fp8) ||
+    CUtensorMap tc, tr;
+    if (!encode_latents(&tc, c->k_pool, c->num_phys_pages, a.fp8) ||
         !encode_rows(&tr, c->v_pool, kRopeDim, c->num_phys_pages * kPage, kPage))
         return SV_ERR_CUDA;
     if (a.planned && launch_pdl(latent_plan_kernel, dim3(1), dim3(kPlanThreads), 0, stream, a) != cudaSuccess) return SV_ERR_CUDA;
@@ -1639,13 +1645,13 @@ int launch_latent_attention(const sv_cache* c, const void* q, int num_q_heads, c
     const int ctas = groups * lay.share;
     int st;
     if (a.fp8)
-        st = lay.tile_rows == 16   ? launch_tiles<16, true>(a, tq, tc, tr, ctas, stream)
-             : lay.tile_rows == 32 ? launch_tiles<32, true>(a, tq, tc, tr, ctas, stream)
-                                   : launch_tiles<64, true>(a, tq, tc, tr, ctas, stream);
+        st = lay.tile_rows == 16   ? launch_tiles<16, true>(a, tc, tr, ctas, stream)
+             : lay.tile_rows == 32 ? launch_tiles<32, true>(a, tc, tr, ctas, stream)
+                                   : launch_tiles<64, true>(a, tc, tr, ctas, stream);
     else
-        st = lay.tile_rows == 16   ? launch_tiles<16, false>(a, tq, tc, tr, ctas, stream)
-             : lay.tile_rows == 32 ? launch_tiles<32, false>(a, tq, tc, tr, ctas, stream)
-                                   : launch_tiles<64, false>(a, tq, tc, tr, ctas, stream);
+        st = lay.tile_rows == 16   ? launch_tiles<16, false>(a, tc, tr, ctas, stream)
+             : lay.tile_rows == 32 ? launch_tiles<32, false>(a, tc, tr, ctas, stream)
+                                   : launch_tiles<64, false>(a, tc, tr, ctas, stream);
     if (st || groups < 2) return st;
     const int rows = lay.share * lay.tile_rows;
     return launch_pdl(latent_join_kernel, dim3(groups - 1, rows < 16 ? rows : 16), dim3(kJoinThreads), 0, stream, a) == cudaSuccess
