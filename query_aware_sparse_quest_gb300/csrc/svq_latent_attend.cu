@@ -36,7 +36,7 @@
 //   warps 8-11   load a page of the tile each: units of 64 tokens x 128 channels (16
 //                KB), each freed when its part of the second product is done, and
 //                rotary keys
-//   warps 12-15  (e4m3) widen the codes
+//   e4m3: the last four widen the codes; with 64 rows a CTA, warps 0 and 3 load, two pages of the tile each
 #include <climits>
 #include <type_traits>
 
@@ -75,12 +75,17 @@ struct Cfg {
     // Pairs of warps that widen a unit each, in turn.  (A pair sees every phase of the slots it reads: kCodes % kPairs is 0.)
     static constexpr int kPairs = 2, kWiden = 2 * kPairs;
     static_assert(kCodes % kPairs == 0, "code slots");
-    // Registers a thread: bf16 168 at launch, then 96 for the first four warps and the loads and 248 for the softmax
-    // (128 x (96 + 248 + 96) < 384 x 168); e4m3 128, then 72, 232, 64 and 128 (128 x (72 + 232 + 64 + 128) < 512 x 128).
-    // (The compiler keeps every role's code near the count at launch: with eight warps that widen, 640 threads of 96, the
-    // softmax takes half as long again, 7 requests' chunks 935 us for 800.)
-    static constexpr int kThreads = FP8 ? 512 : 384;
-    static constexpr int kMmaRegs = FP8 ? 72 : 96, kSoftmaxRegs = FP8 ? 232 : 248, kLoadRegs = FP8 ? 64 : 96, kWidenRegs = 128;
+    // Warps that load.  e4m3, 64 rows: the two that else idle, so that the threads are few; with fewer rows a tile is over
+    // too soon for two (32 requests of 16 heads 185 us, 165 with four; 7 requests' chunks 601 us, 625 with four).
+    static constexpr int kLoads = FP8 && N == 64 ? 2 : kPages;
+    // Registers a thread: 168 at launch, then 96 for the first four warps and the loads, 248 for the softmax and 128 for
+    // widening (128 x (96 + 248 + 128) < 384 x 168); e4m3 with four warps that load 128, then 72, 64, 232 and 128.  (The
+    // compiler keeps every role's code near the count at launch: with eight warps that widen, 640 threads of 96, the
+    // softmax took half as long again.)
+    static constexpr int kThreads = FP8 && kLoads == kPages ? 512 : 384;
+    static constexpr int kFirstWiden = kThreads / 32 - kWiden;
+    static constexpr int kMmaRegs = kThreads == 512 ? 72 : 96, kSoftmaxRegs = kThreads == 512 ? 232 : 248;
+    static constexpr int kLoadRegs = kThreads == 512 ? 64 : 96, kWidenRegs = 128;
     // Softmax warps that share 16 rows, kCols tokens each.  (Q's rows are repeated on the M side, so every warp's quarter
     // of TMEM holds its rows' logits.)
     static constexpr int kGroups = N / 16, kSplit = 4 / kGroups, kCols = kTok / kSplit;
@@ -324,8 +329,9 @@ __device__ __forceinline__ int warp_find_le(const int64_t* a, int n, int64_t v) 
 }
 
 // What an entry costs beside its tiles, in tiles, and the least share that is worth a CTA.
-constexpr int kEntryCost = 3, kMinShare = 4;
-__device__ __forceinline__ int cost_of_entry(int tiles) { return tiles ? tiles + kEntryCost : 0; }
+constexpr int kMinShare = 3;
+__host__ __device__ constexpr int entry_cost(int rows) { return rows == 64 ? 9 : 3; }
+__device__ __forceinline__ int cost_of_entry(int tiles, int rows) { return tiles ? tiles + entry_cost(rows) : 0; }
 // Groups of CTAs that share the work.
 __device__ __forceinline__ int groups_of(int64_t total, int most) {
     const int64_t n = (total + kMinShare - 1) / kMinShare;
@@ -334,8 +340,8 @@ __device__ __forceinline__ int groups_of(int64_t total, int most) {
 struct PlacedEntry {
     int64_t begin;
     int c0, c1;
-    __device__ __forceinline__ PlacedEntry(const Share& share, int64_t at, int n)
-        : begin(at), c0(share.cta_of(at + kEntryCost)), c1(share.cta_of(at + kEntryCost + n - 1)) {}
+    __device__ __forceinline__ PlacedEntry(const Share& share, int64_t at, int n, int rows)
+        : begin(at), c0(share.cta_of(at + entry_cost(rows))), c1(share.cta_of(at + entry_cost(rows) + n - 1)) {}
 };
 
 template <int N, bool FP8>
@@ -371,7 +377,7 @@ __global__ void __launch_bounds__(Cfg<N, FP8>::kThreads, 1)
         for (int i = 0; i < kInfoSlots; ++i) mbar_init(smem_addr(&ct->scale_full[i]), kPages);
         for (int i = 0; i < kSegs; ++i) {
             mbar_init(smem_addr(&ct->seg_full[i]), 1);
-            mbar_init(smem_addr(&ct->seg_empty[i]), kPages + 1 + 4 + (FP8 ? C::kWiden : 0));   // loads, MMAs, softmax, widening
+            mbar_init(smem_addr(&ct->seg_empty[i]), C::kLoads + 1 + 4 + (FP8 ? C::kWiden : 0));   // loads, MMAs, softmax, widening
         }
         mbar_init(smem_addr(&ct->s_full), 1);
         mbar_init(smem_addr(&ct->s_read), 4);
@@ -506,7 +512,7 @@ __global__ void __launch_bounds__(Cfg<N, FP8>::kThreads, 1)
             reg_dec<C::kMmaRegs>();
             int num_entries;
             int64_t total = 0;
-            auto own_cost = [&](int b) { return cost_of_entry((ct->lens[b] + kTok - 1) / kTok); };
+            auto own_cost = [&](int b) { return cost_of_entry((ct->lens[b] + kTok - 1) / kTok, N); };
             if (a.planned) {
                 num_entries = *a.num_entries;
                 total = *a.total;
@@ -587,7 +593,7 @@ __global__ void __launch_bounds__(Cfg<N, FP8>::kThreads, 1)
                         // The group after the one with an entry's first tile names the entry for the join.
                         int4 what = make_int4(0, 0, 0, 0), where = make_int4(0, 0, 0, 0);
                         if (go_on) {
-                            const PlacedEntry it(share, first - off, en.tiles);
+                            const PlacedEntry it(share, first - off, en.tiles, N);
                             if (group == it.c0 + 1) {
                                 what = make_int4(en.row0, en.nrows, it.c1 - it.c0 + 1, e);
                                 where.x = 2 * it.c0 + (share.start(it.c0) >= it.begin ? 0 : 1);
@@ -597,9 +603,9 @@ __global__ void __launch_bounds__(Cfg<N, FP8>::kThreads, 1)
                         a.cut_item[2 * group] = what;
                         a.cut_item[2 * group + 1] = where;
                     }
-                    const int64_t take = min(left, cost_of_entry(en.tiles) - off);
-                    t0 = static_cast<int>(max(static_cast<int64_t>(0), off - kEntryCost));
-                    t1 = static_cast<int>(max(static_cast<int64_t>(0), off + take - kEntryCost));
+                    const int64_t take = min(left, cost_of_entry(en.tiles, N) - off);
+                    t0 = static_cast<int>(max(static_cast<int64_t>(0), off - entry_cost(N)));
+                    t1 = static_cast<int>(max(static_cast<int64_t>(0), off + take - entry_cost(N)));
                     left -= take;
                     off += take;
                 }
@@ -627,7 +633,7 @@ __global__ void __launch_bounds__(Cfg<N, FP8>::kThreads, 1)
                     if (over) break;
                 }
                 first_item = false;
-                if (off == cost_of_entry(en.tiles)) {
+                if (off == cost_of_entry(en.tiles, N)) {
                     off = 0;
                     ++e;
                 }
@@ -1113,17 +1119,18 @@ __global__ void __launch_bounds__(Cfg<N, FP8>::kThreads, 1)
                 seg_done(k);
             }
         softmax_end:;
-        } else if (warp >= 8 && warp < 12) {
-            // ---------------- loads: warp 8 + p page p of every tile, in step
-            reg_dec<C::kLoadRegs>();
+        } else if (C::kLoads == 2 ? warp == 0 || warp == 3 : warp >= 8 && warp < 12) {
+            // ---------------- loads: warp 8 + p page p of every tile, in step; e4m3: of 64 rows: warps 0 and 3, two pages each
+            reg_dec<C::kLoads == 2 ? C::kMmaRegs : C::kLoadRegs>();
             const uint32_t go = elected();
-            const int p = warp - 8;
+            constexpr int kMine = kPages / C::kLoads;
+            const int p0 = C::kLoads == 2 ? (warp == 0 ? 0 : 2) : warp - 8;
             uint32_t tile = 0, loaded = 0;
             constexpr uint32_t kDepth = FP8 ? (C::kCodes ? C::kCodes : 1) : C::kRing;
             constexpr uint32_t kPageBytes = kPage * (FP8 ? 128 : 256);   // of a unit
             uint64_t* const empty = FP8 ? ct->code_empty : ct->empty;
-            const uint32_t to = smem_addr(FP8 ? codes : ring) + p * kPageBytes;
-            const uint32_t rope_to = smem_addr(ropes) + p * (kPage * kRopeDim * 2);
+            const uint32_t to = smem_addr(FP8 ? codes : ring) + p0 * kPageBytes;
+            const uint32_t rope_to = smem_addr(ropes) + p0 * (kPage * kRopeDim * 2);
             for (uint32_t k = 0;; ++k) {
                 TEST_WAIT(ct->seg_full[k % kSegs], (k / kSegs) & 1, loads_end);
                 const Seg& s = ct->seg[k % kSegs];
@@ -1131,35 +1138,43 @@ __global__ void __launch_bounds__(Cfg<N, FP8>::kThreads, 1)
                 if (n == 0) break;
                 const int end = min(s.en.npages, s.t1 * kPages);
                 const int32_t* const pages = a.page_table + static_cast<int64_t>(s.en.req) * a.max_pages;
-                // Lane l resolves the page of tile i + l, well before the loads that need it: -2 behind the last page, -1
+                // Lane l resolves the pages of tile i + l, well before the loads that need them: -2 behind the last page, -1
                 // what the table does not give.
-                auto fetch = [&](int i0) {
-                    const int i = (t0 + i0 + lane) * kPages + p;
+                auto fetch = [&](int i0, int p) {
+                    const int i = (t0 + i0 + lane) * kPages + p0 + p;
                     if (i0 + lane >= n || i >= end) return -2;
                     const int ph = pages[i];
                     return ph < 0 || ph >= a.num_pages ? -1 : ph;
                 };
-                int cur = -2, nxt = fetch(0);
+                int cur[kMine], nxt[kMine];
+#pragma unroll
+                for (int p = 0; p < kMine; ++p) nxt[p] = fetch(0, p);
                 for (int i = 0; i < n; ++i, ++tile) {
                     if (i % 32 == 0) {
-                        cur = nxt;
-                        if (i + 32 < n) nxt = fetch(i + 32);
+#pragma unroll
+                        for (int p = 0; p < kMine; ++p) {
+                            cur[p] = nxt[p];
+                            if (i + 32 < n) nxt[p] = fetch(i + 32, p);
+                        }
                     }
-                    const int ph = uniform(__shfl_sync(0xffffffffu, cur, i % 32));
-                    const uint32_t on = ph >= 0 ? go : 0u;
                     const uint32_t slot = tile % kInfoSlots;
-                    if (go) {
-                        if (ph == -1) svq_flag(SV_DEVERR_PAGE_TABLE);
-                        ct->fault[slot][p] = ph == -1;
-                    }
-                    if (FP8) {
-                        const uint32_t bar = smem_addr(&ct->scale_full[slot]);
+                    int ph[kMine];
+#pragma unroll
+                    for (int p = 0; p < kMine; ++p) {
+                        ph[p] = uniform(__shfl_sync(0xffffffffu, cur[p], i % 32));
                         if (go) {
-                            if (ph >= 0) {
-                                mbar_arrive_expect_tx(bar, kPage * 4);
-                                bulk_copy_g2s(smem_addr(scales + slot * kTok + p * kPage), a.scale + static_cast<int64_t>(ph) * kPage, kPage * 4, bar);
-                            } else {
-                                mbar_arrive(bar);
+                            if (ph[p] == -1) svq_flag(SV_DEVERR_PAGE_TABLE);
+                            ct->fault[slot][p0 + p] = ph[p] == -1;
+                        }
+                        if (FP8) {
+                            const uint32_t bar = smem_addr(&ct->scale_full[slot]);
+                            if (go) {
+                                if (ph[p] >= 0) {
+                                    mbar_arrive_expect_tx(bar, kPage * 4);
+                                    bulk_copy_g2s(smem_addr(scales + slot * kTok + (p0 + p) * kPage), a.scale + static_cast<int64_t>(ph[p]) * kPage, kPage * 4, bar);
+                                } else {
+                                    mbar_arrive(bar);
+                                }
                             }
                         }
                     }
@@ -1168,24 +1183,31 @@ __global__ void __launch_bounds__(Cfg<N, FP8>::kThreads, 1)
                         const uint32_t at = tile * kUnits + u, st = at % kDepth;
                         TEST_WAIT(empty[st], ((at / kDepth) & 1) ^ 1, loads_end);
                         const uint32_t bar = smem_addr(FP8 ? &ct->code_full[st] : &ct->full[st]);
-                        if (go) {
-                            if (ph >= 0) mbar_arrive_expect_tx(bar, kPageBytes);
-                            else mbar_arrive(bar);
+#pragma unroll
+                        for (int p = 0; p < kMine; ++p) {
+                            const uint32_t on = ph[p] >= 0 ? go : 0u, dst = to + st * (kPageBytes * kPages) + p * kPageBytes;
+                            if (go) {
+                                if (ph[p] >= 0) mbar_arrive_expect_tx(bar, kPageBytes);
+                                else mbar_arrive(bar);
+                            }
+                            __syncwarp();
+                            if (FP8) tma_2d_if(on, dst, &tmap_c, u * 128, ph[p] * kPage, bar);
+                            else tma_page_if(on, dst, &tmap_c, 2 * u, 2 * ph[p], bar);
                         }
-                        __syncwarp();
-                        if (FP8) tma_2d_if(on, to + st * (kPageBytes * kPages), &tmap_c, u * 128, ph * kPage, bar);
-                        else tma_page_if(on, to + st * (kPageBytes * kPages), &tmap_c, 2 * u, 2 * ph, bar);
                         loaded = at + 1;
                     }
                     const uint32_t st = tile % C::kRope;
                     TEST_WAIT(ct->rope_empty[st], ((tile / C::kRope) & 1) ^ 1, loads_end);
                     const uint32_t bar = smem_addr(&ct->rope_full[st]);
-                    if (go) {
-                        if (ph >= 0) mbar_arrive_expect_tx(bar, kPage * kRopeDim * 2);
-                        else mbar_arrive(bar);
+#pragma unroll
+                    for (int p = 0; p < kMine; ++p) {
+                        if (go) {
+                            if (ph[p] >= 0) mbar_arrive_expect_tx(bar, kPage * kRopeDim * 2);
+                            else mbar_arrive(bar);
+                        }
+                        __syncwarp();
+                        tma_2d_if(ph[p] >= 0 ? go : 0u, rope_to + st * kRopeBytes + p * (kPage * kRopeDim * 2), &tmap_r, 0, ph[p] * kPage, bar);
                     }
-                    __syncwarp();
-                    tma_2d_if(on, rope_to + st * kRopeBytes, &tmap_r, 0, ph * kPage, bar);
                 }
                 seg_done(k);
             }
@@ -1198,10 +1220,10 @@ __global__ void __launch_bounds__(Cfg<N, FP8>::kThreads, 1)
                 (void)bar_wait(smem_addr(&ct->rope_full[x % C::kRope]), (x / C::kRope) & 1);
             if (FP8) (void)bar_wait(smem_addr(&ct->scale_full[tile % kInfoSlots]), (tile / kInfoSlots) & 1);
         loads_done:;
-        } else if (FP8 && warp >= 12) {
+        } else if (FP8 && warp >= C::kFirstWiden) {
             // ---------------- e4m3 codes -> fp16 units in the MMAs' layout, two warps a unit
             reg_dec<C::kWidenRegs>();
-            const int tid = threadIdx.x & 63, mine = (warp - 12) >> 1;
+            const int tid = threadIdx.x & 63, mine = (warp - C::kFirstWiden) >> 1;
             uint32_t at = mine, until = 0;
             constexpr uint32_t kDepth = FP8 ? C::kCodes : 1;
             for (uint32_t k = 0;; ++k) {
@@ -1314,7 +1336,7 @@ __global__ void __launch_bounds__(kPlanThreads) latent_plan_kernel(const __grid_
             empty = len == 0;
         }
         en.tiles = (en.npages + kPages - 1) / kPages;
-        const int64_t before = base + block_scan(cost_of_entry(en.tiles), warp_sums, total);
+        const int64_t before = base + block_scan(cost_of_entry(en.tiles, a.tile_rows), warp_sums, total);
         base += total;
         if (e < n) {
             a.entries[e] = en;
