@@ -219,6 +219,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
     }
     pdl_wait();
+    pdl_launch_dependents();   // the join, which waits
     tc_fence_before();
     __syncthreads();
     tc_fence_after();

@@ -397,6 +397,7 @@ __global__ void __launch_bounds__(Cfg<N, FP8>::kThreads, 1)
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
     }
     pdl_wait();
+    pdl_launch_dependents();   // the join, which waits (where SMs are free for it, or at once when they are)
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -578,9 +579,9 @@ __global__ void __launch_bounds__(Cfg<N, FP8>::kThreads, 1)
                 const int pages = (ct->lens[e] + kPage - 1) / kPage;
                 return Entry{e * a.heads, a.heads, ct->lens[e] - e - 1, e, pages, (pages + kPages - 1) / kPages, {0, 0}};
             };
-            const bool go_on = off > 0;      // the share begins inside an entry
+            const int64_t into = off;        // (where the share begins inside its first entry)
             if (left <= 0 && lane == 0 && part == 0) a.cut_item[2 * group] = make_int4(0, 0, 0, 0);
-            bool first_item = true;
+            bool first_item = true, name = left > 0;
             Entry en = {};
             for (uint32_t k = 0;;) {
                 int t0 = 0, t1 = 0;
@@ -589,20 +590,6 @@ __global__ void __launch_bounds__(Cfg<N, FP8>::kThreads, 1)
                         do en = entry(e);   // (entries without tiles: rows that see nothing)
                         while (en.tiles == 0 && ++e < num_entries);
                     }
-                    if (first_item && lane == 0 && part == 0) {
-                        // The group after the one with an entry's first tile names the entry for the join.
-                        int4 what = make_int4(0, 0, 0, 0), where = make_int4(0, 0, 0, 0);
-                        if (go_on) {
-                            const PlacedEntry it(share, first - off, en.tiles, N);
-                            if (group == it.c0 + 1) {
-                                what = make_int4(en.row0, en.nrows, it.c1 - it.c0 + 1, e);
-                                where.x = 2 * it.c0 + (share.start(it.c0) >= it.begin ? 0 : 1);
-                                where.y = 2 * (it.c0 + 1);
-                            }
-                        }
-                        a.cut_item[2 * group] = what;
-                        a.cut_item[2 * group + 1] = where;
-                    }
                     const int64_t take = min(left, cost_of_entry(en.tiles, N) - off);
                     t0 = static_cast<int>(max(static_cast<int64_t>(0), off - entry_cost(N)));
                     t1 = static_cast<int>(max(static_cast<int64_t>(0), off + take - entry_cost(N)));
@@ -610,6 +597,7 @@ __global__ void __launch_bounds__(Cfg<N, FP8>::kThreads, 1)
                     off += take;
                 }
                 const int rows = min(N, en.nrows - part * N);
+                bool over = false;   // the last one
                 if ((t1 > t0 && rows > 0) || left <= 0) {
                     for (int round = 0;; ++round) {
                         if (!__any_sync(0xffffffffu, !bar_wait(smem_addr(&ct->seg_empty[k % kSegs]), ((k / kSegs) & 1) ^ 1))) break;
@@ -618,7 +606,7 @@ __global__ void __launch_bounds__(Cfg<N, FP8>::kThreads, 1)
                             goto plan_end;
                         }
                     }
-                    const bool over = t1 == t0 || rows <= 0;   // (the last one)
+                    over = t1 == t0 || rows <= 0;
                     if (lane == 0) {
                         Seg& s = ct->seg[k % kSegs];
                         s.en = en;
@@ -630,9 +618,23 @@ __global__ void __launch_bounds__(Cfg<N, FP8>::kThreads, 1)
                         mbar_arrive(smem_addr(&ct->seg_full[k % kSegs]));
                     }
                     ++k;
-                    if (over) break;
                 }
-                first_item = false;
+                if (name && lane == 0 && part == 0) {
+                    // The group after the one with an entry's first tile names the entry for the join.
+                    int4 what = make_int4(0, 0, 0, 0), where = make_int4(0, 0, 0, 0);
+                    if (into > 0) {
+                        const PlacedEntry it(share, first - into, en.tiles, N);
+                        if (group == it.c0 + 1) {
+                            what = make_int4(en.row0, en.nrows, it.c1 - it.c0 + 1, e);
+                            where.x = 2 * it.c0 + (share.start(it.c0) >= it.begin ? 0 : 1);
+                            where.y = 2 * (it.c0 + 1);
+                        }
+                    }
+                    a.cut_item[2 * group] = what;
+                    a.cut_item[2 * group + 1] = where;
+                }
+                if (over) break;
+                first_item = name = false;
                 if (off == cost_of_entry(en.tiles, N)) {
                     off = 0;
                     ++e;
@@ -1492,17 +1494,18 @@ __global__ void __launch_bounds__(kJoinThreads) latent_join_kernel(const __grid_
         };
         float m = -INFINITY, l = 0.f, lr = 0.f;
         float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-        for (int k0 = 0; k0 < pieces; k0 += 4) {
-            float4 ml[4], x[4];
+        constexpr int kAhead = 8;   // pieces on their way at a time
+        for (int k0 = 0; k0 < pieces; k0 += kAhead) {
+            float4 ml[kAhead], x[kAhead];
 #pragma unroll
-            for (int u = 0; u < 4; ++u) {
+            for (int u = 0; u < kAhead; ++u) {
                 const bool on = k0 + u < pieces;
                 ml[u] = on ? a.cut_ml[row_of(k0 + u)] : make_float4(-INFINITY, 0.f, 0.f, 0.f);
                 x[u] = on ? *reinterpret_cast<const float4*>(a.cut_o + row_of(k0 + u) * kLatentDim + 4 * tid) : make_float4(0.f, 0.f, 0.f, 0.f);
             }
             float mn = m;
 #pragma unroll
-            for (int u = 0; u < 4; ++u) mn = fmaxf(mn, ml[u].x);
+            for (int u = 0; u < kAhead; ++u) mn = fmaxf(mn, ml[u].x);
             const float base = mn == -INFINITY ? 0.f : mn;   // pieces without a visible token: weights 0
             const float e = ex2(m - base);
             m = mn;
@@ -1510,7 +1513,7 @@ __global__ void __launch_bounds__(kJoinThreads) latent_join_kernel(const __grid_
             lr *= e;
             o.x *= e, o.y *= e, o.z *= e, o.w *= e;
 #pragma unroll
-            for (int u = 0; u < 4; ++u) {
+            for (int u = 0; u < kAhead; ++u) {
                 const float f = ex2(ml[u].x - base);
                 l = fmaf(ml[u].y, f, l);
                 lr = fmaf(ml[u].z, f, lr);
@@ -1663,7 +1666,11 @@ int launch_latent_attention(const sv_cache* c, const void* q, int num_q_heads, c
         !encode_rows(&tr, c->v_pool, kRopeDim, c->num_phys_pages * kPage, kPage))
         return SV_ERR_CUDA;
     if (a.planned && launch_pdl(latent_plan_kernel, dim3(1), dim3(kPlanThreads), 0, stream, a) != cudaSuccess) return SV_ERR_CUDA;
-    const int groups = (sm_count < kMaxCtas ? sm_count : kMaxCtas) / lay.share;
+    // No more groups than the longest requests that the table can name could use.
+    const int64_t cost = (max_pages + kPages - 1) / kPages + static_cast<int64_t>(entry_cost(lay.tile_rows));
+    const int64_t most = (cost * (a.planned ? lay.max_entries : batch) + kMinShare - 1) / kMinShare;
+    const int fit = (sm_count < kMaxCtas ? sm_count : kMaxCtas) / lay.share;
+    const int groups = most < fit ? static_cast<int>(most) : fit;
     const int ctas = groups * lay.share;
     int st;
     if (a.fp8)
