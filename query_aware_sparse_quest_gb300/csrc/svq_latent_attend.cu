@@ -1683,7 +1683,7 @@ int launch_latent_attention(const sv_cache* c, const void* q, int num_q_heads, c
                                    : launch_tiles<64, false>(a, tc, tr, ctas, stream);
     if (st || groups < 2) return st;
     const int rows = lay.share * lay.tile_rows;
-    return launch_pdl(latent_join_kernel, dim3(groups - 1, rows < 16 ? rows : 16), dim3(kJoinThreads), 0, stream, a) == cudaSuccess
+    return launch_pdl(latent_join_kernel, dim3(groups - 1, rows < 64 ? rows : 64), dim3(kJoinThreads), 0, stream, a) == cudaSuccess
                ? SV_OK
                : SV_ERR_CUDA;
 }
