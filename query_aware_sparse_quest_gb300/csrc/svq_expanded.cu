@@ -219,7 +219,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
     }
     pdl_wait();
-    pdl_launch_dependents();   // the join, which waits
+    if (gridDim.x > 1) pdl_launch_dependents();   // the join, which waits (without one: the next call, which may not)
     tc_fence_before();
     __syncthreads();
     tc_fence_after();

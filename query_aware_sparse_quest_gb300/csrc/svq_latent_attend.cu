@@ -397,7 +397,8 @@ __global__ void __launch_bounds__(Cfg<N, FP8>::kThreads, 1)
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
     }
     pdl_wait();
-    pdl_launch_dependents();   // the join, which waits (where SMs are free for it, or at once when they are)
+    // The join, which waits.  (Without one the next call's kernels are the dependents: some read their inputs at once.)
+    if (gridDim.x > static_cast<unsigned>(a.share)) pdl_launch_dependents();
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -859,8 +860,8 @@ __global__ void __launch_bounds__(Cfg<N, FP8>::kThreads, 1)
                             unpack2(e0, y[0], y[1]);
                             unpack2(e1, y[2], y[3]);
                             if (FP8) {
-                                big0 = fmaxf(big0, fmaxf(y[0], y[1]));
-                                big1 = fmaxf(big1, fmaxf(y[2], y[3]));
+                                big0 = fmaxf(big0, fmaxf(fabsf(y[0]), fabsf(y[1])));
+                                big1 = fmaxf(big1, fmaxf(fabsf(y[2]), fabsf(y[3])));
                             }
                             p[c][0] = FP8 ? pack_f16x2(y[0], y[1]) : pack_bf16x2(y[0], y[1]);
                             p[c][1] = FP8 ? pack_f16x2(y[2], y[3]) : pack_bf16x2(y[2], y[3]);

@@ -109,6 +109,17 @@ def test_long_and_many(heads, lens, sizes, fp8):
 
 
 @pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("batch", [256, 257, 300])
+def test_single_tokens_of_many_requests(batch, fp8):
+    """Up to 256 requests every CTA plans for itself, behind that a kernel does; some have no tokens."""
+    lens = [(7 * i) % 50 for i in range(batch)]
+    case = LatentCase(lens, fp8=fp8, seed=6)
+    q = queries(batch, 2, seed=6)
+    out, lse = call(case, q)
+    check_all(case, q, [1] * batch, out, lse)
+
+
+@pytest.mark.parametrize("fp8", [False, True])
 def test_logits_of_any_size(fp8):
     """Weights that are all equal, that fall on one token, and that grow along the row."""
     case = LatentCase([1000, 1000, 1000], fp8=fp8, seed=2, mean=1.0)
@@ -130,6 +141,33 @@ def test_latents_of_any_scale(fp8):
         q[..., :LATENT] /= scale
         out, lse = call(case, q)
         check_all(case, q, [1, 1], out, lse)
+
+
+@pytest.mark.parametrize("heads", [1, 16, 20, 128])
+def test_scales_of_one_request_far_apart(heads):
+    """Tokens whose scales are up to 2^60 apart, and tiles of zero tokens (scale 0) before the first other one.
+
+    A token's weight times its scale is rounded to fp16 in a unit that is at most the largest of the row: below 2^-14 of
+    that the rounding is off by up to 2^-25 of it, whatever the product, which comes on top of the bounds of `attend`."""
+    lens = [300, 130, 200]
+    case = LatentCase(lens, fp8=True, seed=5)
+    g = torch.Generator().manual_seed(9)
+    case.scale *= torch.exp2(torch.randint(-30, 31, case.scale.shape, generator=g).float())
+    for t in range(140):
+        page = case.table[2, t // PAGE]
+        case.latent[page, t % PAGE], case.scale[page, t % PAGE] = 0, 0.0
+    q = queries(3, heads)
+    q[..., :LATENT] *= 2.0 ** -32                # the largest scales' logits are of the rotary part's size
+    out, lse = call(case, q)
+    for b, n in enumerate(lens):
+        o, l, tol, tol_lse = reference(case, q, [1, 1, 1], b)
+        page = case.table[b, : -(-n // PAGE)].long()
+        size = case.scale[page].flatten()[:n].double().to(DEV)
+        codes = case.latent[page].flatten(0, 1)[:n].to(DEV).view(torch.float8_e4m3fn).double().abs()
+        c, r = case.tokens(b)
+        z = (q[b].double() @ torch.cat((c, r), 1).T) * SCALE
+        largest = (torch.exp(z - l[0][:, None]) * size).amax(1)
+        check(out[b:b + 1], lse[b:b + 1], (o, l, tol + 2.0 ** -25 * largest[None, :, None] * codes.sum(0), tol_lse))
 
 
 @pytest.mark.parametrize("fp8", [False, True])
