@@ -64,31 +64,30 @@ constexpr float kBig = 256.f;                       // e4m3: weights times scale
 // Key tiles after which O moves into fp32 sums and starts again from zero: the MMAs cut their sums off at fp32's last
 // bit, four times a tile, always towards zero (values of one sign lose 2^-21.4 of their sum a tile).
 constexpr int kFoldTiles = 1024;
-constexpr int kControlBytes = 3072;
 constexpr int kMaxRows = 64;                        // rows of a CTA's tile at most
 
 template <int N, bool FP8>
 struct Cfg {
     static constexpr int kRing = FP8 ? (N == 64 ? 8 : 10) : (N == 64 ? 11 : 12);           // units: two tiles at least
     static constexpr int kRope = 2;                                        // rotary tiles
-    static constexpr int kCodes = FP8 ? (N == 64 ? 2 : 4) : 0;             // units of codes, 8 KB
-    // Pairs of warps that widen a unit each, in turn.  (A pair sees every phase of the slots it reads: kCodes % kPairs is 0.)
-    static constexpr int kPairs = 2, kWiden = 2 * kPairs;
-    static_assert(kCodes % kPairs == 0, "code slots");
-    // Warps that load.  e4m3, 64 rows: the two that else idle, so that the threads are few; with fewer rows a tile is over
-    // too soon for two (32 requests of 16 heads 185 us, 165 with four; 7 requests' chunks 601 us, 625 with four).
+    static constexpr int kCodes = FP8 ? (N == 64 ? 3 : 4) : 0;             // units of codes, 8 KB
+    static constexpr int kWiden = 4;                                       // warps that widen, all of a unit
+    // Warps that load.  e4m3, 64 rows: the two that else idle, and eight softmax warps; with fewer rows a tile is over too
+    // soon for two (32 requests of 16 heads 185 us, 165 with four).
     static constexpr int kLoads = FP8 && N == 64 ? 2 : kPages;
-    // Registers a thread: 168 at launch, then 96 for the first four warps and the loads, 248 for the softmax and 128 for
-    // widening (128 x (96 + 248 + 128) < 384 x 168); e4m3 with four warps that load 128, then 72, 64, 232 and 128.  (The
-    // compiler keeps every role's code near the count at launch: with eight warps that widen, 640 threads of 96, the
-    // softmax took half as long again.)
-    static constexpr int kThreads = FP8 && kLoads == kPages ? 512 : 384;
+    static constexpr int kSoft = FP8 && N == 64 ? 8 : 4;
+    // Registers a thread: bf16 168 at launch, then 96 for the first four warps and the loads and 248 for the softmax
+    // (128 x (96 + 248 + 96) < 384 x 168); e4m3 128, then 72, 64, 232 and 128 for widening, or with eight softmax warps 96,
+    // 160 (twice) and 96.  (The compiler keeps every role's code near the count at launch: with eight warps that widen, 640
+    // threads of 96, the softmax took half as long again.)
+    static constexpr int kThreads = FP8 ? 512 : 384;
     static constexpr int kFirstWiden = kThreads / 32 - kWiden;
-    static constexpr int kMmaRegs = kThreads == 512 ? 72 : 96, kSoftmaxRegs = kThreads == 512 ? 232 : 248;
-    static constexpr int kLoadRegs = kThreads == 512 ? 64 : 96, kWidenRegs = 128;
+    static constexpr int kMmaRegs = FP8 && kSoft == 4 ? 72 : 96, kSoftmaxRegs = !FP8 ? 248 : (kSoft == 4 ? 232 : 160);
+    static constexpr int kLoadRegs = FP8 && kSoft == 4 ? 64 : 96, kWidenRegs = kSoft == 4 ? 128 : 96;
     // Softmax warps that share 16 rows, kCols tokens each.  (Q's rows are repeated on the M side, so every warp's quarter
     // of TMEM holds its rows' logits.)
-    static constexpr int kGroups = N / 16, kSplit = 4 / kGroups, kCols = kTok / kSplit;
+    static constexpr int kGroups = N / 16, kSplit = kSoft / kGroups, kCols = kTok / kSplit;
+    static constexpr int kControl = FP8 ? 4096 : 3072;
     // TMEM columns: O^T of channels 128 m .. at m N, then S (e4m3: its latent and its rotary part), then the first
     // kQUnits units of Q's channels, two a column.  The others and the rotary ones are in shared memory.
     static constexpr int kSCols = FP8 ? 2 * kTok : kTok;
@@ -98,7 +97,7 @@ struct Cfg {
     static constexpr int kQ = kQBlocks * kBlockQ;
     static constexpr int kP = N * kTok * 2;
     static constexpr int kScales = FP8 ? kInfoSlots * kTok * 4 : 0;
-    static constexpr int kSmem = kRing * kUnit + kRope * kRopeBytes + kCodes * (kUnit / 2) + kQ + kP + kScales + kControlBytes;
+    static constexpr int kSmem = kRing * kUnit + kRope * kRopeBytes + kCodes * (kUnit / 2) + kQ + kP + kScales + kControl;
     static_assert(kSmem <= 227 * 1024, "shared memory of one CTA");
 };
 
@@ -250,13 +249,15 @@ __device__ __forceinline__ void tma_2d_if(uint32_t go, uint32_t dst, const void*
         : "memory");
 }
 // The softmax warps' barrier.
-__device__ __forceinline__ void softmax_sync() { asm volatile("barrier.cta.sync 1, 128;" ::: "memory"); }
+template <int WARPS>
+__device__ __forceinline__ void softmax_sync() { asm volatile("barrier.cta.sync 1, %0;" ::"n"(32 * WARPS) : "memory"); }
+template <int WARPS>
 __device__ __forceinline__ bool softmax_any(bool mine) {
     uint32_t any;
     asm volatile(
-        "{\n\t.reg .pred p, r;\n\tsetp.ne.u32 p, %1, 0;\n\tbarrier.cta.red.or.pred r, 1, 128, p;\n\tselp.u32 %0, 1, 0, r;\n\t}"
+        "{\n\t.reg .pred p, r;\n\tsetp.ne.u32 p, %1, 0;\n\tbarrier.cta.red.or.pred r, 1, %2, p;\n\tselp.u32 %0, 1, 0, r;\n\t}"
         : "=r"(any)
-        : "r"(static_cast<uint32_t>(mine))
+        : "r"(static_cast<uint32_t>(mine)), "n"(32 * WARPS)
         : "memory");
     return any != 0;
 }
@@ -282,6 +283,7 @@ constexpr int kSegs = 4;
 // kernel before takes 3 us; one request of 4096 tokens 25.5 -> 22 us).
 constexpr int kOwnPlan = 256;
 
+template <int SOFT, bool FP8>   // softmax warps
 struct Control {
     uint64_t full[12], empty[12];          // units
     uint64_t rope_full[2], rope_empty[2];
@@ -298,15 +300,16 @@ struct Control {
     // Rows' maxima of the warps that share them, and at a segment's end their sums.
     union {
         struct {
-            float top[kMaxRows], big[kMaxRows];
+            float top[16 * SOFT], big[16 * SOFT];
         };
-        float2 sum[kMaxRows];
+        float2 sum[16 * SOFT];
     };
+    float unit[FP8 ? kMaxRows : 1];        // e4m3: of the rows of Q
     alignas(16) float alpha[kMaxRows], factor[kMaxRows];   // of a row's O: where its base moves, and at a segment's end
 };
-static_assert(sizeof(Control) <= kControlBytes, "control block");
 
-__device__ __forceinline__ void gave_up(Control* ct) {
+template <int SOFT, bool FP8>
+__device__ __forceinline__ void gave_up(Control<SOFT, FP8>* ct) {
     svq_flag(SV_DEVERR_TIMEOUT);
     *static_cast<volatile int*>(&ct->gave_up) = 1;
 }
@@ -356,14 +359,16 @@ __global__ void __launch_bounds__(Cfg<N, FP8>::kThreads, 1)
     unsigned char* const qs = codes + C::kCodes * (kUnit / 2);
     unsigned char* const ps = qs + C::kQ;
     float* const scales = reinterpret_cast<float*>(ps + C::kP);
-    Control* const ct = reinterpret_cast<Control*>(ps + C::kP + C::kScales);
+    using Ctrl = Control<C::kSoft, FP8>;
+    static_assert(sizeof(Ctrl) <= C::kControl, "control block");
+    Ctrl* const ct = reinterpret_cast<Ctrl*>(ps + C::kP + C::kScales);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int part = blockIdx.x % a.share, group = blockIdx.x / a.share;
 
     if (threadIdx.x == 0) {
         ct->gave_up = 0;
         for (int i = 0; i < C::kRing; ++i) {
-            mbar_init(smem_addr(&ct->full[i]), FP8 ? 2 : kPages);
+            mbar_init(smem_addr(&ct->full[i]), FP8 ? C::kWiden : kPages);
             mbar_init(smem_addr(&ct->empty[i]), 1);
         }
         for (int i = 0; i < C::kRope; ++i) {
@@ -372,19 +377,19 @@ __global__ void __launch_bounds__(Cfg<N, FP8>::kThreads, 1)
         }
         for (int i = 0; i < C::kCodes; ++i) {
             mbar_init(smem_addr(&ct->code_full[i]), kPages);
-            mbar_init(smem_addr(&ct->code_empty[i]), 2);
+            mbar_init(smem_addr(&ct->code_empty[i]), C::kWiden);
         }
         for (int i = 0; i < kInfoSlots; ++i) mbar_init(smem_addr(&ct->scale_full[i]), kPages);
         for (int i = 0; i < kSegs; ++i) {
             mbar_init(smem_addr(&ct->seg_full[i]), 1);
-            mbar_init(smem_addr(&ct->seg_empty[i]), C::kLoads + 1 + 4 + (FP8 ? C::kWiden : 0));   // loads, MMAs, softmax, widening
+            mbar_init(smem_addr(&ct->seg_empty[i]), C::kLoads + 1 + C::kSoft + (FP8 ? C::kWiden : 0));   // loads, MMAs, softmax, widening
         }
         mbar_init(smem_addr(&ct->s_full), 1);
-        mbar_init(smem_addr(&ct->s_read), 4);
-        mbar_init(smem_addr(&ct->p_full), 4);
+        mbar_init(smem_addr(&ct->s_read), C::kSoft);
+        mbar_init(smem_addr(&ct->p_full), C::kSoft);
         mbar_init(smem_addr(&ct->pv_done), 1);
         mbar_init(smem_addr(&ct->q_full), 4);
-        mbar_init(smem_addr(&ct->vote), 4);
+        mbar_init(smem_addr(&ct->vote), C::kSoft);
         for (int i = 0; i < 4; ++i) ct->over[i] = 0;
         mbar_init(smem_addr(&ct->drain), 1);
         mbar_init_fence();
@@ -650,7 +655,7 @@ __global__ void __launch_bounds__(Cfg<N, FP8>::kThreads, 1)
                 for (int i = lane; i < a.heads * (kLatentDim / 8); i += 32) o[i] = make_uint4(0u, 0u, 0u, 0u);
                 for (int i = lane; i < a.heads; i += 32) a.lse[r0 + i] = -INFINITY;
             }
-        } else if (warp >= 4 && warp < 8) {
+        } else if (warp >= 4 && warp < 4 + C::kSoft) {
             // ---------------- softmax: warp w rows 16 (w % kGroups) .. and kCols tokens from tok0 on, lane l rows l / 4 and
             // + 8 of those and tokens 8 c + 2 (l % 4), + 1
             constexpr int kC = C::kCols / 8;
@@ -658,14 +663,17 @@ __global__ void __launch_bounds__(Cfg<N, FP8>::kThreads, 1)
             const int w = warp - 4, tid = threadIdx.x - 128;
             const int rg = w % C::kGroups, tp = w / C::kGroups, tok0 = tp * C::kCols;
             const int quad = lane & 3;
-            const uint32_t lanes = static_cast<uint32_t>(w * 32) << 16;
+            const uint32_t lanes = static_cast<uint32_t>((w & 3) * 32) << 16;
+            // O^T's columns from first_col on are this warp's to scale and to write, its channels 128 u + chan.
+            constexpr int kOCols = 4 * N / (C::kSoft / 4);
+            const int first_col = (w >> 2) * kOCols, chan = tid & 127;
             uint32_t tile = 0;
             bool dead = false;   // a wait of this warp's ran out
             // Q of a segment's rows: the first units to TMEM, where row r is lane 32 (r / 16) + r % 16, the rest to shared
             // memory.  Eight lanes read a row, rows 4 i + lane / 8 and chunks of 8 channels (a row a lane would touch 32
             // lines a load), and the way to TMEM leads through the warp's rows of the last block.
-            float qs0 = 1.f, qs1 = 1.f;   // e4m3: what the lane's rows of Q are in units of
             auto load_q = [&](const Seg& g) {
+                if (w >= 4) return;   // (the first four)
                 if (16 * rg < g.en.nrows) {
                     constexpr int kBlocks = kQueryDim / 64;
                     const uint4* from[4];
@@ -683,7 +691,6 @@ __global__ void __launch_bounds__(Cfg<N, FP8>::kThreads, 1)
                                 const uint4 v = from[i][8 * c];
                                 top[i] = __vmaxu2(top[i], __vmaxu2(__vmaxu2(v.x & 0x7f807f80u, v.y & 0x7f807f80u), __vmaxu2(v.z & 0x7f807f80u, v.w & 0x7f807f80u)));
                             }
-                        float of[4];
 #pragma unroll
                         for (int i = 0; i < 4; ++i) {
                             uint32_t t = max(top[i] >> 16, top[i] & 0xffffu);
@@ -691,11 +698,8 @@ __global__ void __launch_bounds__(Cfg<N, FP8>::kThreads, 1)
                             for (int d = 1; d < 8; d <<= 1) t = max(t, __shfl_xor_sync(0xffffffffu, t, d));
                             const int up = max(static_cast<int>(min(t >> 7, 254u)) - 127 - kQueryTop, -126);
                             shrink[i] = __uint_as_float(static_cast<uint32_t>(127 - up) << 23);
-                            of[i] = __shfl_sync(0xffffffffu, __uint_as_float(static_cast<uint32_t>(127 + up) << 23), 8 * ((lane >> 2) & 3));
+                            if ((lane & 7) == 0) ct->unit[16 * w + 4 * i + (lane >> 3)] = __uint_as_float(static_cast<uint32_t>(127 + up) << 23);
                         }
-                        // (Row l / 4 is held as i = l / 16, row l / 4 + 8 as i + 2.)
-                        qs0 = lane & 16 ? of[1] : of[0];
-                        qs1 = lane & 16 ? of[3] : of[2];
                     }
                     constexpr int kBatch = 5;   // blocks on their way at a time
                     unsigned char* const to = qs + w * 2048, * const way = to + (C::kQBlocks - 1) * kBlockQ;
@@ -744,14 +748,16 @@ __global__ void __launch_bounds__(Cfg<N, FP8>::kThreads, 1)
                 const Seg& s = ct->seg[k % kSegs];
                 if (k == 0) {
                     LATENT_WAIT(ct->seg_full[0], 0);
-                    if (softmax_any(dead)) goto softmax_end;
+                    if (softmax_any<C::kSoft>(dead)) goto softmax_end;
                     if (s.t1 > s.t0) load_q(s);
                 }
                 const int n = s.t1 - s.t0;
                 if (n == 0) break;
                 LATENT_WAIT(ct->seg_full[(k + 1) % kSegs], ((k + 1) / kSegs) & 1);
-                if (softmax_any(dead)) goto softmax_end;
+                if (softmax_any<C::kSoft>(dead)) goto softmax_end;
                 const Seg& nx = ct->seg[(k + 1) % kSegs];
+                // e4m3: what the lane's rows of Q are in units of (the barrier has passed since they were written).
+                const float qs0 = FP8 ? ct->unit[16 * (w & 3) + (lane >> 2)] : 1.f, qs1 = FP8 ? ct->unit[16 * (w & 3) + 8 + (lane >> 2)] : 1.f;
                 const int rows = s.en.nrows;
                 // Tokens that a row sees.
                 auto see = [&](int r) { return s.en.posbase + (s.en.row0 + min(r, rows - 1)) / a.heads + 1; };
@@ -778,7 +784,7 @@ __global__ void __launch_bounds__(Cfg<N, FP8>::kThreads, 1)
                         at[16 * w + (lane >> 2)] = v0;
                         at[16 * w + 8 + (lane >> 2)] = v1;
                     }
-                    softmax_sync();
+                    softmax_sync<C::kSoft>();
 #pragma unroll
                     for (int i = 0; i < C::kSplit; ++i) {
                         v0 = fmaxf(v0, at[i * N + r0]);
@@ -901,7 +907,7 @@ __global__ void __launch_bounds__(Cfg<N, FP8>::kThreads, 1)
                     // (The slot of the tile after the next: all have read it, and none is there yet.)
                     if (tid == 0) *static_cast<volatile int*>(&ct->over[(tile + 2) & 3]) = 0;
                     if (any) {
-                        if (softmax_any(dead)) goto softmax_end;
+                        if (softmax_any<C::kSoft>(dead)) goto softmax_end;
                         float top0 = -INFINITY, top1 = -INFINITY;
                         if (on) {
 #pragma unroll
@@ -954,9 +960,9 @@ __global__ void __launch_bounds__(Cfg<N, FP8>::kThreads, 1)
                         if (j > 0) {
                             publish(ct->alpha, alpha0, alpha1);
                             tc_fence_after();
-                            softmax_sync();
+                            softmax_sync<C::kSoft>();
 #pragma unroll 1
-                            for (int c = 0; c < 4 * N; c += 16) {
+                            for (int c = first_col; c < first_col + kOCols; c += 16) {
                                 uint32_t y[16];
                                 tc_ld16(tmem + lanes + c, y);
                                 tc_wait_ld();
@@ -969,15 +975,15 @@ __global__ void __launch_bounds__(Cfg<N, FP8>::kThreads, 1)
                         if (on) weights(FP8 ? ex2(-up0) : 1.f, FP8 ? ex2(-up1) : 1.f);
                     }
                     if (j > 0 && (j & (kFoldTiles - 1)) == 0) {
-                        // O moves to the fp32 sums: thread's channel 128 u + tid, row after row.
+                        // O moves to the fp32 sums: thread's channel 128 u + chan, row after row.
                         tc_fence_after();
                         const float o0 = FP8 ? m0 + up0 : m0, o1 = FP8 ? m1 + up1 : m1;
                         publish(ct->factor, folded0 == -INFINITY ? 0.f : ex2(folded0 - o0), folded1 == -INFINITY ? 0.f : ex2(folded1 - o1));
                         folded0 = o0;
                         folded1 = o1;
-                        softmax_sync();
+                        softmax_sync<C::kSoft>();
 #pragma unroll 1
-                        for (int c = 0; c < 4 * N; c += 16) {
+                        for (int c = first_col; c < first_col + kOCols; c += 16) {
                             uint32_t y[16];
                             tc_ld16(tmem + lanes + c, y);
                             tc_wait_ld();
@@ -985,12 +991,12 @@ __global__ void __launch_bounds__(Cfg<N, FP8>::kThreads, 1)
                             for (int u = 0; u < 16; ++u) {
                                 const int r = (c + u) % N;
                                 if (r < rows) {
-                                    float* const at = fold_to + r * kLatentDim + (c + u) / N * 128 + tid;
+                                    float* const at = fold_to + r * kLatentDim + (c + u) / N * 128 + chan;
                                     *at = j > kFoldTiles ? fmaf(*at, ct->factor[r], __uint_as_float(y[u])) : __uint_as_float(y[u]);
                                 }
                             }
                         }
-                        softmax_sync();   // (the factors are written again)
+                        softmax_sync<C::kSoft>();   // (the factors are written again)
                     }
                     // P, a row of 64 tokens each: blocks of 8 rows x 8 tokens.
                     if (on) {
@@ -1004,7 +1010,7 @@ __global__ void __launch_bounds__(Cfg<N, FP8>::kThreads, 1)
                     // NaN) in the pages that the product reads.
                     const int pages = min(kPages, s.en.npages - (s.t0 + j) * kPages);
                     if (fault || first + pages * kPage > see_any) {
-                        for (int i = tid; i < pages * kPage * kUnits * 16; i += 128) {
+                        for (int i = tid; i < pages * kPage * kUnits * 16; i += 32 * C::kSoft) {
                             const int r = i >> 6, u = (i >> 4) & 3, c = i & 15;
                             if (first + r >= see_any || ((fault >> (r / kPage * 8)) & 1u))
                                 *reinterpret_cast<uint4*>(ring + (tile * kUnits + u) % C::kRing * kUnit + (r >> 3) * 2048 + (c >> 3) * 1024 +
@@ -1044,7 +1050,7 @@ __global__ void __launch_bounds__(Cfg<N, FP8>::kThreads, 1)
                         ct->sum[16 * w + (lane >> 2)] = make_float2(l0, lr0);
                         ct->sum[16 * w + 8 + (lane >> 2)] = make_float2(l1, lr1);
                     }
-                    softmax_sync();
+                    softmax_sync<C::kSoft>();
                     l0 = l1 = lr0 = lr1 = 0.f;
 #pragma unroll
                     for (int i = 0; i < C::kSplit; ++i) {
@@ -1071,14 +1077,14 @@ __global__ void __launch_bounds__(Cfg<N, FP8>::kThreads, 1)
                         result(r1, m1, l1, lr1);
                     }
                 }
-                softmax_sync();
+                softmax_sync<C::kSoft>();
                 float odd = 0.f;   // NaN once a channel of a row that sees something is not finite
                 const bool fold = n > kFoldTiles;
 #pragma unroll 1
-                for (int c = 0; c < 4 * N; c += 16) {   // channel 128 (c / N) + tid of 16 rows
+                for (int c = first_col; c < first_col + kOCols; c += 16) {   // channel 128 (c / N) + chan of 16 rows
                     uint32_t y[16];
                     tc_ld16(tmem + lanes + c, y);
-                    const int first_row = c % N, channel = c / N * 128 + tid, left = rows - first_row;
+                    const int first_row = c % N, channel = c / N * 128 + chan, left = rows - first_row;
                     float f[16];
 #pragma unroll
                     for (int u = 0; u < 16; u += 4) *reinterpret_cast<float4*>(&f[u]) = *reinterpret_cast<const float4*>(&ct->factor[first_row + u]);
@@ -1115,10 +1121,10 @@ __global__ void __launch_bounds__(Cfg<N, FP8>::kThreads, 1)
                     else write(std::false_type{});
                 }
                 // (Rows of one token see the same.)
-                if (whole && softmax_any(odd != 0.f) && tid == 0 && see_all != see_any)
+                if (whole && softmax_any<C::kSoft>(odd != 0.f) && tid == 0 && see_all != see_any)
                     a.odd[atomicAdd(a.num_odd, 1)] = static_cast<uint32_t>(~s.slot) * a.share + part;
                 tc_fence_before();
-                softmax_sync();   // all have read O before the next segment's first product writes it
+                softmax_sync<C::kSoft>();   // all have read O before the next segment's first product writes it
                 seg_done(k);
             }
         softmax_end:;
@@ -1224,10 +1230,10 @@ __global__ void __launch_bounds__(Cfg<N, FP8>::kThreads, 1)
             if (FP8) (void)bar_wait(smem_addr(&ct->scale_full[tile % kInfoSlots]), (tile / kInfoSlots) & 1);
         loads_done:;
         } else if (FP8 && warp >= C::kFirstWiden) {
-            // ---------------- e4m3 codes -> fp16 units in the MMAs' layout, two warps a unit
+            // ---------------- e4m3 codes -> fp16 units in the MMAs' layout, four warps a unit
             reg_dec<C::kWidenRegs>();
-            const int tid = threadIdx.x & 63, mine = (warp - C::kFirstWiden) >> 1;
-            uint32_t at = mine, until = 0;
+            const int tid = threadIdx.x & 127;
+            uint32_t at = 0, until = 0;
             constexpr uint32_t kDepth = FP8 ? C::kCodes : 1;
             for (uint32_t k = 0;; ++k) {
                 TEST_WAIT(ct->seg_full[k % kSegs], (k / kSegs) & 1, widen_end);
@@ -1235,24 +1241,24 @@ __global__ void __launch_bounds__(Cfg<N, FP8>::kThreads, 1)
                 const int n = s.t1 - s.t0;
                 if (n == 0) break;
                 until += n * kUnits;
-                for (; mine < C::kPairs && at < until; at += C::kPairs) {
+                for (; at < until; ++at) {
                     const uint32_t cs = at % kDepth, st = at % C::kRing;
                     TEST_WAIT(ct->code_full[cs], (at / kDepth) & 1, widen_end);
-                    // 16 codes at chunk tid / 8 of rows tid % 8, + 8, ...: eight lanes read, and write, eight rows' bytes in
+                    // 16 codes at chunk tid / 8 % 8 of every eighth row: eight lanes read, and write, eight rows' bytes in
                     // different banks.  The fence keeps the next copy into the slot behind these reads.
-                    const int r = tid & 7, c = tid >> 3;
-                    uint4 v[8];
+                    const int r = tid & 7, c = (tid >> 3) & 7, u0 = (tid >> 6) * 4;
+                    uint4 v[4];
 #pragma unroll
-                    for (int u = 0; u < 8; ++u)
-                        v[u] = *reinterpret_cast<const uint4*>(codes + cs * (kUnit / 2) + (r + 8 * u) * 128 + ((c ^ r) << 4));
+                    for (int u = 0; u < 4; ++u)
+                        v[u] = *reinterpret_cast<const uint4*>(codes + cs * (kUnit / 2) + (r + 8 * (u0 + u)) * 128 + ((c ^ r) << 4));
                     fence_proxy_async_smem();
                     __syncwarp();
                     if (lane == 0) mbar_arrive(smem_addr(&ct->code_empty[cs]));
                     TEST_WAIT(ct->empty[st], ((at / C::kRing) & 1) ^ 1, widen_end);
-                    unsigned char* const o = ring + st * kUnit + (c >> 2) * 1024 + r * 128;
+                    unsigned char* const o = ring + st * kUnit + u0 * 2048 + (c >> 2) * 1024 + r * 128;
                     const int at0 = ((2 * c) & 7 ^ r) << 4, at1 = ((2 * c + 1) & 7 ^ r) << 4;
 #pragma unroll
-                    for (int u = 0; u < 8; ++u) {
+                    for (int u = 0; u < 4; ++u) {
                         uint4 lo, hi;
                         widen4_f16(v[u].x, lo.x, lo.y);
                         widen4_f16(v[u].y, lo.z, lo.w);
