@@ -6,7 +6,7 @@
 // tokens x 512) are keys and values both.  With Q (rows x 576) and K = C beside the
 // rotary keys,
 //   S = Q K^T                 (fp32 in TMEM: 64 rows x 64 tokens, 36 MMAs of k = 16 channels)
-//   P = exp2(S * scale - base)   (bf16 in shared memory; base = a running maximum a row)
+//   P = exp2(S * scale - base)   (16 bits in shared memory; base = a running maximum a row)
 //   O^T = O^T * 2^(old - new base) + C^T P^T   (fp32 in TMEM: 512 channels x rows,
 //                             4 MMAs of 128 channels for each 16 tokens)
 // The second product is turned round, channels on the MMA's M side and rows on its
@@ -20,9 +20,15 @@
 // over the sum of the rounded weights, so that rows of equal weights lose nothing.
 // Sums, bases and outputs are fp32.
 //
-// e4m3 latents: codes are widened to bf16 tiles, exactly; a token's scale acts on
-// its logits and on its weights, and the rotary part of the logits is a product of
-// its own (64 more columns).
+// e4m3 latents: codes are widened to fp16 tiles, exactly, by the conversion unit (77
+// codes a cycle and SM; to bf16 28).  Q's latent part is fp16 as well, each row
+// scaled by a power of two that puts its largest value at 2^10 .. 2^11: values down to
+// 2^-27 of that stay exact, smaller ones are off by up to 2^-35 of it.  A token's scale
+// acts on its logits and on its weights.  A weight times its scale is rounded to fp16
+// (2^-12 of it) in a unit of the row that at most equals the largest so far, so that
+// those below 2^-14 of the largest are off by up to 2^-25 of it; the unit moves with
+// the base.  The average is taken over the sum of the weights themselves.  The rotary
+// part of the logits is a product of its own in bf16 (64 more columns).
 //
 // Work.  An entry is up to kShare x N rows of a request with the pages they see;
 // every group of kShare CTAs takes an equal run of the (entry, key tile) sequence.
@@ -32,11 +38,20 @@
 // Roles of a CTA (one per SM):
 //   warp 1       issues the MMAs
 //   warp 2       walks the plan
-//   warps 4-7    softmax (16 rows each, or a part of the tokens where there are fewer than 64), outputs
-//   warps 8-11   load a page of the tile each: units of 64 tokens x 128 channels (16
-//                KB), each freed when its part of the second product is done, and
-//                rotary keys
-//   e4m3: the last four widen the codes; with 64 rows a CTA, warps 0 and 3 load, two pages of the tile each
+//   warps 4-7    softmax and outputs: 16 rows each, or where there are fewer than 64 the
+//                tokens of a tile shared out (e4m3, 64 rows: warps 4-11, half the tokens each)
+//   then         four that load a page of the tile each: units of 64 tokens x 128 channels
+//                (16 KB), each freed when its part of the second product is done, and
+//                rotary keys (e4m3, 64 rows: warps 0 and 3, two pages each)
+//   the last     (e4m3) four that widen the codes
+//
+// What bounds it (GB300): 64 bf16 rows, the tensor pipe with shared memory behind it: a
+// tile's MMAs take 2014 cycles by themselves, 2500 in the kernel (8 requests of 128
+// heads at 128000 tokens 325 us, 3.6 TB/s and 0.88 PFLOP/s; 512 query tokens at 8192
+// 1.05 ms).  64 e4m3 rows: shared memory, which carries the codes and their widened
+// tiles on top (7 ragged chunks 468 us).  16 e4m3 rows: the MMAs of a tile, 1776 cycles,
+// half of them for rows that repeat others (32 requests 168 us, 4.2 TB/s).  One request:
+// the start, the plan, Q and the join, one after the other (15 us, 4 tiles a CTA).
 #include <climits>
 #include <type_traits>
 
@@ -68,12 +83,14 @@ constexpr int kMaxRows = 64;                        // rows of a CTA's tile at m
 
 template <int N, bool FP8>
 struct Cfg {
-    static constexpr int kRing = FP8 ? (N == 64 ? 8 : 10) : (N == 64 ? 11 : 12);           // units: two tiles at least
-    static constexpr int kRope = 2;                                        // rotary tiles
-    static constexpr int kCodes = FP8 ? (N == 64 ? 3 : 4) : 0;             // units of codes, 8 KB
-    static constexpr int kWiden = 4;                                       // warps that widen, all of a unit
-    // Warps that load.  e4m3, 64 rows: the two that else idle, and eight softmax warps; with fewer rows a tile is over too
-    // soon for two (32 requests of 16 heads 185 us, 165 with four).
+    // Units of the ring, two tiles at least, and units of codes, 8 KB each: what shared memory holds.  (e4m3, 16 rows: 8 and
+    // 8 189 us for 32 requests, 9 and 6 168, 10 and 4 170, 11 and 2 248.)
+    static constexpr int kRing = FP8 ? (N == 64 ? 8 : 9) : (N == 64 ? 11 : 12);
+    static constexpr int kCodes = FP8 ? (N == 64 ? 3 : 6) : 0;
+    static constexpr int kRope = 2;     // rotary tiles
+    static constexpr int kWiden = 4;    // warps that widen, all of them a unit
+    // Warps that load.  e4m3, 64 rows: the two that else idle, and eight softmax warps (490 -> 468 us for 7 requests'
+    // chunks); with fewer rows a tile is over too soon for two (32 requests of 16 heads 185 us, 165 with four).
     static constexpr int kLoads = FP8 && N == 64 ? 2 : kPages;
     static constexpr int kSoft = FP8 && N == 64 ? 8 : 4;
     // Registers a thread: bf16 168 at launch, then 96 for the first four warps and the loads and 248 for the softmax
@@ -331,7 +348,9 @@ __device__ __forceinline__ int warp_find_le(const int64_t* a, int n, int64_t v) 
     return lo;
 }
 
-// What an entry costs beside its tiles, in tiles, and the least share that is worth a CTA.
+// What an entry costs beside its tiles, in tiles (Q, the first tile's bases, the outputs: 64 rows take 25000 cycles, and
+// with 3 for them 7 requests' e4m3 chunks take 603 us, with 9 490, with 14 520; 16 rows 1: 32 requests 169 us, 3: 165, 5:
+// 164), and the least share that is worth a CTA (one request of 64 tiles and 16 heads: 1 20.1 us, 2 19.5, 3 17.4, 4 18.0).
 constexpr int kMinShare = 3;
 __host__ __device__ constexpr int entry_cost(int rows) { return rows == 64 ? 9 : 3; }
 __device__ __forceinline__ int cost_of_entry(int tiles, int rows) { return tiles ? tiles + entry_cost(rows) : 0; }
@@ -402,8 +421,6 @@ __global__ void __launch_bounds__(Cfg<N, FP8>::kThreads, 1)
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
     }
     pdl_wait();
-    // The join, which waits.  (Without one the next call's kernels are the dependents: some read their inputs at once.)
-    if (gridDim.x > static_cast<unsigned>(a.share)) pdl_launch_dependents();
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
