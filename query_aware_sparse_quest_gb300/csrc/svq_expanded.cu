@@ -12,10 +12,12 @@
 // the paged calls do.  P is rounded to bf16 because one MMA takes both operands in
 // one type; the sum is taken of the unrounded weights, in fp32.
 //
-// Work.  An entry is a row tile with the tokens it sees; every CTA takes an equal
-// run of the (request, head, entry, key tile) sequence, so that the row tiles of a
-// head follow one another and find its keys and values in L2; a run that starts or
-// ends inside an item leaves a partial (O, base, sum), joined by a second kernel.
+// Work.  An entry is a row tile with the tokens it sees, an item an entry of one
+// head.  Every CTA takes an equal run of the (request, head, entry, key tile)
+// sequence; a run that starts or ends inside an item leaves a partial (O, base,
+// sum), joined by a second kernel.  Where the keys and values do not fit the L2,
+// CTAs take whole items first, in step with one another (see ExpandedArgs), and such
+// runs of the rest.
 //
 // Roles of a CTA (one per SM; TMEM holds S0, S1, O0, O1 of 128 columns each):
 //   warp 0       loads keys, warp 3 values: a ring of 8 blocks of 16 KB (TMA), of
@@ -66,6 +68,13 @@ struct __align__(16) Entry {
     int pad[2];
 };
 
+// Waves: CTAs that start items at the same time, in the items' order, read the keys and values of the same heads at the
+// same time, which then come from L2 (equal runs of the whole sequence have every CTA at a head of its own: each item's
+// keys and values come from HBM).  A 4096-token chunk of 32 heads at 32768 tokens 1855 -> 1533 us.  Not worth it where
+// the L2 holds them anyway (tokens times heads, 512 bytes each; 5 ragged requests of 60 MB 62.5 us, in waves 63.6), nor for
+// many requests, as the plan looks up items one by one.
+constexpr int kMaxWaves = 64, kWaveBatch = 32;
+constexpr int64_t kWaveTokens = 128 << 10;
 struct ExpandedArgs {
     const __nv_bfloat16* q;
     int heads;
@@ -87,10 +96,13 @@ struct ExpandedArgs {
     // Plan
     Entry* entries;
     int64_t* cum;         // [E + 1] cost per head of the entries before each
-    int* num_entries;
     int* req_first;       // [batch + 1] first entry of each request
     int64_t* req_cum;     // [batch + 1] cost per head of the requests before each
     int max_entries;
+    int* waves;           // whole items that a CTA takes first: c, c + CTAs, ...
+    int64_t* starts;      // [CTAs + 1] cost before each CTA's share of the others
+    int ctas;
+    bool in_step;         // waves pay
     // Partials
     float* cut_o;         // [2 CTAs][slot_rows][128]
     float2* cut_ml;
@@ -417,12 +429,48 @@ __global__ void __launch_bounds__(kThreads, 1)
         } else if (warp == 2) {
             // ---------------- the CTA's share of the plan, segment by segment
             reg_dec<kOtherRegs>();
-            const int num_entries = *a.num_entries;
-            const Share share(a.cum[num_entries] * a.heads, gridDim.x);
-            const int64_t first = share.start(blockIdx.x);
-            int64_t left = share.start(blockIdx.x + 1) - first;
+            const int waves = *a.waves;
+            const int64_t first = a.starts[blockIdx.x];
+            int64_t left = a.starts[blockIdx.x + 1] - first;
             int b = 0, h = 0, e = 0, e0 = 0, e1 = 0;   // request, head, entry, the request's entries
-            int64_t off = 0;                           // into the item's cost
+            int64_t off = 0, into = 0;                 // into the item's cost; where the share begins
+            bool first_item = true;
+            Entry en;
+            uint32_t k = 0;
+            auto fetch = [&](int e) {
+                const int4* p = reinterpret_cast<const int4*>(a.entries + e);
+                const int4 x = p[0], y = p[1];
+                return Entry{x.x, x.y, x.z, x.w, y.x, y.y, {0, 0}};
+            };
+            auto publish = [&](int t0, int t1, int slot) {   // false: gave up
+                for (int round = 0;; ++round) {
+                    if (!__any_sync(0xffffffffu, !bar_wait(smem_addr(&ct->seg_empty[k % kSegs]), ((k / kSegs) & 1) ^ 1))) break;
+                    if (__any_sync(0xffffffffu, *static_cast<volatile int*>(&ct->gave_up)) || round == kSegRounds) {
+                        if (lane == 0) gave_up(ct);
+                        return false;
+                    }
+                }
+                if (lane == 0) {
+                    Seg& s = ct->seg[k % kSegs];
+                    s.en = en;
+                    s.h = h;
+                    s.t0 = t0;
+                    s.t1 = t1;
+                    s.slot = slot;
+                    mbar_arrive(smem_addr(&ct->seg_full[k % kSegs]));
+                }
+                ++k;
+                return true;
+            };
+            for (int64_t j = 0, i = blockIdx.x; j < waves; ++j, i += gridDim.x) {
+                while (i >= static_cast<int64_t>(a.heads) * a.req_first[b + 1]) ++b;
+                e0 = a.req_first[b];
+                const int64_t in = i - static_cast<int64_t>(a.heads) * e0, n = a.req_first[b + 1] - e0;
+                h = static_cast<int>(div64(in, n));
+                e = e0 + static_cast<int>(in - h * n);
+                en = fetch(e);
+                if (en.tiles && !publish(0, en.tiles, -1 - (e * a.heads + h))) goto plan_end;
+            }
             if (left > 0) {
                 const int64_t u = div64(first, a.heads);
                 b = warp_find_le(a.req_cum, a.batch, u);
@@ -433,36 +481,31 @@ __global__ void __launch_bounds__(kThreads, 1)
                 off = in - h * one;
                 e = e0 + warp_find_le(a.cum + e0, e1 - e0, c0 + off);
                 off -= a.cum[e] - c0;
+                into = off;
+                en = fetch(e);
             }
-            const bool go_on = off > 0;      // the share begins inside an item
-            if (left <= 0 && lane == 0) a.cut_item[2 * blockIdx.x] = make_int4(0, 0, 0, 0);
-            bool first_item = true;
-            Entry en;
-            int held = -1;
-            for (uint32_t k = 0;;) {
+            {
+                // The CTA after the one with an item's first tile names the item for the join.
+                int4 what = make_int4(0, 0, 0, 0), where = make_int4(0, 0, 0, 0);
+                if (into > 0) {
+                    const int64_t begin = first - into;
+                    const int c0 = warp_find_le(a.starts, gridDim.x, begin + kItemCost);
+                    if (static_cast<int>(blockIdx.x) == c0 + 1) {
+                        const int c1 = warp_find_le(a.starts, gridDim.x, begin + kItemCost + en.tiles - 1);
+                        what = make_int4(en.row0, en.ntok, h, c1 - c0 + 1);
+                        where.x = 2 * c0 + (a.starts[c0] >= begin ? 0 : 1);
+                        where.y = 2 * (c0 + 1);
+                        where.z = e;
+                    }
+                }
+                if (lane == 0) {
+                    a.cut_item[2 * blockIdx.x] = what;
+                    a.cut_item[2 * blockIdx.x + 1] = where;
+                }
+            }
+            for (;;) {
                 int t0 = 0, t1 = 0;
                 if (left > 0) {
-                    if (held != e) {
-                        const int4* p = reinterpret_cast<const int4*>(a.entries + e);
-                        const int4 x = p[0], y = p[1];
-                        en = Entry{x.x, x.y, x.z, x.w, y.x, y.y, {0, 0}};
-                        held = e;
-                    }
-                    if (first_item && lane == 0) {
-                        // The CTA after the one with an item's first tile names the item for the join.
-                        int4 what = make_int4(0, 0, 0, 0), where = make_int4(0, 0, 0, 0);
-                        if (go_on) {
-                            const Placed it(share, first - off, en.tiles);
-                            if (static_cast<int>(blockIdx.x) == it.c0 + 1) {
-                                what = make_int4(en.row0, en.ntok, h, it.c1 - it.c0 + 1);
-                                where.x = 2 * it.c0 + (share.start(it.c0) >= it.begin ? 0 : 1);
-                                where.y = 2 * (it.c0 + 1);
-                                where.z = e;
-                            }
-                        }
-                        a.cut_item[2 * blockIdx.x] = what;
-                        a.cut_item[2 * blockIdx.x + 1] = where;
-                    }
                     const int64_t take = min(left, cost_of(en.tiles) - off);
                     t0 = static_cast<int>(max(static_cast<int64_t>(0), off - kItemCost));
                     t1 = static_cast<int>(max(static_cast<int64_t>(0), off + take - kItemCost));
@@ -470,30 +513,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                     off += take;
                 }
                 if (t1 > t0 || left <= 0) {
-                    for (int round = 0;; ++round) {
-                        if (!__any_sync(0xffffffffu, !bar_wait(smem_addr(&ct->seg_empty[k % kSegs]), ((k / kSegs) & 1) ^ 1))) break;
-                        if (__any_sync(0xffffffffu, *static_cast<volatile int*>(&ct->gave_up)) || round == kSegRounds) {
-                            if (lane == 0) gave_up(ct);
-                            goto plan_end;
-                        }
-                    }
-                    if (lane == 0) {
-                        Seg& s = ct->seg[k % kSegs];
-                        s.en = en;
-                        s.h = h;
-                        s.t0 = t0;
-                        s.t1 = t1;
-                        s.slot = t0 == 0 && t1 == en.tiles ? -1 - (e * a.heads + h) : static_cast<int>(blockIdx.x) * 2 + (first_item ? 0 : 1);
-                        mbar_arrive(smem_addr(&ct->seg_full[k % kSegs]));
-                    }
-                    ++k;
+                    const bool whole = t0 == 0 && t1 == en.tiles;
+                    if (!publish(t0, t1, whole ? -1 - (e * a.heads + h) : static_cast<int>(blockIdx.x) * 2 + (first_item ? 0 : 1))) break;
                     if (t1 == t0) break;
                 }
                 first_item = false;
-                if (off == cost_of(en.tiles)) {
+                if (left > 0 && off == cost_of(en.tiles)) {
                     off = 0;
-                    held = -1;
-                    if (++e == e1 && left > 0) {   // the next head, or the next request with tokens
+                    if (++e == e1) {   // the next head, or the next request with tokens
                         e = e0;
                         if (++h == a.heads) {
                             h = 0;
@@ -503,6 +530,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                             e1 = a.req_first[b + 1];
                         }
                     }
+                    en = fetch(e);
                 }
             }
         plan_end:;
@@ -745,6 +773,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 // ---------------------------------------------------------------- plan
 constexpr int kPlanThreads = 1024;
+static_assert(kMaxCtas <= kPlanThreads, "a thread a CTA");
 
 // The tokens of request b's range: false for ranges that are none.
 __device__ __forceinline__ bool kv_range(const ExpandedArgs& a, int b, int size, int& k0, int& n) {
@@ -819,11 +848,46 @@ __global__ void __launch_bounds__(kPlanThreads) expanded_plan_kernel(const __gri
     }
     if (tid == 0) {
         a.cum[n] = base;
-        *a.num_entries = n;
         *a.num_odd = 0;
     }
     __syncthreads();
     for (int i = tid; i <= a.batch; i += kPlanThreads) a.req_cum[i] = a.cum[a.req_first[i]];
+
+    // Thread c: the shares of CTA c.  Whole items first, the waves, and of the others what makes its share equal.
+    const int64_t cost = base * a.heads, items = static_cast<int64_t>(n) * a.heads;
+    const Share share(cost, a.ctas);
+    const int64_t equal = tid < a.ctas ? share.start(tid + 1) - share.start(tid) : 0;
+    int waves = a.in_step ? static_cast<int>(min(items / a.ctas, static_cast<int64_t>(kMaxWaves))) : 0;
+    if (!waves) {
+        if (tid < a.ctas) a.starts[tid] = share.start(tid);
+        if (tid == 0) {
+            a.starts[a.ctas] = cost;
+            *a.waves = 0;
+        }
+        __threadfence();
+        return;
+    }
+    int64_t len = equal, whole = 0;   // of the thread's; of all waves
+    for (; waves > 0; --waves) {
+        int64_t mine = 0;
+        int b = 0;
+        for (int64_t j = 0, i = tid; j < waves && tid < a.ctas; ++j, i += a.ctas) {
+            while (i >= static_cast<int64_t>(a.heads) * a.req_first[b + 1]) ++b;
+            const int e0 = a.req_first[b], e = e0 + static_cast<int>((i - static_cast<int64_t>(a.heads) * e0) % (a.req_first[b + 1] - e0));
+            mine += a.cum[e + 1] - a.cum[e];
+        }
+        len = equal - mine;
+        (void)block_scan(mine, warp_sums, whole);
+        if (!__syncthreads_or(tid < a.ctas && len < 1)) break;
+        len = equal;
+        whole = 0;
+    }
+    const int64_t before = whole + block_scan(len, warp_sums, total);
+    if (tid < a.ctas) a.starts[tid] = before;
+    if (tid == 0) {
+        a.starts[a.ctas] = cost;
+        *a.waves = waves;
+    }
     __threadfence();
 }
 
@@ -932,7 +996,7 @@ __global__ void __launch_bounds__(kCutThreads, 4) expanded_join_kernel(const __g
 size_t up(size_t n) { return (n + 255) / 256 * 256; }
 
 struct Layout {
-    size_t entries, cum, num, req_first, req_cum, cut_item, cut_o, cut_ml, odd, num_odd, total;
+    size_t entries, cum, waves, starts, req_first, req_cum, cut_item, cut_o, cut_ml, odd, num_odd, total;
     int max_entries, item_rows, slot_rows;
     Layout(int64_t batch, int64_t rows, int heads) {
         const int64_t e = rows / kRowTile + batch;
@@ -943,7 +1007,8 @@ struct Layout {
         auto take = [&](size_t bytes) { const size_t r = at; at += up(bytes); return r; };
         entries = take(e * sizeof(Entry));
         cum = take((e + 1) * sizeof(int64_t));
-        num = take(sizeof(int));
+        waves = take(sizeof(int));
+        starts = take((kMaxCtas + 1) * sizeof(int64_t));
         req_first = take((batch + 1) * sizeof(int));
         req_cum = take((batch + 1) * sizeof(int64_t));
         cut_item = take(2 * kMaxCtas * sizeof(int4));
@@ -1002,7 +1067,10 @@ int launch_expanded(const void* q, int num_heads, const int32_t* q_start, int to
     a.lse = lse;
     a.entries = reinterpret_cast<Entry*>(ws + lay.entries);
     a.cum = reinterpret_cast<int64_t*>(ws + lay.cum);
-    a.num_entries = reinterpret_cast<int*>(ws + lay.num);
+    a.waves = reinterpret_cast<int*>(ws + lay.waves);
+    a.starts = reinterpret_cast<int64_t*>(ws + lay.starts);
+    a.ctas = sm_count < kMaxCtas ? sm_count : kMaxCtas;
+    a.in_step = batch <= kWaveBatch && static_cast<int64_t>(total_kv) * num_heads >= kWaveTokens;
     a.req_first = reinterpret_cast<int*>(ws + lay.req_first);
     a.req_cum = reinterpret_cast<int64_t*>(ws + lay.req_cum);
     a.max_entries = lay.max_entries;
@@ -1027,7 +1095,7 @@ int launch_expanded(const void* q, int num_heads, const int32_t* q_start, int to
                    : SV_ERR_CUDA;
     });
     if (st) return st;
-    const int ctas = sm_count < kMaxCtas ? sm_count : kMaxCtas;
+    const int ctas = a.ctas;
     if (launch_pdl(expanded_kernel, dim3(ctas), dim3(kThreads), kSmem, stream, a, tq, tk, tr, tv) != cudaSuccess)
         return SV_ERR_CUDA;
     if (ctas < 2) return SV_OK;

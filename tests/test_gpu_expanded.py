@@ -105,6 +105,19 @@ def test_long_and_many(sizes, lens, heads, causal):
     r.check(*r.call(causal), causal)
 
 
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("sizes,lens,heads", [
+    ([2100, 0, 700, 300], [2100, 40, 700, 1000], 64),   # items of 1 to 17 key tiles
+    ([2000], [4000], 40),                               # 320 items, nearly alike: two waves
+    ([256], [1100], 152),                               # as many items as SMs, or about
+    ([30], [900], 310),
+])
+def test_items_in_waves(sizes, lens, heads, causal):
+    """Sizes whose keys and values do not fit the L2, where CTAs first take whole items in step."""
+    r = Rows(sizes, lens, heads, seed=3)
+    r.check(*r.call(causal), causal)
+
+
 def test_more_query_tokens_than_tokens_without_a_mask():
     r = Rows([300, 40], [7, 200], 3)
     r.check(*r.call(False), False)
