@@ -35,7 +35,7 @@ int launch_latent_append(const sv_cache* c, const void* latent, int64_t latent_s
                          int64_t rope_stride, const int32_t* slot_mapping, int64_t num_tokens, cudaStream_t stream);
 int launch_latent_gather(const sv_cache* c, const int32_t* page_table, const int32_t* seq_lens, int batch, int max_pages,
                          const int32_t* row_start, const int32_t* first_token, int64_t total_rows, void* latent,
-                         int64_t latent_stride, void* rope, int64_t rope_stride, int sm_count, cudaStream_t stream);
+                         int64_t latent_stride, void* rope, int64_t rope_stride, cudaStream_t stream);
 size_t latent_workspace_bytes(int batch, int num_q_heads, int total_q);
 int launch_latent_attention(const sv_cache* c, const void* q, int num_q_heads, const int32_t* q_start, int total_q,
                             const int32_t* page_table, const int32_t* seq_lens, int batch, int max_pages,
@@ -621,10 +621,8 @@ int sv_latent_gather(const sv_cache* cache, const int32_t* page_table, const int
     if (!page_table || !seq_lens || !row_start || batch < 1 || max_pages < 1) return SV_ERR_INVALID_ARG;
     if (batch > 65535 || max_pages >= kMaxRowPages || total_rows > INT_MAX) return SV_ERR_UNSUPPORTED;
     if ((st = check_latent_rows(latent, latent_stride, rope, rope_stride, total_rows))) return st;
-    int sms = 0;
-    if ((st = sm_count_of_current_device(&sms))) return st;
     return launch_latent_gather(cache, page_table, seq_lens, batch, max_pages, row_start, first_token, total_rows, latent,
-                                latent_stride, rope, rope_stride, sms, static_cast<cudaStream_t>(stream));
+                                latent_stride, rope, rope_stride, static_cast<cudaStream_t>(stream));
 }
 
 size_t sv_latent_attention_workspace_size(int32_t batch, int32_t num_q_heads, int32_t total_q) {

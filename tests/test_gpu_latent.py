@@ -379,6 +379,29 @@ def test_gather_ranges(fp8):
     assert torch.equal(rope[:16].double(), case.tokens(0)[1][:16]) and torch.equal(rope[32:40].double(), case.tokens(0)[1][32:40])
 
 
+@pytest.mark.parametrize("fp8", [False, True])
+def test_gather_many_rows(fp8):
+    """More rows than a warp takes one by one: odd range ends, a request without rows, a page that is not there."""
+    from query_aware_sparse_quest_gb300 import binding
+    case = LatentCase([20011, 50, 15000, 9, 3], fp8=fp8, seed=8)
+    cache, table = case.cache(), case.table.to(DEV)
+    firsts, sizes = [37, 0, 1, 0, 0], [19973, 0, 14999, 9, 3]
+    table[2, 500] = -1
+    total = sum(sizes)
+    latent = torch.full((total + 5, LATENT), 7.0, dtype=torch.bfloat16, device=DEV)
+    rope = torch.full((total + 5, ROPE), 7.0, dtype=torch.bfloat16, device=DEV)
+    binding.sv_latent_gather(cache, table, ints(case.lens), ints(starts_of(sizes)), latent, rope, first_token=ints(firsts))
+    assert binding.sv_get_device_error() == 0x1
+    for b, (f, n) in enumerate(zip(firsts, sizes)):
+        c, r = (x.clone() for x in case.tokens(b))
+        if b == 2:
+            c[500 * PAGE:501 * PAGE] = r[500 * PAGE:501 * PAGE] = 0.0
+        at = sum(sizes[:b])
+        assert ((latent[at:at + n].double() - c[f:f + n]).abs() <= c[f:f + n].abs() * (2.0 ** -8 + 2.0 ** -23) * (1 if fp8 else 0)).all()
+        assert torch.equal(rope[at:at + n].double(), r[f:f + n])
+    assert (latent[total:] == 7).all() and (rope[total:] == 7).all()
+
+
 def test_append_leaves_out_slots_outside_the_pool_and_codes_rows_that_are_not_finite():
     from query_aware_sparse_quest_gb300 import binding
     cache = binding.LatentCache.empty(2, fp8=True)
