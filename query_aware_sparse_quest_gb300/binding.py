@@ -530,6 +530,8 @@ class LatentCache:
             raise ValueError("a cache's tensors must be on one device")
         self.c = sv_cache(latent.data_ptr(), rope.data_ptr(), None, n, 1, p, d,
                           SV_KV_LATENT_E4M3 if fp8 else SV_KV_LATENT_BF16, scale.data_ptr() if fp8 else None, None)
+        self.device_index = latent.get_device()
+        self._ref = ctypes.byref(self.c)
 
     @classmethod
     def empty(cls, num_phys_pages: int, fp8: bool = False, device="cuda") -> "LatentCache":
@@ -543,7 +545,13 @@ class LatentCache:
         return self.latent
 
     def ref(self):
-        return ctypes.byref(self.c)
+        return self._ref
+
+    def ref_at(self, dev: int):
+        """ref(), after checking that the cache is on the current device `dev`."""
+        if self.device_index != dev:
+            raise ValueError(f"the cache is on cuda:{self.device_index} while cuda:{dev} is current")
+        return self._ref
 
 
 def _strided(t: torch.Tensor, shape, name: str, dev: int):
@@ -553,14 +561,12 @@ def _strided(t: torch.Tensor, shape, name: str, dev: int):
         _shape(t, shape, name)
     if t.get_device() != dev or t.dtype is not _BF16:
         _at(t.reshape(-1)[:0], _BF16, name, dev)
-    strides = t.stride()
-    if strides[-1] != 1 and t.numel():
+    s = t.stride()
+    if s[-1] != 1 and t.numel():
         raise ValueError(f"{name} must be contiguous in its last dimension")
-    if len(shape) == 2:
-        return t.data_ptr(), strides[0] if shape[0] > 1 else shape[1]
-    n, h, d = shape
-    inner = strides[1] if h > 1 else d
-    return t.data_ptr(), strides[0] if n > 1 else max(h, 1) * d, inner
+    if len(s) == 2:
+        return t.data_ptr(), s[0] if shape[0] > 1 else shape[1]
+    return t.data_ptr(), s[0] if shape[0] > 1 else max(shape[1], 1) * shape[2], s[1] if shape[1] > 1 else shape[2]
 
 
 def sv_latent_append(cache: LatentCache, latent: torch.Tensor, rope: torch.Tensor, slot_mapping: torch.Tensor,
@@ -568,9 +574,8 @@ def sv_latent_append(cache: LatentCache, latent: torch.Tensor, rope: torch.Tenso
     """latent [T][512] and rope [T][64], rows of any stride, to the slots of the pool."""
     n = slot_mapping.numel()
     dev = torch.cuda.current_device()
-    _at(cache.latent, None, "the cache", dev)
     _check("sv_latent_append", _load().sv_latent_append(
-        cache.ref(), *_strided(latent, (n, LATENT_DIM), "latent", dev), *_strided(rope, (n, ROPE_DIM), "rope", dev),
+        cache.ref_at(dev), *_strided(latent, (n, LATENT_DIM), "latent", dev), *_strided(rope, (n, ROPE_DIM), "rope", dev),
         _at(slot_mapping, _I32, "slot_mapping", dev), n, _on(stream, dev)))
 
 
@@ -586,9 +591,8 @@ def sv_latent_gather(cache: LatentCache, page_table: torch.Tensor, seq_lens: tor
     if first_token is not None:
         _shape(first_token, (B,), "first_token")
     dev = torch.cuda.current_device()
-    _at(cache.latent, None, "the cache", dev)
     _check("sv_latent_gather", _load().sv_latent_gather(
-        cache.ref(), _at(page_table, _I32, "page_table", dev), _at(seq_lens, _I32, "seq_lens", dev), B, max_pages,
+        cache.ref_at(dev), _at(page_table, _I32, "page_table", dev), _at(seq_lens, _I32, "seq_lens", dev), B, max_pages,
         _at(row_start, _I32, "row_start", dev), _at(first_token, _I32, "first_token", dev), N,
         *_strided(latent, (N, LATENT_DIM), "latent", dev), *_strided(rope, (N, ROPE_DIM), "rope", dev), _on(stream, dev)))
 
@@ -611,9 +615,8 @@ def sv_latent_attention(cache: LatentCache, q: torch.Tensor, page_table: torch.T
     if q_start is not None:
         _shape(q_start, (B + 1,), "q_start")
     dev = torch.cuda.current_device()
-    _at(cache.latent, None, "the cache", dev)
     _check("sv_latent_attention", _load().sv_latent_attention(
-        cache.ref(), _at(q, _BF16, "q", dev), Hq, _at(q_start, _I32, "q_start", dev), T,
+        cache.ref_at(dev), _at(q, _BF16, "q", dev), Hq, _at(q_start, _I32, "q_start", dev), T,
         _at(page_table, _I32, "page_table", dev), _at(seq_lens, _I32, "seq_lens", dev), B, max_pages, softmax_scale,
         _at(out, _BF16, "out", dev), _at(lse, _F32, "lse", dev), _at(workspace, None, "workspace", dev), workspace.nbytes,
         _on(stream, dev)))
