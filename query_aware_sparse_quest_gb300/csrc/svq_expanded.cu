@@ -29,6 +29,13 @@
 // Two streams keep the tensor cores busy while the other's softmax runs: the two
 // 128-row halves of a tile, each over every key tile; or, for up to 128 rows, the
 // even and the odd key tiles of the same rows, joined at the end.
+//
+// What bounds it (GB300): long chunks, the tensor pipe at the card's power limit (4096
+// tokens of 32 heads at 32768 1533 us, 1.68 PFLOP/s, where the library's product
+// sustains 1.73); short ones, the filling and emptying of the pipeline once an item and
+// the three kernels' start (300 tokens of 16 heads 20.6 us, 5 ragged requests 62 us).
+// 256 rows an item because K and V are read once for them: with 128 the ring would
+// carry twice the bytes a product.
 #include <climits>
 
 #include "svq_fold.cuh"
@@ -52,7 +59,7 @@ constexpr int kThreads = 384;
 // 128 x 88 + 256 x 208 = 384 x 168.
 constexpr int kOtherRegs = 88, kSoftmaxRegs = 208;
 constexpr int kQBytes = 128 * kQueryDim * 2;        // a stream's rows
-constexpr int kControlBytes = 3072;
+constexpr int kControlBytes = 3 * 1024;
 constexpr int kSmem = kBlocks * kBlock + 2 * kQBytes + kControlBytes;
 static_assert(kSmem <= 227 * 1024, "shared memory of one CTA");
 

@@ -46,12 +46,12 @@
 //   the last     (e4m3) four that widen the codes
 //
 // What bounds it (GB300): 64 bf16 rows, the tensor pipe with shared memory behind it: a
-// tile's MMAs take 2014 cycles by themselves, 2500 in the kernel (8 requests of 128
-// heads at 128000 tokens 325 us, 3.6 TB/s and 0.88 PFLOP/s; 512 query tokens at 8192
-// 1.05 ms).  64 e4m3 rows: shared memory, which carries the codes and their widened
-// tiles on top (7 ragged chunks 468 us).  16 e4m3 rows: the MMAs of a tile, 1776 cycles,
-// half of them for rows that repeat others (32 requests 168 us, 4.2 TB/s).  One request:
-// the start, the plan, Q and the join, one after the other (15 us, 4 tiles a CTA).
+// tile's MMAs take 2014 cycles by themselves, 2700 in the kernel (8 requests of 128
+// heads at 128000 tokens 324 us, 3.6 TB/s and 0.88 PFLOP/s; 512 query tokens at 8192
+// 1.06 ms).  64 e4m3 rows: shared memory, which carries the codes and their widened
+// tiles on top (7 ragged chunks 460 us).  16 e4m3 rows: the MMAs of a tile, 1776 cycles,
+// half of them for rows that repeat others (32 requests 165 us, 4.3 TB/s).  One request:
+// the start, the plan, Q and the join, one after the other (15 us, 3 tiles a CTA).
 #include <climits>
 #include <type_traits>
 
@@ -104,7 +104,7 @@ struct Cfg {
     // Softmax warps that share 16 rows, kCols tokens each.  (Q's rows are repeated on the M side, so every warp's quarter
     // of TMEM holds its rows' logits.)
     static constexpr int kGroups = N / 16, kSplit = kSoft / kGroups, kCols = kTok / kSplit;
-    static constexpr int kControl = FP8 ? 4096 : 3072;
+    static constexpr int kControl = (FP8 ? 4 : 3) * 1024;
     // TMEM columns: O^T of channels 128 m .. at m N, then S (e4m3: its latent and its rotary part), then the first
     // kQUnits units of Q's channels, two a column.  The others and the rotary ones are in shared memory.
     static constexpr int kSCols = FP8 ? 2 * kTok : kTok;
