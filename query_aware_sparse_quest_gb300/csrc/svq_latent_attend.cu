@@ -45,13 +45,13 @@
 //                rotary keys (e4m3, 64 rows: warps 0 and 3, two pages each)
 //   the last     (e4m3) four that widen the codes
 //
-// What bounds it (GB300): 64 bf16 rows, the tensor pipe with shared memory behind it: a
-// tile's MMAs take 2014 cycles by themselves, 2700 in the kernel (8 requests of 128
-// heads at 128000 tokens 324 us, 3.6 TB/s and 0.88 PFLOP/s; 512 query tokens at 8192
-// 1.06 ms).  64 e4m3 rows: shared memory, which carries the codes and their widened
-// tiles on top (7 ragged chunks 460 us).  16 e4m3 rows: the MMAs of a tile, 1776 cycles,
-// half of them for rows that repeat others (32 requests 165 us, 4.3 TB/s).  One request:
-// the start, the plan, Q and the join, one after the other (15 us, 3 tiles a CTA).
+// What bounds it (GB300): the MMAs and shared memory, each in the other's way.  64 bf16
+// rows: a tile takes 2700 cycles, its MMAs alone 2014, its 276 KB through shared memory
+// (operands 194, copies and P 82) 2160 at 128 bytes a cycle; 8 requests of 128 heads at
+// 128000 tokens 324 us, 3.6 TB/s and 0.88 PFLOP/s; 512 query tokens at 8192 1.05 ms.
+// e4m3: the widened tiles make it 340 KB, 2650 of 3400 cycles, or with 16 rows 290 KB,
+// 2270 of 2600: 7 ragged chunks 455 us, 32 requests of 16 heads 165 us (4.3 TB/s).  One
+// request: the start, the plan, Q and the join, one after the other (15 us, 3 tiles a CTA).
 #include <climits>
 #include <type_traits>
 
@@ -457,8 +457,8 @@ __global__ void __launch_bounds__(Cfg<N, FP8>::kThreads, 1)
                 ok = wait(ct->q_full, segs & 1);
                 ++segs;
                 // S of tile t, then the product with P of the tile before: while the softmax works on one tile the tensor
-                // cores work on the next.  What the one needs is asked for between the MMAs of the other, which the
-                // queue covers (`seen`: a unit each, the rotary keys, S of the tile before read; and P).
+                // cores work on the next.  What the start of the one needs is asked for between the MMAs of the other, which
+                // the queue covers (`seen`: the first unit, the rotary keys, S of the tile before read; and P).
                 uint32_t seen = 0;
                 bool p_seen = false;
 #pragma unroll 1
@@ -504,9 +504,8 @@ __global__ void __launch_bounds__(Cfg<N, FP8>::kThreads, 1)
                                 if (u == kUnits - 1) {
                                     seen |= test(ct->rope_full[rope], rope_ph) ? 1u << kUnits : 0u;
                                     seen |= test(ct->s_read, t & 1) ? 2u << kUnits : 0u;
-                                } else {
-                                    const uint32_t ahead = next(qk_slot, u);
-                                    seen |= test(ct->full[ahead], qk_ph ^ (ahead < qk_slot)) ? 1u << u : 0u;
+                                } else if (u == 0) {
+                                    seen |= test(ct->full[qk_slot], qk_ph) ? 1u : 0u;
                                 }
                                 commit(ct->empty[slot]);
                             }
