@@ -576,6 +576,9 @@ int sv_latent_gather(const sv_cache* cache, const int32_t* page_table, const int
  *  - q and out are 16-byte aligned.  The page table, lengths, rows that no
  *    request holds, requests without tokens, errors, and what rows that are not
  *    finite cost those that do not see them, are as in sv_window_attention.
+ *  - Weights enter the average as bf16 (2^-8 of each; the sum is that of the
+ *    rounded ones), over codes as the weight times the token's scale in fp16 (2^-11
+ *    of it, or 2^-25 of the row's largest where that is more).
  *  - workspace: sv_latent_attention_workspace_size(...) bytes, not shared with a
  *    call that may run at the same time; nothing in it needs to start at zero.
  *    total_q * num_q_heads < 2^31, max_pages < 2^26.

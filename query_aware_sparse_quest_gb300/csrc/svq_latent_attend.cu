@@ -25,7 +25,7 @@
 // scaled by a power of two that puts its largest value at 2^10 .. 2^11: values down to
 // 2^-27 of that stay exact, smaller ones are off by up to 2^-35 of it.  A token's scale
 // acts on its logits and on its weights.  A weight times its scale is rounded to fp16
-// (2^-12 of it) in a unit of the row that at most equals the largest so far, so that
+// (2^-11 of it) in a unit of the row that at most equals the largest so far, so that
 // those below 2^-14 of the largest are off by up to 2^-25 of it; the unit moves with
 // the base.  The average is taken over the sum of the weights themselves.  The rotary
 // part of the logits is a product of its own in bf16 (64 more columns).
