@@ -51,7 +51,7 @@
 // 128000 tokens 324 us, 3.6 TB/s and 0.88 PFLOP/s; 512 query tokens at 8192 1.05 ms.
 // e4m3: the widened tiles make it 340 KB, 2650 of 3400 cycles, or with 16 rows 290 KB,
 // 2270 of 2600: 7 ragged chunks 455 us, 32 requests of 16 heads 165 us (4.3 TB/s).  One
-// request: the start, the plan, Q and the join, one after the other (15 us, 3 tiles a CTA).
+// request: the start, the plan, three tiles and the join, one after the other (14.5 us).
 #include <climits>
 #include <type_traits>
 
@@ -688,14 +688,14 @@ __global__ void __launch_bounds__(Cfg<N, FP8>::kThreads, 1)
             // Q of a segment's rows: the first units to TMEM, where row r is lane 32 (r / 16) + r % 16, the rest to shared
             // memory.  Eight lanes read a row, rows 4 i + lane / 8 and chunks of 8 channels (a row a lane would touch 32
             // lines a load), and the way to TMEM leads through the warp's rows of the last block.
-            auto load_q = [&](const Seg& g) {
+            auto load_q = [&](int row0, int nrows) {
                 if (w >= 4) return;   // (the first four)
-                if (16 * rg < g.en.nrows) {
+                if (16 * rg < nrows) {
                     constexpr int kBlocks = kQueryDim / 64;
                     const uint4* from[4];
 #pragma unroll
                     for (int i = 0; i < 4; ++i)
-                        from[i] = reinterpret_cast<const uint4*>(a.q + static_cast<int64_t>(g.en.row0 + min(16 * rg + 4 * i + (lane >> 3), g.en.nrows - 1)) * kQueryDim) + (lane & 7);
+                        from[i] = reinterpret_cast<const uint4*>(a.q + static_cast<int64_t>(row0 + min(16 * rg + 4 * i + (lane >> 3), nrows - 1)) * kQueryDim) + (lane & 7);
                     float shrink[4];
                     if (FP8) {
                         // The rows' largest exponents (of their finite values).
@@ -763,9 +763,18 @@ __global__ void __launch_bounds__(Cfg<N, FP8>::kThreads, 1)
             for (uint32_t k = 0;; ++k) {
                 const Seg& s = ct->seg[k % kSegs];
                 if (k == 0) {
-                    LATENT_WAIT(ct->seg_full[0], 0);
-                    if (softmax_any<C::kSoft>(dead)) goto softmax_end;
-                    if (s.t1 > s.t0) load_q(s);
+                    // The rows of a single request are known before the plan (one request of 4096 tokens 15.3 -> 14.5 us).
+                    const bool known = !a.planned && a.batch == 1;
+                    if (!known) {
+                        LATENT_WAIT(ct->seg_full[0], 0);
+                        if (softmax_any<C::kSoft>(dead)) goto softmax_end;
+                    }
+                    const int rows = known ? min(N, a.heads - part * N) : s.en.nrows;
+                    if (known || s.t1 > s.t0) load_q(known ? part * N : s.en.row0, rows);
+                    if (known) {
+                        LATENT_WAIT(ct->seg_full[0], 0);
+                        if (softmax_any<C::kSoft>(dead)) goto softmax_end;
+                    }
                 }
                 const int n = s.t1 - s.t0;
                 if (n == 0) break;
@@ -1044,7 +1053,7 @@ __global__ void __launch_bounds__(Cfg<N, FP8>::kThreads, 1)
                         lr1 += add_r1;
                     }
                 }
-                if (nx.t1 > nx.t0) load_q(nx);   // the segment's last use of Q is over
+                if (nx.t1 > nx.t0) load_q(nx.en.row0, nx.en.nrows);   // the segment's last use of Q is over
 
                 // ---------------- the segment's end
 #pragma unroll
