@@ -52,6 +52,7 @@
 // e4m3: the widened tiles make it 340 KB, 2650 of 3400 cycles, or with 16 rows 290 KB,
 // 2270 of 2600: 7 ragged chunks 455 us, 32 requests of 16 heads 165 us (4.3 TB/s).  One
 // request: the start, the plan, three tiles and the join, one after the other (14.5 us).
+#include <cfloat>
 #include <climits>
 #include <type_traits>
 
@@ -860,13 +861,16 @@ __global__ void __launch_bounds__(Cfg<N, FP8>::kThreads, 1)
                     }
                     // Weights go by the rows' bases as they are, unless a logit is more than kSlack above its row's: then
                     // (at a run's first tile, and seldom behind it) the tile's maxima move the bases.  The warps say so to
-                    // one another while they work out the weights, as each holds channels of all rows' O.
+                    // one another while they work out the weights, as each holds channels of all rows' O.  A row without
+                    // a base has seen nothing in the run's tiles so far (pages that are not there): there any finite logit
+                    // is far above -FLT_MAX, and -inf, all that such a row has in a tile if its base does not move, has the
+                    // weight 0.
                     uint32_t p[kC][2];
                     float add0, add1, add_r0, add_r1, over = -INFINITY;
                     float big0, big1;   // e4m3: the largest weight times scale, in O's unit
                     auto weights = [&](float g0, float g1) {
                         big0 = big1 = 0.f;
-                        const float b0 = m0 == -INFINITY ? 0.f : m0, b1 = m1 == -INFINITY ? 0.f : m1;
+                        const float b0 = m0 == -INFINITY ? -FLT_MAX : m0, b1 = m1 == -INFINITY ? -FLT_MAX : m1;
                         const uint64_t scale2 = pack2(a.scale_log2, a.scale_log2), base0 = pack2(-b0, -b0), base1 = pack2(-b1, -b1);
                         uint64_t sum0 = 0ull, sum1 = 0ull, sumr0 = 0ull, sumr1 = 0ull;
 #pragma unroll

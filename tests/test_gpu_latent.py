@@ -535,3 +535,52 @@ def test_sums_of_more_than_65536_tokens(fp8):
     for b in (0, 1, 77, 159):
         check(out[b:b + 1], lse[b:b + 1], attend(q[b:b + 1], torch.cat((c, r), 1), c,
                                                  torch.ones((1, n), dtype=torch.bool, device=DEV), SCALE))
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("how", ["page", "logit"])
+@pytest.mark.parametrize("heads,lens,sizes", [
+    (16, [5000], None),                  # runs of a few tiles each
+    (128, [5000, 70, 400], None),
+    (16, [200, 330] * 100, None),        # whole requests and cut ones
+    (5, [130, 3000, 260], [3, 40, 1]),
+    (128, [500, 1000], [40, 1]),
+])
+def test_rows_that_see_nothing_in_their_first_tiles(heads, lens, sizes, how, fp8):
+    """The first tokens are not there (64 make a key tile: the table does not give their pages, or their logits are
+    -inf), and what follows has logits of any size, below 0 too; over codes the next tokens are zeros (scale 0)."""
+    from query_aware_sparse_quest_gb300 import binding
+    steps = [1] * len(lens) if sizes is None else sizes
+    case = LatentCase(lens, fp8=fp8, seed=21)
+    if fp8:
+        for b in range(0, len(lens), 2):
+            for t in range(min(130, lens[b] - 70)):
+                page = case.table[b, t // PAGE]
+                case.latent[page, t % PAGE], case.scale[page, t % PAGE] = 0, 0.0
+    case.rope[..., 0] = 64.0
+    for hidden in (64, 128):
+        keep = case.rope.clone()
+        table = case.table.clone()
+        if how == "page":
+            table[:, : hidden // PAGE] = -1
+        else:
+            for b, n in enumerate(lens):
+                for t in range(min(hidden, n)):
+                    case.rope[case.table[b, t // PAGE], t % PAGE, 1] = -float("inf")
+        cache = case.cache()
+        for size, shift in ((1.0, 0.0), (0.03, 0.0), (0.3, -0.8), (0.3, -40.0)):
+            q = queries(sum(steps), heads, seed=hidden, size=size)
+            q[..., LATENT], q[..., LATENT + 1] = shift, 0.5
+            good, case.table = case.table, table
+            out, lse = call(case, q, sizes, cache=cache)
+            case.table = good
+            assert binding.sv_get_device_error() == (0x1 if how == "page" else 0)
+            for b in list(range(len(lens)))[:6]:
+                n, at = lens[b], sum(steps[:b])
+                c, r = case.tokens(b)
+                seen = causal_seen(n, steps[b], DEV)
+                seen[:, :hidden] = False
+                r = torch.nan_to_num(r, neginf=0.0)
+                check(out[at:at + steps[b]], lse[at:at + steps[b]],
+                      attend(q[at:at + steps[b]], torch.cat((c, r), 1), c, seen, SCALE))
+        case.rope = keep
