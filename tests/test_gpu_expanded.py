@@ -240,3 +240,27 @@ def test_sums_of_more_than_65536_tokens():
     q, k, v = r.q[:, pick], r.k[:, pick], r.v[:, pick]
     k = torch.cat((k.double(), r.rope[:, None].double().expand(-1, len(pick), -1)), -1)
     check(out[:, pick], lse[:, pick], attend(q, k, v.double(), causal_seen(n, size, DEV), SCALE))
+
+
+@pytest.mark.parametrize("size,n,spikes", [
+    (70, 270000, ((1500, 100.0), (1501, 100.0), (2080, 186.0), (2081, 186.0))),   # even and odd tiles: 1055 a stream
+    (200, 140000, ((700, 100.0), (1050, 186.0))),                                 # two row halves: 1094 each
+])
+def test_sums_that_leave_the_tensor_memory_more_than_once(size, n, spikes):
+    """As above, with tokens in some tiles whose logits move the bases: what was summed before is part of the average."""
+    heads = 160
+    r = Rows([size], [n], 1, seed=7, mean=2.0, spare=heads)
+    r.heads = heads
+    g = torch.Generator().manual_seed(8)
+    r.q = (torch.randn((size, heads, 192), generator=g) * 0.1).bfloat16().to(DEV)
+    r.q[..., 128] = 1.0
+    flat_k, flat_v = (torch.nan_to_num(x.reshape(-1, 128).contiguous()) for x in (r.k, r.v))
+    r.k, r.v = (x.as_strided((n, heads, 128), (128, 128, 1)) for x in (flat_k, flat_v))
+    r.rope = r.rope[:n]
+    for tile, value in spikes:
+        r.rope[tile * 128 + 77, 0] = value
+    out, lse = r.call()
+    pick = [0, 1, 79, 159]
+    q, k, v = r.q[:, pick], r.k[:, pick], r.v[:, pick]
+    k = torch.cat((k.double(), r.rope[:, None].double().expand(-1, len(pick), -1)), -1)
+    check(out[:, pick], lse[:, pick], attend(q, k, v.double(), causal_seen(n, size, DEV), SCALE))

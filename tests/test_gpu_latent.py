@@ -584,3 +584,28 @@ def test_rows_that_see_nothing_in_their_first_tiles(heads, lens, sizes, how, fp8
                 check(out[at:at + steps[b]], lse[at:at + steps[b]],
                       attend(q[at:at + steps[b]], torch.cat((c, r), 1), c, seen, SCALE))
         case.rope = keep
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("heads,batch", [(16, 160), (128, 80)])
+def test_sums_that_leave_the_tensor_memory_more_than_once(heads, batch, fp8):
+    """Runs of 3200 tiles, with a token at tile 1500 and one at 2600 whose logits move the bases: what was summed before
+    is a quarter of the average."""
+    n = 204805
+    count = -(-n // PAGE)
+    case = LatentCase([642 * PAGE], fp8=fp8, seed=12, mean=2.0)
+    at = torch.arange(count) * 640 // count
+    for i, (tile, size) in enumerate(((1500, 100.0), (2600, 186.0))):
+        at[4 * tile] = 640 + i
+        case.rope[case.table[0, 640 + i], 3, 0] = size
+    case.table = case.table[:1, at].contiguous()
+    q = queries(batch, heads, seed=13, size=0.1)
+    q[..., LATENT] = 1.0
+    case.lens, case.table = [n] * batch, case.table.expand(batch, -1).contiguous()
+    out, lse = call(case, q)
+    case.lens, case.table = [n], case.table[:1]
+    c, r = case.tokens(0)
+    seen = torch.ones((1, n), dtype=torch.bool, device=DEV)
+    pick = sorted({0, heads // 2 - 1, heads // 2, heads - 1})
+    for b in (0, 1, batch // 2, batch - 1):
+        check(out[b:b + 1, pick], lse[b:b + 1, pick], attend(q[b:b + 1, pick], torch.cat((c, r), 1), c, seen, SCALE))
