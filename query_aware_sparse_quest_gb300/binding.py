@@ -420,7 +420,7 @@ class CacheList:
 def _cache_list(caches) -> CacheList:
     if isinstance(caches, CacheList):
         return caches
-    return CacheList([caches] if isinstance(caches, Cache) else caches)
+    return CacheList([caches] if isinstance(caches, (Cache, LatentCache)) else caches)
 
 
 def _rows(page_table: torch.Tensor, seq_lens: torch.Tensor, ref_counts: torch.Tensor, dev: int,
@@ -439,7 +439,7 @@ def sv_pages_workspace_size(num_phys_pages: int, num_rows: int, n: int) -> int:
 
 
 def sv_pages_copy(caches, src: torch.Tensor, dst: torch.Tensor, stream=None) -> None:
-    """Copies page src[i] to page dst[i] in every cache (a Cache, several, or a CacheList)."""
+    """Copies page src[i] to page dst[i] in every cache (a Cache or LatentCache, several, or a CacheList)."""
     cl = _cache_list(caches)
     _shape(dst, src.shape, "dst")
     dev = torch.cuda.current_device()

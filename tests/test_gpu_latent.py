@@ -609,3 +609,52 @@ def test_sums_that_leave_the_tensor_memory_more_than_once(heads, batch, fp8):
     pick = sorted({0, heads // 2 - 1, heads // 2, heads - 1})
     for b in (0, 1, batch // 2, batch - 1):
         check(out[b:b + 1, pick], lse[b:b + 1, pick], attend(q[b:b + 1, pick], torch.cat((c, r), 1), c, seen, SCALE))
+
+
+def pools(pages, kinds, seed):
+    """Caches of the given formats whose pages hold anything, and all their tensors."""
+    from query_aware_sparse_quest_gb300 import binding
+    g = torch.Generator().manual_seed(seed)
+
+    def new(dtype, *shape):
+        size = {torch.uint8: 1, torch.bfloat16: 2, torch.float32: 4}[dtype]
+        return torch.randint(0, 256, (pages, *shape[:-1], shape[-1] * size), generator=g, dtype=torch.uint8).to(DEV).view(dtype)
+    caches, tensors = [], []
+    for kind in kinds:
+        code = torch.uint8 if kind.endswith("e4m3") else torch.bfloat16
+        if kind.startswith("latent"):
+            t = [new(code, PAGE, LATENT), new(torch.bfloat16, PAGE, ROPE)] + ([new(torch.float32, PAGE)] if code == torch.uint8 else [])
+            caches.append(binding.LatentCache(*t))
+        else:
+            t = [new(code, 2, PAGE, 128), new(code, 2, PAGE, 128), new(torch.bfloat16, 2, 2, 128)]
+            t += [new(torch.float32, 2, PAGE) for _ in range(2)] if code == torch.uint8 else []
+            caches.append(binding.Cache(*t))
+        tensors += t
+    return caches, tensors
+
+
+@pytest.mark.parametrize("kinds", [["latent"], ["latent e4m3"], ["latent", "heads", "latent e4m3", "heads e4m3"]])
+def test_pages_of_any_formats_are_copied(kinds):
+    """One latent cache as it is, and caches of all formats in one list: every byte of a copied page, and no other."""
+    from query_aware_sparse_quest_gb300 import binding
+    pages = 9
+    caches, tensors = pools(pages, kinds, seed=len(kinds))
+    src, dst = [0, 8, 5], [3, 1, 7]
+    want = []
+    for t in tensors:
+        w = t.view(torch.uint8).clone()
+        w[dst] = w[src]
+        want.append(w)
+    binding.sv_pages_copy(caches[0] if len(caches) == 1 else caches, ints(src), ints(dst))
+    for t, w in zip(tensors, want):
+        assert torch.equal(t.view(torch.uint8), w)
+    # A fork copies the partly filled page of its row.
+    table = ints([[2, 4, -1], [-1, -1, -1]])
+    lens, counts = ints([20, 0]), ints([0, 0, 1, 0, 1, 0, 0, 0, 0])
+    ws = torch.empty(binding.sv_pages_workspace_size(pages, 2, 1), dtype=torch.uint8, device=DEV)
+    binding.sv_pages_fork(caches[0] if len(caches) == 1 else caches, table, lens, counts, ints([0]), ints([1]), ws)
+    new = int(table[1, 1])
+    assert table[1, 0] == 2 and new not in (2, 4) and lens.tolist() == [20, 20] and counts[2] == 2
+    for t, w in zip(tensors, want):
+        w[new] = w[4]
+        assert torch.equal(t.view(torch.uint8), w)

@@ -141,3 +141,11 @@ def test_binding_refuses_what_the_calls_cannot_check(lib):
         binding.LatentCache(t((3, 16, 512), dtype=torch.bfloat16), t((4, 16, 64), dtype=torch.bfloat16))
     with pytest.raises((ValueError, TypeError)):
         binding.LatentCache(t((3, 16, 512)), t((3, 16, 64)))
+
+
+def test_page_calls_take_a_latent_cache_by_itself():
+    c = binding.LatentCache.__new__(binding.LatentCache)
+    c.latent, c.c = torch.zeros((3, 16, 512), dtype=torch.bfloat16), cache(pages=3)
+    assert binding._cache_list(c).caches == (c,)
+    assert binding._cache_list(c).num_phys_pages == 3
+    assert binding._cache_list((c, c)).caches == (c, c)
