@@ -469,6 +469,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 ++k;
                 return true;
             };
+            // (A CTA that gives up in its waves names no item for the join.)
+            if (lane == 0) a.cut_item[2 * blockIdx.x] = make_int4(0, 0, 0, 0);
             for (int64_t j = 0, i = blockIdx.x; j < waves; ++j, i += gridDim.x) {
                 while (i >= static_cast<int64_t>(a.heads) * a.req_first[b + 1]) ++b;
                 e0 = a.req_first[b];
