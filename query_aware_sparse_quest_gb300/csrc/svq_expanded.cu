@@ -799,6 +799,7 @@ __device__ __forceinline__ bool kv_range(const ExpandedArgs& a, int b, int size,
 // One CTA: the list of entries, and the running sums of their costs.
 __global__ void __launch_bounds__(kPlanThreads) expanded_plan_kernel(const __grid_constant__ ExpandedArgs a) {
     __shared__ int64_t warp_sums[32];
+    __shared__ int most_waves;
     const int tid = threadIdx.x, lane = tid & 31, threads = blockDim.x;
     int64_t total;
     pdl_wait();   // the workspace may still be read by the call before
@@ -877,21 +878,35 @@ __global__ void __launch_bounds__(kPlanThreads) expanded_plan_kernel(const __gri
         __threadfence();
         return;
     }
-    int64_t len = equal, whole = 0;   // of the thread's; of all waves
-    for (; waves > 0; --waves) {
-        int64_t mine = 0;
-        int b = 0;
-        for (int64_t j = 0, i = tid; j < waves && tid < a.ctas; ++j, i += a.ctas) {
+    // Costs only add up, so the waves that fit are the fewest that fit a thread's share, each thread going through its own
+    // items once.  (Looking from the most waves down, each time through all of them, took 140 us of 930 for 32 requests of
+    // 1024 tokens and 64 heads.)
+    auto first_items = [&](int most, int64_t limit, int64_t& sum) {   // how many of them stay within the limit; their cost
+        int b = 0, j = 0;
+        sum = 0;
+        for (int64_t i = tid; j < most; ++j, i += a.ctas) {
             while (i >= static_cast<int64_t>(a.heads) * a.req_first[b + 1]) ++b;
-            const int e0 = a.req_first[b], e = e0 + static_cast<int>((i - static_cast<int64_t>(a.heads) * e0) % (a.req_first[b + 1] - e0));
-            mine += a.cum[e + 1] - a.cum[e];
+            const int e0 = a.req_first[b];
+            const int64_t in = i - static_cast<int64_t>(a.heads) * e0, entries = a.req_first[b + 1] - e0;
+            const int e = e0 + static_cast<int>(in - div64(in, entries) * entries);
+            const int64_t more = sum + a.cum[e + 1] - a.cum[e];
+            if (more > limit) break;
+            sum = more;
         }
-        len = equal - mine;
-        (void)block_scan(mine, warp_sums, whole);
-        if (!__syncthreads_or(tid < a.ctas && len < 1)) break;
-        len = equal;
-        whole = 0;
+        return j;
+    };
+    int64_t mine = 0, whole;          // of the thread's waves; of all
+    if (tid == 0) most_waves = waves;
+    __syncthreads();
+    if (tid < a.ctas) {
+        const int fit = first_items(waves, equal - 1, mine);
+        if (fit < waves) atomicMin(&most_waves, fit);
     }
+    __syncthreads();
+    waves = most_waves;
+    if (tid < a.ctas) (void)first_items(waves, equal, mine);
+    const int64_t len = equal - mine;
+    (void)block_scan(mine, warp_sums, whole);
     const int64_t before = whole + block_scan(len, warp_sums, total);
     if (tid < a.ctas) a.starts[tid] = before;
     if (tid == 0) {
