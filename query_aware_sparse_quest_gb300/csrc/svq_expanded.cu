@@ -15,9 +15,9 @@
 // Work.  An entry is a row tile with the tokens it sees, an item an entry of one
 // head.  Every CTA takes an equal run of the (request, head, entry, key tile)
 // sequence; a run that starts or ends inside an item leaves a partial (O, base,
-// sum), joined by a second kernel.  Where the keys and values do not fit the L2,
-// CTAs take whole items first, in step with one another (see ExpandedArgs), and such
-// runs of the rest.
+// sum), joined by a second kernel.  Where the keys and values do not fit the L2 and
+// a head has several row tiles, CTAs take whole items first, in step with one another
+// (see ExpandedArgs), and such runs of the rest.
 //
 // Roles of a CTA (one per SM; TMEM holds S0, S1, O0, O1 of 128 columns each):
 //   warp 0       loads keys, warp 3 values: a ring of 8 blocks of 16 KB (TMA), of
@@ -79,8 +79,11 @@ struct __align__(16) Entry {
 // same time, which then come from L2 (equal runs of the whole sequence have every CTA at a head of its own: each item's
 // keys and values come from HBM).  A 4096-token chunk of 32 heads at 32768 tokens 1855 -> 1533 us.  Not worth it where
 // the L2 holds them anyway (tokens times heads, 512 bytes each; 5 ragged requests of 60 MB 62.5 us, in waves 63.6), nor for
-// many requests, as the plan looks up items one by one.
-constexpr int kMaxWaves = 64, kWaveBatch = 32;
+// many requests, as the plan looks up items one by one, nor where a head has few row tiles, which a CTA with an equal run
+// takes one after the other.  Fresh prompts of 32 requests and 64 heads, equal runs / waves, us: 512 tokens 281 / 313, 1024
+// 718 / 784, 1280 1013 / 1021, 1536 1431 / 1403, 1792 1832 / 1747, 3000 5291 / 5084; 300-token chunks of 16 requests and 16
+// heads at 4096 tokens 215 / 252.  So from a mean of kWaveRows query tokens a request on.
+constexpr int kMaxWaves = 64, kWaveBatch = 32, kWaveRows = 1536;
 constexpr int64_t kWaveTokens = 128 << 10;
 struct ExpandedArgs {
     const __nv_bfloat16* q;
@@ -1095,7 +1098,8 @@ int launch_expanded(const void* q, int num_heads, const int32_t* q_start, int to
     a.waves = reinterpret_cast<int*>(ws + lay.waves);
     a.starts = reinterpret_cast<int64_t*>(ws + lay.starts);
     a.ctas = sm_count < kMaxCtas ? sm_count : kMaxCtas;
-    a.in_step = batch <= kWaveBatch && static_cast<int64_t>(total_kv) * num_heads >= kWaveTokens;
+    a.in_step = batch <= kWaveBatch && total_q >= static_cast<int64_t>(kWaveRows) * batch &&
+                static_cast<int64_t>(total_kv) * num_heads >= kWaveTokens;
     a.req_first = reinterpret_cast<int*>(ws + lay.req_first);
     a.req_cum = reinterpret_cast<int64_t*>(ws + lay.req_cum);
     a.max_entries = lay.max_entries;

@@ -264,3 +264,15 @@ def test_sums_that_leave_the_tensor_memory_more_than_once(size, n, spikes):
     q, k, v = r.q[:, pick], r.k[:, pick], r.v[:, pick]
     k = torch.cat((k.double(), r.rope[:, None].double().expand(-1, len(pick), -1)), -1)
     check(out[:, pick], lse[:, pick], attend(q, k, v.double(), causal_seen(n, size, DEV), SCALE))
+
+
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("sizes,lens,heads", [
+    ([5000, 0, 2100, 300], [5000, 40, 2100, 1000], 40),
+    ([1600, 1536, 1537], [1700, 1536, 5000], 24),
+    ([1550], [1550], 152),
+])
+def test_long_prompts_in_waves(sizes, lens, heads, causal):
+    """Prompts of several row tiles a head, whose keys and values do not fit the L2: whole items first, in step."""
+    r = Rows(sizes, lens, heads, seed=4)
+    r.check(*r.call(causal), causal)
