@@ -104,7 +104,9 @@ __device__ __forceinline__ int find_row(const int32_t* a, int n, int v) {
 }
 
 // Rows of a warp of the read-back: one, or where they are many, kRowsEach (152489 rows: 1 67.2 us, 4 60.6, 8 62.6; 4096
-// rows: 1 or 2 4.2 us, 8 5.2).
+// rows: 1 or 2 4.2 us, 8 5.2; 1 / 4, one request bf16 and 16 e4m3: 8192 rows 5.7 / 5.7 and 5.9 / 5.7, 24576 11.9 / 11.3 and 11.8
+// / 11.7, 16 of bf16 12.4 / 13.4; from 32768 on 4 is ahead everywhere, 14.4 / 13.9 and 14.7 / 12.9, 65536 28.3 / 26.9 and 27.2 /
+// 24.4).
 constexpr int kRowsEach = 4, kManyRows = 32768;
 
 struct GatherArgs {

@@ -50,8 +50,10 @@
 // (operands 194, copies and P 82) 2160 at 128 bytes a cycle; 8 requests of 128 heads at
 // 128000 tokens 324 us, 3.6 TB/s and 0.88 PFLOP/s; 512 query tokens at 8192 1.05 ms.
 // e4m3: the widened tiles make it 340 KB, 2650 of 3400 cycles, or with 16 rows 290 KB,
-// 2270 of 2600: 7 ragged chunks 455 us, 32 requests of 16 heads 165 us (4.3 TB/s).  One
-// request: the start, the plan, three tiles and the join, one after the other (14.5 us).
+// 2270 of 2600: 7 ragged chunks 455 us, 32 requests of 16 heads 165 us (4.3 TB/s).  So
+// codes are the slower cache from 33 rows on (8 requests of 128 heads at 32768 tokens 135
+// us, bf16 108).  One request: the start, the plan, three tiles and the join, one after
+// the other (14.5 us).
 #include <cfloat>
 #include <climits>
 #include <type_traits>
@@ -97,7 +99,7 @@ struct Cfg {
     // Registers a thread: bf16 168 at launch, then 96 for the first four warps and the loads and 248 for the softmax
     // (128 x (96 + 248 + 96) < 384 x 168); e4m3 128, then 72, 64, 232 and 128 for widening, or with eight softmax warps 96,
     // 160 (twice) and 96.  (The compiler keeps every role's code near the count at launch: with eight warps that widen, 640
-    // threads of 96, the softmax took half as long again.)
+    // threads of 96, the softmax took half as long again.  At 128 it spills 32 bytes a thread with 64 e4m3 rows, 4 with 16.)
     static constexpr int kThreads = FP8 ? 512 : 384;
     static constexpr int kFirstWiden = kThreads / 32 - kWiden;
     static constexpr int kMmaRegs = FP8 && kSoft == 4 ? 72 : 96, kSoftmaxRegs = !FP8 ? 248 : (kSoft == 4 ? 232 : 160);
@@ -350,8 +352,11 @@ __device__ __forceinline__ int warp_find_le(const int64_t* a, int n, int64_t v) 
 }
 
 // What an entry costs beside its tiles, in tiles (Q, the first tile's bases, the outputs: 64 rows take 25000 cycles, and
-// with 3 for them 7 requests' e4m3 chunks take 603 us, with 9 490, with 14 520; 16 rows 1: 32 requests 169 us, 3: 165, 5:
-// 164), and the least share that is worth a CTA (one request of 64 tiles and 16 heads: 1 20.1 us, 2 19.5, 3 17.4, 4 18.0).
+// with 3 for them 7 requests' e4m3 chunks take 603 us, with 9 490, with 14 520; seven others with 5 / 9 / 13: e4m3 1099 / 956
+// / 976, bf16 732 / 662 / 680; 300 tokens of 128 heads 102 / 94 / 88 and 75 / 69 / 68; 40 single tokens of 64 heads at 3000 60 /
+// 61 / 65 and 57 / 58 / 60; 16 rows 1: 32 requests 169 us, 3: 165, 5: 164), and the least share that is worth a CTA (one request
+// of 64 tiles and 16 heads: 1 20.1 us, 2 19.5, 3 17.4, 4 18.0; later 2 / 3 / 5, bf16: 16 heads at 1000 tokens 12.9 / 13.9 /
+// 15.5, 4096 14.9 / 15.4 / 16.1, 16000 24.2 / 21.0 / 20.5; 128 heads 20.3 / 18.9 / 21.7, 29.1 / 24.9 / 24.2, 45.9 / 46.6 / 37.8).
 constexpr int kMinShare = 3;
 __host__ __device__ constexpr int entry_cost(int rows) { return rows == 64 ? 9 : 3; }
 __device__ __forceinline__ int cost_of_entry(int tiles, int rows) { return tiles ? tiles + entry_cost(rows) : 0; }
